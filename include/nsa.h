@@ -461,6 +461,121 @@ NSA_API nsa_status nsa_layer_bwd(const nsa_shape* shape, const void* q, const vo
                                  void* dv, float* d_gate_logits, void* workspace, size_t workspace_bytes,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Paged cache.  A server's K/V cache that grows page by page: pages of page_size tokens in
+ * one pool, and per sequence a row of the block table listing its pages in order.  Position
+ * j of sequence b lives in page block_table[b][j / page_size], row j % page_size.  The calls
+ * below are this library's own (the pages cited above decode over a contiguous cache, as
+ * nsa_sparse_decode does); they share its conventions.
+ *   k_pages, v_pages  [n_pages][page_stride elements] bf16; a page is page_size rows
+ *                     [h_kv, d].  page_stride >= page_size * h_kv * d, a multiple of 8
+ *                     (larger strides serve pools that hold K and V of a page side by side)
+ *   weights           [n_pages, h_kv, page_size] fp32: the accumulated attention weight of
+ *                     every cached key, for eviction; NULL where a call does not need it
+ *   block_table       device int32 [n_seqs, max_pages].  An entry outside [0, n_pages) is
+ *                     no page: keys there are masked and never read (a server may take the
+ *                     pages that left a sliding window out of the table by writing -1)
+ *   cache_lens        device int32 [n_seqs]: cached tokens of each sequence, its new tokens
+ *                     included.  Lengths outside [0, max_pages * page_size] are clamped.
+ * The values at positions below cache_lens have to be finite; memory past them, and pages
+ * that no table row names, may hold anything.
+ * page_size is a power of two in [16, 256]; bf16; d in {64, 128}; h/h_kv <= 128; at most 2^30
+ * positions per table row, 65535 sequences. */
+typedef struct nsa_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* weights;
+  const int32_t* block_table;
+  const int32_t* cache_lens;
+  int32_t n_pages, page_size, max_pages;
+  int64_t page_stride;
+} nsa_paged_cache;
+
+/* Write the keys and values of new tokens into the cache.  shape describes the new tokens
+ * (its sequences are the table's rows, dense or varlen): token i of a sequence with Lq new
+ * tokens goes to position cache_lens[b] - Lq + i.  Tokens whose position is negative, past
+ * the table row or in no page are dropped, as are rows past the last sequence.  The weights
+ * (if given) of the written positions become 0.
+ *   k_new, v_new  [tokens, h_kv, d] bf16 */
+NSA_API nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, const void* v_new,
+                                    const nsa_paged_cache* cache, cudaStream_t stream);
+
+/* Attention of a chunk of new tokens over the paged cache: the chunk of a prompt, a few
+ * speculative tokens or the one token of a decode step; lengths may differ per sequence.
+ * Query i of a sequence with Lq queries stands at position p = cache_lens[b] - Lq + i (the
+ * cache already holds the chunk's own keys, nsa_paged_append) and sees key j when j <= p
+ * and (window == 0, or j > p - window, or j < n_sink): causal, optionally within a sliding
+ * window beside which the first n_sink tokens stay visible.  Softmax in fp32; P enters the
+ * second product as bf16.  A query that sees no key gets o = 0, lse = -inf.  Rows past the
+ * last sequence are left as they were.
+ *   q, o           [tokens, h, d] bf16
+ *   lse            nullable [tokens, h] fp32 out, natural log
+ *   max_cache_len  a bound on cache_lens known to the host (0: max_pages * page_size); it
+ *                  decides how the keys are divided over the GPU, never the result's rows
+ *   workspace      nsa_paged_attn_fwd_workspace_size() bytes, 256-byte aligned (partial
+ *                  results of divided rows); NULL allowed when that size is 0
+ * Deterministic.  0 <= window, n_sink <= 2^30. */
+NSA_API size_t nsa_paged_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink);
+NSA_API nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
+                                      int64_t max_cache_len, int window, int n_sink, float scale, void* o, float* lse,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Attention weight of every cached key, for eviction.  With the queries, masks and lse of a
+ * nsa_paged_attn_fwd call: for each cached position j and kv-head g
+ *   weights_out[j, g] = decay * weights[j, g] + sum over the queries i that see j and the
+ *                       heads of group g of exp(scale q_i.k_j - lse_i).
+ * Every cached position is written (those no query sees keep decay times their weight; with
+ * cache->weights == NULL the sum alone is written), positions past cache_lens are left as
+ * they were.  Sums in fp32 without atomics: deterministic.
+ *   q    [tokens, h, d] bf16;  lse [tokens, h] fp32
+ *   weights_out  [n_pages, h_kv, page_size] fp32; may be cache->weights itself.  A page
+ *                listed by several sequences (a shared prefix) would be written by each, so
+ *                give such sequences weights of their own.
+ * v_pages is not read. */
+NSA_API nsa_status nsa_paged_attn_weights(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
+                                          const float* lse, int window, int n_sink, float scale, float decay,
+                                          float* weights_out, cudaStream_t stream);
+
+/* Cut caches to a budget of keys by accumulated weight.  Per sequence and kv-head the first
+ * n_sink and the last n_recent positions stay, and of the others those with the largest
+ * weights (equal weights: the lower position; NaN and positions in no page rank lowest),
+ * `budget` in all; a sequence with cache_lens <= budget keeps everything.  The kept rows of
+ * K, V and the weights are copied, in order of position, to positions 0, 1, ... of
+ * new_table's pages, so the pages listed before may then be freed (they stay unchanged: pages
+ * shared with other sequences need no care).  Keys keep the rotary phase, if any, that they
+ * were stored with.  The heads of a sequence may keep different positions.
+ *   new_table  device int32 [n_seqs, new_max_pages]; its pages must not be among those the
+ *              call reads or writes for another sequence; rows whose entry is no page are
+ *              dropped
+ *   keep       device int32 [n_seqs, h_kv, budget] out: kept positions, ascending, -1 padded
+ *   new_lens   device int32 [n_seqs] out: min(cache_lens, budget); may be cache_lens itself
+ * Requires 1 <= budget, n_sink + n_recent <= budget, new_max_pages * page_size >=
+ * min(budget, max_pages * page_size); cache->weights. */
+NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_cache* cache, int budget, int n_sink,
+                                   int n_recent, const int32_t* new_table, int new_max_pages, int32_t* keep,
+                                   int32_t* new_lens, cudaStream_t stream);
+
+/* Sliding window with sinks, for training: nsa_swa_fwd's window beside which the first
+ * n_sink tokens of each sequence stay visible to every later token, the masks with which
+ * nsa_paged_attn_fwd then serves.  Token t sees keys max(0, t-window+1) .. t and
+ * 0 .. min(n_sink - 1, t).
+ *   q, o [tokens, h, d]; k, v [tokens, h_kv, d] bf16;  lse nullable [tokens, h] fp32 out
+ *   workspace  nsa_swa_sink_fwd_workspace_size() bytes, 256-byte aligned (0 but for
+ *              few rows); NULL allowed when that size is 0
+ * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^30, 0 <= n_sink <= 2^30.
+ * The backward returns the gradients for an upstream d_o (formulas of nsa_sparse_bwd over
+ * the seen keys, P and dS as bf16 in their products); o and lse are the forward's.  dk and
+ * dv are written for every row of a sequence.  Deterministic.  Requires n_sink <= 1024. */
+NSA_API size_t nsa_swa_sink_fwd_workspace_size(const nsa_shape* shape, int window, int n_sink);
+NSA_API nsa_status nsa_swa_sink_fwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,
+                                    int n_sink, float scale, void* o, float* lse, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+NSA_API size_t nsa_swa_sink_bwd_workspace_size(const nsa_shape* shape, int window, int n_sink);
+NSA_API nsa_status nsa_swa_sink_bwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,
+                                    int n_sink, float scale, const void* o, const float* lse, const void* d_o,
+                                    void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

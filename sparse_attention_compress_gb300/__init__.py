@@ -12,7 +12,9 @@ from ._lib import (NsaError, load, make_shape, nsa_block_sparse_fwd, nsa_block_s
                    nsa_gate_combine, nsa_layer_fwd, nsa_select, nsa_select_workspace_size, nsa_layer_fwd_workspace_size, nsa_sparse_decode,
                    nsa_sparse_decode_noalloc, nsa_sparse_decode_workspace_size, nsa_sparse_bwd,
                    nsa_sparse_bwd_workspace_size, nsa_sparse_fwd, nsa_swa_fwd, nsa_topk_select, num_cmp,
-                   nsa_set_wait_limit_ns)
+                   nsa_set_wait_limit_ns, nsa_paged_append, nsa_paged_attn_fwd, nsa_paged_attn_fwd_workspace_size,
+                   nsa_paged_attn_weights, nsa_paged_evict, nsa_swa_sink_fwd, nsa_swa_sink_fwd_workspace_size,
+                   nsa_swa_sink_bwd, nsa_swa_sink_bwd_workspace_size)
 
 __all__ = ["NsaError", "load", "make_shape", "nsa_block_sparse_fwd", "nsa_block_sparse_workspace_size",
            "nsa_cis_block_scores", "nsa_sparse_cis_fwd", "nsa_topk_two_stage", "nsa_cmp_attn_bwd",
@@ -21,4 +23,6 @@ __all__ = ["NsaError", "load", "make_shape", "nsa_block_sparse_fwd", "nsa_block_
            "nsa_gate_combine", "nsa_layer_fwd", "nsa_select", "nsa_select_workspace_size", "nsa_layer_fwd_workspace_size", "nsa_sparse_decode",
            "nsa_sparse_decode_noalloc", "nsa_sparse_decode_workspace_size", "nsa_sparse_bwd",
            "nsa_sparse_bwd_workspace_size", "nsa_sparse_fwd", "nsa_swa_fwd", "nsa_topk_select", "num_cmp",
-           "nsa_set_wait_limit_ns"]
+           "nsa_set_wait_limit_ns", "nsa_paged_append", "nsa_paged_attn_fwd", "nsa_paged_attn_fwd_workspace_size",
+           "nsa_paged_attn_weights", "nsa_paged_evict", "nsa_swa_sink_fwd", "nsa_swa_sink_fwd_workspace_size",
+           "nsa_swa_sink_bwd", "nsa_swa_sink_bwd_workspace_size"]

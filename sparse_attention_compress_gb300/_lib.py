@@ -7,6 +7,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -29,6 +30,12 @@ class NsaShape(ctypes.Structure):
 class NsaLayerSaved(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_cmp", "v_cmp", "o_cmp", "o_slc", "o_swa", "lse_cmp", "lse_slc",
                                                 "lse_swa", "idx")]
+
+
+class NsaPagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("cache_lens", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64)]
 
 
 _SIGS = {
@@ -83,6 +90,17 @@ _SIGS = {
                        _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
     "nsa_layer_fwd": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f,
                        _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
+    "nsa_paged_append": ([_c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
+    "nsa_paged_attn_fwd_workspace_size": ([_c_p, _c_i64, _c_int, _c_int], _c_sz),
+    "nsa_paged_attn_fwd": ([_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
+    "nsa_paged_attn_weights": ([_c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_f, _c_f, _c_p, _c_p], _c_int),
+    "nsa_paged_evict": ([_c_int, _c_int, _c_int, _c_p, _c_int, _c_int, _c_int, _c_p, _c_int, _c_p, _c_p, _c_p],
+                        _c_int),
+    "nsa_swa_sink_fwd_workspace_size": ([_c_p, _c_int, _c_int], _c_sz),
+    "nsa_swa_sink_fwd": ([_c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
+    "nsa_swa_sink_bwd_workspace_size": ([_c_p, _c_int, _c_int], _c_sz),
+    "nsa_swa_sink_bwd": ([_c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                          _c_sz, _c_p], _c_int),
 }
 
 _lib = None
@@ -593,3 +611,238 @@ def nsa_layer_bwd(q, k, v, gate_logits, saved, d_o, kernel=32, stride=16, block_
                                 _ptr(dv), _ptr(dg), _ptr(workspace), workspace.numel(), _stream(stream)),
            "nsa_layer_bwd")
     return dq, dk, dv, dg
+
+
+# ----------------------------------------------------------------------------- paged cache
+# These calls check what the C entry points cannot see: that every tensor lies on one GPU,
+# dense and of its type.  Tensors they allocate belong to the stream the call runs on.
+def _expect(fn, device, **tensors):
+    """Every named (tensor, dtype, shape); None where the caller left a tensor out.  Entries of
+    a shape that are None may be anything."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{fn}: {name} is on {t.device}, q or the pages on {device}")
+        if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be dense (contiguous)")
+
+
+def _on(device, stream):
+    """(context that makes the call's device and stream current, the stream)."""
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    now = torch.cuda.current_stream(device)
+    s = stream if stream is not None else now
+    if s.device != device:
+        raise ValueError(f"the stream belongs to {s.device}, the tensors to {device}")
+    here = s == now and torch.cuda.current_device() == device.index
+    return (contextlib.nullcontext() if here else torch.cuda.stream(s)), s
+
+
+def _new(like_stream, caller_stream, shape, dtype, device):
+    """A tensor of the call's stream that the caller's current stream may also use."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if caller_stream != like_stream:
+        t.record_stream(caller_stream)
+    return t
+
+
+def _page_stride(fn, name, t):
+    """Pages may lie apart (a pool that interleaves K and V); a page itself is dense."""
+    if t.dim() != 4:
+        raise ValueError(f"{fn}: {name} must be [n_pages, page_size, h_kv, d]")
+    n, p, h, d = t.shape
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{fn}: {name} must be {torch.bfloat16}, not {t.dtype}")
+    if t.stride(3) != 1 or (h > 1 and t.stride(2) != d) or (p > 1 and t.stride(1) != h * d):
+        raise ValueError(f"{fn}: the rows of a page of {name} must be dense")
+    return t.stride(0) if n > 1 else p * h * d
+
+
+def _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n_seqs, weights=None):
+    """(struct, page_size, h_kv, d) of a paged cache."""
+    stride = _page_stride(fn, "k_pages", k_pages)
+    n_pages, page, h_kv, d = k_pages.shape
+    if v_pages is not None:
+        if _page_stride(fn, "v_pages", v_pages) != stride or v_pages.shape != k_pages.shape:
+            raise ValueError(f"{fn}: v_pages must have the shape and strides of k_pages")
+        if v_pages.device != k_pages.device:
+            raise ValueError(f"{fn}: v_pages is on {v_pages.device}, k_pages on {k_pages.device}")
+    i32 = torch.int32
+    _expect(fn, k_pages.device, block_table=(block_table, i32, (n_seqs, None)), cache_lens=(cache_lens, i32, (n_seqs,)),
+            weights=(weights, torch.float32, (n_pages, h_kv, page)))
+    c = NsaPagedCache()
+    c.k_pages = k_pages.data_ptr()
+    c.v_pages = None if v_pages is None else v_pages.data_ptr()
+    c.weights = None if weights is None else weights.data_ptr()
+    c.block_table, c.cache_lens = block_table.data_ptr(), cache_lens.data_ptr()
+    c.n_pages, c.page_size, c.max_pages, c.page_stride = n_pages, page, block_table.shape[1], stride
+    return c, page, h_kv, d
+
+
+def _span_shape(fn, q, h_kv, d, device, cu_seqlens, max_seqlen):
+    """(flat q, shape) of new tokens [B, T, H, d] or packed [tokens, H, d]."""
+    if q.dim() not in (3, 4) or q.shape[-1] != d or q.shape[-2] % h_kv:
+        raise ValueError(f"{fn}: expected [..., heads, {d}] with heads a multiple of {h_kv}, got {tuple(q.shape)}")
+    if q.dim() == 4 and cu_seqlens is not None:
+        raise ValueError(f"{fn}: with cu_seqlens the tokens are packed [tokens, heads, d]")
+    _expect(fn, device, tokens=(q, torch.bfloat16, q.shape), cu_seqlens=(cu_seqlens, torch.int32, (None,)))
+    if cu_seqlens is not None and cu_seqlens.numel() < 2:
+        raise ValueError(f"{fn}: cu_seqlens needs at least two entries")
+    return _shape_for(q, h_kv, cu_seqlens, max_seqlen)
+
+
+def _n_seqs(shp):
+    return shp.n_seqs if shp.cu_seqlens else shp.batch
+
+
+def nsa_paged_append(k_new, v_new, k_pages, v_pages, block_table, cache_lens, *, weights=None, cu_seqlens=None,
+                     max_seqlen=None, stream=None):
+    """New tokens' keys and values [B, T, Hkv, d] or packed [tokens, Hkv, d] into the cache, at the
+    last positions of cache_lens; the weights of the written positions become 0."""
+    fn = "nsa_paged_append"
+    ctx, s = _on(k_pages.device, stream)
+    kf, shp = _span_shape(fn, k_new, k_pages.shape[-2], k_pages.shape[-1], k_pages.device, cu_seqlens, max_seqlen)
+    if k_new.shape[-2] != k_pages.shape[-2]:
+        raise ValueError(f"{fn}: k_new has {k_new.shape[-2]} heads, the cache {k_pages.shape[-2]}")
+    _expect(fn, k_pages.device, v_new=(v_new, torch.bfloat16, k_new.shape))
+    c, *_ = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, _n_seqs(shp), weights)
+    with ctx:
+        _check(load().nsa_paged_append(ctypes.byref(shp), _ptr(kf), _ptr(v_new), ctypes.byref(c), _stream(s)), fn)
+
+
+def nsa_paged_attn_fwd_workspace_size(shape: NsaShape, max_cache_len: int = 0, window: int = 0, n_sink: int = 0) -> int:
+    return int(load().nsa_paged_attn_fwd_workspace_size(ctypes.byref(shape), max_cache_len, window, n_sink))
+
+
+def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n_sink=0, scale=0.0, *, cu_seqlens=None,
+                       max_seqlen=None, max_cache_len=None, workspace=None, out=None, lse=None, stream=None):
+    """Attention of new tokens q [B, T, H, d] or packed [tokens, H, d] over the paged cache (which
+    already holds their keys), causal, with an optional window and n_sink tokens that stay
+    visible beside it.  Returns out, shaped like q; fills lse [tokens, H] fp32 if given."""
+    fn = "nsa_paged_attn_fwd"
+    dev = k_pages.device
+    ctx, s = _on(dev, stream)
+    qf, shp = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c, page, _, _ = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, _n_seqs(shp))
+    _expect(fn, dev, out=(out, torch.bfloat16, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
+            workspace=(workspace, torch.uint8, (None,)))
+    if max_cache_len is None:
+        max_cache_len = block_table.shape[1] * page
+    now = torch.cuda.current_stream(dev)
+    with ctx:
+        out = _new(s, now, q.shape, q.dtype, dev) if out is None else out
+        ws = _workspace(nsa_paged_attn_fwd_workspace_size(shp, max_cache_len, window, n_sink), dev, workspace)
+        _check(load().nsa_paged_attn_fwd(ctypes.byref(shp), _ptr(qf), ctypes.byref(c), max_cache_len, window, n_sink,
+                                         float(scale), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
+                                         _stream(s)), fn)
+    return out
+
+
+def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n_sink=0, scale=0.0, *, weights=None,
+                           decay=1.0, cu_seqlens=None, max_seqlen=None, out=None, stream=None):
+    """out[page, kv-head, row] = decay * weights + the attention probabilities that the queries of a
+    nsa_paged_attn_fwd call (same masks, its lse) gave to the key, over the heads of its group.
+    Without weights the sum alone; out may be weights (the default when weights are given)."""
+    fn = "nsa_paged_attn_weights"
+    dev = k_pages.device
+    ctx, s = _on(dev, stream)
+    qf, shp = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c, page, h_kv, _ = _paged_cache(fn, k_pages, None, block_table, cache_lens, _n_seqs(shp), weights)
+    _expect(fn, dev, lse=(lse, torch.float32, qf.shape[:2]),
+            out=(out, torch.float32, (k_pages.shape[0], h_kv, page)))
+    now = torch.cuda.current_stream(dev)
+    with ctx:
+        if out is None:
+            out = weights if weights is not None else _new(s, now, (k_pages.shape[0], h_kv, page), torch.float32, dev)
+        _check(load().nsa_paged_attn_weights(ctypes.byref(shp), _ptr(qf), ctypes.byref(c), _ptr(lse), window, n_sink,
+                                             float(scale), float(decay), _ptr(out), _stream(s)), fn)
+    return out
+
+
+def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_table, budget, n_sink=0, n_recent=0, *,
+                    keep=None, new_lens=None, stream=None):
+    """Cut every cache to at most `budget` keys per kv-head: the first n_sink, the last n_recent and
+    the heaviest others, copied in order to new_table's pages.  Returns (keep [n_seqs, Hkv,
+    budget] int32, -1 padded, and new_lens [n_seqs] int32)."""
+    fn = "nsa_paged_evict"
+    dev = k_pages.device
+    ctx, s = _on(dev, stream)
+    n = cache_lens.shape[0]
+    if weights is None:
+        raise ValueError(f"{fn}: the cache has no weights")
+    c, _, h_kv, d = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n, weights)
+    i32 = torch.int32
+    _expect(fn, dev, new_table=(new_table, i32, (n, None)), keep=(keep, i32, (n, h_kv, budget)),
+            new_lens=(new_lens, i32, (n,)))
+    now = torch.cuda.current_stream(dev)
+    with ctx:
+        keep = _new(s, now, (n, h_kv, max(0, budget)), i32, dev) if keep is None else keep
+        new_lens = _new(s, now, (n,), i32, dev) if new_lens is None else new_lens
+        _check(load().nsa_paged_evict(n, h_kv, d, ctypes.byref(c), budget, n_sink, n_recent, _ptr(new_table),
+                                      new_table.shape[1], _ptr(keep), _ptr(new_lens), _stream(s)), fn)
+    return keep, new_lens
+
+
+# ----------------------------------------------------------------------------- window with sinks
+def nsa_swa_sink_fwd_workspace_size(shape: NsaShape, window: int = 512, n_sink: int = 4) -> int:
+    return int(load().nsa_swa_sink_fwd_workspace_size(ctypes.byref(shape), window, n_sink))
+
+
+def _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen):
+    if k.dim() != q.dim() or q.dim() not in (3, 4):
+        raise ValueError(f"{fn}: q and k must both be [B, T, heads, d] or packed [tokens, heads, d]")
+    kv = (*q.shape[:-2], k.shape[-2], q.shape[-1])
+    _expect(fn, q.device, k=(k, torch.bfloat16, kv), v=(v, torch.bfloat16, kv))
+    return _span_shape(fn, q, k.shape[-2], q.shape[-1], q.device, cu_seqlens, max_seqlen)
+
+
+def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=None, max_seqlen=None, workspace=None,
+                     out=None, lse=None, stream=None):
+    """Sliding window beside which the first n_sink tokens of each sequence stay visible.  Returns
+    out, shaped like q; fills lse [tokens, H] fp32 if given."""
+    fn = "nsa_swa_sink_fwd"
+    ctx, s = _on(q.device, stream)
+    qf, shp = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
+    _expect(fn, q.device, out=(out, torch.bfloat16, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
+            workspace=(workspace, torch.uint8, (None,)))
+    now = torch.cuda.current_stream(q.device)
+    with ctx:
+        out = _new(s, now, q.shape, q.dtype, q.device) if out is None else out
+        ws = _workspace(nsa_swa_sink_fwd_workspace_size(shp, window, n_sink), q.device, workspace)
+        _check(load().nsa_swa_sink_fwd(ctypes.byref(shp), _ptr(qf), _ptr(k), _ptr(v), window, n_sink, float(scale),
+                                       _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(s)), fn)
+    return out
+
+
+def nsa_swa_sink_bwd_workspace_size(shape: NsaShape, window: int = 512, n_sink: int = 4) -> int:
+    return int(load().nsa_swa_sink_bwd_workspace_size(ctypes.byref(shape), window, n_sink))
+
+
+def nsa_swa_sink_bwd(q, k, v, o, lse, d_o, window=512, n_sink=4, scale=0.0, *, cu_seqlens=None, max_seqlen=None,
+                     workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """Backward of nsa_swa_sink_fwd: (dq, dk, dv) shaped like q, k, v from its o and lse."""
+    fn = "nsa_swa_sink_bwd"
+    dev = q.device
+    ctx, s = _on(dev, stream)
+    qf, shp = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
+    b = torch.bfloat16
+    _expect(fn, dev, o=(o, b, q.shape), d_o=(d_o, b, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
+            dq=(dq, b, q.shape), dk=(dk, b, k.shape), dv=(dv, b, k.shape), workspace=(workspace, torch.uint8, (None,)))
+    now = torch.cuda.current_stream(dev)
+    with ctx:
+        dq = _new(s, now, q.shape, b, dev) if dq is None else dq
+        dk = _new(s, now, k.shape, b, dev) if dk is None else dk
+        dv = _new(s, now, v.shape, b, dev) if dv is None else dv
+        ws = _workspace(nsa_swa_sink_bwd_workspace_size(shp, window, n_sink), dev, workspace)
+        _check(load().nsa_swa_sink_bwd(ctypes.byref(shp), _ptr(qf), _ptr(k), _ptr(v), window, n_sink, float(scale),
+                                       _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
+                                       0 if ws is None else ws.numel(), _stream(s)), fn)
+    return dq, dk, dv

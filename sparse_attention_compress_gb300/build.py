@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnsa.so")
 SOURCES = ["api.cu", "compress.cu", "select.cu", "sparse_fwd.cu", "sparse_bwd.cu", "sparse_bwd_tc.cu", "dense_attn.cu", "dense_tc.cu",
-           "decode.cu", "decode_nosa.cu", "noalloc.cu", "nosa.cu"]
+           "decode.cu", "decode_nosa.cu", "noalloc.cu", "nosa.cu",
+           "span_attn.cu", "span_bwd.cu", "span_weights.cu", "paged_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -117,13 +117,16 @@ const char* nsa_last_error(void) { return g_err; }
 nsa_status nsa_device_status(int32_t* status, int reset) {
   NSA_RANGE();
   NSA_REQUIRE(status != nullptr, NSA_ERR_INVALID, "nsa_device_status: status is NULL");
-  int32_t a = 0, b = 0, c = 0, f = 0, k = 0;
+  int32_t a = 0, b = 0, c = 0, f = 0, k = 0, m = 0, w = 0, x = 0;
   cudaError_t e = status_word_dense_tc(&a, reset != 0);
   if (e == cudaSuccess) e = status_word_decode(&b, reset != 0);
   if (e == cudaSuccess) e = status_word_decode_nosa(&c, reset != 0);
   if (e == cudaSuccess) e = status_word_sparse_fwd(&f, reset != 0);
   if (e == cudaSuccess) e = status_word_sparse_bwd_tc(&k, reset != 0);
-  *status = a ? a : b ? b : c ? c : f ? f : k;
+  if (e == cudaSuccess) e = status_word_span_attn(&m, reset != 0);
+  if (e == cudaSuccess) e = status_word_span_weights(&w, reset != 0);
+  if (e == cudaSuccess) e = status_word_span_bwd(&x, reset != 0);
+  *status = a ? a : b ? b : c ? c : f ? f : k ? k : m ? m : w ? w : x;
   return cuda_status(e, "nsa_device_status");
 }
 
@@ -135,6 +138,9 @@ nsa_status nsa_set_wait_limit_ns(uint64_t ns) {
   if (e == cudaSuccess) e = wait_limit_decode_nosa(v);
   if (e == cudaSuccess) e = wait_limit_sparse_fwd(v);
   if (e == cudaSuccess) e = wait_limit_sparse_bwd_tc(v);
+  if (e == cudaSuccess) e = wait_limit_span_attn(v);
+  if (e == cudaSuccess) e = wait_limit_span_weights(v);
+  if (e == cudaSuccess) e = wait_limit_span_bwd(v);
   return cuda_status(e, "nsa_set_wait_limit_ns");
 }
 
@@ -1062,6 +1068,236 @@ nsa_status nsa_layer_bwd(const nsa_shape* shape, const void* q, const void* k, c
       (e = launch_add3(dv3, dv3 + ksz, dv3 + 2 * ksz, dv, s.tokens * hkv * d, stream)))
     return cuda_status(e, "layer bwd/sum over branches");
   return NSA_OK;
+}
+
+// ---------------------------------------------------------------------------- paged cache
+// Query heads, dtype and dimensions shared by the paged-cache and sink-window calls.
+static nsa_status check_span_shape(const nsa_shape* shape, Seqs* s, const char* fn) {
+  if (nsa_status st = make_seqs(shape, s, fn)) return st;
+  NSA_REQUIRE(shape->dtype == NSA_BF16, NSA_ERR_UNSUPPORTED, "%s: bf16 only", fn);
+  NSA_REQUIRE(shape->d == 64 || shape->d == 128, NSA_ERR_UNSUPPORTED, "%s: d must be 64 or 128", fn);
+  NSA_REQUIRE(shape->h / shape->h_kv <= 128, NSA_ERR_UNSUPPORTED, "%s: h/h_kv must be <= 128", fn);
+  NSA_REQUIRE(s->n_seqs <= 65535 && shape->h_kv <= 4096, NSA_ERR_UNSUPPORTED,
+              "%s: at most 65535 sequences and 4096 kv-heads", fn);
+  NSA_REQUIRE(s->tokens <= (int64_t)1 << 30 && s->max_len <= 1 << 30, NSA_ERR_UNSUPPORTED,
+              "%s: at most 2^30 tokens", fn);
+  return NSA_OK;
+}
+
+static nsa_status check_span(int window, int n_sink, const char* fn) {
+  NSA_REQUIRE(window >= 0 && n_sink >= 0, NSA_ERR_INVALID, "%s: negative window or n_sink", fn);
+  NSA_REQUIRE(window <= 1 << 30 && n_sink <= 1 << 30, NSA_ERR_UNSUPPORTED, "%s: window and n_sink must be <= 2^30", fn);
+  return NSA_OK;
+}
+
+// Validate a paged cache and build the kernel-side view of it.
+static nsa_status check_cache(const nsa_paged_cache* c, int h_kv, int d, bool need_v, PagedView* out, const char* fn) {
+  NSA_REQUIRE(c != nullptr, NSA_ERR_INVALID, "%s: null cache", fn);
+  NSA_REQUIRE(c->n_pages >= 1 && c->max_pages >= 1, NSA_ERR_INVALID, "%s: n_pages and max_pages must be positive", fn);
+  NSA_REQUIRE(c->page_size >= 16 && c->page_size <= 256 && (c->page_size & (c->page_size - 1)) == 0,
+              NSA_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64, 128 or 256 (got %d)", fn, c->page_size);
+  NSA_REQUIRE((int64_t)c->max_pages * c->page_size <= (int64_t)1 << 30, NSA_ERR_UNSUPPORTED,
+              "%s: max_pages * page_size must be <= 2^30", fn);
+  NSA_REQUIRE(c->page_stride >= (int64_t)c->page_size * h_kv * d && c->page_stride % 8 == 0, NSA_ERR_INVALID,
+              "%s: page_stride must be >= page_size * h_kv * d and a multiple of 8", fn);
+  NSA_REQUIRE(c->page_stride < (int64_t)1 << 38, NSA_ERR_UNSUPPORTED, "%s: page_stride must be < 2^38", fn);
+  NSA_REQUIRE(c->k_pages != nullptr && aligned16(c->k_pages), NSA_ERR_INVALID,
+              "%s: k_pages must be non-null and 16-byte aligned", fn);
+  if (need_v)
+    NSA_REQUIRE(c->v_pages != nullptr && aligned16(c->v_pages), NSA_ERR_INVALID,
+                "%s: v_pages must be non-null and 16-byte aligned", fn);
+  NSA_REQUIRE(c->block_table != nullptr && c->cache_lens != nullptr, NSA_ERR_INVALID,
+              "%s: block_table and cache_lens must be non-null", fn);
+  NSA_REQUIRE(((reinterpret_cast<uintptr_t>(c->block_table) | reinterpret_cast<uintptr_t>(c->cache_lens) |
+                reinterpret_cast<uintptr_t>(c->weights)) & 3u) == 0, NSA_ERR_INVALID,
+              "%s: block_table, cache_lens and weights must be 4-byte aligned", fn);
+  out->table = c->block_table;
+  out->lens = c->cache_lens;
+  out->n_pages = c->n_pages;
+  out->max_pages = c->max_pages;
+  out->page_stride = c->page_stride;
+  out->page_log2 = 0;
+  while ((1 << out->page_log2) < c->page_size) ++out->page_log2;
+  return NSA_OK;
+}
+
+static nsa_status check_workspace(const void* workspace, size_t bytes, size_t need, const char* fn) {
+  if (need == 0) return NSA_OK;
+  NSA_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, NSA_ERR_INVALID,
+              "%s: workspace must be non-null and 256-byte aligned", fn);
+  NSA_REQUIRE(bytes >= need, NSA_ERR_INVALID, "%s: workspace %zu < %zu bytes", fn, bytes, need);
+  return NSA_OK;
+}
+
+nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, const void* v_new, const nsa_paged_cache* cache,
+                            cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache(cache, shape->h_kv, shape->d, true, &c, __func__)) return st;
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(k_new);
+  NSA_PTR(v_new);
+  return cuda_status(launch_paged_append(s, k_new, v_new, c, cache->k_pages, cache->v_pages, cache->weights,
+                                         shape->h_kv, shape->d, stream),
+                     "nsa_paged_append");
+}
+
+// The bound of the cached lengths that divides the keys (none given: no bound).
+static int span_keys(int64_t max_cache_len) {
+  return max_cache_len <= 0 || max_cache_len > (int64_t)1 << 30 ? 1 << 30 : (int)max_cache_len;
+}
+
+size_t nsa_paged_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink) {
+  Seqs s;
+  if (check_span_shape(shape, &s, __func__) != NSA_OK || check_span(window, n_sink, __func__) != NSA_OK) return 0;
+  return span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, span_keys(max_cache_len), window, n_sink);
+}
+
+nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
+                              int64_t max_cache_len, int window, int n_sink, float scale, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache(cache, shape->h_kv, shape->d, true, &c, __func__)) return st;
+  if (nsa_status st = check_span(window, n_sink, __func__)) return st;
+  NSA_REQUIRE(max_cache_len >= 0, NSA_ERR_INVALID, "nsa_paged_attn_fwd: negative max_cache_len");
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(q);
+  NSA_PTR(o);
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(NSA_ERR_INVALID, "nsa_paged_attn_fwd: lse misaligned");
+  const int keys = span_keys(max_cache_len);
+  const size_t need = span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, keys, window, n_sink);
+  if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
+  return cuda_status(launch_span_attn(s, q, &c, cache->k_pages, cache->v_pages, shape->h, shape->h_kv, shape->d, keys,
+                                      window, n_sink, scale, o, lse, workspace, stream),
+                     "nsa_paged_attn_fwd");
+}
+
+nsa_status nsa_paged_attn_weights(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
+                                  const float* lse, int window, int n_sink, float scale, float decay,
+                                  float* weights_out, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache(cache, shape->h_kv, shape->d, false, &c, __func__)) return st;
+  if (nsa_status st = check_span(window, n_sink, __func__)) return st;
+  NSA_REQUIRE(weights_out != nullptr && (reinterpret_cast<uintptr_t>(weights_out) & 3u) == 0, NSA_ERR_INVALID,
+              "nsa_paged_attn_weights: weights_out must be non-null and 4-byte aligned");
+  NSA_REQUIRE(s.tokens == 0 || (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u) == 0), NSA_ERR_INVALID,
+              "nsa_paged_attn_weights: lse must be non-null and 4-byte aligned");
+  if (s.n_seqs == 0) return NSA_OK;
+  if (s.tokens > 0) NSA_PTR(q);
+  if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
+  return cuda_status(launch_span_weights(s, q, c, cache->k_pages, shape->h, shape->h_kv, shape->d, window, n_sink,
+                                         scale, decay, lse, cache->weights, weights_out, stream),
+                     "nsa_paged_attn_weights");
+}
+
+nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_cache* cache, int budget, int n_sink,
+                           int n_recent, const int32_t* new_table, int new_max_pages, int32_t* keep,
+                           int32_t* new_lens, cudaStream_t stream) {
+  NSA_RANGE();
+  PagedView c;
+  NSA_REQUIRE(n_seqs >= 0 && h_kv > 0, NSA_ERR_INVALID, "nsa_paged_evict: bad sizes");
+  NSA_REQUIRE(d == 64 || d == 128, NSA_ERR_UNSUPPORTED, "nsa_paged_evict: d must be 64 or 128");
+  NSA_REQUIRE(n_seqs <= 65535 && h_kv <= 4096, NSA_ERR_UNSUPPORTED,
+              "nsa_paged_evict: at most 65535 sequences and 4096 kv-heads");
+  if (nsa_status st = check_cache(cache, h_kv, d, true, &c, __func__)) return st;
+  NSA_REQUIRE(cache->weights != nullptr, NSA_ERR_INVALID, "nsa_paged_evict: the cache has no weights");
+  NSA_REQUIRE(budget >= 1 && n_sink >= 0 && n_recent >= 0 && (int64_t)n_sink + n_recent <= budget, NSA_ERR_INVALID,
+              "nsa_paged_evict: needs budget >= 1, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= budget");
+  const int64_t cap = (int64_t)cache->max_pages * cache->page_size;
+  NSA_REQUIRE(new_max_pages >= 1 && (int64_t)new_max_pages * cache->page_size >= (budget < cap ? budget : cap),
+              NSA_ERR_INVALID, "nsa_paged_evict: new_table's rows do not hold the budget");
+  NSA_REQUIRE((int64_t)new_max_pages * cache->page_size <= (int64_t)1 << 30, NSA_ERR_UNSUPPORTED,
+              "nsa_paged_evict: new_max_pages * page_size must be <= 2^30");
+  NSA_REQUIRE(new_table != nullptr && keep != nullptr && new_lens != nullptr &&
+                  ((reinterpret_cast<uintptr_t>(new_table) | reinterpret_cast<uintptr_t>(keep) |
+                    reinterpret_cast<uintptr_t>(new_lens)) & 3u) == 0,
+              NSA_ERR_INVALID, "nsa_paged_evict: new_table, keep and new_lens must be non-null and 4-byte aligned");
+  PagedView to = c;
+  to.table = new_table;
+  to.max_pages = new_max_pages;
+  return cuda_status(launch_paged_evict(n_seqs, c, to, cache->k_pages, cache->v_pages, cache->weights, h_kv, d,
+                                        budget, n_sink, n_recent, keep, new_lens, stream),
+                     "nsa_paged_evict");
+}
+
+// ---------------------------------------------------------------------------- window with sinks
+static nsa_status check_sink_window(const nsa_shape* shape, int window, int n_sink, Seqs* s, const char* fn) {
+  if (nsa_status st = check_span_shape(shape, s, fn)) return st;
+  NSA_REQUIRE(window >= 1, NSA_ERR_INVALID, "%s: window must be >= 1", fn);
+  return check_span(window, n_sink, fn);
+}
+
+size_t nsa_swa_sink_fwd_workspace_size(const nsa_shape* shape, int window, int n_sink) {
+  Seqs s;
+  if (check_sink_window(shape, window, n_sink, &s, __func__) != NSA_OK) return 0;
+  return span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, s.max_len, window, n_sink);
+}
+
+nsa_status nsa_swa_sink_fwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,
+                            int n_sink, float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  if (nsa_status st = check_sink_window(shape, window, n_sink, &s, __func__)) return st;
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(q);
+  NSA_PTR(k);
+  NSA_PTR(v);
+  NSA_PTR(o);
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(NSA_ERR_INVALID, "nsa_swa_sink_fwd: lse misaligned");
+  const size_t need = span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, s.max_len, window, n_sink);
+  if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
+  return cuda_status(launch_span_attn(s, q, nullptr, k, v, shape->h, shape->h_kv, shape->d, s.max_len, window, n_sink,
+                                      scale, o, lse, workspace, stream),
+                     "nsa_swa_sink_fwd");
+}
+
+static nsa_status check_sink_bwd(const nsa_shape* shape, int window, int n_sink, Seqs* s, const char* fn) {
+  if (nsa_status st = check_sink_window(shape, window, n_sink, s, fn)) return st;
+  NSA_REQUIRE(n_sink <= 1024, NSA_ERR_UNSUPPORTED, "%s: n_sink must be <= 1024", fn);
+  return NSA_OK;
+}
+
+size_t nsa_swa_sink_bwd_workspace_size(const nsa_shape* shape, int window, int n_sink) {
+  Seqs s;
+  if (check_sink_bwd(shape, window, n_sink, &s, __func__) != NSA_OK) return 0;
+  return span_bwd_workspace_bytes(s, shape->h, shape->h_kv, shape->d, window, n_sink);
+}
+
+nsa_status nsa_swa_sink_bwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,
+                            int n_sink, float scale, const void* o, const float* lse, const void* d_o, void* dq,
+                            void* dk, void* dv, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  if (nsa_status st = check_sink_bwd(shape, window, n_sink, &s, __func__)) return st;
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(q);
+  NSA_PTR(k);
+  NSA_PTR(v);
+  NSA_PTR(o);
+  NSA_PTR(d_o);
+  NSA_PTR(dq);
+  NSA_PTR(dk);
+  NSA_PTR(dv);
+  NSA_REQUIRE(lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u) == 0, NSA_ERR_INVALID,
+              "nsa_swa_sink_bwd: lse must be non-null and 4-byte aligned");
+  const size_t need = span_bwd_workspace_bytes(s, shape->h, shape->h_kv, shape->d, window, n_sink);
+  if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
+  return cuda_status(launch_span_bwd(s, q, k, v, shape->h, shape->h_kv, shape->d, window, n_sink, scale, o, lse, d_o,
+                                     dq, dk, dv, workspace, stream),
+                     "nsa_swa_sink_bwd");
 }
 
 }  // extern "C"

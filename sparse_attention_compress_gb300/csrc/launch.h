@@ -160,4 +160,43 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 // The NOSA variant (a.cis set): decode_nosa.cu; launch_decode calls it after the memset.
 cudaError_t launch_decode_nosa(const DecodeArgs& a, const DecodeLayout& l, cudaStream_t st);
 
+// A paged K/V cache (csrc/span.cuh): pages of 2^page_log2 rows, page_stride elements apart.
+struct PagedView {
+  const int32_t* table;  // [n_seqs, max_pages]
+  const int32_t* lens;   // [n_seqs]
+  int n_pages, page_log2, max_pages;
+  int64_t page_stride;
+};
+
+// Attention of each sequence's queries over a paged cache (cache != null) or over the packed
+// rows themselves (csrc/span_attn.cu).  max_keys bounds the cached lengths (it only sets how
+// the keys are divided over CTAs).
+size_t span_attn_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink);
+cudaError_t launch_span_attn(const Seqs& s, const void* q, const PagedView* cache, const void* k, const void* v, int h,
+                             int hkv, int d, int max_keys, int window, int n_sink, float scale, void* o, float* lse,
+                             void* workspace, cudaStream_t st);
+// Backward of the packed case under a window with sinks (csrc/span_bwd.cu).
+size_t span_bwd_workspace_bytes(const Seqs& s, int h, int hkv, int d, int window, int n_sink);
+cudaError_t launch_span_bwd(const Seqs& s, const void* q, const void* k, const void* v, int h, int hkv, int d,
+                            int window, int n_sink, float scale, const void* o, const float* lse, const void* dout,
+                            void* dq, void* dk, void* dv, void* workspace, cudaStream_t st);
+// Accumulated attention weights of the cached keys (csrc/span_weights.cu): for every cached
+// key, w_out = decay * w_in + the sum of its probabilities over queries and group heads.
+cudaError_t launch_span_weights(const Seqs& s, const void* q, const PagedView& cache, const void* k, int h, int hkv,
+                                int d, int window, int n_sink, float scale, float decay,
+                                const float* lse, const float* w_in, float* w_out, cudaStream_t st);
+// Paged-cache upkeep (csrc/paged_cache.cu).
+cudaError_t launch_paged_append(const Seqs& s, const void* k_new, const void* v_new, const PagedView& cache,
+                                void* k_pages, void* v_pages, float* weights, int hkv, int d, cudaStream_t st);
+cudaError_t launch_paged_evict(int n_seqs, const PagedView& cache, const PagedView& to, void* k_pages, void* v_pages,
+                               float* weights, int hkv, int d, int budget, int n_sink, int n_recent,
+                               int32_t* keep, int32_t* new_lens, cudaStream_t st);
+
+cudaError_t status_word_span_attn(int32_t* out, bool reset);
+cudaError_t wait_limit_span_attn(unsigned long long ns);
+cudaError_t status_word_span_weights(int32_t* out, bool reset);
+cudaError_t wait_limit_span_weights(unsigned long long ns);
+cudaError_t status_word_span_bwd(int32_t* out, bool reset);
+cudaError_t wait_limit_span_bwd(unsigned long long ns);
+
 }  // namespace nsa

@@ -1,0 +1,230 @@
+// Pieces shared by the kernels whose queries see a span of a sequence's keys: attention
+// over a paged cache (span_attn.cu), the accumulated attention weights (span_weights.cu)
+// and the sliding window with sinks and its backward (span_attn.cu, span_bwd.cu).
+//
+// A query at position p sees key j when j <= p and (window == 0, or j > p - window, or
+// j < n_sink).  The rows of one CTA are consecutive positions p_first .. p_last, so the
+// keys any of them sees are at most two spans: the sinks [0, n_sink) and
+// [p_first - window + 1, p_last].  Both are walked in 128-key tiles whose last one is cut
+// to a multiple of 16 keys (the granularity of the tensor-core N and K extents), so a few
+// sinks cost a 16-key tile and not a 128-key one.
+#pragma once
+
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace nsa {
+namespace span {
+
+constexpr int KT = 128;     // keys per tile
+constexpr int ROWS = 128;   // (token, head) rows per tile
+constexpr int GRAN = 16;    // key granularity of a tile's width
+
+// Keys and values.  table == nullptr: packed rows [tokens, hkv, D] of the query sequences
+// themselves.  Otherwise pages [n_pages][page_stride elements] of 2^page_log2 rows
+// [hkv, D]; row `seq` of the table lists a sequence's pages.
+struct Keys {
+  const __nv_bfloat16 *k, *v;
+  const int32_t* table;
+  const int32_t* lens;  // cached tokens of each sequence, its new tokens included
+  int n_pages, page_log2, max_pages;
+  int64_t page_stride;
+};
+
+// Cached tokens of a sequence, within what its table row can hold.
+__device__ __forceinline__ int cached_len(const Keys& c, int seq) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_log2;
+  const int n = c.lens[seq];
+  return n < 0 ? 0 : (n > cap ? (int)cap : n);
+}
+
+// Page of key `key` of a sequence, or -1 when the table holds no valid page for it.
+__device__ __forceinline__ int page_of(const Keys& c, int seq, int key) {
+  const int pid = __ldg(c.table + (int64_t)seq * c.max_pages + (key >> c.page_log2));
+  return (unsigned)pid < (unsigned)c.n_pages ? pid : -1;
+}
+
+inline Keys keys_of(const PagedView* c, const void* k, const void* v) {
+  Keys r{};
+  r.k = (const __nv_bfloat16*)k;
+  r.v = (const __nv_bfloat16*)v;
+  if (c) {
+    r.table = c->table;
+    r.lens = c->lens;
+    r.n_pages = c->n_pages;
+    r.page_log2 = c->page_log2;
+    r.max_pages = c->max_pages;
+    r.page_stride = c->page_stride;
+  }
+  return r;
+}
+
+__host__ __device__ __forceinline__ int up16(int x) { return (x + GRAN - 1) & ~(GRAN - 1); }
+
+// The key tiles that rows at positions p_first .. p_last see (at least in part).
+struct Tiles {
+  int sink_end, lo, hi, n_sink_tiles, n;
+  __device__ __forceinline__ Tiles(int p_first, int p_last, int window, int n_sink) {
+    hi = p_last + 1;
+    lo = window > 0 ? max(0, p_first - window + 1) & ~(GRAN - 1) : 0;
+    sink_end = up16(n_sink);
+    if (window == 0 || lo <= sink_end) lo = sink_end = 0;  // one span
+    n_sink_tiles = (sink_end + KT - 1) / KT;
+    n = hi > lo ? n_sink_tiles + (hi - lo + KT - 1) / KT : 0;
+  }
+  __device__ __forceinline__ int key0(int i) const {
+    return i < n_sink_tiles ? i * KT : lo + (i - n_sink_tiles) * KT;
+  }
+  // keys of tile i, rounded up to 16 (rows past the sequence's keys are masked and zero)
+  __device__ __forceinline__ int width(int i) const {
+    return min(KT, up16((i < n_sink_tiles ? sink_end : hi) - key0(i)));
+  }
+};
+
+// One warp fills a tile of `w` (a multiple of 16) rows x D, keys key0 .. key0 + w - 1 of
+// kv-head g, in the 128-byte-swizzled layout (64-column groups KT * 128 bytes apart), and
+// lane 0 arrives on `bar` with the bytes still to come.  The rows travel as TMA boxes,
+// issued by as many lanes as there are boxes: whole pages (at most 128 rows) when the tile
+// is whole and starts on a page, else 16 rows.  What holds no key (rows at or past kv_len,
+// rows of a page the table does not name) is written as zeros by plain bounds-checked
+// copies, so whatever lies there (NaN included) never meets a product.
+template <int D, bool PAGED>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* big, const CUtensorMap* small,
+                                              const __nv_bfloat16* src, const Keys& c, int hkv, int g, int seq,
+                                              int64_t start, int key0, int w, int kv_len, uint32_t bar, int lane) {
+  constexpr int H = D / 64;
+  const int page = PAGED ? 1 << c.page_log2 : KT;
+  const int box = page < KT ? page : KT;
+  const bool whole = w == KT && key0 + KT <= kv_len && (!PAGED || (key0 & (box - 1)) == 0);
+  const int br = whole ? box : GRAN;
+  const int n = w / br;
+  const int ci = lane / H, hf = lane % H;
+  const bool mine = ci < n;
+  const int key = key0 + ci * br;
+  int pid = 0;
+  if (PAGED) pid = mine && key < kv_len ? page_of(c, seq, key) : 0;
+  const bool ok = pid >= 0;
+  const bool plain = mine && (!ok || key + br > kv_len);
+  if (mine && !plain) {
+    const uint32_t to = dst + hf * (KT * 128) + ci * br * 128;
+    if (PAGED)
+      tc::tma3d(to, whole ? big : small, g * D + hf * 64, key & (page - 1), pid, bar);
+    else
+      tc::tma2d(to, whole ? big : small, g * D + hf * 64, (int)(start + key), bar);
+  }
+  const uint32_t bad = __ballot_sync(0xffffffffu, mine && !ok && hf == 0);
+  uint32_t todo = __ballot_sync(0xffffffffu, plain && hf == 0);
+  const int bytes = (n - __popc(todo)) * br * D * 2;
+  if (todo) {
+    while (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int cc = l / H;
+      const bool okc = !((bad >> l) & 1u);
+      const int64_t pidc = __shfl_sync(0xffffffffu, pid, l);
+      for (int e = lane; e < br * (D / 8); e += 32) {
+        const int r = cc * br + e / (D / 8), ch = e % (D / 8);
+        const int kk = key0 + r;
+        const bool in = okc && kk < kv_len;
+        const int64_t row = PAGED ? pidc * c.page_stride + (int64_t)(kk & (page - 1)) * hkv * D
+                                  : (start + kk) * hkv * D;
+        cp_async16(dst + (ch >> 3) * (KT * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   in ? (const void*)(src + row + g * D + ch * 8) : (const void*)src, in ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  }
+  __syncwarp();
+  if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)bytes);
+}
+
+// A bit for every 16-row group of a tile that the table names no page for (a warp's call).
+__device__ __forceinline__ uint32_t missing_groups(const Keys& c, int seq, int key0, int w, int kv_len, int lane) {
+  const int key = key0 + lane * GRAN;
+  return __ballot_sync(0xffffffffu, lane * GRAN < w && key < kv_len && page_of(c, seq, key) < 0);
+}
+
+// Shared-memory descriptor of an MN-major operand with 128-byte swizzling: rows of 64
+// MN-elements (128 B) along K in 1024-byte atoms of 8 rows; lbo: bytes between groups of
+// 64 MN-elements.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFF) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kBMn = 1u << 16;  // instruction descriptor: B is MN-major
+
+// S[128 x w] = A[128 x D] B[w x D]^T, both K-major tiles (64-column groups 16 KB apart).
+template <int D>
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int w) {
+  const uint32_t id = tc::idesc(ROWS, w);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    const uint32_t off = (s >> 2) * (KT * 128) + (s & 3) * 32;
+    tc::mma_ss(d_tmem, tc::sdesc(a + off), tc::sdesc(b + off), id, s > 0);
+  }
+}
+// O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, int w, bool first) {
+  constexpr uint32_t id = tc::idesc(ROWS, D) | kBMn;
+#pragma unroll
+  for (int s = 0; s < KT / 16; ++s)
+    if (s * 16 < w) tc::mma_ts(d_tmem, p_tmem + s * 8, sdesc_mn(v + s * 2048, KT * 128), id, (first && s == 0) ? 0u : 1u);
+}
+
+// TMEM stores of 16 words without the wait (the caller issues tmem_wait_st).
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_alloc(uint32_t holder, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(holder), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// ---------------------------------------------------------------------- host side
+// Maps of K (or V): the tile box and the 16-row box.
+inline bool key_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, const Keys& c, int hkv, int D,
+                     int64_t packed_rows) {
+  for (int i = 0; i < 2; ++i) {
+    if (c.table) {
+      const uint32_t page = 1u << c.page_log2;
+      const uint64_t dims[3] = {(uint64_t)hkv * D, page, (uint64_t)c.n_pages};
+      const uint64_t strides[2] = {(uint64_t)hkv * D * 2, (uint64_t)c.page_stride * 2};
+      const uint32_t box[3] = {64, i ? (uint32_t)GRAN : (page < KT ? page : (uint32_t)KT), 1};
+      if (!tc::make_map(i ? small : big, ptr, 3, dims, strides, box)) return false;
+    } else {
+      const uint64_t dims[2] = {(uint64_t)hkv * D, (uint64_t)packed_rows};
+      const uint64_t strides[1] = {(uint64_t)hkv * D * 2};
+      const uint32_t box[2] = {64, i ? (uint32_t)GRAN : (uint32_t)KT};
+      if (!tc::make_map(i ? small : big, ptr, 2, dims, strides, box)) return false;
+    }
+  }
+  return true;
+}
+// Map of query rows [tokens, h, D]: a box is 64 columns of R heads of tpc tokens.
+inline bool query_map(CUtensorMap* m, const void* ptr, int64_t tokens, int h, int D, int R, int tpc) {
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)h, (uint64_t)tokens};
+  const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)h * D * 2};
+  const uint32_t box[3] = {64, (uint32_t)R, (uint32_t)tpc};
+  return tc::make_map(m, ptr, 3, dims, strides, box);
+}
+
+}  // namespace span
+}  // namespace nsa

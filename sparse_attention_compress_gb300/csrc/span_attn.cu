@@ -1,0 +1,496 @@
+// Attention of a chunk of new tokens over a paged cache, and of packed sequences under a
+// sliding window with sinks: per (token, head) row at position p,
+//   s_j = scale q.k_j over the keys p sees (span.cuh),  lse = log sum_j exp s_j,
+//   o = sum_j exp(s_j - lse) v_j;   a row that sees no key gets o = 0, lse = -inf.
+// One pass over the keys with a running maximum and sum, base-2 exponentials, all
+// statistics and accumulators in fp32; P enters the second product as bf16 (half a step,
+// 2^-9 relative on each weight, which averages out over a row's keys and stays below the
+// rounding of the bf16 output itself).
+//
+// A tile is 128 rows = 128 / group tokens x the heads of a kv-group, so each K / V tile is
+// read once for the whole group.  A CTA holds two such row tiles ("halves", four softmax
+// warps each, one row a thread) over one K / V ring: while one half's softmax runs, the
+// tensor cores work for the other.  With few rows (a decode step, or chunks whose rows fit
+// one tile: SPLIT) both halves take the same rows and alternate key tiles instead, and the
+// keys are also divided over CTAs; every part leaves (max, sum, unnormalised o) in the
+// workspace and combine_kernel joins them in a fixed order.  Roles: warps 0-7 softmax,
+// warp 8 loads (TMA, span.cuh), warps 9 and 10 issue the products of their half.
+// TMEM (512 columns): S of half x at 128 x with P over its first columns, O at 256 + 128 x.
+// V is used as it lies (MN-major B operand), so nothing is transposed.
+#include <algorithm>
+
+#include "launch.h"
+#include "span.cuh"
+
+namespace nsa {
+namespace span {
+
+constexpr int kThreads = 352;
+constexpr uint32_t kTmemCols = 512;
+
+template <int D, bool SPLIT>
+struct Cfg {
+  static constexpr int NQ = SPLIT ? 1 : 2;               // row tiles in shared memory
+  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int KV_BYTES = KT * D * 2;
+  static constexpr int NS = D == 64 ? 4 : (SPLIT ? 3 : 2);  // ring stages (what 227 KB hold)
+  static constexpr int SMEM = NQ * Q_BYTES + 2 * NS * KV_BYTES + 1024;
+};
+
+struct AttnParams {
+  Seqs seqs;
+  Keys keys;
+  __nv_bfloat16* o;
+  float* lse;     // optional
+  float* part_o;  // [parts][tokens * h][D] fp32, or null: one part, written to o
+  float2* part_ml;  // [parts][tokens * h] (running max in base-2 units, sum)
+  int h, hkv, R, tpc, window, n_sink, n_splits;
+  float scale_log2;
+};
+
+template <int NS>
+struct Bars {
+  enum : int {
+    Q = 0,
+    KFULL = 1,
+    KEMPTY = KFULL + NS,
+    VFULL = KEMPTY + NS,
+    VEMPTY = VFULL + NS,
+    SFULL = VEMPTY + NS,  // [2] by half
+    PFULL = SFULL + 2,    // [2]
+    ODONE = PFULL + 2,    // [2]
+    DRAIN = ODONE + 2,
+    COUNT = DRAIN + 1
+  };
+};
+
+// Index of the last of tiles 0..last that went to ring stage st (-1 if none).
+__device__ __forceinline__ int last_in_stage(int last, int st, int ns) {
+  return last < st ? -1 : last - (last - st) % ns;
+}
+
+template <int D, bool PAGED, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_v16, const AttnParams p) {
+  using C = Cfg<D, SPLIT>;
+  using B = Bars<C::NS>;
+  constexpr int NS = C::NS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[B::COUNT];
+  __shared__ uint32_t s_tmem, s_bad[8];  // s_bad: missing 16-row groups of tile i, at i % 8
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_s = base, k_s = q_s + C::NQ * C::Q_BYTES, v_s = k_s + NS * C::KV_BYTES;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  volatile int* abort = &s_abort;
+
+  if (tc::device_status_set()) return;
+  const int seq = blockIdx.y, g = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
+  const int64_t start = seq_start(p.seqs, seq);
+  const int Lq = seq_len(p.seqs, seq);
+  const int rows_tok = C::NQ * p.tpc;  // tokens of this CTA
+  const int t0 = ((Lq + rows_tok - 1) / rows_tok - 1 - (int)blockIdx.x) * rows_tok;  // longest spans first
+  if (t0 < 0) return;
+  const int kv_len = PAGED ? cached_len(p.keys, seq) : Lq;
+  const int off = kv_len - Lq;  // position of the sequence's first query
+  const Tiles tiles(off + t0, off + min(t0 + rows_tok, Lq) - 1, p.window, p.n_sink);
+  const int a = (int)((int64_t)tiles.n * split / p.n_splits);
+  const int n = (int)((int64_t)tiles.n * (split + 1) / p.n_splits) - a;  // this CTA's tiles: a .. a + n - 1
+  const bool two = SPLIT || t0 + p.tpc < Lq;  // the second half has rows
+  // tiles of half x: every one, or (SPLIT) every second one
+  auto count_of = [&](int x) { return SPLIT ? (n + 1 - x) >> 1 : (x == 0 || two ? n : 0); };
+  auto tile_of = [&](int x, int it) { return SPLIT ? 2 * it + x : it; };
+
+  if (tid == 0) {
+    const int users = !SPLIT && two ? 2 : 1;
+    tc::mbar_init(bar(B::Q), 1);
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(bar(B::KFULL + i), 1);
+      tc::mbar_init(bar(B::KEMPTY + i), users);
+      tc::mbar_init(bar(B::VFULL + i), 1);
+      tc::mbar_init(bar(B::VEMPTY + i), users);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(B::SFULL + i), 1);
+      tc::mbar_init(bar(B::PFULL + i), 128);
+      tc::mbar_init(bar(B::ODONE + i), 1);
+    }
+    tc::mbar_init(bar(B::DRAIN), 2);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  int last_k = -1, last_v = -1;
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0 && n > 0) {
+      const int nq = two && !SPLIT ? 2 : 1;
+      tc::mbar_expect_tx(bar(B::Q), (uint32_t)(nq * p.tpc * p.R * D * 2));
+      for (int x = 0; x < nq; ++x)
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma3d(q_s + x * C::Q_BYTES + c * (ROWS * 128), &tm_q, c * 64, g * p.R, (int)(start + t0 + x * p.tpc),
+                    bar(B::Q));
+    }
+    for (int j = 0; j < n; ++j) {
+      const int st = j % NS, key0 = tiles.key0(a + j), w = tiles.width(a + j);
+      if (j >= NS && !tc::warp_wait(bar(B::KEMPTY + st), ((j / NS) - 1) & 1, abort)) break;
+      const uint32_t kb = bar(B::KFULL + st);
+      // the flags of tile j are read by its softmax after S(j), so they are in place before
+      // the K tile's arrival; the missing pages of K and V are the same
+      if (PAGED) {
+        const uint32_t bad = missing_groups(p.keys, seq, key0, w, kv_len, lane);
+        if (lane == 0) s_bad[j & 7] = bad;
+        __syncwarp();
+      }
+      load_tile<D, PAGED>(k_s + st * C::KV_BYTES, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w,
+                          kv_len, kb, lane);
+      last_k = j;
+      if (j >= NS && !tc::warp_wait(bar(B::VEMPTY + st), ((j / NS) - 1) & 1, abort)) break;
+      load_tile<D, PAGED>(v_s + st * C::KV_BYTES, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w,
+                          kv_len, bar(B::VFULL + st), lane);
+      last_v = j;
+    }
+  } else if (warp > 8) {
+    // ------------------------------------------------------------------ products of half x
+    const int x = warp - 9, cnt = count_of(x);
+    const uint32_t qh = q_s + (SPLIT ? 0 : x * C::Q_BYTES), s_t = tmem + x * 128, o_t = tmem + 256 + x * 128;
+    bool ok = cnt == 0 || tc::warp_wait(bar(B::Q), 0, abort);
+    for (int it = 0; ok && it < cnt; ++it) {
+      const int j = tile_of(x, it), st = j % NS, w = tiles.width(a + j);
+      // P(it - 1), over S, has been read
+      if (it > 0 && !(ok = tc::warp_wait(bar(B::ODONE + x), (it - 1) & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(B::KFULL + st), (j / NS) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_abt<D>(s_t, qh, k_s + st * C::KV_BYTES, w);
+        tc::commit(bar(B::SFULL + x));
+        tc::commit(bar(B::KEMPTY + st));
+      }
+      __syncwarp();
+      if (!(ok = tc::warp_wait(bar(B::PFULL + x), it & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(B::VFULL + st), (j / NS) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_pv<D>(o_t, s_t, v_s + st * C::KV_BYTES, w, it == 0);
+        tc::commit(bar(B::ODONE + x));
+        tc::commit(bar(B::VEMPTY + st));
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax of half x
+    const int x = warp >> 2, row = tid & 127, cnt = count_of(x);
+    const int tl = row / p.R, hd = row % p.R, t = t0 + (SPLIT ? 0 : x * p.tpc) + tl;
+    const bool valid = tl < p.tpc && t < Lq;
+    const int pos = valid ? off + t : -1;
+    const bool work = __any_sync(0xffffffffu, pos >= 0);  // warps without rows only keep the barriers moving
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + x * 128 + lane_base, o_t = tmem + 256 + x * 128 + lane_base;
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    for (int it = 0; it < cnt; ++it) {
+      const int j = tile_of(x, it), key0 = tiles.key0(a + j), w = tiles.width(a + j);
+      if (!(ok = tc::warp_wait(bar(B::SFULL + x), it & 1, abort))) break;
+      tc::fence_after();
+      if (work) {
+        float sv[KT];
+#pragma unroll
+        for (int c = 0; c < KT; c += 32)
+          if (c < w) tc::tmem_ld32_nowait(s_t + c, sv + c);
+        // seen columns: [j_lo, j_hi) and, of those before j_lo, the sinks [0, j_sink)
+        const int j_hi = min(pos + 1 - key0, w);
+        const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = p.n_sink - key0;
+        const uint32_t bad = PAGED ? s_bad[j & 7] : 0u;
+        const bool all = j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0;
+        tc::tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+          for (int c = 0; c < KT; ++c) {
+            const bool see = c < j_hi && (c >= j_lo || c < j_sink) && !((bad >> (c / GRAN)) & 1u);
+            sv[c] = see ? sv[c] : kNegInf;
+          }
+        }
+        float mx = kNegInf;
+        {
+          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int c = 4; c < KT; c += 4) {
+            m4[0] = fmaxf(m4[0], sv[c]);
+            m4[1] = fmaxf(m4[1], sv[c + 1]);
+            m4[2] = fmaxf(m4[2], sv[c + 2]);
+            m4[3] = fmaxf(m4[3], sv[c + 3]);
+          }
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        }
+        // the running maximum moves only when a score exceeds it by 2^8 (P stays within
+        // range, and O in TMEM is rarely rescaled); S(it) was issued after PV(it - 1), so O
+        // is complete here
+        const bool need = mx > m + 8.f;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2(m - mx) : 1.f;
+          if (it > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float ov[32];
+              tc::tmem_ld32(o_t + c, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+              tc::tmem_st32(o_t + c, reinterpret_cast<const uint32_t*>(ov));
+            }
+          }
+          if (need) {
+            l *= alpha;
+            m = mx;
+          }
+        }
+        const float mu = m == kNegInf ? 0.f : m;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KT; c += 32) {
+          if (c >= w) break;
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float e0 = ex2(fmaf(sv[c + e], p.scale_log2, -mu)), e1 = ex2(fmaf(sv[c + e + 1], p.scale_log2, -mu));
+            l4[(e >> 1) & 3] += e0 + e1;
+            pk[e / 2] = pack_bf16(e0, e1);
+          }
+          tmem_st16_nowait(s_t + c / 2, pk);
+        }
+        tmem_wait_st();
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      }
+      tc::fence_before();
+      tc::mbar_arrive(bar(B::PFULL + x));
+    }
+    if (ok && cnt > 0) {
+      ok = tc::warp_wait(bar(B::ODONE + x), (cnt - 1) & 1, abort);
+      tc::fence_after();
+    }
+    if (ok && (SPLIT || x == 0 || two)) {
+      const int64_t rr = (start + t) * p.h + g * p.R + hd;
+      if (SPLIT || p.part_o) {
+        const int64_t at = (int64_t)(SPLIT ? split * 2 + x : split) * p.seqs.tokens * p.h + rr;
+        if (valid) p.part_ml[at] = make_float2(m, l);
+        if (__any_sync(0xffffffffu, l > 0.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float ov[32];
+            tc::tmem_ld32(o_t + c, ov);
+            if (l > 0.f) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(p.part_o + at * D + c + e) =
+                    make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            }
+          }
+        }
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          if (cnt > 0) tc::tmem_ld32(o_t + c, ov);
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (l > 0.f) {  // (a row without keys holds no product)
+                v.x = pack_bf16(ov[e] * inv, ov[e + 1] * inv);
+                v.y = pack_bf16(ov[e + 2] * inv, ov[e + 3] * inv);
+                v.z = pack_bf16(ov[e + 4] * inv, ov[e + 5] * inv);
+                v.w = pack_bf16(ov[e + 6] * inv, ov[e + 7] * inv);
+              }
+              *reinterpret_cast<uint4*>(p.o + rr * D + c + e) = v;
+            }
+          }
+        }
+        if (p.lse && valid) p.lse[rr] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort) {
+    // copies and products still in flight land before the CTA leaves
+    if (warp == 8) {
+      if (n > 0) tc::warp_drain(bar(B::Q), 0);
+      for (int st = 0; st < NS; ++st) {
+        const int ik = last_in_stage(last_k, st, NS), iv = last_in_stage(last_v, st, NS);
+        if (ik >= 0) tc::warp_drain(bar(B::KFULL + st), (ik / NS) & 1);
+        if (iv >= 0) tc::warp_drain(bar(B::VFULL + st), (iv / NS) & 1);
+      }
+    } else if (warp > 8) {
+      if (lane == 0) tc::commit(bar(B::DRAIN));
+      __syncwarp();
+      tc::warp_drain(bar(B::DRAIN), 0);
+    }
+  } else if (warp == 8) {
+    // the last release of every stage lands before the CTA leaves
+    for (int st = 0; st < NS; ++st) {
+      const int ik = last_in_stage(last_k, st, NS), iv = last_in_stage(last_v, st, NS);
+      if (ik >= 0) tc::warp_drain(bar(B::KEMPTY + st), (ik / NS) & 1);
+      if (iv >= 0) tc::warp_drain(bar(B::VEMPTY + st), (iv / NS) & 1);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_free(tmem, kTmemCols);
+}
+
+// Joins the parts of a row in order: one warp a (token, head) row.  Reads every part once
+// (a part without keys is skipped), writes bf16 o and the lse.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int parts) {
+  const int64_t rows = p.seqs.tokens * p.h;
+  const int64_t rr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (rr >= rows) return;
+  const int64_t tok = rr / p.h;
+  const int seq = seq_of_token(p.seqs, tok);
+  if (tok < seq_start(p.seqs, seq) || tok - seq_start(p.seqs, seq) >= seq_len(p.seqs, seq)) return;  // no sequence's row
+  float m = kNegInf;
+  for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * rows + rr].x);
+#pragma unroll
+  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  constexpr int E = D / 32;
+  float acc[E] = {}, l = 0.f;
+  if (m > kNegInf) {
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float wl = 0.f, w = 0.f;
+      if (i0 + lane < parts) {
+        const float2 ml = p.part_ml[(int64_t)(i0 + lane) * rows + rr];
+        if (ml.y > 0.f) {
+          w = ex2(ml.x - m);
+          wl = w * ml.y;
+        }
+      }
+      const int e1 = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < e1; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, wl, i);
+        l += li;
+        if (li > 0.f) {  // (an underflowed weight would only add zeros)
+          const float* src = p.part_o + ((int64_t)(i0 + i) * rows + rr) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + e);
+            acc[e] += wi * v.x;
+            acc[e + 1] += wi * v.y;
+          }
+        }
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(p.o + rr * D + lane * E + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[rr] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+}
+
+// How a call is cut.  Key tiles are bounded by the longest cache and the window.
+struct Plan {
+  bool split;    // one row tile a CTA, halves alternate key tiles
+  int tpc, row_ctas, n_splits, parts;
+  size_t ml, bytes;  // workspace: part_o at 0, part_ml at `ml`
+};
+Plan make_plan(const Seqs& s, int h, int hkv, int D, int max_keys, int window, int n_sink) {
+  Plan pl{};
+  const int R = h / hkv;
+  pl.tpc = std::max(1, std::min(ROWS / R, s.max_len));
+  // Few rows: every sequence's queries fit one row tile, so a second row tile would idle.
+  pl.split = s.max_len <= pl.tpc;
+  const int rows_tok = pl.split ? pl.tpc : 2 * pl.tpc;
+  pl.row_ctas = (s.max_len + rows_tok - 1) / rows_tok;
+  int64_t keys = max_keys;
+  if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + rows_tok + up16(n_sink) + 2 * GRAN);
+  const int64_t tiles = std::max<int64_t>(1, (keys + KT - 1) / KT);
+  const int64_t ctas = std::max<int64_t>(1, (int64_t)pl.row_ctas * s.n_seqs * hkv);
+  // Enough CTAs for about four rounds of the 152 SMs (ragged caches then even out), but no
+  // part below two key tiles (a tile for each half).
+  int64_t want = pl.split ? (4 * 152 + ctas - 1) / ctas : (152 + ctas - 1) / ctas;
+  want = std::max<int64_t>(1, std::min<int64_t>(want, (tiles + 1) / 2));
+  pl.n_splits = (int)std::min<int64_t>(want, std::min(256, 65535 / hkv));
+  pl.parts = pl.split ? 2 * pl.n_splits : pl.n_splits;
+  if (pl.parts > 1) {
+    const size_t rows = (size_t)s.tokens * h;
+    pl.ml = (pl.parts * rows * D * 4 + 255) & ~size_t(255);
+    pl.bytes = pl.ml + pl.parts * rows * 8;
+  }
+  return pl;
+}
+
+template <int D, bool PAGED, bool SPLIT>
+cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, dim3 grid, cudaStream_t st) {
+  auto kern = attn_kernel<D, PAGED, SPLIT>;
+  constexpr int smem = Cfg<D, SPLIT>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int hkv, int max_keys, int window,
+                     int n_sink, float scale, void* o, float* lse, void* workspace, cudaStream_t st) {
+  const Plan pl = make_plan(s, h, hkv, D, max_keys, window, n_sink);
+  AttnParams p{};
+  p.seqs = s;
+  p.keys = keys;
+  p.o = (__nv_bfloat16*)o;
+  p.lse = lse;
+  if (pl.parts > 1) {
+    p.part_o = (float*)workspace;
+    p.part_ml = (float2*)((uint8_t*)workspace + pl.ml);
+  }
+  p.h = h;
+  p.hkv = hkv;
+  p.R = h / hkv;
+  p.tpc = pl.tpc;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.n_splits = pl.n_splits;
+  p.scale_log2 = scale * kLog2e;
+  CUtensorMap m[5];
+  if (!query_map(&m[0], q, s.tokens, h, D, p.R, p.tpc) || !key_maps(&m[1], &m[2], keys.k, keys, hkv, D, s.tokens) ||
+      !key_maps(&m[3], &m[4], keys.v, keys, hkv, D, s.tokens))
+    return cudaErrorInvalidValue;
+  const dim3 grid(pl.row_ctas, s.n_seqs, hkv * pl.n_splits);
+  cudaError_t e = keys.table ? (pl.split ? run_attn<D, true, true>(m, p, grid, st) : run_attn<D, true, false>(m, p, grid, st))
+                             : (pl.split ? run_attn<D, false, true>(m, p, grid, st) : run_attn<D, false, false>(m, p, grid, st));
+  if (e != cudaSuccess || pl.parts == 1) return e;
+  const int64_t rows = s.tokens * h;
+  combine_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl.parts);
+  return cudaGetLastError();
+}
+
+}  // namespace span
+
+size_t span_attn_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink) {
+  if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
+  return span::make_plan(s, h, hkv, d, max_keys, window, n_sink).bytes;
+}
+
+cudaError_t launch_span_attn(const Seqs& s, const void* q, const PagedView* cache, const void* k, const void* v, int h,
+                             int hkv, int d, int max_keys, int window, int n_sink, float scale, void* o, float* lse,
+                             void* workspace, cudaStream_t st) {
+  if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return cudaSuccess;
+  const span::Keys keys = span::keys_of(cache, k, v);
+  return d == 64 ? span::launch_d<64>(s, q, keys, h, hkv, max_keys, window, n_sink, scale, o, lse, workspace, st)
+                 : span::launch_d<128>(s, q, keys, h, hkv, max_keys, window, n_sink, scale, o, lse, workspace, st);
+}
+
+NSA_STATUS_ACCESSOR(span_attn)
+
+}  // namespace nsa

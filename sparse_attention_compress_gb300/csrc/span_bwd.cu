@@ -1,0 +1,764 @@
+// Backward of the sliding window with sinks (span_attn.cu on packed sequences).  Per row
+// with seen keys j:  p_j = exp(scale q.k_j - lse),  D = dO.o,  dp_j = dO.v_j,
+//   ds_j = p_j (dp_j - D),  dq = scale sum_j ds_j k_j,
+//   dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dO.
+// S, dP and all accumulators are fp32 (TMEM); P and dS enter the last products as bf16:
+// one rounding of at most 2^-9 relative per weight, of either sign over a sum's terms, so
+// that the sums stay within the rounding of the bf16 gradients themselves.
+//
+// Two kernels, each a chain of M = 128 products over 128-wide tiles with eight softmax
+// warps (two threads a TMEM lane, 64 columns each):
+//   dq_kernel   a CTA owns 128 rows and walks the key tiles they see (S, dP, dQ).  It also
+//               stores each row's base-2 lse and D for the second kernel.
+//   dkv_kernel  a CTA owns 128 keys and walks the query tiles that see them, transposed
+//               (S^T = K Q^T, dP^T = V dO^T), so that P^T and dS^T are, in place in TMEM,
+//               the A operands of dV += P^T dO and dK += dS^T Q, and nothing passes through
+//               shared memory but the tiles.
+// Sinks are seen by every later query, so the queries past a sink tile's window are cut
+// into chunks with a CTA each; their fp32 partials are summed in order by sink_sum_kernel.
+// No atomics: results are the same on every run.
+#include <algorithm>
+
+#include "launch.h"
+#include "span.cuh"
+
+namespace nsa {
+namespace span {
+
+constexpr uint32_t kBwdTmem = 512;
+
+struct BwdParams {
+  Seqs seqs;
+  Keys keys;  // packed
+  const __nv_bfloat16 *q, *o, *dout;
+  const float* lse;
+  float* lse2;  // [tokens, h] workspace: base-2 lse (+inf for rows without keys)
+  float* dsum;  // [tokens, h] workspace: D
+  __nv_bfloat16 *dq, *dk, *dv;
+  float* part;  // [n_seqs][hkv][sink tiles][1 + n_far][2][sink_rows][D] fp32
+  int h, hkv, R, tpc, cols, window, n_sink;
+  int n_far, far_tokens, sink_tiles, sink_rows;
+  float scale, scale_log2;
+};
+
+__device__ __forceinline__ int last_in(int last, int st, int ns) { return last < st ? -1 : last - (last - st) % ns; }
+
+// (+)= A[128 x w] (bf16 in TMEM: columns 0..31 hold the first 64, 64..95 the others)
+// B[w x D], a tile of w rows read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int w, bool first) {
+  constexpr uint32_t id = tc::idesc(ROWS, D) | kBMn;
+#pragma unroll
+  for (int s = 0; s < KT / 16; ++s)
+    if (s * 16 < w)
+      tc::mma_ts(d_tmem, a_tmem + (s < 4 ? s * 8 : 64 + (s - 4) * 8), sdesc_mn(b + s * 2048, KT * 128), id,
+                 (first && s == 0) ? 0u : 1u);
+}
+
+// ---------------------------------------------------------------------------- dQ
+// Warps 0-7 softmax, 8 loads, 9 issues S, 10 dP, 11 dQ.  TMEM: S / dS of tile j at
+// 128 (j & 1), dP at 256, dQ at 384: S of the next tile is computed while this one's dS is
+// formed, dP once this tile's dP has been read.
+constexpr int kDqThreads = 384, kNK = 3, kNV = 2;
+
+template <int D>
+constexpr int dq_smem() {
+  return (2 + kNK + kNV) * KT * D * 2 + 1024;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDqThreads, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k16,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v16,
+              const BwdParams p) {
+  enum : int {
+    Q = 0,
+    KFULL = 1,
+    KEMPTY = KFULL + kNK,
+    VFULL = KEMPTY + kNK,
+    VEMPTY = VFULL + kNV,
+    SFULL = VEMPTY + kNV,  // [2] by S buffer
+    PFULL = SFULL + 2,     // dP computed
+    PFREE = PFULL + 1,     // dP read
+    DSFULL = PFREE + 1,    // [2] dS written
+    DQDONE = DSFULL + 2,   // [2] dQ product of that buffer done
+    DRAIN = DQDONE + 2,
+    COUNT
+  };
+  constexpr int TB = KT * D * 2;  // bytes of a tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[COUNT];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_s = base, do_s = q_s + TB, k_s = do_s + TB, v_s = k_s + kNK * TB;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  volatile int* abort = &s_abort;
+
+  if (tc::device_status_set()) return;
+  const int seq = blockIdx.y, g = blockIdx.z;
+  const int64_t start = seq_start(p.seqs, seq);
+  const int L = seq_len(p.seqs, seq);
+  const int t0 = ((L + p.tpc - 1) / p.tpc - 1 - (int)blockIdx.x) * p.tpc;
+  if (t0 < 0) return;
+  const Tiles tiles(t0, min(t0 + p.tpc, L) - 1, p.window, p.n_sink);
+  const int n = tiles.n;
+
+  if (tid == 0) {
+    tc::mbar_init(bar(Q), 1);
+    for (int i = 0; i < kNK; ++i) {
+      tc::mbar_init(bar(KFULL + i), 1);
+      tc::mbar_init(bar(KEMPTY + i), 1);
+    }
+    for (int i = 0; i < kNV; ++i) {
+      tc::mbar_init(bar(VFULL + i), 1);
+      tc::mbar_init(bar(VEMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(SFULL + i), 1);
+      tc::mbar_init(bar(DSFULL + i), 256);
+      tc::mbar_init(bar(DQDONE + i), 1);
+    }
+    tc::mbar_init(bar(PFULL), 1);
+    tc::mbar_init(bar(PFREE), 256);
+    tc::mbar_init(bar(DRAIN), 3);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&s_tmem), kBwdTmem);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  int last_k = -1, last_v = -1;
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      tc::mbar_expect_tx(bar(Q), (uint32_t)(2 * p.tpc * p.R * D * 2));
+      for (int c = 0; c < D / 64; ++c) {
+        tc::tma3d(q_s + c * (ROWS * 128), &tm_q, c * 64, g * p.R, (int)(start + t0), bar(Q));
+        tc::tma3d(do_s + c * (ROWS * 128), &tm_do, c * 64, g * p.R, (int)(start + t0), bar(Q));
+      }
+    }
+    __syncwarp();
+    for (int j = 0; j < n; ++j) {
+      const int key0 = tiles.key0(j), w = tiles.width(j), sk = j % kNK, sv = j % kNV;
+      if (j >= kNK && !tc::warp_wait(bar(KEMPTY + sk), ((j / kNK) - 1) & 1, abort)) break;
+      load_tile<D, false>(k_s + sk * TB, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, L,
+                          bar(KFULL + sk), lane);
+      last_k = j;
+      if (j >= kNV && !tc::warp_wait(bar(VEMPTY + sv), ((j / kNV) - 1) & 1, abort)) break;
+      load_tile<D, false>(v_s + sv * TB, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w, L,
+                          bar(VFULL + sv), lane);
+      last_v = j;
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ S
+    bool ok = tc::warp_wait(bar(Q), 0, abort);
+    for (int j = 0; ok && j < n; ++j) {
+      const int b = j & 1, sk = j % kNK;
+      if (j >= 2 && !(ok = tc::warp_wait(bar(DQDONE + b), ((j >> 1) - 1) & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(KFULL + sk), (j / kNK) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_abt<D>(tmem + b * 128, q_s, k_s + sk * TB, tiles.width(j));
+        tc::commit(bar(SFULL + b));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ dP
+    bool ok = tc::warp_wait(bar(Q), 0, abort);
+    for (int j = 0; ok && j < n; ++j) {
+      const int sv = j % kNV;
+      if (j >= 1 && !(ok = tc::warp_wait(bar(PFREE), (j - 1) & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(VFULL + sv), (j / kNV) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_abt<D>(tmem + 256, do_s, v_s + sv * TB, tiles.width(j));
+        tc::commit(bar(PFULL));
+        tc::commit(bar(VEMPTY + sv));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------------ dQ += dS K
+    bool ok = true;
+    for (int j = 0; ok && j < n; ++j) {
+      const int b = j & 1, sk = j % kNK;
+      // (dS of this tile was formed from S, so its K tile is in place)
+      if (!(ok = tc::warp_wait(bar(DSFULL + b), (j >> 1) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_split_a<D>(tmem + 384, tmem + b * 128, k_s + sk * TB, tiles.width(j), j == 0);
+        tc::commit(bar(DQDONE + b));
+        tc::commit(bar(KEMPTY + sk));
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // columns 64 x .. 64 x + 63 of every tile
+    const int tl = row / p.R, hd = row % p.R, t = t0 + tl;
+    const bool valid = tl < p.tpc && t < L;
+    const int pos = valid ? t : -1;
+    const int64_t rr = (start + t) * p.h + g * p.R + hd;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    float l2 = __builtin_inff(), dsum = 0.f;
+    if (valid) {
+      const float l = p.lse[rr];
+      l2 = l == kNegInf ? __builtin_inff() : l * kLog2e;
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int c = 0; c < D; c += 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p.o + rr * D + c);
+        const uint4 b = *reinterpret_cast<const uint4*>(p.dout + rr * D + c);
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
+          const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
+          s4[e] = fmaf(u.x, v.x, fmaf(u.y, v.y, s4[e]));
+        }
+      }
+      dsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      if (x == 0) {
+        p.lse2[rr] = l2;
+        p.dsum[rr] = dsum;
+      }
+    }
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
+      if (!(ok = tc::warp_wait(bar(SFULL + b), (j >> 1) & 1, abort))) break;
+      tc::fence_after();
+      const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
+      const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)
+      float sv[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32)
+        if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
+      const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = p.n_sink - key0;
+      const bool all = j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64);
+      tc::tmem_wait_ld();
+      if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const int cc = c0 + c;
+          sv[c] = cc < j_hi && (cc >= j_lo || cc < j_sink) ? sv[c] : kNegInf;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 64; ++c) sv[c] = ex2(fmaf(sv[c], p.scale_log2, -l2));
+      if (!(ok = tc::warp_wait(bar(PFULL), j & 1, abort))) break;
+      tc::fence_after();
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        if (c >= nc) break;
+        float dp[32];
+        tc::tmem_ld32(p_t + c, dp);
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          // (an unseen key has p = 0, and contributes nothing whatever its dp)
+          const float d0 = sv[c + e] > 0.f ? sv[c + e] * (dp[e] - dsum) : 0.f;
+          const float d1 = sv[c + e + 1] > 0.f ? sv[c + e + 1] * (dp[e + 1] - dsum) : 0.f;
+          pk[e / 2] = pack_bf16(d0, d1);
+        }
+        tmem_st16_nowait(s_t + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc::fence_before();
+      tc::mbar_arrive(bar(PFREE));
+      tc::mbar_arrive(bar(DSFULL + b));
+    }
+    if (ok) {
+      ok = tc::warp_wait(bar(DQDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort);
+      tc::fence_after();
+    }
+    if (ok) {
+      __nv_bfloat16* dst = p.dq + rr * D;
+#pragma unroll 1
+      for (int c = x * (D / 2); c < (x + 1) * (D / 2); c += 32) {
+        float v[32];
+        tc::tmem_ld32(tmem + 384 + lane_base + c, v);
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 u;
+            u.x = pack_bf16(v[e] * p.scale, v[e + 1] * p.scale);
+            u.y = pack_bf16(v[e + 2] * p.scale, v[e + 3] * p.scale);
+            u.z = pack_bf16(v[e + 4] * p.scale, v[e + 5] * p.scale);
+            u.w = pack_bf16(v[e + 6] * p.scale, v[e + 7] * p.scale);
+            *reinterpret_cast<uint4*>(dst + c + e) = u;
+          }
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort) {
+    if (warp == 8) {
+      tc::warp_drain(bar(Q), 0);
+      for (int st = 0; st < kNK; ++st)
+        if (const int i = last_in(last_k, st, kNK); i >= 0) tc::warp_drain(bar(KFULL + st), (i / kNK) & 1);
+      for (int st = 0; st < kNV; ++st)
+        if (const int i = last_in(last_v, st, kNV); i >= 0) tc::warp_drain(bar(VFULL + st), (i / kNV) & 1);
+    } else if (warp > 8) {
+      if (lane == 0) tc::commit(bar(DRAIN));
+      __syncwarp();
+      tc::warp_drain(bar(DRAIN), 0);
+    }
+  } else if (warp == 8) {
+    for (int st = 0; st < kNK; ++st)
+      if (const int i = last_in(last_k, st, kNK); i >= 0) tc::warp_drain(bar(KEMPTY + st), (i / kNK) & 1);
+    for (int st = 0; st < kNV; ++st)
+      if (const int i = last_in(last_v, st, kNV); i >= 0) tc::warp_drain(bar(VEMPTY + st), (i / kNV) & 1);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_free(tmem, kBwdTmem);
+}
+
+// ---------------------------------------------------------------------------- dK, dV
+// Warps 0-7 softmax, 8 loads, 9 issues S^T and dV, 10 dP^T and dK.  TMEM: S^T (then P^T) at
+// 0, dP^T (then dS^T) at 128, dV at 256, dK at 384.  The two issuers' chains interleave on
+// the tensor pipe: while P^T is formed dK of the tile before and dP^T run, while dS^T is
+// formed dV and the next S^T do.
+constexpr int kDkvThreads = 352;
+
+template <int D>
+constexpr int dkv_smem() {
+  return 6 * KT * D * 2 + 1024;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDkvThreads, 1)
+    dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k16,
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v16,
+               const BwdParams p) {
+  enum : int {
+    KV = 0,      // [2] K, V
+    QFULL = 2,   // [2] by stage: Q rows, lse, D
+    QEMPTY = 4,  // [2]
+    DFULL = 6,   // [2] dO rows
+    DEMPTY = 8,  // [2]
+    SFULL = 10,
+    PFULL = 11,   // P^T written
+    DVDONE = 12,
+    DPFULL = 13,
+    DSFULL = 14,  // dS^T written
+    DKDONE = 15,
+    DRAIN = 16,
+    COUNT
+  };
+  constexpr int TB = KT * D * 2;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[COUNT];
+  __shared__ __align__(16) float s_l2[2][ROWS], s_d[2][ROWS];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t k_s = base, v_s = k_s + TB, q_s = v_s + TB, do_s = q_s + 2 * TB;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  volatile int* abort = &s_abort;
+
+  if (tc::device_status_set()) return;
+  // items of a (sequence, kv-head): the chunks of far queries of the sink tiles, then every
+  // key tile with the queries within its window
+  const int n_far_items = p.sink_tiles * p.n_far;
+  const int seq = blockIdx.y, g = blockIdx.z;
+  const int64_t start = seq_start(p.seqs, seq);
+  const int L = seq_len(p.seqs, seq);
+  const bool far = (int)blockIdx.x < n_far_items;
+  const int kt = far ? (int)blockIdx.x / p.n_far : (int)blockIdx.x - n_far_items;
+  const int chunk = far ? (int)blockIdx.x % p.n_far : -1;
+  const int key0 = kt * KT;
+  if (key0 >= L) return;
+  const int near_end = min(L, key0 + KT - 1 + p.window);
+  const int t_lo = far ? near_end + chunk * p.far_tokens : key0;
+  const int t_hi = far ? min(L, t_lo + p.far_tokens) : near_end;
+  if (t_lo >= t_hi) return;  // (an empty chunk: sink_sum_kernel does not read it)
+  const int n = (t_hi - t_lo + p.tpc - 1) / p.tpc;
+  const int used = p.tpc * p.R;  // rows of a tile
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(KV + i), 1);
+      tc::mbar_init(bar(QFULL + i), 1);
+      tc::mbar_init(bar(QEMPTY + i), 1);
+      tc::mbar_init(bar(DFULL + i), 1);
+      tc::mbar_init(bar(DEMPTY + i), 2);  // dP^T and dV have read dO
+    }
+    tc::mbar_init(bar(SFULL), 1);
+    tc::mbar_init(bar(PFULL), 256);
+    tc::mbar_init(bar(DVDONE), 1);
+    tc::mbar_init(bar(DPFULL), 1);
+    tc::mbar_init(bar(DSFULL), 256);
+    tc::mbar_init(bar(DKDONE), 1);
+    tc::mbar_init(bar(DRAIN), 2);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  // rows between the tile's own and the next multiple of 16 (group sizes that do not divide
+  // 128) enter the products as zeros; no copy ever writes them
+  for (int e = tid; e < (p.cols - used) * 4 * (D / 8); e += kDkvThreads) {
+    const int ch = e % (D / 8), which = (e / (D / 8)) & 3, r = used + e / (4 * (D / 8));
+    const uint32_t to = q_s + which * TB + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to), "r"(0u) : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&s_tmem), kBwdTmem);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  int last_q = -1, last_d = -1;
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loads
+    const int w = min(KT, up16(L - key0));
+    load_tile<D, false>(k_s, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, L, bar(KV), lane);
+    load_tile<D, false>(v_s, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w, L, bar(KV + 1), lane);
+    // Rows of tokens t .. t + tpc - 1 (those past the sequence as zeros: they are another
+    // sequence's, or lie past the tensors).
+    auto load_rows = [&](uint32_t to, const CUtensorMap* map, const __nv_bfloat16* src, int t, uint32_t full) {
+      uint32_t bytes = 0;
+      if (t + p.tpc <= L) {
+        bytes = (uint32_t)(used * D * 2);
+        if (lane < D / 64) tc::tma3d(to + lane * (ROWS * 128), map, lane * 64, g * p.R, (int)(start + t), full);
+      } else {
+        for (int e = lane; e < used * (D / 8); e += 32) {
+          const int r = e / (D / 8), ch = e % (D / 8), tt = t + r / p.R;
+          const bool in = tt < L;
+          cp_async16(to + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                     in ? (const void*)(src + ((start + tt) * p.h + g * p.R + r % p.R) * D + ch * 8) : (const void*)src,
+                     in ? 16 : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_expect_tx(full, bytes);
+    };
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 1, t = t_lo + j * p.tpc;
+      if (j >= 2 && !tc::warp_wait(bar(QEMPTY + st), ((j >> 1) - 1) & 1, abort)) break;
+#pragma unroll
+      for (int e = lane; e < ROWS; e += 32) {
+        float a = __builtin_inff(), b = 0.f;
+        if (e < used && t + e / p.R < L) {
+          const int64_t rr = (start + t + e / p.R) * p.h + g * p.R + e % p.R;
+          a = p.lse2[rr];
+          b = p.dsum[rr];
+        }
+        s_l2[st][e] = a;
+        s_d[st][e] = b;
+      }
+      load_rows(q_s + st * TB, &tm_q, p.q, t, bar(QFULL + st));
+      last_q = j;
+      if (j >= 2 && !tc::warp_wait(bar(DEMPTY + st), ((j >> 1) - 1) & 1, abort)) break;
+      load_rows(do_s + st * TB, &tm_do, p.dout, t, bar(DFULL + st));
+      last_d = j;
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ S^T, dV += P^T dO
+    bool ok = tc::warp_wait(bar(KV), 0, abort);
+    for (int j = 0; ok && j < n; ++j) {
+      const int st = j & 1;
+      // P^T of the tile before has been read
+      if (j > 0 && !(ok = tc::warp_wait(bar(DVDONE), (j - 1) & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_abt<D>(tmem, k_s, q_s + st * TB, p.cols);
+        tc::commit(bar(SFULL));
+      }
+      __syncwarp();
+      if (!(ok = tc::warp_wait(bar(PFULL), j & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(DFULL + st), (j >> 1) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_split_a<D>(tmem + 256, tmem, do_s + st * TB, p.cols, j == 0);
+        tc::commit(bar(DVDONE));
+        tc::commit(bar(DEMPTY + st));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ dP^T, dK += dS^T Q
+    bool ok = tc::warp_wait(bar(KV + 1), 0, abort);
+    for (int j = 0; ok && j < n; ++j) {
+      const int st = j & 1;
+      if (j > 0 && !(ok = tc::warp_wait(bar(DKDONE), (j - 1) & 1, abort))) break;
+      if (!(ok = tc::warp_wait(bar(DFULL + st), (j >> 1) & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_abt<D>(tmem + 128, v_s, do_s + st * TB, p.cols);
+        tc::commit(bar(DPFULL));
+        tc::commit(bar(DEMPTY + st));
+      }
+      __syncwarp();
+      if (!(ok = tc::warp_wait(bar(DSFULL), j & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_split_a<D>(tmem + 384, tmem + 128, q_s + st * TB, p.cols, j == 0);
+        tc::commit(bar(DKDONE));
+        tc::commit(bar(QEMPTY + st));  // (S^T of the tile was done before its dS^T)
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane, key = key0 + row, c0 = x * 64;
+    const bool have = key < L;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + c0 + lane_base, p_t = tmem + 128 + c0 + lane_base;
+    const int nc = min(64, p.cols - c0);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 1, t = t_lo + j * p.tpc;
+      // columns [c_lo, c_hi) of this half are rows whose query sees this key
+      int c_lo = 0, c_hi = 0;
+      if (have) {
+        int64_t end = (int64_t)min(p.tpc, t_hi - t) * p.R;
+        if (key >= p.n_sink) end = min(end, ((int64_t)key + p.window - t) * p.R);
+        c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
+        c_hi = (int)max((int64_t)0, end) - c0;
+      }
+      if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;  // lse and D
+      if (!(ok = tc::warp_wait(bar(SFULL), j & 1, abort))) break;
+      tc::fence_after();
+      float sv[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32)
+        if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
+      const bool all = c_lo <= 0 && c_hi >= 64;
+      tc::tmem_wait_ld();
+      const float4* l4 = reinterpret_cast<const float4*>(&s_l2[st][c0]);
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l = l4[c / 4];
+        sv[c] = ex2(fmaf(sv[c], p.scale_log2, -l.x));
+        sv[c + 1] = ex2(fmaf(sv[c + 1], p.scale_log2, -l.y));
+        sv[c + 2] = ex2(fmaf(sv[c + 2], p.scale_log2, -l.z));
+        sv[c + 3] = ex2(fmaf(sv[c + 3], p.scale_log2, -l.w));
+      }
+      if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) sv[c] = c >= c_lo && c < c_hi ? sv[c] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        if (c >= nc) break;
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
+        tmem_st16_nowait(s_t + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc::fence_before();
+      tc::mbar_arrive(bar(PFULL));
+      if (!(ok = tc::warp_wait(bar(DPFULL), j & 1, abort))) break;
+      tc::fence_after();
+      const float4* d4 = reinterpret_cast<const float4*>(&s_d[st][c0]);
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        if (c >= nc) break;
+        float dp[32];
+        tc::tmem_ld32(p_t + c, dp);
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d = d4[(c + e) / 4];
+          // (zero rows past the sequence have dp = 0, so p = 0 gives ds = 0)
+          pk[e / 2] = pack_bf16(sv[c + e] * (dp[e] - d.x), sv[c + e + 1] * (dp[e + 1] - d.y));
+          pk[e / 2 + 1] = pack_bf16(sv[c + e + 2] * (dp[e + 2] - d.z), sv[c + e + 3] * (dp[e + 3] - d.w));
+        }
+        tmem_st16_nowait(p_t + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc::fence_before();
+      tc::mbar_arrive(bar(DSFULL));
+    }
+    if (ok) {
+      ok = tc::warp_wait(bar(DVDONE), (n - 1) & 1, abort) && tc::warp_wait(bar(DKDONE), (n - 1) & 1, abort);
+      tc::fence_after();
+    }
+    if (ok) {
+      // half 0 writes dK, half 1 dV
+      const float f = x ? 1.f : p.scale;
+      const bool to_part = kt < p.sink_tiles && p.n_far > 0 && key < p.n_sink;
+      float* part = p.part + (((((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) + (chunk + 1)) * 2 + x) *
+                                 p.sink_rows * D + (int64_t)row * D;
+      __nv_bfloat16* dst = (x ? p.dv : p.dk) + ((start + key) * p.hkv + g) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
+        tc::tmem_ld32(tmem + (x ? 256 : 384) + lane_base + c, v);
+        if (have && to_part) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else if (have && !far) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 u;
+            u.x = pack_bf16(v[e] * f, v[e + 1] * f);
+            u.y = pack_bf16(v[e + 2] * f, v[e + 3] * f);
+            u.z = pack_bf16(v[e + 4] * f, v[e + 5] * f);
+            u.w = pack_bf16(v[e + 6] * f, v[e + 7] * f);
+            *reinterpret_cast<uint4*>(dst + c + e) = u;
+          }
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort) {
+    if (warp == 8) {
+      tc::warp_drain(bar(KV), 0);
+      tc::warp_drain(bar(KV + 1), 0);
+      for (int st = 0; st < 2; ++st) {
+        if (const int i = last_in(last_q, st, 2); i >= 0) tc::warp_drain(bar(QFULL + st), (i >> 1) & 1);
+        if (const int i = last_in(last_d, st, 2); i >= 0) tc::warp_drain(bar(DFULL + st), (i >> 1) & 1);
+      }
+    } else if (warp > 8) {
+      if (lane == 0) tc::commit(bar(DRAIN));
+      __syncwarp();
+      tc::warp_drain(bar(DRAIN), 0);
+    }
+  } else if (warp == 8) {
+    for (int st = 0; st < 2; ++st) {
+      if (const int i = last_in(last_q, st, 2); i >= 0) tc::warp_drain(bar(QEMPTY + st), (i >> 1) & 1);
+      if (const int i = last_in(last_d, st, 2); i >= 0) tc::warp_drain(bar(DEMPTY + st), (i >> 1) & 1);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_free(tmem, kBwdTmem);
+}
+
+// dK and dV of the sinks: the near part and the far chunks, in order.  One block a (sink,
+// kv-head, sequence); thread: column of dK (first D threads) or dV.
+template <int D>
+__global__ void __launch_bounds__(2 * D) sink_sum_kernel(const BwdParams p) {
+  const int key = blockIdx.x, g = blockIdx.y, seq = blockIdx.z;
+  const int L = seq_len(p.seqs, seq);
+  if (key >= L) return;
+  const int x = threadIdx.x / D, c = threadIdx.x % D, kt = key / KT;
+  const int near_end = min(L, kt * KT + KT - 1 + p.window);
+  const int parts = 1 + (L - near_end + p.far_tokens - 1) / p.far_tokens;
+  const int64_t step = (int64_t)2 * p.sink_rows * D;
+  const float* src = p.part + (((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) * step +
+                     ((int64_t)x * p.sink_rows + key % KT) * D + c;
+  float acc = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) acc += src[i * step];
+  __nv_bfloat16* dst = (x ? p.dv : p.dk) + ((seq_start(p.seqs, seq) + key) * (int64_t)p.hkv + g) * D + c;
+  *dst = __float2bfloat16_rn(x ? acc : acc * p.scale);
+}
+
+struct BwdLayout {
+  int tpc, n_far, far_tokens, sink_tiles, sink_rows;
+  size_t dsum, part, bytes;
+};
+BwdLayout bwd_layout(const Seqs& s, int h, int hkv, int D, int window, int n_sink) {
+  BwdLayout l{};
+  const int R = h / hkv;
+  l.tpc = std::max(1, std::min(ROWS / R, s.max_len));
+  const int sinks = std::min(n_sink, s.max_len);
+  const int64_t far = sinks > 0 ? (int64_t)s.max_len - (KT - 1) - window : 0;  // queries past the first tile's window
+  if (far > 0) {
+    // a chunk is about as long as a key tile's own queries, at most 64 chunks
+    const int64_t len = std::max<int64_t>((int64_t)window + KT - 1, (far + 63) / 64);
+    l.far_tokens = (int)((len + l.tpc - 1) / l.tpc * l.tpc);
+    l.n_far = (int)((far + l.far_tokens - 1) / l.far_tokens);
+    l.sink_tiles = (sinks + KT - 1) / KT;
+    l.sink_rows = std::min(sinks, KT);
+  }
+  auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  l.dsum = a256((size_t)s.tokens * h * 4);
+  l.part = 2 * l.dsum;
+  l.bytes = l.part + (size_t)s.n_seqs * hkv * l.sink_tiles * (1 + l.n_far) * 2 * l.sink_rows * D * 4;
+  return l;
+}
+
+template <int D>
+cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
+  const Seqs& s = p.seqs;
+  CUtensorMap mq, md, mk, mk16, mv, mv16;
+  if (!query_map(&mq, p.q, s.tokens, p.h, D, p.R, p.tpc) || !query_map(&md, p.dout, s.tokens, p.h, D, p.R, p.tpc) ||
+      !key_maps(&mk, &mk16, p.keys.k, p.keys, p.hkv, D, s.tokens) ||
+      !key_maps(&mv, &mv16, p.keys.v, p.keys, p.hkv, D, s.tokens))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<D>());
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<D>());
+  if (e != cudaSuccess) return e;
+  dq_kernel<D><<<dim3((s.max_len + p.tpc - 1) / p.tpc, s.n_seqs, p.hkv), kDqThreads, dq_smem<D>(), st>>>(
+      mq, md, mk, mk16, mv, mv16, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int items = l.sink_tiles * l.n_far + (s.max_len + KT - 1) / KT;
+  dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem<D>(), st>>>(mq, md, mk, mk16, mv, mv16, p);
+  if ((e = cudaGetLastError()) != cudaSuccess || l.n_far == 0) return e;
+  sink_sum_kernel<D><<<dim3(std::min(p.n_sink, s.max_len), p.hkv, s.n_seqs), 2 * D, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace span
+
+size_t span_bwd_workspace_bytes(const Seqs& s, int h, int hkv, int d, int window, int n_sink) {
+  if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
+  return span::bwd_layout(s, h, hkv, d, window, n_sink).bytes;
+}
+
+cudaError_t launch_span_bwd(const Seqs& s, const void* q, const void* k, const void* v, int h, int hkv, int d,
+                            int window, int n_sink, float scale, const void* o, const float* lse, const void* dout,
+                            void* dq, void* dk, void* dv, void* workspace, cudaStream_t st) {
+  if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return cudaSuccess;
+  const span::BwdLayout l = span::bwd_layout(s, h, hkv, d, window, n_sink);
+  span::BwdParams p{};
+  p.seqs = s;
+  p.keys = span::keys_of(nullptr, k, v);
+  p.q = (const __nv_bfloat16*)q;
+  p.o = (const __nv_bfloat16*)o;
+  p.dout = (const __nv_bfloat16*)dout;
+  p.lse = lse;
+  p.lse2 = (float*)workspace;
+  p.dsum = (float*)((uint8_t*)workspace + l.dsum);
+  p.part = (float*)((uint8_t*)workspace + l.part);
+  p.dq = (__nv_bfloat16*)dq;
+  p.dk = (__nv_bfloat16*)dk;
+  p.dv = (__nv_bfloat16*)dv;
+  p.h = h;
+  p.hkv = hkv;
+  p.R = h / hkv;
+  p.tpc = l.tpc;
+  p.cols = span::up16(l.tpc * p.R);
+  p.window = window;
+  p.n_sink = n_sink;
+  p.n_far = l.n_far;
+  p.far_tokens = l.far_tokens;
+  p.sink_tiles = l.sink_tiles;
+  p.sink_rows = l.sink_rows;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  return d == 64 ? span::launch_bwd_d<64>(p, l, st) : span::launch_bwd_d<128>(p, l, st);
+}
+
+NSA_STATUS_ACCESSOR(span_bwd)
+
+}  // namespace nsa
