@@ -4,7 +4,7 @@
 //   o = sum_j exp(s_j - lse) v_j;   a row that sees no key gets o = 0, lse = -inf.
 // One pass over the keys with a running maximum and sum, base-2 exponentials, all
 // statistics and accumulators in fp32; P enters the second product as bf16 (half a step,
-// 2^-9 relative on each weight, which averages out over a row's keys and stays below the
+// 2^-8 relative on each weight, which averages out over a row's keys and stays below the
 // rounding of the bf16 output itself).
 //
 // A tile is 128 rows = 128 / group tokens x the heads of a kv-group, so each K / V tile is

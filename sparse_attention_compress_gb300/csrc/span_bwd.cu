@@ -3,7 +3,7 @@
 //   ds_j = p_j (dp_j - D),  dq = scale sum_j ds_j k_j,
 //   dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dO.
 // S, dP and all accumulators are fp32 (TMEM); P and dS enter the last products as bf16:
-// one rounding of at most 2^-9 relative per weight, of either sign over a sum's terms, so
+// one rounding of at most 2^-8 relative per weight, of either sign over a sum's terms, so
 // that the sums stay within the rounding of the bf16 gradients themselves.
 //
 // Two kernels, each a chain of M = 128 products over 128-wide tiles with eight softmax

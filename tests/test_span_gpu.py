@@ -1,0 +1,605 @@
+"""Paged-cache and sink-window operators on the GPU against the 64-bit reference, elementwise
+within the bounds of the kernels' own roundings (tests/span_reference.py)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import sparse_attention_compress_gb300 as nsa
+from tests import span_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, I32, NAN = torch.bfloat16, torch.int32, float("nan")
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _bf(shape, gen, scale=1.0):
+    return (torch.randn(shape, generator=gen) * scale).to(BF)
+
+
+class Cache:
+    """Pages, table and plain copies of a cache.  Slots that hold no position are NaN."""
+
+    def __init__(self, lens, hk, d, page, seed, spare=2, scale=1.0, interleave=False):
+        g = _gen(seed)
+        need = [-(-n // page) for n in lens]
+        self.lens, self.hk, self.d, self.page = lens, hk, d, page
+        n_pages = sum(need) + spare
+        order = torch.randperm(n_pages, generator=g).tolist()
+        self.table = torch.full((len(lens), max(1, max(need)) + 1), -1, dtype=I32)
+        pool = torch.full((n_pages, 2, page, hk, d), NAN, dtype=BF)
+        self.k, self.v = [], []
+        for b, n in enumerate(lens):
+            k, v = _bf((n, hk, d), g, scale), _bf((n, hk, d), g)
+            self.k.append(k.double())
+            self.v.append(v.double())
+            for i in range(need[b]):
+                pid = order.pop()
+                self.table[b, i] = pid
+                m = min(page, n - i * page)
+                pool[pid, 0, :m], pool[pid, 1, :m] = k[i * page:i * page + m], v[i * page:i * page + m]
+        self.free = order
+        self.cpu_pool = pool
+        if interleave:
+            dev = pool.cuda()
+            self.k_pages, self.v_pages = dev[:, 0], dev[:, 1]
+        else:
+            self.k_pages, self.v_pages = pool[:, 0].contiguous().cuda(), pool[:, 1].contiguous().cuda()
+        self.dev_table, self.dev_lens = self.table.cuda(), torch.tensor(lens, dtype=I32, device="cuda")
+
+    @property
+    def args(self):
+        return self.k_pages, self.v_pages, self.dev_table, self.dev_lens
+
+    def weights(self, fill):
+        return torch.full((self.k_pages.shape[0], self.hk, self.page), fill, device="cuda")
+
+    def at(self, w, b):
+        """[n, Hkv] of a weights tensor for the positions of sequence b."""
+        w, n = w.cpu(), self.lens[b]
+        return torch.stack([w[self.table[b, j // self.page].item(), :, j % self.page] for j in range(n)]) if n else \
+            torch.zeros(0, self.hk)
+
+
+def _queries(q_lens, H, d, seed, scale=1.0):
+    cu = torch.tensor([0] + q_lens).cumsum(0).to(I32)
+    return _bf((int(cu[-1]), H, d), _gen(seed), scale), cu
+
+
+def _reference(c, q, cu, b, window, n_sink, scale, hide=()):
+    a, e = int(cu[b]), int(cu[b + 1])
+    see = ref.visible(range(c.lens[b] - (e - a), c.lens[b]), c.lens[b], window, n_sink)
+    for lo, hi in hide:
+        see[:, lo:hi] = False
+    return a, e, see, ref.attend(q[a:e].double(), c.k[b], c.v[b], see, scale)
+
+
+# lengths (cached), lengths (new), heads, kv-heads, d, page, window, sinks
+CASES = [
+    ([1], [1], 1, 1, 64, 16, 0, 0),
+    ([1, 130, 0, 77], [1, 1, 1, 1], 16, 2, 128, 64, 0, 0),          # a sequence with an empty cache
+    ([300, 17, 128, 129], [1, 1, 1, 1], 6, 2, 64, 16, 0, 0),        # group 3, pages of 16
+    ([5, 260], [9, 12], 4, 4, 128, 32, 0, 0),                       # more queries than cached tokens
+    ([127, 128, 129, 400], [127, 1, 0, 130], 8, 1, 128, 128, 0, 0),  # a sequence without queries
+    ([513, 255], [200, 33], 16, 1, 64, 256, 0, 0),
+    ([700, 40], [300, 40], 10, 2, 128, 64, 100, 0),                 # group 5
+    ([700, 1000, 3], [300, 1, 3], 8, 2, 128, 16, 37, 5),
+    ([900, 640], [1, 1], 32, 2, 64, 32, 64, 130),                   # sinks over more than a tile
+    ([450], [450], 12, 4, 64, 16, 1, 1),
+    ([333], [90], 128, 1, 128, 64, 50, 16),                         # group 128: one token a tile
+    ([2000, 1500], [1, 3], 16, 2, 128, 64, 1000, 4),
+]
+
+
+@pytest.mark.parametrize("lens,q_lens,H,hk,d,page,window,n_sink", CASES)
+@pytest.mark.parametrize("interleave", [False, True])
+def test_paged_attention_and_weights(lens, q_lens, H, hk, d, page, window, n_sink, interleave):
+    c = Cache(lens, hk, d, page, 1, interleave=interleave)
+    q, cu = _queries(q_lens, H, d, 2)
+    dq, dcu, scale = q.cuda(), cu.cuda(), 1.0 / math.sqrt(d)
+    lse = torch.full((q.shape[0], H), NAN, device="cuda")
+    kw = dict(window=window, n_sink=n_sink, cu_seqlens=dcu, max_seqlen=max(q_lens))
+    o = nsa.nsa_paged_attn_fwd(dq, *c.args, lse=lse, **kw)
+    w0 = c.weights(0.0).copy_(torch.rand(c.k_pages.shape[0], hk, page, generator=_gen(3)))
+    w = nsa.nsa_paged_attn_weights(dq, c.k_pages, lse, *c.args[2:], weights=w0, decay=0.5, out=c.weights(-7.0), **kw)
+    alone = nsa.nsa_paged_attn_weights(dq, c.k_pages, lse, *c.args[2:], out=c.weights(-7.0), **kw)
+    assert nsa.nsa_device_status() == 0
+    written = torch.zeros(w.shape, dtype=torch.bool)
+    for b in range(len(lens)):
+        a, e, see, (ro, rl, eo, el) = _reference(c, q, cu, b, window, n_sink, scale)
+        ref.within(o[a:e], ro, eo, f"o of sequence {b}")
+        ref.within(lse[a:e], rl, el, f"lse of sequence {b}")
+        # the weights of the call's own lse, as a caller passes it
+        rw, ew = ref.key_weights(q[a:e].double(), c.k[b], see, lse[a:e].cpu().double(), scale)
+        ref.within(c.at(alone, b), rw, ew, f"weights of sequence {b}")
+        half = 0.5 * c.at(w0, b).double()
+        ref.within(c.at(w, b), half + rw, ew + 2 * ref.U * (half + rw), f"decayed weights of sequence {b}")
+        for j in range(lens[b]):
+            written[c.table[b, j // page].item(), :, j % page] = True
+    assert (w.cpu()[~written] == -7.0).all() and (alone.cpu()[~written] == -7.0).all()
+
+
+def test_attention_is_the_same_on_every_run_and_for_every_division():
+    """Any bound of the cached lengths divides the keys differently and gives the same rows."""
+    c = Cache([5000, 1200], 2, 128, 64, 5)
+    for q_lens in ([1, 1], [40, 3]):
+        q, cu = _queries(q_lens, 16, 128, 6)
+        kw = dict(cu_seqlens=cu.cuda(), max_seqlen=max(q_lens))
+        first = None
+        for bound in (None, 5000, 128, 1 << 20):
+            o = [nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, max_cache_len=bound, **kw) for _ in range(2)]
+            assert torch.equal(*o)
+            first = o[0] if first is None else first
+            for b in range(2):
+                a, e, _, (ro, _, eo, _) = _reference(c, q, cu, b, 0, 0, 1.0 / math.sqrt(128))
+                ref.within(o[0][a:e], ro, eo, f"bound {bound}")
+
+
+@pytest.mark.parametrize("scale", [0.3, 4.0])
+def test_large_scores_and_a_rising_maximum(scale):
+    """Keys that grow along the cache move the running maximum in every tile."""
+    c = Cache([900], 1, 64, 64, 7)
+    ramp = torch.linspace(0.1, 3.0, 900)[:, None, None].to(BF)
+    k = (c.k[0].to(BF) * ramp).to(BF)
+    c.k[0] = k.double()
+    for j in range(900):
+        c.k_pages[c.table[0, j // 64].item(), j % 64] = k[j].cuda()
+    for n in (1, 200):
+        q, cu = _queries([n], 4, 64, 8)
+        lse = torch.empty(n, 4, device="cuda")
+        o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, scale=scale, cu_seqlens=cu.cuda(), max_seqlen=n, lse=lse)
+        _, _, _, (ro, rl, eo, el) = _reference(c, q, cu, 0, 0, 0, scale)
+        ref.within(o, ro, eo, "o")
+        ref.within(lse, rl, el, "lse")
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+@pytest.mark.parametrize("n", [1, 70])
+def test_missing_pages_are_masked(bad, n):
+    """Entries that name no page hide their keys, wherever they lie in a tile; a page inside the
+    pool that only holds NaN is never touched through them."""
+    c = Cache([600], 2, 128, 32, 9)
+    hide = [(64, 96), (224, 288), (576, 600)]
+    for lo, hi in hide:
+        c.dev_table[0, lo // 32:-(-hi // 32)] = bad
+    q, cu = _queries([n], 8, 128, 10)
+    lse = torch.empty(n, 8, device="cuda")
+    kw = dict(cu_seqlens=cu.cuda(), max_seqlen=n)
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    _, _, see, (ro, rl, eo, el) = _reference(c, q, cu, 0, 0, 0, 1 / math.sqrt(128), hide)
+    ref.within(o, ro, eo, "o")
+    ref.within(lse, rl, el, "lse")
+    w = nsa.nsa_paged_attn_weights(q.cuda(), c.k_pages, lse, *c.args[2:], out=c.weights(-7.0), **kw)
+    rw, ew = ref.key_weights(q.double(), c.k[0], see, lse.cpu().double(), 1 / math.sqrt(128))
+    got = c.at(w, 0)
+    hidden = torch.zeros(600, dtype=torch.bool)
+    for lo, hi in hide:
+        hidden[lo:hi] = True
+    assert (got[hidden] == -7.0).all()
+    ref.within(got[~hidden], rw[~hidden], ew[~hidden], "weights")
+    c.dev_table.fill_(bad)  # nothing left: no key
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_pages_behind_a_window_may_leave_the_table():
+    c = Cache([800], 1, 64, 16, 11)
+    q, cu = _queries([20], 4, 64, 12)
+    kw = dict(window=100, n_sink=4, cu_seqlens=cu.cuda(), max_seqlen=20)
+    whole = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, **kw)
+    c.dev_table[0, 1:(800 - 20 - 100) // 16] = -1
+    assert torch.equal(whole, nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, **kw))
+
+
+def test_rows_past_the_last_sequence_stay():
+    c = Cache([100, 50], 2, 64, 16, 13)
+    for q_lens in ([1, 1], [60, 20]):
+        q, cu = _queries(q_lens, 4, 64, 14)
+        n = int(cu[-1])
+        q = torch.cat([q, torch.full((9, 4, 64), NAN, dtype=BF)]).cuda()
+        out, lse = torch.full_like(q, 7.0), torch.full((n + 9, 4), 7.0, device="cuda")
+        kw = dict(cu_seqlens=cu.cuda(), max_seqlen=max(q_lens), out=out, lse=lse)
+        nsa.nsa_paged_attn_fwd(q, *c.args, **kw)
+        assert (out[n:] == 7).all() and (lse[n:] == 7).all() and torch.isfinite(out[:n]).all()
+        k_new = torch.full((n + 9, 2, 64), 3.0, dtype=BF, device="cuda")
+        before = c.k_pages.clone()
+        nsa.nsa_paged_append(k_new, k_new, *c.args, cu_seqlens=cu.cuda(), max_seqlen=max(q_lens))
+        assert int((c.k_pages != before).any(-1).any(-1).sum()) >= n  # (NaN slots count as changed)
+        assert int((c.k_pages == 3.0).all(-1).all(-1).sum()) == n
+
+
+# ----------------------------------------------------------------------------- append
+@pytest.mark.parametrize("interleave", [False, True])
+@pytest.mark.parametrize("lens,q_lens,hk,d,page", [
+    ([1], [1], 1, 64, 16), ([17, 200, 64, 5], [17, 1, 0, 9], 3, 128, 32), ([70, 300], [33, 255], 2, 64, 256),
+])
+def test_append(lens, q_lens, hk, d, page, interleave):
+    c = Cache(lens, hk, d, page, 15, interleave=interleave)
+    k, cu = _queries(q_lens, hk, d, 16)
+    v, _ = _queries(q_lens, hk, d, 17)
+    want_k, want_v, w = c.k_pages.clone(), c.v_pages.clone(), c.weights(2.0)
+    want_w = w.clone()
+    for b in range(len(lens)):
+        for i in range(q_lens[b]):
+            p = lens[b] - q_lens[b] + i
+            if p < 0:
+                continue
+            pid, slot = c.table[b, p // page].item(), p % page
+            want_k[pid, slot], want_v[pid, slot], want_w[pid, :, slot] = k[cu[b] + i], v[cu[b] + i], 0.0
+    nsa.nsa_paged_append(k.cuda(), v.cuda(), *c.args, weights=w, cu_seqlens=cu.cuda(), max_seqlen=max(q_lens))
+    for got, want in ((c.k_pages, want_k), (c.v_pages, want_v), (w, want_w)):
+        assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
+
+
+def test_append_drops_tokens_without_a_place():
+    c = Cache([64, 64], 1, 64, 16, 18)
+    c.dev_table[0, 2] = -1
+    c.dev_lens[1] = 200  # past the table row
+    before = c.k_pages.clone()
+    k = torch.ones(2, 40, 1, 64, dtype=BF, device="cuda")
+    nsa.nsa_paged_append(k, k, *c.args)
+    ones = (c.k_pages == 1).all(-1).all(-1)
+    assert int(ones.sum()) == 24  # 40 tokens, 16 of them in the missing page; none of sequence 1
+    rows = before.nan_to_num(9.0) != c.k_pages.nan_to_num(9.0)
+    assert not rows.any(-1).any(-1)[~ones].any()
+
+
+# ----------------------------------------------------------------------------- evict
+def _evict_case(c, w, budget, n_sink, n_recent, alias=False):
+    pages = -(-budget // c.page)
+    n = len(c.lens)
+    new_table = torch.arange(c.k_pages.shape[0], c.k_pages.shape[0] + n * pages, dtype=I32).view(n, pages)
+    new_table = new_table[:, torch.randperm(pages, generator=_gen(1))].contiguous()
+    grow = torch.full((n * pages, c.page, c.hk, c.d), 5.0, dtype=BF, device="cuda")
+    k, v = torch.cat([c.k_pages, grow]), torch.cat([c.v_pages, grow])
+    ww = torch.cat([w, torch.full((n * pages, c.hk, c.page), 5.0, device="cuda")])
+    old = ww.cpu()
+    lens = c.dev_lens.clone()
+    keep, new_lens = nsa.nsa_paged_evict(k, v, ww, c.dev_table, lens, new_table.cuda(), budget, n_sink, n_recent,
+                                         new_lens=lens if alias else None)
+    assert nsa.nsa_device_status() == 0
+    for b, L in enumerate(c.lens):
+        m = min(L, budget)
+        assert int(new_lens[b]) == m
+        for g in range(c.hk):
+            want = ref.choose(c.at(w, b)[:, g].tolist(), L, budget, n_sink, n_recent)
+            assert keep[b, g].tolist() == want + [-1] * (budget - m), (b, g)
+            for i in range(0, budget, max(1, budget // 37)):
+                pid, slot = int(new_table[b, i // c.page]), i % c.page
+                if i < m:
+                    src = c.table[b, want[i] // c.page].item(), want[i] % c.page
+                    assert torch.equal(k[pid, slot, g].cpu().double(), c.k[b][want[i], g])
+                    assert torch.equal(v[pid, slot, g].cpu().double(), c.v[b][want[i], g])
+                    got, exp = float(ww[pid, g, slot]), float(old[src[0], g, src[1]])
+                    assert got == exp or (math.isnan(got) and math.isnan(exp))
+                else:
+                    assert (k[pid, slot, g] == 5).all() and float(ww[pid, g, slot]) == 5.0
+    # what was listed before stays as it was
+    assert torch.equal(k[:c.k_pages.shape[0]].nan_to_num(9.0), c.k_pages.nan_to_num(9.0))
+    return keep
+
+
+@pytest.mark.parametrize("lens,hk,d,page,budget,n_sink,n_recent", [
+    ([1], 1, 64, 16, 1, 0, 0), ([40, 16, 17, 0], 2, 64, 16, 16, 2, 5), ([500, 300], 3, 128, 32, 100, 100, 0),
+    ([500, 130], 1, 128, 64, 129, 0, 129), ([2100, 900, 64], 2, 64, 256, 300, 4, 64), ([1025], 2, 64, 16, 1024, 1, 1),
+])
+def test_evict(lens, hk, d, page, budget, n_sink, n_recent):
+    c = Cache(lens, hk, d, page, 19)
+    w = torch.rand(c.k_pages.shape[0], hk, page, generator=_gen(20)).cuda()
+    _evict_case(c, w, budget, n_sink, n_recent)
+    _evict_case(c, (w * 4).floor() / 4, budget, n_sink, n_recent, alias=True)  # many equal weights
+    _evict_case(c, torch.zeros_like(w), budget, n_sink, n_recent)              # all equal
+
+
+def test_evict_orders_special_weights():
+    c = Cache([64], 1, 64, 16, 21)
+    w = torch.zeros(c.k_pages.shape[0], 1, 16)
+    special = [0.0, -0.0, math.inf, -math.inf, NAN, -1.0, 1e-45, -1e-45, 3e38, -3e38, -NAN, 1.0]
+    for j in range(64):
+        w[c.table[0, j // 16].item(), 0, j % 16] = special[j % len(special)]
+    for budget in (5, 16, 20, 31, 40, 53, 63):
+        _evict_case(c, w.cuda(), budget, 1, 2)
+
+
+def test_evict_long_cache():
+    """More keys than shared memory holds ranks for."""
+    L, budget = 60001, 700
+    page = 256
+    pages = -(-L // page)
+    g = _gen(22)
+    table = torch.randperm(pages + 3, generator=g)[None, :pages].to(I32)
+    k = torch.zeros(pages + 6, page, 1, 64, dtype=BF, device="cuda")
+    w = torch.rand(pages + 6, 1, page, generator=g)
+    new = torch.arange(pages + 3, pages + 6, dtype=I32)[None]
+    keep, lens = nsa.nsa_paged_evict(k, k.clone(), w.cuda(), table.cuda(), torch.tensor([L], dtype=I32).cuda(),
+                                     new.cuda(), budget, 4, 100)
+    at = w[table[0].long(), 0].reshape(-1)[:L]
+    assert keep[0, 0].tolist() == ref.choose(at.tolist(), L, budget, 4, 100) and int(lens) == budget
+
+
+def test_evict_with_missing_pages():
+    """Positions in no page rank lowest, and come as zeros when even they are kept."""
+    c = Cache([64], 1, 64, 16, 23)
+    w = torch.rand(c.k_pages.shape[0], 1, 16, generator=_gen(24)).cuda() - 2.0
+    c.dev_table[0, 1] = -1
+    new = torch.tensor([c.free[:1] + [-1] + c.free[1:2]], dtype=I32, device="cuda")
+    keep, lens = nsa.nsa_paged_evict(c.k_pages, c.v_pages, w, c.dev_table, c.dev_lens, new, 48)
+    assert keep[0, 0].tolist() == [j for j in range(64) if not 16 <= j < 32] and int(lens) == 48
+    assert torch.equal(c.k_pages[c.free[1], 0, 0].cpu().double(), c.k[0][48, 0])  # kept row 32: position 48
+    c = Cache([64], 1, 64, 16, 23, spare=5)
+    c.dev_table[0, 1] = -1
+    new = torch.tensor([c.free[:4]], dtype=I32, device="cuda")
+    keep, _ = nsa.nsa_paged_evict(c.k_pages, c.v_pages, c.weights(1.0), c.dev_table, c.dev_lens, new, 49)
+    assert keep[0, 0].tolist() == list(range(17)) + list(range(32, 64))
+    assert (c.k_pages[c.free[1], 0] == 0).all()  # kept row 16: position 16
+
+
+# ----------------------------------------------------------------------------- the run of them
+def test_serving_run():
+    """Prompt chunks, single tokens and evictions over one pool, every call checked."""
+    H, hk, d, page, budget = 8, 2, 64, 16, 96
+    g = _gen(25)
+    n_pages = 128
+    free = torch.randperm(n_pages, generator=g).tolist()
+    k_pages = torch.full((n_pages, page, hk, d), NAN, dtype=BF, device="cuda")
+    v_pages, w = k_pages.clone(), torch.full((n_pages, hk, page), NAN, device="cuda")
+    B = 2
+    table = torch.full((B, 16), -1, dtype=I32)
+    lens = [0] * B
+    # per sequence and kv-head: the rows in cache order and their weights, in 64 bits
+    rows = [[(torch.zeros(0, d, dtype=torch.float64),) * 2 for _ in range(hk)] for _ in range(B)]
+    acc = [[torch.zeros(0, dtype=torch.float64) for _ in range(hk)] for _ in range(B)]
+    scale = 1 / math.sqrt(d)
+    for step, q_lens in enumerate([[50, 7], [60, 90], [1, 1], [1, 1], [33, 2], [1, 1]]):
+        for b in range(B):
+            while int((table[b] >= 0).sum()) * page < lens[b] + q_lens[b]:
+                table[b, int((table[b] >= 0).sum())] = free.pop()
+            lens[b] += q_lens[b]
+        q, cu = _queries(q_lens, H, d, 100 + step)
+        k, _ = _queries(q_lens, hk, d, 200 + step)
+        v, _ = _queries(q_lens, hk, d, 300 + step)
+        dt, dl = table.cuda(), torch.tensor(lens, dtype=I32, device="cuda")
+        kw = dict(cu_seqlens=cu.cuda(), max_seqlen=max(q_lens))
+        lse = torch.empty(int(cu[-1]), H, device="cuda")
+        nsa.nsa_paged_append(k.cuda(), v.cuda(), k_pages, v_pages, dt, dl, weights=w, **kw)
+        o = nsa.nsa_paged_attn_fwd(q.cuda(), k_pages, v_pages, dt, dl, lse=lse, **kw)
+        nsa.nsa_paged_attn_weights(q.cuda(), k_pages, lse, dt, dl, weights=w, decay=0.75, **kw)
+        bound = max(lens)
+        for b in range(B):
+            a, e = int(cu[b]), int(cu[b + 1])
+            for h in range(hk):
+                kk, vv = (torch.cat([x, y[a:e, h].double()]) for x, y in zip(rows[b][h], (k, v)))
+                rows[b][h] = (kk, vv)
+                hs = slice(h * (H // hk), (h + 1) * (H // hk))
+                see = ref.visible(range(lens[b] - (e - a), lens[b]), lens[b], 0, 0)
+                ro, rl, eo, el = ref.attend(q[a:e, hs].double(), kk[:, None], vv[:, None], see, scale)
+                ref.within(o[a:e, hs], ro, eo, f"step {step} o")
+                ref.within(lse[a:e, hs], rl, el, f"step {step} lse")
+                rw, _ = ref.key_weights(q[a:e, hs].double(), kk[:, None], see, rl, scale)
+                old = torch.cat([acc[b][h], torch.zeros(e - a, dtype=torch.float64)])
+                acc[b][h] = 0.75 * old + rw[:, 0]
+                got = torch.stack([w[table[b, j // page].item(), h, j % page] for j in range(lens[b])]).cpu()
+                # sums of at most `bound` rows' probabilities, each within 1e-4 of its value
+                ref.within(got, acc[b][h], 1e-4 * acc[b][h] + 1e-9, f"step {step} weights")
+        if bound > budget:
+            new = torch.full((B, budget // page), -1, dtype=I32)
+            for b in range(B):
+                for i in range(-(-min(budget, lens[b]) // page)):
+                    new[b, i] = free.pop()
+            keep, new_lens = nsa.nsa_paged_evict(k_pages, v_pages, w, dt, dl, new.cuda(), budget, 4, 20)
+            keep = keep.cpu()
+            for b in range(B):
+                free += [x for x in table[b].tolist() if x >= 0]
+                table[b].fill_(-1)
+                table[b, :new.shape[1]] = new[b]
+                lens[b] = min(lens[b], budget)
+                for h in range(hk):
+                    at = keep[b, h][keep[b, h] >= 0].long()
+                    assert len(at) == lens[b]
+                    assert set(range(4)) <= set(at.tolist())
+                    left = torch.ones(len(acc[b][h]), dtype=torch.bool)
+                    left[at] = False
+                    mid = at[(at >= 4) & (at < len(left) - 20)]
+                    if left.any() and len(mid):  # what stayed weighs at least what went
+                        assert acc[b][h][mid].min() >= acc[b][h][left].max() * (1 - 1e-3)
+                    rows[b][h] = tuple(x[at] for x in rows[b][h])
+                    acc[b][h] = acc[b][h][at]
+            assert new_lens.tolist() == lens
+    assert nsa.nsa_device_status() == 0
+
+
+def test_captured_steps_share_nothing():
+    """Two captured decode steps, each with its own buffers, replayed on two streams at once, and
+    a call on a stream of the caller's own."""
+    c = Cache([3000, 2500], 2, 128, 64, 30)
+    q = [_bf((2, 1, 16, 128), _gen(31 + i)).cuda() for i in range(2)]
+    want = [nsa.nsa_paged_attn_fwd(x, *c.args) for x in q]
+    graphs, outs = [], []
+    for x in q:
+        lse = torch.empty(2, 16, device="cuda")
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = nsa.nsa_paged_attn_fwd(x, *c.args, lse=lse)
+        graphs.append(gr)
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [nsa.nsa_paged_attn_fwd(x, *c.args, stream=s) for x in q for _ in range(10)]
+    torch.cuda.current_stream().wait_stream(s)
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i // 10])
+
+
+# ----------------------------------------------------------------------------- window with sinks
+TRAIN = [
+    ([1], 1, 1, 64, 1, 0), ([1, 2, 17], 4, 2, 64, 1, 1), ([130, 0, 77], 6, 2, 128, 16, 4), ([300], 16, 1, 128, 64, 0),
+    ([700, 129, 128], 8, 2, 128, 100, 3), ([260, 515], 10, 2, 64, 33, 40), ([900], 2, 2, 128, 20, 150),
+    ([640, 383], 24, 8, 64, 1000, 7), ([210], 128, 1, 128, 32, 2), ([1500], 4, 1, 128, 5, 128), ([127, 255], 3, 1, 128, 200, 4),
+]
+
+
+@pytest.mark.parametrize("lens,H,hk,d,window,n_sink", TRAIN)
+def test_sink_window_forward_and_backward(lens, H, hk, d, window, n_sink):
+    q, cu = _queries(lens, H, d, 40)
+    k, _ = _queries(lens, hk, d, 41)
+    v, _ = _queries(lens, hk, d, 42)
+    do, _ = _queries(lens, H, d, 43)
+    n = int(cu[-1])
+    pad = lambda x: torch.cat([x, torch.full((5, *x.shape[1:]), NAN, dtype=BF)]).cuda()  # noqa: E731  rows of no sequence
+    dq, dk, dv, ddo, dcu = pad(q), pad(k), pad(v), pad(do), cu.cuda()
+    lse = torch.full((n + 5, H), 7.0, device="cuda")
+    kw = dict(cu_seqlens=dcu, max_seqlen=max(lens))
+    o = nsa.nsa_swa_sink_fwd(dq, dk, dv, window, n_sink, lse=lse, out=torch.full_like(dq, 7.0), **kw)
+    grads = nsa.nsa_swa_sink_bwd(dq, dk, dv, o, lse, ddo, window, n_sink, dq=torch.full_like(dq, 7.0),
+                                 dk=torch.full_like(dk, 7.0), dv=torch.full_like(dv, 7.0), **kw)
+    again = nsa.nsa_swa_sink_bwd(dq, dk, dv, o, lse, ddo, window, n_sink, **kw)
+    assert nsa.nsa_device_status() == 0
+    for x, y in zip((o, lse, *grads), (None, None, *again)):
+        assert (x[n:] == 7.0).all()
+        assert y is None or torch.equal(x[:n], y[:n])
+    scale = 1 / math.sqrt(d)
+    for b, L in enumerate(lens):
+        a, e = int(cu[b]), int(cu[b + 1])
+        if L == 0:
+            continue
+        see = ref.visible(range(L), L, window, n_sink)
+        x = [t[a:e].double() for t in (q, k, v, do)]
+        ro, rl, eo, el = ref.attend(*x[:3], see, scale)
+        ref.within(o[a:e], ro, eo, f"o of sequence {b}")
+        ref.within(lse[a:e], rl, el, f"lse of sequence {b}")
+        want, bounds = ref.gradients(*x, o[a:e].cpu().double(), lse[a:e].cpu().double(), see, scale)
+        for name, got, w, bd in zip(("dq", "dk", "dv"), grads, want, bounds):
+            ref.within(got[a:e], w, bd, f"{name} of sequence {b}")
+
+
+def test_sink_gradients_against_differences():
+    """The kernel's gradients along random directions against central differences of the 64-bit
+    forward.  A component's error is at most its elementwise bound, so a direction's is at most
+    the bounds' sum weighted by the direction's magnitudes; D from the rounded o adds at most
+    2^-8 sum |dO o| to every dp - D of its row."""
+    T, H, hk, d, window, n_sink, scale = 200, 4, 2, 64, 24, 3, 1 / 8
+    q, cu = _queries([T], H, d, 50)
+    k, _ = _queries([T], hk, d, 51)
+    v, _ = _queries([T], hk, d, 52)
+    do, _ = _queries([T], H, d, 53)
+    lse = torch.empty(T, H, device="cuda")
+    args = [x.cuda() for x in (q, k, v)]
+    o = nsa.nsa_swa_sink_fwd(*args, window, n_sink, lse=lse)
+    grads = nsa.nsa_swa_sink_bwd(*args, o, lse, do.cuda(), window, n_sink)
+    see = ref.visible(range(T), T, window, n_sink)
+    x = [t.double() for t in (q, k, v, do)]
+    ro, rl, _, _ = ref.attend(*x[:3], see, scale)
+    _, bounds = ref.gradients(*x, ro, rl, see, scale)
+    off = ref.B * (x[3] * ro).abs().sum(-1)  # [T, H]: error of D
+    more = [torch.zeros_like(t) for t in x[:3]]
+    for h in range(H):
+        p = torch.where(see, torch.exp(x[0][:, h] @ x[1][:, h // 2].T * scale - rl[:, h][:, None]), 0.0)
+        more[0][:, h] = scale * (p * off[:, h][:, None]) @ x[1][:, h // 2].abs()
+        more[1][:, h // 2] += scale * (p * off[:, h][:, None]).T @ x[0][:, h].abs()
+    for i, (g, bd) in enumerate(zip(grads, bounds)):
+        u = torch.randn(g.shape, generator=_gen(60 + i), dtype=torch.float64)
+        loss = []
+        for s in (1e-5, -1e-5):
+            y = list(x[:3])
+            y[i] = y[i] + s * u
+            loss.append(float((ref.attend(*y, see, scale)[0] * x[3]).sum()))
+        diff = (loss[0] - loss[1]) / 2e-5
+        got = float((g.cpu().double() * u).sum())
+        assert abs(got - diff) <= float(((bd + more[i]) * u.abs()).sum()) + 1e-6 * abs(diff)
+
+
+def test_sink_window_agrees_with_the_window_and_the_cache():
+    """Without sinks the forward is the sliding-window branch's; with them it is what a paged
+    cache of the same tokens serves, token by token and in chunks."""
+    T, H, hk, d, window, n_sink = 500, 16, 2, 128, 64, 4
+    q, cu = _queries([T], H, d, 70)
+    c = Cache([T], hk, d, 64, 71)
+    k, v = (x[0].to(BF).cuda() for x in (c.k, c.v))
+    a = nsa.nsa_swa_sink_fwd(q.cuda(), k, v, window, 0)
+    b = nsa.nsa_swa_fwd(q.cuda(), k, v, window)
+    # both round P and o once: 2 (2^-8 of sum p |v|, at most 2^-8 max |v|) and 2 2^-8 |o|
+    assert ((a - b).abs().float() <= 2 * ref.B * (v.abs().max() + a.abs().float()) * 1.01).all()
+    o = nsa.nsa_swa_sink_fwd(q.cuda(), k, v, window, n_sink)
+    for n in (1, 37, 200):
+        for end in (n, 333, T):
+            if end < n:
+                continue
+            lens = torch.tensor([end], dtype=I32, device="cuda")
+            got = nsa.nsa_paged_attn_fwd(q[None, end - n:end].contiguous().cuda(), *c.args[:3], lens, window, n_sink)
+            e = o[end - n:end]
+            assert ((got[0] - e).abs().float() <= 2 * ref.B * (v.abs().max() + e.abs().float()) * 1.01).all()
+
+
+def test_training_step_captures_while_an_eager_one_lives():
+    T, H, hk, d = 300, 8, 2, 128
+    q, cu = _queries([T], H, d, 80)
+    k, _ = _queries([T], hk, d, 81)
+    v, _ = _queries([T], hk, d, 82)
+    x = [t.cuda() for t in (q, k, v)]
+
+    def step():
+        lse = torch.empty(T, H, device="cuda")
+        o = nsa.nsa_swa_sink_fwd(*x, 50, 4, lse=lse)
+        return (o, *nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 50, 4))
+
+    want = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step()
+    for _ in range(2):
+        gr.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------- bounded waits
+def test_waits_run_out_and_recover():
+    """With a limit of 1 ns the waits give up, the kernels drain and return, the status word says
+    so; with the default limit the next calls are right."""
+    assert nsa.nsa_device_status(reset=True) == 0
+    c = Cache([2000, 900], 2, 128, 64, 90)
+    q, cu = _queries([150, 20], 16, 128, 91)
+    one = _bf((2, 1, 16, 128), _gen(92)).cuda()
+    kw = dict(cu_seqlens=cu.cuda(), max_seqlen=150)
+    lse = torch.zeros(170, 16, device="cuda")
+    k = _bf((170, 2, 128), _gen(93)).cuda()
+    dq = q.cuda()
+    calls = [lambda: nsa.nsa_paged_attn_fwd(dq, *c.args, lse=lse, **kw), lambda: nsa.nsa_paged_attn_fwd(one, *c.args),
+             lambda: nsa.nsa_paged_attn_weights(dq, c.k_pages, lse, *c.args[2:], out=c.weights(0.0), **kw),
+             lambda: nsa.nsa_swa_sink_bwd(dq, k, k, dq, lse, dq, 40, 4, **kw)[1]]
+    want = [f() for f in calls]
+    try:
+        for f in calls:
+            torch.empty(96 << 20, dtype=torch.float32, device="cuda").fill_(1.0)  # past the L2: first copies come late
+            torch.cuda.synchronize()
+            nsa.nsa_set_wait_limit_ns(1)
+            f()
+            torch.cuda.synchronize()
+            assert nsa.nsa_device_status(reset=True) == 4
+            nsa.nsa_set_wait_limit_ns(0)
+    finally:
+        nsa.nsa_set_wait_limit_ns(0)
+        nsa.nsa_device_status(reset=True)
+    for f, w in zip(calls, want):
+        assert torch.equal(f(), w)
+    assert nsa.nsa_device_status() == 0
