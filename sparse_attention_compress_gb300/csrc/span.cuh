@@ -169,13 +169,83 @@ __device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b,
     tc::mma_ss(d_tmem, tc::sdesc(a + off), tc::sdesc(b + off), id, s > 0);
   }
 }
-// O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major.
-template <int D>
+// O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major: the
+// steps S0 .. S1 - 1 of 16 keys.
+template <int D, int S0, int S1>
 __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, int w, bool first) {
   constexpr uint32_t id = tc::idesc(ROWS, D) | kBMn;
 #pragma unroll
-  for (int s = 0; s < KT / 16; ++s)
+  for (int s = S0; s < S1; ++s)
     if (s * 16 < w) tc::mma_ts(d_tmem, p_tmem + s * 8, sdesc_mn(v + s * 2048, KT * 128), id, (first && s == 0) ? 0u : 1u);
+}
+
+// Bounded wait of a warp for phase `parity` (tc::warp_wait's rules: abort flag, time limit,
+// status word), inline: a call would keep the caller's registers in local memory across it,
+// and with nearly all of L1 given to shared memory that is a trip to L2 or DRAM per wait.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const unsigned long long lim = tc::wait_limit();
+  bool ok = lim < tc::kQuickNs ? tc::mbar_test(bar, parity) : tc::mbar_try(bar, parity);
+  if (!ok) {
+    const unsigned long long t0 = tc::globaltimer();
+    const uint32_t hint = lim < 10000000ull ? (uint32_t)lim : 10000000u;
+    while (lim >= tc::kQuickNs && !(ok = tc::mbar_try_for(bar, parity, hint)) && !*abort &&
+           tc::globaltimer() - t0 < lim) {
+    }
+    if (!ok && !*abort) {
+      *abort = 1;
+      atomicExch(&g_device_status, (int)NSA_ERR_TIMEOUT);
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 32 TMEM columns whose load was issued with tc::tmem_ld32_nowait: waits for every load of
+// the thread so far and makes v's registers depend on the wait.
+__device__ __forceinline__ void tmem_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+// Two fp32 operations in one instruction (a pair in a 64-bit register).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Bits lo .. hi - 1 of a word, clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+  const uint32_t below_lo = lo >= 32 ? ~0u : (lo <= 0 ? 0u : (1u << lo) - 1u);
+  return below_hi & ~below_lo;
 }
 
 // TMEM stores of 16 words without the wait (the caller issues tmem_wait_st).

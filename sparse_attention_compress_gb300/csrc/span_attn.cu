@@ -14,7 +14,8 @@
 // one tile: SPLIT) both halves take the same rows and alternate key tiles instead, and the
 // keys are also divided over CTAs; every part leaves (max, sum, unnormalised o) in the
 // workspace and combine_kernel joins them in a fixed order.  Roles: warps 0-7 softmax,
-// warp 8 loads (TMA, span.cuh), warps 9 and 10 issue the products of their half.
+// warps 8 and 11 load K and V (TMA, span.cuh), warps 9 and 10 issue the products of their
+// half.
 // TMEM (512 columns): S of half x at 128 x with P over its first columns, O at 256 + 128 x.
 // V is used as it lies (MN-major B operand), so nothing is transposed.
 #include <algorithm>
@@ -25,7 +26,9 @@
 namespace nsa {
 namespace span {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+// Registers a thread: the softmax warps keep a row of 128 scores, the others next to nothing.
+constexpr int kSoftRegs = 208, kOtherRegs = 56, kMinRegs = 160;  // 256 * 208 + 128 * 56 <= 384 * 160
 constexpr uint32_t kTmemCols = 512;
 
 template <int D, bool SPLIT>
@@ -33,8 +36,11 @@ struct Cfg {
   static constexpr int NQ = SPLIT ? 1 : 2;               // row tiles in shared memory
   static constexpr int Q_BYTES = ROWS * D * 2;
   static constexpr int KV_BYTES = KT * D * 2;
-  static constexpr int NS = D == 64 ? 4 : (SPLIT ? 3 : 2);  // ring stages (what 227 KB hold)
-  static constexpr int SMEM = NQ * Q_BYTES + 2 * NS * KV_BYTES + 1024;
+  // Ring stages (what 227 KB hold).  Even numbers in SPLIT: a stage then always serves the
+  // same half, which so sees every phase of the stage's barriers (one that skipped a phase
+  // could take the phase before the one it waits for for it).
+  static constexpr int NK = D == 64 || SPLIT ? 4 : 3, NV = D == 64 ? 4 : 2;
+  static constexpr int SMEM = NQ * Q_BYTES + (NK + NV) * KV_BYTES + 1024;
 };
 
 struct AttnParams {
@@ -48,18 +54,19 @@ struct AttnParams {
   float scale_log2;
 };
 
-template <int NS>
+template <int NK, int NV>
 struct Bars {
   enum : int {
     Q = 0,
     KFULL = 1,
-    KEMPTY = KFULL + NS,
-    VFULL = KEMPTY + NS,
-    VEMPTY = VFULL + NS,
-    SFULL = VEMPTY + NS,  // [2] by half
-    PFULL = SFULL + 2,    // [2]
-    ODONE = PFULL + 2,    // [2]
-    DRAIN = ODONE + 2,
+    KEMPTY = KFULL + NK,
+    VFULL = KEMPTY + NK,
+    VEMPTY = VFULL + NV,
+    SFULL = VEMPTY + NV,  // [2] by half
+    PFULL = SFULL + 2,    // [2][2] by half and 64-key part
+    ODONE = PFULL + 4,    // [2] the half's last product is done
+    STAGGER = ODONE + 2,  // half 0 is about to form its first P
+    DRAIN = STAGGER + 1,
     COUNT = DRAIN + 1
   };
 };
@@ -75,15 +82,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_v16, const AttnParams p) {
   using C = Cfg<D, SPLIT>;
-  using B = Bars<C::NS>;
-  constexpr int NS = C::NS;
+  using B = Bars<C::NK, C::NV>;
+  constexpr int NK = C::NK, NV = C::NV;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B::COUNT];
   __shared__ uint32_t s_tmem, s_bad[8];  // s_bad: missing 16-row groups of tile i, at i % 8
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, k_s = q_s + C::NQ * C::Q_BYTES, v_s = k_s + NS * C::KV_BYTES;
+  const uint32_t q_s = base, k_s = q_s + C::NQ * C::Q_BYTES, v_s = k_s + NK * C::KV_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
@@ -107,17 +114,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     const int users = !SPLIT && two ? 2 : 1;
     tc::mbar_init(bar(B::Q), 1);
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NK; ++i) {
       tc::mbar_init(bar(B::KFULL + i), 1);
       tc::mbar_init(bar(B::KEMPTY + i), users);
+    }
+    for (int i = 0; i < NV; ++i) {
       tc::mbar_init(bar(B::VFULL + i), 1);
       tc::mbar_init(bar(B::VEMPTY + i), users);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(B::SFULL + i), 1);
-      tc::mbar_init(bar(B::PFULL + i), 128);
+      tc::mbar_init(bar(B::PFULL + 2 * i), 128);
+      tc::mbar_init(bar(B::PFULL + 2 * i + 1), 128);
       tc::mbar_init(bar(B::ODONE + i), 1);
     }
+    tc::mbar_init(bar(B::STAGGER), 128);
     tc::mbar_init(bar(B::DRAIN), 2);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -131,8 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
 
   int last_k = -1, last_v = -1;
+  // (each warpgroup states its register share in its own branch: the compiler allots by branch)
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
   if (warp == 8) {
-    // ------------------------------------------------------------------ loads
+    // ------------------------------------------------------------------ Q and K
     if (lane == 0 && n > 0) {
       const int nq = two && !SPLIT ? 2 : 1;
       tc::mbar_expect_tx(bar(B::Q), (uint32_t)(nq * p.tpc * p.R * D * 2));
@@ -141,10 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tma3d(q_s + x * C::Q_BYTES + c * (ROWS * 128), &tm_q, c * 64, g * p.R, (int)(start + t0 + x * p.tpc),
                     bar(B::Q));
     }
+    __syncwarp();
     for (int j = 0; j < n; ++j) {
-      const int st = j % NS, key0 = tiles.key0(a + j), w = tiles.width(a + j);
-      if (j >= NS && !tc::warp_wait(bar(B::KEMPTY + st), ((j / NS) - 1) & 1, abort)) break;
-      const uint32_t kb = bar(B::KFULL + st);
+      const int sk = j % NK, key0 = tiles.key0(a + j), w = tiles.width(a + j);
+      if (j >= NK && !wait(bar(B::KEMPTY + sk), ((j / NK) - 1) & 1, abort)) break;
       // the flags of tile j are read by its softmax after S(j), so they are in place before
       // the K tile's arrival; the missing pages of K and V are the same
       if (PAGED) {
@@ -152,43 +165,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) s_bad[j & 7] = bad;
         __syncwarp();
       }
-      load_tile<D, PAGED>(k_s + st * C::KV_BYTES, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w,
-                          kv_len, kb, lane);
+      load_tile<D, PAGED>(k_s + sk * C::KV_BYTES, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w,
+                          kv_len, bar(B::KFULL + sk), lane);
       last_k = j;
-      if (j >= NS && !tc::warp_wait(bar(B::VEMPTY + st), ((j / NS) - 1) & 1, abort)) break;
-      load_tile<D, PAGED>(v_s + st * C::KV_BYTES, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w,
-                          kv_len, bar(B::VFULL + st), lane);
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------------ V
+    for (int j = 0; j < n; ++j) {
+      const int sv = j % NV;
+      if (j >= NV && !wait(bar(B::VEMPTY + sv), ((j / NV) - 1) & 1, abort)) break;
+      load_tile<D, PAGED>(v_s + sv * C::KV_BYTES, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start,
+                          tiles.key0(a + j), tiles.width(a + j), kv_len, bar(B::VFULL + sv), lane);
       last_v = j;
     }
-  } else if (warp > 8) {
+  } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------------ products of half x
     const int x = warp - 9, cnt = count_of(x);
     const uint32_t qh = q_s + (SPLIT ? 0 : x * C::Q_BYTES), s_t = tmem + x * 128, o_t = tmem + 256 + x * 128;
-    bool ok = cnt == 0 || tc::warp_wait(bar(B::Q), 0, abort);
+    bool ok = cnt == 0 || wait(bar(B::Q), 0, abort);
+    // the halves start half a tile apart, else they would form their P at the same time and
+    // leave the tensor cores idle together: in step 5580 cycles a tile, apart 3100
+    if (ok && !SPLIT && x == 1 && cnt > 0) ok = wait(bar(B::STAGGER), 0, abort);
     for (int it = 0; ok && it < cnt; ++it) {
-      const int j = tile_of(x, it), st = j % NS, w = tiles.width(a + j);
-      // P(it - 1), over S, has been read
-      if (it > 0 && !(ok = tc::warp_wait(bar(B::ODONE + x), (it - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(B::KFULL + st), (j / NS) & 1, abort))) break;
+      const int j = tile_of(x, it), sk = j % NK, sv = j % NV, w = tiles.width(a + j);
+      if (!(ok = wait(bar(B::KFULL + sk), (j / NK) & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_abt<D>(s_t, qh, k_s + st * C::KV_BYTES, w);
+        // over P(it - 1): this lane issued its product, and products execute in issue order
+        mma_abt<D>(s_t, qh, k_s + sk * C::KV_BYTES, w);
         tc::commit(bar(B::SFULL + x));
-        tc::commit(bar(B::KEMPTY + st));
+        tc::commit(bar(B::KEMPTY + sk));
       }
       __syncwarp();
-      if (!(ok = tc::warp_wait(bar(B::PFULL + x), it & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(B::VFULL + st), (j / NS) & 1, abort))) break;
+      // the first 64 keys' product runs while the softmax forms the others
+      if (!(ok = wait(bar(B::VFULL + sv), (j / NV) & 1, abort))) break;
+      if (!(ok = wait(bar(B::PFULL + 2 * x), it & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_pv<D>(o_t, s_t, v_s + st * C::KV_BYTES, w, it == 0);
-        tc::commit(bar(B::ODONE + x));
-        tc::commit(bar(B::VEMPTY + st));
+        mma_pv<D, 0, 4>(o_t, s_t, v_s + sv * C::KV_BYTES, w, it == 0);
+      }
+      __syncwarp();
+      if (!(ok = wait(bar(B::PFULL + 2 * x + 1), it & 1, abort))) break;
+      if (lane == 0) {
+        tc::fence_after();
+        mma_pv<D, 4, 8>(o_t, s_t, v_s + sv * C::KV_BYTES, w, false);
+        tc::commit(bar(B::VEMPTY + sv));
+        if (it == cnt - 1) tc::commit(bar(B::ODONE + x));
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax of half x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     const int x = warp >> 2, row = tid & 127, cnt = count_of(x);
     const int tl = row / p.R, hd = row % p.R, t = t0 + (SPLIT ? 0 : x * p.tpc) + tl;
     const bool valid = tl < p.tpc && t < Lq;
@@ -200,41 +228,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int it = 0; it < cnt; ++it) {
       const int j = tile_of(x, it), key0 = tiles.key0(a + j), w = tiles.width(a + j);
-      if (!(ok = tc::warp_wait(bar(B::SFULL + x), it & 1, abort))) break;
+      if (!(ok = wait(bar(B::SFULL + x), it & 1, abort))) break;
       tc::fence_after();
       if (work) {
         float sv[KT];
-#pragma unroll
-        for (int c = 0; c < KT; c += 32)
-          if (c < w) tc::tmem_ld32_nowait(s_t + c, sv + c);
+        tc::tmem_ld32_nowait(s_t, sv);
+        if (w > 32) tc::tmem_ld32_nowait(s_t + 32, sv + 32);
         // seen columns: [j_lo, j_hi) and, of those before j_lo, the sinks [0, j_sink)
         const int j_hi = min(pos + 1 - key0, w);
         const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = p.n_sink - key0;
         const uint32_t bad = PAGED ? s_bad[j & 7] : 0u;
-        const bool all = j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0;
-        tc::tmem_wait_ld();
-        if (!__all_sync(0xffffffffu, all)) {
+        const bool all =
+            __all_sync(0xffffffffu, j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0);
+        // columns c .. c + 31 that are not seen get -inf
+        auto mask = [&](int c) {
+          uint32_t see = bits(j_lo - c, j_hi - c) | bits(0, min(j_sink, j_hi) - c);
+          if (PAGED) {
+            const uint32_t b2 = (bad >> (c / GRAN)) & 3u;
+            see &= ~((b2 & 1u ? 0xffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
+          }
 #pragma unroll
-          for (int c = 0; c < KT; ++c) {
-            const bool see = c < j_hi && (c >= j_lo || c < j_sink) && !((bad >> (c / GRAN)) & 1u);
-            sv[c] = see ? sv[c] : kNegInf;
+          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+        };
+        float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        auto max_of = [&](int c) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            mx4[0] = max3(mx4[0], sv[c + e], sv[c + e + 1]);
+            mx4[1] = max3(mx4[1], sv[c + e + 2], sv[c + e + 3]);
+            mx4[2] = max3(mx4[2], sv[c + e + 4], sv[c + e + 5]);
+            mx4[3] = max3(mx4[3], sv[c + e + 6], sv[c + e + 7]);
+          }
+        };
+        tmem_wait_ld(sv);
+        tmem_wait_ld(sv + 32);
+        if (w > 64) tc::tmem_ld32_nowait(s_t + 64, sv + 64);
+        if (w > 96) tc::tmem_ld32_nowait(s_t + 96, sv + 96);
+        if (all) {
+          max_of(0);
+          max_of(32);
+          tmem_wait_ld(sv + 64);
+          tmem_wait_ld(sv + 96);
+          max_of(64);
+          max_of(96);
+        } else {
+          tmem_wait_ld(sv + 64);
+          tmem_wait_ld(sv + 96);
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) {
+            mask(c);
+            max_of(c);
           }
         }
-        float mx = kNegInf;
-        {
-          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int c = 4; c < KT; c += 4) {
-            m4[0] = fmaxf(m4[0], sv[c]);
-            m4[1] = fmaxf(m4[1], sv[c + 1]);
-            m4[2] = fmaxf(m4[2], sv[c + 2]);
-            m4[3] = fmaxf(m4[3], sv[c + 3]);
-          }
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         // the running maximum moves only when a score exceeds it by 2^8 (P stays within
-        // range, and O in TMEM is rarely rescaled); S(it) was issued after PV(it - 1), so O
-        // is complete here
+        // range, and O in TMEM is rarely rescaled); S(it) followed PV(it - 1) on the tensor
+        // pipe, so O is complete here
         const bool need = mx > m + 8.f;
         if (__any_sync(0xffffffffu, need)) {
           const float alpha = need ? ex2(m - mx) : 1.f;
@@ -253,28 +302,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mx;
           }
         }
+        if (!SPLIT && x == 0 && it == 0) tc::mbar_arrive(bar(B::STAGGER));
         const float mu = m == kNegInf ? 0.f : m;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), mu2 = pair(-mu, -mu);
+        uint64_t l2[4] = {0, 0, 0, 0};  // four chains of two row sums
 #pragma unroll
         for (int c = 0; c < KT; c += 32) {
-          if (c >= w) break;
-          uint32_t pk[16];
+          if (c < w) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float e0 = ex2(fmaf(sv[c + e], p.scale_log2, -mu)), e1 = ex2(fmaf(sv[c + e + 1], p.scale_log2, -mu));
-            l4[(e >> 1) & 3] += e0 + e1;
-            pk[e / 2] = pack_bf16(e0, e1);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, mu2));
+              const float e0 = ex2(y.x), e1 = ex2(y.y);
+              l2[(e >> 1) & 3] = add2(l2[(e >> 1) & 3], pair(e0, e1));
+              pk[e / 2] = pack_bf16(e0, e1);
+            }
+            tmem_st16_nowait(s_t + c / 2, pk);
           }
-          tmem_st16_nowait(s_t + c / 2, pk);
+          if (c == 32) {  // P of the first 64 keys
+            tmem_wait_st();
+            tc::fence_before();
+            tc::mbar_arrive(bar(B::PFULL + 2 * x));
+          }
         }
         tmem_wait_st();
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        const float2 la = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
+        l += la.x + la.y;
+      } else {
+        if (!SPLIT && x == 0 && it == 0) tc::mbar_arrive(bar(B::STAGGER));
+        tc::fence_before();
+        tc::mbar_arrive(bar(B::PFULL + 2 * x));
       }
       tc::fence_before();
-      tc::mbar_arrive(bar(B::PFULL + x));
+      tc::mbar_arrive(bar(B::PFULL + 2 * x + 1));
     }
     if (ok && cnt > 0) {
-      ok = tc::warp_wait(bar(B::ODONE + x), (cnt - 1) & 1, abort);
+      ok = wait(bar(B::ODONE + x), 0, abort);
       tc::fence_after();
     }
     if (ok && (SPLIT || x == 0 || two)) {
@@ -325,23 +388,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // copies and products still in flight land before the CTA leaves
     if (warp == 8) {
       if (n > 0) tc::warp_drain(bar(B::Q), 0);
-      for (int st = 0; st < NS; ++st) {
-        const int ik = last_in_stage(last_k, st, NS), iv = last_in_stage(last_v, st, NS);
-        if (ik >= 0) tc::warp_drain(bar(B::KFULL + st), (ik / NS) & 1);
-        if (iv >= 0) tc::warp_drain(bar(B::VFULL + st), (iv / NS) & 1);
-      }
-    } else if (warp > 8) {
+      for (int st = 0; st < NK; ++st)
+        if (const int i = last_in_stage(last_k, st, NK); i >= 0) tc::warp_drain(bar(B::KFULL + st), (i / NK) & 1);
+    } else if (warp == 11) {
+      for (int st = 0; st < NV; ++st)
+        if (const int i = last_in_stage(last_v, st, NV); i >= 0) tc::warp_drain(bar(B::VFULL + st), (i / NV) & 1);
+    } else if (warp == 9 || warp == 10) {
       if (lane == 0) tc::commit(bar(B::DRAIN));
       __syncwarp();
       tc::warp_drain(bar(B::DRAIN), 0);
     }
   } else if (warp == 8) {
     // the last release of every stage lands before the CTA leaves
-    for (int st = 0; st < NS; ++st) {
-      const int ik = last_in_stage(last_k, st, NS), iv = last_in_stage(last_v, st, NS);
-      if (ik >= 0) tc::warp_drain(bar(B::KEMPTY + st), (ik / NS) & 1);
-      if (iv >= 0) tc::warp_drain(bar(B::VEMPTY + st), (iv / NS) & 1);
-    }
+    for (int st = 0; st < NK; ++st)
+      if (const int i = last_in_stage(last_k, st, NK); i >= 0) tc::warp_drain(bar(B::KEMPTY + st), (i / NK) & 1);
+  } else if (warp == 11) {
+    for (int st = 0; st < NV; ++st)
+      if (const int i = last_in_stage(last_v, st, NV); i >= 0) tc::warp_drain(bar(B::VEMPTY + st), (i / NV) & 1);
   }
   tc::fence_before();
   __syncthreads();
@@ -437,6 +500,10 @@ cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, dim3 grid, cudaS
   constexpr int smem = Cfg<D, SPLIT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // the softmax warps' share must come out of what the block is launched with
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+  if (at.numRegs < kMinRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
   return cudaGetLastError();
 }
