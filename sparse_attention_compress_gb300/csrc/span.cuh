@@ -146,58 +146,100 @@ __device__ __forceinline__ uint32_t missing_groups(const Keys& c, int seq, int k
   return __ballot_sync(0xffffffffu, lane * GRAN < w && key < kv_len && page_of(c, seq, key) < 0);
 }
 
-// Shared-memory descriptor of an MN-major operand with 128-byte swizzling: rows of 64
-// MN-elements (128 B) along K in 1024-byte atoms of 8 rows; lbo: bytes between groups of
-// 64 MN-elements.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFF) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// ------------------------------------------------------------------ products
+// The issuing warp shares its scheduler with softmax warps, so every instruction it needs
+// per product shows up as tensor-core time.  All its lanes run the same code (operands then
+// stay in uniform registers) and one elected lane's products and commits take effect;
+// descriptors differ from a per-tile base by constants.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred q;\n.reg .b32 l;\nelect.sync l|q, 0xffffffff;\nselp.b32 %0, 1, 0, q;\n}\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+// Low words of the shared-memory descriptors (address and leading offset); the high word is
+// the same for both: 8 rows of 128 bytes to an atom, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// K-major tile (tc::sdesc), and MN-major tile with 64-element groups KT * 128 bytes apart.
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFF) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) {
+  return ((saddr & 0x3FFFF) >> 4) | ((uint32_t)(KT * 128 >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accum, uint32_t lead) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "mov.b64 x, {%1, %6};\nmov.b64 y, {%2, %6};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accum, uint32_t lead) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "mov.b64 y, {%2, %6};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(kDescHi)
+      : "memory");
 }
 constexpr uint32_t kBMn = 1u << 16;  // instruction descriptor: B is MN-major
 
-// S[128 x w] = A[128 x D] B[w x D]^T, both K-major tiles (64-column groups 16 KB apart).
+// S[128 x w] = A[128 x D] B[w x D]^T, both K-major tiles (64-column groups 16 KB apart); a
+// and b: desc_k of their bases.
 template <int D>
-__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int w) {
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int w, uint32_t lead) {
   const uint32_t id = tc::idesc(ROWS, w);
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
-    const uint32_t off = (s >> 2) * (KT * 128) + (s & 3) * 32;
-    tc::mma_ss(d_tmem, tc::sdesc(a + off), tc::sdesc(b + off), id, s > 0);
+    const uint32_t off = ((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4;
+    mma_ss(d_tmem, a + off, b + off, id, s > 0, lead);
   }
 }
-// O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major: the
-// steps S0 .. S1 - 1 of 16 keys.
+// O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major (v:
+// desc_mn of its base): the steps S0 .. S1 - 1 of 16 keys.
 template <int D, int S0, int S1>
-__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, int w, bool first) {
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, int w, bool first, uint32_t lead) {
   constexpr uint32_t id = tc::idesc(ROWS, D) | kBMn;
+  if (w >= S1 * 16) {
 #pragma unroll
-  for (int s = S0; s < S1; ++s)
-    if (s * 16 < w) tc::mma_ts(d_tmem, p_tmem + s * 8, sdesc_mn(v + s * 2048, KT * 128), id, (first && s == 0) ? 0u : 1u);
+    for (int s = S0; s < S1; ++s)
+      mma_ts(d_tmem, p_tmem + s * 8, v + s * (2048 >> 4), id, s == 0 ? !first : 1u, lead);
+  } else {
+#pragma unroll
+    for (int s = S0; s < S1; ++s)
+      if (s * 16 < w) mma_ts(d_tmem, p_tmem + s * 8, v + s * (2048 >> 4), id, s == 0 ? !first : 1u, lead);
+  }
 }
 
 // Bounded wait of a warp for phase `parity` (tc::warp_wait's rules: abort flag, time limit,
 // status word), inline: a call would keep the caller's registers in local memory across it,
 // and with nearly all of L1 given to shared memory that is a trip to L2 or DRAM per wait.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  const unsigned long long lim = tc::wait_limit();
-  bool ok = lim < tc::kQuickNs ? tc::mbar_test(bar, parity) : tc::mbar_try(bar, parity);
-  if (!ok) {
-    const unsigned long long t0 = tc::globaltimer();
-    const uint32_t hint = lim < 10000000ull ? (uint32_t)lim : 10000000u;
-    while (lim >= tc::kQuickNs && !(ok = tc::mbar_try_for(bar, parity, hint)) && !*abort &&
-           tc::globaltimer() - t0 < lim) {
+// `quick`: the limit is below tc::kQuickNs (one unsuccessful probe gives up).
+struct Waits {
+  volatile int* abort;
+  bool quick;
+  __device__ __forceinline__ explicit Waits(volatile int* a) : abort(a), quick(tc::wait_limit() < tc::kQuickNs) {}
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    bool ok = quick ? tc::mbar_test(bar, parity) : tc::mbar_try(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      const unsigned long long t0 = tc::globaltimer(), lim = tc::wait_limit();
+      const uint32_t hint = lim < 10000000ull ? (uint32_t)lim : 10000000u;
+      while (!quick && !ok && !(ok = tc::mbar_try_for(bar, parity, hint)) && !*abort && tc::globaltimer() - t0 < lim) {
+      }
+      if (!ok && !*abort) {
+        *abort = 1;
+        atomicExch(&g_device_status, (int)NSA_ERR_TIMEOUT);
+      }
+      return __all_sync(0xffffffffu, ok);
     }
-    if (!ok && !*abort) {
-      *abort = 1;
-      atomicExch(&g_device_status, (int)NSA_ERR_TIMEOUT);
-    }
+    return true;
   }
-  return __all_sync(0xffffffffu, ok);
-}
+};
 
 // 32 TMEM columns whose load was issued with tc::tmem_ld32_nowait: waits for every load of
 // the thread so far and makes v's registers depend on the wait.

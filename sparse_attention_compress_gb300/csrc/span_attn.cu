@@ -14,8 +14,7 @@
 // one tile: SPLIT) both halves take the same rows and alternate key tiles instead, and the
 // keys are also divided over CTAs; every part leaves (max, sum, unnormalised o) in the
 // workspace and combine_kernel joins them in a fixed order.  Roles: warps 0-7 softmax,
-// warps 8 and 11 load K and V (TMA, span.cuh), warps 9 and 10 issue the products of their
-// half.
+// warps 8 and 11 load (TMA, span.cuh), warp 9 (SPLIT: and 10) issues the products.
 // TMEM (512 columns): S of half x at 128 x with P over its first columns, O at 256 + 128 x.
 // V is used as it lies (MN-major B operand), so nothing is transposed.
 #include <algorithm>
@@ -30,17 +29,34 @@ constexpr int kThreads = 384;
 // Registers a thread: the softmax warps keep a row of 128 scores, the others next to nothing.
 constexpr int kSoftRegs = 208, kOtherRegs = 56, kMinRegs = 160;  // 256 * 208 + 128 * 56 <= 384 * 160
 constexpr uint32_t kTmemCols = 512;
+// P may exceed 1 by 2^kLazy before the running maximum moves: the floating-point formats of
+// P, of the sums and of O hold it with the same relative precision.
+constexpr float kLazy = 16.f;
 
 template <int D, bool SPLIT>
 struct Cfg {
-  static constexpr int NQ = SPLIT ? 1 : 2;               // row tiles in shared memory
+  static constexpr int NQ = SPLIT ? 1 : 2;  // row tiles in shared memory
   static constexpr int Q_BYTES = ROWS * D * 2;
   static constexpr int KV_BYTES = KT * D * 2;
-  // Ring stages (what 227 KB hold).  Even numbers in SPLIT: a stage then always serves the
-  // same half, which so sees every phase of the stage's barriers (one that skipped a phase
-  // could take the phase before the one it waits for for it).
-  static constexpr int NK = D == 64 || SPLIT ? 4 : 3, NV = D == 64 ? 4 : 2;
-  static constexpr int SMEM = NQ * Q_BYTES + (NK + NV) * KV_BYTES + 1024;
+  // Two rings of tiles.  Otherwise K tiles go through ring 0 and V tiles through ring 1, read
+  // by both halves; SPLIT: ring x is half x's own and holds its K and V tiles in turn, so
+  // that every wait sees every phase of its slot (halves that took alternate items of one
+  // ring would skip phases, and mistake the one before for the one they wait for).
+  static constexpr int N0 = D == 64 ? (SPLIT ? 6 : 5) : 3, N1 = D == 64 ? (SPLIT ? 6 : 5) : (SPLIT ? 3 : 2);
+  static constexpr int SMEM = NQ * Q_BYTES + (N0 + N1) * KV_BYTES + 1024;
+};
+
+// Position in a ring of n slots: the slot and the parity of its phase.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 struct AttnParams {
@@ -54,19 +70,16 @@ struct AttnParams {
   float scale_log2;
 };
 
-template <int NK, int NV>
+template <int NS>
 struct Bars {
   enum : int {
     Q = 0,
-    KFULL = 1,
-    KEMPTY = KFULL + NK,
-    VFULL = KEMPTY + NK,
-    VEMPTY = VFULL + NV,
-    SFULL = VEMPTY + NV,  // [2] by half
+    FULL = 1,             // [NS] ring 0's slots, then ring 1's
+    EMPTY = FULL + NS,
+    SFULL = EMPTY + NS,   // [2] by half
     PFULL = SFULL + 2,    // [2][2] by half and 64-key part
     ODONE = PFULL + 4,    // [2] the half's last product is done
-    STAGGER = ODONE + 2,  // half 0 is about to form its first P
-    DRAIN = STAGGER + 1,
+    DRAIN = ODONE + 2,
     COUNT = DRAIN + 1
   };
 };
@@ -82,19 +95,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_v16, const AttnParams p) {
   using C = Cfg<D, SPLIT>;
-  using B = Bars<C::NK, C::NV>;
-  constexpr int NK = C::NK, NV = C::NV;
+  constexpr int N0 = C::N0, N1 = C::N1, NS = N0 + N1;
+  using B = Bars<NS>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B::COUNT];
-  __shared__ uint32_t s_tmem, s_bad[8];  // s_bad: missing 16-row groups of tile i, at i % 8
+  __shared__ uint32_t s_tmem, s_bad[2][8];  // s_bad: missing 16-row groups of a half's (else any) tile i, at i % 8
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, k_s = q_s + C::NQ * C::Q_BYTES, v_s = k_s + NK * C::KV_BYTES;
+  const uint32_t q_s = base, slots = q_s + C::NQ * C::Q_BYTES;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
   if (tc::device_status_set()) return;
+  const Waits wait(abort);
   const int seq = blockIdx.y, g = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
   const int64_t start = seq_start(p.seqs, seq);
   const int Lq = seq_len(p.seqs, seq);
@@ -114,13 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     const int users = !SPLIT && two ? 2 : 1;
     tc::mbar_init(bar(B::Q), 1);
-    for (int i = 0; i < NK; ++i) {
-      tc::mbar_init(bar(B::KFULL + i), 1);
-      tc::mbar_init(bar(B::KEMPTY + i), users);
-    }
-    for (int i = 0; i < NV; ++i) {
-      tc::mbar_init(bar(B::VFULL + i), 1);
-      tc::mbar_init(bar(B::VEMPTY + i), users);
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(bar(B::FULL + i), 1);
+      tc::mbar_init(bar(B::EMPTY + i), users);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(B::SFULL + i), 1);
@@ -128,7 +138,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(B::PFULL + 2 * i + 1), 128);
       tc::mbar_init(bar(B::ODONE + i), 1);
     }
-    tc::mbar_init(bar(B::STAGGER), 128);
     tc::mbar_init(bar(B::DRAIN), 2);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -141,12 +150,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
-  int last_k = -1, last_v = -1;
+  int last_item = -1;  // loading warps: the last item handed to their ring
   // (each warpgroup states its register share in its own branch: the compiler allots by branch)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-  if (warp == 8) {
-    // ------------------------------------------------------------------ Q and K
-    if (lane == 0 && n > 0) {
+  if (warp == 8 || warp == 11) {
+    // ------------------------------------------------------------------ loads of ring y
+    const int y = warp == 8 ? 0 : 1;
+    if (y == 0 && lane == 0 && n > 0) {
       const int nq = two && !SPLIT ? 2 : 1;
       tc::mbar_expect_tx(bar(B::Q), (uint32_t)(nq * p.tpc * p.R * D * 2));
       for (int x = 0; x < nq; ++x)
@@ -155,64 +165,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bar(B::Q));
     }
     __syncwarp();
-    for (int j = 0; j < n; ++j) {
-      const int sk = j % NK, key0 = tiles.key0(a + j), w = tiles.width(a + j);
-      if (j >= NK && !wait(bar(B::KEMPTY + sk), ((j / NK) - 1) & 1, abort)) break;
-      // the flags of tile j are read by its softmax after S(j), so they are in place before
-      // the K tile's arrival; the missing pages of K and V are the same
-      if (PAGED) {
+    const int cnt = SPLIT ? 2 * count_of(y) : n, ns = y ? N1 : N0, first = y ? N0 : 0;
+    int slot = 0;
+    uint32_t phase = 1;
+    for (int i = 0; i < cnt; ++i) {
+      const int it = SPLIT ? i >> 1 : i, j = SPLIT ? 2 * it + y : i;
+      const bool is_v = SPLIT ? (i & 1) : y == 1;
+      const int key0 = tiles.key0(a + j), w = tiles.width(a + j);
+      if (i >= ns && !wait(bar(B::EMPTY + first + slot), phase)) break;
+      // the flags of a tile are read by its softmax after S, so they are in place before the
+      // K tile's arrival; the missing pages of K and V are the same
+      if (PAGED && !is_v) {
         const uint32_t bad = missing_groups(p.keys, seq, key0, w, kv_len, lane);
-        if (lane == 0) s_bad[j & 7] = bad;
+        if (lane == 0) s_bad[SPLIT ? y : 0][it & 7] = bad;
         __syncwarp();
       }
-      load_tile<D, PAGED>(k_s + sk * C::KV_BYTES, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w,
-                          kv_len, bar(B::KFULL + sk), lane);
-      last_k = j;
+      load_tile<D, PAGED>(slots + (first + slot) * C::KV_BYTES, is_v ? &tm_v : &tm_k, is_v ? &tm_v16 : &tm_k16,
+                          is_v ? p.keys.v : p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, kv_len,
+                          bar(B::FULL + first + slot), lane);
+      last_item = i;
+      if (++slot == ns) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
-  } else if (warp == 11) {
-    // ------------------------------------------------------------------ V
-    for (int j = 0; j < n; ++j) {
-      const int sv = j % NV;
-      if (j >= NV && !wait(bar(B::VEMPTY + sv), ((j / NV) - 1) & 1, abort)) break;
-      load_tile<D, PAGED>(v_s + sv * C::KV_BYTES, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start,
-                          tiles.key0(a + j), tiles.width(a + j), kv_len, bar(B::VFULL + sv), lane);
-      last_v = j;
+  } else if (warp == 9 || (SPLIT && warp == 10)) {
+    // ------------------------------------------------------------------ products
+    // SPLIT: each warp issues for its own half, as its softmax proceeds.  Otherwise one warp
+    // issues for both in turn: PV and the next S of a half go out together, so the halves run
+    // half a tile apart.  (Two issuers' products interleave on the pipe and end together;
+    // the halves then form their P at the same time and the tensor cores wait for both.)
+    const int x0 = SPLIT ? warp - 9 : 0, nx = SPLIT ? 1 : (two ? 2 : 1), cnt = count_of(x0);
+    bool ok = cnt == 0 || wait(bar(B::Q), 0);
+    // K and V items: one ring of the half's own (SPLIT), or the two common rings
+    Ring<N0> rk;
+    Ring<N1> rv;
+    const int first_k = SPLIT ? x0 * N0 : 0, first_v = SPLIT ? x0 * N0 : N0;
+    if (SPLIT) rv.next();
+    auto next = [&](auto& r) {
+      r.next();
+      if (SPLIT) r.next();
+    };
+    const uint32_t lead = elect(), q_d = desc_k(q_s), slots_k = desc_k(slots), slots_v = desc_mn(slots);
+    constexpr uint32_t kSlot = C::KV_BYTES >> 4;  // in descriptor units
+    auto issue_s = [&](int x, int w) {
+      mma_abt<D>(tmem + x * 128, q_d + (SPLIT ? 0 : x * (C::Q_BYTES >> 4)), slots_k + (first_k + rk.slot) * kSlot, w,
+                 lead);
+      commit(bar(B::SFULL + x), lead);
+      commit(bar(B::EMPTY + first_k + rk.slot), lead);
+    };
+    int w = tiles.width(a + tile_of(x0, 0));
+    if (ok && cnt > 0) {
+      ok = wait(bar(B::FULL + first_k + rk.slot), rk.phase);
+      if (ok) {
+        tc::fence_after();
+        for (int q = 0; q < nx; ++q) issue_s(x0 + q, w);
+      }
+      next(rk);
     }
-  } else if (warp == 9 || warp == 10) {
-    // ------------------------------------------------------------------ products of half x
-    const int x = warp - 9, cnt = count_of(x);
-    const uint32_t qh = q_s + (SPLIT ? 0 : x * C::Q_BYTES), s_t = tmem + x * 128, o_t = tmem + 256 + x * 128;
-    bool ok = cnt == 0 || wait(bar(B::Q), 0, abort);
-    // the halves start half a tile apart, else they would form their P at the same time and
-    // leave the tensor cores idle together: in step 5580 cycles a tile, apart 3100
-    if (ok && !SPLIT && x == 1 && cnt > 0) ok = wait(bar(B::STAGGER), 0, abort);
     for (int it = 0; ok && it < cnt; ++it) {
-      const int j = tile_of(x, it), sk = j % NK, sv = j % NV, w = tiles.width(a + j);
-      if (!(ok = wait(bar(B::KFULL + sk), (j / NK) & 1, abort))) break;
-      if (lane == 0) {
+      const bool more = it + 1 < cnt;
+      const int w_next = more ? tiles.width(a + tile_of(x0, it + 1)) : 0;
+      const uint32_t vs = slots_v + (first_v + rv.slot) * kSlot;
+      if (!(ok = wait(bar(B::FULL + first_v + rv.slot), rv.phase))) break;
+      for (int x = x0; ok && x < x0 + nx; ++x) {
+        const uint32_t s_t = tmem + x * 128, o_t = tmem + 256 + x * 128;
+        // the first 64 keys' product runs while the softmax forms the others
+        if (!(ok = wait(bar(B::PFULL + 2 * x), it & 1))) break;
         tc::fence_after();
-        // over P(it - 1): this lane issued its product, and products execute in issue order
-        mma_abt<D>(s_t, qh, k_s + sk * C::KV_BYTES, w);
-        tc::commit(bar(B::SFULL + x));
-        tc::commit(bar(B::KEMPTY + sk));
-      }
-      __syncwarp();
-      // the first 64 keys' product runs while the softmax forms the others
-      if (!(ok = wait(bar(B::VFULL + sv), (j / NV) & 1, abort))) break;
-      if (!(ok = wait(bar(B::PFULL + 2 * x), it & 1, abort))) break;
-      if (lane == 0) {
+        mma_pv<D, 0, 4>(o_t, s_t, vs, w, it == 0, lead);
+        if (more && !(ok = wait(bar(B::FULL + first_k + rk.slot), rk.phase))) break;
+        if (!(ok = wait(bar(B::PFULL + 2 * x + 1), it & 1))) break;
         tc::fence_after();
-        mma_pv<D, 0, 4>(o_t, s_t, v_s + sv * C::KV_BYTES, w, it == 0);
+        mma_pv<D, 4, 8>(o_t, s_t, vs, w, false, lead);
+        commit(bar(B::EMPTY + first_v + rv.slot), lead);
+        if (more)  // over P(it): this lane issued its product, and products execute in issue order
+          issue_s(x, w_next);
+        else
+          commit(bar(B::ODONE + x), lead);
       }
-      __syncwarp();
-      if (!(ok = wait(bar(B::PFULL + 2 * x + 1), it & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_pv<D, 4, 8>(o_t, s_t, v_s + sv * C::KV_BYTES, w, false);
-        tc::commit(bar(B::VEMPTY + sv));
-        if (it == cnt - 1) tc::commit(bar(B::ODONE + x));
-      }
-      __syncwarp();
+      next(rk);
+      next(rv);
+      w = w_next;
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax of half x
@@ -228,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int it = 0; it < cnt; ++it) {
       const int j = tile_of(x, it), key0 = tiles.key0(a + j), w = tiles.width(a + j);
-      if (!(ok = wait(bar(B::SFULL + x), it & 1, abort))) break;
+      if (!(ok = wait(bar(B::SFULL + x), it & 1))) break;
       tc::fence_after();
       if (work) {
         float sv[KT];
@@ -237,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // seen columns: [j_lo, j_hi) and, of those before j_lo, the sinks [0, j_sink)
         const int j_hi = min(pos + 1 - key0, w);
         const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = p.n_sink - key0;
-        const uint32_t bad = PAGED ? s_bad[j & 7] : 0u;
+        const uint32_t bad = PAGED ? s_bad[SPLIT ? x : 0][it & 7] : 0u;
         const bool all =
             __all_sync(0xffffffffu, j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0);
         // columns c .. c + 31 that are not seen get -inf
@@ -260,34 +294,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx4[3] = max3(mx4[3], sv[c + e + 6], sv[c + e + 7]);
           }
         };
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+        uint64_t mu2, l2[4];  // minus the maximum, twice; four chains of two row sums
+        uint32_t pk[32];
+        // P of columns c .. c + 31 to pk[at ..]
+        auto exps = [&](int c, int at) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, mu2));
+            const float e0 = ex2(y.x), e1 = ex2(y.y);
+            l2[(e >> 1) & 3] = add2(l2[(e >> 1) & 3], pair(e0, e1));
+            pk[at + e / 2] = pack_bf16(e0, e1);
+          }
+        };
+        auto first_half = [&]() {
+          const float mu = m == kNegInf ? 0.f : -m;
+          mu2 = pair(mu, mu);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l2[e] = 0;
+          exps(0, 0);
+          exps(32, 16);
+        };
         tmem_wait_ld(sv);
         tmem_wait_ld(sv + 32);
         if (w > 64) tc::tmem_ld32_nowait(s_t + 64, sv + 64);
         if (w > 96) tc::tmem_ld32_nowait(s_t + 96, sv + 96);
-        if (all) {
-          max_of(0);
-          max_of(32);
-          tmem_wait_ld(sv + 64);
-          tmem_wait_ld(sv + 96);
-          max_of(64);
-          max_of(96);
-        } else {
-          tmem_wait_ld(sv + 64);
-          tmem_wait_ld(sv + 96);
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) {
-            mask(c);
-            max_of(c);
-          }
+        if (!all) {
+          mask(0);
+          mask(32);
         }
+        // the first 64 exponentials are taken with the maximum so far, while the other scores
+        // arrive and the tile's own maximum is found; the running maximum moves (and they are
+        // taken again) only when a score exceeds it by 2^kLazy
+        if (it > 0) first_half();
+        max_of(0);
+        max_of(32);
+        tmem_wait_ld(sv + 64);
+        tmem_wait_ld(sv + 96);
+        if (!all) {
+          mask(64);
+          mask(96);
+        }
+        max_of(64);
+        max_of(96);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-        // the running maximum moves only when a score exceeds it by 2^8 (P stays within
-        // range, and O in TMEM is rarely rescaled); S(it) followed PV(it - 1) on the tensor
-        // pipe, so O is complete here
-        const bool need = mx > m + 8.f;
-        if (__any_sync(0xffffffffu, need)) {
+        const bool need = mx > m + kLazy;
+        if (__any_sync(0xffffffffu, need) || it == 0) {
           const float alpha = need ? ex2(m - mx) : 1.f;
           if (it > 0) {
+            // S(it) followed PV(it - 1) on the tensor pipe, so O is complete here
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float ov[32];
@@ -301,35 +356,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= alpha;
             m = mx;
           }
+          first_half();
         }
-        if (!SPLIT && x == 0 && it == 0) tc::mbar_arrive(bar(B::STAGGER));
-        const float mu = m == kNegInf ? 0.f : m;
-        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), mu2 = pair(-mu, -mu);
-        uint64_t l2[4] = {0, 0, 0, 0};  // four chains of two row sums
-#pragma unroll
-        for (int c = 0; c < KT; c += 32) {
-          if (c < w) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, mu2));
-              const float e0 = ex2(y.x), e1 = ex2(y.y);
-              l2[(e >> 1) & 3] = add2(l2[(e >> 1) & 3], pair(e0, e1));
-              pk[e / 2] = pack_bf16(e0, e1);
-            }
-            tmem_st16_nowait(s_t + c / 2, pk);
-          }
-          if (c == 32) {  // P of the first 64 keys
-            tmem_wait_st();
-            tc::fence_before();
-            tc::mbar_arrive(bar(B::PFULL + 2 * x));
-          }
-        }
+        tmem_st16_nowait(s_t, pk);
+        if (w > 32) tmem_st16_nowait(s_t + 16, pk + 16);
+        if (w > 64) exps(64, 0);
         tmem_wait_st();
+        tc::fence_before();
+        tc::mbar_arrive(bar(B::PFULL + 2 * x));  // P of the first 64 keys
+        if (w > 64) {
+          tmem_st16_nowait(s_t + 32, pk);
+          if (w > 96) {
+            exps(96, 16);
+            tmem_st16_nowait(s_t + 48, pk + 16);
+          }
+          tmem_wait_st();
+        }
         const float2 la = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
         l += la.x + la.y;
       } else {
-        if (!SPLIT && x == 0 && it == 0) tc::mbar_arrive(bar(B::STAGGER));
         tc::fence_before();
         tc::mbar_arrive(bar(B::PFULL + 2 * x));
       }
@@ -337,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_arrive(bar(B::PFULL + 2 * x + 1));
     }
     if (ok && cnt > 0) {
-      ok = wait(bar(B::ODONE + x), 0, abort);
+      ok = wait(bar(B::ODONE + x), 0);
       tc::fence_after();
     }
     if (ok && (SPLIT || x == 0 || two)) {
@@ -386,75 +431,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort) {
     // copies and products still in flight land before the CTA leaves
-    if (warp == 8) {
-      if (n > 0) tc::warp_drain(bar(B::Q), 0);
-      for (int st = 0; st < NK; ++st)
-        if (const int i = last_in_stage(last_k, st, NK); i >= 0) tc::warp_drain(bar(B::KFULL + st), (i / NK) & 1);
-    } else if (warp == 11) {
-      for (int st = 0; st < NV; ++st)
-        if (const int i = last_in_stage(last_v, st, NV); i >= 0) tc::warp_drain(bar(B::VFULL + st), (i / NV) & 1);
+    if (warp == 8 || warp == 11) {
+      if (warp == 8 && n > 0) tc::warp_drain(bar(B::Q), 0);
+      const int ns = warp == 8 ? N0 : N1, first = warp == 8 ? 0 : N0;
+      for (int st = 0; st < ns; ++st)
+        if (const int i = last_in_stage(last_item, st, ns); i >= 0)
+          tc::warp_drain(bar(B::FULL + first + st), (i / ns) & 1);
     } else if (warp == 9 || warp == 10) {
       if (lane == 0) tc::commit(bar(B::DRAIN));
       __syncwarp();
       tc::warp_drain(bar(B::DRAIN), 0);
     }
-  } else if (warp == 8) {
-    // the last release of every stage lands before the CTA leaves
-    for (int st = 0; st < NK; ++st)
-      if (const int i = last_in_stage(last_k, st, NK); i >= 0) tc::warp_drain(bar(B::KEMPTY + st), (i / NK) & 1);
-  } else if (warp == 11) {
-    for (int st = 0; st < NV; ++st)
-      if (const int i = last_in_stage(last_v, st, NV); i >= 0) tc::warp_drain(bar(B::VEMPTY + st), (i / NV) & 1);
+  } else if (warp == 8 || warp == 11) {
+    // the last release of every slot lands before the CTA leaves
+    const int ns = warp == 8 ? N0 : N1, first = warp == 8 ? 0 : N0;
+    for (int st = 0; st < ns; ++st)
+      if (const int i = last_in_stage(last_item, st, ns); i >= 0)
+        tc::warp_drain(bar(B::EMPTY + first + st), (i / ns) & 1);
   }
   tc::fence_before();
   __syncthreads();
   if (warp == 9) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the parts of a row in order: one warp a (token, head) row.  Reads every part once
-// (a part without keys is skipped), writes bf16 o and the lse.
-template <int D>
+// Joins the parts of a row in order: PW warps a (token, head) row, each every PW-th part
+// (eight warps where there are many parts, whose loads would otherwise wait for one
+// another), then a sum over the warps.  Reads every part once (a part without keys is
+// skipped), writes bf16 o and the lse.
+template <int D, int PW>
 __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int parts) {
-  const int64_t rows = p.seqs.tokens * p.h;
-  const int64_t rr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (rr >= rows) return;
-  const int64_t tok = rr / p.h;
-  const int seq = seq_of_token(p.seqs, tok);
-  if (tok < seq_start(p.seqs, seq) || tok - seq_start(p.seqs, seq) >= seq_len(p.seqs, seq)) return;  // no sequence's row
-  float m = kNegInf;
-  for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * rows + rr].x);
-#pragma unroll
-  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   constexpr int E = D / 32;
-  float acc[E] = {}, l = 0.f;
-  if (m > kNegInf) {
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float wl = 0.f, w = 0.f;
-      if (i0 + lane < parts) {
-        const float2 ml = p.part_ml[(int64_t)(i0 + lane) * rows + rr];
-        if (ml.y > 0.f) {
-          w = ex2(ml.x - m);
-          wl = w * ml.y;
-        }
-      }
-      const int e1 = min(32, parts - i0);
-#pragma unroll 4
-      for (int i = 0; i < e1; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, wl, i);
-        l += li;
-        if (li > 0.f) {  // (an underflowed weight would only add zeros)
-          const float* src = p.part_o + ((int64_t)(i0 + i) * rows + rr) * D + lane * E;
+  __shared__ float s_acc[8][D + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pw = warp % PW;
+  const int64_t rows = p.seqs.tokens * p.h;
+  const int64_t rr = (int64_t)blockIdx.x * (8 / PW) + warp / PW;
+  bool mine = rr < rows;
+  if (mine) {
+    const int64_t tok = rr / p.h;
+    const int seq = seq_of_token(p.seqs, tok);
+    const int64_t i = tok - seq_start(p.seqs, seq);
+    mine = i >= 0 && i < seq_len(p.seqs, seq);  // (a row of no sequence is left alone)
+  }
+  float m = kNegInf, acc[E] = {}, l = 0.f;
+  if (mine) {
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * rows + rr].x);
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(src + e);
-            acc[e] += wi * v.x;
-            acc[e + 1] += wi * v.y;
+    for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    if (m > kNegInf) {
+      for (int i0 = pw; i0 < parts; i0 += 32 * PW) {
+        float wl = 0.f, w = 0.f;
+        if (i0 + lane * PW < parts) {
+          const float2 ml = p.part_ml[(int64_t)(i0 + lane * PW) * rows + rr];
+          if (ml.y > 0.f) {
+            w = ex2(ml.x - m);
+            wl = w * ml.y;
+          }
+        }
+        const int e1 = min(32, (parts - i0 + PW - 1) / PW);
+#pragma unroll 4
+        for (int i = 0; i < e1; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, wl, i);
+          l += li;
+          if (li > 0.f) {  // (an underflowed weight would only add zeros)
+            const float* src = p.part_o + ((int64_t)(i0 + i * PW) * rows + rr) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(src + e);
+              acc[e] += wi * v.x;
+              acc[e + 1] += wi * v.y;
+            }
           }
         }
       }
     }
   }
+  if (PW > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_acc[warp][D] = l;
+    __syncthreads();
+    if (pw != 0) return;
+#pragma unroll
+    for (int w = 1; w < PW; ++w) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + w][lane * E + e];
+      l += s_acc[warp + w][D];
+    }
+  }
+  if (!mine) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -538,7 +602,10 @@ cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int 
                              : (pl.split ? run_attn<D, false, true>(m, p, grid, st) : run_attn<D, false, false>(m, p, grid, st));
   if (e != cudaSuccess || pl.parts == 1) return e;
   const int64_t rows = s.tokens * h;
-  combine_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl.parts);
+  if (pl.parts >= 8)
+    combine_kernel<D, 8><<<(unsigned)rows, 256, 0, st>>>(p, pl.parts);
+  else
+    combine_kernel<D, 1><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl.parts);
   return cudaGetLastError();
 }
 

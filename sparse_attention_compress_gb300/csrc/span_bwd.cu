@@ -43,6 +43,11 @@ struct BwdParams {
 
 __device__ __forceinline__ int last_in(int last, int st, int ns) { return last < st ? -1 : last - (last - st) % ns; }
 
+template <int D>
+__device__ __forceinline__ void mma_abt1(uint32_t d_tmem, uint32_t a, uint32_t b, int w) {
+  mma_abt<D>(d_tmem, desc_k(a), desc_k(b), w, 1u);
+}
+
 // (+)= A[128 x w] (bf16 in TMEM: columns 0..31 hold the first 64, 64..95 the others)
 // B[w x D], a tile of w rows read MN-major.
 template <int D>
@@ -51,8 +56,8 @@ __device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, ui
 #pragma unroll
   for (int s = 0; s < KT / 16; ++s)
     if (s * 16 < w)
-      tc::mma_ts(d_tmem, a_tmem + (s < 4 ? s * 8 : 64 + (s - 4) * 8), sdesc_mn(b + s * 2048, KT * 128), id,
-                 (first && s == 0) ? 0u : 1u);
+      mma_ts(d_tmem, a_tmem + (s < 4 ? s * 8 : 64 + (s - 4) * 8), desc_mn(b) + s * (2048 >> 4), id,
+             (first && s == 0) ? 0u : 1u, 1u);
 }
 
 // ---------------------------------------------------------------------------- dQ
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!(ok = tc::warp_wait(bar(KFULL + sk), (j / kNK) & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_abt<D>(tmem + b * 128, q_s, k_s + sk * TB, tiles.width(j));
+        mma_abt1<D>(tmem + b * 128, q_s, k_s + sk * TB, tiles.width(j));
         tc::commit(bar(SFULL + b));
       }
       __syncwarp();
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!(ok = tc::warp_wait(bar(VFULL + sv), (j / kNV) & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_abt<D>(tmem + 256, do_s, v_s + sv * TB, tiles.width(j));
+        mma_abt1<D>(tmem + 256, do_s, v_s + sv * TB, tiles.width(j));
         tc::commit(bar(PFULL));
         tc::commit(bar(VEMPTY + sv));
       }
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_abt<D>(tmem, k_s, q_s + st * TB, p.cols);
+        mma_abt1<D>(tmem, k_s, q_s + st * TB, p.cols);
         tc::commit(bar(SFULL));
       }
       __syncwarp();
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       if (!(ok = tc::warp_wait(bar(DFULL + st), (j >> 1) & 1, abort))) break;
       if (lane == 0) {
         tc::fence_after();
-        mma_abt<D>(tmem + 128, v_s, do_s + st * TB, p.cols);
+        mma_abt1<D>(tmem + 128, v_s, do_s + st * TB, p.cols);
         tc::commit(bar(DPFULL));
         tc::commit(bar(DEMPTY + st));
       }
