@@ -189,16 +189,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
 }
 constexpr uint32_t kBMn = 1u << 16;  // instruction descriptor: B is MN-major
 
-// S[128 x w] = A[128 x D] B[w x D]^T, both K-major tiles (64-column groups 16 KB apart); a
-// and b: desc_k of their bases.
+// S[128 x w] = A[128 x D] B[w x D]^T, both K-major tiles (64-column groups 16 KB apart, A's
+// a_group descriptor units); a and b: desc_k of their bases.
 template <int D>
-__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int w, uint32_t lead) {
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int w, uint32_t lead,
+                                        uint32_t a_group = KT * 128 >> 4) {
   const uint32_t id = tc::idesc(ROWS, w);
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const uint32_t off = ((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4;
-    mma_ss(d_tmem, a + off, b + off, id, s > 0, lead);
-  }
+  for (int s = 0; s < D / 16; ++s)
+    mma_ss(d_tmem, a + (s >> 2) * a_group + (s & 3) * 2, b + (s >> 2) * (KT * 128 >> 4) + (s & 3) * 2, id, s > 0,
+           lead);
 }
 // O[128 x D] (+)= P[128 x w] (bf16 in TMEM) V[w x D], V a tile of w rows read MN-major (v:
 // desc_mn of its base): the steps S0 .. S1 - 1 of 16 keys.

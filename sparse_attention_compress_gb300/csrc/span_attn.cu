@@ -8,14 +8,19 @@
 // rounding of the bf16 output itself).
 //
 // A tile is 128 rows = 128 / group tokens x the heads of a kv-group, so each K / V tile is
-// read once for the whole group.  A CTA holds two such row tiles ("halves", four softmax
-// warps each, one row a thread) over one K / V ring: while one half's softmax runs, the
-// tensor cores work for the other.  With few rows (a decode step, or chunks whose rows fit
-// one tile: SPLIT) both halves take the same rows and alternate key tiles instead, and the
-// keys are also divided over CTAs; every part leaves (max, sum, unnormalised o) in the
-// workspace and combine_kernel joins them in a fixed order.  Roles: warps 0-7 softmax,
-// warps 8 and 11 load (TMA, span.cuh), warp 9 (SPLIT: and 10) issues the products.
-// TMEM (512 columns): S of half x at 128 x with P over its first columns, O at 256 + 128 x.
+// read once for the whole group.  Two forms of one kernel:
+//   many rows   a CTA (one an SM) holds two row tiles ("halves", four softmax warps each, one
+//               row a thread) over common K and V rings; while one half's softmax runs the
+//               tensor cores work for the other.
+//   FEW         (a decode step, a few speculative tokens: at most 48 rows a sequence and
+//               kv-head) a CTA holds one row tile whose Q takes only the rows it has, so
+//               that two CTAs share an SM and keep HBM busy through each other's starts and
+//               ends; the rows past Q's are whatever lies there and stay in their own lanes.
+// Work units (row tile, sequence, kv-head) that would not fill the SMs evenly have their keys
+// divided over several CTAs: each leaves (max, sum, unnormalised o) in the workspace and
+// combine_kernel joins them in a fixed order.  Roles: softmax warps (one row a thread),
+// loading warps (TMA, span.cuh), one warp that issues the products.
+// TMEM: S of half x at 128 x with P over its first columns, then O of the halves.
 // V is used as it lies (MN-major B operand), so nothing is transposed.
 #include <algorithm>
 
@@ -25,25 +30,25 @@
 namespace nsa {
 namespace span {
 
-constexpr int kThreads = 384;
 // Registers a thread: the softmax warps keep a row of 128 scores, the others next to nothing.
-constexpr int kSoftRegs = 208, kOtherRegs = 56, kMinRegs = 160;  // 256 * 208 + 128 * 56 <= 384 * 160
-constexpr uint32_t kTmemCols = 512;
+constexpr int kSoftRegs = 208;
 // P may exceed 1 by 2^kLazy before the running maximum moves: the floating-point formats of
 // P, of the sums and of O hold it with the same relative precision.
 constexpr float kLazy = 16.f;
+constexpr int kFewRows = 48;  // what leaves room for two FEW CTAs on an SM
+constexpr int kSms = 152;
 
-template <int D, bool SPLIT>
+template <int D, bool FEW>
 struct Cfg {
-  static constexpr int NQ = SPLIT ? 1 : 2;  // row tiles in shared memory
-  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int NH = FEW ? 1 : 2;  // row tiles (halves)
+  static constexpr int THREADS = FEW ? 256 : 384;
   static constexpr int KV_BYTES = KT * D * 2;
-  // Two rings of tiles.  Otherwise K tiles go through ring 0 and V tiles through ring 1, read
-  // by both halves; SPLIT: ring x is half x's own and holds its K and V tiles in turn, so
-  // that every wait sees every phase of its slot (halves that took alternate items of one
-  // ring would skip phases, and mistake the one before for the one they wait for).
-  static constexpr int N0 = D == 64 ? (SPLIT ? 6 : 5) : 3, N1 = D == 64 ? (SPLIT ? 6 : 5) : (SPLIT ? 3 : 2);
-  static constexpr int SMEM = NQ * Q_BYTES + (N0 + N1) * KV_BYTES + 1024;
+  // Two rings of tiles, for K and for V.  FEW: one ring holds K and V tiles in turn.
+  static constexpr int N0 = D == 64 ? (FEW ? 6 : 5) : 3, N1 = FEW ? 0 : (D == 64 ? 5 : 2);
+  static constexpr uint32_t TMEM = FEW ? 256 : 512;
+  static constexpr int OTHER_REGS = FEW ? 40 : 56;
+  // what the launch must give a thread for the shares to add up
+  static constexpr int MIN_REGS = (NH * 128 * kSoftRegs + 128 * OTHER_REGS + THREADS - 1) / THREADS;
 };
 
 // Position in a ring of n slots: the slot and the parity of its phase.
@@ -64,10 +69,26 @@ struct AttnParams {
   Keys keys;
   __nv_bfloat16* o;
   float* lse;     // optional
-  float* part_o;  // [parts][tokens * h][D] fp32, or null: one part, written to o
-  float2* part_ml;  // [parts][tokens * h] (running max in base-2 units, sum)
-  int h, hkv, R, tpc, window, n_sink, n_splits;
+  float* part_o;    // [divided units][n_splits][cta_rows][D] fp32: unnormalised o
+  float2* part_ml;  // [divided units][n_splits][cta_rows]: (running max in base-2 units, sum)
+  int h, hkv, R, tpc, window, n_sink;
+  int n_whole, n_splits, cta_rows, q_group;  // units 0 .. n_whole - 1 are not divided; q_group: bytes
+                                             // between Q's 64-column groups
   float scale_log2;
+};
+
+// Unit u: row tile `rev` from a sequence's last (the longest spans first), sequence, kv-head.
+struct Unit {
+  int seq, g, t0, Lq;  // t0 < 0: no such rows
+  int64_t start;
+  __device__ __forceinline__ Unit(const AttnParams& p, int64_t u, int rows_tok) {
+    g = (int)(u % p.hkv);
+    seq = (int)(u / p.hkv % p.seqs.n_seqs);
+    const int rev = (int)(u / p.hkv / p.seqs.n_seqs);
+    start = seq_start(p.seqs, seq);
+    Lq = seq_len(p.seqs, seq);
+    t0 = ((Lq + rows_tok - 1) / rows_tok - 1 - rev) * rows_tok;
+  }
 };
 
 template <int NS>
@@ -89,61 +110,62 @@ __device__ __forceinline__ int last_in_stage(int last, int st, int ns) {
   return last < st ? -1 : last - (last - st) % ns;
 }
 
-template <int D, bool PAGED, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool PAGED, bool FEW>
+__global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_v16, const AttnParams p) {
-  using C = Cfg<D, SPLIT>;
-  constexpr int N0 = C::N0, N1 = C::N1, NS = N0 + N1;
+  using C = Cfg<D, FEW>;
+  constexpr int NH = C::NH, N0 = C::N0, N1 = C::N1, NS = N0 + N1;
   using B = Bars<NS>;
+  constexpr int kLoad0 = 4 * NH, kIssue = 4 * NH + 1, kLoad1 = FEW ? -1 : 4 * NH + 2;  // warps; 0 .. 4 NH - 1: softmax
+  constexpr uint32_t kO = NH * 128;  // TMEM column of O
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B::COUNT];
-  __shared__ uint32_t s_tmem, s_bad[2][8];  // s_bad: missing 16-row groups of a half's (else any) tile i, at i % 8
+  __shared__ uint32_t s_tmem, s_bad[8];  // s_bad: missing 16-row groups of tile i, at i % 8
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, slots = q_s + C::NQ * C::Q_BYTES;
+  const uint32_t q_bytes = (D / 64) * p.q_group;  // of a half
+  const uint32_t q_s = base, slots = q_s + NH * q_bytes;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
   if (tc::device_status_set()) return;
   const Waits wait(abort);
-  const int seq = blockIdx.y, g = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
-  const int64_t start = seq_start(p.seqs, seq);
-  const int Lq = seq_len(p.seqs, seq);
-  const int rows_tok = C::NQ * p.tpc;  // tokens of this CTA
-  const int t0 = ((Lq + rows_tok - 1) / rows_tok - 1 - (int)blockIdx.x) * rows_tok;  // longest spans first
-  if (t0 < 0) return;
+  const int rows_tok = NH * p.tpc;  // tokens of this CTA
+  const bool whole = (int64_t)blockIdx.x < p.n_whole;
+  const int64_t part_unit = whole ? 0 : ((int64_t)blockIdx.x - p.n_whole) / p.n_splits;
+  const int split = whole ? 0 : (int)(((int64_t)blockIdx.x - p.n_whole) % p.n_splits), n_splits = whole ? 1 : p.n_splits;
+  const Unit un(p, whole ? (int64_t)blockIdx.x : p.n_whole + part_unit, rows_tok);
+  if (un.t0 < 0) return;
+  const int seq = un.seq, g = un.g, t0 = un.t0, Lq = un.Lq;
+  const int64_t start = un.start;
   const int kv_len = PAGED ? cached_len(p.keys, seq) : Lq;
   const int off = kv_len - Lq;  // position of the sequence's first query
   const Tiles tiles(off + t0, off + min(t0 + rows_tok, Lq) - 1, p.window, p.n_sink);
-  const int a = (int)((int64_t)tiles.n * split / p.n_splits);
-  const int n = (int)((int64_t)tiles.n * (split + 1) / p.n_splits) - a;  // this CTA's tiles: a .. a + n - 1
-  const bool two = SPLIT || t0 + p.tpc < Lq;  // the second half has rows
-  // tiles of half x: every one, or (SPLIT) every second one
-  auto count_of = [&](int x) { return SPLIT ? (n + 1 - x) >> 1 : (x == 0 || two ? n : 0); };
-  auto tile_of = [&](int x, int it) { return SPLIT ? 2 * it + x : it; };
+  const int a = (int)((int64_t)tiles.n * split / n_splits);
+  const int n = (int)((int64_t)tiles.n * (split + 1) / n_splits) - a;  // this CTA's tiles: a .. a + n - 1
+  const int nh = !FEW && t0 + p.tpc < Lq ? 2 : 1;  // halves that have rows
 
   if (tid == 0) {
-    const int users = !SPLIT && two ? 2 : 1;
     tc::mbar_init(bar(B::Q), 1);
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(bar(B::FULL + i), 1);
-      tc::mbar_init(bar(B::EMPTY + i), users);
+      tc::mbar_init(bar(B::EMPTY + i), nh);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(B::SFULL + i), 1);
-      tc::mbar_init(bar(B::PFULL + 2 * i), 128);
-      tc::mbar_init(bar(B::PFULL + 2 * i + 1), 128);
+      tc::mbar_init(bar(B::PFULL + 2 * i), 4);  // one arrival a softmax warp
+      tc::mbar_init(bar(B::PFULL + 2 * i + 1), 4);
       tc::mbar_init(bar(B::ODONE + i), 1);
     }
-    tc::mbar_init(bar(B::DRAIN), 2);
+    tc::mbar_init(bar(B::DRAIN), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+  if (warp == kIssue) {
+    tmem_alloc(smem_u32(&s_tmem), C::TMEM);
     tc::fence_before();
   }
   __syncthreads();
@@ -152,32 +174,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int last_item = -1;  // loading warps: the last item handed to their ring
   // (each warpgroup states its register share in its own branch: the compiler allots by branch)
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-  if (warp == 8 || warp == 11) {
+  if (warp >= 4 * NH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER_REGS));
+  if (warp == kLoad0 || warp == kLoad1) {
     // ------------------------------------------------------------------ loads of ring y
-    const int y = warp == 8 ? 0 : 1;
+    const int y = warp == kLoad0 ? 0 : 1;
     if (y == 0 && lane == 0 && n > 0) {
-      const int nq = two && !SPLIT ? 2 : 1;
-      tc::mbar_expect_tx(bar(B::Q), (uint32_t)(nq * p.tpc * p.R * D * 2));
-      for (int x = 0; x < nq; ++x)
+      tc::mbar_expect_tx(bar(B::Q), (uint32_t)(nh * p.tpc * p.R * D * 2));
+      for (int x = 0; x < nh; ++x)
         for (int c = 0; c < D / 64; ++c)
-          tc::tma3d(q_s + x * C::Q_BYTES + c * (ROWS * 128), &tm_q, c * 64, g * p.R, (int)(start + t0 + x * p.tpc),
-                    bar(B::Q));
+          tc::tma3d(q_s + x * q_bytes + c * p.q_group, &tm_q, c * 64, g * p.R, (int)(start + t0 + x * p.tpc), bar(B::Q));
     }
     __syncwarp();
-    const int cnt = SPLIT ? 2 * count_of(y) : n, ns = y ? N1 : N0, first = y ? N0 : 0;
+    const int cnt = FEW ? 2 * n : n, ns = y ? N1 : N0, first = y ? N0 : 0;
     int slot = 0;
     uint32_t phase = 1;
     for (int i = 0; i < cnt; ++i) {
-      const int it = SPLIT ? i >> 1 : i, j = SPLIT ? 2 * it + y : i;
-      const bool is_v = SPLIT ? (i & 1) : y == 1;
+      const int j = FEW ? i >> 1 : i;
+      const bool is_v = FEW ? (i & 1) : y == 1;
       const int key0 = tiles.key0(a + j), w = tiles.width(a + j);
       if (i >= ns && !wait(bar(B::EMPTY + first + slot), phase)) break;
       // the flags of a tile are read by its softmax after S, so they are in place before the
       // K tile's arrival; the missing pages of K and V are the same
       if (PAGED && !is_v) {
         const uint32_t bad = missing_groups(p.keys, seq, key0, w, kv_len, lane);
-        if (lane == 0) s_bad[SPLIT ? y : 0][it & 7] = bad;
+        if (lane == 0) s_bad[j & 7] = bad;
         __syncwarp();
       }
       load_tile<D, PAGED>(slots + (first + slot) * C::KV_BYTES, is_v ? &tm_v : &tm_k, is_v ? &tm_v16 : &tm_k16,
@@ -189,52 +209,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u;
       }
     }
-  } else if (warp == 9 || (SPLIT && warp == 10)) {
+  } else if (warp == kIssue) {
     // ------------------------------------------------------------------ products
-    // SPLIT: each warp issues for its own half, as its softmax proceeds.  Otherwise one warp
-    // issues for both in turn: PV and the next S of a half go out together, so the halves run
-    // half a tile apart.  (Two issuers' products interleave on the pipe and end together;
-    // the halves then form their P at the same time and the tensor cores wait for both.)
-    const int x0 = SPLIT ? warp - 9 : 0, nx = SPLIT ? 1 : (two ? 2 : 1), cnt = count_of(x0);
-    bool ok = cnt == 0 || wait(bar(B::Q), 0);
-    // K and V items: one ring of the half's own (SPLIT), or the two common rings
+    // One warp issues for both halves in turn: PV and the next S of a half go out together,
+    // so the halves run half a tile apart.  (Two issuers' products interleave on the pipe and
+    // end together; the halves then form their P at the same time and the tensor cores wait
+    // for both.)
+    bool ok = n == 0 || wait(bar(B::Q), 0);
     Ring<N0> rk;
-    Ring<N1> rv;
-    const int first_k = SPLIT ? x0 * N0 : 0, first_v = SPLIT ? x0 * N0 : N0;
-    if (SPLIT) rv.next();
+    Ring<FEW ? N0 : N1> rv;  // FEW: the same ring, one item on
+    constexpr int first_v = FEW ? 0 : N0;
+    if (FEW) rv.next();
     auto next = [&](auto& r) {
       r.next();
-      if (SPLIT) r.next();
+      if (FEW) r.next();
     };
     const uint32_t lead = elect(), q_d = desc_k(q_s), slots_k = desc_k(slots), slots_v = desc_mn(slots);
     constexpr uint32_t kSlot = C::KV_BYTES >> 4;  // in descriptor units
     auto issue_s = [&](int x, int w) {
-      mma_abt<D>(tmem + x * 128, q_d + (SPLIT ? 0 : x * (C::Q_BYTES >> 4)), slots_k + (first_k + rk.slot) * kSlot, w,
-                 lead);
+      mma_abt<D>(tmem + x * 128, q_d + x * (q_bytes >> 4), slots_k + rk.slot * kSlot, w, lead, p.q_group >> 4);
       commit(bar(B::SFULL + x), lead);
-      commit(bar(B::EMPTY + first_k + rk.slot), lead);
+      commit(bar(B::EMPTY + rk.slot), lead);
     };
-    int w = tiles.width(a + tile_of(x0, 0));
-    if (ok && cnt > 0) {
-      ok = wait(bar(B::FULL + first_k + rk.slot), rk.phase);
+    int w = tiles.width(a);
+    if (ok && n > 0) {
+      ok = wait(bar(B::FULL + rk.slot), rk.phase);
       if (ok) {
         tc::fence_after();
-        for (int q = 0; q < nx; ++q) issue_s(x0 + q, w);
+        for (int x = 0; x < nh; ++x) issue_s(x, w);
       }
       next(rk);
     }
-    for (int it = 0; ok && it < cnt; ++it) {
-      const bool more = it + 1 < cnt;
-      const int w_next = more ? tiles.width(a + tile_of(x0, it + 1)) : 0;
+    for (int it = 0; ok && it < n; ++it) {
+      const bool more = it + 1 < n;
+      const int w_next = more ? tiles.width(a + it + 1) : 0;
       const uint32_t vs = slots_v + (first_v + rv.slot) * kSlot;
       if (!(ok = wait(bar(B::FULL + first_v + rv.slot), rv.phase))) break;
-      for (int x = x0; ok && x < x0 + nx; ++x) {
-        const uint32_t s_t = tmem + x * 128, o_t = tmem + 256 + x * 128;
+      for (int x = 0; ok && x < nh; ++x) {
+        const uint32_t s_t = tmem + x * 128, o_t = tmem + kO + x * 128;
         // the first 64 keys' product runs while the softmax forms the others
         if (!(ok = wait(bar(B::PFULL + 2 * x), it & 1))) break;
         tc::fence_after();
         mma_pv<D, 0, 4>(o_t, s_t, vs, w, it == 0, lead);
-        if (more && !(ok = wait(bar(B::FULL + first_k + rk.slot), rk.phase))) break;
+        if (more && !(ok = wait(bar(B::FULL + rk.slot), rk.phase))) break;
         if (!(ok = wait(bar(B::PFULL + 2 * x + 1), it & 1))) break;
         tc::fence_after();
         mma_pv<D, 4, 8>(o_t, s_t, vs, w, false, lead);
@@ -248,20 +265,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       next(rv);
       w = w_next;
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 * NH) {
     // ------------------------------------------------------------------ softmax of half x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
-    const int x = warp >> 2, row = tid & 127, cnt = count_of(x);
-    const int tl = row / p.R, hd = row % p.R, t = t0 + (SPLIT ? 0 : x * p.tpc) + tl;
+    const int x = warp >> 2, row = tid & 127, cnt = x < nh ? n : 0;
+    const int tl = row / p.R, hd = row % p.R, t = t0 + x * p.tpc + tl;
     const bool valid = tl < p.tpc && t < Lq;
     const int pos = valid ? off + t : -1;
     const bool work = __any_sync(0xffffffffu, pos >= 0);  // warps without rows only keep the barriers moving
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_t = tmem + x * 128 + lane_base, o_t = tmem + 256 + x * 128 + lane_base;
+    const uint32_t s_t = tmem + x * 128 + lane_base, o_t = tmem + kO + x * 128 + lane_base;
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int it = 0; it < cnt; ++it) {
-      const int j = tile_of(x, it), key0 = tiles.key0(a + j), w = tiles.width(a + j);
+      const int key0 = tiles.key0(a + it), w = tiles.width(a + it);
       if (!(ok = wait(bar(B::SFULL + x), it & 1))) break;
       tc::fence_after();
       if (work) {
@@ -271,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // seen columns: [j_lo, j_hi) and, of those before j_lo, the sinks [0, j_sink)
         const int j_hi = min(pos + 1 - key0, w);
         const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = p.n_sink - key0;
-        const uint32_t bad = PAGED ? s_bad[SPLIT ? x : 0][it & 7] : 0u;
+        const uint32_t bad = PAGED ? s_bad[it & 7] : 0u;
         const bool all =
             __all_sync(0xffffffffu, j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0);
         // columns c .. c + 31 that are not seen get -inf
@@ -363,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w > 64) exps(64, 0);
         tmem_wait_st();
         tc::fence_before();
-        tc::mbar_arrive(bar(B::PFULL + 2 * x));  // P of the first 64 keys
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::PFULL + 2 * x));  // P of the first 64 keys
         if (w > 64) {
           tmem_st16_nowait(s_t + 32, pk);
           if (w > 96) {
@@ -374,28 +392,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float2 la = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
         l += la.x + la.y;
-      } else {
-        tc::fence_before();
+      } else if (lane == 0) {
         tc::mbar_arrive(bar(B::PFULL + 2 * x));
       }
       tc::fence_before();
-      tc::mbar_arrive(bar(B::PFULL + 2 * x + 1));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B::PFULL + 2 * x + 1));
     }
     if (ok && cnt > 0) {
       ok = wait(bar(B::ODONE + x), 0);
       tc::fence_after();
     }
-    if (ok && (SPLIT || x == 0 || two)) {
+    if (ok && x < nh) {
       const int64_t rr = (start + t) * p.h + g * p.R + hd;
-      if (SPLIT || p.part_o) {
-        const int64_t at = (int64_t)(SPLIT ? split * 2 + x : split) * p.seqs.tokens * p.h + rr;
+      if (!whole) {
+        const int64_t at = (part_unit * p.n_splits + split) * p.cta_rows + x * p.tpc * p.R + row;
         if (valid) p.part_ml[at] = make_float2(m, l);
         if (__any_sync(0xffffffffu, l > 0.f)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float ov[32];
             tc::tmem_ld32(o_t + c, ov);
-            if (l > 0.f) {
+            if (valid && l > 0.f) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(p.part_o + at * D + c + e) =
@@ -431,27 +449,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort) {
     // copies and products still in flight land before the CTA leaves
-    if (warp == 8 || warp == 11) {
-      if (warp == 8 && n > 0) tc::warp_drain(bar(B::Q), 0);
-      const int ns = warp == 8 ? N0 : N1, first = warp == 8 ? 0 : N0;
+    if (warp == kLoad0 || warp == kLoad1) {
+      if (warp == kLoad0 && n > 0) tc::warp_drain(bar(B::Q), 0);
+      const int ns = warp == kLoad0 ? N0 : N1, first = warp == kLoad0 ? 0 : N0;
       for (int st = 0; st < ns; ++st)
         if (const int i = last_in_stage(last_item, st, ns); i >= 0)
           tc::warp_drain(bar(B::FULL + first + st), (i / ns) & 1);
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == kIssue) {
       if (lane == 0) tc::commit(bar(B::DRAIN));
       __syncwarp();
       tc::warp_drain(bar(B::DRAIN), 0);
     }
-  } else if (warp == 8 || warp == 11) {
+  } else if (warp == kLoad0 || warp == kLoad1) {
     // the last release of every slot lands before the CTA leaves
-    const int ns = warp == 8 ? N0 : N1, first = warp == 8 ? 0 : N0;
+    const int ns = warp == kLoad0 ? N0 : N1, first = warp == kLoad0 ? 0 : N0;
     for (int st = 0; st < ns; ++st)
       if (const int i = last_in_stage(last_item, st, ns); i >= 0)
         tc::warp_drain(bar(B::EMPTY + first + st), (i / ns) & 1);
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 9) tmem_free(tmem, kTmemCols);
+  if (warp == kIssue) tmem_free(tmem, C::TMEM);
 }
 
 // Joins the parts of a row in order: PW warps a (token, head) row, each every PW-th part
@@ -459,29 +477,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 // another), then a sum over the warps.  Reads every part once (a part without keys is
 // skipped), writes bf16 o and the lse.
 template <int D, int PW>
-__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int parts) {
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int64_t rows) {
   constexpr int E = D / 32;
   __shared__ float s_acc[8][D + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pw = warp % PW;
-  const int64_t rows = p.seqs.tokens * p.h;
-  const int64_t rr = (int64_t)blockIdx.x * (8 / PW) + warp / PW;
-  bool mine = rr < rows;
-  if (mine) {
-    const int64_t tok = rr / p.h;
-    const int seq = seq_of_token(p.seqs, tok);
-    const int64_t i = tok - seq_start(p.seqs, seq);
-    mine = i >= 0 && i < seq_len(p.seqs, seq);  // (a row of no sequence is left alone)
-  }
+  const int64_t row = (int64_t)blockIdx.x * (8 / PW) + warp / PW;  // of the divided units
+  const int parts = p.n_splits, R = p.R;
+  const Unit un(p, p.n_whole + row / p.cta_rows, p.cta_rows / R);
+  const int t = un.t0 + (int)(row % p.cta_rows) / R;
+  const bool mine = row < rows && un.t0 >= 0 && t < un.Lq;
+  const int64_t rr = (un.start + t) * p.h + un.g * R + (int)(row % p.cta_rows) % R;
+  const int64_t at = row / p.cta_rows * parts * p.cta_rows + row % p.cta_rows;  // of part 0
   float m = kNegInf, acc[E] = {}, l = 0.f;
   if (mine) {
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[i * rows + rr].x);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[at + (int64_t)i * p.cta_rows].x);
 #pragma unroll
     for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     if (m > kNegInf) {
       for (int i0 = pw; i0 < parts; i0 += 32 * PW) {
         float wl = 0.f, w = 0.f;
         if (i0 + lane * PW < parts) {
-          const float2 ml = p.part_ml[(int64_t)(i0 + lane * PW) * rows + rr];
+          const float2 ml = p.part_ml[at + (int64_t)(i0 + lane * PW) * p.cta_rows];
           if (ml.y > 0.f) {
             w = ex2(ml.x - m);
             wl = w * ml.y;
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int pa
           const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, wl, i);
           l += li;
           if (li > 0.f) {  // (an underflowed weight would only add zeros)
-            const float* src = p.part_o + ((int64_t)(i0 + i * PW) * rows + rr) * D + lane * E;
+            const float* src = p.part_o + (at + (int64_t)(i0 + i * PW) * p.cta_rows) * D + lane * E;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
               const float2 v = *reinterpret_cast<const float2*>(src + e);
@@ -526,49 +542,70 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int pa
   if (p.lse && lane == 0) p.lse[rr] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
 }
 
-// How a call is cut.  Key tiles are bounded by the longest cache and the window.
+// How a call is cut.  The number of key tiles follows from the longest cache and the window.
 struct Plan {
-  bool split;    // one row tile a CTA, halves alternate key tiles
-  int tpc, row_ctas, n_splits, parts;
-  size_t ml, bytes;  // workspace: part_o at 0, part_ml at `ml`
+  bool few;
+  int tpc, cta_rows, n_splits;
+  int64_t units, whole;  // units 0 .. whole - 1 take one CTA, the others n_splits
+  size_t ml, bytes;      // workspace: part_o at 0, part_ml at `ml`
 };
 Plan make_plan(const Seqs& s, int h, int hkv, int D, int max_keys, int window, int n_sink) {
   Plan pl{};
   const int R = h / hkv;
   pl.tpc = std::max(1, std::min(ROWS / R, s.max_len));
-  // Few rows: every sequence's queries fit one row tile, so a second row tile would idle.
-  pl.split = s.max_len <= pl.tpc;
-  const int rows_tok = pl.split ? pl.tpc : 2 * pl.tpc;
-  pl.row_ctas = (s.max_len + rows_tok - 1) / rows_tok;
+  pl.few = (int64_t)s.max_len * R <= kFewRows;
+  const int rows_tok = pl.few ? pl.tpc : 2 * pl.tpc;
+  pl.cta_rows = rows_tok * R;
+  pl.units = ((int64_t)s.max_len + rows_tok - 1) / rows_tok * s.n_seqs * hkv;
   int64_t keys = max_keys;
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + rows_tok + up16(n_sink) + 2 * GRAN);
   const int64_t tiles = std::max<int64_t>(1, (keys + KT - 1) / KT);
-  const int64_t ctas = std::max<int64_t>(1, (int64_t)pl.row_ctas * s.n_seqs * hkv);
-  // Enough CTAs for about four rounds of the 152 SMs (ragged caches then even out), but no
-  // part below two key tiles (a tile for each half).
-  int64_t want = pl.split ? (4 * 152 + ctas - 1) / ctas : (152 + ctas - 1) / ctas;
-  want = std::max<int64_t>(1, std::min<int64_t>(want, (tiles + 1) / 2));
-  pl.n_splits = (int)std::min<int64_t>(want, std::min(256, 65535 / hkv));
-  pl.parts = pl.split ? 2 * pl.n_splits : pl.n_splits;
-  if (pl.parts > 1) {
-    const size_t rows = (size_t)s.tokens * h;
-    pl.ml = (pl.parts * rows * D * 4 + 255) & ~size_t(255);
-    pl.bytes = pl.ml + pl.parts * rows * 8;
+  if (pl.few) {
+    // About four rounds of CTAs (two an SM), so that ragged caches even out.
+    const int64_t want = (4 * 2 * kSms + pl.units - 1) / pl.units;
+    pl.n_splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles, 256}));
+    pl.whole = pl.n_splits == 1 ? pl.units : 0;
+  } else {
+    // Whole rounds of the SMs as they are; the units of the last, partial round are divided
+    // where that shortens it.  In the time of a key tile (1.6 us at d = 128): a CTA takes its
+    // tiles and about 5 more to start and end, each part about 3 to pass through memory.  The
+    // chunk of 2048 tokens x 64 heads at 32768 keys (512 units, 56 of them in the last round)
+    // takes 1463 us with those in 5 parts, 1507 in 8 and 1684 undivided; 224 units of 10
+    // tiles 30 us undivided and 43 us with the last 72 halved.
+    const int64_t rest = pl.units % kSms;
+    double best = 1e30;
+    pl.n_splits = 1;
+    for (int sp = 1; rest > 0 && sp <= 16 && (sp == 1 || 2 * sp <= tiles); ++sp) {
+      const double cost = (double)((rest * sp + kSms - 1) / kSms) * ((double)tiles / sp + 5.0) + (sp > 1 ? 3.0 * sp : 0.0);
+      if (cost < best) {
+        best = cost;
+        pl.n_splits = sp;
+      }
+    }
+    pl.whole = pl.n_splits == 1 ? pl.units : pl.units - rest;
   }
+  const size_t rows = (size_t)(pl.units - pl.whole) * pl.n_splits * pl.cta_rows;
+  pl.ml = (rows * D * 4 + 255) & ~size_t(255);
+  pl.bytes = rows ? pl.ml + rows * 8 : 0;
   return pl;
 }
 
-template <int D, bool PAGED, bool SPLIT>
-cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, dim3 grid, cudaStream_t st) {
-  auto kern = attn_kernel<D, PAGED, SPLIT>;
-  constexpr int smem = Cfg<D, SPLIT>::SMEM;
+template <int D, bool PAGED, bool FEW>
+cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, int64_t ctas, cudaStream_t st) {
+  using C = Cfg<D, FEW>;
+  auto kern = attn_kernel<D, PAGED, FEW>;
+  const int smem = C::NH * (D / 64) * p.q_group + (C::N0 + C::N1) * C::KV_BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // the softmax warps' share must come out of what the block is launched with
-  cudaFuncAttributes at;
-  if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-  if (at.numRegs < kMinRegs) return cudaErrorInvalidConfiguration;
-  kern<<<grid, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
+  static int regs = 0;
+  if (regs == 0) {
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+    regs = at.numRegs;
+  }
+  if (regs < C::MIN_REGS) return cudaErrorInvalidConfiguration;
+  kern<<<(unsigned)ctas, C::THREADS, smem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
   return cudaGetLastError();
 }
 
@@ -581,31 +618,33 @@ cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int 
   p.keys = keys;
   p.o = (__nv_bfloat16*)o;
   p.lse = lse;
-  if (pl.parts > 1) {
-    p.part_o = (float*)workspace;
-    p.part_ml = (float2*)((uint8_t*)workspace + pl.ml);
-  }
+  p.part_o = (float*)workspace;
+  p.part_ml = (float2*)((uint8_t*)workspace + pl.ml);
   p.h = h;
   p.hkv = hkv;
   p.R = h / hkv;
   p.tpc = pl.tpc;
   p.window = window;
   p.n_sink = n_sink;
+  p.n_whole = (int)pl.whole;
   p.n_splits = pl.n_splits;
+  p.cta_rows = pl.cta_rows;
+  p.q_group = pl.few ? up16(pl.cta_rows) * 128 : ROWS * 128;
   p.scale_log2 = scale * kLog2e;
   CUtensorMap m[5];
   if (!query_map(&m[0], q, s.tokens, h, D, p.R, p.tpc) || !key_maps(&m[1], &m[2], keys.k, keys, hkv, D, s.tokens) ||
       !key_maps(&m[3], &m[4], keys.v, keys, hkv, D, s.tokens))
     return cudaErrorInvalidValue;
-  const dim3 grid(pl.row_ctas, s.n_seqs, hkv * pl.n_splits);
-  cudaError_t e = keys.table ? (pl.split ? run_attn<D, true, true>(m, p, grid, st) : run_attn<D, true, false>(m, p, grid, st))
-                             : (pl.split ? run_attn<D, false, true>(m, p, grid, st) : run_attn<D, false, false>(m, p, grid, st));
-  if (e != cudaSuccess || pl.parts == 1) return e;
-  const int64_t rows = s.tokens * h;
-  if (pl.parts >= 8)
-    combine_kernel<D, 8><<<(unsigned)rows, 256, 0, st>>>(p, pl.parts);
+  const int64_t ctas = pl.whole + (pl.units - pl.whole) * pl.n_splits;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaError_t e = keys.table ? (pl.few ? run_attn<D, true, true>(m, p, ctas, st) : run_attn<D, true, false>(m, p, ctas, st))
+                             : (pl.few ? run_attn<D, false, true>(m, p, ctas, st) : run_attn<D, false, false>(m, p, ctas, st));
+  if (e != cudaSuccess || pl.bytes == 0) return e;
+  const int64_t rows = (pl.units - pl.whole) * pl.cta_rows;
+  if (pl.n_splits >= 8)
+    combine_kernel<D, 8><<<(unsigned)rows, 256, 0, st>>>(p, rows);
   else
-    combine_kernel<D, 1><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl.parts);
+    combine_kernel<D, 1><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, rows);
   return cudaGetLastError();
 }
 
