@@ -5,9 +5,10 @@
 // A query at position p sees key j when j <= p and (window == 0, or j > p - window, or
 // j < n_sink).  The rows of one CTA are consecutive positions p_first .. p_last, so the
 // keys any of them sees are at most two spans: the sinks [0, n_sink) and
-// [p_first - window + 1, p_last].  Both are walked in 128-key tiles whose last one is cut
-// to a multiple of 16 keys (the granularity of the tensor-core N and K extents), so a few
-// sinks cost a 16-key tile and not a 128-key one.
+// [p_first - window + 1, p_last].  The spans, one after the other (each starting on a
+// multiple of 16 keys), are walked in 128-key tiles whose last one is cut to a multiple of
+// 16 (the granularity of the tensor-core N and K extents), so a few sinks cost 16 columns of
+// a tile and not a tile.
 #pragma once
 
 #include "launch.h"
@@ -61,46 +62,54 @@ inline Keys keys_of(const PagedView* c, const void* k, const void* v) {
 
 __host__ __device__ __forceinline__ int up16(int x) { return (x + GRAN - 1) & ~(GRAN - 1); }
 
-// The key tiles that rows at positions p_first .. p_last see (at least in part).
+// The key tiles that rows at positions p_first .. p_last see (at least in part).  Column c of
+// tile i is place 128 i + c of the two spans: key `place` below sink_end, place + shift from
+// there on.
 struct Tiles {
-  int sink_end, lo, hi, n_sink_tiles, n;
+  int sink_end, shift, total, n;
   __device__ __forceinline__ Tiles(int p_first, int p_last, int window, int n_sink) {
-    hi = p_last + 1;
-    lo = window > 0 ? max(0, p_first - window + 1) & ~(GRAN - 1) : 0;
+    const int hi = p_last + 1;
+    int lo = window > 0 ? max(0, p_first - window + 1) & ~(GRAN - 1) : 0;
     sink_end = up16(n_sink);
-    if (window == 0 || lo <= sink_end) lo = sink_end = 0;  // one span
-    n_sink_tiles = (sink_end + KT - 1) / KT;
-    n = hi > lo ? n_sink_tiles + (hi - lo + KT - 1) / KT : 0;
+    if (window == 0 || n_sink == 0) sink_end = 0;
+    if (lo <= sink_end && sink_end > 0) lo = sink_end = 0;  // the spans meet: one span
+    shift = lo - sink_end;
+    total = hi > lo ? sink_end + hi - lo : 0;
+    n = (total + KT - 1) / KT;
   }
-  __device__ __forceinline__ int key0(int i) const {
-    return i < n_sink_tiles ? i * KT : lo + (i - n_sink_tiles) * KT;
-  }
-  // keys of tile i, rounded up to 16 (rows past the sequence's keys are masked and zero)
-  __device__ __forceinline__ int width(int i) const {
-    return min(KT, up16((i < n_sink_tiles ? sink_end : hi) - key0(i)));
+  __device__ __forceinline__ int width(int i) const { return min(KT, up16(total - i * KT)); }
+  // key of column 0 of tile i, counted in the last span
+  __device__ __forceinline__ int key0(int i) const { return i * KT + shift; }
+  // columns of tile i before this one are sinks
+  __device__ __forceinline__ int sinks(int i, int n_sink) const {
+    return n_sink - i * KT - (sink_end > 0 ? 0 : shift);
   }
 };
 
-// One warp fills a tile of `w` (a multiple of 16) rows x D, keys key0 .. key0 + w - 1 of
-// kv-head g, in the 128-byte-swizzled layout (64-column groups KT * 128 bytes apart), and
-// lane 0 arrives on `bar` with the bytes still to come.  The rows travel as TMA boxes,
-// issued by as many lanes as there are boxes: whole pages (at most 128 rows) when the tile
-// is whole and starts on a page, else 16 rows.  What holds no key (rows at or past kv_len,
-// rows of a page the table does not name) is written as zeros by plain bounds-checked
-// copies, so whatever lies there (NaN included) never meets a product.
+// One warp fills a tile of `w` (a multiple of 16) rows x D of kv-head g, the keys at places
+// place0 .. place0 + w - 1 (Tiles: key `place` below sink_end, place + shift from there on),
+// in the 128-byte-swizzled layout (64-column groups KT * 128 bytes apart), and lane 0 arrives
+// on `bar` with the bytes still to come.  The rows travel as TMA boxes, issued by as many
+// lanes as there are boxes: whole pages (at most 128 rows) when the tile is whole and starts
+// on a page, else 16 rows.  What holds no key (rows at or past kv_len, rows of a page the
+// table does not name) is written as zeros by plain bounds-checked copies, so whatever lies
+// there (NaN included) never meets a product.
 template <int D, bool PAGED>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* big, const CUtensorMap* small,
-                                              const __nv_bfloat16* src, const Keys& c, int hkv, int g, int seq,
-                                              int64_t start, int key0, int w, int kv_len, uint32_t bar, int lane) {
+                                          const __nv_bfloat16* src, const Keys& c, int hkv, int g, int seq,
+                                          int64_t start, int place0, int sink_end, int shift, int w, int kv_len,
+                                          uint32_t bar, int lane) {
   constexpr int H = D / 64;
   const int page = PAGED ? 1 << c.page_log2 : KT;
   const int box = page < KT ? page : KT;
-  const bool whole = w == KT && key0 + KT <= kv_len && (!PAGED || (key0 & (box - 1)) == 0);
+  const int first = place0 + shift;
+  const bool whole =
+      w == KT && place0 >= sink_end && first + KT <= kv_len && (!PAGED || (first & (box - 1)) == 0);
   const int br = whole ? box : GRAN;
   const int n = w / br;
   const int ci = lane / H, hf = lane % H;
   const bool mine = ci < n;
-  const int key = key0 + ci * br;
+  const int place = place0 + ci * br, key = place < sink_end ? place : place + shift;
   int pid = 0;
   if (PAGED) pid = mine && key < kv_len ? page_of(c, seq, key) : 0;
   const bool ok = pid >= 0;
@@ -122,9 +131,10 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* big, 
       const int cc = l / H;
       const bool okc = !((bad >> l) & 1u);
       const int64_t pidc = __shfl_sync(0xffffffffu, pid, l);
+      const int keyc = __shfl_sync(0xffffffffu, key, l);
       for (int e = lane; e < br * (D / 8); e += 32) {
         const int r = cc * br + e / (D / 8), ch = e % (D / 8);
-        const int kk = key0 + r;
+        const int kk = keyc + e / (D / 8);
         const bool in = okc && kk < kv_len;
         const int64_t row = PAGED ? pidc * c.page_stride + (int64_t)(kk & (page - 1)) * hkv * D
                                   : (start + kk) * hkv * D;
@@ -141,9 +151,9 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* big, 
 }
 
 // A bit for every 16-row group of a tile that the table names no page for (a warp's call).
-__device__ __forceinline__ uint32_t missing_groups(const Keys& c, int seq, int key0, int w, int kv_len, int lane) {
-  const int key = key0 + lane * GRAN;
-  return __ballot_sync(0xffffffffu, lane * GRAN < w && key < kv_len && page_of(c, seq, key) < 0);
+__device__ __forceinline__ uint32_t missing_groups(const Keys& c, int seq, const Tiles& t, int i, int kv_len, int lane) {
+  const int place = i * KT + lane * GRAN, key = place < t.sink_end ? place : place + t.shift;
+  return __ballot_sync(0xffffffffu, lane * GRAN < t.width(i) && key < kv_len && page_of(c, seq, key) < 0);
 }
 
 // ------------------------------------------------------------------ products

@@ -191,18 +191,17 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
     for (int i = 0; i < cnt; ++i) {
       const int j = FEW ? i >> 1 : i;
       const bool is_v = FEW ? (i & 1) : y == 1;
-      const int key0 = tiles.key0(a + j), w = tiles.width(a + j);
       if (i >= ns && !wait(bar(B::EMPTY + first + slot), phase)) break;
       // the flags of a tile are read by its softmax after S, so they are in place before the
       // K tile's arrival; the missing pages of K and V are the same
       if (PAGED && !is_v) {
-        const uint32_t bad = missing_groups(p.keys, seq, key0, w, kv_len, lane);
+        const uint32_t bad = missing_groups(p.keys, seq, tiles, a + j, kv_len, lane);
         if (lane == 0) s_bad[j & 7] = bad;
         __syncwarp();
       }
       load_tile<D, PAGED>(slots + (first + slot) * C::KV_BYTES, is_v ? &tm_v : &tm_k, is_v ? &tm_v16 : &tm_k16,
-                          is_v ? p.keys.v : p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, kv_len,
-                          bar(B::FULL + first + slot), lane);
+                          is_v ? p.keys.v : p.keys.k, p.keys, p.hkv, g, seq, start, (a + j) * KT,
+                          tiles.sink_end, tiles.shift, tiles.width(a + j), kv_len, bar(B::FULL + first + slot), lane);
       last_item = i;
       if (++slot == ns) {
         slot = 0;
@@ -285,9 +284,9 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
         float sv[KT];
         tc::tmem_ld32_nowait(s_t, sv);
         if (w > 32) tc::tmem_ld32_nowait(s_t + 32, sv + 32);
-        // seen columns: [j_lo, j_hi) and, of those before j_lo, the sinks [0, j_sink)
+        // seen columns: [j_lo, j_hi) and the sinks [0, j_sink) before j_hi
         const int j_hi = min(pos + 1 - key0, w);
-        const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = p.n_sink - key0;
+        const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = tiles.sinks(a + it, p.n_sink);
         const uint32_t bad = PAGED ? s_bad[it & 7] : 0u;
         const bool all =
             __all_sync(0xffffffffu, j_hi == KT && (j_lo <= 0 || j_sink >= KT) && bad == 0);

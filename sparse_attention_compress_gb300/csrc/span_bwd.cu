@@ -43,21 +43,30 @@ struct BwdParams {
 
 __device__ __forceinline__ int last_in(int last, int st, int ns) { return last < st ? -1 : last - (last - st) % ns; }
 
-template <int D>
-__device__ __forceinline__ void mma_abt1(uint32_t d_tmem, uint32_t a, uint32_t b, int w) {
-  mma_abt<D>(d_tmem, desc_k(a), desc_k(b), w, 1u);
-}
-
 // (+)= A[128 x w] (bf16 in TMEM: columns 0..31 hold the first 64, 64..95 the others)
 // B[w x D], a tile of w rows read MN-major.
+// b: desc_mn of the tile.
 template <int D>
-__device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int w, bool first) {
+__device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int w, bool first,
+                                            uint32_t lead) {
   constexpr uint32_t id = tc::idesc(ROWS, D) | kBMn;
+  auto step = [&](int s) {
+    mma_ts(d_tmem, a_tmem + (s < 4 ? s * 8 : 64 + (s - 4) * 8), b + s * (2048 >> 4), id, s == 0 ? !first : 1u, lead);
+  };
+  if (w == KT) {
 #pragma unroll
-  for (int s = 0; s < KT / 16; ++s)
-    if (s * 16 < w)
-      mma_ts(d_tmem, a_tmem + (s < 4 ? s * 8 : 64 + (s - 4) * 8), desc_mn(b) + s * (2048 >> 4), id,
-             (first && s == 0) ? 0u : 1u, 1u);
+    for (int s = 0; s < KT / 16; ++s) step(s);
+  } else {
+#pragma unroll
+    for (int s = 0; s < KT / 16; ++s)
+      if (s * 16 < w) step(s);
+  }
+}
+
+// Two bf16 products p (dp - D) of pairs: nd is minus D, twice.
+__device__ __forceinline__ uint32_t ds_pair(uint64_t p, uint64_t dp, uint64_t nd) {
+  const float2 d = unpair(mul2(p, add2(dp, nd)));
+  return pack_bf16(d.x, d.y);
 }
 
 // ---------------------------------------------------------------------------- dQ
@@ -103,6 +112,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   volatile int* abort = &s_abort;
 
   if (tc::device_status_set()) return;
+  const Waits wait(abort);
   const int seq = blockIdx.y, g = blockIdx.z;
   const int64_t start = seq_start(p.seqs, seq);
   const int L = seq_len(p.seqs, seq);
@@ -123,11 +133,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(SFULL + i), 1);
-      tc::mbar_init(bar(DSFULL + i), 256);
+      tc::mbar_init(bar(DSFULL + i), 8);  // one arrival a softmax warp
       tc::mbar_init(bar(DQDONE + i), 1);
     }
     tc::mbar_init(bar(PFULL), 1);
-    tc::mbar_init(bar(PFREE), 256);
+    tc::mbar_init(bar(PFREE), 8);
     tc::mbar_init(bar(DRAIN), 3);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -152,59 +162,53 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     }
     __syncwarp();
     for (int j = 0; j < n; ++j) {
-      const int key0 = tiles.key0(j), w = tiles.width(j), sk = j % kNK, sv = j % kNV;
-      if (j >= kNK && !tc::warp_wait(bar(KEMPTY + sk), ((j / kNK) - 1) & 1, abort)) break;
-      load_tile<D, false>(k_s + sk * TB, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, L,
-                          bar(KFULL + sk), lane);
+      const int w = tiles.width(j), sk = j % kNK, sv = j % kNV;
+      if (j >= kNK && !wait(bar(KEMPTY + sk), ((j / kNK) - 1) & 1)) break;
+      load_tile<D, false>(k_s + sk * TB, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, j * KT, tiles.sink_end,
+                          tiles.shift, w, L, bar(KFULL + sk), lane);
       last_k = j;
-      if (j >= kNV && !tc::warp_wait(bar(VEMPTY + sv), ((j / kNV) - 1) & 1, abort)) break;
-      load_tile<D, false>(v_s + sv * TB, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w, L,
-                          bar(VFULL + sv), lane);
+      if (j >= kNV && !wait(bar(VEMPTY + sv), ((j / kNV) - 1) & 1)) break;
+      load_tile<D, false>(v_s + sv * TB, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, j * KT, tiles.sink_end,
+                          tiles.shift, w, L, bar(VFULL + sv), lane);
       last_v = j;
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ S
-    bool ok = tc::warp_wait(bar(Q), 0, abort);
+    const uint32_t lead = elect();
+    bool ok = wait(bar(Q), 0);
     for (int j = 0; ok && j < n; ++j) {
       const int b = j & 1, sk = j % kNK;
-      if (j >= 2 && !(ok = tc::warp_wait(bar(DQDONE + b), ((j >> 1) - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(KFULL + sk), (j / kNK) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_abt1<D>(tmem + b * 128, q_s, k_s + sk * TB, tiles.width(j));
-        tc::commit(bar(SFULL + b));
-      }
-      __syncwarp();
+      if (j >= 2 && !(ok = wait(bar(DQDONE + b), ((j >> 1) - 1) & 1))) break;
+      if (!(ok = wait(bar(KFULL + sk), (j / kNK) & 1))) break;
+      tc::fence_after();
+      mma_abt<D>(tmem + b * 128, desc_k(q_s), desc_k(k_s) + sk * (TB >> 4), tiles.width(j), lead);
+      commit(bar(SFULL + b), lead);
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------------ dP
-    bool ok = tc::warp_wait(bar(Q), 0, abort);
+    const uint32_t lead = elect();
+    bool ok = wait(bar(Q), 0);
     for (int j = 0; ok && j < n; ++j) {
       const int sv = j % kNV;
-      if (j >= 1 && !(ok = tc::warp_wait(bar(PFREE), (j - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(VFULL + sv), (j / kNV) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_abt1<D>(tmem + 256, do_s, v_s + sv * TB, tiles.width(j));
-        tc::commit(bar(PFULL));
-        tc::commit(bar(VEMPTY + sv));
-      }
-      __syncwarp();
+      if (j >= 1 && !(ok = wait(bar(PFREE), (j - 1) & 1))) break;
+      if (!(ok = wait(bar(VFULL + sv), (j / kNV) & 1))) break;
+      tc::fence_after();
+      mma_abt<D>(tmem + 256, desc_k(do_s), desc_k(v_s) + sv * (TB >> 4), tiles.width(j), lead);
+      commit(bar(PFULL), lead);
+      commit(bar(VEMPTY + sv), lead);
     }
   } else if (warp == 11) {
     // ------------------------------------------------------------------ dQ += dS K
+    const uint32_t lead = elect();
     bool ok = true;
     for (int j = 0; ok && j < n; ++j) {
       const int b = j & 1, sk = j % kNK;
       // (dS of this tile was formed from S, so its K tile is in place)
-      if (!(ok = tc::warp_wait(bar(DSFULL + b), (j >> 1) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_split_a<D>(tmem + 384, tmem + b * 128, k_s + sk * TB, tiles.width(j), j == 0);
-        tc::commit(bar(DQDONE + b));
-        tc::commit(bar(KEMPTY + sk));
-      }
-      __syncwarp();
+      if (!(ok = wait(bar(DSFULL + b), (j >> 1) & 1))) break;
+      tc::fence_after();
+      mma_split_a<D>(tmem + 384, tmem + b * 128, desc_mn(k_s) + sk * (TB >> 4), tiles.width(j), j == 0, lead);
+      commit(bar(DQDONE + b), lead);
+      commit(bar(KEMPTY + sk), lead);
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -237,10 +241,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         p.dsum[rr] = dsum;
       }
     }
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nl2 = pair(-l2, -l2), nd2 = pair(-dsum, -dsum);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
-      if (!(ok = tc::warp_wait(bar(SFULL + b), (j >> 1) & 1, abort))) break;
+      if (!(ok = wait(bar(SFULL + b), (j >> 1) & 1))) break;
       tc::fence_after();
       const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
       const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)
@@ -248,42 +253,51 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
         if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
-      const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = p.n_sink - key0;
+      const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
       const bool all = j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64);
-      tc::tmem_wait_ld();
+      tmem_wait_ld(sv);
+      tmem_wait_ld(sv + 32);
       if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const int cc = c0 + c;
-          sv[c] = cc < j_hi && (cc >= j_lo || cc < j_sink) ? sv[c] : kNegInf;
+        for (int c = 0; c < 64; c += 32) {
+          const uint32_t see = bits(j_lo - c0 - c, j_hi - c0 - c) | bits(0, min(j_sink, j_hi) - c0 - c);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
         }
       }
 #pragma unroll
-      for (int c = 0; c < 64; ++c) sv[c] = ex2(fmaf(sv[c], p.scale_log2, -l2));
-      if (!(ok = tc::warp_wait(bar(PFULL), j & 1, abort))) break;
+      for (int c = 0; c < 64; c += 2) {
+        const float2 y = unpair(fma2(pair(sv[c], sv[c + 1]), scale2, nl2));
+        sv[c] = ex2(y.x);
+        sv[c + 1] = ex2(y.y);
+      }
+      if (!(ok = wait(bar(PFULL), j & 1))) break;
       tc::fence_after();
+      float dp[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32)
+        if (c < nc) tc::tmem_ld32_nowait(p_t + c, dp + c);
+      tmem_wait_ld(dp);
+      tmem_wait_ld(dp + 32);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(PFREE));
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         if (c >= nc) break;
-        float dp[32];
-        tc::tmem_ld32(p_t + c, dp);
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          // (an unseen key has p = 0, and contributes nothing whatever its dp)
-          const float d0 = sv[c + e] > 0.f ? sv[c + e] * (dp[e] - dsum) : 0.f;
-          const float d1 = sv[c + e + 1] > 0.f ? sv[c + e + 1] * (dp[e + 1] - dsum) : 0.f;
-          pk[e / 2] = pack_bf16(d0, d1);
-        }
+        for (int e = 0; e < 32; e += 2)  // (an unseen key has p = 0)
+          pk[e / 2] = ds_pair(pair(sv[c + e], sv[c + e + 1]), pair(dp[c + e], dp[c + e + 1]), nd2);
         tmem_st16_nowait(s_t + c / 2, pk);
       }
       tmem_wait_st();
       tc::fence_before();
-      tc::mbar_arrive(bar(PFREE));
-      tc::mbar_arrive(bar(DSFULL + b));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(DSFULL + b));
     }
     if (ok) {
-      ok = tc::warp_wait(bar(DQDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort);
+      ok = wait(bar(DQDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
       tc::fence_after();
     }
     if (ok) {
@@ -335,7 +349,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 // Warps 0-7 softmax, 8 loads, 9 issues S^T and dV, 10 dP^T and dK.  TMEM: S^T (then P^T) at
 // 0, dP^T (then dS^T) at 128, dV at 256, dK at 384.  The two issuers' chains interleave on
 // the tensor pipe: while P^T is formed dK of the tile before and dP^T run, while dS^T is
-// formed dV and the next S^T do.
+// formed dV and the next S^T do.  (S^T of a tile overwrites P^T of the one before, and dP^T
+// its dS^T: the same lane issued the products that read them, and products execute in
+// issue order.)
 constexpr int kDkvThreads = 352;
 
 template <int D>
@@ -357,17 +373,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     DEMPTY = 8,  // [2]
     SFULL = 10,
     PFULL = 11,   // P^T written
-    DVDONE = 12,
+    DVDONE = 12,  // every dV product is done
     DPFULL = 13,
     DSFULL = 14,  // dS^T written
-    DKDONE = 15,
+    DKDONE = 15,  // every dK product is done
     DRAIN = 16,
     COUNT
   };
   constexpr int TB = KT * D * 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ __align__(16) float s_l2[2][ROWS], s_d[2][ROWS];
+  __shared__ __align__(16) float s_l2[2][ROWS], s_d[2][ROWS];  // minus the rows' base-2 lse and D
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -377,6 +393,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   volatile int* abort = &s_abort;
 
   if (tc::device_status_set()) return;
+  const Waits wait(abort);
   // items of a (sequence, kv-head): the chunks of far queries of the sink tiles, then every
   // key tile with the queries within its window
   const int n_far_items = p.sink_tiles * p.n_far;
@@ -404,10 +421,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc::mbar_init(bar(DEMPTY + i), 2);  // dP^T and dV have read dO
     }
     tc::mbar_init(bar(SFULL), 1);
-    tc::mbar_init(bar(PFULL), 256);
+    tc::mbar_init(bar(PFULL), 8);  // one arrival a softmax warp
     tc::mbar_init(bar(DVDONE), 1);
     tc::mbar_init(bar(DPFULL), 1);
-    tc::mbar_init(bar(DSFULL), 256);
+    tc::mbar_init(bar(DSFULL), 8);
     tc::mbar_init(bar(DKDONE), 1);
     tc::mbar_init(bar(DRAIN), 2);
     s_abort = 0;
@@ -433,8 +450,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------------ loads
     const int w = min(KT, up16(L - key0));
-    load_tile<D, false>(k_s, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, L, bar(KV), lane);
-    load_tile<D, false>(v_s, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, w, L, bar(KV + 1), lane);
+    load_tile<D, false>(k_s, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, 0, 0, w, L, bar(KV),
+                        lane);
+    load_tile<D, false>(v_s, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, 0, 0, w, L,
+                        bar(KV + 1), lane);
     // Rows of tokens t .. t + tpc - 1 (those past the sequence as zeros: they are another
     // sequence's, or lie past the tensors).
     auto load_rows = [&](uint32_t to, const CUtensorMap* map, const __nv_bfloat16* src, int t, uint32_t full) {
@@ -459,7 +478,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     };
     for (int j = 0; j < n; ++j) {
       const int st = j & 1, t = t_lo + j * p.tpc;
-      if (j >= 2 && !tc::warp_wait(bar(QEMPTY + st), ((j >> 1) - 1) & 1, abort)) break;
+      if (j >= 2 && !wait(bar(QEMPTY + st), ((j >> 1) - 1) & 1)) break;
 #pragma unroll
       for (int e = lane; e < ROWS; e += 32) {
         float a = __builtin_inff(), b = 0.f;
@@ -468,61 +487,48 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           a = p.lse2[rr];
           b = p.dsum[rr];
         }
-        s_l2[st][e] = a;
-        s_d[st][e] = b;
+        s_l2[st][e] = -a;
+        s_d[st][e] = -b;
       }
       load_rows(q_s + st * TB, &tm_q, p.q, t, bar(QFULL + st));
       last_q = j;
-      if (j >= 2 && !tc::warp_wait(bar(DEMPTY + st), ((j >> 1) - 1) & 1, abort)) break;
+      if (j >= 2 && !wait(bar(DEMPTY + st), ((j >> 1) - 1) & 1)) break;
       load_rows(do_s + st * TB, &tm_do, p.dout, t, bar(DFULL + st));
       last_d = j;
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ S^T, dV += P^T dO
-    bool ok = tc::warp_wait(bar(KV), 0, abort);
+    const uint32_t lead = elect();
+    bool ok = wait(bar(KV), 0);
     for (int j = 0; ok && j < n; ++j) {
       const int st = j & 1;
-      // P^T of the tile before has been read
-      if (j > 0 && !(ok = tc::warp_wait(bar(DVDONE), (j - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_abt1<D>(tmem, k_s, q_s + st * TB, p.cols);
-        tc::commit(bar(SFULL));
-      }
-      __syncwarp();
-      if (!(ok = tc::warp_wait(bar(PFULL), j & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(DFULL + st), (j >> 1) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_split_a<D>(tmem + 256, tmem, do_s + st * TB, p.cols, j == 0);
-        tc::commit(bar(DVDONE));
-        tc::commit(bar(DEMPTY + st));
-      }
-      __syncwarp();
+      if (!(ok = wait(bar(QFULL + st), (j >> 1) & 1))) break;
+      tc::fence_after();
+      mma_abt<D>(tmem, desc_k(k_s), desc_k(q_s) + st * (TB >> 4), p.cols, lead);
+      commit(bar(SFULL), lead);
+      if (!(ok = wait(bar(PFULL), j & 1))) break;
+      if (!(ok = wait(bar(DFULL + st), (j >> 1) & 1))) break;
+      tc::fence_after();
+      mma_split_a<D>(tmem + 256, tmem, desc_mn(do_s) + st * (TB >> 4), p.cols, j == 0, lead);
+      commit(bar(DEMPTY + st), lead);
+      if (j == n - 1) commit(bar(DVDONE), lead);
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------------ dP^T, dK += dS^T Q
-    bool ok = tc::warp_wait(bar(KV + 1), 0, abort);
+    const uint32_t lead = elect();
+    bool ok = wait(bar(KV + 1), 0);
     for (int j = 0; ok && j < n; ++j) {
       const int st = j & 1;
-      if (j > 0 && !(ok = tc::warp_wait(bar(DKDONE), (j - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(DFULL + st), (j >> 1) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_abt1<D>(tmem + 128, v_s, do_s + st * TB, p.cols);
-        tc::commit(bar(DPFULL));
-        tc::commit(bar(DEMPTY + st));
-      }
-      __syncwarp();
-      if (!(ok = tc::warp_wait(bar(DSFULL), j & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_split_a<D>(tmem + 384, tmem + 128, q_s + st * TB, p.cols, j == 0);
-        tc::commit(bar(DKDONE));
-        tc::commit(bar(QEMPTY + st));  // (S^T of the tile was done before its dS^T)
-      }
-      __syncwarp();
+      if (!(ok = wait(bar(DFULL + st), (j >> 1) & 1))) break;
+      tc::fence_after();
+      mma_abt<D>(tmem + 128, desc_k(v_s), desc_k(do_s) + st * (TB >> 4), p.cols, lead);
+      commit(bar(DPFULL), lead);
+      commit(bar(DEMPTY + st), lead);
+      if (!(ok = wait(bar(DSFULL), j & 1))) break;
+      tc::fence_after();
+      mma_split_a<D>(tmem + 384, tmem + 128, desc_mn(q_s) + st * (TB >> 4), p.cols, j == 0, lead);
+      if (j == n - 1) commit(bar(DKDONE), lead);
+      commit(bar(QEMPTY + st), lead);  // (S^T of the tile was done before its dS^T)
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -531,6 +537,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + c0 + lane_base, p_t = tmem + 128 + c0 + lane_base;
     const int nc = min(64, p.cols - c0);
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int st = j & 1, t = t_lo + j * p.tpc;
@@ -542,63 +549,76 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
         c_hi = (int)max((int64_t)0, end) - c0;
       }
-      if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;  // lse and D
-      if (!(ok = tc::warp_wait(bar(SFULL), j & 1, abort))) break;
+      if (!(ok = wait(bar(QFULL + st), (j >> 1) & 1))) break;  // lse and D
+      if (!(ok = wait(bar(SFULL), j & 1))) break;
       tc::fence_after();
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
         if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
       const bool all = c_lo <= 0 && c_hi >= 64;
-      tc::tmem_wait_ld();
       const float4* l4 = reinterpret_cast<const float4*>(&s_l2[st][c0]);
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 l = l4[c / 4];
-        sv[c] = ex2(fmaf(sv[c], p.scale_log2, -l.x));
-        sv[c + 1] = ex2(fmaf(sv[c + 1], p.scale_log2, -l.y));
-        sv[c + 2] = ex2(fmaf(sv[c + 2], p.scale_log2, -l.z));
-        sv[c + 3] = ex2(fmaf(sv[c + 3], p.scale_log2, -l.w));
-      }
+      tmem_wait_ld(sv);
+      tmem_wait_ld(sv + 32);
       if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) sv[c] = c >= c_lo && c < c_hi ? sv[c] : 0.f;
+        for (int c = 0; c < 64; c += 32) {
+          const uint32_t see = bits(c_lo - c, c_hi - c);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+        }
       }
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
-        if (c >= nc) break;
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
-        tmem_st16_nowait(s_t + c / 2, pk);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = l4[(c + e) / 4];
+          const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, pair(l.x, l.y)));
+          const float2 z = unpair(fma2(pair(sv[c + e + 2], sv[c + e + 3]), scale2, pair(l.z, l.w)));
+          sv[c + e] = ex2(y.x);
+          sv[c + e + 1] = ex2(y.y);
+          sv[c + e + 2] = ex2(z.x);
+          sv[c + e + 3] = ex2(z.y);
+          pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
+          pk[e / 2 + 1] = pack_bf16(sv[c + e + 2], sv[c + e + 3]);
+        }
+        if (c < nc) tmem_st16_nowait(s_t + c / 2, pk);
       }
       tmem_wait_st();
       tc::fence_before();
-      tc::mbar_arrive(bar(PFULL));
-      if (!(ok = tc::warp_wait(bar(DPFULL), j & 1, abort))) break;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(PFULL));
+      if (!(ok = wait(bar(DPFULL), j & 1))) break;
       tc::fence_after();
       const float4* d4 = reinterpret_cast<const float4*>(&s_d[st][c0]);
+      float dp[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32)
+        if (c < nc) tc::tmem_ld32_nowait(p_t + c, dp + c);
+      tmem_wait_ld(dp);
+      tmem_wait_ld(dp + 32);
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         if (c >= nc) break;
-        float dp[32];
-        tc::tmem_ld32(p_t + c, dp);
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 d = d4[(c + e) / 4];
           // (zero rows past the sequence have dp = 0, so p = 0 gives ds = 0)
-          pk[e / 2] = pack_bf16(sv[c + e] * (dp[e] - d.x), sv[c + e + 1] * (dp[e + 1] - d.y));
-          pk[e / 2 + 1] = pack_bf16(sv[c + e + 2] * (dp[e + 2] - d.z), sv[c + e + 3] * (dp[e + 3] - d.w));
+          pk[e / 2] = ds_pair(pair(sv[c + e], sv[c + e + 1]), pair(dp[c + e], dp[c + e + 1]), pair(d.x, d.y));
+          pk[e / 2 + 1] =
+              ds_pair(pair(sv[c + e + 2], sv[c + e + 3]), pair(dp[c + e + 2], dp[c + e + 3]), pair(d.z, d.w));
         }
         tmem_st16_nowait(p_t + c / 2, pk);
       }
       tmem_wait_st();
       tc::fence_before();
-      tc::mbar_arrive(bar(DSFULL));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(DSFULL));
     }
     if (ok) {
-      ok = tc::warp_wait(bar(DVDONE), (n - 1) & 1, abort) && tc::warp_wait(bar(DKDONE), (n - 1) & 1, abort);
+      ok = wait(bar(DVDONE), 0) && wait(bar(DKDONE), 0);
       tc::fence_after();
     }
     if (ok) {

@@ -3,13 +3,15 @@
 // exp(scale q_i.k_j - lse_i), with the lse of the attention call on the same inputs, added
 // to decay times the weight so far.
 //
-// One CTA owns 128 keys and walks the query tiles that see them, so every key's sum stays
-// in one thread's fp32 registers: no atomics, the same result on every run, K read once.
-// The product is taken transposed, S^T = K Q^T (M = 128 keys, N = the tile's rows), so that
-// a TMEM lane is a key and the sum over queries needs no exchange between threads.  Roles:
-// warps 0-3 sum (one key a thread), warp 4 loads, warp 5 issues.  A decode step has few
-// columns: its Q stages and TMEM buffers are sized to them, so that up to five CTAs share
-// an SM and their loads overlap.
+// Every key's sum stays in one thread's fp32 registers: no atomics, the same result on every
+// run, K read once.  The product is taken transposed, S^T = K Q^T (M = 128 keys, N = the
+// tile's rows), so that a TMEM lane is a key and the sum over queries needs no exchange
+// between threads.  One operand of a CTA stays and the other streams through a ring:
+//   many rows   128 keys stay, the query tiles that see them stream: bound by the tensor
+//               cores and the exponentials, which two CTAs an SM overlap.
+//   FEW         (the queries of a sequence fit one tile) the queries stay and a run of key
+//               tiles streams: bound by HBM; two CTAs an SM.
+// Roles: warps 0-3 sum (one key a thread), warp 4 loads, warp 5 issues.
 #include <algorithm>
 
 #include "launch.h"
@@ -19,7 +21,6 @@ namespace nsa {
 namespace span {
 
 constexpr int kWThreads = 192;
-constexpr int kWStages = 2;
 
 struct WeightParams {
   Seqs seqs;
@@ -27,197 +28,261 @@ struct WeightParams {
   const float* lse;
   const float* w_in;  // optional
   float* w_out;
-  int h, hkv, R, tpc, cols, q_bytes, window, n_sink;  // cols: columns of a full query tile, up to a multiple of 16
+  int h, hkv, R, tpc, cols, window, n_sink;  // cols: columns of a full query tile, up to a multiple of 16
+  int q_group, n_splits;                     // bytes between Q's 64-column groups; FEW: CTAs of a (sequence, kv-head)
   uint32_t tmem_cols, buf_cols;
   float scale_log2, decay;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWThreads, 3)
+template <int D, bool FEW>
+struct WCfg {
+  static constexpr int K_BYTES = KT * D * 2;
+  static constexpr int NS = FEW ? (D == 64 ? 6 : 3) : 2;  // slots of the streamed operand
+};
+
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kWThreads, 2)
     weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_k16, const WeightParams p) {
-  enum : int { K = 0, QFULL = 1, QEMPTY = 3, SFULL = 5, SFREE = 7, DRAIN = 9, COUNT = 10 };
+  using C = WCfg<D, FEW>;
+  constexpr int NS = C::NS;
+  enum : int { FIXED = 0, FULL = 1, EMPTY = FULL + NS, SFULL = EMPTY + NS, SFREE = SFULL + 2, DRAIN = SFREE + 2, COUNT };
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ __align__(16) float s_lse[4][ROWS];  // by summing warp: the tile's base-2 lse
-  __shared__ uint32_t s_tmem, s_bad;
+  __shared__ __align__(16) float s_lse[FEW ? 1 : 4][ROWS];  // minus the base-2 lse of tile i's rows, at i % 4
+  __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t k_s = base, q_s = base + KT * D * 2;
+  const uint32_t q_bytes = (D / 64) * p.q_group, slot_bytes = FEW ? C::K_BYTES : q_bytes;
+  const uint32_t fixed_s = base, ring_s = fixed_s + (FEW ? q_bytes : C::K_BYTES);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
   if (tc::device_status_set()) return;
-  const int seq = blockIdx.y, g = blockIdx.z, key0 = (int)blockIdx.x * KT;
+  const Waits wait(abort);
+  const int seq = blockIdx.y, g = blockIdx.z;
   const int kv_len = cached_len(p.keys, seq);
-  if (key0 >= kv_len) return;
   const int64_t start = seq_start(p.seqs, seq);
   const int Lq = seq_len(p.seqs, seq);
   const int off = kv_len - Lq;
-  const int w = min(KT, up16(kv_len - key0));
-  // queries [t_lo, t_hi) see some key of the tile
-  const int t_lo = max(0, key0 - off);
-  const int t_hi = p.window > 0 && key0 >= p.n_sink ? min(Lq, key0 + KT - 1 + p.window - off) : Lq;
-  const int n = t_hi > t_lo ? (t_hi - t_lo + p.tpc - 1) / p.tpc : 0;
+  // this CTA's key tiles, and (many rows) the queries [t_lo, t_hi) that see some key of its one
+  const int n_kt = (kv_len + KT - 1) / KT;
+  const int kt0 = FEW ? (int)((int64_t)n_kt * blockIdx.x / p.n_splits) : (int)blockIdx.x;
+  const int kt1 = FEW ? (int)((int64_t)n_kt * (blockIdx.x + 1) / p.n_splits) : kt0 + 1;
+  if (kt0 >= min(kt1, n_kt)) return;
+  const int fkey0 = kt0 * KT;
+  const int t_lo = FEW ? 0 : max(0, fkey0 - off);
+  const int t_hi = !FEW && p.window > 0 && fkey0 >= p.n_sink ? min(Lq, fkey0 + KT - 1 + p.window - off) : Lq;
+  const int n_q = t_hi > t_lo ? (t_hi - t_lo + p.tpc - 1) / p.tpc : 0;
+  const int n = FEW ? kt1 - kt0 : n_q;  // streamed items
+  const bool any = n_q > 0;             // without queries nothing is loaded
 
   if (tid == 0) {
-    tc::mbar_init(bar(K), 1);
+    tc::mbar_init(bar(FIXED), 1);
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(bar(FULL + i), 1);
+      tc::mbar_init(bar(EMPTY + i), 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(bar(QFULL + i), 1);
-      tc::mbar_init(bar(QEMPTY + i), 1);
       tc::mbar_init(bar(SFULL + i), 1);
-      tc::mbar_init(bar(SFREE + i), 128);
+      tc::mbar_init(bar(SFREE + i), 4);  // one arrival a summing warp
     }
     tc::mbar_init(bar(DRAIN), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  // minus the base-2 lse of the rows of query tile t, for a warp's lanes (-inf for rows of no
+  // query, so that they add 0)
+  auto stage_lse = [&](float* to, int t, int from, int step) {
+    for (int e = from; e < ROWS; e += step) {
+      float le = kNegInf;
+      if (e < p.tpc * p.R && t + e / p.R < Lq) {
+        le = -p.lse[(start + t + e / p.R) * p.h + g * p.R + e % p.R] * kLog2e;
+        if (le == -kNegInf) le = kNegInf;  // a row without keys
+      }
+      to[e] = le;
+    }
+  };
   if (warp == 5) {
     tmem_alloc(smem_u32(&s_tmem), p.tmem_cols);
     tc::fence_before();
   }
-  if (warp == 4) {
-    const uint32_t bad = missing_groups(p.keys, seq, key0, w, kv_len, lane);
-    if (lane == 0) s_bad = bad;
-  }
+  if (FEW && warp < 4) stage_lse(s_lse[0], 0, tid, 128);
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
-  int last_q = -1;
+  int last_item = -1;
   if (warp == 4) {
     // ------------------------------------------------------------------ loads
-    if (n > 0)
-      load_tile<D, true>(k_s, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, w, kv_len, bar(K), lane);
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1;
-      if (j >= 2 && !tc::warp_wait(bar(QEMPTY + st), ((j >> 1) - 1) & 1, abort)) break;
+    auto load_q = [&](uint32_t to, int t, uint32_t full) {
       if (lane == 0) {
-        tc::mbar_expect_tx(bar(QFULL + st), (uint32_t)(p.tpc * p.R * D * 2));
+        tc::mbar_expect_tx(full, (uint32_t)(p.tpc * p.R * D * 2));
         for (int c = 0; c < D / 64; ++c)
-          tc::tma3d(q_s + st * p.q_bytes + c * (p.q_bytes / (D / 64)), &tm_q, c * 64, g * p.R,
-                    (int)(start + t_lo + j * p.tpc), bar(QFULL + st));
+          tc::tma3d(to + c * p.q_group, &tm_q, c * 64, g * p.R, (int)(start + t), full);
       }
       __syncwarp();
-      last_q = j;
+    };
+    auto load_k = [&](uint32_t to, int key0, uint32_t full) {
+      load_tile<D, true>(to, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, key0, 0, 0,
+                         min(KT, up16(kv_len - key0)), kv_len, full, lane);
+    };
+    if (any && FEW) load_q(fixed_s, 0, bar(FIXED));
+    if (any && !FEW) load_k(fixed_s, fkey0, bar(FIXED));
+    int slot = 0;
+    uint32_t phase = 1;
+    for (int i = 0; any && i < n; ++i) {
+      if (i >= NS && !wait(bar(EMPTY + slot), phase)) break;
+      if (FEW) {
+        load_k(ring_s + slot * slot_bytes, (kt0 + i) * KT, bar(FULL + slot));
+      } else {
+        stage_lse(s_lse[i & 3], t_lo + i * p.tpc, lane, 32);
+        __syncwarp();
+        load_q(ring_s + slot * slot_bytes, t_lo + i * p.tpc, bar(FULL + slot));
+      }
+      last_item = i;
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------------ products
-    bool ok = n == 0 || tc::warp_wait(bar(K), 0, abort);
-    for (int j = 0; ok && j < n; ++j) {
-      const int st = j & 1;
-      if (j >= 2 && !(ok = tc::warp_wait(bar(SFREE + st), ((j >> 1) - 1) & 1, abort))) break;
-      if (!(ok = tc::warp_wait(bar(QFULL + st), (j >> 1) & 1, abort))) break;
-      if (lane == 0) {
-        tc::fence_after();
-        const uint32_t id = tc::idesc(KT, p.cols), qh = p.q_bytes / (D / 64);
+    bool ok = !any || wait(bar(FIXED), 0);
+    const uint32_t lead = elect(), id = tc::idesc(KT, p.cols), fixed_d = desc_k(fixed_s), ring_d = desc_k(ring_s);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int i = 0; ok && any && i < n; ++i) {
+      const int b = i & 1;
+      if (i >= 2 && !(ok = wait(bar(SFREE + b), ((i >> 1) - 1) & 1))) break;
+      if (!(ok = wait(bar(FULL + slot), phase))) break;
+      tc::fence_after();
+      const uint32_t at = ring_d + slot * (slot_bytes >> 4);
+      const uint32_t kd = FEW ? at : fixed_d, qd = FEW ? fixed_d : at, qg = p.q_group >> 4;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          tc::mma_ss(tmem + st * p.buf_cols, tc::sdesc(k_s + (s >> 2) * (KT * 128) + (s & 3) * 32),
-                     tc::sdesc(q_s + st * p.q_bytes + (s >> 2) * qh + (s & 3) * 32), id, s > 0);
-        tc::commit(bar(SFULL + st));
-        tc::commit(bar(QEMPTY + st));
+      for (int s = 0; s < D / 16; ++s)
+        mma_ss(tmem + b * p.buf_cols, kd + (s >> 2) * (KT * 128 >> 4) + (s & 3) * 2, qd + (s >> 2) * qg + (s & 3) * 2,
+               id, s > 0, lead);
+      commit(bar(SFULL + b), lead);
+      commit(bar(EMPTY + slot), lead);
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
       }
-      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------------ sums, one key a thread
-    const int key = key0 + tid;
-    const bool have = key < kv_len && !((s_bad >> (tid / GRAN)) & 1u);
     const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
     float acc = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1, t = t_lo + j * p.tpc;
-      // this tile's lse, a copy for each warp (rows of no query: +inf, so that they add 0)
-      __syncwarp();
-#pragma unroll
-      for (int e = lane; e < ROWS; e += 32) {
-        float le = __builtin_inff();
-        if (e < p.tpc * p.R && t + e / p.R < Lq) {
-          le = p.lse[(start + t + e / p.R) * p.h + g * p.R + e % p.R];
-          le = le == kNegInf ? __builtin_inff() : le * kLog2e;
-        }
-        s_lse[warp][e] = le;
+    auto finish = [&](float sum, float before, int64_t at) {
+      if (at >= 0) p.w_out[at] = p.w_in ? fmaf(p.decay, before, sum) : sum;
+    };
+    auto place = [&](int key) -> int64_t {  // the key's weight, or -1 (no key, or in no page)
+      if (key >= kv_len) return -1;
+      const int pid = page_of(p.keys, seq, key);
+      return pid < 0 ? -1 : (((int64_t)pid * p.hkv + g) << p.keys.page_log2) + (key & ((1 << p.keys.page_log2) - 1));
+    };
+    for (int i = 0; i < n; ++i) {
+      const int b = i & 1, key = FEW ? (kt0 + i) * KT + tid : fkey0 + tid, t = FEW ? 0 : t_lo + i * p.tpc;
+      int64_t at = -1;
+      float before = 0.f;
+      if (FEW) {  // (read ahead of the product)
+        at = place(key);
+        if (at >= 0 && p.w_in) before = p.w_in[at];
+        acc = 0.f;
       }
-      __syncwarp();
-      // columns [c_lo, c_hi) are rows whose query sees this key
-      int c_lo = 0, c_hi = 0;
-      if (have) {
+      if (any) {
+        // columns [c_lo, c_hi) are rows whose query sees this key
         const int64_t first = (int64_t)(key - off - t) * p.R;
         int64_t end = (int64_t)min(p.tpc, Lq - t) * p.R;
-        if (p.window > 0 && key >= p.n_sink) end = min(end, (int64_t)(key + (int64_t)p.window - off - t) * p.R);
-        c_lo = first > 0 ? (int)min(first, (int64_t)ROWS) : 0;
-        c_hi = end > 0 ? (int)end : 0;
-      }
-      if (!(ok = tc::warp_wait(bar(SFULL + st), (j >> 1) & 1, abort))) break;
-      tc::fence_after();
-      float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < p.cols; c += 32) {
-        float sv[32];
-        tc::tmem_ld32(t_lane + st * p.buf_cols + c, sv);
-        const float4* l4 = reinterpret_cast<const float4*>(&s_lse[warp][c]);
-        if (__all_sync(0xffffffffu, c_lo <= c && c_hi >= c + 32)) {
+        if (p.window > 0 && key >= p.n_sink) end = min(end, ((int64_t)key + p.window - off - t) * p.R);
+        const int c_lo = (int)max((int64_t)0, min(first, (int64_t)ROWS));
+        const int c_hi = key < kv_len ? (int)max((int64_t)0, end) : 0;
+        if (!(ok = wait(bar(SFULL + b), (i >> 1) & 1))) break;
+        tc::fence_after();
+        const float* lse = s_lse[FEW ? 0 : i & 3];
+        uint64_t a2[4] = {0, 0, 0, 0};
+        const uint32_t s_t = t_lane + b * p.buf_cols;
+        auto sum = [&](float (&sv)[32], int c) {
+          const float4* l4 = reinterpret_cast<const float4*>(lse + c);
+          const uint32_t see = bits(c_lo - c, c_hi - c);
+          if (!__all_sync(0xffffffffu, see == ~0u)) {
+            // (a column of no query holds whatever lies past the tile's rows)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 l = l4[e];
-            a4[0] += ex2(fmaf(sv[4 * e], p.scale_log2, -l.x));
-            a4[1] += ex2(fmaf(sv[4 * e + 1], p.scale_log2, -l.y));
-            a4[2] += ex2(fmaf(sv[4 * e + 2], p.scale_log2, -l.z));
-            a4[3] += ex2(fmaf(sv[4 * e + 3], p.scale_log2, -l.w));
+            for (int e = 0; e < 32; ++e) sv[e] = (see >> e) & 1u ? sv[e] : kNegInf;
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 l = l4[e];
-            const int cc = c + 4 * e;
-            a4[0] += cc >= c_lo && cc < c_hi ? ex2(fmaf(sv[4 * e], p.scale_log2, -l.x)) : 0.f;
-            a4[1] += cc + 1 >= c_lo && cc + 1 < c_hi ? ex2(fmaf(sv[4 * e + 1], p.scale_log2, -l.y)) : 0.f;
-            a4[2] += cc + 2 >= c_lo && cc + 2 < c_hi ? ex2(fmaf(sv[4 * e + 2], p.scale_log2, -l.z)) : 0.f;
-            a4[3] += cc + 3 >= c_lo && cc + 3 < c_hi ? ex2(fmaf(sv[4 * e + 3], p.scale_log2, -l.w)) : 0.f;
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l = l4[e / 4];
+            const float2 y = unpair(fma2(pair(sv[e], sv[e + 1]), scale2, pair(l.x, l.y)));
+            const float2 z = unpair(fma2(pair(sv[e + 2], sv[e + 3]), scale2, pair(l.z, l.w)));
+            a2[(e >> 1) & 3] = add2(a2[(e >> 1) & 3], pair(ex2(y.x), ex2(y.y)));
+            a2[((e >> 1) + 1) & 3] = add2(a2[((e >> 1) + 1) & 3], pair(ex2(z.x), ex2(z.y)));
           }
+        };
+        // 32 columns at a time, the next ones on their way while these are summed
+        float sa[32], sb[32];
+        tc::tmem_ld32_nowait(s_t, sa);
+        tmem_wait_ld(sa);
+        if (p.cols > 32) tc::tmem_ld32_nowait(s_t + 32, sb);
+        sum(sa, 0);
+        if (p.cols > 32) {
+          tmem_wait_ld(sb);
+          if (p.cols > 64) tc::tmem_ld32_nowait(s_t + 64, sa);
+          sum(sb, 32);
         }
+        if (p.cols > 64) {
+          tmem_wait_ld(sa);
+          if (p.cols > 96) tc::tmem_ld32_nowait(s_t + 96, sb);
+          sum(sa, 64);
+        }
+        if (p.cols > 96) {
+          tmem_wait_ld(sb);
+          sum(sb, 96);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(SFREE + b));
+        const float2 s2 = unpair(add2(add2(a2[0], a2[1]), add2(a2[2], a2[3])));
+        acc += s2.x + s2.y;
       }
-      acc += (a4[0] + a4[1]) + (a4[2] + a4[3]);
-      tc::fence_before();
-      tc::mbar_arrive(bar(SFREE + st));
+      if (FEW) finish(acc, before, at);
     }
-    if (ok && have) {
-      const int64_t at = ((int64_t)page_of(p.keys, seq, key) * p.hkv + g << p.keys.page_log2) +
-                         (key & ((1 << p.keys.page_log2) - 1));
-      p.w_out[at] = p.w_in ? fmaf(p.decay, p.w_in[at], acc) : acc;
+    if (!FEW && ok) {
+      const int64_t at = place(fkey0 + tid);
+      finish(acc, at >= 0 && p.w_in ? p.w_in[at] : 0.f, at);
     }
   }
 
   __syncthreads();
   if (*abort) {
+    // copies and products still in flight land before the CTA leaves
     if (warp == 4) {
-      if (n > 0) tc::warp_drain(bar(K), 0);
-      for (int st = 0; st < 2; ++st)
-        if (last_q >= st) tc::warp_drain(bar(QFULL + st), ((last_q - ((last_q ^ st) & 1)) >> 1) & 1);
+      if (any) tc::warp_drain(bar(FIXED), 0);
+      for (int st = 0; st < NS; ++st)
+        if (last_item >= st) tc::warp_drain(bar(FULL + st), ((last_item - st) / NS) & 1);
     } else if (warp == 5) {
       if (lane == 0) tc::commit(bar(DRAIN));
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }
   } else if (warp == 4) {
-    for (int st = 0; st < 2; ++st)
-      if (last_q >= st) tc::warp_drain(bar(QEMPTY + st), ((last_q - ((last_q ^ st) & 1)) >> 1) & 1);
+    for (int st = 0; st < NS; ++st)
+      if (last_item >= st) tc::warp_drain(bar(EMPTY + st), ((last_item - st) / NS) & 1);
   }
   tc::fence_before();
   __syncthreads();
   if (warp == 5) tmem_free(tmem, p.tmem_cols);
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
-  p.R = p.h / p.hkv;
-  p.tpc = std::max(1, std::min(ROWS / p.R, p.seqs.max_len));
+  using C = WCfg<D, FEW>;
   p.cols = up16(p.tpc * p.R);
-  p.q_bytes = p.cols * D * 2;
-  // 128-byte-swizzled tiles start on 1024 bytes: 16 rows of 128 bytes are 2048
+  p.q_group = p.cols * 128;
   p.buf_cols = 32;
   while ((int)p.buf_cols < p.cols) p.buf_cols *= 2;
   p.tmem_cols = 2 * p.buf_cols;
@@ -227,14 +292,18 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   if (!query_map(&mq, any ? q : p.keys.k, any ? p.seqs.tokens : 1, p.h, D, p.R, p.tpc) ||
       !key_maps(&mk, &mk16, p.keys.k, p.keys, p.hkv, D, 0))
     return cudaErrorInvalidValue;
-  int smem = KT * D * 2 + kWStages * p.q_bytes + 1024;
+  const int q_bytes = (D / 64) * p.q_group;
+  int smem = (FEW ? q_bytes + C::NS * C::K_BYTES : C::K_BYTES + C::NS * q_bytes) + 1024;
   // no more CTAs on an SM than its 512 TMEM columns serve (228 KB, 1 KB of it per CTA reserved)
   smem = std::max(smem, 228 * 1024 / (512 / (int)p.tmem_cols + 1) - 1024 + 16);
-  auto kern = weights_kernel<D>;
+  auto kern = weights_kernel<D, FEW>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t cap = (int64_t)p.keys.max_pages << p.keys.page_log2;
-  const dim3 grid((unsigned)((cap + KT - 1) / KT), p.seqs.n_seqs, p.hkv);
+  const int64_t tiles = (((int64_t)p.keys.max_pages << p.keys.page_log2) + KT - 1) / KT;
+  const int64_t units = (int64_t)p.seqs.n_seqs * p.hkv;
+  // FEW: about four rounds of two CTAs an SM, so that ragged caches even out
+  p.n_splits = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, (4 * 2 * 152 + units - 1) / units));
+  const dim3 grid((unsigned)(FEW ? p.n_splits : tiles), p.seqs.n_seqs, p.hkv);
   kern<<<grid, kWThreads, smem, st>>>(mq, mk, mk16, p);
   return cudaGetLastError();
 }
@@ -253,11 +322,16 @@ cudaError_t launch_span_weights(const Seqs& s, const void* q, const PagedView& c
   p.w_out = w_out;
   p.h = h;
   p.hkv = hkv;
+  p.R = h / hkv;
+  p.tpc = std::max(1, std::min(span::ROWS / p.R, s.max_len));
   p.window = window;
   p.n_sink = n_sink;
   p.scale_log2 = scale * kLog2e;
   p.decay = decay;
-  return d == 64 ? span::launch_weights_d<64>(p, q, st) : span::launch_weights_d<128>(p, q, st);
+  // a sequence's queries fit one tile of at most 48 rows (what leaves room for two CTAs an SM)
+  if ((int64_t)s.max_len * p.R <= 48)
+    return d == 64 ? span::launch_weights_d<64, true>(p, q, st) : span::launch_weights_d<128, true>(p, q, st);
+  return d == 64 ? span::launch_weights_d<64, false>(p, q, st) : span::launch_weights_d<128, false>(p, q, st);
 }
 
 NSA_STATUS_ACCESSOR(span_weights)
