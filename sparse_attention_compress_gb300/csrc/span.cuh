@@ -251,6 +251,19 @@ struct Waits {
   }
 };
 
+// Position in a ring of n slots: the slot and the parity of its phase.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // 32 TMEM columns whose load was issued with tc::tmem_ld32_nowait: waits for every load of
 // the thread so far and makes v's registers depend on the wait.
 __device__ __forceinline__ void tmem_wait_ld(float* v) {

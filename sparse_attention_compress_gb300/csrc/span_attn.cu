@@ -51,19 +51,6 @@ struct Cfg {
   static constexpr int MIN_REGS = (NH * 128 * kSoftRegs + 128 * OTHER_REGS + THREADS - 1) / THREADS;
 };
 
-// Position in a ring of n slots: the slot and the parity of its phase.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 struct AttnParams {
   Seqs seqs;
   Keys keys;

@@ -9,7 +9,7 @@
 // Two kernels, each a chain of M = 128 products over 128-wide tiles with eight softmax
 // warps (two threads a TMEM lane, 64 columns each):
 //   dq_kernel   a CTA owns 128 rows and walks the key tiles they see (S, dP, dQ).  It also
-//               stores each row's base-2 lse and D for the second kernel.
+//               stores each row's base-2 lse and D (negated) for the second kernel.
 //   dkv_kernel  a CTA owns 128 keys and walks the query tiles that see them, transposed
 //               (S^T = K Q^T, dP^T = V dO^T), so that P^T and dS^T are, in place in TMEM,
 //               the A operands of dV += P^T dO and dK += dS^T Q, and nothing passes through
@@ -32,8 +32,8 @@ struct BwdParams {
   Keys keys;  // packed
   const __nv_bfloat16 *q, *o, *dout;
   const float* lse;
-  float* lse2;  // [tokens, h] workspace: base-2 lse (+inf for rows without keys)
-  float* dsum;  // [tokens, h] workspace: D
+  float* nlse2;  // [tokens, h] workspace: minus the base-2 lse (-inf for rows without keys)
+  float* ndsum;  // [tokens, h] workspace: minus D
   __nv_bfloat16 *dq, *dk, *dv;
   float* part;  // [n_seqs][hkv][sink tiles][1 + n_far][2][sink_rows][D] fp32
   int h, hkv, R, tpc, cols, window, n_sink;
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
       dsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
       if (x == 0) {
-        p.lse2[rr] = l2;
-        p.dsum[rr] = dsum;
+        p.nlse2[rr] = -l2;
+        p.ndsum[rr] = -dsum;
       }
     }
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nl2 = pair(-l2, -l2), nd2 = pair(-dsum, -dsum);
@@ -352,11 +352,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 // formed dV and the next S^T do.  (S^T of a tile overwrites P^T of the one before, and dP^T
 // its dS^T: the same lane issued the products that read them, and products execute in
 // issue order.)
-constexpr int kDkvThreads = 352;
+// (Three Q slots would fit but for the 3 KB of lse and D beside them.)
+constexpr int kDkvThreads = 352, kNQ = 2, kND = 2;
 
 template <int D>
 constexpr int dkv_smem() {
-  return 6 * KT * D * 2 + 1024;
+  return (2 + kNQ + kND) * KT * D * 2 + 1024;
 }
 
 template <int D>
@@ -367,28 +368,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                const BwdParams p) {
   enum : int {
     KV = 0,      // [2] K, V
-    QFULL = 2,   // [2] by stage: Q rows, lse, D
-    QEMPTY = 4,  // [2]
-    DFULL = 6,   // [2] dO rows
-    DEMPTY = 8,  // [2]
-    SFULL = 10,
-    PFULL = 11,   // P^T written
-    DVDONE = 12,  // every dV product is done
-    DPFULL = 13,
-    DSFULL = 14,  // dS^T written
-    DKDONE = 15,  // every dK product is done
-    DRAIN = 16,
+    QFULL = 2,             // by slot: Q rows, lse, D
+    QEMPTY = QFULL + kNQ,
+    DFULL = QEMPTY + kNQ,  // by slot: dO rows
+    DEMPTY = DFULL + kND,
+    SFULL = DEMPTY + kND,
+    PFULL,   // P^T written
+    DVDONE,  // every dV product is done
+    DPFULL,
+    DSFULL,  // dS^T written
+    DKDONE,  // every dK product is done
+    DRAIN,
     COUNT
   };
   constexpr int TB = KT * D * 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ __align__(16) float s_l2[2][ROWS], s_d[2][ROWS];  // minus the rows' base-2 lse and D
+  __shared__ __align__(16) float s_l2[kNQ][ROWS], s_d[kNQ][ROWS];  // minus the rows' base-2 lse and D
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t k_s = base, v_s = k_s + TB, q_s = v_s + TB, do_s = q_s + 2 * TB;
+  const uint32_t k_s = base, v_s = k_s + TB, q_s = v_s + TB, do_s = q_s + kNQ * TB;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
@@ -413,10 +414,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int used = p.tpc * p.R;  // rows of a tile
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(bar(KV + i), 1);
+    tc::mbar_init(bar(KV), 1);
+    tc::mbar_init(bar(KV + 1), 1);
+    for (int i = 0; i < kNQ; ++i) {
       tc::mbar_init(bar(QFULL + i), 1);
       tc::mbar_init(bar(QEMPTY + i), 1);
+    }
+    for (int i = 0; i < kND; ++i) {
       tc::mbar_init(bar(DFULL + i), 1);
       tc::mbar_init(bar(DEMPTY + i), 2);  // dP^T and dV have read dO
     }
@@ -432,8 +436,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   }
   // rows between the tile's own and the next multiple of 16 (group sizes that do not divide
   // 128) enter the products as zeros; no copy ever writes them
-  for (int e = tid; e < (p.cols - used) * 4 * (D / 8); e += kDkvThreads) {
-    const int ch = e % (D / 8), which = (e / (D / 8)) & 3, r = used + e / (4 * (D / 8));
+  for (int e = tid; e < (p.cols - used) * (kNQ + kND) * (D / 8); e += kDkvThreads) {
+    const int ch = e % (D / 8), which = e / (D / 8) % (kNQ + kND), r = used + e / ((kNQ + kND) * (D / 8));
     const uint32_t to = q_s + which * TB + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to), "r"(0u) : "memory");
   }
@@ -455,80 +459,105 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     load_tile<D, false>(v_s, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, key0, 0, 0, w, L,
                         bar(KV + 1), lane);
     // Rows of tokens t .. t + tpc - 1 (those past the sequence as zeros: they are another
-    // sequence's, or lie past the tensors).
+    // sequence's, or lie past the tensors); returns the bytes to come.
     auto load_rows = [&](uint32_t to, const CUtensorMap* map, const __nv_bfloat16* src, int t, uint32_t full) {
-      uint32_t bytes = 0;
       if (t + p.tpc <= L) {
-        bytes = (uint32_t)(used * D * 2);
         if (lane < D / 64) tc::tma3d(to + lane * (ROWS * 128), map, lane * 64, g * p.R, (int)(start + t), full);
-      } else {
-        for (int e = lane; e < used * (D / 8); e += 32) {
-          const int r = e / (D / 8), ch = e % (D / 8), tt = t + r / p.R;
-          const bool in = tt < L;
-          cp_async16(to + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                     in ? (const void*)(src + ((start + tt) * p.h + g * p.R + r % p.R) * D + ch * 8) : (const void*)src,
-                     in ? 16 : 0);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        return (uint32_t)(used * D * 2);
+      }
+      for (int e = lane; e < used * (D / 8); e += 32) {
+        const int r = e / (D / 8), ch = e % (D / 8), tt = t + r / p.R;
+        const bool in = tt < L;
+        cp_async16(to + (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   in ? (const void*)(src + ((start + tt) * p.h + g * p.R + r % p.R) * D + ch * 8) : (const void*)src,
+                   in ? 16 : 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      return 0u;
+    };
+    // minus the base-2 lse and D of a tile's rows, four a lane, fetched a tile ahead
+    float nl[ROWS / 32], nd[ROWS / 32];
+    int tok[ROWS / 32], at[ROWS / 32];  // a row's token (past every sequence: no row) and place in the tile
+#pragma unroll
+    for (int i = 0; i < ROWS / 32; ++i) {
+      const int e = lane + i * 32;
+      tok[i] = e < used ? e / p.R : 1 << 30;
+      at[i] = e / p.R * p.h + e % p.R;
+    }
+    auto fetch = [&](int t) {
+      const int64_t r0 = (start + t) * p.h + g * p.R;
+#pragma unroll
+      for (int i = 0; i < ROWS / 32; ++i) {
+        const bool in = tok[i] < L - t;
+        nl[i] = in ? __ldg(p.nlse2 + r0 + at[i]) : kNegInf;
+        nd[i] = in ? __ldg(p.ndsum + r0 + at[i]) : 0.f;
+      }
+    };
+    fetch(t_lo);
+    Ring<kNQ> rq;
+    Ring<kND> rd;
+    for (int j = 0; j < n; ++j) {
+      const int t = t_lo + j * p.tpc;
+      if (j >= kNQ && !wait(bar(QEMPTY + rq.slot), rq.phase ^ 1u)) break;
+      uint32_t bytes = load_rows(q_s + rq.slot * TB, &tm_q, p.q, t, bar(QFULL + rq.slot));
+#pragma unroll
+      for (int i = 0; i < ROWS / 32; ++i) {
+        s_l2[rq.slot][lane + i * 32] = nl[i];
+        s_d[rq.slot][lane + i * 32] = nd[i];
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_expect_tx(full, bytes);
-    };
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1, t = t_lo + j * p.tpc;
-      if (j >= 2 && !wait(bar(QEMPTY + st), ((j >> 1) - 1) & 1)) break;
-#pragma unroll
-      for (int e = lane; e < ROWS; e += 32) {
-        float a = __builtin_inff(), b = 0.f;
-        if (e < used && t + e / p.R < L) {
-          const int64_t rr = (start + t + e / p.R) * p.h + g * p.R + e % p.R;
-          a = p.lse2[rr];
-          b = p.dsum[rr];
-        }
-        s_l2[st][e] = -a;
-        s_d[st][e] = -b;
-      }
-      load_rows(q_s + st * TB, &tm_q, p.q, t, bar(QFULL + st));
+      if (lane == 0) tc::mbar_expect_tx(bar(QFULL + rq.slot), bytes);
       last_q = j;
-      if (j >= 2 && !wait(bar(DEMPTY + st), ((j >> 1) - 1) & 1)) break;
-      load_rows(do_s + st * TB, &tm_do, p.dout, t, bar(DFULL + st));
+      if (j + 1 < n) fetch(t + p.tpc);
+      if (j >= kND && !wait(bar(DEMPTY + rd.slot), rd.phase ^ 1u)) break;
+      bytes = load_rows(do_s + rd.slot * TB, &tm_do, p.dout, t, bar(DFULL + rd.slot));
+      __syncwarp();
+      if (lane == 0) tc::mbar_expect_tx(bar(DFULL + rd.slot), bytes);
       last_d = j;
+      rq.next();
+      rd.next();
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ S^T, dV += P^T dO
-    const uint32_t lead = elect();
+    const uint32_t lead = elect(), kd = desc_k(k_s), qd = desc_k(q_s), dd = desc_mn(do_s);
+    Ring<kNQ> rq;
+    Ring<kND> rd;
     bool ok = wait(bar(KV), 0);
     for (int j = 0; ok && j < n; ++j) {
-      const int st = j & 1;
-      if (!(ok = wait(bar(QFULL + st), (j >> 1) & 1))) break;
+      if (!(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
       tc::fence_after();
-      mma_abt<D>(tmem, desc_k(k_s), desc_k(q_s) + st * (TB >> 4), p.cols, lead);
+      mma_abt<D>(tmem, kd, qd + rq.slot * (TB >> 4), p.cols, lead);
       commit(bar(SFULL), lead);
+      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
       if (!(ok = wait(bar(PFULL), j & 1))) break;
-      if (!(ok = wait(bar(DFULL + st), (j >> 1) & 1))) break;
       tc::fence_after();
-      mma_split_a<D>(tmem + 256, tmem, desc_mn(do_s) + st * (TB >> 4), p.cols, j == 0, lead);
-      commit(bar(DEMPTY + st), lead);
+      mma_split_a<D>(tmem + 256, tmem, dd + rd.slot * (TB >> 4), p.cols, j == 0, lead);
+      commit(bar(DEMPTY + rd.slot), lead);
       if (j == n - 1) commit(bar(DVDONE), lead);
+      rq.next();
+      rd.next();
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------------ dP^T, dK += dS^T Q
-    const uint32_t lead = elect();
+    const uint32_t lead = elect(), vd = desc_k(v_s), dd = desc_k(do_s), qd = desc_mn(q_s);
+    Ring<kNQ> rq;
+    Ring<kND> rd;
     bool ok = wait(bar(KV + 1), 0);
     for (int j = 0; ok && j < n; ++j) {
-      const int st = j & 1;
-      if (!(ok = wait(bar(DFULL + st), (j >> 1) & 1))) break;
+      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
       tc::fence_after();
-      mma_abt<D>(tmem + 128, desc_k(v_s), desc_k(do_s) + st * (TB >> 4), p.cols, lead);
+      mma_abt<D>(tmem + 128, vd, dd + rd.slot * (TB >> 4), p.cols, lead);
       commit(bar(DPFULL), lead);
-      commit(bar(DEMPTY + st), lead);
+      commit(bar(DEMPTY + rd.slot), lead);
       if (!(ok = wait(bar(DSFULL), j & 1))) break;
       tc::fence_after();
-      mma_split_a<D>(tmem + 384, tmem + 128, desc_mn(q_s) + st * (TB >> 4), p.cols, j == 0, lead);
+      mma_split_a<D>(tmem + 384, tmem + 128, qd + rq.slot * (TB >> 4), p.cols, j == 0, lead);
       if (j == n - 1) commit(bar(DKDONE), lead);
-      commit(bar(QEMPTY + st), lead);  // (S^T of the tile was done before its dS^T)
+      commit(bar(QEMPTY + rq.slot), lead);  // (S^T of the tile was done before its dS^T)
+      rq.next();
+      rd.next();
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -538,9 +567,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t s_t = tmem + c0 + lane_base, p_t = tmem + 128 + c0 + lane_base;
     const int nc = min(64, p.cols - c0);
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+    Ring<kNQ> rq;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1, t = t_lo + j * p.tpc;
+    for (int j = 0; j < n; ++j, rq.next()) {
+      const int st = rq.slot, t = t_lo + j * p.tpc;
       // columns [c_lo, c_hi) of this half are rows whose query sees this key
       int c_lo = 0, c_hi = 0;
       if (have) {
@@ -549,7 +579,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
         c_hi = (int)max((int64_t)0, end) - c0;
       }
-      if (!(ok = wait(bar(QFULL + st), (j >> 1) & 1))) break;  // lse and D
+      if (!(ok = wait(bar(QFULL + st), rq.phase))) break;  // lse and D
       if (!(ok = wait(bar(SFULL), j & 1))) break;
       tc::fence_after();
       float sv[64];
@@ -656,20 +686,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (warp == 8) {
       tc::warp_drain(bar(KV), 0);
       tc::warp_drain(bar(KV + 1), 0);
-      for (int st = 0; st < 2; ++st) {
-        if (const int i = last_in(last_q, st, 2); i >= 0) tc::warp_drain(bar(QFULL + st), (i >> 1) & 1);
-        if (const int i = last_in(last_d, st, 2); i >= 0) tc::warp_drain(bar(DFULL + st), (i >> 1) & 1);
-      }
+      for (int st = 0; st < kNQ; ++st)
+        if (const int i = last_in(last_q, st, kNQ); i >= 0) tc::warp_drain(bar(QFULL + st), (i / kNQ) & 1);
+      for (int st = 0; st < kND; ++st)
+        if (const int i = last_in(last_d, st, kND); i >= 0) tc::warp_drain(bar(DFULL + st), (i / kND) & 1);
     } else if (warp > 8) {
       if (lane == 0) tc::commit(bar(DRAIN));
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }
   } else if (warp == 8) {
-    for (int st = 0; st < 2; ++st) {
-      if (const int i = last_in(last_q, st, 2); i >= 0) tc::warp_drain(bar(QEMPTY + st), (i >> 1) & 1);
-      if (const int i = last_in(last_d, st, 2); i >= 0) tc::warp_drain(bar(DEMPTY + st), (i >> 1) & 1);
-    }
+    for (int st = 0; st < kNQ; ++st)
+      if (const int i = last_in(last_q, st, kNQ); i >= 0) tc::warp_drain(bar(QEMPTY + st), (i / kNQ) & 1);
+    for (int st = 0; st < kND; ++st)
+      if (const int i = last_in(last_d, st, kND); i >= 0) tc::warp_drain(bar(DEMPTY + st), (i / kND) & 1);
   }
   tc::fence_before();
   __syncthreads();
@@ -762,8 +792,8 @@ cudaError_t launch_span_bwd(const Seqs& s, const void* q, const void* k, const v
   p.o = (const __nv_bfloat16*)o;
   p.dout = (const __nv_bfloat16*)dout;
   p.lse = lse;
-  p.lse2 = (float*)workspace;
-  p.dsum = (float*)((uint8_t*)workspace + l.dsum);
+  p.nlse2 = (float*)workspace;
+  p.ndsum = (float*)((uint8_t*)workspace + l.dsum);
   p.part = (float*)((uint8_t*)workspace + l.part);
   p.dq = (__nv_bfloat16*)dq;
   p.dk = (__nv_bfloat16*)dk;

@@ -92,23 +92,21 @@ __global__ void __launch_bounds__(kWThreads, 2)
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  // minus the base-2 lse of the rows of query tile t, for a warp's lanes (-inf for rows of no
-  // query, so that they add 0)
-  auto stage_lse = [&](float* to, int t, int from, int step) {
-    for (int e = from; e < ROWS; e += step) {
-      float le = kNegInf;
-      if (e < p.tpc * p.R && t + e / p.R < Lq) {
-        le = -p.lse[(start + t + e / p.R) * p.h + g * p.R + e % p.R] * kLog2e;
-        if (le == -kNegInf) le = kNegInf;  // a row without keys
-      }
-      to[e] = le;
+  // minus the base-2 lse of row e of query tile t (-inf for a row of no query or without keys,
+  // so that it adds 0)
+  auto row_lse = [&](int t, int e) {
+    float le = kNegInf;
+    if (e < p.tpc * p.R && t + e / p.R < Lq) {
+      le = -__ldg(p.lse + (start + t + e / p.R) * p.h + g * p.R + e % p.R) * kLog2e;
+      if (le == -kNegInf) le = kNegInf;
     }
+    return le;
   };
   if (warp == 5) {
     tmem_alloc(smem_u32(&s_tmem), p.tmem_cols);
     tc::fence_before();
   }
-  if (FEW && warp < 4) stage_lse(s_lse[0], 0, tid, 128);
+  if (FEW && warp < 4) s_lse[0][tid] = row_lse(0, tid);
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
@@ -132,12 +130,20 @@ __global__ void __launch_bounds__(kWThreads, 2)
     if (any && !FEW) load_k(fixed_s, fkey0, bar(FIXED));
     int slot = 0;
     uint32_t phase = 1;
+    float nl[ROWS / 32];  // lse of a tile's rows, four a lane, fetched a tile ahead
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int e = 0; e < ROWS / 32; ++e) nl[e] = row_lse(t, lane + e * 32);
+    };
+    if (!FEW) fetch(t_lo);
     for (int i = 0; any && i < n; ++i) {
       if (i >= NS && !wait(bar(EMPTY + slot), phase)) break;
       if (FEW) {
         load_k(ring_s + slot * slot_bytes, (kt0 + i) * KT, bar(FULL + slot));
       } else {
-        stage_lse(s_lse[i & 3], t_lo + i * p.tpc, lane, 32);
+#pragma unroll
+        for (int e = 0; e < ROWS / 32; ++e) s_lse[i & 3][lane + e * 32] = nl[e];
+        if (i + 1 < n) fetch(t_lo + (i + 1) * p.tpc);
         __syncwarp();
         load_q(ring_s + slot * slot_bytes, t_lo + i * p.tpc, bar(FULL + slot));
       }
