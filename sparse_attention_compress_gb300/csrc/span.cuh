@@ -333,6 +333,53 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(cols) : "memory");
 }
 
+// Output rows staged in shared memory (the layout of the tiles: 64-column groups `group`
+// bytes apart, 16-byte chunk ch of row r at chunk ch ^ (r & 7)), so that they leave in whole
+// lines: a thread that wrote its own row to global memory would touch 32 lines per store.
+__device__ __forceinline__ uint32_t stage_at(uint32_t base, uint32_t group, int r, int ch) {
+  return base + (ch >> 3) * group + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// 32 columns c .. c + 31 of a row, times f, as bf16 to the stage.
+__device__ __forceinline__ void stage_cols(uint32_t base, uint32_t group, int r, int c, const float* v, float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    uint4 u;
+    u.x = pack_bf16(v[e] * f, v[e + 1] * f);
+    u.y = pack_bf16(v[e + 2] * f, v[e + 3] * f);
+    u.z = pack_bf16(v[e + 4] * f, v[e + 5] * f);
+    u.w = pack_bf16(v[e + 6] * f, v[e + 7] * f);
+    st_shared(stage_at(base, group, r, (c + e) / 8), u);
+  }
+}
+// The staged rows 0 .. rows - 1 (token r / R, head r % R; those of the first t_left tokens)
+// to dst, the first row's place; `threads` threads, this one `i`.
+template <int D>
+__device__ __forceinline__ void unstage_rows(uint32_t base, uint32_t group, int rows, int R, int h, int t_left,
+                                             __nv_bfloat16* dst, int i, int threads) {
+  constexpr int CH = D / 8;
+#pragma unroll 4
+  for (int e = i; e < rows * CH; e += threads) {
+    const int r = e / CH, ch = e % CH, tl = r / R;
+    if (tl < t_left)
+      *reinterpret_cast<uint4*>(dst + ((int64_t)tl * h + r % R) * D + ch * 8) = ld_shared(stage_at(base, group, r, ch));
+  }
+}
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ---------------------------------------------------------------------- host side
 // Maps of K (or V): the tile box and the 16-row box.
 inline bool key_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, const Keys& c, int hkv, int D,

@@ -409,26 +409,25 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
         }
       } else {
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const uint32_t stage = q_s + x * q_bytes;  // the half's Q, which its last S has read
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float ov[32];
-          if (cnt > 0) tc::tmem_ld32(o_t + c, ov);
-          if (valid) {
+          if (n > 0) tc::tmem_ld32(o_t + c, ov);  // (the whole warp's load)
+          if (!(l > 0.f)) {  // a row without keys holds no product
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (l > 0.f) {  // (a row without keys holds no product)
-                v.x = pack_bf16(ov[e] * inv, ov[e + 1] * inv);
-                v.y = pack_bf16(ov[e + 2] * inv, ov[e + 3] * inv);
-                v.z = pack_bf16(ov[e + 4] * inv, ov[e + 5] * inv);
-                v.w = pack_bf16(ov[e + 6] * inv, ov[e + 7] * inv);
-              }
-              *reinterpret_cast<uint4*>(p.o + rr * D + c + e) = v;
-            }
+            for (int e = 0; e < 32; ++e) ov[e] = 0.f;
           }
+          if (row < p.tpc * p.R) stage_cols(stage, p.q_group, row, c, ov, inv);
         }
         if (p.lse && valid) p.lse[rr] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
       }
+    }
+    if (whole && x < nh) {
+      named_barrier(1 + x, 128);  // (also after a timeout: every warp of the half comes here)
+      if (ok)
+        unstage_rows<D>(q_s + x * q_bytes, p.q_group, p.tpc * p.R, p.R, p.h, Lq - t0 - x * p.tpc,
+                        p.o + ((start + t0 + x * p.tpc) * p.h + g * p.R) * D, row, 128);
     }
   }
 

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   constexpr int TB = KT * D * 2;  // bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
+  __shared__ float s_dsum[ROWS];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -217,33 +218,52 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const bool valid = tl < p.tpc && t < L;
     const int pos = valid ? t : -1;
     const int64_t rr = (start + t) * p.h + g * p.R + hd;
+    bool ok = true;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    float l2 = __builtin_inff(), dsum = 0.f;
-    if (valid) {
-      const float l = p.lse[rr];
-      l2 = l == kNegInf ? __builtin_inff() : l * kLog2e;
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int c = 0; c < D; c += 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p.o + rr * D + c);
-        const uint4 b = *reinterpret_cast<const uint4*>(p.dout + rr * D + c);
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    // D of the CTA's rows, sixteen lanes (d = 128) a row: o from global memory, dO from its tile
+    constexpr int CH = D / 8, RPW = 32 / CH, NIT = ROWS / (8 * RPW);  // chunks a row, rows a warp at a time
+    {
+      const int used = p.tpc * p.R;
+      uint4 ov[NIT];
+#pragma unroll
+      for (int i = 0; i < NIT; ++i) {
+        const int r = (i * 8 + warp) * RPW + lane / CH;
+        ov[i] = make_uint4(0, 0, 0, 0);
+        if (r < used && t0 + r / p.R < L)
+          ov[i] = *reinterpret_cast<const uint4*>(p.o + ((start + t0 + r / p.R) * p.h + g * p.R + r % p.R) * D +
+                                                  lane % CH * 8);
+      }
+      ok = wait(bar(Q), 0);
+#pragma unroll
+      for (int i = 0; i < NIT; ++i) {
+        const int r = (i * 8 + warp) * RPW + lane / CH;
+        const uint4 dv = ld_shared(stage_at(do_s, ROWS * 128, r, lane % CH));
+        const uint32_t av[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, bv[4] = {dv.x, dv.y, dv.z, dv.w};
+        float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
           const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
-          s4[e] = fmaf(u.x, v.x, fmaf(u.y, v.y, s4[e]));
+          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
         }
+#pragma unroll
+        for (int o = CH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane % CH == 0) s_dsum[r] = sum;
       }
-      dsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      named_barrier(1, 256);  // (after a timeout too: every softmax warp comes here)
+    }
+    float l2 = __builtin_inff(), dsum = 0.f;
+    if (valid) {
+      const float l = p.lse[rr];
+      l2 = l == kNegInf ? __builtin_inff() : l * kLog2e;
+      dsum = s_dsum[row];
       if (x == 0) {
         p.nlse2[rr] = -l2;
         p.ndsum[rr] = -dsum;
       }
     }
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nl2 = pair(-l2, -l2), nd2 = pair(-dsum, -dsum);
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; ok && j < n; ++j) {
       const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
       if (!(ok = wait(bar(SFULL + b), (j >> 1) & 1))) break;
       tc::fence_after();
@@ -301,24 +321,18 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       tc::fence_after();
     }
     if (ok) {
-      __nv_bfloat16* dst = p.dq + rr * D;
+      // staged over Q, which every S has read
 #pragma unroll 1
       for (int c = x * (D / 2); c < (x + 1) * (D / 2); c += 32) {
         float v[32];
         tc::tmem_ld32(tmem + 384 + lane_base + c, v);
-        if (valid) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 u;
-            u.x = pack_bf16(v[e] * p.scale, v[e + 1] * p.scale);
-            u.y = pack_bf16(v[e + 2] * p.scale, v[e + 3] * p.scale);
-            u.z = pack_bf16(v[e + 4] * p.scale, v[e + 5] * p.scale);
-            u.w = pack_bf16(v[e + 6] * p.scale, v[e + 7] * p.scale);
-            *reinterpret_cast<uint4*>(dst + c + e) = u;
-          }
-        }
+        stage_cols(q_s, ROWS * 128, row, c, v, p.scale);
       }
     }
+    named_barrier(1, 256);
+    if (ok)
+      unstage_rows<D>(q_s, ROWS * 128, p.tpc * p.R, p.R, p.h, L - t0, p.dq + ((start + t0) * p.h + g * p.R) * D, tid,
+                      256);
   }
 
   __syncthreads();
