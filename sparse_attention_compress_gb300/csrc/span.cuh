@@ -275,6 +275,18 @@ __device__ __forceinline__ void tmem_wait_ld(float* v) {
                  "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
+// Starts the load of 32 columns if `on`; else the registers get a value all the same (what a
+// skipped load would leave in them is their last one, which would keep them occupied from
+// tile to tile).
+__device__ __forceinline__ void tmem_ld32_if(bool on, uint32_t taddr, float* v) {
+  if (on) {
+    tc::tmem_ld32_nowait(taddr, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+  }
+}
+
 // Two fp32 operations in one instruction (a pair in a 64-bit register).
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
       if (work) {
         float sv[KT];
         tc::tmem_ld32_nowait(s_t, sv);
-        if (w > 32) tc::tmem_ld32_nowait(s_t + 32, sv + 32);
+        tmem_ld32_if(w > 32, s_t + 32, sv + 32);
         // seen columns: [j_lo, j_hi) and the sinks [0, j_sink) before j_hi
         const int j_hi = min(pos + 1 - key0, w);
         const int j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, j_sink = tiles.sinks(a + it, p.n_sink);
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
         };
         tmem_wait_ld(sv);
         tmem_wait_ld(sv + 32);
-        if (w > 64) tc::tmem_ld32_nowait(s_t + 64, sv + 64);
-        if (w > 96) tc::tmem_ld32_nowait(s_t + 96, sv + 96);
+        tmem_ld32_if(w > 64, s_t + 64, sv + 64);
+        tmem_ld32_if(w > 96, s_t + 96, sv + 96);
         if (!all) {
           mask(0);
           mask(32);
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float ov[32];
-          if (n > 0) tc::tmem_ld32(o_t + c, ov);  // (the whole warp's load)
+          tmem_ld32_if(n > 0, o_t + c, ov);  // (the whole warp's load)
+          tmem_wait_ld(ov);
           if (!(l > 0.f)) {  // a row without keys holds no product
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] = 0.f;

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
+        tmem_ld32_if(c < nc, s_t + c, sv + c);
       const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
       const bool all = j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64);
       tmem_wait_ld(sv);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       float dp[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        if (c < nc) tc::tmem_ld32_nowait(p_t + c, dp + c);
+        tmem_ld32_if(c < nc, p_t + c, dp + c);
       tmem_wait_ld(dp);
       tmem_wait_ld(dp + 32);
       tc::fence_before();
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        if (c < nc) tc::tmem_ld32_nowait(s_t + c, sv + c);
+        tmem_ld32_if(c < nc, s_t + c, sv + c);
       const bool all = c_lo <= 0 && c_hi >= 64;
       const float4* l4 = reinterpret_cast<const float4*>(&s_l2[st][c0]);
       tmem_wait_ld(sv);
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       float dp[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        if (c < nc) tc::tmem_ld32_nowait(p_t + c, dp + c);
+        tmem_ld32_if(c < nc, p_t + c, dp + c);
       tmem_wait_ld(dp);
       tmem_wait_ld(dp + 32);
 #pragma unroll

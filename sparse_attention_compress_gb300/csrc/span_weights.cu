@@ -233,16 +233,16 @@ __global__ void __launch_bounds__(kWThreads, 2)
         float sa[32], sb[32];
         tc::tmem_ld32_nowait(s_t, sa);
         tmem_wait_ld(sa);
-        if (p.cols > 32) tc::tmem_ld32_nowait(s_t + 32, sb);
+        tmem_ld32_if(p.cols > 32, s_t + 32, sb);
         sum(sa, 0);
         if (p.cols > 32) {
           tmem_wait_ld(sb);
-          if (p.cols > 64) tc::tmem_ld32_nowait(s_t + 64, sa);
+          tmem_ld32_if(p.cols > 64, s_t + 64, sa);
           sum(sb, 32);
         }
         if (p.cols > 64) {
           tmem_wait_ld(sa);
-          if (p.cols > 96) tc::tmem_ld32_nowait(s_t + 96, sb);
+          tmem_ld32_if(p.cols > 96, s_t + 96, sb);
           sum(sa, 64);
         }
         if (p.cols > 96) {
