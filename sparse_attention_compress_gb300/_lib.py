@@ -615,10 +615,22 @@ def nsa_layer_bwd(q, k, v, gate_logits, saved, d_o, kernel=32, stride=16, block_
 
 # ----------------------------------------------------------------------------- paged cache
 # These calls check what the C entry points cannot see: that every tensor lies on one GPU,
-# dense and of its type.  Tensors they allocate belong to the stream the call runs on.
+# dense and of its type.  Tensors they allocate belong to the stream the call runs on.  A
+# decode step is a few microseconds of GPU time, so the checks come in two forms: a quick
+# test, and the search for what is wrong when it fails.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_HERE = contextlib.nullcontext()
+
+
+def _fits(t, dtype, shape, index) -> bool:
+    """A dense tensor of this type and shape on GPU `index` (or none given)."""
+    return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                         and t.get_device() == index and t.is_contiguous())
+
+
 def _expect(fn, device, **tensors):
-    """Every named (tensor, dtype, shape); None where the caller left a tensor out.  Entries of
-    a shape that are None may be anything."""
+    """Raise for the first of the named (tensor, dtype, shape) that does not fit.  Entries of a
+    shape that are None may be anything."""
     for name, (t, dtype, shape) in tensors.items():
         if t is None:
             continue
@@ -627,7 +639,7 @@ def _expect(fn, device, **tensors):
         if t.dtype != dtype:
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
         if t.device != device:
-            raise ValueError(f"{fn}: {name} is on {t.device}, q or the pages on {device}")
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on {device}")
         if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
@@ -635,72 +647,88 @@ def _expect(fn, device, **tensors):
 
 
 def _on(device, stream):
-    """(context that makes the call's device and stream current, the stream)."""
+    """(context that makes the call's device and stream current, raw stream, the caller's stream
+    where it is another one)."""
     if device.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {device}")
+    if stream is None:
+        here = torch.cuda.current_device() == device.index
+        return _HERE if here else torch.cuda.device(device), torch._C._cuda_getCurrentRawStream(device.index), None
+    if stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
     now = torch.cuda.current_stream(device)
-    s = stream if stream is not None else now
-    if s.device != device:
-        raise ValueError(f"the stream belongs to {s.device}, the tensors to {device}")
-    here = s == now and torch.cuda.current_device() == device.index
-    return (contextlib.nullcontext() if here else torch.cuda.stream(s)), s
+    return torch.cuda.stream(stream), stream.cuda_stream, (None if now == stream else now)
 
 
-def _new(like_stream, caller_stream, shape, dtype, device):
-    """A tensor of the call's stream that the caller's current stream may also use."""
+def _new(shape, dtype, device, share):
+    """A tensor of the call's stream; `share`: the caller's stream, which may use it too."""
     t = torch.empty(shape, dtype=dtype, device=device)
-    if caller_stream != like_stream:
-        t.record_stream(caller_stream)
+    if share is not None:
+        t.record_stream(share)
     return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _page_stride(fn, name, t):
     """Pages may lie apart (a pool that interleaves K and V); a page itself is dense."""
-    if t.dim() != 4:
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{fn}: {name} must be [n_pages, page_size, h_kv, d]")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{fn}: {name} must be {_BF16}, not {t.dtype}")
     n, p, h, d = t.shape
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{fn}: {name} must be {torch.bfloat16}, not {t.dtype}")
-    if t.stride(3) != 1 or (h > 1 and t.stride(2) != d) or (p > 1 and t.stride(1) != h * d):
+    s = t.stride()
+    if s[3] != 1 or (h > 1 and s[2] != d) or (p > 1 and s[1] != h * d):
         raise ValueError(f"{fn}: the rows of a page of {name} must be dense")
-    return t.stride(0) if n > 1 else p * h * d
+    return s[0] if n > 1 else p * h * d
 
 
 def _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n_seqs, weights=None):
     """(struct, page_size, h_kv, d) of a paged cache."""
     stride = _page_stride(fn, "k_pages", k_pages)
-    n_pages, page, h_kv, d = k_pages.shape
-    if v_pages is not None:
-        if _page_stride(fn, "v_pages", v_pages) != stride or v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    n_pages, page, h_kv, d = shape
+    if v_pages is not None and v_pages is not k_pages:
+        if _page_stride(fn, "v_pages", v_pages) != stride or v_pages.shape != shape:
             raise ValueError(f"{fn}: v_pages must have the shape and strides of k_pages")
         if v_pages.device != k_pages.device:
             raise ValueError(f"{fn}: v_pages is on {v_pages.device}, k_pages on {k_pages.device}")
-    i32 = torch.int32
-    _expect(fn, k_pages.device, block_table=(block_table, i32, (n_seqs, None)), cache_lens=(cache_lens, i32, (n_seqs,)),
-            weights=(weights, torch.float32, (n_pages, h_kv, page)))
-    c = NsaPagedCache()
-    c.k_pages = k_pages.data_ptr()
-    c.v_pages = None if v_pages is None else v_pages.data_ptr()
-    c.weights = None if weights is None else weights.data_ptr()
-    c.block_table, c.cache_lens = block_table.data_ptr(), cache_lens.data_ptr()
-    c.n_pages, c.page_size, c.max_pages, c.page_stride = n_pages, page, block_table.shape[1], stride
-    return c, page, h_kv, d
+    index = k_pages.get_device()
+    width = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    if (block_table is None or cache_lens is None or not _fits(block_table, _I32, (n_seqs, width), index)
+            or not _fits(cache_lens, _I32, (n_seqs,), index)
+            or not _fits(weights, _F32, (n_pages, h_kv, page), index)):
+        if block_table is None or cache_lens is None:
+            raise TypeError(f"{fn}: block_table and cache_lens must be tensors")
+        _expect(fn, k_pages.device, block_table=(block_table, _I32, (n_seqs, None)),
+                cache_lens=(cache_lens, _I32, (n_seqs,)), weights=(weights, _F32, (n_pages, h_kv, page)))
+    return (NsaPagedCache(k_pages.data_ptr(), _addr(v_pages), _addr(weights), block_table.data_ptr(),
+                          cache_lens.data_ptr(), n_pages, page, width, stride), page, h_kv, d)
 
 
 def _span_shape(fn, q, h_kv, d, device, cu_seqlens, max_seqlen):
-    """(flat q, shape) of new tokens [B, T, H, d] or packed [tokens, H, d]."""
-    if q.dim() not in (3, 4) or q.shape[-1] != d or q.shape[-2] % h_kv:
-        raise ValueError(f"{fn}: expected [..., heads, {d}] with heads a multiple of {h_kv}, got {tuple(q.shape)}")
-    if q.dim() == 4 and cu_seqlens is not None:
+    """(tokens, shape struct, number of sequences) of new tokens [B, T, H, d] or packed
+    [tokens, H, d]."""
+    dims = q.shape if isinstance(q, torch.Tensor) else ()
+    if len(dims) not in (3, 4) or dims[-1] != d or dims[-2] % h_kv:
+        raise ValueError(f"{fn}: expected [..., heads, {d}] with heads a multiple of {h_kv}, got {tuple(dims)}")
+    index = device.index if device.type == "cuda" else -1
+    if not _fits(q, _BF16, dims, index):
+        _expect(fn, device, tokens=(q, _BF16, dims))
+    if cu_seqlens is None:
+        B, T = (dims[0], dims[1]) if len(dims) == 4 else (1, dims[0])
+        return B * T, NsaShape(B, T, None, 0, B * T, dims[-2], h_kv, d, NSA_BF16), B
+    if len(dims) == 4:
         raise ValueError(f"{fn}: with cu_seqlens the tokens are packed [tokens, heads, d]")
-    _expect(fn, device, tokens=(q, torch.bfloat16, q.shape), cu_seqlens=(cu_seqlens, torch.int32, (None,)))
-    if cu_seqlens is not None and cu_seqlens.numel() < 2:
+    n = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
+    if n < 1 or not _fits(cu_seqlens, _I32, (n + 1,), index):
+        _expect(fn, device, cu_seqlens=(cu_seqlens, _I32, (None,)))
         raise ValueError(f"{fn}: cu_seqlens needs at least two entries")
-    return _shape_for(q, h_kv, cu_seqlens, max_seqlen)
-
-
-def _n_seqs(shp):
-    return shp.n_seqs if shp.cu_seqlens else shp.batch
+    if max_seqlen is None:
+        raise ValueError(f"{fn}: cu_seqlens needs max_seqlen")
+    return dims[0], NsaShape(0, int(max_seqlen), cu_seqlens.data_ptr(), n, dims[0], dims[1], h_kv, d, NSA_BF16), n
 
 
 def nsa_paged_append(k_new, v_new, k_pages, v_pages, block_table, cache_lens, *, weights=None, cu_seqlens=None,
@@ -708,18 +736,31 @@ def nsa_paged_append(k_new, v_new, k_pages, v_pages, block_table, cache_lens, *,
     """New tokens' keys and values [B, T, Hkv, d] or packed [tokens, Hkv, d] into the cache, at the
     last positions of cache_lens; the weights of the written positions become 0."""
     fn = "nsa_paged_append"
-    ctx, s = _on(k_pages.device, stream)
-    kf, shp = _span_shape(fn, k_new, k_pages.shape[-2], k_pages.shape[-1], k_pages.device, cu_seqlens, max_seqlen)
-    if k_new.shape[-2] != k_pages.shape[-2]:
-        raise ValueError(f"{fn}: k_new has {k_new.shape[-2]} heads, the cache {k_pages.shape[-2]}")
-    _expect(fn, k_pages.device, v_new=(v_new, torch.bfloat16, k_new.shape))
-    c, *_ = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, _n_seqs(shp), weights)
+    dev = k_pages.device
+    ctx, raw, _ = _on(dev, stream)
+    _, shp, n = _span_shape(fn, k_new, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n, weights)[0]
+    if v_new is None or k_new.shape[-2] != k_pages.shape[-2] or not _fits(v_new, _BF16, k_new.shape, dev.index):
+        want = (*k_new.shape[:-2], *k_pages.shape[-2:])
+        _expect(fn, dev, k_new=(k_new, _BF16, want), v_new=(v_new, _BF16, want))
+        raise TypeError(f"{fn}: v_new must be a tensor")
     with ctx:
-        _check(load().nsa_paged_append(ctypes.byref(shp), _ptr(kf), _ptr(v_new), ctypes.byref(c), _stream(s)), fn)
+        rc = load().nsa_paged_append(ctypes.byref(shp), k_new.data_ptr(), v_new.data_ptr(), ctypes.byref(c), raw)
+    if rc:
+        _check(rc, fn)
 
 
 def nsa_paged_attn_fwd_workspace_size(shape: NsaShape, max_cache_len: int = 0, window: int = 0, n_sink: int = 0) -> int:
     return int(load().nsa_paged_attn_fwd_workspace_size(ctypes.byref(shape), max_cache_len, window, n_sink))
+
+
+def _scratch(fn, workspace, need, dev, index):
+    """(tensor to keep alive, its address, its bytes) of a call's workspace."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=_U8, device=dev) if need else None
+    elif not _fits(workspace, _U8, workspace.shape if workspace.dim() == 1 else (0,), index):
+        _expect(fn, dev, workspace=(workspace, _U8, (None,)))
+    return workspace, _addr(workspace), 0 if workspace is None else workspace.numel()
 
 
 def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n_sink=0, scale=0.0, *, cu_seqlens=None,
@@ -729,20 +770,24 @@ def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n
     visible beside it.  Returns out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_paged_attn_fwd"
     dev = k_pages.device
-    ctx, s = _on(dev, stream)
-    qf, shp = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
-    c, page, _, _ = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, _n_seqs(shp))
-    _expect(fn, dev, out=(out, torch.bfloat16, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
-            workspace=(workspace, torch.uint8, (None,)))
+    ctx, raw, share = _on(dev, stream)
+    tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c, page, _, _ = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n)
+    rows = (tokens, q.shape[-2])
+    if not _fits(out, _BF16, q.shape, dev.index) or not _fits(lse, _F32, rows, dev.index):
+        _expect(fn, dev, out=(out, _BF16, q.shape), lse=(lse, _F32, rows))
     if max_cache_len is None:
-        max_cache_len = block_table.shape[1] * page
-    now = torch.cuda.current_stream(dev)
+        max_cache_len = c.max_pages * page
+    lib, sp = load(), ctypes.byref(shp)
     with ctx:
-        out = _new(s, now, q.shape, q.dtype, dev) if out is None else out
-        ws = _workspace(nsa_paged_attn_fwd_workspace_size(shp, max_cache_len, window, n_sink), dev, workspace)
-        _check(load().nsa_paged_attn_fwd(ctypes.byref(shp), _ptr(qf), ctypes.byref(c), max_cache_len, window, n_sink,
-                                         float(scale), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
-                                         _stream(s)), fn)
+        if out is None:
+            out = _new(q.shape, _BF16, dev, share)
+        need = 0 if workspace is not None else lib.nsa_paged_attn_fwd_workspace_size(sp, max_cache_len, window, n_sink)
+        ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
+        rc = lib.nsa_paged_attn_fwd(sp, q.data_ptr(), ctypes.byref(c), max_cache_len, window, n_sink, scale,
+                                    out.data_ptr(), _addr(lse), at, size, raw)
+    if rc:
+        _check(rc, fn)
     return out
 
 
@@ -753,17 +798,20 @@ def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n
     Without weights the sum alone; out may be weights (the default when weights are given)."""
     fn = "nsa_paged_attn_weights"
     dev = k_pages.device
-    ctx, s = _on(dev, stream)
-    qf, shp = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
-    c, page, h_kv, _ = _paged_cache(fn, k_pages, None, block_table, cache_lens, _n_seqs(shp), weights)
-    _expect(fn, dev, lse=(lse, torch.float32, qf.shape[:2]),
-            out=(out, torch.float32, (k_pages.shape[0], h_kv, page)))
-    now = torch.cuda.current_stream(dev)
+    ctx, raw, share = _on(dev, stream)
+    tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c, page, h_kv, _ = _paged_cache(fn, k_pages, None, block_table, cache_lens, n, weights)
+    rows, cells = (tokens, q.shape[-2]), (k_pages.shape[0], h_kv, page)
+    if lse is None or not _fits(lse, _F32, rows, dev.index) or not _fits(out, _F32, cells, dev.index):
+        _expect(fn, dev, lse=(lse, _F32, rows), out=(out, _F32, cells))
+        raise TypeError(f"{fn}: lse must be a tensor")
     with ctx:
         if out is None:
-            out = weights if weights is not None else _new(s, now, (k_pages.shape[0], h_kv, page), torch.float32, dev)
-        _check(load().nsa_paged_attn_weights(ctypes.byref(shp), _ptr(qf), ctypes.byref(c), _ptr(lse), window, n_sink,
-                                             float(scale), float(decay), _ptr(out), _stream(s)), fn)
+            out = weights if weights is not None else _new(cells, _F32, dev, share)
+        rc = load().nsa_paged_attn_weights(ctypes.byref(shp), q.data_ptr(), ctypes.byref(c), lse.data_ptr(), window,
+                                           n_sink, scale, decay, out.data_ptr(), raw)
+    if rc:
+        _check(rc, fn)
     return out
 
 
@@ -774,20 +822,28 @@ def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_tabl
     budget] int32, -1 padded, and new_lens [n_seqs] int32)."""
     fn = "nsa_paged_evict"
     dev = k_pages.device
-    ctx, s = _on(dev, stream)
-    n = cache_lens.shape[0]
+    ctx, raw, share = _on(dev, stream)
     if weights is None:
         raise ValueError(f"{fn}: the cache has no weights")
+    if not isinstance(cache_lens, torch.Tensor) or cache_lens.dim() != 1:
+        raise ValueError(f"{fn}: cache_lens must be [n_seqs]")
+    n = cache_lens.shape[0]
     c, _, h_kv, d = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n, weights)
-    i32 = torch.int32
-    _expect(fn, dev, new_table=(new_table, i32, (n, None)), keep=(keep, i32, (n, h_kv, budget)),
-            new_lens=(new_lens, i32, (n,)))
-    now = torch.cuda.current_stream(dev)
+    width = new_table.shape[1] if isinstance(new_table, torch.Tensor) and new_table.dim() == 2 else 0
+    kept = (n, h_kv, budget)
+    if (new_table is None or not _fits(new_table, _I32, (n, width), dev.index)
+            or not _fits(keep, _I32, kept, dev.index) or not _fits(new_lens, _I32, (n,), dev.index)):
+        _expect(fn, dev, new_table=(new_table, _I32, (n, None)), keep=(keep, _I32, kept), new_lens=(new_lens, _I32, (n,)))
+        raise TypeError(f"{fn}: new_table must be a tensor")
     with ctx:
-        keep = _new(s, now, (n, h_kv, max(0, budget)), i32, dev) if keep is None else keep
-        new_lens = _new(s, now, (n,), i32, dev) if new_lens is None else new_lens
-        _check(load().nsa_paged_evict(n, h_kv, d, ctypes.byref(c), budget, n_sink, n_recent, _ptr(new_table),
-                                      new_table.shape[1], _ptr(keep), _ptr(new_lens), _stream(s)), fn)
+        if keep is None:
+            keep = _new((n, h_kv, max(0, budget)), _I32, dev, share)
+        if new_lens is None:
+            new_lens = _new((n,), _I32, dev, share)
+        rc = load().nsa_paged_evict(n, h_kv, d, ctypes.byref(c), budget, n_sink, n_recent, new_table.data_ptr(), width,
+                                    keep.data_ptr(), new_lens.data_ptr(), raw)
+    if rc:
+        _check(rc, fn)
     return keep, new_lens
 
 
@@ -797,11 +853,16 @@ def nsa_swa_sink_fwd_workspace_size(shape: NsaShape, window: int = 512, n_sink: 
 
 
 def _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen):
-    if k.dim() != q.dim() or q.dim() not in (3, 4):
+    """_span_shape of q, with k and v checked against it."""
+    if not isinstance(k, torch.Tensor) or k.dim() != q.dim() or q.dim() not in (3, 4) or k.shape[-2] == 0:
         raise ValueError(f"{fn}: q and k must both be [B, T, heads, d] or packed [tokens, heads, d]")
+    r = _span_shape(fn, q, k.shape[-2], q.shape[-1], q.device, cu_seqlens, max_seqlen)
     kv = (*q.shape[:-2], k.shape[-2], q.shape[-1])
-    _expect(fn, q.device, k=(k, torch.bfloat16, kv), v=(v, torch.bfloat16, kv))
-    return _span_shape(fn, q, k.shape[-2], q.shape[-1], q.device, cu_seqlens, max_seqlen)
+    index = q.get_device()
+    if v is None or not _fits(k, _BF16, kv, index) or not _fits(v, _BF16, kv, index):
+        _expect(fn, q.device, k=(k, _BF16, kv), v=(v, _BF16, kv))
+        raise TypeError(f"{fn}: v must be a tensor")
+    return r
 
 
 def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=None, max_seqlen=None, workspace=None,
@@ -809,16 +870,22 @@ def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=Non
     """Sliding window beside which the first n_sink tokens of each sequence stay visible.  Returns
     out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_swa_sink_fwd"
-    ctx, s = _on(q.device, stream)
-    qf, shp = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
-    _expect(fn, q.device, out=(out, torch.bfloat16, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
-            workspace=(workspace, torch.uint8, (None,)))
-    now = torch.cuda.current_stream(q.device)
+    dev = q.device
+    ctx, raw, share = _on(dev, stream)
+    tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
+    rows = (tokens, q.shape[-2])
+    if not _fits(out, _BF16, q.shape, dev.index) or not _fits(lse, _F32, rows, dev.index):
+        _expect(fn, dev, out=(out, _BF16, q.shape), lse=(lse, _F32, rows))
+    lib, sp = load(), ctypes.byref(shp)
     with ctx:
-        out = _new(s, now, q.shape, q.dtype, q.device) if out is None else out
-        ws = _workspace(nsa_swa_sink_fwd_workspace_size(shp, window, n_sink), q.device, workspace)
-        _check(load().nsa_swa_sink_fwd(ctypes.byref(shp), _ptr(qf), _ptr(k), _ptr(v), window, n_sink, float(scale),
-                                       _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(s)), fn)
+        if out is None:
+            out = _new(q.shape, _BF16, dev, share)
+        need = 0 if workspace is not None else lib.nsa_swa_sink_fwd_workspace_size(sp, window, n_sink)
+        ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
+        rc = lib.nsa_swa_sink_fwd(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), window, n_sink, scale, out.data_ptr(),
+                                  _addr(lse), at, size, raw)
+    if rc:
+        _check(rc, fn)
     return out
 
 
@@ -831,18 +898,26 @@ def nsa_swa_sink_bwd(q, k, v, o, lse, d_o, window=512, n_sink=4, scale=0.0, *, c
     """Backward of nsa_swa_sink_fwd: (dq, dk, dv) shaped like q, k, v from its o and lse."""
     fn = "nsa_swa_sink_bwd"
     dev = q.device
-    ctx, s = _on(dev, stream)
-    qf, shp = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
-    b = torch.bfloat16
-    _expect(fn, dev, o=(o, b, q.shape), d_o=(d_o, b, q.shape), lse=(lse, torch.float32, qf.shape[:2]),
-            dq=(dq, b, q.shape), dk=(dk, b, k.shape), dv=(dv, b, k.shape), workspace=(workspace, torch.uint8, (None,)))
-    now = torch.cuda.current_stream(dev)
+    ctx, raw, share = _on(dev, stream)
+    tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
+    rows = (tokens, q.shape[-2])
+    like_q, like_k = q.shape, k.shape
+    if (o is None or d_o is None or lse is None
+            or not all(_fits(t, _BF16, like_q, dev.index) for t in (o, d_o, dq))
+            or not all(_fits(t, _BF16, like_k, dev.index) for t in (dk, dv)) or not _fits(lse, _F32, rows, dev.index)):
+        _expect(fn, dev, o=(o, _BF16, like_q), d_o=(d_o, _BF16, like_q), lse=(lse, _F32, rows), dq=(dq, _BF16, like_q),
+                dk=(dk, _BF16, like_k), dv=(dv, _BF16, like_k))
+        raise TypeError(f"{fn}: o, lse and d_o must be tensors")
+    lib, sp = load(), ctypes.byref(shp)
     with ctx:
-        dq = _new(s, now, q.shape, b, dev) if dq is None else dq
-        dk = _new(s, now, k.shape, b, dev) if dk is None else dk
-        dv = _new(s, now, v.shape, b, dev) if dv is None else dv
-        ws = _workspace(nsa_swa_sink_bwd_workspace_size(shp, window, n_sink), dev, workspace)
-        _check(load().nsa_swa_sink_bwd(ctypes.byref(shp), _ptr(qf), _ptr(k), _ptr(v), window, n_sink, float(scale),
-                                       _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
-                                       0 if ws is None else ws.numel(), _stream(s)), fn)
+        dq = _new(like_q, _BF16, dev, share) if dq is None else dq
+        dk = _new(like_k, _BF16, dev, share) if dk is None else dk
+        dv = _new(like_k, _BF16, dev, share) if dv is None else dv
+        need = 0 if workspace is not None else lib.nsa_swa_sink_bwd_workspace_size(sp, window, n_sink)
+        ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
+        rc = lib.nsa_swa_sink_bwd(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), window, n_sink, scale, o.data_ptr(),
+                                  lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), at, size,
+                                  raw)
+    if rc:
+        _check(rc, fn)
     return dq, dk, dv

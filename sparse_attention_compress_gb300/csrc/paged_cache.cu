@@ -37,6 +37,10 @@ __global__ void __launch_bounds__(256) append_kernel(Seqs s, Keys c, const uint4
 // ---------------------------------------------------------------------------- evict
 constexpr int kSelThreads = 1024;
 constexpr int kSelCached = 49152;  // keys whose ranks shared memory holds (192 KB)
+// Copies of the histogram: a warp's lanes count into the copy of their lane % 4, since many
+// keys share a digit (weights within a few octaves, or zeros) and counts of one address are
+// taken one after another.
+constexpr int kCopies = 4, kHistBytes = 2048 * kCopies * 4;
 
 // Order of a weight as an unsigned key: larger weights have larger keys, -0 equals +0, NaN
 // (and a key in a missing page) is the lowest.
@@ -48,19 +52,22 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 
 // The `budget` keys of one (sequence, kv-head) that stay, ascending: the first n_sink, the
 // last n_recent, and the best of the others by weight (equal weights: the lower index).
-// A radix selection on 8-bit digits (four counting passes) finds the rank of the last key
-// that stays and how many keys of exactly that rank do; then every warp takes a contiguous
-// run of keys, counts what it keeps, and after one scan over the warps writes its run in
-// order.  Counting in shared-memory integers, so the result is the same on every run.
+// A radix selection on 11, 11 and 10 bits (three counting passes, the first while the
+// weights are read; 43 us for 64 caches of 16384 to 32768 keys with four passes of 8 bits)
+// finds the rank of the last key that stays and how many keys of exactly that rank do; then
+// every warp takes a contiguous run of keys, counts what it keeps, and after one scan over
+// the warps writes its run in order.  Counting in shared-memory integers, so the result is
+// the same on every run.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const float* __restrict__ weights, int hkv,
                                                                    int budget, int n_sink, int n_recent, int room,
                                                                    int32_t* __restrict__ keep) {
-  extern __shared__ uint32_t s_rank[];
-  __shared__ int s_hist[256], s_gt[32], s_eq[32];
+  extern __shared__ int s_hist[];  // [2048][kCopies], then the ranks
+  __shared__ int s_gt[32], s_eq[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
   const int seq = blockIdx.x, g = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* s_rank = reinterpret_cast<uint32_t*>(s_hist + 2048 * kCopies);
   const int L = cached_len(c, seq);
   int32_t* out = keep + ((int64_t)seq * hkv + g) * budget;
   if (L <= budget) {  // everything stays
@@ -69,49 +76,75 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
   }
   const int page = 1 << c.page_log2;
   const bool cached = L <= room;  // the ranks fit the launch's shared memory
-  auto rank = [&](int i) -> uint32_t {
-    if (i < n_sink || i >= L - n_recent) return 0xffffffffu;  // above +inf
+  // (no branches: the loads of several keys have to be in flight together)
+  auto place = [&](int i) -> int64_t {  // of key i's weight (-1: in no page)
     const int pid = page_of(c, seq, i);
-    return pid < 0 ? 0u : rank_of(__ldg(weights + (((int64_t)pid * hkv + g) << c.page_log2) + (i & (page - 1))));
+    return pid < 0 ? -1 : (((int64_t)pid * hkv + g) << c.page_log2) + (i & (page - 1));
   };
-  if (cached) {
-#pragma unroll 4
-    for (int i = tid; i < L; i += kSelThreads) s_rank[i] = rank(i);
-  }
+  auto order = [&](int i, int64_t at, float w) -> uint32_t {
+    const uint32_t r = at < 0 ? 0u : rank_of(w);
+    return i < n_sink || i >= L - n_recent ? 0xffffffffu : r;  // above +inf
+  };
+  auto rank = [&](int i) -> uint32_t {
+    const int64_t at = place(i);
+    return order(i, at, __ldg(weights + (at < 0 ? 0 : at)));
+  };
   auto get = [&](int i) { return cached ? s_rank[i] : rank(i); };
   uint32_t prefix = 0;
   int left = budget;  // keys still to take among those that match the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = tid; i < L; i += kSelThreads) {
-      const uint32_t r = get(i);
-      if ((r & mask) == prefix) atomicAdd(&s_hist[(r >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {  // the digit of the last key that stays, from the top
-      int sum = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass < 2 ? 2048 : 1024;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += s_hist[255 - (lane * 8 + e)];
-      int incl = sum;
+    for (int i = 0; i < 2048 * kCopies / kSelThreads; ++i) s_hist[tid + i * kSelThreads] = 0;
+    __syncthreads();
+    if (pass == 0) {
+      constexpr int U = 8;  // weights in flight a thread
+      for (int b = 0; b < L; b += U * kSelThreads) {
+        int64_t at[U];
+        uint32_t r[U];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      int before = incl - sum;
-      if (before < left && incl >= left) {
-        for (int e = 0; e < 8; ++e) {
-          const int dgt = 255 - (lane * 8 + e), n = s_hist[dgt];
-          if (before + n >= left) {
-            s_prefix = prefix | ((uint32_t)dgt << shift);
-            s_left = left - before;
-            break;
+        for (int u = 0; u < U; ++u) at[u] = place(min(b + u * kSelThreads + tid, L - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          r[u] = order(b + u * kSelThreads + tid, at[u], __ldg(weights + (at[u] < 0 ? 0 : at[u])));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = b + u * kSelThreads + tid;
+          if (i < L) {
+            if (cached) s_rank[i] = r[u];
+            atomicAdd(&s_hist[(r[u] >> 21) * kCopies + lane % kCopies], 1);
           }
-          before += n;
         }
       }
+    } else {
+      const uint32_t mask = pass == 1 ? 0xffe00000u : 0xfffffc00u;
+#pragma unroll 8
+      for (int i = tid; i < L; i += kSelThreads) {
+        const uint32_t r = get(i);
+        if ((r & mask) == prefix) atomicAdd(&s_hist[((r >> shift) & (digits - 1)) * kCopies + lane % kCopies], 1);
+      }
+    }
+    __syncthreads();
+    // the digit of the last key that stays, from the top: thread tid has digits 2047 - 2 tid
+    // and 2046 - 2 tid
+    const int d0 = 2047 - 2 * tid;
+    const int4 c0 = reinterpret_cast<const int4*>(s_hist)[d0], c1 = reinterpret_cast<const int4*>(s_hist)[d0 - 1];
+    const int h0 = c0.x + c0.y + c0.z + c0.w, sum = h0 + c1.x + c1.y + c1.z + c1.w;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_gt[warp] = incl;
+    __syncthreads();
+    const int others = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+    const int before = others + incl - sum;
+    if (before < left && before + sum >= left) {
+      const bool second = before + h0 < left;
+      s_prefix = prefix | ((uint32_t)(d0 - second) << shift);
+      s_left = left - before - (second ? h0 : 0);
     }
     __syncthreads();
     prefix = s_prefix;
@@ -120,6 +153,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
   // keys of rank > prefix stay, and the first `left` of rank == prefix
   const int run = (L + 31) / 32, i0 = min(L, warp * run), i1 = min(L, i0 + run);
   int gt = 0, eq = 0;
+#pragma unroll 8
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t r = get(i);
     gt += r > prefix;
@@ -138,16 +172,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
     ties += s_eq[w];
   }
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int b = i0; b < i1; b += 32) {
     const int i = b + lane;
     const uint32_t r = i < i1 ? get(i) : 0u;
-    const bool tie = i < i1 && r == prefix;
-    const uint32_t mt = __ballot_sync(0xffffffffu, tie);
-    const bool stay = i < i1 && (r > prefix || (tie && ties + __popc(mt & below) < left));
-    const uint32_t ms = __ballot_sync(0xffffffffu, stay);
-    if (stay) out[at + __popc(ms & below)] = i;
-    at += __popc(ms);
-    ties += __popc(mt);
+    uint32_t stay = __ballot_sync(0xffffffffu, i < i1 && r > prefix);
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < i1 && r == prefix);
+    if (tie && ties < left) {  // the first left - ties of them
+      const int room_left = left - ties;
+      const bool in = ((tie >> lane) & 1u) && __popc(tie & below) < room_left;
+      stay |= __ballot_sync(0xffffffffu, in);
+    }
+    if ((stay >> lane) & 1u) out[at + __popc(stay & below)] = i;
+    at += __popc(stay);
+    ties += __popc(tie);
   }
 }
 
@@ -207,9 +245,9 @@ cudaError_t launch_paged_evict(int n_seqs, const PagedView& cache, const PagedVi
   const span::Keys c = span::keys_of(&cache, k_pages, v_pages), t = span::keys_of(&to, k_pages, v_pages);
   const int room = (int)std::min<int64_t>(span::kSelCached, (int64_t)cache.max_pages << cache.page_log2);
   cudaError_t e = cudaFuncSetAttribute(span::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       span::kSelCached * 4);
+                                       span::kSelCached * 4 + span::kHistBytes);
   if (e != cudaSuccess) return e;
-  span::evict_select_kernel<<<dim3(n_seqs, hkv), span::kSelThreads, room * 4, st>>>(c, weights, hkv, budget, n_sink,
+  span::evict_select_kernel<<<dim3(n_seqs, hkv), span::kSelThreads, span::kHistBytes + room * 4, st>>>(c, weights, hkv, budget, n_sink,
                                                                                    n_recent, room, keep);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int per = 256 / (d / 8);

@@ -205,7 +205,7 @@ def test_python_checks():
                               bad.get("lens", lens), 2, bad.get("w"))
     q = torch.zeros(5, 4, 64, dtype=bf)
     cu = torch.zeros(3, dtype=i32)
-    assert _lib._span_shape("f", q, 2, 64, q.device, cu, 3)[1].n_seqs == 2
+    assert _lib._span_shape("f", q, 2, 64, q.device, cu, 3)[2] == 2
     for args in ((q.float(), cu), (q[:, :3], cu), (q[..., :32], cu), (q[:, ::2], cu), (q, cu.long()), (q, cu[:1]),
                  (q[None], cu)):
         with pytest.raises((TypeError, ValueError)):
