@@ -8,10 +8,12 @@
 // tile's rows), so that a TMEM lane is a key and the sum over queries needs no exchange
 // between threads.  One operand of a CTA stays and the other streams through a ring:
 //   many rows   128 keys stay, the query tiles that see them stream: bound by the tensor
-//               cores and the exponentials, which two CTAs an SM overlap.
+//               cores and the exponentials.  Four groups of summing warps take the tiles in
+//               turn, each with an S buffer of its own, and add their sums at the end.
 //   FEW         (the queries of a sequence fit one tile) the queries stay and a run of key
-//               tiles streams: bound by HBM; two CTAs an SM.
-// Roles: warps 0-3 sum (one key a thread), warp 4 loads, warp 5 issues.
+//               tiles streams: bound by HBM; one group, two CTAs an SM.
+// Roles: groups of four warps sum (one key a thread), then a warp that loads and one that
+// issues the products.
 #include <algorithm>
 
 #include "launch.h"
@@ -19,8 +21,6 @@
 
 namespace nsa {
 namespace span {
-
-constexpr int kWThreads = 192;
 
 struct WeightParams {
   Seqs seqs;
@@ -37,19 +37,23 @@ struct WeightParams {
 template <int D, bool FEW>
 struct WCfg {
   static constexpr int K_BYTES = KT * D * 2;
-  static constexpr int NS = FEW ? (D == 64 ? 6 : 3) : 2;  // slots of the streamed operand
+  static constexpr int NS = FEW ? (D == 64 ? 6 : 3) : 4;  // slots of the streamed operand
+  static constexpr int NG = FEW ? 1 : 4;                  // groups of summing warps
+  static constexpr int NB = FEW ? 2 : 4;                  // S buffers: item i in i % NB, summed by group i % NG
+  static constexpr int THREADS = (4 * NG + 2) * 32;
 };
 
 template <int D, bool FEW>
-__global__ void __launch_bounds__(kWThreads, 2)
+__global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
     weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_k16, const WeightParams p) {
   using C = WCfg<D, FEW>;
-  constexpr int NS = C::NS;
-  enum : int { FIXED = 0, FULL = 1, EMPTY = FULL + NS, SFULL = EMPTY + NS, SFREE = SFULL + 2, DRAIN = SFREE + 2, COUNT };
+  constexpr int NS = C::NS, NG = C::NG, NB = C::NB, kLoad = 4 * NG, kIssue = kLoad + 1;
+  enum : int { FIXED = 0, FULL = 1, EMPTY = FULL + NS, SFULL = EMPTY + NS, SFREE = SFULL + NB, DRAIN = SFREE + NB, COUNT };
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ __align__(16) float s_lse[FEW ? 1 : 4][ROWS];  // minus the base-2 lse of tile i's rows, at i % 4
+  __shared__ __align__(16) float s_lse[4 * NG][ROWS];  // by summing warp: minus the base-2 lse of its tile's rows
+  __shared__ float s_sum[NG][ROWS];                    // the groups' sums (many rows)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       tc::mbar_init(bar(FULL + i), 1);
       tc::mbar_init(bar(EMPTY + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       tc::mbar_init(bar(SFULL + i), 1);
       tc::mbar_init(bar(SFREE + i), 4);  // one arrival a summing warp
     }
@@ -92,27 +96,24 @@ __global__ void __launch_bounds__(kWThreads, 2)
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  // minus the base-2 lse of row e of query tile t (-inf for a row of no query or without keys,
-  // so that it adds 0)
-  auto row_lse = [&](int t, int e) {
-    float le = kNegInf;
-    if (e < p.tpc * p.R && t + e / p.R < Lq) {
-      le = -__ldg(p.lse + (start + t + e / p.R) * p.h + g * p.R + e % p.R) * kLog2e;
-      if (le == -kNegInf) le = kNegInf;
-    }
-    return le;
+  auto place = [&](int key) -> int64_t {  // of the key's weight, or -1 (no key, or in no page)
+    if (key >= kv_len) return -1;
+    const int pid = page_of(p.keys, seq, key);
+    return pid < 0 ? -1 : (((int64_t)pid * p.hkv + g) << p.keys.page_log2) + (key & ((1 << p.keys.page_log2) - 1));
   };
-  if (warp == 5) {
+  auto finish = [&](float sum, float before, int64_t at) {
+    if (at >= 0) p.w_out[at] = p.w_in ? fmaf(p.decay, before, sum) : sum;
+  };
+  if (warp == kIssue) {
     tmem_alloc(smem_u32(&s_tmem), p.tmem_cols);
     tc::fence_before();
   }
-  if (FEW && warp < 4) s_lse[0][tid] = row_lse(0, tid);
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
   int last_item = -1;
-  if (warp == 4) {
+  if (warp == kLoad) {
     // ------------------------------------------------------------------ loads
     auto load_q = [&](uint32_t to, int t, uint32_t full) {
       if (lane == 0) {
@@ -130,21 +131,11 @@ __global__ void __launch_bounds__(kWThreads, 2)
     if (any && !FEW) load_k(fixed_s, fkey0, bar(FIXED));
     int slot = 0;
     uint32_t phase = 1;
-    float nl[ROWS / 32];  // lse of a tile's rows, four a lane, fetched a tile ahead
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int e = 0; e < ROWS / 32; ++e) nl[e] = row_lse(t, lane + e * 32);
-    };
-    if (!FEW) fetch(t_lo);
     for (int i = 0; any && i < n; ++i) {
       if (i >= NS && !wait(bar(EMPTY + slot), phase)) break;
       if (FEW) {
         load_k(ring_s + slot * slot_bytes, (kt0 + i) * KT, bar(FULL + slot));
       } else {
-#pragma unroll
-        for (int e = 0; e < ROWS / 32; ++e) s_lse[i & 3][lane + e * 32] = nl[e];
-        if (i + 1 < n) fetch(t_lo + (i + 1) * p.tpc);
-        __syncwarp();
         load_q(ring_s + slot * slot_bytes, t_lo + i * p.tpc, bar(FULL + slot));
       }
       last_item = i;
@@ -153,15 +144,15 @@ __global__ void __launch_bounds__(kWThreads, 2)
         phase ^= 1u;
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kIssue) {
     // ------------------------------------------------------------------ products
     bool ok = !any || wait(bar(FIXED), 0);
     const uint32_t lead = elect(), id = tc::idesc(KT, p.cols), fixed_d = desc_k(fixed_s), ring_d = desc_k(ring_s);
     int slot = 0;
     uint32_t phase = 0;
     for (int i = 0; ok && any && i < n; ++i) {
-      const int b = i & 1;
-      if (i >= 2 && !(ok = wait(bar(SFREE + b), ((i >> 1) - 1) & 1))) break;
+      const int b = i % NB;
+      if (i >= NB && !(ok = wait(bar(SFREE + b), (i / NB - 1) & 1))) break;
       if (!(ok = wait(bar(FULL + slot), phase))) break;
       tc::fence_after();
       const uint32_t at = ring_d + slot * (slot_bytes >> 4);
@@ -179,20 +170,30 @@ __global__ void __launch_bounds__(kWThreads, 2)
     }
   } else {
     // ------------------------------------------------------------------ sums, one key a thread
-    const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    const int row = tid & 127;  // the thread's key of a tile
+    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
     float acc = 0.f;
     bool ok = true;
-    auto finish = [&](float sum, float before, int64_t at) {
-      if (at >= 0) p.w_out[at] = p.w_in ? fmaf(p.decay, before, sum) : sum;
+    // minus the base-2 lse of a query tile's rows (-inf for a row of no query or without keys,
+    // so that it adds 0), four a lane, fetched a turn of the group ahead
+    float nl[ROWS / 32];
+    int tok[ROWS / 32], ofs[ROWS / 32];
+#pragma unroll
+    for (int e = 0; e < ROWS / 32; ++e) {
+      const int r = lane + e * 32;
+      tok[e] = r < p.tpc * p.R ? r / p.R : 1 << 30;
+      ofs[e] = r / p.R * p.h + r % p.R;
+    }
+    auto fetch = [&](int i) {
+      const int t = FEW ? 0 : t_lo + i * p.tpc;
+      const float* src = p.lse + (start + t) * p.h + g * p.R;
+#pragma unroll
+      for (int e = 0; e < ROWS / 32; ++e) nl[e] = any && i < n && tok[e] < Lq - t ? __ldg(src + ofs[e]) : kNegInf;
     };
-    auto place = [&](int key) -> int64_t {  // the key's weight, or -1 (no key, or in no page)
-      if (key >= kv_len) return -1;
-      const int pid = page_of(p.keys, seq, key);
-      return pid < 0 ? -1 : (((int64_t)pid * p.hkv + g) << p.keys.page_log2) + (key & ((1 << p.keys.page_log2) - 1));
-    };
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1, key = FEW ? (kt0 + i) * KT + tid : fkey0 + tid, t = FEW ? 0 : t_lo + i * p.tpc;
+    fetch(warp >> 2);
+    for (int i = warp >> 2; i < n; i += NG) {
+      const int b = i % NB, key = FEW ? (kt0 + i) * KT + row : fkey0 + row, t = FEW ? 0 : t_lo + i * p.tpc;
       int64_t at = -1;
       float before = 0.f;
       if (FEW) {  // (read ahead of the product)
@@ -207,9 +208,16 @@ __global__ void __launch_bounds__(kWThreads, 2)
         if (p.window > 0 && key >= p.n_sink) end = min(end, ((int64_t)key + p.window - off - t) * p.R);
         const int c_lo = (int)max((int64_t)0, min(first, (int64_t)ROWS));
         const int c_hi = key < kv_len ? (int)max((int64_t)0, end) : 0;
-        if (!(ok = wait(bar(SFULL + b), (i >> 1) & 1))) break;
+        float* lse = s_lse[warp];
+        if (!FEW || i == 0) {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < ROWS / 32; ++e) lse[lane + e * 32] = nl[e] > kNegInf ? -nl[e] * kLog2e : kNegInf;
+          __syncwarp();
+          if (!FEW) fetch(i + NG);
+        }
+        if (!(ok = wait(bar(SFULL + b), (i / NB) & 1))) break;
         tc::fence_after();
-        const float* lse = s_lse[FEW ? 0 : i & 3];
         uint64_t a2[4] = {0, 0, 0, 0};
         const uint32_t s_t = t_lane + b * p.buf_cols;
         auto sum = [&](float (&sv)[32], int c) {
@@ -257,31 +265,35 @@ __global__ void __launch_bounds__(kWThreads, 2)
       }
       if (FEW) finish(acc, before, at);
     }
-    if (!FEW && ok) {
-      const int64_t at = place(fkey0 + tid);
-      finish(acc, at >= 0 && p.w_in ? p.w_in[at] : 0.f, at);
-    }
+    s_sum[warp >> 2][row] = acc;
   }
 
   __syncthreads();
+  if (!FEW && tid < ROWS && !*abort) {
+    const int64_t at = place(fkey0 + tid);
+    float sum = s_sum[0][tid];
+#pragma unroll
+    for (int i = 1; i < NG; ++i) sum += s_sum[i][tid];
+    finish(sum, at >= 0 && p.w_in ? p.w_in[at] : 0.f, at);
+  }
   if (*abort) {
     // copies and products still in flight land before the CTA leaves
-    if (warp == 4) {
+    if (warp == kLoad) {
       if (any) tc::warp_drain(bar(FIXED), 0);
       for (int st = 0; st < NS; ++st)
         if (last_item >= st) tc::warp_drain(bar(FULL + st), ((last_item - st) / NS) & 1);
-    } else if (warp == 5) {
+    } else if (warp == kIssue) {
       if (lane == 0) tc::commit(bar(DRAIN));
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }
-  } else if (warp == 4) {
+  } else if (warp == kLoad) {
     for (int st = 0; st < NS; ++st)
       if (last_item >= st) tc::warp_drain(bar(EMPTY + st), ((last_item - st) / NS) & 1);
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 5) tmem_free(tmem, p.tmem_cols);
+  if (warp == kIssue) tmem_free(tmem, p.tmem_cols);
 }
 
 template <int D, bool FEW>
@@ -291,7 +303,7 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   p.q_group = p.cols * 128;
   p.buf_cols = 32;
   while ((int)p.buf_cols < p.cols) p.buf_cols *= 2;
-  p.tmem_cols = 2 * p.buf_cols;
+  p.tmem_cols = C::NB * p.buf_cols;
   CUtensorMap mq, mk, mk16;
   // (a map needs rows; without queries none is ever loaded)
   const bool any = p.seqs.tokens > 0;
@@ -310,7 +322,7 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   // FEW: about four rounds of two CTAs an SM, so that ragged caches even out
   p.n_splits = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, (4 * 2 * 152 + units - 1) / units));
   const dim3 grid((unsigned)(FEW ? p.n_splits : tiles), p.seqs.n_seqs, p.hkv);
-  kern<<<grid, kWThreads, smem, st>>>(mq, mk, mk16, p);
+  kern<<<grid, C::THREADS, smem, st>>>(mq, mk, mk16, p);
   return cudaGetLastError();
 }
 
