@@ -346,8 +346,8 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 }
 
 // Output rows staged in shared memory (the layout of the tiles: 64-column groups `group`
-// bytes apart, 16-byte chunk ch of row r at chunk ch ^ (r & 7)), so that they leave in whole
-// lines: a thread that wrote its own row to global memory would touch 32 lines per store.
+// bytes apart, 16-byte chunk ch of row r at chunk ch ^ (r & 7)), so that they leave by TMA
+// or in whole lines: a warp whose threads wrote a row each would touch 32 lines per store.
 __device__ __forceinline__ uint32_t stage_at(uint32_t base, uint32_t group, int r, int ch) {
   return base + (ch >> 3) * group + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
@@ -374,6 +374,18 @@ __device__ __forceinline__ void stage_cols(uint32_t base, uint32_t group, int r,
     u.w = pack_bf16(v[e + 6] * f, v[e + 7] * f);
     st_shared(stage_at(base, group, r, (c + e) / 8), u);
   }
+}
+// A staged tile of D / 64 column groups to the rows of a query map (one thread, after every
+// writer's fence and a barrier); returns once shared memory has been read.
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t base, uint32_t group, int head, int tok) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c * 64), "r"(head), "r"(tok), "r"(base + c * group)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;\n" ::: "memory");
 }
 // The staged rows 0 .. rows - 1 (token r / R, head r % R; those of the first t_left tokens)
 // to dst, the first row's place; `threads` threads, this one `i`.

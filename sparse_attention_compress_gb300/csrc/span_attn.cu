@@ -101,7 +101,8 @@ template <int D, bool PAGED, bool FEW>
 __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
-                const __grid_constant__ CUtensorMap tm_v16, const AttnParams p) {
+                const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ CUtensorMap tm_o,
+                const AttnParams p) {
   using C = Cfg<D, FEW>;
   constexpr int NH = C::NH, N0 = C::N0, N1 = C::N1, NS = N0 + N1;
   using B = Bars<NS>;
@@ -425,10 +426,15 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
       }
     }
     if (whole && x < nh) {
+      const int tx = t0 + x * p.tpc;
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       named_barrier(1 + x, 128);  // (also after a timeout: every warp of the half comes here)
-      if (ok)
-        unstage_rows<D>(q_s + x * q_bytes, p.q_group, p.tpc * p.R, p.R, p.h, Lq - t0 - x * p.tpc,
-                        p.o + ((start + t0 + x * p.tpc) * p.h + g * p.R) * D, row, 128);
+      if (ok && tx + p.tpc <= Lq) {
+        if (row == 0) store_tile<D>(&tm_o, q_s + x * q_bytes, p.q_group, g * p.R, (int)(start + tx));
+      } else if (ok) {  // the box would reach into the next sequence
+        unstage_rows<D>(q_s + x * q_bytes, p.q_group, p.tpc * p.R, p.R, p.h, Lq - tx,
+                        p.o + ((start + tx) * p.h + g * p.R) * D, row, 128);
+      }
     }
   }
 
@@ -591,7 +597,7 @@ cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, int64_t ctas, cu
     regs = at.numRegs;
   }
   if (regs < C::MIN_REGS) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)ctas, C::THREADS, smem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
+  kern<<<(unsigned)ctas, C::THREADS, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
   return cudaGetLastError();
 }
 
@@ -617,8 +623,9 @@ cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int 
   p.cta_rows = pl.cta_rows;
   p.q_group = pl.few ? up16(pl.cta_rows) * 128 : ROWS * 128;
   p.scale_log2 = scale * kLog2e;
-  CUtensorMap m[5];
-  if (!query_map(&m[0], q, s.tokens, h, D, p.R, p.tpc) || !key_maps(&m[1], &m[2], keys.k, keys, hkv, D, s.tokens) ||
+  CUtensorMap m[6];
+  if (!query_map(&m[5], o, s.tokens, h, D, p.R, p.tpc) ||
+      !query_map(&m[0], q, s.tokens, h, D, p.R, p.tpc) || !key_maps(&m[1], &m[2], keys.k, keys, hkv, D, s.tokens) ||
       !key_maps(&m[3], &m[4], keys.v, keys, hkv, D, s.tokens))
     return cudaErrorInvalidValue;
   const int64_t ctas = pl.whole + (pl.units - pl.whole) * pl.n_splits;

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k16,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v16,
+              const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_dq,
               const BwdParams p) {
   enum : int {
     Q = 0,
@@ -162,16 +163,25 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
     }
     __syncwarp();
+    // o passes through the V ring's first slot (its rows' D is formed there): by plain loads it
+    // took three times as long to arrive as Q and dO do
+    if (lane == 0) {
+      tc::mbar_expect_tx(bar(VFULL), (uint32_t)(p.tpc * p.R * D * 2));
+      for (int c = 0; c < D / 64; ++c)
+        tc::tma3d(v_s + c * (ROWS * 128), &tm_o, c * 64, g * p.R, (int)(start + t0), bar(VFULL));
+    }
+    __syncwarp();
+    last_v = 0;
     for (int j = 0; j < n; ++j) {
-      const int w = tiles.width(j), sk = j % kNK, sv = j % kNV;
+      const int w = tiles.width(j), sk = j % kNK, sv = (j + 1) % kNV;
       if (j >= kNK && !wait(bar(KEMPTY + sk), ((j / kNK) - 1) & 1)) break;
       load_tile<D, false>(k_s + sk * TB, &tm_k, &tm_k16, p.keys.k, p.keys, p.hkv, g, seq, start, j * KT, tiles.sink_end,
                           tiles.shift, w, L, bar(KFULL + sk), lane);
       last_k = j;
-      if (j >= kNV && !wait(bar(VEMPTY + sv), ((j / kNV) - 1) & 1)) break;
+      if (j + 1 >= kNV && !wait(bar(VEMPTY + sv), (((j + 1) / kNV) - 1) & 1)) break;
       load_tile<D, false>(v_s + sv * TB, &tm_v, &tm_v16, p.keys.v, p.keys, p.hkv, g, seq, start, j * KT, tiles.sink_end,
                           tiles.shift, w, L, bar(VFULL + sv), lane);
-      last_v = j;
+      last_v = j + 1;
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ S
@@ -190,9 +200,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const uint32_t lead = elect();
     bool ok = wait(bar(Q), 0);
     for (int j = 0; ok && j < n; ++j) {
-      const int sv = j % kNV;
+      const int sv = (j + 1) % kNV;
       if (j >= 1 && !(ok = wait(bar(PFREE), (j - 1) & 1))) break;
-      if (!(ok = wait(bar(VFULL + sv), (j / kNV) & 1))) break;
+      if (!(ok = wait(bar(VFULL + sv), ((j + 1) / kNV) & 1))) break;
       tc::fence_after();
       mma_abt<D>(tmem + 256, desc_k(do_s), desc_k(v_s) + sv * (TB >> 4), tiles.width(j), lead);
       commit(bar(PFULL), lead);
@@ -220,42 +230,39 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int64_t rr = (start + t) * p.h + g * p.R + hd;
     bool ok = true;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // D of the CTA's rows, sixteen lanes (d = 128) a row: o from global memory, dO from its tile
+    // D of the CTA's rows, sixteen lanes (d = 128) a row
     constexpr int CH = D / 8, RPW = 32 / CH, NIT = ROWS / (8 * RPW);  // chunks a row, rows a warp at a time
+    const float lse = valid ? p.lse[rr] : kNegInf;
+    ok = wait(bar(Q), 0) && wait(bar(VFULL), 0);
     {
-      const int used = p.tpc * p.R;
-      uint4 ov[NIT];
+      float sum[NIT];
 #pragma unroll
       for (int i = 0; i < NIT; ++i) {
         const int r = (i * 8 + warp) * RPW + lane / CH;
-        ov[i] = make_uint4(0, 0, 0, 0);
-        if (r < used && t0 + r / p.R < L)
-          ov[i] = *reinterpret_cast<const uint4*>(p.o + ((start + t0 + r / p.R) * p.h + g * p.R + r % p.R) * D +
-                                                  lane % CH * 8);
-      }
-      ok = wait(bar(Q), 0);
-#pragma unroll
-      for (int i = 0; i < NIT; ++i) {
-        const int r = (i * 8 + warp) * RPW + lane / CH;
+        const uint4 ov = ld_shared(stage_at(v_s, ROWS * 128, r, lane % CH));
         const uint4 dv = ld_shared(stage_at(do_s, ROWS * 128, r, lane % CH));
-        const uint32_t av[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, bv[4] = {dv.x, dv.y, dv.z, dv.w};
-        float sum = 0.f;
+        const uint32_t av[4] = {ov.x, ov.y, ov.z, ov.w}, bv[4] = {dv.x, dv.y, dv.z, dv.w};
+        sum[i] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
           const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
-          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+          sum[i] = fmaf(u.x, v.x, fmaf(u.y, v.y, sum[i]));
         }
-#pragma unroll
-        for (int o = CH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % CH == 0) s_dsum[r] = sum;
       }
-      named_barrier(1, 256);  // (after a timeout too: every softmax warp comes here)
+#pragma unroll
+      for (int o = CH / 2; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < NIT; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+#pragma unroll
+      for (int i = 0; i < NIT; ++i)
+        if (lane % CH == 0) s_dsum[(i * 8 + warp) * RPW + lane / CH] = sum[i];
     }
+    named_barrier(1, 256);  // (after a timeout too: every softmax warp comes here)
+    if (tid == 0) tc::mbar_arrive(bar(VEMPTY));
     float l2 = __builtin_inff(), dsum = 0.f;
     if (valid) {
-      const float l = p.lse[rr];
-      l2 = l == kNegInf ? __builtin_inff() : l * kLog2e;
+      l2 = lse == kNegInf ? __builtin_inff() : lse * kLog2e;
       dsum = s_dsum[row];
       if (x == 0) {
         p.nlse2[rr] = -l2;
@@ -329,10 +336,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         stage_cols(q_s, ROWS * 128, row, c, v, p.scale);
       }
     }
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     named_barrier(1, 256);
-    if (ok)
+    if (ok && t0 + p.tpc <= L) {
+      if (tid == 0) store_tile<D>(&tm_dq, q_s, ROWS * 128, g * p.R, (int)(start + t0));
+    } else if (ok) {  // the box would reach into the next sequence
       unstage_rows<D>(q_s, ROWS * 128, p.tpc * p.R, p.R, p.h, L - t0, p.dq + ((start + t0) * p.h + g * p.R) * D, tid,
                       256);
+    }
   }
 
   __syncthreads();
@@ -768,8 +779,9 @@ BwdLayout bwd_layout(const Seqs& s, int h, int hkv, int D, int window, int n_sin
 template <int D>
 cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
   const Seqs& s = p.seqs;
-  CUtensorMap mq, md, mk, mk16, mv, mv16;
-  if (!query_map(&mq, p.q, s.tokens, p.h, D, p.R, p.tpc) || !query_map(&md, p.dout, s.tokens, p.h, D, p.R, p.tpc) ||
+  CUtensorMap mq, md, mo, mdq, mk, mk16, mv, mv16;
+  if (!query_map(&mo, p.o, s.tokens, p.h, D, p.R, p.tpc) || !query_map(&mdq, p.dq, s.tokens, p.h, D, p.R, p.tpc) ||
+      !query_map(&mq, p.q, s.tokens, p.h, D, p.R, p.tpc) || !query_map(&md, p.dout, s.tokens, p.h, D, p.R, p.tpc) ||
       !key_maps(&mk, &mk16, p.keys.k, p.keys, p.hkv, D, s.tokens) ||
       !key_maps(&mv, &mv16, p.keys.v, p.keys, p.hkv, D, s.tokens))
     return cudaErrorInvalidValue;
@@ -778,7 +790,7 @@ cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
   e = cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<D>());
   if (e != cudaSuccess) return e;
   dq_kernel<D><<<dim3((s.max_len + p.tpc - 1) / p.tpc, s.n_seqs, p.hkv), kDqThreads, dq_smem<D>(), st>>>(
-      mq, md, mk, mk16, mv, mv16, p);
+      mq, md, mk, mk16, mv, mv16, mo, mdq, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int items = l.sink_tiles * l.n_far + (s.max_len + KT - 1) / KT;
   dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem<D>(), st>>>(mq, md, mk, mk16, mv, mv16, p);
