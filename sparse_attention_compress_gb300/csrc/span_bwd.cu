@@ -377,12 +377,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 // formed dV and the next S^T do.  (S^T of a tile overwrites P^T of the one before, and dP^T
 // its dS^T: the same lane issued the products that read them, and products execute in
 // issue order.)
-// (Three Q slots would fit but for the 3 KB of lse and D beside them.)
-constexpr int kDkvThreads = 352, kNQ = 2, kND = 2;
+// A tile's Q is read from its S^T to its dK, its dO from dP^T to dV, hence three slots and
+// two: all that 227 KB hold at d = 128, to within the alignment of the first.
+constexpr int kDkvThreads = 352, kNQ = 3, kND = 2, kSmemMax = 227 * 1024;
 
 template <int D>
-constexpr int dkv_smem() {
-  return (2 + kNQ + kND) * KT * D * 2 + 1024;
+constexpr int dkv_tiles() {
+  return (2 + kNQ + kND) * KT * D * 2;
 }
 
 template <int D>
@@ -393,9 +394,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                const BwdParams p) {
   enum : int {
     KV = 0,      // [2] K, V
-    QFULL = 2,             // by slot: Q rows, lse, D
+    QFULL = 2,             // by slot: Q rows
     QEMPTY = QFULL + kNQ,
-    DFULL = QEMPTY + kNQ,  // by slot: dO rows
+    DFULL = QEMPTY + kNQ,  // by slot: dO rows, lse, D
     DEMPTY = DFULL + kND,
     SFULL = DEMPTY + kND,
     PFULL,   // P^T written
@@ -409,7 +410,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   constexpr int TB = KT * D * 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ __align__(16) float s_l2[kNQ][ROWS], s_d[kNQ][ROWS];  // minus the rows' base-2 lse and D
+  // minus the rows' base-2 lse (of tile j at j % 2: a tile's dV is done, and its lse read, before
+  // the next but one is loaded) and D (at j % 3: read after that, but before the next tile's P^T)
+  __shared__ __align__(16) float s_l2[2][ROWS], s_d[3][ROWS];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -418,6 +421,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
+  {  // (the tiles fit what the launch gave, wherever the static shared memory ends)
+    uint32_t given;
+    asm("mov.u32 %0, %%dynamic_smem_size;\n" : "=r"(given));
+    if (base + dkv_tiles<D>() > smem_u32(smem_raw) + given) {
+      if (threadIdx.x == 0) atomicExch(&g_device_status, (int)NSA_ERR_CUDA);
+      return;
+    }
+  }
   if (tc::device_status_set()) return;
   const Waits wait(abort);
   // items of a (sequence, kv-head): the chunks of far queries of the sink tiles, then every
@@ -527,19 +538,19 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const int t = t_lo + j * p.tpc;
       if (j >= kNQ && !wait(bar(QEMPTY + rq.slot), rq.phase ^ 1u)) break;
       uint32_t bytes = load_rows(q_s + rq.slot * TB, &tm_q, p.q, t, bar(QFULL + rq.slot));
-#pragma unroll
-      for (int i = 0; i < ROWS / 32; ++i) {
-        s_l2[rq.slot][lane + i * 32] = nl[i];
-        s_d[rq.slot][lane + i * 32] = nd[i];
-      }
       __syncwarp();
       if (lane == 0) tc::mbar_expect_tx(bar(QFULL + rq.slot), bytes);
       last_q = j;
-      if (j + 1 < n) fetch(t + p.tpc);
       if (j >= kND && !wait(bar(DEMPTY + rd.slot), rd.phase ^ 1u)) break;
       bytes = load_rows(do_s + rd.slot * TB, &tm_do, p.dout, t, bar(DFULL + rd.slot));
+#pragma unroll
+      for (int i = 0; i < ROWS / 32; ++i) {
+        s_l2[j & 1][lane + i * 32] = nl[i];
+        s_d[rq.slot][lane + i * 32] = nd[i];
+      }
       __syncwarp();
       if (lane == 0) tc::mbar_expect_tx(bar(DFULL + rd.slot), bytes);
+      if (j + 1 < n) fetch(t + p.tpc);
       last_d = j;
       rq.next();
       rd.next();
@@ -592,10 +603,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t s_t = tmem + c0 + lane_base, p_t = tmem + 128 + c0 + lane_base;
     const int nc = min(64, p.cols - c0);
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
-    Ring<kNQ> rq;
+    Ring<kNQ> rq;  // (D's buffers go with Q's slots: three of each)
+    Ring<kND> rd;
     bool ok = true;
-    for (int j = 0; j < n; ++j, rq.next()) {
-      const int st = rq.slot, t = t_lo + j * p.tpc;
+    for (int j = 0; j < n; ++j, rq.next(), rd.next()) {
+      const int t = t_lo + j * p.tpc;
       // columns [c_lo, c_hi) of this half are rows whose query sees this key
       int c_lo = 0, c_hi = 0;
       if (have) {
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
         c_hi = (int)max((int64_t)0, end) - c0;
       }
-      if (!(ok = wait(bar(QFULL + st), rq.phase))) break;  // lse and D
+      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;  // lse and D
       if (!(ok = wait(bar(SFULL), j & 1))) break;
       tc::fence_after();
       float sv[64];
@@ -612,7 +624,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int c = 0; c < 64; c += 32)
         tmem_ld32_if(c < nc, s_t + c, sv + c);
       const bool all = c_lo <= 0 && c_hi >= 64;
-      const float4* l4 = reinterpret_cast<const float4*>(&s_l2[st][c0]);
+      const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
       tmem_wait_ld(sv);
       tmem_wait_ld(sv + 32);
       if (!__all_sync(0xffffffffu, all)) {
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       if (lane == 0) tc::mbar_arrive(bar(PFULL));
       if (!(ok = wait(bar(DPFULL), j & 1))) break;
       tc::fence_after();
-      const float4* d4 = reinterpret_cast<const float4*>(&s_d[st][c0]);
+      const float4* d4 = reinterpret_cast<const float4*>(&s_d[rq.slot][c0]);
       float dp[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
@@ -787,13 +799,18 @@ cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<D>());
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<D>());
+  // the tiles start on the first multiple of 1024 after the static shared memory
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, dkv_kernel<D>)) != cudaSuccess) return e;
+  const int fixed = (int)at.sharedSizeBytes, dkv_smem = (fixed + 1023) / 1024 * 1024 + dkv_tiles<D>() - fixed;
+  if (fixed + dkv_smem > kSmemMax) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem);
   if (e != cudaSuccess) return e;
   dq_kernel<D><<<dim3((s.max_len + p.tpc - 1) / p.tpc, s.n_seqs, p.hkv), kDqThreads, dq_smem<D>(), st>>>(
       mq, md, mk, mk16, mv, mv16, mo, mdq, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int items = l.sink_tiles * l.n_far + (s.max_len + KT - 1) / KT;
-  dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem<D>(), st>>>(mq, md, mk, mk16, mv, mv16, p);
+  dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem, st>>>(mq, md, mk, mk16, mv, mv16, p);
   if ((e = cudaGetLastError()) != cudaSuccess || l.n_far == 0) return e;
   sink_sum_kernel<D><<<dim3(std::min(p.n_sink, s.max_len), p.hkv, s.n_seqs), 2 * D, 0, st>>>(p);
   return cudaGetLastError();
