@@ -560,19 +560,29 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t lead = elect(), kd = desc_k(k_s), qd = desc_k(q_s), dd = desc_mn(do_s);
     Ring<kNQ> rq;
     Ring<kND> rd;
-    bool ok = wait(bar(KV), 0);
-    for (int j = 0; ok && j < n; ++j) {
-      if (!(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
-      tc::fence_after();
+    // (what a product needs beside P^T is waited for before it, so that dV and the next S^T go
+    // out together)
+    auto issue_s = [&]() {
       mma_abt<D>(tmem, kd, qd + rq.slot * (TB >> 4), p.cols, lead);
       commit(bar(SFULL), lead);
+      rq.next();
+    };
+    bool ok = wait(bar(KV), 0) && wait(bar(QFULL), 0);
+    if (ok) {
+      tc::fence_after();
+      issue_s();
+    }
+    for (int j = 0; ok && j < n; ++j) {
       if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
+      if (j + 1 < n && !(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
       if (!(ok = wait(bar(PFULL), j & 1))) break;
       tc::fence_after();
       mma_split_a<D>(tmem + 256, tmem, dd + rd.slot * (TB >> 4), p.cols, j == 0, lead);
       commit(bar(DEMPTY + rd.slot), lead);
-      if (j == n - 1) commit(bar(DVDONE), lead);
-      rq.next();
+      if (j + 1 < n)
+        issue_s();
+      else
+        commit(bar(DVDONE), lead);
       rd.next();
     }
   } else if (warp == 10) {
@@ -580,20 +590,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t lead = elect(), vd = desc_k(v_s), dd = desc_k(do_s), qd = desc_mn(q_s);
     Ring<kNQ> rq;
     Ring<kND> rd;
-    bool ok = wait(bar(KV + 1), 0);
-    for (int j = 0; ok && j < n; ++j) {
-      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
-      tc::fence_after();
+    auto issue_dp = [&]() {
       mma_abt<D>(tmem + 128, vd, dd + rd.slot * (TB >> 4), p.cols, lead);
       commit(bar(DPFULL), lead);
       commit(bar(DEMPTY + rd.slot), lead);
+      rd.next();
+    };
+    bool ok = wait(bar(KV + 1), 0) && wait(bar(DFULL), 0);
+    if (ok) {
+      tc::fence_after();
+      issue_dp();
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      if (j + 1 < n && !(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
       if (!(ok = wait(bar(DSFULL), j & 1))) break;
       tc::fence_after();
       mma_split_a<D>(tmem + 384, tmem + 128, qd + rq.slot * (TB >> 4), p.cols, j == 0, lead);
-      if (j == n - 1) commit(bar(DKDONE), lead);
       commit(bar(QEMPTY + rq.slot), lead);  // (S^T of the tile was done before its dS^T)
+      if (j + 1 < n)
+        issue_dp();
+      else
+        commit(bar(DKDONE), lead);
       rq.next();
-      rd.next();
     }
   } else {
     // ------------------------------------------------------------------ softmax
