@@ -479,8 +479,8 @@ NSA_API nsa_status nsa_layer_bwd(const nsa_shape* shape, const void* q, const vo
  *                     included.  Lengths outside [0, max_pages * page_size] are clamped.
  * The values at positions below cache_lens have to be finite; memory past them, and pages
  * that no table row names, may hold anything.
- * page_size is a power of two in [16, 256]; bf16; d in {64, 128}; h/h_kv <= 128; at most 2^30
- * positions per table row, 65535 sequences. */
+ * page_size is a power of two in [16, 256]; bf16; d in {64, 128}; h/h_kv <= 128; at most 2^28
+ * positions per table row, 2^28 tokens, 65535 sequences. */
 typedef struct nsa_paged_cache {
   void* k_pages;
   void* v_pages;
@@ -514,7 +514,7 @@ NSA_API nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, c
  *                  decides how the keys are divided over the GPU, never the result's rows
  *   workspace      nsa_paged_attn_fwd_workspace_size() bytes, 256-byte aligned (partial
  *                  results of divided rows); NULL allowed when that size is 0
- * Deterministic.  0 <= window, n_sink <= 2^30. */
+ * Deterministic.  0 <= window, n_sink <= 2^28. */
 NSA_API size_t nsa_paged_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink);
 NSA_API nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
                                       int64_t max_cache_len, int window, int n_sink, float scale, void* o, float* lse,
@@ -562,7 +562,7 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  *   q, o [tokens, h, d]; k, v [tokens, h_kv, d] bf16;  lse nullable [tokens, h] fp32 out
  *   workspace  nsa_swa_sink_fwd_workspace_size() bytes, 256-byte aligned (0 but for
  *              few rows); NULL allowed when that size is 0
- * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^30, 0 <= n_sink <= 2^30.
+ * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^28, 0 <= n_sink <= 2^28.
  * The backward returns the gradients for an upstream d_o (formulas of nsa_sparse_bwd over
  * the seen keys, P and dS as bf16 in their products); o and lse are the forward's.  dk and
  * dv are written for every row of a sequence.  Deterministic.  Requires n_sink <= 1024. */

@@ -781,7 +781,7 @@ def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n
     lib, sp = load(), ctypes.byref(shp)
     with ctx:
         if out is None:
-            out = _new(q.shape, _BF16, dev, share)
+            out = torch.empty_like(q) if share is None else _new(q.shape, _BF16, dev, share)
         need = 0 if workspace is not None else lib.nsa_paged_attn_fwd_workspace_size(sp, max_cache_len, window, n_sink)
         ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
         rc = lib.nsa_paged_attn_fwd(sp, q.data_ptr(), ctypes.byref(c), max_cache_len, window, n_sink, scale,
@@ -879,7 +879,7 @@ def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=Non
     lib, sp = load(), ctypes.byref(shp)
     with ctx:
         if out is None:
-            out = _new(q.shape, _BF16, dev, share)
+            out = torch.empty_like(q) if share is None else _new(q.shape, _BF16, dev, share)
         need = 0 if workspace is not None else lib.nsa_swa_sink_fwd_workspace_size(sp, window, n_sink)
         ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
         rc = lib.nsa_swa_sink_fwd(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), window, n_sink, scale, out.data_ptr(),

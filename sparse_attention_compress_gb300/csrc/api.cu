@@ -1079,14 +1079,14 @@ static nsa_status check_span_shape(const nsa_shape* shape, Seqs* s, const char* 
   NSA_REQUIRE(shape->h / shape->h_kv <= 128, NSA_ERR_UNSUPPORTED, "%s: h/h_kv must be <= 128", fn);
   NSA_REQUIRE(s->n_seqs <= 65535 && shape->h_kv <= 4096, NSA_ERR_UNSUPPORTED,
               "%s: at most 65535 sequences and 4096 kv-heads", fn);
-  NSA_REQUIRE(s->tokens <= (int64_t)1 << 30 && s->max_len <= 1 << 30, NSA_ERR_UNSUPPORTED,
-              "%s: at most 2^30 tokens", fn);
+  NSA_REQUIRE(s->tokens <= (int64_t)1 << 28 && s->max_len <= 1 << 28, NSA_ERR_UNSUPPORTED,
+              "%s: at most 2^28 tokens", fn);
   return NSA_OK;
 }
 
 static nsa_status check_span(int window, int n_sink, const char* fn) {
   NSA_REQUIRE(window >= 0 && n_sink >= 0, NSA_ERR_INVALID, "%s: negative window or n_sink", fn);
-  NSA_REQUIRE(window <= 1 << 30 && n_sink <= 1 << 30, NSA_ERR_UNSUPPORTED, "%s: window and n_sink must be <= 2^30", fn);
+  NSA_REQUIRE(window <= 1 << 28 && n_sink <= 1 << 28, NSA_ERR_UNSUPPORTED, "%s: window and n_sink must be <= 2^28", fn);
   return NSA_OK;
 }
 
@@ -1096,8 +1096,8 @@ static nsa_status check_cache(const nsa_paged_cache* c, int h_kv, int d, bool ne
   NSA_REQUIRE(c->n_pages >= 1 && c->max_pages >= 1, NSA_ERR_INVALID, "%s: n_pages and max_pages must be positive", fn);
   NSA_REQUIRE(c->page_size >= 16 && c->page_size <= 256 && (c->page_size & (c->page_size - 1)) == 0,
               NSA_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64, 128 or 256 (got %d)", fn, c->page_size);
-  NSA_REQUIRE((int64_t)c->max_pages * c->page_size <= (int64_t)1 << 30, NSA_ERR_UNSUPPORTED,
-              "%s: max_pages * page_size must be <= 2^30", fn);
+  NSA_REQUIRE((int64_t)c->max_pages * c->page_size <= (int64_t)1 << 28, NSA_ERR_UNSUPPORTED,
+              "%s: max_pages * page_size must be <= 2^28", fn);
   NSA_REQUIRE(c->page_stride >= (int64_t)c->page_size * h_kv * d && c->page_stride % 8 == 0, NSA_ERR_INVALID,
               "%s: page_stride must be >= page_size * h_kv * d and a multiple of 8", fn);
   NSA_REQUIRE(c->page_stride < (int64_t)1 << 38, NSA_ERR_UNSUPPORTED, "%s: page_stride must be < 2^38", fn);
@@ -1146,7 +1146,7 @@ nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, const voi
 
 // The bound of the cached lengths that divides the keys (none given: no bound).
 static int span_keys(int64_t max_cache_len) {
-  return max_cache_len <= 0 || max_cache_len > (int64_t)1 << 30 ? 1 << 30 : (int)max_cache_len;
+  return max_cache_len <= 0 || max_cache_len > (int64_t)1 << 28 ? 1 << 28 : (int)max_cache_len;
 }
 
 size_t nsa_paged_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink) {
@@ -1216,8 +1216,8 @@ nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_cache* c
   const int64_t cap = (int64_t)cache->max_pages * cache->page_size;
   NSA_REQUIRE(new_max_pages >= 1 && (int64_t)new_max_pages * cache->page_size >= (budget < cap ? budget : cap),
               NSA_ERR_INVALID, "nsa_paged_evict: new_table's rows do not hold the budget");
-  NSA_REQUIRE((int64_t)new_max_pages * cache->page_size <= (int64_t)1 << 30, NSA_ERR_UNSUPPORTED,
-              "nsa_paged_evict: new_max_pages * page_size must be <= 2^30");
+  NSA_REQUIRE((int64_t)new_max_pages * cache->page_size <= (int64_t)1 << 28, NSA_ERR_UNSUPPORTED,
+              "nsa_paged_evict: new_max_pages * page_size must be <= 2^28");
   NSA_REQUIRE(new_table != nullptr && keep != nullptr && new_lens != nullptr &&
                   ((reinterpret_cast<uintptr_t>(new_table) | reinterpret_cast<uintptr_t>(keep) |
                     reinterpret_cast<uintptr_t>(new_lens)) & 3u) == 0,

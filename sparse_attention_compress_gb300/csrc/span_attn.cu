@@ -553,8 +553,10 @@ Plan make_plan(const Seqs& s, int h, int hkv, int D, int max_keys, int window, i
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + rows_tok + up16(n_sink) + 2 * GRAN);
   const int64_t tiles = std::max<int64_t>(1, (keys + KT - 1) / KT);
   if (pl.few) {
-    // About four rounds of CTAs (two an SM), so that ragged caches even out.
-    const int64_t want = (4 * 2 * kSms + pl.units - 1) / pl.units;
+    // At most four rounds of CTAs (two an SM): ragged caches then even out, and a round is not
+    // begun for a few.  32 caches of 16384 to 32768 keys: 146 us with 19 parts (four rounds),
+    // 154 with 10 (2.1 rounds), 152 with 15 (3.2), 157 with 29 (6.1).
+    const int64_t want = 4 * 2 * kSms / pl.units;
     pl.n_splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles, 256}));
     pl.whole = pl.n_splits == 1 ? pl.units : 0;
   } else {

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
   if (kt0 >= min(kt1, n_kt)) return;
   const int fkey0 = kt0 * KT;
   const int t_lo = FEW ? 0 : max(0, fkey0 - off);
-  const int t_hi = !FEW && p.window > 0 && fkey0 >= p.n_sink ? min(Lq, fkey0 + KT - 1 + p.window - off) : Lq;
+  const int t_hi = !FEW && p.window > 0 && fkey0 >= p.n_sink ? min(Lq, fkey0 + KT - 1 + p.window - off) : Lq;  // (sums below 2^31: every size is at most 2^28)
   const int n_q = t_hi > t_lo ? (t_hi - t_lo + p.tpc - 1) / p.tpc : 0;
   const int n = FEW ? kt1 - kt0 : n_q;  // streamed items
   const bool any = n_q > 0;             // without queries nothing is loaded
@@ -319,8 +319,8 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)p.keys.max_pages << p.keys.page_log2) + KT - 1) / KT;
   const int64_t units = (int64_t)p.seqs.n_seqs * p.hkv;
-  // FEW: about four rounds of two CTAs an SM, so that ragged caches even out
-  p.n_splits = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, (4 * 2 * 152 + units - 1) / units));
+  // FEW: at most three rounds of two CTAs an SM, so that ragged caches even out
+  p.n_splits = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, 3 * 2 * 152 / units));
   const dim3 grid((unsigned)(FEW ? p.n_splits : tiles), p.seqs.n_seqs, p.hkv);
   kern<<<grid, C::THREADS, smem, st>>>(mq, mk, mk16, p);
   return cudaGetLastError();

@@ -93,6 +93,8 @@ CASES = [
     ([450], [450], 12, 4, 64, 16, 1, 1),
     ([333], [90], 128, 1, 128, 64, 50, 16),                         # group 128: one token a tile
     ([2000, 1500], [1, 3], 16, 2, 128, 64, 1000, 4),
+    ([200, 650], [3, 2], 16, 1, 128, 32, 0, 0),                     # 48 rows: the most the few-row forms take
+    ([200, 650], [7, 1], 7, 1, 64, 64, 90, 2),                      # 49 rows
 ]
 
 
@@ -138,6 +140,23 @@ def test_attention_is_the_same_on_every_run_and_for_every_division():
             for b in range(2):
                 a, e, _, (ro, _, eo, _) = _reference(c, q, cu, b, 0, 0, 1.0 / math.sqrt(128))
                 ref.within(o[0][a:e], ro, eo, f"bound {bound}")
+
+
+def test_divided_and_whole_units_in_one_call():
+    """More row tiles than SMs, the last round's divided over their keys: 200 units of 47 key
+    tiles.  Checked on two sequences and heads; everything is finite."""
+    lens, n, hk, d = [6000, 5000, 4000, 5500, 5999], 1200, 8, 64
+    c = Cache(lens, hk, d, 64, 33)
+    q, cu = _queries([n] * 5, hk, d, 34)
+    lse = torch.full((5 * n, hk), NAN, device="cuda")
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, cu_seqlens=cu.cuda(), max_seqlen=n, lse=lse)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    for b, h in ((0, 7), (4, 0), (2, 3)):
+        a, e = int(cu[b]), int(cu[b + 1])
+        see = ref.visible(range(lens[b] - n, lens[b]), lens[b], 0, 0)
+        ro, rl, eo, el = ref.attend(q[a:e, h:h + 1].double(), c.k[b][:, h:h + 1], c.v[b][:, h:h + 1], see, 1 / 8)
+        ref.within(o[a:e, h:h + 1], ro, eo, f"o of sequence {b}, head {h}")
+        ref.within(lse[a:e, h:h + 1], rl, el, f"lse of sequence {b}, head {h}")
 
 
 @pytest.mark.parametrize("scale", [0.3, 4.0])
@@ -484,6 +503,23 @@ def test_sink_window_forward_and_backward(lens, H, hk, d, window, n_sink):
         want, bounds = ref.gradients(*x, o[a:e].cpu().double(), lse[a:e].cpu().double(), see, scale)
         for name, got, w, bd in zip(("dq", "dk", "dv"), grads, want, bounds):
             ref.within(got[a:e], w, bd, f"{name} of sequence {b}")
+
+
+def test_sink_window_of_a_dense_batch():
+    """[B, T, heads, d] is the packed layout with equal lengths, bit for bit."""
+    B, T, H, hk, d = 3, 150, 6, 2, 64
+    q, k, v, do = (_bf((B, T, h, d), _gen(45 + i)).cuda() for i, h in enumerate((H, hk, hk, H)))
+    flat = [x.reshape(B * T, *x.shape[2:]) for x in (q, k, v, do)]
+    cu = torch.arange(B + 1, dtype=I32, device="cuda") * T
+    kw = dict(cu_seqlens=cu, max_seqlen=T)
+    lse, lse2 = (torch.empty(B * T, H, device="cuda") for _ in range(2))
+    o = nsa.nsa_swa_sink_fwd(q, k, v, 40, 3, lse=lse)
+    o2 = nsa.nsa_swa_sink_fwd(*flat[:3], 40, 3, lse=lse2, **kw)
+    assert o.shape == q.shape and torch.equal(o.view_as(o2), o2) and torch.equal(lse, lse2)
+    g = nsa.nsa_swa_sink_bwd(q, k, v, o, lse, do, 40, 3)
+    g2 = nsa.nsa_swa_sink_bwd(*flat[:3], o2, lse, flat[3], 40, 3, **kw)
+    for x, y, z in zip(g, g2, (q, k, v)):
+        assert x.shape == z.shape and torch.equal(x.view_as(y), y)
 
 
 def test_sink_gradients_against_differences():
