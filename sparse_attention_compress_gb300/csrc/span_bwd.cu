@@ -1,10 +1,14 @@
 // Backward of the sliding window with sinks (span_attn.cu on packed sequences).  Per row
-// with seen keys j:  p_j = exp(scale q.k_j - lse),  D = dO.o,  dp_j = dO.v_j,
+// with seen keys j:  p_j = exp(scale q.k_j - lse),  dp_j = dO.v_j,  D = sum_j p_j dp_j,
 //   ds_j = p_j (dp_j - D),  dq = scale sum_j ds_j k_j,
 //   dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dO.
 // S, dP and all accumulators are fp32 (TMEM); P and dS enter the last products as bf16:
 // one rounding of at most 2^-8 relative per weight, of either sign over a sum's terms, so
-// that the sums stay within the rounding of the bf16 gradients themselves.
+// that the sums stay within the rounding of the bf16 gradients themselves.  D equals dO.o;
+// where a row's ds_j are formed before all its dp_j are known it is taken so, from the bf16
+// o, and the difference (the sum of the ds_j, which is 0 for the true D) is added for the
+// gradients of k.  Rows with few keys, in whose ds_j the rounding of o would show, have them
+// in one tile, and their D is the sum itself.
 //
 // Two kernels, each a chain of M = 128 products over 128-wide tiles with eight softmax
 // warps (two threads a TMEM lane, 64 columns each):
@@ -63,10 +67,13 @@ __device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, ui
   }
 }
 
-// Two bf16 products p (dp - D) of pairs: nd is minus D, twice.
-__device__ __forceinline__ uint32_t ds_pair(uint64_t p, uint64_t dp, uint64_t nd) {
-  const float2 d = unpair(mul2(p, add2(dp, nd)));
+// Two products p (dp - D), as bf16 (nd is minus D, twice).
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+  const float2 d = unpair(x);
   return pack_bf16(d.x, d.y);
+}
+__device__ __forceinline__ uint32_t ds_pair(uint64_t p, uint64_t dp, uint64_t nd) {
+  return pack_pair(mul2(p, add2(dp, nd)));
 }
 
 // ---------------------------------------------------------------------------- dQ
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   constexpr int TB = KT * D * 2;  // bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[COUNT];
-  __shared__ float s_dsum[ROWS];
+  __shared__ float s_dsum[ROWS], s_half[2][ROWS];  // dO.o of the rows; the halves' parts of a row sum
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -264,15 +271,19 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (valid) {
       l2 = lse == kNegInf ? __builtin_inff() : lse * kLog2e;
       dsum = s_dsum[row];
-      if (x == 0) {
-        p.nlse2[rr] = -l2;
-        p.ndsum[rr] = -dsum;
-      }
     }
-    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nl2 = pair(-l2, -l2), nd2 = pair(-dsum, -dsum);
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nl2 = pair(-l2, -l2);
+    uint64_t nd2 = pair(-dsum, -dsum), e2 = 0;  // e2: this half's sum of ds
+    // the sum of both halves' parts of a row (every softmax warp comes here)
+    auto row_sum = [&](float part) {
+      s_half[x][row] = part;
+      named_barrier(2, 256);
+      return s_half[0][row] + s_half[1][row];
+    };
     for (int j = 0; ok && j < n; ++j) {
       const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
-      if (!(ok = wait(bar(SFULL + b), (j >> 1) & 1))) break;
+      // (with one tile a warp that gave up still comes to the barrier of row_sum)
+      if (!(ok = wait(bar(SFULL + b), (j >> 1) & 1)) && n > 1) break;
       tc::fence_after();
       const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
       const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)
@@ -281,24 +292,26 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       for (int c = 0; c < 64; c += 32)
         tmem_ld32_if(c < nc, s_t + c, sv + c);
       const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
-      const bool all = j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64);
-      tmem_wait_ld(sv);
-      tmem_wait_ld(sv + 32);
-      if (!__all_sync(0xffffffffu, all)) {
+      const bool all = __all_sync(0xffffffffu, j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64));
+      auto mask = [&](float (&y)[64], float out) {  // unseen columns
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           const uint32_t see = bits(j_lo - c0 - c, j_hi - c0 - c) | bits(0, min(j_sink, j_hi) - c0 - c);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+          for (int e = 0; e < 32; ++e) y[c + e] = (see >> e) & 1u ? y[c + e] : out;
         }
-      }
+      };
+      tmem_wait_ld(sv);
+      tmem_wait_ld(sv + 32);
+      if (!all) mask(sv, kNegInf);
 #pragma unroll
       for (int c = 0; c < 64; c += 2) {
         const float2 y = unpair(fma2(pair(sv[c], sv[c + 1]), scale2, nl2));
         sv[c] = ex2(y.x);
         sv[c + 1] = ex2(y.y);
       }
-      if (!(ok = wait(bar(PFULL), j & 1))) break;
+      ok = wait(bar(PFULL), j & 1) && ok;
+      if (!ok && n > 1) break;
       tc::fence_after();
       float dp[64];
 #pragma unroll
@@ -309,13 +322,26 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(PFREE));
+      if (!all) mask(dp, 0.f);  // (columns past the tile's hold anything)
+      if (n == 1) {
+        uint64_t d2 = 0;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) d2 = fma2(pair(sv[c], sv[c + 1]), pair(dp[c], dp[c + 1]), d2);
+        const float2 d = unpair(d2);
+        dsum = row_sum(d.x + d.y);
+        nd2 = pair(-dsum, -dsum);
+        if (!ok) break;
+      }
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
         if (c >= nc) break;
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)  // (an unseen key has p = 0)
-          pk[e / 2] = ds_pair(pair(sv[c + e], sv[c + e + 1]), pair(dp[c + e], dp[c + e + 1]), nd2);
+        for (int e = 0; e < 32; e += 2) {  // (an unseen key has p = 0)
+          const uint64_t d = mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), nd2));
+          e2 = add2(e2, d);
+          pk[e / 2] = pack_pair(d);
+        }
         tmem_st16_nowait(s_t + c / 2, pk);
       }
       tmem_wait_st();
@@ -326,6 +352,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (ok) {
       ok = wait(bar(DQDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
       tc::fence_after();
+    }
+    if (n > 1) {
+      const float2 e = unpair(e2);
+      dsum += row_sum(e.x + e.y);  // (the sum of p is 1)
+    }
+    if (ok && valid && x == 0) {
+      p.nlse2[rr] = -l2;
+      p.ndsum[rr] = -dsum;
     }
     if (ok) {
       // staged over Q, which every S has read

@@ -64,8 +64,9 @@ def key_weights(q, k, see, lse, scale):
     return w, e
 
 
-def gradients(q, k, v, do, o, lse, see, scale):
-    """dq, dk, dv from the forward's (rounded) o and its lse, with their error bounds."""
+def gradients(q, k, v, do, o, lse, see, scale, eo=None):
+    """dq, dk, dv with D = sum_j p_j dp_j, and their error bounds.  The kernel takes D = dO.o for
+    dq where a row's keys are many; eo bounds its stored o's distance from the exact one."""
     Q, H, d = q.shape
     n, hk = k.shape[:2]
     r = H // hk
@@ -75,16 +76,20 @@ def gradients(q, k, v, do, o, lse, see, scale):
         g = h // r
         kk, vv, qq, dd = k[:, g], v[:, g], q[:, h], do[:, h]
         p = torch.where(see, torch.exp(qq @ kk.T * scale - lse[:, h][:, None]), 0.0)
-        dsum = (dd * o[:, h]).sum(1, keepdim=True)
         dp = dd @ vv.T
+        dsum = (p * dp).sum(1, keepdim=True)
         ds = p * (dp - dsum)
         dq[:, h] = scale * ds @ kk
         dk[:, g] += scale * ds.T @ qq
         dv[:, g] += p.T @ dd
         arg = (d + 8) * U * (qq.abs() @ kk.abs().T) * scale + 4 * U * lse[:, h].abs()[:, None] + 2.0 ** -20
-        # |dp - D| is known to within d U of the magnitudes that make it up
-        eds = ds.abs() * (B + arg) + p * (d + 4) * U * (dd.abs() @ vv.abs().T + (dd * o[:, h]).abs().sum(1, keepdim=True))
-        eq[:, h] = scale * (eds + n * U * ds.abs()) @ kk.abs()
+        # |dp - D| is known to within d U of the magnitudes that make it up, D to within the
+        # errors of the p that it sums
+        mag = dd.abs() @ vv.abs().T
+        ed = ((arg + n * U) * p * mag).sum(1, keepdim=True) + (dd * o[:, h]).abs().sum(1, keepdim=True) * (d + n) * U
+        eds = ds.abs() * (B + arg) + p * ((d + 4) * U * mag + ed)
+        far = 0.0 if eo is None else p * (dd.abs() * eo[:, h]).sum(1, keepdim=True)
+        eq[:, h] = scale * (eds + far + n * U * ds.abs()) @ kk.abs()
         ek[:, g] += scale * (eds + Q * r * U * ds.abs()).T @ qq.abs()
         ev[:, g] += (p * (B + arg + Q * r * U)).T @ dd.abs()
     return (dq, dk, dv), tuple(e + B * x.abs() * (1 + 2 * B) for e, x in zip((eq, ek, ev), (dq, dk, dv)))
