@@ -19,7 +19,8 @@
 //               the A operands of dV += P^T dO and dK += dS^T Q, and nothing passes through
 //               shared memory but the tiles.
 // Sinks are seen by every later query, so the queries past a sink tile's window are cut
-// into chunks with a CTA each; their fp32 partials are summed in order by sink_sum_kernel.
+// into chunks with a CTA each, and where there are fewer key tiles than SMs their own queries
+// are divided too; the fp32 partials are summed in order by key_sum_kernel.
 // No atomics: results are the same on every run.
 #include <algorithm>
 
@@ -39,9 +40,10 @@ struct BwdParams {
   float* nlse2;  // [tokens, h] workspace: minus the base-2 lse (-inf for rows without keys)
   float* ndsum;  // [tokens, h] workspace: minus D
   __nv_bfloat16 *dq, *dk, *dv;
-  float* part;  // [n_seqs][hkv][sink tiles][1 + n_far][2][sink_rows][D] fp32
+  float* part;  // [n_seqs][hkv][sink tiles][1 + n_far][2][sink_rows][D] fp32 (0: the near queries, undivided)
+  float* near;  // [n_seqs][hkv][key tiles][n_near][2][KT][D] fp32, where n_near > 1
   int h, hkv, R, tpc, cols, window, n_sink;
-  int n_far, far_tokens, sink_tiles, sink_rows;
+  int n_far, far_tokens, sink_tiles, sink_rows, n_near;
   float scale, scale_log2;
 };
 
@@ -472,14 +474,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int64_t start = seq_start(p.seqs, seq);
   const int L = seq_len(p.seqs, seq);
   const bool far = (int)blockIdx.x < n_far_items;
-  const int kt = far ? (int)blockIdx.x / p.n_far : (int)blockIdx.x - n_far_items;
+  const int kt = far ? (int)blockIdx.x / p.n_far : ((int)blockIdx.x - n_far_items) / p.n_near;
   const int chunk = far ? (int)blockIdx.x % p.n_far : -1;
+  const int share = far ? 0 : ((int)blockIdx.x - n_far_items) % p.n_near;
   const int key0 = kt * KT;
   if (key0 >= L) return;
   const int near_end = min(L, key0 + KT - 1 + p.window);
-  const int t_lo = far ? near_end + chunk * p.far_tokens : key0;
-  const int t_hi = far ? min(L, t_lo + p.far_tokens) : near_end;
-  if (t_lo >= t_hi) return;  // (an empty chunk: sink_sum_kernel does not read it)
+  const int near_tiles = (near_end - key0 + p.tpc - 1) / p.tpc;
+  const int t_lo = far ? near_end + chunk * p.far_tokens : key0 + near_tiles * share / p.n_near * p.tpc;
+  const int t_hi = far ? min(L, t_lo + p.far_tokens) : min(near_end, key0 + near_tiles * (share + 1) / p.n_near * p.tpc);
+  if (t_lo >= t_hi) return;  // (an empty chunk or share: key_sum_kernel does not read it)
   const int n = (t_hi - t_lo + p.tpc - 1) / p.tpc;
   const int used = p.tpc * p.R;  // rows of a tile
   // A query tile is seen by the key tiles of its whole window, CTAs that run side by side.
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   // time and all but one find it in L2: begun at the first tile instead, 8192 tokens x 64
   // heads read 1.30 GB from HBM for 0.27 GB of q and dO.
   const int round = (KT - 1 + p.window + p.tpc - 1) / p.tpc;
-  const int first = far ? 0 : (round - t_lo / p.tpc % round) % round;
+  const int first = far || p.n_near > 1 ? 0 : (round - t_lo / p.tpc % round) % round;
   auto token_of = [&](int j) {  // first token of the round's tile j
     const int i = j + (first < n ? first : 0);
     return t_lo + (i < n ? i : i - n) * p.tpc;
@@ -754,9 +758,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (ok) {
       // half 0 writes dK, half 1 dV
       const float f = x ? 1.f : p.scale;
-      const bool to_part = kt < p.sink_tiles && p.n_far > 0 && key < p.n_sink;
-      float* part = p.part + (((((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) + (chunk + 1)) * 2 + x) *
-                                 p.sink_rows * D + (int64_t)row * D;
+      const bool divided = !far && p.n_near > 1;
+      const bool to_part = divided || (kt < p.sink_tiles && p.n_far > 0 && key < p.n_sink);
+      float* part;
+      if (divided) {
+        const int n_kt = ((int)gridDim.x - n_far_items) / p.n_near;
+        part = p.near + (((((int64_t)seq * p.hkv + g) * n_kt + kt) * p.n_near + share) * 2 + x) * KT * D + row * D;
+      } else {
+        part = p.part + (((((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) + (chunk + 1)) * 2 + x) *
+                            p.sink_rows * D + (int64_t)row * D;
+      }
       __nv_bfloat16* dst = (x ? p.dv : p.dk) + ((start + key) * p.hkv + g) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -806,29 +817,39 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (warp == 9) tmem_free(tmem, kBwdTmem);
 }
 
-// dK and dV of the sinks: the near part and the far chunks, in order.  One block a (sink,
-// kv-head, sequence); thread: column of dK (first D threads) or dV.
+// dK and dV of the keys that several CTAs hold parts of: the near parts and, for sinks, the
+// far chunks, in order.  One block a (key, kv-head, sequence); thread: column of dK (first D
+// threads) or dV.
 template <int D>
-__global__ void __launch_bounds__(2 * D) sink_sum_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(2 * D) key_sum_kernel(const BwdParams p, int n_kt) {
   const int key = blockIdx.x, g = blockIdx.y, seq = blockIdx.z;
   const int L = seq_len(p.seqs, seq);
   if (key >= L) return;
   const int x = threadIdx.x / D, c = threadIdx.x % D, kt = key / KT;
   const int near_end = min(L, kt * KT + KT - 1 + p.window);
-  const int parts = 1 + (L - near_end + p.far_tokens - 1) / p.far_tokens;
-  const int64_t step = (int64_t)2 * p.sink_rows * D;
-  const float* src = p.part + (((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) * step +
-                     ((int64_t)x * p.sink_rows + key % KT) * D + c;
   float acc = 0.f;
+  if (p.n_near > 1) {
+    const int tiles = (near_end - kt * KT + p.tpc - 1) / p.tpc;
+    const float* src = p.near + ((((int64_t)seq * p.hkv + g) * n_kt + kt) * p.n_near * 2 + x) * KT * D +
+                       (int64_t)(key % KT) * D + c;
+    for (int i = 0; i < p.n_near; ++i)
+      if (tiles * (i + 1) / p.n_near > tiles * i / p.n_near) acc += src[(int64_t)i * 2 * KT * D];
+  }
+  if (p.n_far > 0 && key < p.n_sink) {
+    const int64_t step = (int64_t)2 * p.sink_rows * D;
+    const float* src = p.part + (((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) * step +
+                       ((int64_t)x * p.sink_rows + key % KT) * D + c;
+    const int parts = 1 + (L - near_end + p.far_tokens - 1) / p.far_tokens;
 #pragma unroll 4
-  for (int i = 0; i < parts; ++i) acc += src[i * step];
+    for (int i = p.n_near > 1; i < parts; ++i) acc += src[i * step];
+  }
   __nv_bfloat16* dst = (x ? p.dv : p.dk) + ((seq_start(p.seqs, seq) + key) * (int64_t)p.hkv + g) * D + c;
   *dst = __float2bfloat16_rn(x ? acc : acc * p.scale);
 }
 
 struct BwdLayout {
-  int tpc, n_far, far_tokens, sink_tiles, sink_rows;
-  size_t dsum, part, bytes;
+  int tpc, n_far, far_tokens, sink_tiles, sink_rows, n_near;
+  size_t dsum, part, near, bytes;
 };
 BwdLayout bwd_layout(const Seqs& s, int h, int hkv, int D, int window, int n_sink) {
   BwdLayout l{};
@@ -836,18 +857,29 @@ BwdLayout bwd_layout(const Seqs& s, int h, int hkv, int D, int window, int n_sin
   l.tpc = std::max(1, std::min(ROWS / R, s.max_len));
   const int sinks = std::min(n_sink, s.max_len);
   const int64_t far = sinks > 0 ? (int64_t)s.max_len - (KT - 1) - window : 0;  // queries past the first tile's window
+  const int64_t own = (int64_t)window + KT - 1;                                // queries of a key tile
+  const int64_t n_kt = ((int64_t)s.max_len + KT - 1) / KT, units = (int64_t)s.n_seqs * hkv;
+  l.sink_tiles = far > 0 ? (sinks + KT - 1) / KT : 0;
+  // Fewer key tiles (and chunks of a tile's length) than SMs: their queries are divided as far
+  // as one round of the SMs holds the shares, none below eight query tiles.  3 sequences of at
+  // most 1001 tokens x 16 heads, window 256 (60 CTAs that walk 48 query tiles each): 65 us whole,
+  // 39 us and 10 us to sum in 2 shares.
+  const int64_t far_chunks = far > 0 ? std::min<int64_t>(64, (far + own - 1) / own) : 0;
+  const int64_t walk = (std::min<int64_t>(s.max_len, own) + l.tpc - 1) / l.tpc;
+  const int64_t ctas = std::max<int64_t>(1, (n_kt + l.sink_tiles * far_chunks) * units);
+  l.n_near = (int)std::max<int64_t>(1, std::min<int64_t>(152 / ctas, walk / 8));
   if (far > 0) {
-    // a chunk is about as long as a key tile's own queries, at most 64 chunks
-    const int64_t len = std::max<int64_t>((int64_t)window + KT - 1, (far + 63) / 64);
+    // a chunk is about as long as a share of a key tile's own queries, at most 64 chunks
+    const int64_t len = std::max<int64_t>((own + l.n_near - 1) / l.n_near, (far + 63) / 64);
     l.far_tokens = (int)((len + l.tpc - 1) / l.tpc * l.tpc);
     l.n_far = (int)((far + l.far_tokens - 1) / l.far_tokens);
-    l.sink_tiles = (sinks + KT - 1) / KT;
     l.sink_rows = std::min(sinks, KT);
   }
   auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   l.dsum = a256((size_t)s.tokens * h * 4);
   l.part = 2 * l.dsum;
-  l.bytes = l.part + (size_t)s.n_seqs * hkv * l.sink_tiles * (1 + l.n_far) * 2 * l.sink_rows * D * 4;
+  l.near = a256(l.part + (size_t)s.n_seqs * hkv * l.sink_tiles * (1 + l.n_far) * 2 * l.sink_rows * D * 4);
+  l.bytes = l.near + (l.n_near > 1 ? (size_t)(n_kt * units) * l.n_near * 2 * KT * D * 4 : 0);
   return l;
 }
 
@@ -872,10 +904,11 @@ cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
   dq_kernel<D><<<dim3((s.max_len + p.tpc - 1) / p.tpc, s.n_seqs, p.hkv), kDqThreads, dq_smem<D>(), st>>>(
       mq, md, mk, mk16, mv, mv16, mo, mdq, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int items = l.sink_tiles * l.n_far + (s.max_len + KT - 1) / KT;
+  const int n_kt = (s.max_len + KT - 1) / KT, items = l.sink_tiles * l.n_far + n_kt * l.n_near;
   dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem, st>>>(mq, md, mk, mk16, mv, mv16, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || l.n_far == 0) return e;
-  sink_sum_kernel<D><<<dim3(std::min(p.n_sink, s.max_len), p.hkv, s.n_seqs), 2 * D, 0, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || (l.n_far == 0 && l.n_near == 1)) return e;
+  const int keys = l.n_near > 1 ? s.max_len : std::min(p.n_sink, s.max_len);
+  key_sum_kernel<D><<<dim3(keys, p.hkv, s.n_seqs), 2 * D, 0, st>>>(p, n_kt);
   return cudaGetLastError();
 }
 
@@ -901,6 +934,8 @@ cudaError_t launch_span_bwd(const Seqs& s, const void* q, const void* k, const v
   p.nlse2 = (float*)workspace;
   p.ndsum = (float*)((uint8_t*)workspace + l.dsum);
   p.part = (float*)((uint8_t*)workspace + l.part);
+  p.near = (float*)((uint8_t*)workspace + l.near);
+  p.n_near = l.n_near;
   p.dq = (__nv_bfloat16*)dq;
   p.dk = (__nv_bfloat16*)dk;
   p.dv = (__nv_bfloat16*)dv;
