@@ -468,6 +468,7 @@ TRAIN = [
     ([1], 1, 1, 64, 1, 0), ([1, 2, 17], 4, 2, 64, 1, 1), ([130, 0, 77], 6, 2, 128, 16, 4), ([300], 16, 1, 128, 64, 0),
     ([700, 129, 128], 8, 2, 128, 100, 3), ([260, 515], 10, 2, 64, 33, 40), ([900], 2, 2, 128, 20, 150),
     ([640, 383], 24, 8, 64, 1000, 7), ([210], 128, 1, 128, 32, 2), ([1500], 4, 1, 128, 5, 128), ([127, 255], 3, 1, 128, 200, 4),
+    ([1300, 900], 16, 8, 128, 100, 5), ([1100, 1290], 8, 8, 64, 300, 0),  # key tiles for every SM: walked in step
 ]
 
 
