@@ -282,10 +282,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       named_barrier(2, 256);
       return s_half[0][row] + s_half[1][row];
     };
-    for (int j = 0; ok && j < n; ++j) {
+    // (with one tile a warp that gave up, here or before, still comes to the barrier of row_sum:
+    // the others may not have)
+    for (int j = 0; (ok || n == 1) && j < n; ++j) {
       const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
-      // (with one tile a warp that gave up still comes to the barrier of row_sum)
-      if (!(ok = wait(bar(SFULL + b), (j >> 1) & 1)) && n > 1) break;
+      ok = wait(bar(SFULL + b), (j >> 1) & 1) && ok;
+      if (!ok && n > 1) break;
       tc::fence_after();
       const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
       const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)

@@ -633,3 +633,27 @@ def test_waits_run_out_and_recover():
     for f, w in zip(calls, want):
         assert torch.equal(f(), w)
     assert nsa.nsa_device_status() == 0
+
+
+def test_waits_of_one_key_tile_run_out_and_recover():
+    """Rows whose keys lie in one tile have a block-wide sum in their backward: a warp that gave up
+    comes to it like the others, so the kernel returns."""
+    assert nsa.nsa_device_status(reset=True) == 0
+    x = [_bf((1, 64, h, 128), _gen(95 + i)).cuda() for i, h in enumerate((16, 2, 2))]
+    lse = torch.empty(64, 16, device="cuda")
+    o = nsa.nsa_swa_sink_fwd(*x, 40, 4, lse=lse)
+    want = nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 40, 4)
+    try:
+        for limit in (1, 1000, 1500, 2000, 2500, 3000, 4000):
+            torch.empty(96 << 20, dtype=torch.float32, device="cuda").fill_(1.0)
+            torch.cuda.synchronize()
+            nsa.nsa_set_wait_limit_ns(limit)
+            nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 40, 4)
+            torch.cuda.synchronize()
+            nsa.nsa_device_status(reset=True)  # (whether a wait ran out depends on the clock)
+    finally:
+        nsa.nsa_set_wait_limit_ns(0)
+        nsa.nsa_device_status(reset=True)
+    for a, b in zip(nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 40, 4), want):
+        assert torch.equal(a, b)
+    assert nsa.nsa_device_status() == 0
