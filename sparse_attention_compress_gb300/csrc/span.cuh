@@ -226,6 +226,10 @@ __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_
   }
 }
 
+// A wait ran out in an earlier kernel or CTA: the block leaves.  One answer for all its threads
+// (the word may change between their reads, and some would go on without the others' set-up).
+__device__ __forceinline__ bool stopped() { return __syncthreads_or(tc::device_status_set()); }
+
 // Bounded wait of a warp for phase `parity` (tc::warp_wait's rules: abort flag, time limit,
 // status word), inline: a call would keep the caller's registers in local memory across it,
 // and with nearly all of L1 given to shared memory that is a trip to L2 or DRAM per wait.

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
-  if (tc::device_status_set()) return;
+  if (stopped()) return;
   const Waits wait(abort);
   const int rows_tok = NH * p.tpc;  // tokens of this CTA
   const bool whole = (int64_t)blockIdx.x < p.n_whole;

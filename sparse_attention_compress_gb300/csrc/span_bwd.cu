@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
-  if (tc::device_status_set()) return;
+  if (stopped()) return;
   const Waits wait(abort);
   const int seq = blockIdx.y, g = blockIdx.z;
   const int64_t start = seq_start(p.seqs, seq);
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       return;
     }
   }
-  if (tc::device_status_set()) return;
+  if (stopped()) return;
   const Waits wait(abort);
   // items of a (sequence, kv-head): the chunks of far queries of the sink tiles, then every
   // key tile with the queries within its window

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
-  if (tc::device_status_set()) return;
+  if (stopped()) return;
   const Waits wait(abort);
   const int seq = blockIdx.y, g = blockIdx.z;
   const int kv_len = cached_len(p.keys, seq);

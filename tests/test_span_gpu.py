@@ -657,3 +657,44 @@ def test_waits_of_one_key_tile_run_out_and_recover():
     for a, b in zip(nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 40, 4), want):
         assert torch.equal(a, b)
     assert nsa.nsa_device_status() == 0
+
+
+def test_calls_after_a_timeout_return_and_recover():
+    """While the status word is set every block leaves at once (joined outputs then hold anything); after
+    a reset the calls are right."""
+    assert nsa.nsa_device_status(reset=True) == 0
+    c = Cache([700, 90], 2, 128, 64, 97)
+    q, cu = _queries([150, 20], 16, 128, 98)
+    q, cu = q.cuda(), cu.cuda()
+    kw = dict(cu_seqlens=cu, max_seqlen=150)
+    k = _bf((170, 2, 128), _gen(99)).cuda()
+    lse = torch.zeros(170, 16, device="cuda")
+
+    def step(fill):
+        out = [torch.full_like(q, fill), torch.full_like(q, fill), torch.full_like(q, fill), torch.full_like(k, fill),
+               torch.full_like(k, fill), c.weights(fill)]
+        nsa.nsa_paged_attn_fwd(q, *c.args, out=out[0], **kw)
+        nsa.nsa_swa_sink_fwd(q, k, k, 40, 4, out=out[1], **kw)
+        nsa.nsa_swa_sink_bwd(q, k, k, q, lse, q, 40, 4, dq=out[2], dk=out[3], dv=out[4], **kw)
+        nsa.nsa_paged_attn_weights(q, c.k_pages, lse, *c.args[2:], out=out[5], **kw)
+        torch.cuda.synchronize()
+        return out
+
+    want = step(0.0)
+    try:
+        torch.empty(96 << 20, dtype=torch.float32, device="cuda").fill_(1.0)
+        torch.cuda.synchronize()
+        nsa.nsa_set_wait_limit_ns(1)
+        nsa.nsa_paged_attn_fwd(q, *c.args, **kw)
+        nsa.nsa_swa_sink_bwd(q, k, k, q, lse, q, 40, 4, **kw)
+        nsa.nsa_paged_attn_weights(q, c.k_pages, lse, *c.args[2:], out=c.weights(0.0), **kw)
+        torch.cuda.synchronize()
+        nsa.nsa_set_wait_limit_ns(0)
+        assert nsa.nsa_device_status() == 4
+        got = step(7.0)
+        assert torch.all(got[2] == 7.0) and torch.all(got[5] == 7.0)
+    finally:
+        nsa.nsa_set_wait_limit_ns(0)
+        nsa.nsa_device_status(reset=True)
+    for a, b in zip(step(0.0), want):
+        assert torch.equal(a, b)
