@@ -544,12 +544,13 @@ NSA_API nsa_status nsa_paged_attn_weights(const nsa_shape* shape, const void* q,
  * new_table's pages, so the pages listed before may then be freed (they stay unchanged: pages
  * shared with other sequences need no care).  Keys keep the rotary phase, if any, that they
  * were stored with.  The heads of a sequence may keep different positions.
- *   new_table  device int32 [n_seqs, new_max_pages]; its pages must not be among those the
- *              call reads or writes for another sequence; rows whose entry is no page are
- *              dropped
+ *   new_table  device int32 [n_seqs, new_max_pages]; none of its pages may be listed twice or
+ *              be in block_table (for any sequence, its own included: a row would be written
+ *              while another one is still to be read from there); rows whose entry is no page
+ *              are dropped
  *   keep       device int32 [n_seqs, h_kv, budget] out: kept positions, ascending, -1 padded
  *   new_lens   device int32 [n_seqs] out: min(cache_lens, budget); may be cache_lens itself
- * Requires 1 <= budget, n_sink + n_recent <= budget, new_max_pages * page_size >=
+ * Requires 1 <= budget <= 2^28, n_sink + n_recent <= budget, new_max_pages * page_size >=
  * min(budget, max_pages * page_size); cache->weights. */
 NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_cache* cache, int budget, int n_sink,
                                    int n_recent, const int32_t* new_table, int new_max_pages, int32_t* keep,

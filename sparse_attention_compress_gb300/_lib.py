@@ -818,7 +818,8 @@ def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n
 def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_table, budget, n_sink=0, n_recent=0, *,
                     keep=None, new_lens=None, stream=None):
     """Cut every cache to at most `budget` keys per kv-head: the first n_sink, the last n_recent and
-    the heaviest others, copied in order to new_table's pages.  Returns (keep [n_seqs, Hkv,
+    the heaviest others, copied in order to new_table's pages (none of them in block_table, none
+    listed twice).  Returns (keep [n_seqs, Hkv,
     budget] int32, -1 padded, and new_lens [n_seqs] int32)."""
     fn = "nsa_paged_evict"
     dev = k_pages.device

@@ -1213,6 +1213,7 @@ nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_cache* c
   NSA_REQUIRE(cache->weights != nullptr, NSA_ERR_INVALID, "nsa_paged_evict: the cache has no weights");
   NSA_REQUIRE(budget >= 1 && n_sink >= 0 && n_recent >= 0 && (int64_t)n_sink + n_recent <= budget, NSA_ERR_INVALID,
               "nsa_paged_evict: needs budget >= 1, n_sink >= 0, n_recent >= 0, n_sink + n_recent <= budget");
+  NSA_REQUIRE(budget <= 1 << 28, NSA_ERR_UNSUPPORTED, "nsa_paged_evict: budget must be <= 2^28");
   const int64_t cap = (int64_t)cache->max_pages * cache->page_size;
   NSA_REQUIRE(new_max_pages >= 1 && (int64_t)new_max_pages * cache->page_size >= (budget < cap ? budget : cap),
               NSA_ERR_INVALID, "nsa_paged_evict: new_table's rows do not hold the budget");

@@ -164,6 +164,7 @@ def test_calls_refused():
     assert _evict(_cache(weights=None)) == 1
     assert _evict(c, budget=0) == 1 and _evict(c, sink=-1) == 1 and _evict(c, sink=60, recent=5) == 1
     assert _evict(c, n=-1) == 1 and _evict(c, n=65536) == 2 and _evict(c, d=96) == 2
+    assert _evict(_cache(max_pages=1), budget=(1 << 28) + 1) == 2
     assert _evict(c, budget=65) == 1  # one page of 64 does not hold it
     assert _evict(c, table=None) == 1 and _evict(c, keep=None) == 1 and _evict(c, lens=MIS) == 1
     assert _sink_fwd(s, window=0) == 1 and _sink_fwd(s, n_sink=-1) == 1 and _sink_fwd(s, q=None) == 1
