@@ -479,6 +479,7 @@ NSA_API nsa_status nsa_layer_bwd(const nsa_shape* shape, const void* q, const vo
  *                     included.  Lengths outside [0, max_pages * page_size] are clamped.
  * The values at positions below cache_lens have to be finite; memory past them, and pages
  * that no table row names, may hold anything.
+ * Outputs must not overlap inputs but where a call says so.
  * page_size is a power of two in [16, 256]; bf16; d in {64, 128}; h/h_kv <= 128; at most 2^28
  * positions per table row, 2^28 tokens, 65535 sequences. */
 typedef struct nsa_paged_cache {
@@ -567,7 +568,8 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  * The backward returns the gradients for an upstream d_o (formulas of nsa_sparse_bwd over
  * the seen keys, with D = sum_e p_e dp_e where a row's keys are few, and everywhere for dk; P
  * and dS as bf16 in their products); o and lse are the forward's.  dk and
- * dv are written for every row of a sequence.  Deterministic.  Requires n_sink <= 1024. */
+ * dv are written for every row of a sequence.  Outputs must not overlap inputs.
+ * Deterministic.  Requires n_sink <= 1024. */
 NSA_API size_t nsa_swa_sink_fwd_workspace_size(const nsa_shape* shape, int window, int n_sink);
 NSA_API nsa_status nsa_swa_sink_fwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,
                                     int n_sink, float scale, void* o, float* lse, void* workspace,

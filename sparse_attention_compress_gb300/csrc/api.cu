@@ -1144,6 +1144,12 @@ nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, const voi
                      "nsa_paged_append");
 }
 
+// Outputs are written while inputs of other rows are still to be read.
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // The bound of the cached lengths that divides the keys (none given: no bound).
 static int span_keys(int64_t max_cache_len) {
   return max_cache_len <= 0 || max_cache_len > (int64_t)1 << 28 ? 1 << 28 : (int)max_cache_len;
@@ -1173,6 +1179,8 @@ nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_p
   const int keys = span_keys(max_cache_len);
   const size_t need = span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, keys, window, n_sink);
   if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  const size_t qb = (size_t)s.tokens * shape->h * shape->d * 2;
+  NSA_REQUIRE(!overlap(o, qb, q, qb), NSA_ERR_INVALID, "nsa_paged_attn_fwd: o overlaps q");
   if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
   return cuda_status(launch_span_attn(s, q, &c, cache->k_pages, cache->v_pages, shape->h, shape->h_kv, shape->d, keys,
                                       window, n_sink, scale, o, lse, workspace, stream),
@@ -1258,6 +1266,9 @@ nsa_status nsa_swa_sink_fwd(const nsa_shape* shape, const void* q, const void* k
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(NSA_ERR_INVALID, "nsa_swa_sink_fwd: lse misaligned");
   const size_t need = span_attn_workspace_bytes(s, shape->h, shape->h_kv, shape->d, s.max_len, window, n_sink);
   if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  const size_t qb = (size_t)s.tokens * shape->h * shape->d * 2, kb = (size_t)s.tokens * shape->h_kv * shape->d * 2;
+  NSA_REQUIRE(!overlap(o, qb, q, qb) && !overlap(o, qb, k, kb) && !overlap(o, qb, v, kb), NSA_ERR_INVALID,
+              "nsa_swa_sink_fwd: o overlaps an input");
   if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
   return cuda_status(launch_span_attn(s, q, nullptr, k, v, shape->h, shape->h_kv, shape->d, s.max_len, window, n_sink,
                                       scale, o, lse, workspace, stream),
@@ -1295,6 +1306,12 @@ nsa_status nsa_swa_sink_bwd(const nsa_shape* shape, const void* q, const void* k
               "nsa_swa_sink_bwd: lse must be non-null and 4-byte aligned");
   const size_t need = span_bwd_workspace_bytes(s, shape->h, shape->h_kv, shape->d, window, n_sink);
   if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  const size_t qb = (size_t)s.tokens * shape->h * shape->d * 2, kb = (size_t)s.tokens * shape->h_kv * shape->d * 2;
+  const struct { const void* p; size_t bytes; } t[8] = {{dq, qb}, {dk, kb}, {dv, kb}, {q, qb}, {k, kb}, {v, kb}, {o, qb}, {d_o, qb}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      NSA_REQUIRE(!overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes), NSA_ERR_INVALID,
+                  "nsa_swa_sink_bwd: a gradient overlaps another tensor of the call");
   if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
   return cuda_status(launch_span_bwd(s, q, k, v, shape->h, shape->h_kv, shape->d, window, n_sink, scale, o, lse, d_o,
                                      dq, dk, dv, workspace, stream),

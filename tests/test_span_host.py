@@ -173,6 +173,23 @@ def test_calls_refused():
     assert need > 0 and _sink_bwd(s, n=need - 1) == 1 and _sink_bwd(s, ws=None) == 1
 
 
+def test_overlapping_outputs_refused():
+    """Addresses are compared, never read."""
+    lib, s, c = nsa.load(), ctypes.byref(_shape()), _cache()
+    tokens, h, hk, d = _shape().batch * _shape().seqlen, _shape().h, _shape().h_kv, _shape().d
+    qb, kb, at = tokens * h * d * 2, tokens * hk * d * 2, 1 << 32
+    q, k, v, o, d_o, dq, dk, dv = (at + i * (qb + 256) for i in range(8))
+    assert lib.nsa_paged_attn_fwd(s, q, ctypes.byref(c), 0, 0, 0, 0.0, q, None, FAKE, 1 << 40, None) == 1
+    assert b"overlap" in lib.nsa_last_error()
+    assert lib.nsa_paged_attn_fwd(s, q, ctypes.byref(c), 0, 0, 0, 0.0, q + qb - 16, None, FAKE, 1 << 40, None) == 1
+    for bad in (q, q - qb + 16, k, k + kb - 16, v):
+        assert lib.nsa_swa_sink_fwd(s, q, k, v, 64, 4, 0.0, bad, None, FAKE, 1 << 40, None) == 1
+        assert b"overlap" in lib.nsa_last_error()
+    for bad in ((q, dk, dv), (dq, k, dv), (dq, dk, o), (d_o, dk, dv), (dq, dq, dv), (dq, dk, dk), (dq, dk, dk + kb - 16)):
+        assert lib.nsa_swa_sink_bwd(s, q, k, v, 64, 4, 0.0, o, FAKE, d_o, *bad, FAKE, 1 << 40, None) == 1
+        assert b"overlap" in lib.nsa_last_error()
+
+
 def test_nothing_to_do_is_no_error():
     empty = _shape(batch=0)
     assert _append(empty, _cache()) == 0 and _attn(empty, _cache()) == 0 and _weights(empty, _cache()) == 0
