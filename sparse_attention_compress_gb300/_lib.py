@@ -712,7 +712,7 @@ def _span_shape(fn, q, h_kv, d, device, cu_seqlens, max_seqlen):
     """(tokens, shape struct, number of sequences) of new tokens [B, T, H, d] or packed
     [tokens, H, d]."""
     dims = q.shape if isinstance(q, torch.Tensor) else ()
-    if len(dims) not in (3, 4) or dims[-1] != d or dims[-2] % h_kv:
+    if len(dims) not in (3, 4) or dims[-1] != d or h_kv < 1 or dims[-2] % h_kv:
         raise ValueError(f"{fn}: expected [..., heads, {d}] with heads a multiple of {h_kv}, got {tuple(dims)}")
     index = device.index if device.type == "cuda" else -1
     if not _fits(q, _BF16, dims, index):

@@ -841,7 +841,8 @@ __global__ void __launch_bounds__(2 * D) key_sum_kernel(const BwdParams p, int n
     const int64_t step = (int64_t)2 * p.sink_rows * D;
     const float* src = p.part + (((int64_t)seq * p.hkv + g) * p.sink_tiles + kt) * (1 + p.n_far) * step +
                        ((int64_t)x * p.sink_rows + key % KT) * D + c;
-    const int parts = 1 + (L - near_end + p.far_tokens - 1) / p.far_tokens;
+    // (no more than there are, should a sequence be longer than the call's longest length)
+    const int parts = 1 + min(p.n_far, (L - near_end + p.far_tokens - 1) / p.far_tokens);
 #pragma unroll 4
     for (int i = p.n_near > 1; i < parts; ++i) acc += src[i * step];
   }

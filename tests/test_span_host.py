@@ -224,6 +224,8 @@ def test_python_checks():
     q = torch.zeros(5, 4, 64, dtype=bf)
     cu = torch.zeros(3, dtype=i32)
     assert _lib._span_shape("f", q, 2, 64, q.device, cu, 3)[2] == 2
+    with pytest.raises(ValueError):
+        _lib._span_shape("f", q, 0, 64, q.device, cu, 3)
     for args in ((q.float(), cu), (q[:, :3], cu), (q[..., :32], cu), (q[:, ::2], cu), (q, cu.long()), (q, cu[:1]),
                  (q[None], cu)):
         with pytest.raises((TypeError, ValueError)):
