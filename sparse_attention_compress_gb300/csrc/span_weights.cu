@@ -220,10 +220,12 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
         tc::fence_after();
         uint64_t a2[4] = {0, 0, 0, 0};
         const uint32_t s_t = t_lane + b * p.buf_cols;
-        auto sum = [&](float (&sv)[32], int c) {
+        // (a tile whose every column is seen goes without masks, in code of its own: joined, the
+        // two ways would meet in copies of the scores)
+        auto sum = [&](auto full, float (&sv)[32], int c) {
           const float4* l4 = reinterpret_cast<const float4*>(lse + c);
-          const uint32_t see = bits(c_lo - c, c_hi - c);
-          if (!__all_sync(0xffffffffu, see == ~0u)) {
+          if constexpr (!decltype(full)::value) {
+            const uint32_t see = bits(c_lo - c, c_hi - c);
             // (a column of no query holds whatever lies past the tile's rows)
 #pragma unroll
             for (int e = 0; e < 32; ++e) sv[e] = (see >> e) & 1u ? sv[e] : kNegInf;
@@ -241,21 +243,27 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
         float sa[32], sb[32];
         tc::tmem_ld32_nowait(s_t, sa);
         tmem_wait_ld(sa);
-        tmem_ld32_if(p.cols > 32, s_t + 32, sb);
-        sum(sa, 0);
-        if (p.cols > 32) {
+        if (!FEW && __all_sync(0xffffffffu, c_lo == 0 && c_hi >= ROWS)) {
+          constexpr std::true_type full{};
+          tc::tmem_ld32_nowait(s_t + 32, sb);
+          sum(full, sa, 0);
           tmem_wait_ld(sb);
-          tmem_ld32_if(p.cols > 64, s_t + 64, sa);
-          sum(sb, 32);
-        }
-        if (p.cols > 64) {
+          tc::tmem_ld32_nowait(s_t + 64, sa);
+          sum(full, sb, 32);
           tmem_wait_ld(sa);
-          tmem_ld32_if(p.cols > 96, s_t + 96, sb);
-          sum(sa, 64);
-        }
-        if (p.cols > 96) {
+          tc::tmem_ld32_nowait(s_t + 96, sb);
+          sum(full, sa, 64);
           tmem_wait_ld(sb);
-          sum(sb, 96);
+          sum(full, sb, 96);
+        } else {
+          constexpr std::false_type full{};
+          sum(full, sa, 0);
+#pragma unroll 1
+          for (int c = 32; c < p.cols; c += 32) {
+            tc::tmem_ld32_nowait(s_t + c, sa);
+            tmem_wait_ld(sa);
+            sum(full, sa, c);
+          }
         }
         tc::fence_before();
         __syncwarp();
