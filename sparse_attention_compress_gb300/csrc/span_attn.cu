@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
             const uint32_t b2 = (bad >> (c / GRAN)) & 3u;
             see &= ~((b2 & 1u ? 0xffffu : 0u) | (b2 & 2u ? 0xffff0000u : 0u));
           }
+          if (__all_sync(0xffffffffu, see == ~0u)) return;  // (a boundary crosses one or two of the four)
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
         };
