@@ -294,20 +294,19 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        tmem_ld32_if(c < nc, s_t + c, sv + c);
+        tc::tmem_ld32_nowait(s_t + c, sv + c);
       const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
       const bool all = __all_sync(0xffffffffu, j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64));
-      auto mask = [&](float (&y)[64], float out) {  // unseen columns
+      tmem_wait_ld(sv);
+      tmem_wait_ld(sv + 32);
+      if (!all) {
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           const uint32_t see = bits(j_lo - c0 - c, j_hi - c0 - c) | bits(0, min(j_sink, j_hi) - c0 - c);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[c + e] = (see >> e) & 1u ? y[c + e] : out;
+          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
         }
-      };
-      tmem_wait_ld(sv);
-      tmem_wait_ld(sv + 32);
-      if (!all) mask(sv, kNegInf);
+      }
 #pragma unroll
       for (int c = 0; c < 64; c += 2) {
         const float2 y = unpair(fma2(pair(sv[c], sv[c + 1]), scale2, nl2));
@@ -320,13 +319,19 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       float dp[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        tmem_ld32_if(c < nc, p_t + c, dp + c);
+        tc::tmem_ld32_nowait(p_t + c, dp + c);
       tmem_wait_ld(dp);
       tmem_wait_ld(dp + 32);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(PFREE));
-      if (!all) mask(dp, 0.f);  // (columns past the tile's hold anything)
+      // (an unseen key's p is 0 and its dp finite; columns past the tile's hold anything)
+#pragma unroll
+      for (int c = 0; c < 64; c += GRAN)
+        if (c >= nc) {
+#pragma unroll
+          for (int e = 0; e < GRAN; ++e) dp[c + e] = 0.f;
+        }
       if (n == 1) {
         uint64_t d2 = 0;
 #pragma unroll
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        tmem_ld32_if(c < nc, s_t + c, sv + c);
+        tc::tmem_ld32_nowait(s_t + c, sv + c);
       const bool all = c_lo <= 0 && c_hi >= 64;
       const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
       tmem_wait_ld(sv);
@@ -731,7 +736,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       float dp[64];
 #pragma unroll
       for (int c = 0; c < 64; c += 32)
-        tmem_ld32_if(c < nc, p_t + c, dp + c);
+        tc::tmem_ld32_nowait(p_t + c, dp + c);
       tmem_wait_ld(dp);
       tmem_wait_ld(dp + 32);
 #pragma unroll
