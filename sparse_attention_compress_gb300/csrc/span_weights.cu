@@ -239,6 +239,11 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
             a2[((e >> 1) + 1) & 3] = add2(a2[((e >> 1) + 1) & 3], pair(ex2(z.x), ex2(z.y)));
           }
         };
+        auto release = [&]() {  // the buffer's scores are in registers
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(SFREE + b));
+        };
         // 32 columns at a time, the next ones on their way while these are summed
         float sa[32], sb[32];
         tc::tmem_ld32_nowait(s_t, sa);
@@ -254,6 +259,7 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
           tc::tmem_ld32_nowait(s_t + 96, sb);
           sum(full, sa, 64);
           tmem_wait_ld(sb);
+          release();
           sum(full, sb, 96);
         } else {
           constexpr std::false_type full{};
@@ -264,10 +270,8 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
             tmem_wait_ld(sa);
             sum(full, sa, c);
           }
+          release();
         }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(SFREE + b));
         const float2 s2 = unpair(add2(add2(a2[0], a2[1]), add2(a2[2], a2[3])));
         acc += s2.x + s2.y;
       }
