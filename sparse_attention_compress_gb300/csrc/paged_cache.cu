@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
                                                                    int budget, int n_sink, int n_recent, int room,
                                                                    int32_t* __restrict__ keep) {
   extern __shared__ int s_hist[];  // [2048][kCopies], then the ranks
+  launch_dependents();
   __shared__ int s_gt[32], s_eq[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(Keys c, Keys to, __nv_b
   const int32_t* list = keep + ((int64_t)seq * hkv + g) * budget;
   const int i = blockIdx.x * PER + threadIdx.x / CH, ch = threadIdx.x % CH;
   const int64_t cap = (int64_t)to.max_pages << to.page_log2;
+  wait_primary();
   if (i >= budget) return;
   const int src = list[i];
   // the kept count of head 0 (the same for every head): the list is filled from the front
@@ -252,13 +254,8 @@ cudaError_t launch_paged_evict(int n_seqs, const PagedView& cache, const PagedVi
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int per = 256 / (d / 8);
   const dim3 grid((budget + per - 1) / per, hkv, n_seqs);
-  if (d == 64)
-    span::evict_copy_kernel<64><<<grid, 256, 0, st>>>(c, t, (__nv_bfloat16*)k_pages, (__nv_bfloat16*)v_pages, weights,
-                                                      hkv, budget, keep, new_lens);
-  else
-    span::evict_copy_kernel<128><<<grid, 256, 0, st>>>(c, t, (__nv_bfloat16*)k_pages, (__nv_bfloat16*)v_pages,
-                                                       weights, hkv, budget, keep, new_lens);
-  return cudaGetLastError();
+  return span::launch_second(d == 64 ? span::evict_copy_kernel<64> : span::evict_copy_kernel<128>, grid, 256, 0, st, c, t,
+                             (__nv_bfloat16*)k_pages, (__nv_bfloat16*)v_pages, weights, hkv, budget, keep, new_lens);
 }
 
 }  // namespace nsa

@@ -349,6 +349,16 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(cols) : "memory");
 }
 
+// A call's kernels follow one another without the gap of a launch: the second one's blocks start
+// as the first one's last blocks leave room, set themselves up, and wait for the first to be
+// complete before they read what it wrote.  (Every block of a first kernel says so at its start;
+// every block of a second one waits, so that whoever waits for the second waits for both.)
+// 3 x 1001 tokens forward and backward 80 -> 76 us, a cache of 4096 keys cut to 1024 13.6 -> 12.8;
+// the attention's parts, whose waiting blocks would take room from the last round of others, gain
+// nothing (decode 146 -> 148) and are joined by an ordinary launch.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // Output rows staged in shared memory (the layout of the tiles: 64-column groups `group`
 // bytes apart, 16-byte chunk ch of row r at chunk ch ^ (r & 7)), so that they leave by TMA
 // or in whole lines: a warp whose threads wrote a row each would touch 32 lines per store.
@@ -409,6 +419,20 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 }
 
 // ---------------------------------------------------------------------- host side
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...);
+}
 // Maps of K (or V): the tile box and the 16-row box.
 inline bool key_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, const Keys& c, int hkv, int D,
                      int64_t packed_rows) {

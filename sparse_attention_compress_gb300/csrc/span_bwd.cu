@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
+  launch_dependents();
   if (stopped()) return;
   const Waits wait(abort);
   const int seq = blockIdx.y, g = blockIdx.z;
@@ -472,7 +473,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       return;
     }
   }
-  if (stopped()) return;
+  launch_dependents();
+  if (stopped()) {
+    wait_primary();
+    return;
+  }
   const Waits wait(abort);
   // items of a (sequence, kv-head): the chunks of far queries of the sink tiles, then every
   // key tile with the queries within its window
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int chunk = far ? (int)blockIdx.x % p.n_far : -1;
   const int share = far ? 0 : ((int)blockIdx.x - n_far_items) % p.n_near;
   const int key0 = kt * KT;
-  if (key0 >= L) return;
+  if (key0 >= L) return;  // (some block of the call has keys, and waits)
   const int near_end = min(L, key0 + KT - 1 + p.window);
   const int near_tiles = (near_end - key0 + p.tpc - 1) / p.tpc;
   const int t_lo = far ? near_end + chunk * p.far_tokens : key0 + near_tiles * share / p.n_near * p.tpc;
@@ -587,6 +592,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         nd[i] = in ? __ldg(p.ndsum + r0 + at[i]) : 0.f;
       }
     };
+    wait_primary();  // (K and V are on their way)
     fetch(token_of(0));
     Ring<kNQ> rq;
     Ring<kND> rd;
@@ -829,6 +835,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 // threads) or dV.
 template <int D>
 __global__ void __launch_bounds__(2 * D) key_sum_kernel(const BwdParams p, int n_kt) {
+  wait_primary();
   const int key = blockIdx.x, g = blockIdx.y, seq = blockIdx.z;
   const int L = seq_len(p.seqs, seq);
   if (key >= L) return;
@@ -913,11 +920,10 @@ cudaError_t launch_bwd_d(BwdParams& p, const BwdLayout& l, cudaStream_t st) {
       mq, md, mk, mk16, mv, mv16, mo, mdq, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int n_kt = (s.max_len + KT - 1) / KT, items = l.sink_tiles * l.n_far + n_kt * l.n_near;
-  dkv_kernel<D><<<dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem, st>>>(mq, md, mk, mk16, mv, mv16, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || (l.n_far == 0 && l.n_near == 1)) return e;
+  e = launch_second(dkv_kernel<D>, dim3(items, s.n_seqs, p.hkv), kDkvThreads, dkv_smem, st, mq, md, mk, mk16, mv, mv16, p);
+  if (e != cudaSuccess || (l.n_far == 0 && l.n_near == 1)) return e;
   const int keys = l.n_near > 1 ? s.max_len : std::min(p.n_sink, s.max_len);
-  key_sum_kernel<D><<<dim3(keys, p.hkv, s.n_seqs), 2 * D, 0, st>>>(p, n_kt);
-  return cudaGetLastError();
+  return launch_second(key_sum_kernel<D>, dim3(keys, p.hkv, s.n_seqs), 2 * D, 0, st, p, n_kt);
 }
 
 }  // namespace span
