@@ -8,14 +8,22 @@
 // rounding of the bf16 output itself).
 //
 // A tile is 128 rows = 128 / group tokens x the heads of a kv-group, so each K / V tile is
-// read once for the whole group.  Two forms of one kernel:
-//   many rows   a CTA (one an SM) holds two row tiles ("halves", four softmax warps each, one
+// read once for the whole group.  Three forms of one kernel:
+//   long        a CTA (one an SM) holds two row tiles ("halves", four softmax warps each, one
 //               row a thread) over common K and V rings; while one half's softmax runs the
-//               tensor cores work for the other.
-//   FEW         (a decode step, a few speculative tokens: at most 48 rows a sequence and
-//               kv-head) a CTA holds one row tile whose Q takes only the rows it has, so
-//               that two CTAs share an SM and keep HBM busy through each other's starts and
-//               ends; the rows past Q's are whatever lies there and stay in their own lanes.
+//               tensor cores work for the other.  Bound by the tensor cores and, beside them,
+//               by the instructions that turn S into P: 2048 tokens x 64 heads at 32768 keys,
+//               d = 128, 1.46 ms (1460 TFLOP/s, 77% of a large library product).
+//   short       (spans of at most 16 key tiles) a CTA holds one row tile over one ring, so
+//               that two CTAs share an SM and a start or an end, which the few tiles do not
+//               hide, runs beside the other's products: 65536 tokens x 64 heads, window 512,
+//               1.53 ms (1.67 in the long form).
+//   few         (a decode step, a few speculative tokens: at most 48 rows a sequence and
+//               kv-head) as short, Q taking only the rows it has and the ring the rest, for
+//               HBM: 32 tokens over caches of 16384 to 32768 keys x 2 kv-heads 146 us
+//               (5.5 TB/s, 81% of a copy); one token over 4096 keys 15 us, the length of
+//               its two launches and of one CTA's start and end.  The rows past Q's are
+//               whatever lies there and stay in their own lanes.
 // Work units (row tile, sequence, kv-head) that would not fill the SMs evenly have their keys
 // divided over several CTAs: each leaves (max, sum, unnormalised o) in the workspace and
 // combine_kernel joins them in a fixed order.  Roles: softmax warps (one row a thread),
@@ -35,18 +43,25 @@ constexpr int kSoftRegs = 208;
 // P may exceed 1 by 2^kLazy before the running maximum moves: the floating-point formats of
 // P, of the sums and of O hold it with the same relative precision.
 constexpr float kLazy = 16.f;
-constexpr int kFewRows = 48;  // what leaves room for two FEW CTAs on an SM
+constexpr int kFewRows = 48;  // what leaves room for two such CTAs on an SM beside three tiles each
 constexpr int kSms = 152;
+// Key tiles of a row tile up to which its CTA shares an SM.  32768 tokens x 64 heads (4 kv-heads,
+// d = 128) short and long: window 64 402 and 475 us, 512 767 and 841, 1024 1131 and 1186, 2048
+// 1841 and 1860, 4096 3230 and 3141; 1024 tokens x 16 heads, window 512, 14.8 and 17.2.
+constexpr int kShortTiles = 16;
 
-template <int D, bool FEW>
+enum Form { kLong, kShort, kFew };
+
+template <int D, int FORM>
 struct Cfg {
-  static constexpr int NH = FEW ? 1 : 2;  // row tiles (halves)
-  static constexpr int THREADS = FEW ? 256 : 384;
+  static constexpr bool ONE = FORM != kLong;
+  static constexpr int NH = ONE ? 1 : 2;  // row tiles (halves)
+  static constexpr int THREADS = ONE ? 256 : 384;
   static constexpr int KV_BYTES = KT * D * 2;
-  // Two rings of tiles, for K and for V.  FEW: one ring holds K and V tiles in turn.
-  static constexpr int N0 = D == 64 ? (FEW ? 6 : 5) : 3, N1 = FEW ? 0 : (D == 64 ? 5 : 2);
-  static constexpr uint32_t TMEM = FEW ? 256 : 512;
-  static constexpr int OTHER_REGS = FEW ? 40 : 56;
+  // Two rings of tiles, for K and for V.  ONE: one ring holds K and V tiles in turn.
+  static constexpr int N0 = D == 64 ? (FORM == kFew ? 6 : 5) : (FORM == kShort ? 2 : 3), N1 = ONE ? 0 : (D == 64 ? 5 : 2);
+  static constexpr uint32_t TMEM = ONE ? 256 : 512;
+  static constexpr int OTHER_REGS = ONE ? 40 : 56;
   // what the launch must give a thread for the shares to add up
   static constexpr int MIN_REGS = (NH * 128 * kSoftRegs + 128 * OTHER_REGS + THREADS - 1) / THREADS;
 };
@@ -97,16 +112,17 @@ __device__ __forceinline__ int last_in_stage(int last, int st, int ns) {
   return last < st ? -1 : last - (last - st) % ns;
 }
 
-template <int D, bool PAGED, bool FEW>
-__global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
+template <int D, bool PAGED, int FORM>
+__global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
     attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ CUtensorMap tm_o,
                 const AttnParams p) {
-  using C = Cfg<D, FEW>;
+  using C = Cfg<D, FORM>;
+  constexpr bool ONE = C::ONE;  // one row tile, one ring of K and V in turn
   constexpr int NH = C::NH, N0 = C::N0, N1 = C::N1, NS = N0 + N1;
   using B = Bars<NS>;
-  constexpr int kLoad0 = 4 * NH, kIssue = 4 * NH + 1, kLoad1 = FEW ? -1 : 4 * NH + 2;  // warps; 0 .. 4 NH - 1: softmax
+  constexpr int kLoad0 = 4 * NH, kIssue = 4 * NH + 1, kLoad1 = ONE ? -1 : 4 * NH + 2;  // warps; 0 .. 4 NH - 1: softmax
   constexpr uint32_t kO = NH * 128;  // TMEM column of O
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B::COUNT];
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
   const Tiles tiles(off + t0, off + min(t0 + rows_tok, Lq) - 1, p.window, p.n_sink);
   const int a = (int)((int64_t)tiles.n * split / n_splits);
   const int n = (int)((int64_t)tiles.n * (split + 1) / n_splits) - a;  // this CTA's tiles: a .. a + n - 1
-  const int nh = !FEW && t0 + p.tpc < Lq ? 2 : 1;  // halves that have rows
+  const int nh = !ONE && t0 + p.tpc < Lq ? 2 : 1;  // halves that have rows
 
   if (tid == 0) {
     tc::mbar_init(bar(B::Q), 1);
@@ -173,12 +189,12 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
           tc::tma3d(q_s + x * q_bytes + c * p.q_group, &tm_q, c * 64, g * p.R, (int)(start + t0 + x * p.tpc), bar(B::Q));
     }
     __syncwarp();
-    const int cnt = FEW ? 2 * n : n, ns = y ? N1 : N0, first = y ? N0 : 0;
+    const int cnt = ONE ? 2 * n : n, ns = y ? N1 : N0, first = y ? N0 : 0;
     int slot = 0;
     uint32_t phase = 1;
     for (int i = 0; i < cnt; ++i) {
-      const int j = FEW ? i >> 1 : i;
-      const bool is_v = FEW ? (i & 1) : y == 1;
+      const int j = ONE ? i >> 1 : i;
+      const bool is_v = ONE ? (i & 1) : y == 1;
       if (i >= ns && !wait(bar(B::EMPTY + first + slot), phase)) break;
       // the flags of a tile are read by its softmax after S, so they are in place before the
       // K tile's arrival; the missing pages of K and V are the same
@@ -204,12 +220,12 @@ __global__ void __launch_bounds__(Cfg<D, FEW>::THREADS, FEW ? 2 : 1)
     // for both.)
     bool ok = n == 0 || wait(bar(B::Q), 0);
     Ring<N0> rk;
-    Ring<FEW ? N0 : N1> rv;  // FEW: the same ring, one item on
-    constexpr int first_v = FEW ? 0 : N0;
-    if (FEW) rv.next();
+    Ring<ONE ? N0 : N1> rv;  // ONE: the same ring, one item on
+    constexpr int first_v = ONE ? 0 : N0;
+    if (ONE) rv.next();
     auto next = [&](auto& r) {
       r.next();
-      if (FEW) r.next();
+      if (ONE) r.next();
     };
     const uint32_t lead = elect(), q_d = desc_k(q_s), slots_k = desc_k(slots), slots_v = desc_mn(slots);
     constexpr uint32_t kSlot = C::KV_BYTES >> 4;  // in descriptor units
@@ -537,7 +553,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int64_
 
 // How a call is cut.  The number of key tiles follows from the longest cache and the window.
 struct Plan {
-  bool few;
+  int form;
   int tpc, cta_rows, n_splits;
   int64_t units, whole;  // units 0 .. whole - 1 take one CTA, the others n_splits
   size_t ml, bytes;      // workspace: part_o at 0, part_ml at `ml`
@@ -546,14 +562,19 @@ Plan make_plan(const Seqs& s, int h, int hkv, int D, int max_keys, int window, i
   Plan pl{};
   const int R = h / hkv;
   pl.tpc = std::max(1, std::min(ROWS / R, s.max_len));
-  pl.few = (int64_t)s.max_len * R <= kFewRows;
-  const int rows_tok = pl.few ? pl.tpc : 2 * pl.tpc;
+  int64_t span = max_keys;  // keys of a row tile
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + pl.tpc + up16(n_sink) + 2 * GRAN);
+  pl.form = (int64_t)s.max_len * R <= kFewRows ? kFew : span <= kShortTiles * KT ? kShort : kLong;
+  const int rows_tok = pl.form != kLong ? pl.tpc : 2 * pl.tpc;
   pl.cta_rows = rows_tok * R;
   pl.units = ((int64_t)s.max_len + rows_tok - 1) / rows_tok * s.n_seqs * hkv;
   int64_t keys = max_keys;
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + rows_tok + up16(n_sink) + 2 * GRAN);
   const int64_t tiles = std::max<int64_t>(1, (keys + KT - 1) / KT);
-  if (pl.few) {
+  if (pl.form == kShort) {
+    pl.n_splits = 1;
+    pl.whole = pl.units;
+  } else if (pl.form == kFew) {
     // At most four rounds of CTAs (two an SM): ragged caches then even out, and a round is not
     // begun for a few.  32 caches of 16384 to 32768 keys: 146 us with 19 parts (four rounds),
     // 154 with 10 (2.1 rounds), 152 with 15 (3.2), 157 with 29 (6.1).
@@ -585,10 +606,10 @@ Plan make_plan(const Seqs& s, int h, int hkv, int D, int max_keys, int window, i
   return pl;
 }
 
-template <int D, bool PAGED, bool FEW>
+template <int D, bool PAGED, int FORM>
 cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, int64_t ctas, cudaStream_t st) {
-  using C = Cfg<D, FEW>;
-  auto kern = attn_kernel<D, PAGED, FEW>;
+  using C = Cfg<D, FORM>;
+  auto kern = attn_kernel<D, PAGED, FORM>;
   const int smem = C::NH * (D / 64) * p.q_group + (C::N0 + C::N1) * C::KV_BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -624,7 +645,7 @@ cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int 
   p.n_whole = (int)pl.whole;
   p.n_splits = pl.n_splits;
   p.cta_rows = pl.cta_rows;
-  p.q_group = pl.few ? up16(pl.cta_rows) * 128 : ROWS * 128;
+  p.q_group = pl.form == kFew ? up16(pl.cta_rows) * 128 : ROWS * 128;
   p.scale_log2 = scale * kLog2e;
   CUtensorMap m[6];
   if (!query_map(&m[5], o, s.tokens, h, D, p.R, p.tpc) ||
@@ -633,8 +654,13 @@ cudaError_t launch_d(const Seqs& s, const void* q, const Keys& keys, int h, int 
     return cudaErrorInvalidValue;
   const int64_t ctas = pl.whole + (pl.units - pl.whole) * pl.n_splits;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cudaError_t e = keys.table ? (pl.few ? run_attn<D, true, true>(m, p, ctas, st) : run_attn<D, true, false>(m, p, ctas, st))
-                             : (pl.few ? run_attn<D, false, true>(m, p, ctas, st) : run_attn<D, false, false>(m, p, ctas, st));
+  auto run = [&](auto form) {
+    constexpr int F = decltype(form)::value;
+    return keys.table ? run_attn<D, true, F>(m, p, ctas, st) : run_attn<D, false, F>(m, p, ctas, st);
+  };
+  cudaError_t e = pl.form == kFew     ? run(std::integral_constant<int, kFew>{})
+                  : pl.form == kShort ? run(std::integral_constant<int, kShort>{})
+                                      : run(std::integral_constant<int, kLong>{});
   if (e != cudaSuccess || pl.bytes == 0) return e;
   const int64_t rows = (pl.units - pl.whole) * pl.cta_rows;
   if (pl.n_splits >= 8)

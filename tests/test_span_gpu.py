@@ -698,3 +698,64 @@ def test_calls_after_a_timeout_return_and_recover():
         nsa.nsa_device_status(reset=True)
     for a, b in zip(step(0.0), want):
         assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------- long spans
+# The form for spans of more than 16 key tiles (two row tiles a block, two rings).  A bound of
+# the cached lengths that is far too large takes it at any size.
+LONG = [(x[0], x[1], *x[2:6], 0, 0, 1 << 20) for x in CASES if x[6] == 0 and max(x[1]) * x[2] // x[3] > 48] + [
+    ([2700, 2200, 5], [300, 130, 5], 8, 2, 128, 64, 2200, 130, None),
+    ([3000, 0, 2400], [260, 0, 1], 6, 2, 64, 16, 2100, 3, None),
+    ([2600], [2600], 4, 4, 64, 32, 2050, 0, None),
+]
+
+
+@pytest.mark.parametrize("lens,q_lens,H,hk,d,page,window,n_sink,bound", LONG)
+def test_attention_over_long_spans(lens, q_lens, H, hk, d, page, window, n_sink, bound):
+    c = Cache(lens, hk, d, page, 101)
+    q, cu = _queries(q_lens, H, d, 102)
+    lse = torch.full((q.shape[0], H), NAN, device="cuda")
+    kw = dict(window=window, n_sink=n_sink, cu_seqlens=cu.cuda(), max_seqlen=max(q_lens), max_cache_len=bound)
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    assert nsa.nsa_device_status() == 0
+    for b in range(len(lens)):
+        a, e, _, (ro, rl, eo, el) = _reference(c, q, cu, b, window, n_sink, 1.0 / math.sqrt(d))
+        ref.within(o[a:e], ro, eo, f"o of sequence {b}")
+        ref.within(lse[a:e], rl, el, f"lse of sequence {b}")
+
+
+def test_missing_pages_are_masked_in_long_spans():
+    c = Cache([600], 2, 128, 32, 103)
+    hide = [(64, 96), (224, 288), (576, 600)]
+    for lo, hi in hide:
+        c.dev_table[0, lo // 32:-(-hi // 32)] = -1
+    q, cu = _queries([70], 8, 128, 104)
+    lse = torch.empty(70, 8, device="cuda")
+    kw = dict(cu_seqlens=cu.cuda(), max_seqlen=70, max_cache_len=1 << 20)
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    _, _, _, (ro, rl, eo, el) = _reference(c, q, cu, 0, 0, 0, 1 / math.sqrt(128), hide)
+    ref.within(o, ro, eo, "o")
+    ref.within(lse, rl, el, "lse")
+    c.dev_table.fill_(-1)  # nothing left: no key
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("T,H,hk,d,window,n_sink", [
+    (2500, 2, 1, 64, 2100, 10), (2300, 4, 4, 128, 2048, 0), (1990, 2, 2, 128, 1900, 60), (2080, 2, 2, 128, 1900, 60),
+])
+def test_sink_window_forward_at_the_forms_boundary(T, H, hk, d, window, n_sink):
+    """Windows (and lengths) around the 16 key tiles at which the form changes, with rows of no
+    sequence behind the last."""
+    q, k, v = (_bf((T + 3, h, d), _gen(105 + i)) for i, h in enumerate((H, hk, hk)))
+    q[T:], k[T:], v[T:] = NAN, NAN, NAN
+    cu = torch.tensor([0, T - 40, T], dtype=I32, device="cuda")
+    lse, out = torch.full((T + 3, H), 7.0, device="cuda"), torch.full((T + 3, H, d), 7.0, dtype=BF, device="cuda")
+    o = nsa.nsa_swa_sink_fwd(q.cuda(), k.cuda(), v.cuda(), window, n_sink, cu_seqlens=cu, max_seqlen=T - 40, lse=lse,
+                             out=out)
+    assert (o[T:] == 7.0).all() and (lse[T:] == 7.0).all()
+    for a, e in ((0, T - 40), (T - 40, T)):
+        see = ref.visible(range(e - a), e - a, window, n_sink)
+        ro, rl, eo, el = ref.attend(q[a:e].double(), k[a:e].double(), v[a:e].double(), see, 1 / math.sqrt(d))
+        ref.within(o[a:e], ro, eo, "o")
+        ref.within(lse[a:e], rl, el, "lse")
