@@ -75,12 +75,13 @@ NSA_API const char* nsa_last_error(void);
 
 /* Device status word of the current device.  Kernels that wait on other warps, copies
  * or CTAs (the tcgen05 branches of nsa_layer_fwd, the TMA-fed selected attention, the
- * decode step's wait for a row's block list) bound every wait to about a second;
+ * decode step's wait for a row's block list, the attention, weights and backward kernels of
+ * the paged cache and of the window with sinks) bound every wait to about a second;
  * when one runs out the kernel sets the word to NSA_ERR_TIMEOUT, stops waiting, drains
  * its copies in flight and releases its tensor memory, so the context stays usable; while
- * the word is set, the tcgen05 branches and the decode step skip their work.  Outputs of a
- * call that set the word are not valid.  Runtime error reporting, with no counterpart in
- * the pages.
+ * the word is set, the tcgen05 branches, the decode step and the kernels of the paged cache
+ * and the window with sinks skip their work.  Outputs of a call that set the word, or found
+ * it set, are not valid.  Runtime error reporting, with no counterpart in the pages.
  *   status  host int32 out: NSA_OK or NSA_ERR_TIMEOUT
  *   reset   nonzero: clear the word after reading it
  * Blocks until the device is idle (a synchronous copy).  Returns NSA_ERR_INVALID for a
@@ -494,9 +495,9 @@ typedef struct nsa_paged_cache {
 
 /* Write the keys and values of new tokens into the cache.  shape describes the new tokens
  * (its sequences are the table's rows, dense or varlen): token i of a sequence with Lq new
- * tokens goes to position cache_lens[b] - Lq + i.  Tokens whose position is negative, past
- * the table row or in no page are dropped, as are rows past the last sequence.  The weights
- * (if given) of the written positions become 0.
+ * tokens goes to position cache_lens[b] - Lq + i (the length as it is given).  Tokens whose
+ * position is negative, past the table row or in no page are dropped, as are rows past the
+ * last sequence.  The weights (if given) of the written positions become 0.
  *   k_new, v_new  [tokens, h_kv, d] bf16 */
 NSA_API nsa_status nsa_paged_append(const nsa_shape* shape, const void* k_new, const void* v_new,
                                     const nsa_paged_cache* cache, cudaStream_t stream);

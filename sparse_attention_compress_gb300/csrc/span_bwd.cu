@@ -22,6 +22,12 @@
 // into chunks with a CTA each, and where there are fewer key tiles than SMs their own queries
 // are divided too; the fp32 partials are summed in order by key_sum_kernel.
 // No atomics: results are the same on every run.
+//
+// 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.2 ms, dkv 1.95 ms, together
+// 660 TFLOP/s.  dkv keeps the tensor cores busy 72% of its time.  dq is bound by its CTAs' starts
+// and ends (five key tiles each, and 227 KB leave room for one on an SM) and by the chain S - P - dS
+// of a tile: tensor cores 31%.  Small calls are bound by the four kernels' own lengths: 3 sequences
+// of at most 1001 tokens x 16 heads, window 256, forward and backward 77 us.
 #include <algorithm>
 
 #include "launch.h"
