@@ -563,8 +563,8 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  * nsa_paged_attn_fwd then serves.  Token t sees keys max(0, t-window+1) .. t and
  * 0 .. min(n_sink - 1, t).
  *   q, o [tokens, h, d]; k, v [tokens, h_kv, d] bf16;  lse nullable [tokens, h] fp32 out
- *   workspace  nsa_swa_sink_fwd_workspace_size() bytes, 256-byte aligned (0 but for
- *              few rows); NULL allowed when that size is 0
+ *   workspace  nsa_swa_sink_fwd_workspace_size() bytes, 256-byte aligned (0 where no
+ *              row's keys are divided); NULL allowed when that size is 0
  * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^28, 0 <= n_sink <= 2^28.
  * The backward returns the gradients for an upstream d_o (formulas of nsa_sparse_bwd over
  * the seen keys, with D = sum_e p_e dp_e where a row's keys are few, and everywhere for dk; P
