@@ -759,3 +759,110 @@ def test_sink_window_forward_at_the_forms_boundary(T, H, hk, d, window, n_sink):
         ro, rl, eo, el = ref.attend(q[a:e].double(), k[a:e].double(), v[a:e].double(), see, 1 / math.sqrt(d))
         ref.within(o[a:e], ro, eo, "o")
         ref.within(lse[a:e], rl, el, "lse")
+
+
+# ----------------------------------------------------------------------------- places and streams
+def test_sequences_that_share_pages():
+    """A forked sequence lists its parent's pages, and both lists name one page twice."""
+    c = Cache([400, 300], 2, 64, 32, 111)
+    c.dev_table[1, :5] = c.dev_table[0, :5]  # 160 shared tokens
+    c.dev_table[:, 6] = c.dev_table[:, 5]
+    for kv, pool in ((c.k, c.k_pages), (c.v, c.v_pages)):
+        for b in range(2):
+            rows = pool[c.dev_table[b, :-(-c.lens[b] // 32)].long()].reshape(-1, 2, 64)
+            kv[b] = rows[:c.lens[b]].cpu().double()
+    q, cu = _queries([50, 1], 6, 64, 112)
+    o = nsa.nsa_paged_attn_fwd(q.cuda(), *c.args, cu_seqlens=cu.cuda(), max_seqlen=50)
+    for b in range(2):
+        a, e, _, (ro, _, eo, _) = _reference(c, q, cu, b, 0, 0, 1 / 8)
+        ref.within(o[a:e], ro, eo, f"sequence {b}")
+
+
+def test_calls_on_other_streams_at_once():
+    """Two streams' calls run beside one another and give what they give alone."""
+    c = Cache([3000, 900], 2, 128, 64, 113)
+    q, cu = _queries([1, 60], 16, 128, 114)
+    q, cu = q.cuda(), cu.cuda()
+    x = [_bf((1, 500, h, 128), _gen(115 + i)).cuda() for i, h in enumerate((16, 2, 2))]
+    kw = dict(cu_seqlens=cu, max_seqlen=60)
+
+    def serve(s=None):
+        lse = torch.empty(61, 16, device="cuda")
+        o = nsa.nsa_paged_attn_fwd(q, *c.args, lse=lse, stream=s, **kw)
+        return o, nsa.nsa_paged_attn_weights(q, c.k_pages, lse, *c.args[2:], weights=c.weights(1.0), out=c.weights(0.0),
+                                             stream=s, **kw)
+
+    def train(s=None):
+        lse = torch.empty(500, 16, device="cuda")
+        o = nsa.nsa_swa_sink_fwd(*x, 100, 3, lse=lse, stream=s)
+        return o, *nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 100, 3, stream=s)
+
+    want = serve() + train()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        for s in (s1, s2):  # (fills of serve() run on the current stream)
+            s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s1):
+            a = serve(s1)
+        b = train(s2)
+        torch.cuda.synchronize()
+        for g, w in zip(a + b, want):
+            assert torch.equal(g, w)
+
+
+def test_a_cache_past_32_bits():
+    """Pages whose first element lies past 2^31, in a pool that interleaves K and V."""
+    n_pages, page, hk, d, H = 18000, 64, 8, 128, 16
+    pool = torch.empty(n_pages, 2, page, hk, d, dtype=BF, device="cuda")
+    assert (n_pages - 20) * pool.stride(0) > 1 << 31
+    small = torch.empty(20, 2, page, hk, d, dtype=BF, device="cuda")
+    far, near = (torch.arange(k, k + 16, dtype=I32, device="cuda")[None] for k in (n_pages - 20, 0))
+    g = _gen(121)
+    knew, vnew, q = _bf((1, 700, hk, d), g).cuda(), _bf((1, 700, hk, d), g).cuda(), _bf((1, 700, H, d), g).cuda()
+    lens = torch.tensor([700], dtype=I32, device="cuda")
+    out = []
+    for p, table in ((pool, far), (small, near)):
+        k, v = p[:, 0], p[:, 1]
+        w = torch.zeros(p.shape[0], hk, page, device="cuda")
+        nsa.nsa_paged_append(knew, vnew, k, v, table, lens, weights=w)
+        lse = torch.empty(700, H, device="cuda")
+        o = nsa.nsa_paged_attn_fwd(q, k, v, table, lens, lse=lse)
+        last = nsa.nsa_paged_attn_fwd(q[:, -1:].contiguous(), k, v, table, lens)
+        nsa.nsa_paged_attn_weights(q, k, lse, table, lens, weights=w)
+        keep, n = nsa.nsa_paged_evict(k, v, w, table[:, :11].contiguous(), lens, table[:, 11:].contiguous(), 300, 4, 100)
+        rows = p[table[0, 11:16].long()]
+        out.append((o, last, lse, w[table[0].long()], keep, n, rows.reshape(5, 2, page, hk, d)[:4]))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_training_past_32_bits():
+    """Rows whose first element lies past 2^31: with no sinks the last tokens see none but their
+    window, so a call on the end of the sequence alone gives the same rows."""
+    T, H, hk, d, window, cut = 280576, 64, 4, 128, 100, 4096
+    assert (T - cut) * H * d > 1 << 31 and (T - cut) % 128 == 0
+    g = torch.Generator(device="cuda").manual_seed(122)
+    q = torch.randn(1, T, H, d, dtype=BF, device="cuda", generator=g)
+    do = torch.randn(1, T, H, d, dtype=BF, device="cuda", generator=g)
+    k, v = (torch.randn(1, T, hk, d, dtype=BF, device="cuda", generator=g) for _ in range(2))
+
+    def step(*x):
+        lse = torch.empty(x[0].shape[1], H, device="cuda")
+        o = nsa.nsa_swa_sink_fwd(*x[:3], window, 0, lse=lse)
+        return o[0], lse, *(y[0] for y in nsa.nsa_swa_sink_bwd(*x[:3], o, lse, x[3], window, 0))
+
+    whole, end = step(q, k, v, do), step(*(x[:, T - cut:].contiguous() for x in (q, k, v, do)))
+    for a, b in zip(whole[:3], end[:3]):  # o, lse, dq
+        assert torch.equal(a[T - cut + 256:], b[256:])
+    # dk and dv are sums over the window's queries in the order of their tiles, which begins at a
+    # multiple of a round from the sequence's start and so differs between the two calls (0.1% of
+    # the elements come out a step of bf16 apart): these are held to the exact values' bounds, at
+    # one kv-head and the keys whose queries the last 400 tokens hold together with all their keys
+    n, r = 400, H // hk
+    x = [t[0, -n:, -m:].cpu().double() for t, m in ((q, r), (k, 1), (v, 1), (do, r))]
+    see = ref.visible(range(n), n, window, 0)
+    ro, _, eo, _ = ref.attend(*x[:3], see, 1 / math.sqrt(d))
+    want, bounds = ref.gradients(*x, ro, whole[1][-n:, -r:].cpu().double(), see, 1 / math.sqrt(d), eo)
+    for name, got, w, bd in zip(("dk", "dv"), whole[3:], want[1:], bounds[1:]):
+        ref.within(got[-n:, -1:][2 * window:], w[2 * window:], bd[2 * window:], name)
