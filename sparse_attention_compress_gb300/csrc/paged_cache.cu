@@ -2,8 +2,8 @@
 // cache to a budget of keys by accumulated attention weight.  Bound by HBM (and by launch
 // latency for small calls): every row moves once, 16 bytes a lane.  Append of 4 x 2048 tokens
 // x 4 kv-heads, d = 128 9 us (3 TB/s), of 32 tokens 4.4 us; 16 caches of 16384 to 32768 keys x 4
-// kv-heads cut to 4096 keys 78 us (31 us of them the selection, one CTA a (cache, kv-head),
-// bound by the counting passes over shared memory; 3.5 TB/s in all).
+// kv-heads cut to 4096 keys 70 us (25 us of them the selection, one CTA a (cache, kv-head),
+// bound by its instructions on 64 of 152 SMs; the copy runs at 6 TB/s).
 #include <algorithm>
 
 #include "launch.h"
@@ -56,14 +56,15 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 // The `budget` keys of one (sequence, kv-head) that stay, ascending: the first n_sink, the
 // last n_recent, and the best of the others by weight (equal weights: the lower index).
 // A radix selection on 11, 11 and 10 bits (three counting passes, the first while the
-// weights are read; 43 us for 64 caches of 16384 to 32768 keys with four passes of 8 bits)
+// weights are read; 43 us for 64 caches of 16384 to 32768 keys with four passes of 8 bits, 33
+// a key at a time, 25 with four consecutive keys a lane)
 // finds the rank of the last key that stays and how many keys of exactly that rank do; then
 // every warp takes a contiguous run of keys, counts what it keeps, and after one scan over
 // the warps writes its run in order.  Counting in shared-memory integers, so the result is
 // the same on every run.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const float* __restrict__ weights, int hkv,
                                                                    int budget, int n_sink, int n_recent, int room,
-                                                                   int32_t* __restrict__ keep) {
+                                                                   bool vec, int32_t* __restrict__ keep) {
   extern __shared__ int s_hist[];  // [2048][kCopies], then the ranks
   launch_dependents();
   __shared__ int s_gt[32], s_eq[32];
@@ -89,11 +90,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
     const uint32_t r = at < 0 ? 0u : rank_of(w);
     return i < n_sink || i >= L - n_recent ? 0xffffffffu : r;  // above +inf
   };
-  auto rank = [&](int i) -> uint32_t {
-    const int64_t at = place(i);
-    return order(i, at, __ldg(weights + (at < 0 ? 0 : at)));
+  // weights of keys i .. i + 3 (i a multiple of 4: a page holds all four, be they keys or not)
+  auto load4 = [&](int64_t at) -> float4 {
+    const float* src = weights + (at < 0 ? 0 : at);
+    return vec ? __ldg(reinterpret_cast<const float4*>(src))
+               : make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
   };
-  auto get = [&](int i) { return cached ? s_rank[i] : rank(i); };
+  auto order4 = [&](int i, int64_t at, float4 w) {
+    return make_uint4(order(i, at, w.x), order(i + 1, at, w.y), order(i + 2, at, w.z), order(i + 3, at, w.w));
+  };
+  auto get4 = [&](int i) -> uint4 {
+    if (cached) return *reinterpret_cast<const uint4*>(s_rank + i);
+    const int64_t at = place(i);
+    return order4(i, at, load4(at));
+  };
   uint32_t prefix = 0;
   int left = budget;  // keys still to take among those that match the prefix
 #pragma unroll 1
@@ -103,30 +113,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
     for (int i = 0; i < 2048 * kCopies / kSelThreads; ++i) s_hist[tid + i * kSelThreads] = 0;
     __syncthreads();
     if (pass == 0) {
-      constexpr int U = 8;  // weights in flight a thread
-      for (int b = 0; b < L; b += U * kSelThreads) {
+      constexpr int U = 4;  // loads in flight a thread
+      for (int b = 0; b < L; b += U * 4 * kSelThreads) {
         int64_t at[U];
-        uint32_t r[U];
+        float4 w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) at[u] = place(min(b + u * kSelThreads + tid, L - 1));
+        for (int u = 0; u < U; ++u) at[u] = place(min(b + (u * kSelThreads + tid) * 4, (L - 1) & ~3));
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          r[u] = order(b + u * kSelThreads + tid, at[u], __ldg(weights + (at[u] < 0 ? 0 : at[u])));
+        for (int u = 0; u < U; ++u) w[u] = load4(at[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int i = b + u * kSelThreads + tid;
+          const int i = b + (u * kSelThreads + tid) * 4;
           if (i < L) {
-            if (cached) s_rank[i] = r[u];
-            atomicAdd(&s_hist[(r[u] >> 21) * kCopies + lane % kCopies], 1);
+            const uint4 r = order4(i, at[u], w[u]);
+            if (cached) *reinterpret_cast<uint4*>(s_rank + i) = r;
+            const uint32_t re[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (i + e < L) atomicAdd(&s_hist[(re[e] >> 21) * kCopies + lane % kCopies], 1);
           }
         }
       }
     } else {
       const uint32_t mask = pass == 1 ? 0xffe00000u : 0xfffffc00u;
-#pragma unroll 8
-      for (int i = tid; i < L; i += kSelThreads) {
-        const uint32_t r = get(i);
-        if ((r & mask) == prefix) atomicAdd(&s_hist[((r >> shift) & (digits - 1)) * kCopies + lane % kCopies], 1);
+#pragma unroll 4
+      for (int i = tid * 4; i < L; i += 4 * kSelThreads) {
+        const uint4 r = get4(i);
+        const uint32_t re[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((re[e] & mask) == prefix && i + e < L)
+            atomicAdd(&s_hist[((re[e] >> shift) & (digits - 1)) * kCopies + lane % kCopies], 1);
       }
     }
     __syncthreads();
@@ -155,13 +172,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
     left = s_left;
   }
   // keys of rank > prefix stay, and the first `left` of rank == prefix
-  const int run = (L + 31) / 32, i0 = min(L, warp * run), i1 = min(L, i0 + run);
+  const int run = ((L + 31) / 32 + 3) & ~3, i0 = min(L, warp * run), i1 = min(L, i0 + run);
   int gt = 0, eq = 0;
-#pragma unroll 8
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t r = get(i);
-    gt += r > prefix;
-    eq += r == prefix;
+#pragma unroll 4
+  for (int i = i0 + lane * 4; i < i1; i += 128) {
+    const uint4 r = get4(i);
+    const uint32_t re[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += i + e < i1 && re[e] > prefix;
+      eq += i + e < i1 && re[e] == prefix;
+    }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -176,20 +197,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
     ties += s_eq[w];
   }
   const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int b = i0; b < i1; b += 32) {
-    const int i = b + lane;
-    const uint32_t r = i < i1 ? get(i) : 0u;
-    uint32_t stay = __ballot_sync(0xffffffffu, i < i1 && r > prefix);
-    const uint32_t tie = __ballot_sync(0xffffffffu, i < i1 && r == prefix);
-    if (tie && ties < left) {  // the first left - ties of them
-      const int room_left = left - ties;
-      const bool in = ((tie >> lane) & 1u) && __popc(tie & below) < room_left;
-      stay |= __ballot_sync(0xffffffffu, in);
+#pragma unroll 2
+  for (int b = i0; b < i1; b += 128) {
+    const int i = b + lane * 4;
+    const uint4 r = i < i1 ? get4(i) : make_uint4(0, 0, 0, 0);
+    const uint32_t re[4] = {r.x, r.y, r.z, r.w};
+    uint32_t stay[4], tie[4];  // by key of a lane: a bit a lane
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      stay[e] = __ballot_sync(0xffffffffu, i + e < i1 && re[e] > prefix);
+      tie[e] = __ballot_sync(0xffffffffu, i + e < i1 && re[e] == prefix);
     }
-    if ((stay >> lane) & 1u) out[at + __popc(stay & below)] = i;
-    at += __popc(stay);
-    ties += __popc(tie);
+    const int n_ties = __popc(tie[0]) + __popc(tie[1]) + __popc(tie[2]) + __popc(tie[3]);
+    if (n_ties && ties < left) {  // the first left - ties of them
+      int before = ties + __popc(tie[0] & below) + __popc(tie[1] & below) + __popc(tie[2] & below) + __popc(tie[3] & below);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is = (tie[e] >> lane) & 1u;
+        stay[e] |= __ballot_sync(0xffffffffu, is && before < left);
+        before += is;
+      }
+    }
+    int to = at + __popc(stay[0] & below) + __popc(stay[1] & below) + __popc(stay[2] & below) + __popc(stay[3] & below);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((stay[e] >> lane) & 1u) out[to++] = i + e;
+    at += __popc(stay[0]) + __popc(stay[1]) + __popc(stay[2]) + __popc(stay[3]);
+    ties += n_ties;
   }
 }
 
@@ -249,11 +283,12 @@ cudaError_t launch_paged_evict(int n_seqs, const PagedView& cache, const PagedVi
   if (n_seqs == 0) return cudaSuccess;
   const span::Keys c = span::keys_of(&cache, k_pages, v_pages), t = span::keys_of(&to, k_pages, v_pages);
   const int room = (int)std::min<int64_t>(span::kSelCached, (int64_t)cache.max_pages << cache.page_log2);
+  const bool vec = (reinterpret_cast<uintptr_t>(weights) & 15u) == 0;
   cudaError_t e = cudaFuncSetAttribute(span::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        span::kSelCached * 4 + span::kHistBytes);
   if (e != cudaSuccess) return e;
-  span::evict_select_kernel<<<dim3(n_seqs, hkv), span::kSelThreads, span::kHistBytes + room * 4, st>>>(c, weights, hkv, budget, n_sink,
-                                                                                   n_recent, room, keep);
+  span::evict_select_kernel<<<dim3(n_seqs, hkv), span::kSelThreads, span::kHistBytes + room * 4, st>>>(
+      c, weights, hkv, budget, n_sink, n_recent, room, vec, keep);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int per = 256 / (d / 8);
   const dim3 grid((budget + per - 1) / per, hkv, n_seqs);

@@ -866,3 +866,20 @@ def test_training_past_32_bits():
     want, bounds = ref.gradients(*x, ro, whole[1][-n:, -r:].cpu().double(), see, 1 / math.sqrt(d), eo)
     for name, got, w, bd in zip(("dk", "dv"), whole[3:], want[1:], bounds[1:]):
         ref.within(got[-n:, -1:][2 * window:], w[2 * window:], bd[2 * window:], name)
+
+
+def test_evict_by_weights_of_any_alignment():
+    """Weights that start on a multiple of 4 bytes only give the choice that aligned ones give."""
+    c = Cache([1000, 130], 3, 64, 16, 131, spare=2 * 44)
+    new = torch.tensor(c.free, dtype=I32, device="cuda").view(2, 44)
+    n = c.k_pages.shape[0] * 3 * 16
+    w = torch.rand(n, generator=_gen(132)).mul(64).floor().cuda()
+    for budget, n_sink, n_recent in ((200, 3, 50), (701, 0, 1)):
+        want = None
+        for at in range(4):
+            x = torch.empty(n + 4, device="cuda")[at:at + n].copy_(w).view(-1, 3, 16)
+            assert x.data_ptr() % 16 == 4 * at
+            keep, lens = nsa.nsa_paged_evict(c.k_pages, c.v_pages, x, *c.args[2:], new, budget, n_sink, n_recent)
+            want = want or (keep, lens, x[new.long()[0, :12]].clone())
+            for a, b in zip((keep, lens, x[new.long()[0, :12]]), want):
+                assert torch.equal(a, b)
