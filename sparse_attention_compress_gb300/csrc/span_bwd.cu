@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         if (lane % CH == 0) s_dsum[(i * 8 + warp) * RPW + lane / CH] = sum[i];
     }
     named_barrier(1, 256);  // (after a timeout too: every softmax warp comes here)
-    if (tid == 0) tc::mbar_arrive(bar(VEMPTY));
+    // (a thread that gave up on o does not hand its slot on: the copy may still be in flight)
+    if (tid == 0 && ok) tc::mbar_arrive(bar(VEMPTY));
     float l2 = __builtin_inff(), dsum = 0.f;
     if (valid) {
       l2 = lse == kNegInf ? __builtin_inff() : lse * kLog2e;

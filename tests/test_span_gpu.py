@@ -883,3 +883,28 @@ def test_evict_by_weights_of_any_alignment():
             want = want or (keep, lens, x[new.long()[0, :12]].clone())
             for a, b in zip((keep, lens, x[new.long()[0, :12]]), want):
                 assert torch.equal(a, b)
+
+
+def test_waits_of_several_key_tiles_run_out_and_recover():
+    """Limits below, around and above a copy's time, with more key tiles than ring slots: whichever
+    warp gives up first, every copy in flight lands before its slot or its block is given away."""
+    assert nsa.nsa_device_status(reset=True) == 0
+    x = [_bf((1, 900, h, 128), _gen(141 + i)).cuda() for i, h in enumerate((16, 2, 2))]
+    lse = torch.empty(900, 16, device="cuda")
+    o = nsa.nsa_swa_sink_fwd(*x, 700, 4, lse=lse)
+    want = nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 700, 4)
+    try:
+        for limit in (1, 500, 1000, 1500, 2000, 2500, 3000, 4000, 6000):
+            torch.empty(96 << 20, dtype=torch.float32, device="cuda").fill_(1.0)
+            torch.cuda.synchronize()
+            nsa.nsa_set_wait_limit_ns(limit)
+            nsa.nsa_swa_sink_fwd(*x, 700, 4)
+            nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 700, 4)
+            torch.cuda.synchronize()
+            nsa.nsa_device_status(reset=True)  # (whether a wait ran out depends on the clock)
+    finally:
+        nsa.nsa_set_wait_limit_ns(0)
+        nsa.nsa_device_status(reset=True)
+    for a, b in zip((o, *nsa.nsa_swa_sink_bwd(*x, o, lse, x[0], 700, 4)), (nsa.nsa_swa_sink_fwd(*x, 700, 4), *want)):
+        assert torch.equal(a, b)
+    assert nsa.nsa_device_status() == 0
