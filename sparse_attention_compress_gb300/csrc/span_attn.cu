@@ -31,6 +31,7 @@
 // TMEM: S of half x at 128 x with P over its first columns, then O of the halves.
 // V is used as it lies (MN-major B operand), so nothing is transposed.
 #include <algorithm>
+#include <atomic>
 
 #include "launch.h"
 #include "span.cuh"
@@ -64,6 +65,10 @@ struct Cfg {
   static constexpr int OTHER_REGS = ONE ? 40 : 56;
   // what the launch must give a thread for the shares to add up
   static constexpr int MIN_REGS = (NH * 128 * kSoftRegs + 128 * OTHER_REGS + THREADS - 1) / THREADS;
+  // Shared memory of a launch whose Q has `rows` rows a half (few rows: as many as the call's,
+  // to 16), and of the largest.
+  static constexpr int smem(int rows) { return NH * (D / 64) * rows * 128 + (N0 + N1) * KV_BYTES + 1024; }
+  static constexpr int MAX_SMEM = smem(FORM == kFew ? (kFewRows + GRAN - 1) / GRAN * GRAN : ROWS);
 };
 
 struct AttnParams {
@@ -610,18 +615,19 @@ template <int D, bool PAGED, int FORM>
 cudaError_t run_attn(const CUtensorMap* m, const AttnParams& p, int64_t ctas, cudaStream_t st) {
   using C = Cfg<D, FORM>;
   auto kern = attn_kernel<D, PAGED, FORM>;
-  const int smem = C::NH * (D / 64) * p.q_group + (C::N0 + C::N1) * C::KV_BYTES + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit belongs to the kernel, and other threads launch it too: the same for every call)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::MAX_SMEM);
   if (e != cudaSuccess) return e;
   // the softmax warps' share must come out of what the block is launched with
-  static int regs = 0;
+  static std::atomic<int> kernel_regs{0};
+  int regs = kernel_regs.load(std::memory_order_relaxed);
   if (regs == 0) {
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
-    regs = at.numRegs;
+    kernel_regs.store(regs = at.numRegs, std::memory_order_relaxed);
   }
   if (regs < C::MIN_REGS) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)ctas, C::THREADS, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
+  kern<<<(unsigned)ctas, C::THREADS, C::smem(p.q_group / 128), st>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
   return cudaGetLastError();
 }
 

@@ -46,6 +46,20 @@ struct WCfg {
   static constexpr int NG = FEW ? 1 : 4;                  // groups of summing warps
   static constexpr int NB = FEW ? 2 : 4;                  // S buffers: item i in i % NB, summed by group i % NG
   static constexpr int THREADS = (4 * NG + 2) * 32;
+  // TMEM columns of an S buffer for query tiles of `cols` columns, of all of them (powers of two)
+  static constexpr int buf_cols(int cols) { return cols <= 32 ? 32 : cols <= 64 ? 64 : 128; }
+  // Shared memory of a launch, so much that no more CTAs come onto an SM than its 512 TMEM columns
+  // serve (228 KB, 1 KB of it per CTA reserved); and of the largest.
+  static constexpr int smem(int cols) {
+    const int q = (D / 64) * cols * 128, own = (FEW ? q + NS * K_BYTES : K_BYTES + NS * q) + 1024;
+    const int least = 228 * 1024 / (512 / (NB * buf_cols(cols)) + 1) - 1024 + 16;
+    return own > least ? own : least;
+  }
+  static constexpr int max_smem() {
+    int most = 0;
+    for (int c = GRAN; c <= ROWS; c += GRAN) most = smem(c) > most ? smem(c) : most;
+    return most;
+  }
 };
 
 template <int D, bool FEW>
@@ -318,8 +332,7 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   using C = WCfg<D, FEW>;
   p.cols = up16(p.tpc * p.R);
   p.q_group = p.cols * 128;
-  p.buf_cols = 32;
-  while ((int)p.buf_cols < p.cols) p.buf_cols *= 2;
+  p.buf_cols = C::buf_cols(p.cols);
   p.tmem_cols = C::NB * p.buf_cols;
   CUtensorMap mq, mk, mk16;
   // (a map needs rows; without queries none is ever loaded)
@@ -327,19 +340,16 @@ cudaError_t launch_weights_d(WeightParams& p, const void* q, cudaStream_t st) {
   if (!query_map(&mq, any ? q : p.keys.k, any ? p.seqs.tokens : 1, p.h, D, p.R, p.tpc) ||
       !key_maps(&mk, &mk16, p.keys.k, p.keys, p.hkv, D, 0))
     return cudaErrorInvalidValue;
-  const int q_bytes = (D / 64) * p.q_group;
-  int smem = (FEW ? q_bytes + C::NS * C::K_BYTES : C::K_BYTES + C::NS * q_bytes) + 1024;
-  // no more CTAs on an SM than its 512 TMEM columns serve (228 KB, 1 KB of it per CTA reserved)
-  smem = std::max(smem, 228 * 1024 / (512 / (int)p.tmem_cols + 1) - 1024 + 16);
   auto kern = weights_kernel<D, FEW>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit belongs to the kernel, and other threads launch it too: the same for every call)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::max_smem());
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)p.keys.max_pages << p.keys.page_log2) + KT - 1) / KT;
   const int64_t units = (int64_t)p.seqs.n_seqs * p.hkv;
   // FEW: at most three rounds of two CTAs an SM, so that ragged caches even out
   p.n_splits = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, 3 * 2 * 152 / units));
   const dim3 grid((unsigned)(FEW ? p.n_splits : tiles), p.seqs.n_seqs, p.hkv);
-  kern<<<grid, C::THREADS, smem, st>>>(mq, mk, mk16, p);
+  kern<<<grid, C::THREADS, C::smem(p.cols), st>>>(mq, mk, mk16, p);
   return cudaGetLastError();
 }
 
