@@ -96,3 +96,26 @@ def test_weights_of_a_call_without_queries_at_the_largest_group(d):
     out = nsa.nsa_paged_attn_weights(_bf((1, 0, 128, d), 331), k, lse, table, lens, weights=w, decay=0.5,
                                      out=torch.full_like(w, 7.0))
     assert torch.equal(out.view(-1)[:200], 0.5 * w.view(-1)[:200]) and (out.view(-1)[200:] == 7.0).all()
+
+
+@pytest.mark.parametrize("size", [(16, 2, 1), (16, 1, 20)])
+def test_a_thread_whose_first_cuda_call_it_is(size):
+    w = Work(*size, 128, 340)
+    torch.cuda.synchronize()
+    w.run()
+    want, errors = w.out(), []
+    w.o.zero_()
+    torch.cuda.synchronize()
+
+    def run():
+        try:
+            w.run()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert not errors, errors
+    for a, b in zip(w.out(), want):
+        assert torch.equal(a, b)
