@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
         if (const int i = last_in_stage(last_item, st, ns); i >= 0)
           tc::warp_drain(bar(B::FULL + first + st), (i / ns) & 1);
     } else if (warp == kIssue) {
-      if (lane == 0) tc::commit(bar(B::DRAIN));
+      commit(bar(B::DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
       __syncwarp();
       tc::warp_drain(bar(B::DRAIN), 0);
     }

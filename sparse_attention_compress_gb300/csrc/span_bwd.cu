@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       for (int st = 0; st < kNV; ++st)
         if (const int i = last_in(last_v, st, kNV); i >= 0) tc::warp_drain(bar(VFULL + st), (i / kNV) & 1);
     } else if (warp > 8) {
-      if (lane == 0) tc::commit(bar(DRAIN));
+      commit(bar(DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int st = 0; st < kND; ++st)
         if (const int i = last_in(last_d, st, kND); i >= 0) tc::warp_drain(bar(DFULL + st), (i / kND) & 1);
     } else if (warp > 8) {
-      if (lane == 0) tc::commit(bar(DRAIN));
+      commit(bar(DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(WCfg<D, FEW>::THREADS, FEW ? 2 : 1)
       for (int st = 0; st < NS; ++st)
         if (last_item >= st) tc::warp_drain(bar(FULL + st), ((last_item - st) / NS) & 1);
     } else if (warp == kIssue) {
-      if (lane == 0) tc::commit(bar(DRAIN));
+      commit(bar(DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
       __syncwarp();
       tc::warp_drain(bar(DRAIN), 0);
     }
