@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Keys c, const
 }
 
 // Row keep[i] of a (sequence, kv-head) to position i of the new table's pages: K, V and
-// weight.  A half-warp (d = 128) or quarter-warp (d = 64) moves a row of K and of V.
+// weight.  A half-warp (d = 128) or quarter-warp (d = 64) moves a row of K and of V.  (keep is
+// written while this kernel starts: no read-only loads of it.)
 template <int D>
 __global__ void __launch_bounds__(256) evict_copy_kernel(Keys c, Keys to, __nv_bfloat16* k_pages,
                                                          __nv_bfloat16* v_pages, float* weights, int hkv, int budget,
-                                                         const int32_t* __restrict__ keep, int32_t* new_lens) {
+                                                         const int32_t* keep, int32_t* new_lens) {
   constexpr int CH = D / 8, PER = 256 / CH;  // lanes a row, rows a block
   const int seq = blockIdx.z, g = blockIdx.y;
   const int32_t* list = keep + ((int64_t)seq * hkv + g) * budget;

@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 #pragma unroll
       for (int i = 0; i < ROWS / 32; ++i) {
         const bool in = tok[i] < L - t;
-        nl[i] = in ? __ldg(p.nlse2 + r0 + at[i]) : kNegInf;
-        nd[i] = in ? __ldg(p.ndsum + r0 + at[i]) : 0.f;
+        nl[i] = in ? __ldcg(p.nlse2 + r0 + at[i]) : kNegInf;  // (written while this kernel starts)
+        nd[i] = in ? __ldcg(p.ndsum + r0 + at[i]) : 0.f;
       }
     };
     wait_primary();  // (K and V are on their way)

@@ -28,3 +28,16 @@ def test_products_are_committed_by_the_lane_that_issued_them(path):
         assert lead in ("lead", "elect()", "uint32_t lead"), args
     if "lead = elect()" in code:
         assert re.search(r"commit\(bar\((?:B::)?DRAIN\), elect\(\)\)", code)
+
+
+def test_results_of_the_kernel_before_are_not_read_as_read_only():
+    """Kernels that start before the one ahead of them has ended (launch_second) read its results after
+    wait_primary().  The read-only path (__ldg, const __restrict__) is for data that no one writes
+    while the kernel lives, so it must not serve them."""
+    written = {"span_bwd.cu": ("nlse2", "ndsum", "near", "part"), "paged_cache.cu": ("keep", "list")}
+    for name, fields in written.items():
+        code = _code(os.path.join(CSRC, name))
+        assert "launch_second(" in code
+        for f in fields:
+            assert not re.search(rf"__ldg\([^;]*\b{f}\b", code), (name, f)
+            assert not re.search(rf"const (?:float|int32_t)\* __restrict__ {f}\b", code), (name, f)
