@@ -7,8 +7,9 @@
 // that the sums stay within the rounding of the bf16 gradients themselves.  D equals dO.o;
 // where a row's ds_j are formed before all its dp_j are known it is taken so, from the bf16
 // o, and the difference (the sum of the ds_j, which is 0 for the true D) is added for the
-// gradients of k.  Rows with few keys, in whose ds_j the rounding of o would show, have them
-// in one tile, and their D is the sum itself.
+// gradients of k.  Rows of at most kFewKeys keys, in whose ds_j the rounding of o would show (it
+// adds to dq's error the share 1 / sqrt(keys) of a bf16 rounding), have them in one tile, and
+// their D is the sum itself.
 //
 // Two kernels, each a chain of M = 128 products over 128-wide tiles with eight softmax
 // warps (two threads a TMEM lane, 64 columns each):
@@ -37,6 +38,9 @@ namespace nsa {
 namespace span {
 
 constexpr uint32_t kBwdTmem = 512;
+// A row at token t has min(t + 1, window + n_sink) keys.  Those of rows with at most this many lie
+// in one key tile: bwd_layout sees to it.
+constexpr int kFewKeys = 32;
 
 struct BwdParams {
   Seqs seqs;
@@ -877,6 +881,9 @@ BwdLayout bwd_layout(const Seqs& s, int h, int hkv, int D, int window, int n_sin
   BwdLayout l{};
   const int R = h / hkv;
   l.tpc = std::max(1, std::min(ROWS / R, s.max_len));
+  // The sinks and windows of a tile's rows in one key tile (its first token is a multiple of 16 where
+  // this bites: group 1 alone, 80 to 112 rows a tile instead of 128).
+  if ((int64_t)window + n_sink <= kFewKeys) l.tpc = std::min(l.tpc, KT - up16(window - 1) - up16(n_sink));
   const int sinks = std::min(n_sink, s.max_len);
   const int64_t far = sinks > 0 ? (int64_t)s.max_len - (KT - 1) - window : 0;  // queries past the first tile's window
   const int64_t own = (int64_t)window + KT - 1;                                // queries of a key tile
