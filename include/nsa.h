@@ -568,8 +568,8 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^28, 0 <= n_sink <= 2^28.
  * The backward returns the gradients for an upstream d_o (formulas of nsa_sparse_bwd over
  * the seen keys, with D = sum_e p_e dp_e for rows of at most 32 keys, and for every row in dk;
- * elsewhere D = d_o.o from the bf16 o; P and dS as bf16 in their products); o and lse are the
- * forward's.  dk and dv are written for every row of a sequence.  Outputs must not overlap inputs.
+ * elsewhere D = d_o.o from the bf16 o; P and dS as bf16 in their products, to about 16 bits in
+ * rows of at most 32 keys); o and lse are the forward's.  dk and dv are written for every row of a sequence.  Outputs must not overlap inputs.
  * Deterministic.  Requires n_sink <= 1024. */
 NSA_API size_t nsa_swa_sink_fwd_workspace_size(const nsa_shape* shape, int window, int n_sink);
 NSA_API nsa_status nsa_swa_sink_fwd(const nsa_shape* shape, const void* q, const void* k, const void* v, int window,

@@ -2,9 +2,11 @@
 // with seen keys j:  p_j = exp(scale q.k_j - lse),  dp_j = dO.v_j,  D = sum_j p_j dp_j,
 //   ds_j = p_j (dp_j - D),  dq = scale sum_j ds_j k_j,
 //   dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dO.
-// S, dP and all accumulators are fp32 (TMEM); P and dS enter the last products as bf16:
-// one rounding of at most 2^-8 relative per weight, of either sign over a sum's terms, so
-// that the sums stay within the rounding of the bf16 gradients themselves.  D equals dO.o;
+// S, dP and all accumulators are fp32 (TMEM); P and dS enter the last products as bf16: one
+// rounding of at most 2^-8 relative per weight, of either sign over a sum's terms, which adds to a
+// gradient's error about what its own rounding to bf16 does.  In tiles with a row of at most
+// kFewKeys keys, where one term is much of a sum, the remainders x - bf16(x) pass through a second
+// product, so that P and dS count to about 16 bits there.  D equals dO.o;
 // where a row's ds_j are formed before all its dp_j are known it is taken so, from the bf16
 // o, and the difference (the sum of the ds_j, which is 0 for the true D) is added for the
 // gradients of k.  Rows of at most kFewKeys keys, in whose ds_j the rounding of o would show (it
@@ -24,12 +26,13 @@
 // are divided too; the fp32 partials are summed in order by key_sum_kernel.
 // No atomics: results are the same on every run.
 //
-// 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.2 ms, dkv 1.95 ms, together
-// 660 TFLOP/s.  dkv keeps the tensor cores busy 72% of its time.  dq is bound by its CTAs' starts
+// 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.25 ms, dkv 2.0 ms, together
+// 650 TFLOP/s.  dkv keeps the tensor cores busy 72% of its time.  dq is bound by its CTAs' starts
 // and ends (five key tiles each, and 227 KB leave room for one on an SM) and by the chain S - P - dS
 // of a tile: tensor cores 31%.  Small calls are bound by the four kernels' own lengths: 3 sequences
 // of at most 1001 tokens x 16 heads, window 256, forward and backward 77 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "span.cuh"
@@ -39,8 +42,13 @@ namespace span {
 
 constexpr uint32_t kBwdTmem = 512;
 // A row at token t has min(t + 1, window + n_sink) keys.  Those of rows with at most this many lie
-// in one key tile: bwd_layout sees to it.
+// in one key tile: bwd_layout sees to it.  (A test of P's values instead, for any row with a p of
+// 1/4 or more, took 7% of the whole backward at window 512 and 11% at 1024: the softmax warps, which
+// everything else waits for, would do it in every tile.  The remainders' code, a copy of its own,
+// takes 2% of it at window 512.)
 constexpr int kFewKeys = 32;
+// Remainders of a half's 64 values lie this many TMEM columns behind the values.
+constexpr uint32_t kRest = 32;
 
 struct BwdParams {
   Seqs seqs;
@@ -79,13 +87,17 @@ __device__ __forceinline__ void mma_split_a(uint32_t d_tmem, uint32_t a_tmem, ui
   }
 }
 
-// Two products p (dp - D), as bf16 (nd is minus D, twice).
+// Two values as bf16.
 __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
   const float2 d = unpair(x);
   return pack_bf16(d.x, d.y);
 }
-__device__ __forceinline__ uint32_t ds_pair(uint64_t p, uint64_t dp, uint64_t nd) {
-  return pack_pair(mul2(p, add2(dp, nd)));
+// What that leaves of them, as bf16.
+__device__ __forceinline__ uint32_t rest_pair(uint64_t x) {
+  const float2 v = unpair(x);
+  const uint32_t hi = pack_bf16(v.x, v.y);
+  const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
+  return pack_bf16(v.x - h.x, v.y - h.y);
 }
 
 // ---------------------------------------------------------------------------- dQ
@@ -142,6 +154,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   if (t0 < 0) return;
   const Tiles tiles(t0, min(t0 + p.tpc, L) - 1, p.window, p.n_sink);
   const int n = tiles.n;
+  const bool few = min(t0 + 1, p.window + p.n_sink) <= kFewKeys;  // some row has few keys
 
   if (tid == 0) {
     tc::mbar_init(bar(Q), 1);
@@ -238,6 +251,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!(ok = wait(bar(DSFULL + b), (j >> 1) & 1))) break;
       tc::fence_after();
       mma_split_a<D>(tmem + 384, tmem + b * 128, desc_mn(k_s) + sk * (TB >> 4), tiles.width(j), j == 0, lead);
+      if (few)
+        mma_split_a<D>(tmem + 384, tmem + b * 128 + kRest, desc_mn(k_s) + sk * (TB >> 4), tiles.width(j), false, lead);
       commit(bar(DQDONE + b), lead);
       commit(bar(KEMPTY + sk), lead);
     }
@@ -296,80 +311,95 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     };
     // (with one tile a warp that gave up, here or before, still comes to the barrier of row_sum:
     // the others may not have)
-    for (int j = 0; (ok || n == 1) && j < n; ++j) {
-      const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
-      ok = wait(bar(SFULL + b), (j >> 1) & 1) && ok;
-      if (!ok && n > 1) break;
-      tc::fence_after();
-      const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
-      const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)
-      float sv[64];
+    // (remainders or none in code of their own: what the one keeps alive would cost the other)
+    auto walk = [&](auto with_rest) {
+      for (int j = 0; (ok || n == 1) && j < n; ++j) {
+        const int b = j & 1, key0 = tiles.key0(j), w = tiles.width(j);
+        ok = wait(bar(SFULL + b), (j >> 1) & 1) && ok;
+        if (!ok && n > 1) break;
+        tc::fence_after();
+        const uint32_t s_t = tmem + b * 128 + x * 64 + lane_base, p_t = tmem + 256 + x * 64 + lane_base;
+        const int c0 = x * 64, nc = min(64, w - c0);  // columns of this half (nc <= 0: none)
+        float sv[64];
 #pragma unroll
-      for (int c = 0; c < 64; c += 32)
-        tc::tmem_ld32_nowait(s_t + c, sv + c);
-      const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
-      const bool all = __all_sync(0xffffffffu, j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64));
-      tmem_wait_ld(sv);
-      tmem_wait_ld(sv + 32);
-      if (!all) {
+        for (int c = 0; c < 64; c += 32)
+          tc::tmem_ld32_nowait(s_t + c, sv + c);
+        const int j_hi = min(pos + 1 - key0, w), j_lo = pos - p.window + 1 - key0, j_sink = tiles.sinks(j, p.n_sink);
+        const bool all = __all_sync(0xffffffffu, j_hi >= c0 + 64 && (j_lo <= c0 || j_sink >= c0 + 64));
+        tmem_wait_ld(sv);
+        tmem_wait_ld(sv + 32);
+        if (!all) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            const uint32_t see = bits(j_lo - c0 - c, j_hi - c0 - c) | bits(0, min(j_sink, j_hi) - c0 - c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 y = unpair(fma2(pair(sv[c], sv[c + 1]), scale2, nl2));
+          sv[c] = ex2(y.x);
+          sv[c + 1] = ex2(y.y);
+        }
+        ok = wait(bar(PFULL), j & 1) && ok;
+        if (!ok && n > 1) break;
+        tc::fence_after();
+        float dp[64];
+#pragma unroll
+        for (int c = 0; c < 64; c += 32)
+          tc::tmem_ld32_nowait(p_t + c, dp + c);
+        tmem_wait_ld(dp);
+        tmem_wait_ld(dp + 32);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(PFREE));
+        // (an unseen key's p is 0 and its dp finite; columns past the tile's hold anything)
+#pragma unroll
+        for (int c = 0; c < 64; c += GRAN)
+          if (c >= nc) {
+#pragma unroll
+            for (int e = 0; e < GRAN; ++e) dp[c + e] = 0.f;
+          }
+        if (n == 1) {
+          uint64_t d2 = 0;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) d2 = fma2(pair(sv[c], sv[c + 1]), pair(dp[c], dp[c + 1]), d2);
+          const float2 d = unpair(d2);
+          dsum = row_sum(d.x + d.y);
+          nd2 = pair(-dsum, -dsum);
+          if (!ok) break;
+        }
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
-          const uint32_t see = bits(j_lo - c0 - c, j_hi - c0 - c) | bits(0, min(j_sink, j_hi) - c0 - c);
+          if (c >= nc) break;
+          uint32_t pk[16];
+          auto ds = [&](int e) {  // (an unseen key has p = 0)
+            return mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), nd2));
+          };
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t d = ds(e);
+            e2 = add2(e2, d);
+            pk[e / 2] = pack_pair(d);
+          }
+          tmem_st16_nowait(s_t + c / 2, pk);
+          if constexpr (decltype(with_rest)::value) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) pk[e / 2] = rest_pair(ds(e));
+            tmem_st16_nowait(s_t + kRest + c / 2, pk);
+          }
         }
+        tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(DSFULL + b));
       }
-#pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float2 y = unpair(fma2(pair(sv[c], sv[c + 1]), scale2, nl2));
-        sv[c] = ex2(y.x);
-        sv[c + 1] = ex2(y.y);
-      }
-      ok = wait(bar(PFULL), j & 1) && ok;
-      if (!ok && n > 1) break;
-      tc::fence_after();
-      float dp[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 32)
-        tc::tmem_ld32_nowait(p_t + c, dp + c);
-      tmem_wait_ld(dp);
-      tmem_wait_ld(dp + 32);
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(PFREE));
-      // (an unseen key's p is 0 and its dp finite; columns past the tile's hold anything)
-#pragma unroll
-      for (int c = 0; c < 64; c += GRAN)
-        if (c >= nc) {
-#pragma unroll
-          for (int e = 0; e < GRAN; ++e) dp[c + e] = 0.f;
-        }
-      if (n == 1) {
-        uint64_t d2 = 0;
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) d2 = fma2(pair(sv[c], sv[c + 1]), pair(dp[c], dp[c + 1]), d2);
-        const float2 d = unpair(d2);
-        dsum = row_sum(d.x + d.y);
-        nd2 = pair(-dsum, -dsum);
-        if (!ok) break;
-      }
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        if (c >= nc) break;
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {  // (an unseen key has p = 0)
-          const uint64_t d = mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), nd2));
-          e2 = add2(e2, d);
-          pk[e / 2] = pack_pair(d);
-        }
-        tmem_st16_nowait(s_t + c / 2, pk);
-      }
-      tmem_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(DSFULL + b));
-    }
+    };
+    if (few)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
     if (ok) {
       ok = wait(bar(DQDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
       tc::fence_after();
@@ -509,6 +539,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (t_lo >= t_hi) return;  // (an empty chunk or share: key_sum_kernel does not read it)
   const int n = (t_hi - t_lo + p.tpc - 1) / p.tpc;
   const int used = p.tpc * p.R;  // rows of a tile
+  // some tile of the CTA has a row with few keys; the tile at token t has
+  const bool few = min(t_lo + 1, p.window + p.n_sink) <= kFewKeys;
+  auto few_at = [&](int t) { return min(t + 1, p.window + p.n_sink) <= kFewKeys; };
   // A query tile is seen by the key tiles of its whole window, CTAs that run side by side.
   // Each begins its round of query tiles where the others do (at the tile whose index is a
   // multiple of a full round's length), so that they ask for the same tile at about the same
@@ -645,19 +678,27 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc::fence_after();
       issue_s();
     }
-    for (int j = 0; ok && j < n; ++j) {
-      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
-      if (j + 1 < n && !(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
-      if (!(ok = wait(bar(PFULL), j & 1))) break;
-      tc::fence_after();
-      mma_split_a<D>(tmem + 256, tmem, dd + rd.slot * (TB >> 4), p.cols, j == 0, lead);
-      commit(bar(DEMPTY + rd.slot), lead);
-      if (j + 1 < n)
-        issue_s();
-      else
-        commit(bar(DVDONE), lead);
-      rd.next();
-    }
+    auto walk = [&](auto with_rest) {
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
+        if (j + 1 < n && !(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
+        if (!(ok = wait(bar(PFULL), j & 1))) break;
+        tc::fence_after();
+        mma_split_a<D>(tmem + 256, tmem, dd + rd.slot * (TB >> 4), p.cols, j == 0, lead);
+        if (decltype(with_rest)::value && few_at(token_of(j)))
+          mma_split_a<D>(tmem + 256, tmem + kRest, dd + rd.slot * (TB >> 4), p.cols, false, lead);
+        commit(bar(DEMPTY + rd.slot), lead);
+        if (j + 1 < n)
+          issue_s();
+        else
+          commit(bar(DVDONE), lead);
+        rd.next();
+      }
+    };
+    if (few)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
   } else if (warp == 10) {
     // ------------------------------------------------------------------ dP^T, dK += dS^T Q
     const uint32_t lead = elect(), vd = desc_k(v_s), dd = desc_k(do_s), qd = desc_mn(q_s);
@@ -674,18 +715,26 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc::fence_after();
       issue_dp();
     }
-    for (int j = 0; ok && j < n; ++j) {
-      if (j + 1 < n && !(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
-      if (!(ok = wait(bar(DSFULL), j & 1))) break;
-      tc::fence_after();
-      mma_split_a<D>(tmem + 384, tmem + 128, qd + rq.slot * (TB >> 4), p.cols, j == 0, lead);
-      commit(bar(QEMPTY + rq.slot), lead);  // (S^T of the tile was done before its dS^T)
-      if (j + 1 < n)
-        issue_dp();
-      else
-        commit(bar(DKDONE), lead);
-      rq.next();
-    }
+    auto walk = [&](auto with_rest) {
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n && !(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
+        if (!(ok = wait(bar(DSFULL), j & 1))) break;
+        tc::fence_after();
+        mma_split_a<D>(tmem + 384, tmem + 128, qd + rq.slot * (TB >> 4), p.cols, j == 0, lead);
+        if (decltype(with_rest)::value && few_at(token_of(j)))
+          mma_split_a<D>(tmem + 384, tmem + 128 + kRest, qd + rq.slot * (TB >> 4), p.cols, false, lead);
+        commit(bar(QEMPTY + rq.slot), lead);  // (S^T of the tile was done before its dS^T)
+        if (j + 1 < n)
+          issue_dp();
+        else
+          commit(bar(DKDONE), lead);
+        rq.next();
+      }
+    };
+    if (few)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
   } else {
     // ------------------------------------------------------------------ softmax
     const int x = warp >> 2, row = (warp & 3) * 32 + lane, key = key0 + row, c0 = x * 64;
@@ -697,84 +746,108 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     Ring<kNQ> rq;  // (D's buffers go with Q's slots: three of each)
     Ring<kND> rd;
     bool ok = true;
-    for (int j = 0; j < n; ++j, rq.next(), rd.next()) {
-      const int t = token_of(j);
-      // columns [c_lo, c_hi) of this half are rows whose query sees this key
-      int c_lo = 0, c_hi = 0;
-      if (have) {
-        int64_t end = (int64_t)min(p.tpc, t_hi - t) * p.R;
-        if (key >= p.n_sink) end = min(end, ((int64_t)key + p.window - t) * p.R);
-        c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
-        c_hi = (int)max((int64_t)0, end) - c0;
-      }
-      if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;  // lse and D
-      if (!(ok = wait(bar(SFULL), j & 1))) break;
-      tc::fence_after();
-      float sv[64];
+    // (remainders or none in code of their own, as above)
+    auto walk = [&](auto with_rest) {
+      for (int j = 0; j < n; ++j, rq.next(), rd.next()) {
+        const int t = token_of(j);
+        const bool rest = decltype(with_rest)::value && few_at(t);
+        // columns [c_lo, c_hi) of this half are rows whose query sees this key
+        int c_lo = 0, c_hi = 0;
+        if (have) {
+          int64_t end = (int64_t)min(p.tpc, t_hi - t) * p.R;
+          if (key >= p.n_sink) end = min(end, ((int64_t)key + p.window - t) * p.R);
+          c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
+          c_hi = (int)max((int64_t)0, end) - c0;
+        }
+        if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;  // lse and D
+        if (!(ok = wait(bar(SFULL), j & 1))) break;
+        tc::fence_after();
+        float sv[64];
 #pragma unroll
-      for (int c = 0; c < 64; c += 32)
-        tc::tmem_ld32_nowait(s_t + c, sv + c);
-      const bool all = c_lo <= 0 && c_hi >= 64;
-      const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
-      tmem_wait_ld(sv);
-      tmem_wait_ld(sv + 32);
-      if (!__all_sync(0xffffffffu, all)) {
+        for (int c = 0; c < 64; c += 32)
+          tc::tmem_ld32_nowait(s_t + c, sv + c);
+        const bool all = c_lo <= 0 && c_hi >= 64;
+        const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
+        tmem_wait_ld(sv);
+        tmem_wait_ld(sv + 32);
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            const uint32_t see = bits(c_lo - c, c_hi - c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
-          const uint32_t see = bits(c_lo - c, c_hi - c);
+          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l = l4[(c + e) / 4];
+            const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, pair(l.x, l.y)));
+            const float2 z = unpair(fma2(pair(sv[c + e + 2], sv[c + e + 3]), scale2, pair(l.z, l.w)));
+            sv[c + e] = ex2(y.x);
+            sv[c + e + 1] = ex2(y.y);
+            sv[c + e + 2] = ex2(z.x);
+            sv[c + e + 3] = ex2(z.y);
+            pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
+            pk[e / 2 + 1] = pack_bf16(sv[c + e + 2], sv[c + e + 3]);
+          }
+          if (c < nc) tmem_st16_nowait(s_t + c / 2, pk);
+          if (rest) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) pk[e / 2] = rest_pair(pair(sv[c + e], sv[c + e + 1]));
+            if (c < nc) tmem_st16_nowait(s_t + kRest + c / 2, pk);
+          }
         }
-      }
+        tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(PFULL));
+        if (!(ok = wait(bar(DPFULL), j & 1))) break;
+        tc::fence_after();
+        const float4* d4 = reinterpret_cast<const float4*>(&s_d[rq.slot][c0]);
+        float dp[64];
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t pk[16];
+        for (int c = 0; c < 64; c += 32)
+          tc::tmem_ld32_nowait(p_t + c, dp + c);
+        tmem_wait_ld(dp);
+        tmem_wait_ld(dp + 32);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l = l4[(c + e) / 4];
-          const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, pair(l.x, l.y)));
-          const float2 z = unpair(fma2(pair(sv[c + e + 2], sv[c + e + 3]), scale2, pair(l.z, l.w)));
-          sv[c + e] = ex2(y.x);
-          sv[c + e + 1] = ex2(y.y);
-          sv[c + e + 2] = ex2(z.x);
-          sv[c + e + 3] = ex2(z.y);
-          pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
-          pk[e / 2 + 1] = pack_bf16(sv[c + e + 2], sv[c + e + 3]);
-        }
-        if (c < nc) tmem_st16_nowait(s_t + c / 2, pk);
-      }
-      tmem_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(PFULL));
-      if (!(ok = wait(bar(DPFULL), j & 1))) break;
-      tc::fence_after();
-      const float4* d4 = reinterpret_cast<const float4*>(&s_d[rq.slot][c0]);
-      float dp[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 32)
-        tc::tmem_ld32_nowait(p_t + c, dp + c);
-      tmem_wait_ld(dp);
-      tmem_wait_ld(dp + 32);
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        if (c >= nc) break;
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d = d4[(c + e) / 4];
+        for (int c = 0; c < 64; c += 32) {
+          if (c >= nc) break;
+          uint32_t pk[16];
           // (zero rows past the sequence have dp = 0, so p = 0 gives ds = 0)
-          pk[e / 2] = ds_pair(pair(sv[c + e], sv[c + e + 1]), pair(dp[c + e], dp[c + e + 1]), pair(d.x, d.y));
-          pk[e / 2 + 1] =
-              ds_pair(pair(sv[c + e + 2], sv[c + e + 3]), pair(dp[c + e + 2], dp[c + e + 3]), pair(d.z, d.w));
+          auto ds = [&](int e, float x, float y) {
+            return mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), pair(x, y)));
+          };
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d = d4[(c + e) / 4];
+            pk[e / 2] = pack_pair(ds(e, d.x, d.y));
+            pk[e / 2 + 1] = pack_pair(ds(e + 2, d.z, d.w));
+          }
+          tmem_st16_nowait(p_t + c / 2, pk);
+          if (rest) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 d = d4[(c + e) / 4];
+              pk[e / 2] = rest_pair(ds(e, d.x, d.y));
+              pk[e / 2 + 1] = rest_pair(ds(e + 2, d.z, d.w));
+            }
+            tmem_st16_nowait(p_t + kRest + c / 2, pk);
+          }
         }
-        tmem_st16_nowait(p_t + c / 2, pk);
+        tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(DSFULL));
       }
-      tmem_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(DSFULL));
-    }
+    };
+    if (few)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
     if (ok) {
       ok = wait(bar(DVDONE), 0) && wait(bar(DKDONE), 0);
       tc::fence_after();

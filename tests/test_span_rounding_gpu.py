@@ -1,6 +1,6 @@
 """Rows with few keys in the sink-window training pair: there no single rounding averages out, so these
 are held to tighter bounds than tests/test_span_gpu.py's (which grant the gradient of q the
-rounding of the stored o everywhere)."""
+rounding of the stored o everywhere, and P and dS a rounding to bf16)."""
 import math
 
 import pytest
@@ -12,15 +12,17 @@ from tests import span_reference as ref
 pytestmark = pytest.mark.gpu
 
 BF, I32 = torch.bfloat16, torch.int32
-def _bf(shape, seed, scale=1.0):
-    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale).to(BF)
 
 
-def _train(lens, H, hk, d, window, n_sink, q_scale=1.0):
-    """(kernel's o, lse and gradients, and per sequence the exact inputs, masks and slices)."""
+def _bf(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(BF)
+
+
+def _train(lens, H, hk, d, window, n_sink):
+    """(the kernel's gradients; per sequence its rows, lse, mask, exact inputs, exact gradients and bounds)."""
     cu = torch.tensor([0] + lens).cumsum(0).to(I32)
     n = int(cu[-1])
-    x = [_bf((n, h, d), 200 + i, s) for i, (h, s) in enumerate(((H, q_scale), (hk, 1.0), (hk, 1.0), (H, 1.0)))]
+    x = [_bf((n, h, d), 200 + i) for i, h in enumerate((H, hk, hk, H))]
     q, k, v, do = (t.cuda() for t in x)
     lse = torch.empty(n, H, device="cuda")
     kw = dict(cu_seqlens=cu.cuda(), max_seqlen=max(lens))
@@ -33,8 +35,9 @@ def _train(lens, H, hk, d, window, n_sink, q_scale=1.0):
         see = ref.visible(range(L), L, window, n_sink)
         y = [t[a:e].double() for t in x]
         ro = ref.attend(*y[:3], see, 1 / math.sqrt(d))[0]
-        seqs.append((a, e, see, y, ro, ref.gradients(*y, ro, lse[a:e].cpu().double(), see, 1 / math.sqrt(d))))
-    return o, lse, grads, seqs
+        kept = lse[a:e].cpu().double()
+        seqs.append((a, e, kept, see, y, ref.gradients(*y, ro, kept, see, 1 / math.sqrt(d))))
+    return grads, seqs
 
 
 # Sequences of a few tokens, and long ones whose window and sinks hold at most 32 keys.
@@ -50,7 +53,58 @@ FEW = [
 def test_gradients_of_few_keys_carry_no_rounding_of_o(lens, H, hk, d, window, n_sink):
     """The bounds without the term of o's distance from the exact one: D is the sum of p dp."""
     assert max(min(L, window + n_sink) for L in lens) <= 32
-    _, _, grads, seqs = _train(lens, H, hk, d, window, n_sink)
+    grads, seqs = _train(lens, H, hk, d, window, n_sink)
     for b, (a, e, _, _, _, (want, bounds)) in enumerate(seqs):
         for name, got, w, bd in zip(("dq", "dk", "dv"), grads, want, bounds):
             ref.within(got[a:e], w, bd, f"{name} of sequence {b}")
+
+
+# A value and its remainder, both bf16: the remainder is at most 2^-8 of the value and is itself
+# rounded by at most 2^-8 of that.
+BB = ref.B * ref.B
+
+
+def _bounds(q, k, v, do, o, lse, see, scale):
+    """ref.gradients' bounds with P and dS carried as value and remainder and D summed as p dp."""
+    Q, H, d = q.shape
+    n, hk = k.shape[:2]
+    r, U, B = H // hk, ref.U, ref.B
+    grads, _ = ref.gradients(q, k, v, do, o, lse, see, scale)
+    eq, ek, ev = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    for h in range(H):
+        g = h // r
+        kk, vv, qq, dd = k[:, g], v[:, g], q[:, h], do[:, h]
+        p = torch.where(see, torch.exp(qq @ kk.T * scale - lse[:, h][:, None]), 0.0)
+        dp = dd @ vv.T
+        ds = p * (dp - (p * dp).sum(1, keepdim=True))
+        arg = (d + 8) * U * (qq.abs() @ kk.abs().T) * scale + 4 * U * lse[:, h].abs()[:, None] + 2.0 ** -20
+        mag = dd.abs() @ vv.abs().T
+        ed = ((arg + n * U) * p * mag).sum(1, keepdim=True) + (dd * o[:, h]).abs().sum(1, keepdim=True) * (d + n) * U
+        eds = ds.abs() * (BB + arg) + p * ((d + 4) * U * mag + ed)
+        eq[:, h] = scale * (eds + 2 * n * U * ds.abs()) @ kk.abs()
+        ek[:, g] += scale * (eds + 2 * Q * r * U * ds.abs()).T @ qq.abs()
+        ev[:, g] += (p * (BB + arg + 2 * Q * r * U)).T @ dd.abs()
+    return tuple(e + B * x.abs() * (1 + 2 * B) for e, x in zip((eq, ek, ev), grads))
+
+
+def _hold(grads, seqs, names=("dq", "dk", "dv"), rows=None):
+    """Within _bounds (rows: the first ones alone)."""
+    for b, (a, e, lse, see, x, (want, _)) in enumerate(seqs):
+        ro = ref.attend(*x[:3], see, 1 / math.sqrt(x[0].shape[2]))[0]
+        bounds = _bounds(*x, ro, lse, see, 1 / math.sqrt(x[0].shape[2]))
+        for name, got, w, bd in zip(("dq", "dk", "dv"), grads, want, bounds):
+            if name in names:
+                ref.within(got[a:e][:rows], w[:rows], bd[:rows], f"{name} of sequence {b}")
+
+
+@pytest.mark.parametrize("lens,H,hk,d,window,n_sink", FEW)
+def test_gradients_of_rows_with_few_keys(lens, H, hk, d, window, n_sink):
+    assert max(min(L, window + n_sink) for L in lens) <= 32
+    grads, seqs = _train(lens, H, hk, d, window, n_sink)
+    _hold(grads, seqs)
+
+
+@pytest.mark.parametrize("T,H,hk,d,window,n_sink", [(500, 2, 2, 64, 300, 0), (260, 16, 2, 128, 100, 4)])
+def test_gradients_of_a_sequence_s_first_rows(T, H, hk, d, window, n_sink):
+    grads, seqs = _train([T], H, hk, d, window, n_sink)
+    _hold(grads, seqs, names=("dq",), rows=32)
