@@ -44,6 +44,10 @@ constexpr int kSoftRegs = 208;
 // P may exceed 1 by 2^kLazy before the running maximum moves: the floating-point formats of
 // P, of the sums and of O hold it with the same relative precision.
 constexpr float kLazy = 16.f;
+// But a key that outweighs half of all before it moves the maximum at once: its P is then 1, which bf16
+// holds, where otherwise the rounding of the one P that makes up the row would show.  (Window 512
+// 1.520 -> 1.535 ms at 65536 tokens x 64 heads, window 64 19.7 -> 20.5 us at 8192 x 8, longer ones unchanged.)
+constexpr float kOutweighs = -1.f;  // log2
 constexpr int kFewRows = 48;  // what leaves room for two such CTAs on an SM beside three tiles each
 constexpr int kSms = 152;
 // Key tiles of a row tile up to which its CTA shares an SM.  32768 tokens x 64 heads (4 kv-heads,
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
     const bool work = __any_sync(0xffffffffu, pos >= 0);  // warps without rows only keep the barriers moving
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + x * 128 + lane_base, o_t = tmem + kO + x * 128 + lane_base;
-    float m = kNegInf, l = 0.f;
+    float m = kNegInf, l = 0.f, lim = kNegInf;  // lim: what a score must exceed for the maximum to move
     bool ok = true;
     for (int it = 0; it < cnt; ++it) {
       const int key0 = tiles.key0(a + it), w = tiles.width(a + it);
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
         }
         // the first 64 exponentials are taken with the maximum so far, while the other scores
         // arrive and the tile's own maximum is found; the running maximum moves (and they are
-        // taken again) only when a score exceeds it by 2^kLazy
+        // taken again) only when a score exceeds it by 2^kLazy or outweighs the row so far
         if (it > 0) first_half();
         max_of(0);
         max_of(32);
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
         max_of(64);
         max_of(96);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-        const bool need = mx > m + kLazy;
+        const bool need = mx > lim;
         if (__any_sync(0xffffffffu, need) || it == 0) {
           const float alpha = need ? ex2(m - mx) : 1.f;
           if (it > 0) {
@@ -401,6 +405,7 @@ __global__ void __launch_bounds__(Cfg<D, FORM>::THREADS, FORM == kLong ? 1 : 2)
         }
         const float2 la = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
         l += la.x + la.y;
+        lim = m + fminf(kLazy, __log2f(l) + kOutweighs);
       } else if (lane == 0) {
         tc::mbar_arrive(bar(B::PFULL + 2 * x));
       }

@@ -1,6 +1,7 @@
-"""Rows with few keys in the sink-window training pair: there no single rounding averages out, so these
-are held to tighter bounds than tests/test_span_gpu.py's (which grant the gradient of q the
-rounding of the stored o everywhere, and P and dS a rounding to bf16)."""
+"""Rows with few keys in the sink-window training pair, and rows of the attention that one key makes
+up: there no single rounding averages out, so these are held to tighter bounds than
+tests/test_span_gpu.py's (which grant the gradient of q the rounding of the stored o everywhere, and
+P and dS a rounding to bf16)."""
 import math
 
 import pytest
@@ -108,3 +109,37 @@ def test_gradients_of_rows_with_few_keys(lens, H, hk, d, window, n_sink):
 def test_gradients_of_a_sequence_s_first_rows(T, H, hk, d, window, n_sink):
     grads, seqs = _train([T], H, hk, d, window, n_sink)
     _hold(grads, seqs, names=("dq",), rows=32)
+
+
+@pytest.mark.parametrize("q_len,bound", [(64, None), (64, 1 << 20), (1, None)])  # short, long and few-row forms
+def test_a_late_key_that_outweighs_the_others(q_len, bound):
+    """The weight of a key that holds two thirds of a row, or nearly all, is not rounded more than
+    the row's o: with the row's own maximum it is 1, which bf16 holds.  Others' weights may be."""
+    n, H, d, page = 640, 64, 128, 64
+    k, v, q = _bf((n, 1, d), 210), _bf((n, 1, d), 211), _bf((q_len, H, d), 212)
+    u = torch.zeros(d)
+    u[0] = 1.0  # the late key's direction: scores of the other keys keep their size
+    k[:, 0, 0], q[..., 0] = 0.0, 16.0
+    k[550, 0] = (u * 1.0).to(BF)
+    rise = torch.linspace(4.0, 13.0, q_len * H)  # how far its score lies above the others' mean
+    q[..., 0] = (rise.view(q_len, H) * math.sqrt(d)).to(BF)
+    pages = torch.zeros(n // page, page, 1, d, dtype=BF)
+    k_pages, v_pages = pages.clone().cuda(), pages.clone().cuda()
+    k_pages.view(n, 1, d).copy_(k)
+    v_pages.view(n, 1, d).copy_(v)
+    table = torch.arange(n // page, dtype=I32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=I32, device="cuda")
+    o = nsa.nsa_paged_attn_fwd(q[None].cuda(), k_pages, v_pages, table, lens, max_cache_len=bound)[0]
+    see = ref.visible(range(n - q_len, n), n, 0, 0)
+    ro, lse, _, _ = ref.attend(q.double(), k.double(), v.double(), see, 1 / math.sqrt(d))
+    s = torch.einsum("qhd,kd->qhk", q.double(), k[:, 0].double()) / math.sqrt(d)
+    p = torch.where(see[:, None], torch.exp(s - lse[..., None]), 0.0)
+    heavy = p[..., 550] > 0.6
+    assert int(heavy.sum()) >= 0.4 * heavy.numel()
+    mag = torch.einsum("qhd,kd->qhk", q.double().abs(), k[:, 0].double().abs()).amax(-1) / math.sqrt(d)
+    rel = 2 * (d + 8) * ref.U * mag + 2.0 ** -20 + n * ref.U
+    p[..., 550] = 0.0
+    # (its weight next to the maximum in fp32: the exponent's error is in rel)
+    bound = torch.einsum("qhk,kd->qhd", p, v[:, 0].double().abs()) * ref.B \
+        + rel[..., None] * v.double().abs().max() + ref.B * ro.abs() * (1 + ref.B)
+    ref.within(o[heavy], ro[heavy], bound[heavy], "o of rows with a heavy key")
