@@ -646,6 +646,13 @@ def _expect(fn, device, **tensors):
             raise ValueError(f"{fn}: {name} must be dense (contiguous)")
 
 
+def _int32(fn, **values):
+    """ctypes would pass the low 32 bits of a larger number without a word."""
+    for name, x in values.items():
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{fn}: {name} = {x} does not fit 32 bits")
+
+
 def _on(device, stream):
     """(context that makes the call's device and stream current, raw stream, the caller's stream
     where it is another one)."""
@@ -728,6 +735,7 @@ def _span_shape(fn, q, h_kv, d, device, cu_seqlens, max_seqlen):
         raise ValueError(f"{fn}: cu_seqlens needs at least two entries")
     if max_seqlen is None:
         raise ValueError(f"{fn}: cu_seqlens needs max_seqlen")
+    _int32(fn, max_seqlen=max_seqlen)
     return dims[0], NsaShape(0, int(max_seqlen), cu_seqlens.data_ptr(), n, dims[0], dims[1], h_kv, d, NSA_BF16), n
 
 
@@ -751,6 +759,7 @@ def nsa_paged_append(k_new, v_new, k_pages, v_pages, block_table, cache_lens, *,
 
 
 def nsa_paged_attn_fwd_workspace_size(shape: NsaShape, max_cache_len: int = 0, window: int = 0, n_sink: int = 0) -> int:
+    _int32("nsa_paged_attn_fwd_workspace_size", window=window, n_sink=n_sink)
     return int(load().nsa_paged_attn_fwd_workspace_size(ctypes.byref(shape), max_cache_len, window, n_sink))
 
 
@@ -769,6 +778,7 @@ def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n
     already holds their keys), causal, with an optional window and n_sink tokens that stay
     visible beside it.  Returns out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_paged_attn_fwd"
+    _int32(fn, window=window, n_sink=n_sink)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
@@ -797,6 +807,7 @@ def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n
     nsa_paged_attn_fwd call (same masks, its lse) gave to the key, over the heads of its group.
     Without weights the sum alone; out may be weights (the default when weights are given)."""
     fn = "nsa_paged_attn_weights"
+    _int32(fn, window=window, n_sink=n_sink)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
@@ -822,6 +833,7 @@ def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_tabl
     listed twice).  Returns (keep [n_seqs, Hkv,
     budget] int32, -1 padded, and new_lens [n_seqs] int32)."""
     fn = "nsa_paged_evict"
+    _int32(fn, budget=budget, n_sink=n_sink, n_recent=n_recent)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     if weights is None:
@@ -850,6 +862,7 @@ def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_tabl
 
 # ----------------------------------------------------------------------------- window with sinks
 def nsa_swa_sink_fwd_workspace_size(shape: NsaShape, window: int = 512, n_sink: int = 4) -> int:
+    _int32("nsa_swa_sink_fwd_workspace_size", window=window, n_sink=n_sink)
     return int(load().nsa_swa_sink_fwd_workspace_size(ctypes.byref(shape), window, n_sink))
 
 
@@ -871,6 +884,7 @@ def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=Non
     """Sliding window beside which the first n_sink tokens of each sequence stay visible.  Returns
     out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_swa_sink_fwd"
+    _int32(fn, window=window, n_sink=n_sink)
     dev = q.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
@@ -891,6 +905,7 @@ def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=Non
 
 
 def nsa_swa_sink_bwd_workspace_size(shape: NsaShape, window: int = 512, n_sink: int = 4) -> int:
+    _int32("nsa_swa_sink_bwd_workspace_size", window=window, n_sink=n_sink)
     return int(load().nsa_swa_sink_bwd_workspace_size(ctypes.byref(shape), window, n_sink))
 
 
@@ -898,6 +913,7 @@ def nsa_swa_sink_bwd(q, k, v, o, lse, d_o, window=512, n_sink=4, scale=0.0, *, c
                      workspace=None, dq=None, dk=None, dv=None, stream=None):
     """Backward of nsa_swa_sink_fwd: (dq, dk, dv) shaped like q, k, v from its o and lse."""
     fn = "nsa_swa_sink_bwd"
+    _int32(fn, window=window, n_sink=n_sink)
     dev = q.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
