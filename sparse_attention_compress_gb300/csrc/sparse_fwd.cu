@@ -462,8 +462,9 @@ cudaError_t launch_sparse_fwd(const Seqs& s, const void* q, const void* k, const
   if (dtype == kF32) {
     const int max_keys = S * block_size;
     const size_t bytes = (size_t)max_keys * 4 * 5;
-    cudaError_t e = cudaFuncSetAttribute(sparse_fwd_f32, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+    // (the limit belongs to the kernel, and other threads launch it too: the same for every call,
+    // the 4096 keys that nsa_sparse_fwd allows)
+    cudaError_t e = cudaFuncSetAttribute(sparse_fwd_f32, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 4 * 5);
     if (e != cudaSuccess) return e;
     sparse_fwd_f32<<<dim3((unsigned)s.tokens, hkv), 128, bytes, st>>>(
         (const float*)q, (const float*)k, (const float*)v, idx, (float*)o, lse, s, h, hkv, d, S, block_size,
