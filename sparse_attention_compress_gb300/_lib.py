@@ -647,7 +647,8 @@ def _expect(fn, device, **tensors):
 
 
 def _int32(fn, **values):
-    """ctypes would pass the low 32 bits of a larger number without a word."""
+    """ctypes would pass the low 32 bits of a larger number without a word.  (Called where a number
+    has a bit past the 31st: small negative ones are the C entry points' to refuse.)"""
     for name, x in values.items():
         if not -0x80000000 <= x <= 0x7fffffff:
             raise ValueError(f"{fn}: {name} = {x} does not fit 32 bits")
@@ -735,8 +736,10 @@ def _span_shape(fn, q, h_kv, d, device, cu_seqlens, max_seqlen):
         raise ValueError(f"{fn}: cu_seqlens needs at least two entries")
     if max_seqlen is None:
         raise ValueError(f"{fn}: cu_seqlens needs max_seqlen")
-    _int32(fn, max_seqlen=max_seqlen)
-    return dims[0], NsaShape(0, int(max_seqlen), cu_seqlens.data_ptr(), n, dims[0], dims[1], h_kv, d, NSA_BF16), n
+    longest = int(max_seqlen)
+    if longest >> 31:
+        _int32(fn, max_seqlen=longest)
+    return dims[0], NsaShape(0, longest, cu_seqlens.data_ptr(), n, dims[0], dims[1], h_kv, d, NSA_BF16), n
 
 
 def nsa_paged_append(k_new, v_new, k_pages, v_pages, block_table, cache_lens, *, weights=None, cu_seqlens=None,
@@ -778,7 +781,8 @@ def nsa_paged_attn_fwd(q, k_pages, v_pages, block_table, cache_lens, window=0, n
     already holds their keys), causal, with an optional window and n_sink tokens that stay
     visible beside it.  Returns out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_paged_attn_fwd"
-    _int32(fn, window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _int32(fn, window=window, n_sink=n_sink)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
@@ -807,7 +811,8 @@ def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n
     nsa_paged_attn_fwd call (same masks, its lse) gave to the key, over the heads of its group.
     Without weights the sum alone; out may be weights (the default when weights are given)."""
     fn = "nsa_paged_attn_weights"
-    _int32(fn, window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _int32(fn, window=window, n_sink=n_sink)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
@@ -833,7 +838,8 @@ def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_tabl
     listed twice).  Returns (keep [n_seqs, Hkv,
     budget] int32, -1 padded, and new_lens [n_seqs] int32)."""
     fn = "nsa_paged_evict"
-    _int32(fn, budget=budget, n_sink=n_sink, n_recent=n_recent)
+    if (budget | n_sink | n_recent) >> 31:
+        _int32(fn, budget=budget, n_sink=n_sink, n_recent=n_recent)
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)
     if weights is None:
@@ -884,7 +890,8 @@ def nsa_swa_sink_fwd(q, k, v, window=512, n_sink=4, scale=0.0, *, cu_seqlens=Non
     """Sliding window beside which the first n_sink tokens of each sequence stay visible.  Returns
     out, shaped like q; fills lse [tokens, H] fp32 if given."""
     fn = "nsa_swa_sink_fwd"
-    _int32(fn, window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _int32(fn, window=window, n_sink=n_sink)
     dev = q.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
@@ -913,7 +920,8 @@ def nsa_swa_sink_bwd(q, k, v, o, lse, d_o, window=512, n_sink=4, scale=0.0, *, c
                      workspace=None, dq=None, dk=None, dv=None, stream=None):
     """Backward of nsa_swa_sink_fwd: (dq, dk, dv) shaped like q, k, v from its o and lse."""
     fn = "nsa_swa_sink_bwd"
-    _int32(fn, window=window, n_sink=n_sink)
+    if (window | n_sink) >> 31:
+        _int32(fn, window=window, n_sink=n_sink)
     dev = q.device
     ctx, raw, share = _on(dev, stream)
     tokens, shp, _ = _packed_kv(fn, q, k, v, cu_seqlens, max_seqlen)
