@@ -26,7 +26,7 @@
 // are divided too; the fp32 partials are summed in order by key_sum_kernel.
 // No atomics: results are the same on every run.
 //
-// 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.25 ms, dkv 2.0 ms, together
+// 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.28 ms, dkv 1.98 ms, together
 // 650 TFLOP/s.  dkv keeps the tensor cores busy 72% of its time.  dq is bound by its CTAs' starts
 // and ends (five key tiles each, and 227 KB leave room for one on an SM) and by the chain S - P - dS
 // of a tile: tensor cores 31%.  Small calls are bound by the four kernels' own lengths: 3 sequences
@@ -44,8 +44,9 @@ constexpr uint32_t kBwdTmem = 512;
 // A row at token t has min(t + 1, window + n_sink) keys.  Those of rows with at most this many lie
 // in one key tile: bwd_layout sees to it.  (A test of P's values instead, for any row with a p of
 // 1/4 or more, took 7% of the whole backward at window 512 and 11% at 1024: the softmax warps, which
-// everything else waits for, would do it in every tile.  The remainders' code, a copy of its own,
-// takes 2% of it at window 512.)
+// everything else waits for, would do it in every tile.  The remainders' code, a copy of its own
+// that a tile chooses, takes 1% of it at 65536 tokens and window 512, 3 - 5% of small calls, and 17%
+// under a window of 24 and 4 sinks, where every tile has few keys.)
 constexpr int kFewKeys = 32;
 // Remainders of a half's 64 values lie this many TMEM columns behind the values.
 constexpr uint32_t kRest = 32;
@@ -539,9 +540,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (t_lo >= t_hi) return;  // (an empty chunk or share: key_sum_kernel does not read it)
   const int n = (t_hi - t_lo + p.tpc - 1) / p.tpc;
   const int used = p.tpc * p.R;  // rows of a tile
-  // some tile of the CTA has a row with few keys; the tile at token t has
-  const bool few = min(t_lo + 1, p.window + p.n_sink) <= kFewKeys;
-  auto few_at = [&](int t) { return min(t + 1, p.window + p.n_sink) <= kFewKeys; };
+  // Tiles that have a row with few keys come first: all, or those of a sequence's first tokens (where
+  // the round begins with the first tile).
+  const int n_few = p.window + p.n_sink <= kFewKeys ? n : min(n, (max(0, kFewKeys - t_lo) + p.tpc - 1) / p.tpc);
   // A query tile is seen by the key tiles of its whole window, CTAs that run side by side.
   // Each begins its round of query tiles where the others do (at the tile whose index is a
   // multiple of a full round's length), so that they ask for the same tile at about the same
@@ -678,14 +679,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc::fence_after();
       issue_s();
     }
-    auto walk = [&](auto with_rest) {
-      for (int j = 0; ok && j < n; ++j) {
+    auto walk = [&](auto with_rest, int j0, int j1) {
+      for (int j = j0; ok && j < j1; ++j) {
         if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
         if (j + 1 < n && !(ok = wait(bar(QFULL + rq.slot), rq.phase))) break;
         if (!(ok = wait(bar(PFULL), j & 1))) break;
         tc::fence_after();
         mma_split_a<D>(tmem + 256, tmem, dd + rd.slot * (TB >> 4), p.cols, j == 0, lead);
-        if (decltype(with_rest)::value && few_at(token_of(j)))
+        if constexpr (decltype(with_rest)::value)
           mma_split_a<D>(tmem + 256, tmem + kRest, dd + rd.slot * (TB >> 4), p.cols, false, lead);
         commit(bar(DEMPTY + rd.slot), lead);
         if (j + 1 < n)
@@ -695,10 +696,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         rd.next();
       }
     };
-    if (few)
-      walk(std::true_type{});
-    else
-      walk(std::false_type{});
+    walk(std::true_type{}, 0, n_few);
+    walk(std::false_type{}, n_few, n);
   } else if (warp == 10) {
     // ------------------------------------------------------------------ dP^T, dK += dS^T Q
     const uint32_t lead = elect(), vd = desc_k(v_s), dd = desc_k(do_s), qd = desc_mn(q_s);
@@ -715,13 +714,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc::fence_after();
       issue_dp();
     }
-    auto walk = [&](auto with_rest) {
-      for (int j = 0; ok && j < n; ++j) {
+    auto walk = [&](auto with_rest, int j0, int j1) {
+      for (int j = j0; ok && j < j1; ++j) {
         if (j + 1 < n && !(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;
         if (!(ok = wait(bar(DSFULL), j & 1))) break;
         tc::fence_after();
         mma_split_a<D>(tmem + 384, tmem + 128, qd + rq.slot * (TB >> 4), p.cols, j == 0, lead);
-        if (decltype(with_rest)::value && few_at(token_of(j)))
+        if constexpr (decltype(with_rest)::value)
           mma_split_a<D>(tmem + 384, tmem + 128 + kRest, qd + rq.slot * (TB >> 4), p.cols, false, lead);
         commit(bar(QEMPTY + rq.slot), lead);  // (S^T of the tile was done before its dS^T)
         if (j + 1 < n)
@@ -731,10 +730,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         rq.next();
       }
     };
-    if (few)
-      walk(std::true_type{});
-    else
-      walk(std::false_type{});
+    walk(std::true_type{}, 0, n_few);
+    walk(std::false_type{}, n_few, n);
   } else {
     // ------------------------------------------------------------------ softmax
     const int x = warp >> 2, row = (warp & 3) * 32 + lane, key = key0 + row, c0 = x * 64;
@@ -747,107 +744,103 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     Ring<kND> rd;
     bool ok = true;
     // (remainders or none in code of their own, as above)
-    auto walk = [&](auto with_rest) {
-      for (int j = 0; j < n; ++j, rq.next(), rd.next()) {
-        const int t = token_of(j);
-        const bool rest = decltype(with_rest)::value && few_at(t);
-        // columns [c_lo, c_hi) of this half are rows whose query sees this key
-        int c_lo = 0, c_hi = 0;
-        if (have) {
-          int64_t end = (int64_t)min(p.tpc, t_hi - t) * p.R;
-          if (key >= p.n_sink) end = min(end, ((int64_t)key + p.window - t) * p.R);
-          c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
-          c_hi = (int)max((int64_t)0, end) - c0;
-        }
-        if (!(ok = wait(bar(DFULL + rd.slot), rd.phase))) break;  // lse and D
-        if (!(ok = wait(bar(SFULL), j & 1))) break;
-        tc::fence_after();
-        float sv[64];
+    auto tile = [&](auto with_rest, int j) -> bool {
+      const int t = token_of(j);
+      // columns [c_lo, c_hi) of this half are rows whose query sees this key
+      int c_lo = 0, c_hi = 0;
+      if (have) {
+        int64_t end = (int64_t)min(p.tpc, t_hi - t) * p.R;
+        if (key >= p.n_sink) end = min(end, ((int64_t)key + p.window - t) * p.R);
+        c_lo = (int)max((int64_t)0, min((int64_t)(key - t) * p.R, (int64_t)ROWS)) - c0;
+        c_hi = (int)max((int64_t)0, end) - c0;
+      }
+      if (!wait(bar(DFULL + rd.slot), rd.phase)) return false;  // lse and D
+      if (!wait(bar(SFULL), j & 1)) return false;
+      tc::fence_after();
+      float sv[64];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32)
-          tc::tmem_ld32_nowait(s_t + c, sv + c);
-        const bool all = c_lo <= 0 && c_hi >= 64;
-        const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
-        tmem_wait_ld(sv);
-        tmem_wait_ld(sv + 32);
-        if (!__all_sync(0xffffffffu, all)) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            const uint32_t see = bits(c_lo - c, c_hi - c);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
-          }
-        }
+      for (int c = 0; c < 64; c += 32)
+        tc::tmem_ld32_nowait(s_t + c, sv + c);
+      const bool all = c_lo <= 0 && c_hi >= 64;
+      const float4* l4 = reinterpret_cast<const float4*>(&s_l2[j & 1][c0]);
+      tmem_wait_ld(sv);
+      tmem_wait_ld(sv + 32);
+      if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
-          uint32_t pk[16];
+          const uint32_t see = bits(c_lo - c, c_hi - c);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 l = l4[(c + e) / 4];
-            const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, pair(l.x, l.y)));
-            const float2 z = unpair(fma2(pair(sv[c + e + 2], sv[c + e + 3]), scale2, pair(l.z, l.w)));
-            sv[c + e] = ex2(y.x);
-            sv[c + e + 1] = ex2(y.y);
-            sv[c + e + 2] = ex2(z.x);
-            sv[c + e + 3] = ex2(z.y);
-            pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
-            pk[e / 2 + 1] = pack_bf16(sv[c + e + 2], sv[c + e + 3]);
-          }
-          if (c < nc) tmem_st16_nowait(s_t + c / 2, pk);
-          if (rest) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) pk[e / 2] = rest_pair(pair(sv[c + e], sv[c + e + 1]));
-            if (c < nc) tmem_st16_nowait(s_t + kRest + c / 2, pk);
-          }
+          for (int e = 0; e < 32; ++e) sv[c + e] = (see >> e) & 1u ? sv[c + e] : kNegInf;
         }
-        tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(PFULL));
-        if (!(ok = wait(bar(DPFULL), j & 1))) break;
-        tc::fence_after();
-        const float4* d4 = reinterpret_cast<const float4*>(&s_d[rq.slot][c0]);
-        float dp[64];
+      }
 #pragma unroll
-        for (int c = 0; c < 64; c += 32)
-          tc::tmem_ld32_nowait(p_t + c, dp + c);
-        tmem_wait_ld(dp);
-        tmem_wait_ld(dp + 32);
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          if (c >= nc) break;
-          uint32_t pk[16];
-          // (zero rows past the sequence have dp = 0, so p = 0 gives ds = 0)
-          auto ds = [&](int e, float x, float y) {
-            return mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), pair(x, y)));
-          };
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = l4[(c + e) / 4];
+          const float2 y = unpair(fma2(pair(sv[c + e], sv[c + e + 1]), scale2, pair(l.x, l.y)));
+          const float2 z = unpair(fma2(pair(sv[c + e + 2], sv[c + e + 3]), scale2, pair(l.z, l.w)));
+          sv[c + e] = ex2(y.x);
+          sv[c + e + 1] = ex2(y.y);
+          sv[c + e + 2] = ex2(z.x);
+          sv[c + e + 3] = ex2(z.y);
+          pk[e / 2] = pack_bf16(sv[c + e], sv[c + e + 1]);
+          pk[e / 2 + 1] = pack_bf16(sv[c + e + 2], sv[c + e + 3]);
+        }
+        if (c < nc) tmem_st16_nowait(s_t + c / 2, pk);
+        if constexpr (decltype(with_rest)::value) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) pk[e / 2] = rest_pair(pair(sv[c + e], sv[c + e + 1]));
+          if (c < nc) tmem_st16_nowait(s_t + kRest + c / 2, pk);
+        }
+      }
+      tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(PFULL));
+      if (!wait(bar(DPFULL), j & 1)) return false;
+      tc::fence_after();
+      const float4* d4 = reinterpret_cast<const float4*>(&s_d[rq.slot][c0]);
+      float dp[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32)
+        tc::tmem_ld32_nowait(p_t + c, dp + c);
+      tmem_wait_ld(dp);
+      tmem_wait_ld(dp + 32);
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        if (c >= nc) break;
+        uint32_t pk[16];
+        // (zero rows past the sequence have dp = 0, so p = 0 gives ds = 0)
+        auto ds = [&](int e, float x, float y) {
+          return mul2(pair(sv[c + e], sv[c + e + 1]), add2(pair(dp[c + e], dp[c + e + 1]), pair(x, y)));
+        };
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d = d4[(c + e) / 4];
+          pk[e / 2] = pack_pair(ds(e, d.x, d.y));
+          pk[e / 2 + 1] = pack_pair(ds(e + 2, d.z, d.w));
+        }
+        tmem_st16_nowait(p_t + c / 2, pk);
+        if constexpr (decltype(with_rest)::value) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 d = d4[(c + e) / 4];
-            pk[e / 2] = pack_pair(ds(e, d.x, d.y));
-            pk[e / 2 + 1] = pack_pair(ds(e + 2, d.z, d.w));
+            pk[e / 2] = rest_pair(ds(e, d.x, d.y));
+            pk[e / 2 + 1] = rest_pair(ds(e + 2, d.z, d.w));
           }
-          tmem_st16_nowait(p_t + c / 2, pk);
-          if (rest) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 d = d4[(c + e) / 4];
-              pk[e / 2] = rest_pair(ds(e, d.x, d.y));
-              pk[e / 2 + 1] = rest_pair(ds(e + 2, d.z, d.w));
-            }
-            tmem_st16_nowait(p_t + kRest + c / 2, pk);
-          }
+          tmem_st16_nowait(p_t + kRest + c / 2, pk);
         }
-        tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(DSFULL));
       }
+      tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(DSFULL));
+      return true;
     };
-    if (few)
-      walk(std::true_type{});
-    else
-      walk(std::false_type{});
+    for (int j = 0; j < n; ++j, rq.next(), rd.next())
+      if (!(ok = j < n_few ? tile(std::true_type{}, j) : tile(std::false_type{}, j))) break;
     if (ok) {
       ok = wait(bar(DVDONE), 0) && wait(bar(DKDONE), 0);
       tc::fence_after();
