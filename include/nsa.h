@@ -79,9 +79,9 @@ NSA_API const char* nsa_last_error(void);
  * the paged cache and of the window with sinks) bound every wait to about a second;
  * when one runs out the kernel sets the word to NSA_ERR_TIMEOUT, stops waiting, drains
  * its copies in flight and releases its tensor memory, so the context stays usable; while
- * the word is set, the tcgen05 branches, the decode step and the kernels of the paged cache
- * and the window with sinks skip their work.  Outputs of a call that set the word, or found
- * it set, are not valid.  Runtime error reporting, with no counterpart in the pages.
+ * the word is set, the tcgen05 branches, the decode step and the attention, weights and backward
+ * kernels of the paged cache and the window with sinks skip their work (append and eviction wait
+ * for nothing and go on).  Outputs of a call that set the word, or found it set, are not valid.  Runtime error reporting, with no counterpart in the pages.
  *   status  host int32 out: NSA_OK or NSA_ERR_TIMEOUT
  *   reset   nonzero: clear the word after reading it
  * Blocks until the device is idle (a synchronous copy).  Returns NSA_ERR_INVALID for a
@@ -533,7 +533,8 @@ NSA_API nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, con
  *   weights_out  [n_pages, h_kv, page_size] fp32; may be cache->weights itself.  A page
  *                listed by several sequences (a shared prefix) would be written by each, so
  *                give such sequences weights of their own.
- * v_pages is not read. */
+ * v_pages is not read.  With at most 48 rows (queries x heads of a group) a sequence, K is read whole
+ * whatever the window; with more, only the keys that some query sees. */
 NSA_API nsa_status nsa_paged_attn_weights(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,
                                           const float* lse, int window, int n_sink, float scale, float decay,
                                           float* weights_out, cudaStream_t stream);
@@ -563,6 +564,9 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  * nsa_paged_attn_fwd then serves.  Token t sees keys max(0, t-window+1) .. t and
  * 0 .. min(n_sink - 1, t).
  *   q, o [tokens, h, d]; k, v [tokens, h_kv, d] bf16;  lse nullable [tokens, h] fp32 out
+ *              k, v (and d_o, for the gradients) of a sequence's tokens have to be finite, those of
+ *              padding at its end included: a key that a query does not see has weight 0, and 0
+ *              times inf is NaN.  Rows past the last sequence may hold anything.
  *   workspace  nsa_swa_sink_fwd_workspace_size() bytes, 256-byte aligned (0 where no
  *              row's keys are divided); NULL allowed when that size is 0
  * Requires bf16, d in {64, 128}, h/h_kv <= 128, 1 <= window <= 2^28, 0 <= n_sink <= 2^28.

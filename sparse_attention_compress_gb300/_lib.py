@@ -809,7 +809,8 @@ def nsa_paged_attn_weights(q, k_pages, lse, block_table, cache_lens, window=0, n
                            decay=1.0, cu_seqlens=None, max_seqlen=None, out=None, stream=None):
     """out[page, kv-head, row] = decay * weights + the attention probabilities that the queries of a
     nsa_paged_attn_fwd call (same masks, its lse) gave to the key, over the heads of its group.
-    Without weights the sum alone; out may be weights (the default when weights are given)."""
+    Without weights the sum alone; out may be weights (the default when weights are given).  Cells
+    of no cached position are left as they were (in a new tensor they hold anything)."""
     fn = "nsa_paged_attn_weights"
     if (window | n_sink) >> 31:
         _int32(fn, window=window, n_sink=n_sink)

@@ -21,9 +21,9 @@
 //   few         (a decode step, a few speculative tokens: at most 48 rows a sequence and
 //               kv-head) as short, Q taking only the rows it has and the ring the rest, for
 //               HBM: 32 tokens over caches of 16384 to 32768 keys x 2 kv-heads 146 us
-//               (5.5 TB/s, 81% of a copy); one token over 4096 keys 15 us, the length of
-//               its two launches and of one CTA's start and end.  The rows past Q's are
-//               whatever lies there and stay in their own lanes.
+//               (5.5 TB/s, 81% of a copy); one token over 4096 keys 15 us on the device (25 us
+//               a call from Python), the length of its two launches and of one CTA's start
+//               and end.  The rows past Q's are whatever lies there and stay in their own lanes.
 // Work units (row tile, sequence, kv-head) that would not fill the SMs evenly have their keys
 // divided over several CTAs: each leaves (max, sum, unnormalised o) in the workspace and
 // combine_kernel joins them in a fixed order.  Roles: softmax warps (one row a thread),

@@ -4,7 +4,8 @@
 // to decay times the weight so far.
 //
 // Every key's sum stays in one thread's fp32 registers: no atomics, the same result on every
-// run, K read once.  The product is taken transposed, S^T = K Q^T (M = 128 keys, N = the
+// run, K read once (FEW reads all cached keys, seen or not: under a window that is many times what
+// its queries see).  The product is taken transposed, S^T = K Q^T (M = 128 keys, N = the
 // tile's rows), so that a TMEM lane is a key and the sum over queries needs no exchange
 // between threads.  One operand of a CTA stays and the other streams through a ring:
 //   many rows   128 keys stay, the query tiles that see them stream.  Four groups of summing
