@@ -353,7 +353,8 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 // as the first one's last blocks leave room, set themselves up, and wait for the first to be
 // complete before they read what it wrote.  (Every block of a first kernel says so at its start;
 // every block of a second one waits, so that whoever waits for the second waits for both.)
-// 3 x 1001 tokens forward and backward 80 -> 76 us, a cache of 4096 keys cut to 1024 13.6 -> 12.8;
+// On the device, 3 x 1001 tokens forward and backward 80 -> 76 us (77 now), a cache of 4096 keys cut to
+// 1024 13.6 -> 12.8 (12.3 now);
 // the attention's parts, whose waiting blocks would take room from the last round of others, gain
 // nothing (decode 146 -> 148) and are joined by an ordinary launch.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }

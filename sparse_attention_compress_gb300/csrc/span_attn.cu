@@ -17,7 +17,7 @@
 //   short       (spans of at most 16 key tiles) a CTA holds one row tile over one ring, so
 //               that two CTAs share an SM and a start or an end, which the few tiles do not
 //               hide, runs beside the other's products: 65536 tokens x 64 heads, window 512,
-//               1.53 ms (1.67 in the long form).
+//               1.54 ms (1.65 in the long form).
 //   few         (a decode step, a few speculative tokens: at most 48 rows a sequence and
 //               kv-head) as short, Q taking only the rows it has and the ring the rest, for
 //               HBM: 32 tokens over caches of 16384 to 32768 keys x 2 kv-heads 146 us
@@ -51,8 +51,8 @@ constexpr float kOutweighs = -1.f;  // log2
 constexpr int kFewRows = 48;  // what leaves room for two such CTAs on an SM beside three tiles each
 constexpr int kSms = 152;
 // Key tiles of a row tile up to which its CTA shares an SM.  32768 tokens x 64 heads (4 kv-heads,
-// d = 128) short and long: window 64 402 and 475 us, 512 767 and 841, 1024 1131 and 1186, 2048
-// 1841 and 1860, 4096 3230 and 3141; 1024 tokens x 16 heads, window 512, 14.8 and 17.2.
+// d = 128) short and long: window 64 392 and 461 us, 512 774 and 835, 1024 1127 and 1176, 2048
+// 1838 and 1848, 4096 3202 and 3128; 1024 tokens x 16 heads, window 512, 14.8 and 16.9.
 constexpr int kShortTiles = 16;
 
 enum Form { kLong, kShort, kFew };

@@ -27,7 +27,7 @@
 // No atomics: results are the same on every run.
 //
 // 65536 tokens x 64 heads (4 kv-heads, d = 128), window 512: dq 2.28 ms, dkv 1.98 ms, together
-// 650 TFLOP/s.  dkv keeps the tensor cores busy 72% of its time.  dq is bound by its CTAs' starts
+// 650 TFLOP/s.  dkv keeps the tensor cores busy 70% of its time.  dq is bound by its CTAs' starts
 // and ends (five key tiles each, and 227 KB leave room for one on an SM) and by the chain S - P - dS
 // of a tile: tensor cores 31%.  Small calls are bound by the four kernels' own lengths: 3 sequences
 // of at most 1001 tokens x 16 heads, window 256, forward and backward 78 us on the device.
