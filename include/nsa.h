@@ -559,6 +559,80 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
                                    int n_recent, const int32_t* new_table, int new_max_pages, int32_t* keep,
                                    int32_t* new_lens, cudaStream_t stream);
 
+/* Rotary rotation of new tokens' keys, and of their queries, on the way into a cache.  With the
+ * token at position p, pair i of the first rot_dim dimensions of a head (dimensions i and
+ * i + rot_dim / 2, or 2i and 2i + 1 where interleaved) is turned by the angle p * inv_freq[i]:
+ *   (x, y) -> (x cos - y sin, x sin + y cos);
+ * the other dimensions pass.  fp32 arithmetic, rounded once; the angle is reduced to a fraction
+ * of a turn in fixed point, so positions up to 2^31 are as exact as small ones.
+ *   inv_freq   device fp32 [rot_dim / 2], finite, |inv_freq| <= 2 pi
+ *   positions  nullable device int32 [tokens]: the position of every token (NULL: its position
+ *              in the cache; a cache that was cut no longer tells it)
+ *   q, q_out   [tokens, h, d] bf16, or both NULL: the queries of the same tokens, rotated to q_out
+ *              (which may be q itself), those of tokens that find no place in the cache included
+ * rot_dim is a multiple of 16 in [16, d]. */
+typedef struct nsa_rope {
+  const float* inv_freq;
+  const int32_t* positions;
+  int32_t rot_dim, interleaved;
+  const void* q;
+  void* q_out;
+} nsa_rope;
+
+/* nsa_paged_append of keys that are rotated on the way (and of values as they are): the
+ * same rules for places, dropped tokens and weights. */
+NSA_API nsa_status nsa_paged_append_rope(const nsa_shape* shape, const void* k_new, const void* v_new,
+                                         const nsa_rope* rope, const nsa_paged_cache* cache, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Paged cache held in 8 bits: pages, table and lengths as in nsa_paged_cache, with e4m3 codes in
+ * place of bf16 values and an fp32 scale for each block of block_size tokens and kv-head, for K
+ * and for V: value = code * scale.
+ *   k_pages, v_pages    [n_pages][page_stride bytes] e4m3; a page is page_size rows [h_kv, d].
+ *                       page_stride >= page_size * h_kv * d, a multiple of 16
+ *   k_scales, v_scales  [n_pages, h_kv, page_size / block_size] fp32.  nsa_paged_q8_append writes
+ *                       powers of two; the attention takes any in [2^-60, 2^60].  Those of
+ *                       blocks that hold no position below cache_lens may hold anything.
+ * block_size is 16, 32, 64 or 128 and at most page_size; the other limits are nsa_paged_cache's. */
+typedef struct nsa_paged_cache_q8 {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_table;
+  const int32_t* cache_lens;
+  int32_t n_pages, page_size, max_pages, block_size;
+  int64_t page_stride;
+} nsa_paged_cache_q8;
+
+/* Write the keys (rotated on the way, where rope is given) and values of new tokens into a cache held
+ * in 8 bits, at the places that nsa_paged_append gives them.  Per block, kv-head and K or V,
+ * with a the largest finite magnitude of the new values and e the least integer in
+ * [-60, 60] with a <= 448 * 2^e:
+ *   a block without earlier tokens (none at a position below the first new one) gets the scale
+ *   2^e; another one keeps its scale or, where 2^e is larger, takes it, and its earlier codes
+ *   are rounded again, to code * old / new;
+ *   code = value / scale rounded to e4m3 (ties to even; magnitudes above 448, which only infinities
+ *   and values past 448 * 2^60 have, become 448; NaN stays NaN).
+ * A scale never shrinks while its block holds earlier tokens (tokens that were taken back by a smaller
+ * cache_lens and written again find the scale that they left).  Positions behind the
+ * new tokens stay as they are.  Deterministic.  A block is read and written as a whole, so
+ * none that gets new tokens may be listed twice (a shared prefix is shared in whole blocks).
+ *   k_new, v_new  [tokens, h_kv, d] bf16
+ *   rope          nullable: keys as they are (rope->q then goes without rotation too: not at all) */
+NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new, const void* v_new,
+                                       const nsa_rope* rope, const nsa_paged_cache_q8* cache, cudaStream_t stream);
+
+/* nsa_paged_attn_fwd over a cache held in 8 bits: the same arguments, masks, empty rows and
+ * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
+ * cache_lens has to be finite.  Scores see q to 2^-22 of its row's largest element.
+ * Weights enter the second product with a relative error below 2^-10. */
+NSA_API size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window,
+                                                    int n_sink);
+NSA_API nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,
+                                         int64_t max_cache_len, int window, int n_sink, float scale, void* o,
+                                         float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Sliding window with sinks, for training: nsa_swa_fwd's window beside which the first
  * n_sink tokens of each sequence stay visible to every later token, the masks with which
  * nsa_paged_attn_fwd then serves.  Token t sees keys max(0, t-window+1) .. t and

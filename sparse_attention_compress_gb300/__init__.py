@@ -13,7 +13,8 @@ from ._lib import (NsaError, load, make_shape, nsa_block_sparse_fwd, nsa_block_s
                    nsa_sparse_decode_noalloc, nsa_sparse_decode_workspace_size, nsa_sparse_bwd,
                    nsa_sparse_bwd_workspace_size, nsa_sparse_fwd, nsa_swa_fwd, nsa_topk_select, num_cmp,
                    nsa_set_wait_limit_ns, nsa_paged_append, nsa_paged_attn_fwd, nsa_paged_attn_fwd_workspace_size,
-                   nsa_paged_attn_weights, nsa_paged_evict, nsa_swa_sink_fwd, nsa_swa_sink_fwd_workspace_size,
+                   nsa_paged_attn_weights, nsa_paged_evict, nsa_paged_append_rope, nsa_paged_q8_append,
+                   nsa_paged_q8_attn_fwd, nsa_paged_q8_attn_fwd_workspace_size, nsa_swa_sink_fwd, nsa_swa_sink_fwd_workspace_size,
                    nsa_swa_sink_bwd, nsa_swa_sink_bwd_workspace_size)
 
 __all__ = ["NsaError", "load", "make_shape", "nsa_block_sparse_fwd", "nsa_block_sparse_workspace_size",
@@ -24,5 +25,6 @@ __all__ = ["NsaError", "load", "make_shape", "nsa_block_sparse_fwd", "nsa_block_
            "nsa_sparse_decode_noalloc", "nsa_sparse_decode_workspace_size", "nsa_sparse_bwd",
            "nsa_sparse_bwd_workspace_size", "nsa_sparse_fwd", "nsa_swa_fwd", "nsa_topk_select", "num_cmp",
            "nsa_set_wait_limit_ns", "nsa_paged_append", "nsa_paged_attn_fwd", "nsa_paged_attn_fwd_workspace_size",
-           "nsa_paged_attn_weights", "nsa_paged_evict", "nsa_swa_sink_fwd", "nsa_swa_sink_fwd_workspace_size",
+           "nsa_paged_attn_weights", "nsa_paged_evict", "nsa_paged_append_rope", "nsa_paged_q8_append",
+           "nsa_paged_q8_attn_fwd", "nsa_paged_q8_attn_fwd_workspace_size", "nsa_swa_sink_fwd", "nsa_swa_sink_fwd_workspace_size",
            "nsa_swa_sink_bwd", "nsa_swa_sink_bwd_workspace_size"]

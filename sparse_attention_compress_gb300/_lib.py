@@ -38,6 +38,18 @@ class NsaPagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64)]
 
 
+class NsaRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p)]
+
+
+class NsaPagedCacheQ8(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("cache_lens", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("page_stride", ctypes.c_int64)]
+
+
 _SIGS = {
     "nsa_version": ([], ctypes.c_char_p),
     "nsa_last_error": ([], ctypes.c_char_p),
@@ -91,6 +103,10 @@ _SIGS = {
     "nsa_layer_fwd": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f,
                        _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
     "nsa_paged_append": ([_c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
+    "nsa_paged_append_rope": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
+    "nsa_paged_q8_append": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
+    "nsa_paged_q8_attn_fwd_workspace_size": ([_c_p, _c_i64, _c_int, _c_int], _c_sz),
+    "nsa_paged_q8_attn_fwd": ([_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
     "nsa_paged_attn_fwd_workspace_size": ([_c_p, _c_i64, _c_int, _c_int], _c_sz),
     "nsa_paged_attn_fwd": ([_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
     "nsa_paged_attn_weights": ([_c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_f, _c_f, _c_p, _c_p], _c_int),
@@ -618,7 +634,7 @@ def nsa_layer_bwd(q, k, v, gate_logits, saved, d_o, kernel=32, stride=16, block_
 # dense and of its type.  Tensors they allocate belong to the stream the call runs on.  A
 # decode step is a few microseconds of GPU time, so the checks come in two forms: a quick
 # test, and the search for what is wrong when it fails.
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 _HERE = contextlib.nullcontext()
 
 
@@ -680,12 +696,12 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _page_stride(fn, name, t):
+def _page_stride(fn, name, t, dtype=_BF16):
     """Pages may lie apart (a pool that interleaves K and V); a page itself is dense."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{fn}: {name} must be [n_pages, page_size, h_kv, d]")
-    if t.dtype is not _BF16:
-        raise TypeError(f"{fn}: {name} must be {_BF16}, not {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
     n, p, h, d = t.shape
     s = t.stride()
     if s[3] != 1 or (h > 1 and s[2] != d) or (p > 1 and s[1] != h * d):
@@ -865,6 +881,151 @@ def nsa_paged_evict(k_pages, v_pages, weights, block_table, cache_lens, new_tabl
     if rc:
         _check(rc, fn)
     return keep, new_lens
+
+
+# ----------------------------------------------------------------------------- rotation, 8-bit cache
+def _rope(fn, dev, tokens, dims, h_kv, d, q, inv_freq, positions, interleaved, q_out, share):
+    """(struct, q_out) of a rotation; q is shaped like the new tokens but for its heads."""
+    if inv_freq is None or not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError(f"{fn}: inv_freq must be [rot_dim / 2]")
+    index, pairs = dev.index, inv_freq.shape[0]
+    if not _fits(inv_freq, _F32, (pairs,), index) or not _fits(positions, _I32, (tokens,), index):
+        _expect(fn, dev, inv_freq=(inv_freq, _F32, (pairs,)), positions=(positions, _I32, (tokens,)))
+    if q is None:
+        if q_out is not None:
+            raise ValueError(f"{fn}: q_out needs q")
+        return NsaRope(inv_freq.data_ptr(), _addr(positions), 2 * pairs, int(bool(interleaved)), None, None), None
+    heads = q.shape[-2] if isinstance(q, torch.Tensor) and q.dim() == len(dims) else 0
+    if heads < 1 or heads % h_kv:
+        raise ValueError(f"{fn}: q must be shaped like k_new, with heads a multiple of {h_kv}")
+    shape = (*dims[:-2], heads, d)
+    if not _fits(q, _BF16, shape, index) or not _fits(q_out, _BF16, shape, index):
+        _expect(fn, dev, q=(q, _BF16, shape), q_out=(q_out, _BF16, shape))
+    if q_out is None:
+        q_out = _new(shape, _BF16, dev, share)
+    return NsaRope(inv_freq.data_ptr(), _addr(positions), 2 * pairs, int(bool(interleaved)), q.data_ptr(),
+                   q_out.data_ptr()), q_out
+
+
+def nsa_paged_append_rope(k_new, v_new, k_pages, v_pages, block_table, cache_lens, inv_freq, *, q=None, positions=None,
+                          interleaved=False, q_out=None, weights=None, cu_seqlens=None, max_seqlen=None, stream=None):
+    """nsa_paged_append of keys that are rotated by their position on the way: pair i of the first
+    2 * len(inv_freq) dimensions by position * inv_freq[i].  positions (int32 [tokens]) where the
+    place in the cache is not the position.  With q (the same tokens' queries) returns them
+    rotated too, in q_out (which may be q)."""
+    fn = "nsa_paged_append_rope"
+    dev = k_pages.device
+    ctx, raw, share = _on(dev, stream)
+    h_kv, d = k_pages.shape[-2:]
+    tokens, shp, n = _span_shape(fn, k_new, h_kv, d, dev, cu_seqlens, max_seqlen)
+    c = _paged_cache(fn, k_pages, v_pages, block_table, cache_lens, n, weights)[0]
+    if v_new is None or k_new.shape[-2] != h_kv or not _fits(v_new, _BF16, k_new.shape, dev.index):
+        want = (*k_new.shape[:-2], h_kv, d)
+        _expect(fn, dev, k_new=(k_new, _BF16, want), v_new=(v_new, _BF16, want))
+        raise TypeError(f"{fn}: v_new must be a tensor")
+    with ctx:
+        r, q_out = _rope(fn, dev, tokens, k_new.shape, h_kv, d, q, inv_freq, positions, interleaved, q_out, share)
+        if q is not None:
+            shp.h = q.shape[-2]
+        rc = load().nsa_paged_append_rope(ctypes.byref(shp), k_new.data_ptr(), v_new.data_ptr(), ctypes.byref(r),
+                                          ctypes.byref(c), raw)
+    if rc:
+        _check(rc, fn)
+    return q_out
+
+
+def _paged_cache_q8(fn, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, n_seqs):
+    """(struct, page_size) of a cache held in 8 bits."""
+    stride = _page_stride(fn, "k_pages", k_pages, _E4M3)
+    shape = k_pages.shape
+    n_pages, page, h_kv, _ = shape
+    if _page_stride(fn, "v_pages", v_pages, _E4M3) != stride or v_pages.shape != shape:
+        raise ValueError(f"{fn}: v_pages must have the shape and strides of k_pages")
+    if v_pages.device != k_pages.device:
+        raise ValueError(f"{fn}: v_pages is on {v_pages.device}, k_pages on {k_pages.device}")
+    index = k_pages.get_device()
+    blocks = k_scales.shape[2] if isinstance(k_scales, torch.Tensor) and k_scales.dim() == 3 else 0
+    if blocks < 1 or page % blocks:
+        raise ValueError(f"{fn}: k_scales must be [n_pages, h_kv, page_size / block_size]")
+    width = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
+    cells = (n_pages, h_kv, blocks)
+    if (v_scales is None or block_table is None or cache_lens is None or not _fits(k_scales, _F32, cells, index)
+            or not _fits(v_scales, _F32, cells, index) or not _fits(block_table, _I32, (n_seqs, width), index)
+            or not _fits(cache_lens, _I32, (n_seqs,), index)):
+        _expect(fn, k_pages.device, k_scales=(k_scales, _F32, cells), v_scales=(v_scales, _F32, cells),
+                block_table=(block_table, _I32, (n_seqs, None)), cache_lens=(cache_lens, _I32, (n_seqs,)))
+        raise TypeError(f"{fn}: v_scales, block_table and cache_lens must be tensors")
+    return NsaPagedCacheQ8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                           block_table.data_ptr(), cache_lens.data_ptr(), n_pages, page, width, page // blocks,
+                           stride), page
+
+
+def nsa_paged_q8_append(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, *, q=None,
+                        inv_freq=None, positions=None, interleaved=False, q_out=None, cu_seqlens=None, max_seqlen=None,
+                        stream=None):
+    """New tokens' keys and values into a cache held in 8 bits: pages float8_e4m3fn [n_pages,
+    page_size, Hkv, d], scales fp32 [n_pages, Hkv, page_size / block_size], powers of two.  A block's
+    scale grows with its largest value (its earlier codes are then rounded again).  With inv_freq
+    the keys (and q, returned) are rotated on the way as by nsa_paged_append_rope."""
+    fn = "nsa_paged_q8_append"
+    dev = k_pages.device
+    ctx, raw, share = _on(dev, stream)
+    h_kv, d = k_pages.shape[-2:]
+    tokens, shp, n = _span_shape(fn, k_new, h_kv, d, dev, cu_seqlens, max_seqlen)
+    c, _ = _paged_cache_q8(fn, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, n)
+    if v_new is None or k_new.shape[-2] != h_kv or not _fits(v_new, _BF16, k_new.shape, dev.index):
+        want = (*k_new.shape[:-2], h_kv, d)
+        _expect(fn, dev, k_new=(k_new, _BF16, want), v_new=(v_new, _BF16, want))
+        raise TypeError(f"{fn}: v_new must be a tensor")
+    if inv_freq is None and not (q is None and positions is None and q_out is None):
+        raise ValueError(f"{fn}: q, positions and q_out need inv_freq")
+    with ctx:
+        r = None
+        if inv_freq is not None:
+            r, q_out = _rope(fn, dev, tokens, k_new.shape, h_kv, d, q, inv_freq, positions, interleaved, q_out, share)
+            if q is not None:
+                shp.h = q.shape[-2]
+        rc = load().nsa_paged_q8_append(ctypes.byref(shp), k_new.data_ptr(), v_new.data_ptr(),
+                                        None if r is None else ctypes.byref(r), ctypes.byref(c), raw)
+    if rc:
+        _check(rc, fn)
+    return q_out
+
+
+def nsa_paged_q8_attn_fwd_workspace_size(shape: NsaShape, max_cache_len: int = 0, window: int = 0,
+                                         n_sink: int = 0) -> int:
+    _int32("nsa_paged_q8_attn_fwd_workspace_size", window=window, n_sink=n_sink)
+    return int(load().nsa_paged_q8_attn_fwd_workspace_size(ctypes.byref(shape), max_cache_len, window, n_sink))
+
+
+def nsa_paged_q8_attn_fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, window=0, n_sink=0,
+                          scale=0.0, *, cu_seqlens=None, max_seqlen=None, max_cache_len=None, workspace=None, out=None,
+                          lse=None, stream=None):
+    """nsa_paged_attn_fwd over a cache held in 8 bits (as nsa_paged_q8_append writes it): k = code *
+    k_scale, v = code * v_scale, read as they are."""
+    fn = "nsa_paged_q8_attn_fwd"
+    if (window | n_sink) >> 31:
+        _int32(fn, window=window, n_sink=n_sink)
+    dev = k_pages.device
+    ctx, raw, share = _on(dev, stream)
+    tokens, shp, n = _span_shape(fn, q, k_pages.shape[-2], k_pages.shape[-1], dev, cu_seqlens, max_seqlen)
+    c, page = _paged_cache_q8(fn, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, n)
+    rows = (tokens, q.shape[-2])
+    if not _fits(out, _BF16, q.shape, dev.index) or not _fits(lse, _F32, rows, dev.index):
+        _expect(fn, dev, out=(out, _BF16, q.shape), lse=(lse, _F32, rows))
+    if max_cache_len is None:
+        max_cache_len = c.max_pages * page
+    lib, sp = load(), ctypes.byref(shp)
+    with ctx:
+        if out is None:
+            out = torch.empty_like(q) if share is None else _new(q.shape, _BF16, dev, share)
+        need = 0 if workspace is not None else lib.nsa_paged_q8_attn_fwd_workspace_size(sp, max_cache_len, window, n_sink)
+        ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
+        rc = lib.nsa_paged_q8_attn_fwd(sp, q.data_ptr(), ctypes.byref(c), max_cache_len, window, n_sink, scale,
+                                       out.data_ptr(), _addr(lse), at, size, raw)
+    if rc:
+        _check(rc, fn)
+    return out
 
 
 # ----------------------------------------------------------------------------- window with sinks

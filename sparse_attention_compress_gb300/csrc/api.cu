@@ -117,7 +117,7 @@ const char* nsa_last_error(void) { return g_err; }
 nsa_status nsa_device_status(int32_t* status, int reset) {
   NSA_RANGE();
   NSA_REQUIRE(status != nullptr, NSA_ERR_INVALID, "nsa_device_status: status is NULL");
-  int32_t a = 0, b = 0, c = 0, f = 0, k = 0, m = 0, w = 0, x = 0;
+  int32_t a = 0, b = 0, c = 0, f = 0, k = 0, m = 0, w = 0, x = 0, y = 0;
   cudaError_t e = status_word_dense_tc(&a, reset != 0);
   if (e == cudaSuccess) e = status_word_decode(&b, reset != 0);
   if (e == cudaSuccess) e = status_word_decode_nosa(&c, reset != 0);
@@ -126,7 +126,8 @@ nsa_status nsa_device_status(int32_t* status, int reset) {
   if (e == cudaSuccess) e = status_word_span_attn(&m, reset != 0);
   if (e == cudaSuccess) e = status_word_span_weights(&w, reset != 0);
   if (e == cudaSuccess) e = status_word_span_bwd(&x, reset != 0);
-  *status = a ? a : b ? b : c ? c : f ? f : k ? k : m ? m : w ? w : x;
+  if (e == cudaSuccess) e = status_word_span_q8(&y, reset != 0);
+  *status = a ? a : b ? b : c ? c : f ? f : k ? k : m ? m : w ? w : x ? x : y;
   return cuda_status(e, "nsa_device_status");
 }
 
@@ -141,6 +142,7 @@ nsa_status nsa_set_wait_limit_ns(uint64_t ns) {
   if (e == cudaSuccess) e = wait_limit_span_attn(v);
   if (e == cudaSuccess) e = wait_limit_span_weights(v);
   if (e == cudaSuccess) e = wait_limit_span_bwd(v);
+  if (e == cudaSuccess) e = wait_limit_span_q8(v);
   return cuda_status(e, "nsa_set_wait_limit_ns");
 }
 
@@ -1185,6 +1187,126 @@ nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_p
   return cuda_status(launch_span_attn(s, q, &c, cache->k_pages, cache->v_pages, shape->h, shape->h_kv, shape->d, keys,
                                       window, n_sink, scale, o, lse, workspace, stream),
                      "nsa_paged_attn_fwd");
+}
+
+// ---- rotation and the cache held in 8 bits
+// Validate a rotation and the queries that it takes along (`need`: there has to be one).
+static nsa_status check_rope(const nsa_rope* r, const Seqs& s, int h, int d, bool need, RopeArgs* out, const char* fn) {
+  *out = RopeArgs{};
+  if (!r) {
+    NSA_REQUIRE(!need, NSA_ERR_INVALID, "%s: null rope", fn);
+    return NSA_OK;
+  }
+  NSA_REQUIRE(r->rot_dim >= 16 && r->rot_dim <= d && r->rot_dim % 16 == 0, NSA_ERR_UNSUPPORTED,
+              "%s: rot_dim must be a multiple of 16 from 16 to d (got %d)", fn, r->rot_dim);
+  NSA_REQUIRE(r->inv_freq != nullptr && ((reinterpret_cast<uintptr_t>(r->inv_freq) |
+                                          reinterpret_cast<uintptr_t>(r->positions)) & 3u) == 0, NSA_ERR_INVALID,
+              "%s: inv_freq must be non-null, inv_freq and positions 4-byte aligned", fn);
+  NSA_REQUIRE((r->q == nullptr) == (r->q_out == nullptr), NSA_ERR_INVALID, "%s: q and q_out go together", fn);
+  if (r->q) {
+    NSA_REQUIRE(aligned16(r->q) && aligned16(r->q_out), NSA_ERR_INVALID, "%s: q and q_out must be 16-byte aligned", fn);
+    const size_t qb = (size_t)s.tokens * h * d * 2;
+    NSA_REQUIRE(r->q == r->q_out || !overlap(r->q, qb, r->q_out, qb), NSA_ERR_INVALID,
+                "%s: q_out overlaps q and is not q itself", fn);
+  }
+  out->inv_freq = r->inv_freq;
+  out->positions = r->positions;
+  out->rot = r->rot_dim;
+  out->interleaved = r->interleaved != 0;
+  out->q = r->q;
+  out->q_out = r->q_out;
+  return NSA_OK;
+}
+
+nsa_status nsa_paged_append_rope(const nsa_shape* shape, const void* k_new, const void* v_new, const nsa_rope* rope,
+                                 const nsa_paged_cache* cache, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  RopeArgs r;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache(cache, shape->h_kv, shape->d, true, &c, __func__)) return st;
+  if (nsa_status st = check_rope(rope, s, shape->h, shape->d, true, &r, __func__)) return st;
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(k_new);
+  NSA_PTR(v_new);
+  return cuda_status(launch_paged_append_rope(s, k_new, v_new, r, c, cache->k_pages, cache->v_pages, cache->weights,
+                                              shape->h, shape->h_kv, shape->d, stream),
+                     "nsa_paged_append_rope");
+}
+
+// Validate a cache held in 8 bits and build the kernel-side view of it (page_stride in bytes).
+static nsa_status check_cache_q8(const nsa_paged_cache_q8* c, int h_kv, int d, PagedView* out, int* block_log2,
+                                 const char* fn) {
+  NSA_REQUIRE(c != nullptr, NSA_ERR_INVALID, "%s: null cache", fn);
+  NSA_REQUIRE(c->page_stride % 16 == 0, NSA_ERR_INVALID,
+              "%s: page_stride must be >= page_size * h_kv * d and a multiple of 16", fn);
+  const nsa_paged_cache as{c->k_pages,   c->v_pages,   nullptr,      c->block_table, c->cache_lens,
+                           c->n_pages, c->page_size, c->max_pages, c->page_stride};
+  if (nsa_status st = check_cache(&as, h_kv, d, true, out, fn)) return st;
+  NSA_REQUIRE(c->block_size >= 16 && c->block_size <= 128 && c->block_size <= c->page_size &&
+                  (c->block_size & (c->block_size - 1)) == 0,
+              NSA_ERR_UNSUPPORTED, "%s: block_size must be 16, 32, 64 or 128 and at most page_size (got %d)", fn,
+              c->block_size);
+  NSA_REQUIRE(c->k_scales != nullptr && c->v_scales != nullptr &&
+                  ((reinterpret_cast<uintptr_t>(c->k_scales) | reinterpret_cast<uintptr_t>(c->v_scales)) & 3u) == 0,
+              NSA_ERR_INVALID, "%s: k_scales and v_scales must be non-null and 4-byte aligned", fn);
+  *block_log2 = 0;
+  while ((1 << *block_log2) < c->block_size) ++*block_log2;
+  return NSA_OK;
+}
+
+nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new, const void* v_new, const nsa_rope* rope,
+                               const nsa_paged_cache_q8* cache, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  RopeArgs r;
+  int block;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache_q8(cache, shape->h_kv, shape->d, &c, &block, __func__)) return st;
+  if (nsa_status st = check_rope(rope, s, shape->h, shape->d, false, &r, __func__)) return st;
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(k_new);
+  NSA_PTR(v_new);
+  return cuda_status(launch_paged_q8_append(s, k_new, v_new, rope ? &r : nullptr, c, cache->k_pages, cache->v_pages,
+                                            cache->k_scales, cache->v_scales, block, shape->h, shape->h_kv, shape->d,
+                                            stream),
+                     "nsa_paged_q8_append");
+}
+
+size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink) {
+  Seqs s;
+  if (check_span_shape(shape, &s, __func__) != NSA_OK || check_span(window, n_sink, __func__) != NSA_OK) return 0;
+  return span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, span_keys(max_cache_len), window, n_sink);
+}
+
+nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,
+                                 int64_t max_cache_len, int window, int n_sink, float scale, void* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  NSA_RANGE();
+  Seqs s;
+  PagedView c;
+  int block;
+  if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
+  if (nsa_status st = check_cache_q8(cache, shape->h_kv, shape->d, &c, &block, __func__)) return st;
+  if (nsa_status st = check_span(window, n_sink, __func__)) return st;
+  NSA_REQUIRE(max_cache_len >= 0, NSA_ERR_INVALID, "nsa_paged_q8_attn_fwd: negative max_cache_len");
+  if (s.tokens == 0) return NSA_OK;
+  NSA_PTR(q);
+  NSA_PTR(o);
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(NSA_ERR_INVALID, "nsa_paged_q8_attn_fwd: lse misaligned");
+  const int keys = span_keys(max_cache_len);
+  const size_t need = span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, keys, window, n_sink);
+  if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
+  const size_t qb = (size_t)s.tokens * shape->h * shape->d * 2;
+  NSA_REQUIRE(!overlap(o, qb, q, qb), NSA_ERR_INVALID, "nsa_paged_q8_attn_fwd: o overlaps q");
+  if (scale <= 0.f) scale = 1.f / sqrtf((float)shape->d);
+  return cuda_status(launch_span_q8(s, q, c, cache->k_pages, cache->v_pages, cache->k_scales, cache->v_scales, block,
+                                    shape->h, shape->h_kv, shape->d, keys, window, n_sink, scale, o, lse, workspace,
+                                    stream),
+                     "nsa_paged_q8_attn_fwd");
 }
 
 nsa_status nsa_paged_attn_weights(const nsa_shape* shape, const void* q, const nsa_paged_cache* cache,

@@ -192,6 +192,30 @@ cudaError_t launch_paged_evict(int n_seqs, const PagedView& cache, const PagedVi
                                float* weights, int hkv, int d, int budget, int n_sink, int n_recent,
                                int32_t* keep, int32_t* new_lens, cudaStream_t st);
 
+// Appends with the rotary rotation, into the bf16 cache and into the cache held in 8 bits
+// (csrc/paged_rope.cu).  q may be null; rot 0 (or, for the 8-bit cache, no RopeArgs): no rotation.
+struct RopeArgs {
+  const float* inv_freq;
+  const int32_t* positions;
+  int rot, interleaved;
+  const void* q;
+  void* q_out;
+};
+cudaError_t launch_paged_append_rope(const Seqs& s, const void* k_new, const void* v_new, const RopeArgs& rope,
+                                     const PagedView& cache, void* k_pages, void* v_pages, float* weights, int h,
+                                     int hkv, int d, cudaStream_t st);
+cudaError_t launch_paged_q8_append(const Seqs& s, const void* k_new, const void* v_new, const RopeArgs* rope,
+                                   const PagedView& cache, void* k_pages, void* v_pages, float* k_scales,
+                                   float* v_scales, int block_log2, int h, int hkv, int d, cudaStream_t st);
+// Attention over a paged cache of e4m3 codes (page_stride in bytes) with scales (csrc/span_q8.cu).
+size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink);
+cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache, const void* k, const void* v,
+                           const float* k_scales, const float* v_scales, int block_log2, int h, int hkv, int d,
+                           int max_keys, int window, int n_sink, float scale, void* o, float* lse, void* workspace,
+                           cudaStream_t st);
+
+cudaError_t status_word_span_q8(int32_t* out, bool reset);
+cudaError_t wait_limit_span_q8(unsigned long long ns);
 cudaError_t status_word_span_attn(int32_t* out, bool reset);
 cudaError_t wait_limit_span_attn(unsigned long long ns);
 cudaError_t status_word_span_weights(int32_t* out, bool reset);

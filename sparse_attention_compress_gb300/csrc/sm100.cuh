@@ -249,10 +249,11 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 tensor map with 128-byte swizzling; dims and strides innermost first (strides in
+// Tensor map (bf16 with 128-byte swizzling unless said otherwise); dims and strides innermost first (strides in
 // bytes, one fewer than dims); out-of-range elements read as zero.
 inline bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
-                     const uint32_t* box) {
+                     const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gd[3] = {1, 1, 1}, gs[2] = {0, 0};
@@ -263,8 +264,8 @@ inline bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* 
   }
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides[i];
   auto encode = [&]() {
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), gd, gs, bx, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), gd, gs, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (encode()) return true;
