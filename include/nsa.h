@@ -625,8 +625,8 @@ NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new
 
 /* nsa_paged_attn_fwd over a cache held in 8 bits: the same arguments, masks, empty rows and
  * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
- * cache_lens has to be finite.  Scores see q to 2^-22 of its row's largest element.
- * Weights enter the second product with a relative error below 2^-10. */
+ * cache_lens has to be finite.  Scores see q as it is, down to 2^-24 of its row's largest element.
+ * Weights enter the second product with a relative error below 2^-8.6 (as bf16 they would have 2^-8). */
 NSA_API size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window,
                                                     int n_sink);
 NSA_API nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,

@@ -253,7 +253,8 @@ inline EncodeTiledFn encode_fn() {
 // bytes, one fewer than dims); out-of-range elements read as zero.
 inline bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
                      const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gd[3] = {1, 1, 1}, gs[2] = {0, 0};
@@ -265,7 +266,7 @@ inline bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* 
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides[i];
   auto encode = [&]() {
     return fn(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), gd, gs, bx, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (encode()) return true;

@@ -8,24 +8,26 @@
 //   S^T [128 keys x rows]  = K tile [128 keys x d] Q^T
 //   O^T [d x rows]        += V tile^T [d x 128 keys] P^T
 // (kind::f8f6f4; V is read MN-major, so nothing is transposed or converted).  Both partners
-// have to be e4m3 as well, whose 4 significant bits would be too few, so they are sums of
-// e4m3 terms that lie side by side in N, each with an accumulator column of its own:
-//   Q  = 2^-a (q1 + q2 / 32)            a per row, so that max |Q 2^a| is in [128, 256)
-//   P' = p1 + p2 / 32 + p3 / 1024       of P' = exp(t - m) sv 2^6 rounded to f16
-// q1 + q2 / 32 holds a bf16 exactly down to 2^-14 of its row's largest, and to 2^-22 of that below.
-// p1 + p2 / 32 + p3 / 1024 is within 2^-12 of P' (and P' within 2^-11 of its value, half a step
-// of f16; a bf16 P has 2^-8), down to 2^-26 of the row's largest weight.
+// have to be 8-bit floats as well, whose few significant bits would be too few, so they are sums of terms:
+//   Q  = 2^-a (q1 + q2)     a per row, so that max |Q 2^a| is in [128, 256); q1 in e4m3, the rest q2 in e5m2
+//   P' = p1 + p2 + p3       of P' = exp(t - m) sv 2^9 rounded to f16; all in e5m2
+// q1 leaves at most 8 units of bf16's last place, which the 3 significant bits of e5m2 hold, so Q is
+// exact down to 2^-17 of its row's largest element, and to 2^-25 of that below.  p1 + p2 + p3 is within
+// 2^-9 of P' (and P' within 2^-11 of its value, half a step of f16; a bf16 P has 2^-8), down
+// to 2^-26 of the row's largest weight.  q1 and q2 share an accumulator (K is read twice); p1, p2 and p3
+// lie side by side in N with accumulator columns of their own, so that V is read once.
 // A key's value scale sv is part of its weight, and the running maximum is that of t + log2 sv:
 // what is held in few bits is what the sum is made of.  The row sum takes exp(t - m) alone.
 //
 // A thread of the softmax has one key and HR rows, so a mask is a bit mask over rows, scales are
 // scalars of the thread, and only the running maximum has to be agreed on: it moves when some
-// key exceeds it by 2^2 (P' has that room), which a vote finds out for each tile.
+// key exceeds it by 2^6 (P' has that room), which a vote finds out for each tile.
 //
-// Work units (row tile, sequence, kv-head) that would not fill the SMs have their keys divided
-// over several CTAs, which leave (max, sum, unnormalised o); q8_combine_kernel joins them in order.
+// The key tiles of all units (row tile, sequence, kv-head) are cut into equal runs, one for each CTA
+// that fits the GPU: a run may start and end inside a unit, whose parts (max, sum, unnormalised
+// o) q8_combine_kernel joins in order.  So ragged caches even out, and a CTA sets itself
+// up once.
 #include <algorithm>
-#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -36,7 +38,7 @@ namespace nsa {
 namespace span {
 
 constexpr int kSms8 = 152;
-constexpr float kRoom = 6.f, kMoves = 8.f;  // log2 of P' at the running maximum, and at which it moves
+constexpr float kRoom = 9.f, kMoves = 15.f;  // log2 of P' at the running maximum, and at which it moves
 constexpr float kNone = -3e38f;             // running maximum of a row that has seen no key
 
 struct Keys8 {
@@ -48,21 +50,23 @@ struct Keys8 {
 
 template <int D, int NR>
 struct Cfg8 {
-  static constexpr int HR = NR / 2;  // rows a thread
-  static constexpr int PER_SM = NR == 64 ? 1 : 2;
-  static constexpr int THREADS = 352;  // 8 softmax warps, loads, products, scales
+  static constexpr int HR = 8, SUB = 2;   // rows and keys a thread: a turn takes SUB key tiles
+  static constexpr int GROUPS = NR / HR;  // softmax groups of four warps
+  static constexpr int PER_SM = NR <= 16 ? 2 : 1;
+  static constexpr int SOFT = 4 * GROUPS, THREADS = (SOFT + 4) * 32;  // softmax warps; loads of K and of V, products, queries and scales
   static constexpr int TILE = KT * D;
-  static constexpr int QN = 2 * NR, PN = 3 * NR;             // columns of S^T and O^T
-  static constexpr int PG = (PN + 127) / 128;                // 128-column groups of P
-  static constexpr int Q_BYTES = QN * D, P_BYTES = PG * KT * 128;  // of one P buffer
-  static constexpr int NS = ((PER_SM == 2 ? 108 : 220) * 1024 - 2 * P_BYTES - Q_BYTES) / TILE > 16
-                                ? 16
-                                : ((PER_SM == 2 ? 108 : 220) * 1024 - 2 * P_BYTES - Q_BYTES) / TILE;
-  static constexpr int SMEM = 2 * P_BYTES + NS * TILE + Q_BYTES + 1024;
-  static constexpr uint32_t TMEM = NR == 64 ? 512 : NR == 32 ? 256 : 128;
-  static constexpr uint32_t O_COL = 2 * QN;
+  // Rows of one of Q's terms (columns of S^T), columns of O^T: three terms of P; the products want multiples of 16
+  static constexpr int SN = NR < 16 ? 16 : NR, PN = (3 * NR + 15) / 16 * 16;
+  static constexpr int PW = NR == 8 ? 32 : NR == 16 ? 64 : 128;  // bytes of a key's line of P (PN, and room for the swizzle)
+  static constexpr int Q_BYTES = 2 * SN * D, P_TILE = KT * PW;  // of one of two Q buffers, of a key tile's P
+  // Slots of a turn's K tiles and of its V tiles
+  static constexpr int TURN = SUB * TILE, ROOM = ((PER_SM == 2 ? 108 : 219) * 1024 - SUB * P_TILE - 2 * Q_BYTES) / TURN;
+  static constexpr int NS = ROOM > 8 ? 8 : ROOM, NK = NS / 2, NV = NS - NK;
+  static constexpr int SMEM = SUB * P_TILE + NS * TURN + 2 * Q_BYTES + 1024;
+  static constexpr uint32_t O_COL = 2 * SUB * SN;  // behind two turns' S^T
+  static constexpr uint32_t TMEM = NR == 32 ? 256 : 128;
   static_assert(O_COL + PN <= TMEM, "");
-  static_assert(NS >= 4, "");
+  static_assert(NK >= 1 && NV >= 1, "");
 };
 
 struct Q8Params {
@@ -71,76 +75,194 @@ struct Q8Params {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;       // optional
-  float* part_o;    // [units][n_splits][NR][D]
-  float2* part_ml;  // [units][n_splits][NR]: (running maximum, sum)
-  int h, hkv, R, window, n_sink, row_tiles, n_splits;
+  float* part_o;    // [CTAs][2][NR][D]: unnormalised o of a CTA's last unit (1) and of its first (0)
+  float2* part_ml;  // [CTAs][2][NR]: (running maximum, sum)
+  int2* info;       // [units]: (first CTA, CTAs) that a unit's tiles went to
+  int h, hkv, R, window, n_sink, row_tiles;
+  int ctas;         // of a streamed call
+  int streamed;     // the tiles of all units in equal runs; else a CTA a unit
+  int min_tiles;    // of a run
   float scale_log2;
 };
 
-// Unit u: row tile (rows are (token, head of the group), heads fastest), kv-head, sequence.
-struct Unit8 {
-  int seq, g, Lq, row0;
+// Rows of a unit and the key tiles that they see.  Unit ((seq * hkv) + g) * row_tiles + rt: rows rt * NR ..
+// of (token, head of the group), heads fastest.
+template <int NR>
+struct Seq8 {
   int64_t start;
-  __device__ __forceinline__ Unit8(const Q8Params& p, int64_t u, int nr) {
-    const int rt = (int)(u % p.row_tiles);
-    u /= p.row_tiles;
-    g = (int)(u % p.hkv);
-    seq = (int)(u / p.hkv);
+  int Lq, kv_len;
+  __device__ __forceinline__ void load(const Q8Params& p, int seq) {
     start = seq_start(p.seqs, seq);
     Lq = seq_len(p.seqs, seq);
-    row0 = rt * nr;
+    kv_len = cached_len(p.keys.c, seq);
+  }
+  __device__ __forceinline__ int rows(const Q8Params& p, int rt) const {
+    return (int)max((int64_t)0, min((int64_t)NR, (int64_t)Lq * p.R - (int64_t)rt * NR));
+  }
+  __device__ __forceinline__ Tiles tiles(const Q8Params& p, int rt) const {
+    const int64_t row0 = (int64_t)rt * NR;
+    const int off = kv_len - Lq;  // position of the sequence's first query
+    return Tiles(off + (int)(row0 / p.R), off + (int)((row0 + rows(p, rt) - 1) / p.R), p.window, p.n_sink);
+  }
+  // Tiles that a unit counts for: a unit whose rows see nothing has an empty one, which writes them.
+  __device__ __forceinline__ int count(const Q8Params& p, int rt) const {
+    return rt >= p.row_tiles || rows(p, rt) == 0 ? 0 : max(1, tiles(p, rt).n);
   }
 };
+
+// The units of a CTA's run of tiles, one after another.  Every role walks the run for itself.
+template <int NR>
+struct Walk {
+  Seq8<NR> s;
+  int seq, g, rt;
+  int a, n, all;  // tiles a .. a + n - 1 of the unit's `all`
+  int left;       // of the run, these included
+  __device__ __forceinline__ Walk(const Q8Params& p, int seq0, int64_t at, int run) : seq(seq0), g(0), rt(0), left(run) {
+    s.load(p, seq);
+    int64_t per = 0;
+    for (int i = 0; i < p.row_tiles; ++i) per += s.count(p, i);
+    g = (int)(at / per);
+    at -= g * per;
+    for (int c; at >= (c = s.count(p, rt)); ++rt) at -= c;
+    a = (int)at;
+    all = s.count(p, rt);
+    n = min(all - a, left);
+  }
+  // one whole unit
+  __device__ __forceinline__ Walk(const Q8Params& p, int64_t unit) {
+    rt = (int)(unit % p.row_tiles);
+    unit /= p.row_tiles;
+    g = (int)(unit % p.hkv);
+    seq = (int)(unit / p.hkv);
+    s.load(p, seq);
+    a = 0;
+    left = n = all = s.count(p, rt);
+  }
+  __device__ __forceinline__ bool next(const Q8Params& p) {
+    left -= n;
+    if (left <= 0) return false;
+    a = 0;
+    all = s.count(p, ++rt);
+    if (all == 0) {
+      rt = 0;
+      if (++g == p.hkv) {
+        g = 0;
+        do {
+          if (++seq >= p.seqs.n_seqs) return false;
+          s.load(p, seq);
+        } while (s.count(p, 0) == 0);
+      }
+      all = s.count(p, 0);
+    }
+    n = min(all, left);
+    return true;
+  }
+};
+
+// The turns of a run (SUB tiles of a unit each).
+template <int NR, int SUB>
+struct Turns {
+  Walk<NR> u;
+  Tiles tl;
+  int j = 0;
+  bool more = true;
+  __device__ __forceinline__ Turns(const Q8Params& p, const Walk<NR>& w) : u(w), tl(w.s.tiles(p, w.rt)) {}
+  __device__ __forceinline__ void next(const Q8Params& p) {
+    if ((j += SUB) < u.n) return;
+    j = 0;
+    if ((more = u.next(p))) tl = u.s.tiles(p, u.rt);
+  }
+};
+
+// What the softmax has to know of a unit, in shared memory (its registers hold rows).
+struct Part8 {
+  int64_t start;
+  int seq, g, rt, a, n, all, rows, off, kv_len, ctas;  // ctas: how many the unit's tiles go to
+  int sink_end, shift, total, full_lo, full_hi;  // tiles full_lo .. full_hi - 1: every row sees every key that has a page
+};
+template <int NR>
+__device__ __forceinline__ void describe(const Q8Params& p, const Walk<NR>& u, int64_t t, int64_t total, int ctas,
+                                         Part8* s) {
+  const Tiles tl = u.s.tiles(p, u.rt);
+  const int off = u.s.kv_len - u.s.Lq, rows = u.s.rows(p, u.rt);
+  const int64_t row0 = (int64_t)u.rt * NR;
+  const int p0 = off + (int)(row0 / p.R), p1 = off + (int)((row0 + rows - 1) / p.R);
+  s->start = u.s.start;
+  s->seq = u.seq, s->g = u.g, s->rt = u.rt;
+  s->a = u.a, s->n = u.n, s->all = u.all;
+  s->rows = rows, s->off = off, s->kv_len = u.s.kv_len;
+  s->sink_end = tl.sink_end, s->shift = tl.shift, s->total = tl.total;
+  s->full_hi = max(0, p0 + 1 - tl.shift) / KT - u.a;  // the last key is at most the first position
+  s->full_lo = p.window > 0 ? max(0, (max(tl.sink_end, p1 - p.window + 1 - tl.shift) + KT - 1) / KT) - u.a : 0;
+  // the CTA that has tile e - 1 of all: floor((e ctas - 1) / total)
+  s->ctas = p.streamed ? (int)(((t + u.all) * ctas - 1) / total) - (int)blockIdx.x + 1 : 1;
+}
+
+// Index of the last of items 0 .. last that went to slot st of ns (-1 if none).
+__device__ __forceinline__ int last_in_stage(int last, int st, int ns) {
+  return last < st ? -1 : last - (last - st) % ns;
+}
 
 template <int NS>
 struct Bars8 {
   enum : int {
-    FULL = 0,
+    FULL = 0,             // [NS] K's slots, then V's
     EMPTY = NS,
-    SFULL = 2 * NS,       // [2] S^T of a tile
-    PFULL = SFULL + 2,    // [2] P of a tile
-    PVDONE = PFULL + 2,   // [2] its product
-    SCFULL = PVDONE + 2,  // [4] scales of four tiles
+    SFULL = 2 * NS,       // [2] S^T of a turn
+    PFULL = SFULL + 2,    // P of a turn
+    PVDONE = PFULL + 1,   // its product
+    SCFULL = PVDONE + 1,  // [4] scales of up to four tiles
     SCEMPTY = SCFULL + 4,
-    DRAIN = SCEMPTY + 4,
+    QFULL = SCEMPTY + 4,  // [2] queries of a unit
+    QEMPTY = QFULL + 2,
+    DRAIN = QEMPTY + 2,
     COUNT
   };
 };
 
 // ------------------------------------------------------------------ byte tiles
-// Row r of a tile of D-byte rows, 16-byte chunk ch, in the swizzle of D bytes (as TMA writes it).
+// Row r of a tile of D-byte rows (32, 64 or 128), 16-byte chunk ch, in the swizzle of D bytes (as TMA writes it).
 template <int D>
 __device__ __forceinline__ uint32_t at8(uint32_t base, int r, int ch) {
-  return base + r * D + ((ch ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+  return base + r * D + ((ch ^ (D == 128 ? r & 7 : D == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4);
 }
+// Page of the 16 keys at place `place` (a lane's) of a unit: -1 where the table names none, 0 where there are no keys.
+__device__ __forceinline__ int page_at(const Keys& c, int seq, int place, int sink_end, int shift, int kv_len) {
+  const int key = place < sink_end ? place : place + shift;
+  return key < kv_len ? page_of(c, seq, key) : 0;
+}
+// One warp fills a tile of w (a multiple of 32) rows as load_tile (span.cuh) does; pid16: page_at of a lane's 16 rows
+// (lanes 0 .. 7).
 template <int D>
 __device__ __forceinline__ void load_tile8(uint32_t dst, const CUtensorMap* big, const CUtensorMap* small,
-                                           const uint8_t* src, const Keys& c, int hkv, int g, int seq, int place0,
+                                           const uint8_t* src, const Keys& c, int hkv, int g, int pid16, int place0,
                                            int sink_end, int shift, int w, int kv_len, uint32_t bar, int lane) {
   const int page = 1 << c.page_log2;
   const int box = page < KT ? page : KT;
   const int first = place0 + shift;
-  const bool whole = w == KT && place0 >= sink_end && first + KT <= kv_len && (first & (box - 1)) == 0;
-  const int br = whole ? box : GRAN;
-  const int n = w / br;
-  const bool mine = lane < n;
-  const int place = place0 + lane * br, key = place < sink_end ? place : place + shift;
-  const int pid = mine && key < kv_len ? page_of(c, seq, key) : 0;
-  const bool ok = pid >= 0;
-  const bool plain = mine && (!ok || key + br > kv_len);
-  if (mine && !plain) tc::tma3d(dst + lane * br * D, whole ? big : small, g * D, key & (page - 1), pid, bar);
-  const uint32_t bad = __ballot_sync(0xffffffffu, mine && !ok);
+  const uint32_t bad = __ballot_sync(0xffffffffu, lane < w / GRAN && pid16 < 0);
+  if (w == KT && place0 >= sink_end && first + KT <= kv_len && (first & (box - 1)) == 0 && bad == 0) {
+    // whole pages (or parts of one)
+    if (lane == 0) tc::mbar_expect_tx(bar, KT * D);
+    const int pid = __shfl_sync(0xffffffffu, pid16, (lane * box / GRAN) & 7);
+    if (lane * box < KT) tc::tma3d(dst + lane * box * D, big, g * D, (first + lane * box) & (page - 1), pid, bar);
+    __syncwarp();
+    return;
+  }
+  const int place = place0 + lane * GRAN, key = place < sink_end ? place : place + shift;
+  const bool mine = lane < w / GRAN, plain = mine && (pid16 < 0 || key + GRAN > kv_len);
+  if (mine && !plain) tc::tma3d(dst + lane * GRAN * D, small, g * D, key & (page - 1), pid16, bar);
   uint32_t todo = __ballot_sync(0xffffffffu, plain);
-  const int bytes = (n - __popc(todo)) * br * D;
+  const int bytes = (w / GRAN - __popc(todo)) * GRAN * D;
   if (todo) {
     while (todo) {
       const int l = __ffs(todo) - 1;
       todo &= todo - 1;
       const bool okc = !((bad >> l) & 1u);
-      const int64_t pidc = __shfl_sync(0xffffffffu, pid, l);
+      const int64_t pidc = __shfl_sync(0xffffffffu, pid16, l);
       const int keyc = __shfl_sync(0xffffffffu, key, l);
-      for (int e = lane; e < br * (D / 16); e += 32) {
-        const int r = l * br + e / (D / 16), ch = e % (D / 16), kk = keyc + e / (D / 16);
+      for (int e = lane; e < GRAN * (D / 16); e += 32) {
+        const int r = l * GRAN + e / (D / 16), ch = e % (D / 16), kk = keyc + e / (D / 16);
         const bool in = okc && kk < kv_len;
         const int64_t row = pidc * c.page_stride + (int64_t)(kk & (page - 1)) * hkv * D;
         cp_async16(at8<D>(dst, r, ch), in ? src + row + g * D + ch * 16 : src, in ? 16 : 0);
@@ -157,11 +279,11 @@ __device__ __forceinline__ void load_tile8(uint32_t dst, const CUtensorMap* big,
 // ------------------------------------------------------------------ products
 // High word of a descriptor of tiles of B-byte rows in the B-byte swizzle: 8 rows to an atom.
 template <int B>
-constexpr uint32_t kDescHi8 = (uint32_t)(8 * B >> 4) | (1u << 14) | ((B == 128 ? 2u : 4u) << 29);
-// e4m3 x e4m3 -> fp32, M x N; A and B MN-major where said.
-constexpr uint32_t idesc8(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
+constexpr uint32_t kDescHi8 = (uint32_t)(8 * B >> 4) | (1u << 14) | ((B == 128 ? 2u : B == 64 ? 4u : 6u) << 29);
+// e4m3 x (e4m3 or e5m2) -> fp32, M x N; A and B MN-major where said.
+constexpr uint32_t idesc8(int M, int N, bool b_e5m2, bool mn) {
+  return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)mn << 15) | ((uint32_t)mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 template <uint32_t AHI, uint32_t BHI>
 __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accum, uint32_t lead) {
@@ -172,22 +294,33 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t b, uint32_
       "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(AHI), "n"(BHI)
       : "memory");
 }
-// S^T[128 x QN] = K[128 x D] Q[QN x D]^T, both K-major.
-template <int D, int QN>
+// S^T[128 x SN] = K[128 x D] (Q1 + Q2)[SN x D]^T, all K-major, Q2 behind Q1.
+template <int D, int SN>
 __device__ __forceinline__ void mma_s8(uint32_t d_tmem, uint32_t k, uint32_t q, uint32_t lead) {
 #pragma unroll
   for (int s = 0; s < D / 32; ++s)
-    mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + s * 2, idesc8(128, QN, false, false), s > 0, lead);
+    mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + s * 2, idesc8(128, SN, false, false), s > 0, lead);
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s)
+    mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + (SN * D >> 4) + s * 2, idesc8(128, SN, true, false), 1, lead);
 }
-// O^T[128 x PN] (+)= V[w x D]^T P[w x PN], both MN-major (D = 64: the lanes from 64 on repeat the
+// O^T[128 x PN] (+)= V[128 x D]^T P[128 x PN], both MN-major (D = 64: the lanes from 64 on repeat the
 // first ones, V's second column group lying 0 bytes behind the first).
-template <int D, int PN>
-__device__ __forceinline__ void mma_o8(uint32_t d_tmem, uint32_t v, uint32_t p, int w, bool first, uint32_t lead) {
+template <int D, int PN, int PW>
+__device__ __forceinline__ void mma_o8(uint32_t d_tmem, uint32_t v, uint32_t p, bool first, uint32_t lead) {
+#pragma unroll
+  for (int s = 0; s < KT / 32; ++s)
+    mma8<kDescHi8<D>, kDescHi8<PW>>(d_tmem, v + s * (32 * D >> 4), p + s * (32 * PW >> 4), idesc8(128, PN, true, true),
+                                    s > 0 || !first, lead);
+}
+// The same for a tile of w keys.
+template <int D, int PN, int PW>
+__device__ __forceinline__ void mma_o8_cut(uint32_t d_tmem, uint32_t v, uint32_t p, int w, bool first, uint32_t lead) {
 #pragma unroll
   for (int s = 0; s < KT / 32; ++s)
     if (s * 32 < w)
-      mma8<kDescHi8<D>, kDescHi8<128>>(d_tmem, v + s * (32 * D >> 4), p + s * (32 * 128 >> 4),
-                                       idesc8(128, PN, true, true), s > 0 || !first, lead);
+      mma8<kDescHi8<D>, kDescHi8<PW>>(d_tmem, v + s * (32 * D >> 4), p + s * (32 * PW >> 4), idesc8(128, PN, true, true),
+                                      s > 0 || !first, lead);
 }
 
 // N TMEM columns of a lane (8, 16 or 32), without the wait.
@@ -226,32 +359,98 @@ __device__ __forceinline__ void tmem_st_nowait(uint32_t a, const float* v) {
                  : "memory");
 }
 
-// Barrier of a group's 128 threads that also joins a condition.
-__device__ __forceinline__ bool bar_or(int id, bool x) {
+__device__ __forceinline__ bool device_stopped() { return tc::device_status_set(); }
+
+// Barrier of `threads` threads that also joins a condition.
+__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, %2, 128, p;\nselp.b32 %0, 1, 0, q;\n}\n"
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, %2, %3, p;\nselp.b32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x), "r"(id)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
 
-__device__ __forceinline__ uint16_t e4m3x2_of(uint32_t h2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(h2));
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of(uint16_t c) {
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint16_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(c));
   return r;
 }
-// 32 (h - c) for pairs of f16: exact, since c is h rounded to fewer bits.
-__device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t c) {
-  uint32_t r;
-  asm("{\n.reg .b32 d;\nsub.rn.f16x2 d, %1, %2;\nmul.rn.f16x2 %0, d, %3;\n}\n" : "=r"(r) : "r"(h), "r"(c), "r"(0x50005000u));
+__device__ __forceinline__ uint16_t e5m2x2_of(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(h2));
   return r;
+}
+// h less its two e5m2 (the high bytes of f16): exact, since they are h rounded to fewer bits.
+__device__ __forceinline__ uint32_t rest_of(uint32_t h, uint16_t c) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(h), "r"(__byte_perm(c, 0, 0x1404)));
+  return r;
+}
+
+// Query rows r0, r0 + step, ... of a unit as two terms: row r and row SN + r of the operand; what
+// turns their scores into exponents of 2; and the running maximum of no keys.  A warp's call.
+template <int D, int NR>
+__device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, uint32_t q_s, float* s_rs, float* s_nm, int r0, int step,
+                                        int lane) {
+  constexpr int E = D / 32, SN = Cfg8<D, NR>::SN;  // values a lane
+  const int rows = u.s.rows(p, u.rt);
+#pragma unroll 4
+  for (int r = r0; r < SN; r += step) {
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
+    if (r < rows) {
+      const int64_t rho = (int64_t)u.rt * NR + r;
+      const __nv_bfloat16* src = p.q + ((u.s.start + rho / p.R) * p.h + u.g * p.R + rho % p.R) * D + lane * E;
+      if constexpr (E == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
+        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
+        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
+        x[0] = __uint_as_float(w << 16), x[1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int ex = min(120, max(-120, 7 + 127 - (int)(top >> 23)));  // max |x| 2^ex in [128, 256)
+    const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+    uint32_t c1 = 0, c2 = 0;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float y0 = x[e] * up, y1 = x[e + 1] * up;
+      uint16_t h1, h2;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(h1) : "f"(y1), "f"(y0));
+      const uint32_t b = f16x2_of_e4m3(h1);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(h2) : "f"(y1 - f.y), "f"(y0 - f.x));
+      c1 |= (uint32_t)h1 << (8 * e);
+      c2 |= (uint32_t)h2 << (8 * e);
+    }
+    const int ch = lane * E / 16, in = lane * E % 16;
+    if constexpr (E == 4) {
+      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "r"(c1) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, SN + r, ch) + in), "r"(c2) : "memory");
+    } else {
+      asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "h"((uint16_t)c1) : "memory");
+      asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, SN + r, ch) + in), "h"((uint16_t)c2) : "memory");
+    }
+    if (lane == 0 && r < NR) {
+      s_rs[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+      s_nm[r] = -kNone;
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
 
 template <int D, int NR>
@@ -260,54 +459,87 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v16,
                    const Q8Params p) {
   using C = Cfg8<D, NR>;
-  constexpr int HR = C::HR, NS = C::NS, QN = C::QN, PN = C::PN;
+  constexpr int HR = C::HR, NS = C::NS, PN = C::PN, SUB = C::SUB, SOFT = C::SOFT, WARPS = C::THREADS / 32;
   using B = Bars8<NS>;
-  constexpr int kLoad = 8, kIssue = 9, kScale = 10;
+  constexpr int kLoadK = SOFT, kLoadV = SOFT + 1, kIssue = SOFT + 2, kAux = SOFT + 3, NK = C::NK, NV = C::NV;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B::COUNT];
-  __shared__ __align__(16) float4 s_sc[16 * 8];  // of tile i % 16, 16-key group: (sk, log2 sv, 1 / sv, whether there is a page)
-  __shared__ __align__(16) float s_rs[NR];       // scale log2(e) 2^-a of a row
-  __shared__ float s_max[2][4][HR], s_sum[2][4][HR];
+  __shared__ __align__(16) float4 s_sc[4][4][8];  // batch, tile, 16 keys: (sk, log2 sv, 1 / sv, whether there is a page)
+  __shared__ __align__(16) float s_rs[2][NR];    // scale log2(e) 2^-a of a row
+  __shared__ __align__(16) float s_nm[4][2][NR];  // of unit k at k % 4: minus the running maximum less kRoom (twice: see the moves)
+  __shared__ float s_max[C::GROUPS][4][HR], s_sum[C::GROUPS][4][HR];
+  __shared__ int64_t s_scan[WARPS], s_at;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ Part8 s_part[4];  // of unit k of the run, at k % 4
+  __shared__ int s_abort, s_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t p_s = base, slots = p_s + 2 * C::P_BYTES, q_s = slots + NS * C::TILE;
+  const uint32_t p_s = base, slots = p_s + C::SUB * C::P_TILE, q_s = slots + NS * C::TURN;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   volatile int* abort = &s_abort;
 
+  launch_dependents();
   if (stopped()) return;
   const Waits wait(abort);
-  const int64_t unit = (int64_t)blockIdx.x / p.n_splits;
-  const int split = (int)((int64_t)blockIdx.x % p.n_splits);
-  const Unit8 un(p, unit, NR);
-  const int seq = un.seq, g = un.g, R = p.R;
-  const int64_t rows_all = (int64_t)un.Lq * R;
-  if (un.row0 >= rows_all) return;
-  const int rows = (int)min((int64_t)NR, rows_all - un.row0);
-  const int kv_len = cached_len(p.keys.c, seq);
-  const int off = kv_len - un.Lq;  // position of the sequence's first query
-  const Tiles tiles(off + un.row0 / R, off + (un.row0 + rows - 1) / R, p.window, p.n_sink);
-  const int a = (int)((int64_t)tiles.n * split / p.n_splits);
-  const int n = (int)((int64_t)tiles.n * (split + 1) / p.n_splits) - a;  // this CTA's tiles: a .. a + n - 1
-  const int groups = rows > HR ? 2 : 1;                                  // softmax groups that have rows
-  // whole steps of 32 keys (the product's K): what lies past the keys is zeros
-  auto width = [&](int i) { return min(KT, (tiles.width(i) + 31) & ~31); };
+  // ------------------------------------------------------------------ this CTA's run of tiles
+  int run = 0, ctas = 0;
+  int64_t t0 = 0, total = 0;  // the run: tiles t0 .. t0 + run - 1 of `total`
+  if (p.streamed) {
+    const int per = (p.seqs.n_seqs + C::THREADS - 1) / C::THREADS, i0 = min(p.seqs.n_seqs, tid * per),
+              i1 = min(p.seqs.n_seqs, i0 + per);
+    auto tiles_of = [&](int i) {
+      Seq8<NR> s;
+      s.load(p, i);
+      int64_t c = 0;
+      for (int rt = 0; rt < p.row_tiles; ++rt) c += s.count(p, rt);
+      return c * p.hkv;
+    };
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += tiles_of(i);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / p.min_tiles));
+    if (total == 0 || blockIdx.x >= ctas) return;
+    t0 = total * blockIdx.x / ctas;
+    run = (int)(total * (blockIdx.x + 1) / ctas - t0);
+    before += incl - mine;
+    if (before <= t0 && t0 < before + mine) {
+      int i = i0;
+      for (int64_t c; before + (c = tiles_of(i)) <= t0; ++i) before += c;
+      s_seq = i;
+      s_at = t0 - before;
+    }
+  } else {
+    if (Walk<NR>(p, (int64_t)blockIdx.x).n == 0) return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(bar(B::FULL + i), 1);
+      tc::mbar_init(bar(B::FULL + i), SUB);
       tc::mbar_init(bar(B::EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(B::SFULL + i), 1);
-      tc::mbar_init(bar(B::PFULL + i), 4 * groups);
-      tc::mbar_init(bar(B::PVDONE + i), 1);
+      tc::mbar_init(bar(B::QFULL + i), 1);
+      tc::mbar_init(bar(B::QEMPTY + i), SOFT);
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(bar(B::SCFULL + i), 1);
-      tc::mbar_init(bar(B::SCEMPTY + i), 4 * groups);
+      tc::mbar_init(bar(B::SCEMPTY + i), SOFT);
     }
+    tc::mbar_init(bar(B::PFULL), SOFT);
+    tc::mbar_init(bar(B::PVDONE), 1);
     tc::mbar_init(bar(B::DRAIN), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -316,389 +548,472 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
     tmem_alloc(smem_u32(&s_tmem), C::TMEM);
     tc::fence_before();
   }
-  if (warp < 8) {
-    // Q's rows as two e4m3 terms: row r and row NR + r of the operand
-    constexpr int E = D / 32;  // values a lane
-    for (int r = warp; r < NR; r += 8) {
-      float x[E];
-      if (r < rows) {
-        const int64_t rho = un.row0 + r;
-        const __nv_bfloat16* src = p.q + ((un.start + rho / R) * p.h + g * R + rho % R) * D + lane * E;
-        if constexpr (E == 4) {
-          const uint2 u = *reinterpret_cast<const uint2*>(src);
-          x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
-          x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
-        } else {
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(src);
-          x[0] = __uint_as_float(u << 16), x[1] = __uint_as_float(u & 0xffff0000u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-      }
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int ex = min(120, max(-120, 7 + 127 - (int)(top >> 23)));  // max |x| 2^ex in [128, 256)
-      const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-      uint32_t c1 = 0, c2 = 0;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float y0 = x[e] * up, y1 = x[e + 1] * up;
-        uint16_t h1, h2;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(h1) : "f"(y1), "f"(y0));
-        const uint32_t b = f16x2_of(h1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(h2) : "f"((y1 - f.y) * 32.f), "f"((y0 - f.x) * 32.f));
-        c1 |= (uint32_t)h1 << (8 * e);
-        c2 |= (uint32_t)h2 << (8 * e);
-      }
-      const int ch = lane * E / 16, in = lane * E % 16;
-      if constexpr (E == 4) {
-        asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "r"(c1) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, NR + r, ch) + in), "r"(c2) : "memory");
-      } else {
-        asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "h"((uint16_t)c1) : "memory");
-        asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, NR + r, ch) + in), "h"((uint16_t)c2) : "memory");
-      }
-      if (lane == 0) s_rs[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
-    }
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-  }
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
+  Walk<NR> u = p.streamed ? Walk<NR>(p, s_seq, s_at, run) : Walk<NR>(p, (int64_t)blockIdx.x);
+  // whole steps of 32 keys (the product's K): what lies past the keys is zeros
+  auto width = [&](const Tiles& tl, int i) { return max(0, min(KT, (tl.width(i) + 31) & ~31)); };
 
-  int last_item = -1;  // loading warp: the last item handed to the ring
-  if (warp == kLoad) {
-    // ------------------------------------------------------------------ K and V tiles in turn
+  int last_item = -1;  // loading warps: the last turn handed to their ring
+  if (warp == kLoadK || warp == kLoadV) {
+    // ------------------------------------------------------------------ K tiles, or V tiles
+    // (one code for both: instructions of warps that run rarely come from far)
+    const bool is_v = warp == kLoadV;
+    const int first = is_v ? NK : 0, ns = is_v ? NV : NK;
+    const CUtensorMap *big = is_v ? &tm_v : &tm_k, *small = is_v ? &tm_v16 : &tm_k16;
+    const uint8_t* src = is_v ? p.keys.v : p.keys.k;
+    Turns<NR, SUB> t(p, u);
     int slot = 0;
     uint32_t phase = 1;
-    for (int i = 0; i < 2 * n; ++i) {
-      const int j = a + (i >> 1);
-      const bool is_v = i & 1;
-      if (i >= NS && !wait(bar(B::EMPTY + slot), phase)) break;
-      load_tile8<D>(slots + slot * C::TILE, is_v ? &tm_v : &tm_k, is_v ? &tm_v16 : &tm_k16,
-                    is_v ? p.keys.v : p.keys.k, p.keys.c, p.hkv, g, seq, j * KT, tiles.sink_end, tiles.shift, width(j),
-                    kv_len, bar(B::FULL + slot), lane);
-      last_item = i;
-      if (++slot == NS) {
+    auto pages = [&](int i) {
+      return page_at(p.keys.c, t.u.seq, (t.u.a + i) * KT + (lane & 7) * GRAN, t.tl.sink_end, t.tl.shift, t.u.s.kv_len);
+    };
+    for (; t.more; t.next(p)) {
+      int pid = pages(t.j);
+      if (last_item + 1 >= ns && !wait(bar(B::EMPTY + first + slot), phase)) break;
+#pragma unroll 1
+      for (int y = 0; y < SUB; ++y) {
+        const int j = t.j + y;
+        if (j < t.u.n)
+          load_tile8<D>(slots + (first + slot) * C::TURN + y * C::TILE, big, small, src, p.keys.c, p.hkv, t.u.g, pid,
+                        (t.u.a + j) * KT, t.tl.sink_end, t.tl.shift, width(t.tl, t.u.a + j), t.u.s.kv_len,
+                        bar(B::FULL + first + slot), lane);
+        else if (lane == 0)
+          tc::mbar_arrive(bar(B::FULL + first + slot));
+        pid = pages(j + 1);
+      }
+      ++last_item;
+      if (++slot == ns) {
         slot = 0;
         phase ^= 1u;
       }
     }
-  } else if (warp == kScale) {
-    // ------------------------------------------------------------------ scales of four tiles
-    const int batches = (n + 3) / 4;
-    for (int i = 0; i < batches; ++i) {
-      if (i >= 4 && !wait(bar(B::SCEMPTY + (i & 3)), ((i >> 2) - 1) & 1)) break;
-      const int tile = a + i * 4 + (lane >> 3), place = tile * KT + (lane & 7) * GRAN;
-      const int key = place < tiles.sink_end ? place : place + tiles.shift;
-      float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (tile < a + n && place < tiles.total && key < kv_len) {
-        const int pid = page_of(p.keys.c, seq, key);
-        if (pid >= 0) {
-          const int pl = p.keys.c.page_log2, bl = p.keys.block_log2;
-          const int64_t at = (((int64_t)pid * p.hkv + g) << (pl - bl)) + ((key & ((1 << pl) - 1)) >> bl);
-          const float sv = __ldg(p.keys.vs + at);
-          sc = make_float4(__ldg(p.keys.ks + at), log2f(sv), 1.f / sv, 1.f);
-        }
-      }
-      s_sc[(i & 3) * 32 + lane] = sc;
+  } else if (warp == kAux) {
+    // ------------------------------------------------------------------ per unit: what the softmax needs to know, queries, scales
+    // The first unit's queries are the softmax warps' own; a later one's are loaded once the scales of the
+    // unit before are on their way.
+    Ring<2> rq;
+    Ring<4> rs;
+    bool ok = true, again = false;
+    int64_t t = t0;
+    for (int k = 0; ok; ++k) {
+      if (k > 1 && !(ok = wait(bar(B::QEMPTY + rq.slot), rq.phase ^ 1u))) break;
+      if (lane == 0) describe<NR>(p, u, t, total, ctas, &s_part[k & 3]);
+      if (k > 0)
+        load_q8<D, NR>(p, u, q_s + rq.slot * C::Q_BYTES, s_rs[rq.slot], s_nm[k & 3][0], 0, 1, lane);
+      else
+        named_barrier(1, (SOFT + 1) * 32);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(B::SCFULL + (i & 3)));
+      if (lane == 0) tc::mbar_arrive(bar(B::QFULL + rq.slot));
+      rq.next();
+      const Tiles tl = u.s.tiles(p, u.rt);
+      for (int i = 0; i < u.n; i += 4) {
+        if (again && !(ok = wait(bar(B::SCEMPTY + rs.slot), rs.phase ^ 1u))) break;
+        const int tile = u.a + i + (lane >> 3), place = tile * KT + (lane & 7) * GRAN;
+        const int key = place < tl.sink_end ? place : place + tl.shift;
+        float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tile < u.a + u.n && place < tl.total && key < u.s.kv_len) {
+          const int pid = page_of(p.keys.c, u.seq, key);
+          if (pid >= 0) {
+            const int pl = p.keys.c.page_log2, bl = p.keys.block_log2;
+            const int64_t at = (((int64_t)pid * p.hkv + u.g) << (pl - bl)) + ((key & ((1 << pl) - 1)) >> bl);
+            const float sv = __ldg(p.keys.vs + at);
+            sc = make_float4(__ldg(p.keys.ks + at), log2f(sv), 1.f / sv, 1.f);
+          }
+        }
+        s_sc[rs.slot][lane >> 3][lane & 7] = sc;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::SCFULL + rs.slot));
+        rs.next();
+        again |= rs.slot == 0;
+      }
+      t += u.n;
+      if (!u.next(p)) break;
     }
   } else if (warp == kIssue) {
     // ------------------------------------------------------------------ products
-    const uint32_t lead = elect();
-    const uint32_t q_d = desc_k(q_s), k_d = desc_k(slots);
-    // V: the second group of 64 columns (D = 64) is the first again; P: groups P_BYTES / PG apart
-    const uint32_t v_d = (slots & 0x3FFFF) >> 4, p_d = ((p_s & 0x3FFFF) >> 4) | ((uint32_t)(KT * 128 >> 4) << 16);
-    Ring<NS> rk, rv;
-    rv.next();
+    // S^T runs up to two turns ahead of O^T, across the units of the run.
+    const uint32_t lead = elect(), q_d = desc_k(q_s), k_d = desc_k(slots);
+    // V: the second group of 64 columns (D = 64) is the first again
+    const uint32_t v_d = ((slots + NK * C::TURN) & 0x3FFFF) >> 4, p_d = (p_s & 0x3FFFF) >> 4;
+    Turns<NR, SUB> ts(p, u), to = ts;
+    Ring<NK> rk;
+    Ring<NV> rv;
+    Ring<2> rq;
     bool ok = true;
-    auto issue_s = [&](int b) {
-      ok = wait(bar(B::FULL + rk.slot), rk.phase);
-      if (!ok) return;
-      tc::fence_after();
-      mma_s8<D, QN>(tmem + b * QN, k_d + rk.slot * (C::TILE >> 4), q_d, lead);
-      commit(bar(B::SFULL + b), lead);
-      commit(bar(B::EMPTY + rk.slot), lead);
-      rk.next();
-      rk.next();
-    };
-    if (n > 0) issue_s(0);
-    if (ok && n > 1) issue_s(1);
-    for (int it = 0; ok && it < n; ++it) {
-      const int b = it & 1;
-      if (!(ok = wait(bar(B::FULL + rv.slot), rv.phase))) break;
-      if (!(ok = wait(bar(B::PFULL + b), (it >> 1) & 1))) break;
-      tc::fence_after();
-      mma_o8<D, PN>(tmem + C::O_COL, v_d + rv.slot * (C::TILE >> 4), p_d + b * (C::P_BYTES >> 4), width(a + it), it == 0,
-                    lead);
-      commit(bar(B::EMPTY + rv.slot), lead);
-      commit(bar(B::PVDONE + b), lead);
-      rv.next();
-      rv.next();
-      if (it + 2 < n) issue_s(b);  // (its scores were read before P was written)
-    }
-  } else if (warp < 4 * groups) {
-    // ------------------------------------------------------------------ softmax: one key, HR rows
-    const int x = warp >> 2, krow = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_t = tmem + C::O_COL + x * HR + lane_base;
-    float m[HR], l[HR];  // m: the running maximum less kRoom, so that P' = exp2(t - m)
-#pragma unroll
-    for (int e = 0; e < HR; ++e) {
-      m[e] = kNone;
-      l[e] = 0.f;
-    }
-    bool ok = true;
-    int it = 0;
-    for (; it < n; ++it) {
-      const int b = it & 1;
-      const uint32_t s_t = tmem + b * QN + x * HR + lane_base;
-      float t[HR];
-      float inv_sv = 0.f;
-      uint32_t see = 0;
-      bool move = false;
-      ok = ok && wait(bar(B::SCFULL + ((it >> 2) & 3)), (it >> 4) & 1) && wait(bar(B::SFULL + b), (it >> 1) & 1);
-      if (ok) {
+    for (uint32_t it = 0; ok && to.more; ++it) {
+      // turn it's scores, and from the third turn on the product of turn it - 2 before them
+      if (it >= 2) {
+        const int left = to.u.n - to.j;  // of the unit
+        if (!(ok = wait(bar(B::FULL + NK + rv.slot), rv.phase) && wait(bar(B::PFULL), it & 1))) break;
         tc::fence_after();
-        float lo[HR];
-        tmem_ld_nowait<HR>(s_t, t);
-        tmem_ld_nowait<HR>(s_t + NR, lo);
-        const float4 sc = s_sc[(it & 15) * 8 + (krow >> 4)];
-        inv_sv = sc.z;
-        // rows that see the key: from the first at its position on, to the last whose window reaches it
-        const int place = (a + it) * KT + krow, key = place < tiles.sink_end ? place : place + tiles.shift;
-        const int64_t r0 = un.row0 + x * HR;
-        if (sc.w != 0.f && place < tiles.total && key < kv_len && !(place < tiles.sink_end && key >= p.n_sink)) {
-          const int64_t from = (int64_t)(key - off) * R - r0;
-          const int64_t to = p.window > 0 && key >= p.n_sink ? ((int64_t)key + p.window - off) * R - r0 : HR;
-          see = bits((int)min((int64_t)32, max((int64_t)0, from)), (int)min((int64_t)32, max((int64_t)0, to)));
-        }
-        tmem_landed<HR>(t);
+        const uint32_t vv = v_d + rv.slot * (C::TURN >> 4);
+        if (left > SUB) {  // (no branch between the products)
 #pragma unroll
-        for (int e = 0; e < HR; ++e) asm volatile("" : "+f"(lo[e]));
-        float most = kNegInf;
-#pragma unroll
-        for (int e = 0; e < HR; ++e) {
-          const float s = fmaf(lo[e], 0.03125f, t[e]);
-          t[e] = (see >> e) & 1u ? fmaf(s, s_rs[x * HR + e] * sc.x, sc.y) : kNegInf;
-          most = fmaxf(most, t[e] - m[e]);
+          for (int y = 0; y < SUB; ++y)
+            mma_o8<D, PN, C::PW>(tmem + C::O_COL, vv + y * (C::TILE >> 4), p_d + y * (C::P_TILE >> 4), to.j + y == 0, lead);
+        } else {
+#pragma unroll 1
+          for (int y = 0; y < left; ++y)
+            mma_o8_cut<D, PN, C::PW>(tmem + C::O_COL, vv + y * (C::TILE >> 4), p_d + y * (C::P_TILE >> 4),
+                                     width(to.tl, to.u.a + to.j + y), to.j + y == 0, lead);
         }
-        move = most > kMoves;
+        commit(bar(B::PVDONE), lead);
+        commit(bar(B::EMPTY + NK + rv.slot), lead);
+        rv.next();
+        to.next(p);
       }
-      if (bar_or(1 + x, move || !ok)) {
-        // the tile's maxima; a row that one of them exceeds moves
+      if (ts.more) {
+        const int b = it & 1;
+        // (S^T of turn it - 2 was read before its P was written)
+        if (!(ok = (ts.j != 0 || wait(bar(B::QFULL + rq.slot), rq.phase)) && wait(bar(B::FULL + rk.slot), rk.phase))) break;
+        tc::fence_after();
+        const uint32_t q = q_d + rq.slot * (C::Q_BYTES >> 4), kk = k_d + rk.slot * (C::TURN >> 4);
+        const uint32_t s_t = tmem + b * SUB * C::SN;
+        // (without a second tile, at the end of a unit, old keys give scores that no one reads)
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) mma_s8<D, C::SN>(s_t + y * C::SN, kk + y * (C::TILE >> 4), q, lead);
+        commit(bar(B::SFULL + b), lead);
+        commit(bar(B::EMPTY + rk.slot), lead);
+        rk.next();
+        ts.next(p);
+        if (ts.j == 0) rq.next();
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax: one key, HR rows
+    const int x = warp >> 2, krow = (warp & 3) * 32 + lane, x0 = x * HR, vote = 2 + x;  // (vote: the group's barrier)
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_t = tmem + C::O_COL + x0 + lane_base;
+    load_q8<D, NR>(p, u, q_s, s_rs[0], s_nm[0][0], warp, SOFT, lane);
+    named_barrier(1, (SOFT + 1) * 32);
+    int left = u.left;
+    Ring<4> rsc;
+    Ring<2> rq;
+    bool ok = true;
+    uint32_t it = 0;  // turns of the run
+    for (int k = 0;; ++k) {
+      ok = ok && wait(bar(B::QFULL + rq.slot), rq.phase);
+      // (one answer for all that meet at the unit's end: they go through the same turns)
+      if (bar_or(vote, 128, !ok)) break;
+      const volatile Part8& u = s_part[k & 3];
+      const int n = u.n, full_lo = u.full_lo, full_hi = u.full_hi;
+      const int rows = u.rows - x0;  // of the group; without any it only keeps the barriers moving
+      const float* nm = s_nm[k & 3][0] + x0;
+      float l[HR];
+#pragma unroll
+      for (int e = 0; e < HR; ++e) l[e] = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < n; i += SUB, ++it) {
+        const int b = it & 1;
+        const uint32_t s_t = tmem + b * SUB * C::SN + x0 + lane_base;
+        if ((i & 3) == 0) ok = ok && wait(bar(B::SCFULL + rsc.slot), rsc.phase);
+        ok = ok && wait(bar(B::SFULL + b), (it >> 1) & 1);
+        tc::fence_after();
+        float4 sc[SUB];
+        // rows that see the thread's keys: from the first at its position on, to the last whose window reaches it
+        uint32_t see[SUB];
+        bool all = true;
+#pragma unroll
+        for (int y = 0; y < SUB; ++y) {
+          sc[y] = s_sc[rsc.slot][(i & 3) + y][krow >> 4];
+          see[y] = sc[y].w != 0.f ? (1u << HR) - 1u : 0u;  // (0 past the unit's tiles too)
+          if (i + y < full_lo || i + y >= full_hi) {
+            const int place = (u.a + i + y) * KT + krow, sink_end = u.sink_end;
+            const int key = place < sink_end ? place : place + u.shift, off = u.off;
+            const int64_t r0 = (int64_t)u.rt * NR + x0;
+            const bool in = place < u.total && key < u.kv_len && !(place < sink_end && key >= p.n_sink);
+            const int64_t from = (int64_t)(key - off) * p.R - r0;
+            const int64_t to = p.window > 0 && key >= p.n_sink ? ((int64_t)key + p.window - off) * p.R - r0 : HR;
+            if (in)
+              see[y] &= bits((int)min((int64_t)HR, max((int64_t)0, from)), (int)min((int64_t)HR, max((int64_t)0, to)));
+            else
+              see[y] = 0;
+          }
+          all = all && see[y] == (1u << HR) - 1u;
+        }
+        all = __all_sync(0xffffffffu, all);
+        // exponents t of the scores (raw), or t + nm: P' = exp2(t + nm)
+        float v[SUB][HR];
+        auto scores = [&](bool raw) {
+#pragma unroll
+          for (int y = 0; y < SUB; ++y) tmem_ld_nowait<HR>(s_t + y * C::SN, v[y]);
+          tmem_landed<SUB * HR>(&v[0][0]);
+          const float* rs = s_rs[rq.slot] + x0;
+#pragma unroll
+          for (int e = 0; e < HR; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(rs + e);
+            float2 m = make_float2(0.f, 0.f);
+            if (!raw) m = *reinterpret_cast<const float2*>(nm + e);
+#pragma unroll
+            for (int y = 0; y < SUB; ++y) {
+              const float2 t = unpair(fma2(pair(v[y][e], v[y][e + 1]), mul2(pair(f.x, f.y), pair(sc[y].x, sc[y].x)),
+                                           add2(pair(sc[y].y, sc[y].y), pair(m.x, m.y))));
+              v[y][e] = t.x;
+              v[y][e + 1] = t.y;
+            }
+          }
+          if (!all) {
+#pragma unroll
+            for (int y = 0; y < SUB; ++y)
+#pragma unroll
+              for (int e = 0; e < HR; ++e) v[y][e] = (see[y] >> e) & 1u ? v[y][e] : kNegInf;
+          }
+        };
+        bool move = i == 0;  // (a unit's first turn has its maxima found in any case)
+        if (!move) {
+          if (ok && rows > 0) {
+            scores(false);
+            float most = kNegInf;
+#pragma unroll
+            for (int y = 0; y < SUB; ++y)
+#pragma unroll
+              for (int e = 0; e < HR; e += 2) most = max3(most, v[y][e], v[y][e + 1]);
+            move = most > kMoves;
+          }
+          move = bar_or(vote, 128, move || !ok);
+        }
+        if (move) {
+          // the turn's maxima; a row that one of them exceeds moves
+          if (ok && rows > 0) {
+            scores(true);
+#pragma unroll
+            for (int e = 0; e < HR; ++e) {
+              float top = v[0][e];
+#pragma unroll
+              for (int y = 1; y < SUB; ++y) top = fmaxf(top, v[y][e]);
+              top = warp_max(top);
+              if (lane == 0) s_max[x][warp & 3][e] = top;
+            }
+          }
+          if (it > 0) ok = ok && wait(bar(B::PVDONE), (it - 1) & 1);  // O is complete
+          if (bar_or(vote, 128, !ok || *abort)) {  // (every warp of the group leaves here, or none)
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          // Every warp writes the new maxima (the same) where the next turn finds them; the old ones stay
+          // for the warps that are still here, and their place is taken at the next move, after its vote.
+          float* to = s_nm[k & 3][nm == s_nm[k & 3][0] + x0] + x0;
+          float al[HR];
+#pragma unroll
+          for (int e = 0; e < HR; ++e) {
+            const float was = nm[e];
+            const float top = fmaxf(fmaxf(s_max[x][0][e], s_max[x][1][e]), fmaxf(s_max[x][2][e], s_max[x][3][e]));
+            const float now = rows > 0 && top + was > kMoves ? kRoom - top : was;
+            al[e] = ex2(now - was);
+            l[e] *= al[e];
+#pragma unroll
+            for (int y = 0; y < SUB; ++y) v[y][e] += now;
+            if (lane == e) to[e] = now;
+          }
+          if (i > 0) {
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+              float ov[HR];
+              tmem_ld_nowait<HR>(o_t + z * NR, ov);
+              tmem_landed<HR>(ov);
+#pragma unroll
+              for (int e = 0; e < HR; ++e) ov[e] *= al[e];
+              tmem_st_nowait<HR>(o_t + z * NR, ov);
+            }
+            tmem_wait_st();
+          }
+          nm = to;
+          __syncwarp();
+        } else if (it > 0) {
+          ok = ok && wait(bar(B::PVDONE), (it - 1) & 1);  // P's room is free
+        }
+        if (!ok) continue;  // (to the next vote)
+        if (rows > 0) {
+          // three terms of P', to bytes (term NR + row) of the key's line
+#pragma unroll
+          for (int y = 0; y < SUB; ++y) {
+            uint32_t c[3][2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint16_t d[3][2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int e = q * 4 + z * 2;
+                const float w0 = ex2(v[y][e]), w1 = ex2(v[y][e + 1]);
+                const float2 ll = unpair(fma2(pair(w0, w1), pair(sc[y].z, sc[y].z), pair(l[e], l[e + 1])));
+                l[e] = ll.x;
+                l[e + 1] = ll.y;
+                const __half2 hh = __floats2half2_rn(w0, w1);
+                uint32_t h = *reinterpret_cast<const uint32_t*>(&hh);
+                d[0][z] = e5m2x2_of(h);
+                h = rest_of(h, d[0][z]);
+                d[1][z] = e5m2x2_of(h);
+                d[2][z] = e5m2x2_of(rest_of(h, d[1][z]));
+              }
+#pragma unroll
+              for (int z = 0; z < 3; ++z) c[z][q] = d[z][0] | (uint32_t)d[z][1] << 16;
+            }
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+              const int col = z * NR + x0;
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at8<C::PW>(p_s + y * C::P_TILE, krow, col >> 4) + (col & 15)),
+                           "r"(c[z][0]), "r"(c[z][1])
+                           : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        }
+        tc::fence_before();
+        __syncwarp();
+        const bool last = i + SUB >= n, release = last || (i & 3) + SUB == 4;
+        if (lane == 0) {
+          tc::mbar_arrive(bar(B::PFULL));
+          if (release) tc::mbar_arrive(bar(B::SCEMPTY + rsc.slot));
+          if (last) tc::mbar_arrive(bar(B::QEMPTY + rq.slot));
+        }
+        if (release) rsc.next();
+      }
+      // ---------------------------------------------------------------- the unit's rows, or its part of them
+      ok = ok && wait(bar(B::PVDONE), (it - 1) & 1);
+      tc::fence_after();
+      if (rows > 0) {
 #pragma unroll
         for (int e = 0; e < HR; ++e) {
-          float v = ok ? t[e] : kNegInf;
 #pragma unroll
-          for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-          if (lane == 0) s_max[x][warp & 3][e] = v;
+          for (int s = 16; s; s >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
+          if (lane == 0) s_sum[x][warp & 3][e] = l[e];
         }
-        if (it > 0) ok = ok && wait(bar(B::PVDONE + (b ^ 1)), ((it - 1) >> 1) & 1);  // O is complete
-        if (bar_or(1 + x, !ok || *abort)) {  // (every warp of the group leaves here, or none)
-          ok = false;
-          break;
-        }
-        tc::fence_after();
+      }
+      if (bar_or(vote, 128, !ok)) break;  // (also after a timeout: every warp of the group comes here)
+      if (rows > 0) {
+        const bool whole = n == u.all;
+        const int g = u.g;
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (u.a == 0);
+        if (p.streamed && u.a == 0 && tid == 0)
+          p.info[((int64_t)u.seq * p.hkv + g) * p.row_tiles + u.rt] = make_int2(blockIdx.x, u.ctas);
+        int64_t tok = (int64_t)u.rt * NR + x0;  // token and head of the row
+        int head = (int)(tok % p.R);
+        tok = u.start + tok / p.R;
 #pragma unroll
         for (int e0 = 0; e0 < HR; e0 += 8) {
-          float al[8];
+          float w[24];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            const float v = fmaxf(fmaxf(s_max[x][0][e], s_max[x][1][e]), fmaxf(s_max[x][2][e], s_max[x][3][e]));
-            const float now = v - m[e] > kMoves ? v - kRoom : m[e];
-            al[i] = ex2(m[e] - now);
-            l[e] *= al[i];
-            m[e] = now;
-          }
-          if (it > 0) {
+          for (int y = 0; y < 3; ++y) tmem_ld_nowait<8>(o_t + y * NR + e0, w + 8 * y);
+          tmem_landed<24>(w);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              float ov[8];
-              tmem_ld_nowait<8>(o_t + k * NR + e0, ov);
-              tmem_landed<8>(ov);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ov[i] *= al[i];
-              tmem_st_nowait<8>(o_t + k * NR + e0, ov);
+          for (int y = 0; y < 8; ++y) {
+            const int e = e0 + y;
+            const float o = w[y] + (w[8 + y] + w[16 + y]);
+            const float sum = (s_sum[x][0][e] + s_sum[x][1][e]) + (s_sum[x][2][e] + s_sum[x][3][e]), neg = nm[e];
+            if (e < rows) {
+              if (whole) {
+                const int64_t rr = tok * p.h + g * p.R + head;
+                if (krow < D) p.o[rr * D + krow] = __float2bfloat16(sum > 0.f ? o / sum : 0.f);
+                if (p.lse && krow == 0) p.lse[rr] = sum > 0.f ? (log2f(sum) - neg) * kLn2 : kNegInf;
+              } else {
+                if (krow < D && sum > 0.f) p.part_o[(slot * NR + x0 + e) * D + krow] = o;
+                if (krow == 0) p.part_ml[slot * NR + x0 + e] = make_float2(-neg, sum);
+              }
+            }
+            if (++head == p.R) {
+              head = 0;
+              ++tok;
             }
           }
         }
-        tmem_wait_st();
       }
-      if (it >= 2 && ok) ok = wait(bar(B::PVDONE + b), ((it - 2) >> 1) & 1);  // P's buffer is free
-      if (!ok) continue;  // (to the next vote)
-      const uint32_t p_b = p_s + b * C::P_BYTES;
-      // eight rows at a time: three terms of P' each, to bytes (term NR + row) of the key's line
-#pragma unroll
-      for (int e0 = 0; e0 < HR; e0 += 8) {
-        uint32_t c1[2], c2[2], c3[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint16_t d1[2], d2[2], d3[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int e = e0 + q * 4 + y * 2;
-            const float w0 = ex2(t[e] - m[e]), w1 = ex2(t[e + 1] - m[e + 1]);
-            l[e] = fmaf(w0, inv_sv, l[e]);
-            l[e + 1] = fmaf(w1, inv_sv, l[e + 1]);
-            const __half2 hh = __floats2half2_rn(w0, w1);
-            const uint32_t h = *reinterpret_cast<const uint32_t*>(&hh);
-            d1[y] = e4m3x2_of(h);
-            const uint32_t h2 = rest32(h, f16x2_of(d1[y]));
-            d2[y] = e4m3x2_of(h2);
-            d3[y] = e4m3x2_of(rest32(h2, f16x2_of(d2[y])));
-          }
-          c1[q] = d1[0] | (uint32_t)d1[1] << 16;
-          c2[q] = d2[0] | (uint32_t)d2[1] << 16;
-          c3[q] = d3[0] | (uint32_t)d3[1] << 16;
-        }
-        auto put = [&](int term, const uint32_t* c) {
-          const int col = term * NR + x * HR + e0;
-          const uint32_t at = at8<128>(p_b + (col >> 7) * (KT * 128), krow, (col & 127) >> 4) + (col & 15);
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at), "r"(c[0]), "r"(c[1]) : "memory");
-        };
-        put(0, c1);
-        put(1, c2);
-        put(2, c3);
-      }
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(bar(B::PFULL + b));
-        if ((it & 3) == 3) tc::mbar_arrive(bar(B::SCEMPTY + ((it >> 2) & 3)));
-      }
-    }
-    if (n > 1) ok = ok && wait(bar(B::PVDONE + (n & 1)), ((n - 2) >> 1) & 1);
-    if (n > 0) ok = ok && wait(bar(B::PVDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1);
-    tc::fence_after();
-#pragma unroll
-    for (int e = 0; e < HR; ++e) {
-#pragma unroll
-      for (int s = 16; s; s >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
-      if (lane == 0) s_sum[x][warp & 3][e] = l[e];
-    }
-    named_barrier(1 + x, 128);  // (also after a timeout: every warp of the group comes here)
-    if (ok) {
-#pragma unroll
-      for (int e = 0; e < HR; ++e)
-        l[e] = (s_sum[x][0][e] + s_sum[x][1][e]) + (s_sum[x][2][e] + s_sum[x][3][e]);
-      int64_t tok = un.row0 + x * HR;  // token and head of the row
-      int head = (int)(tok % R);
-      tok = un.start + tok / R;
-#pragma unroll
-      for (int e0 = 0; e0 < HR; e0 += 8) {
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-        if (n > 0) {
-          float u[24];
-#pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_ld_nowait<8>(o_t + k * NR + e0, u + 8 * k);
-          tmem_landed<24>(u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fmaf(fmaf(u[16 + i], 0.03125f, u[8 + i]), 0.03125f, u[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = e0 + i, r = x * HR + e;
-          if (r < rows) {
-            if (p.n_splits == 1) {
-              const int64_t rr = tok * p.h + g * R + head;
-              if (krow < D) p.o[rr * D + krow] = __float2bfloat16(l[e] > 0.f ? o[i] / l[e] : 0.f);
-              if (p.lse && krow == 0) p.lse[rr] = l[e] > 0.f ? (m[e] + log2f(l[e])) * kLn2 : kNegInf;
-            } else {
-              const int64_t at = (unit * p.n_splits + split) * NR + r;
-              if (krow < D && l[e] > 0.f) p.part_o[at * D + krow] = o[i];
-              if (krow == 0) p.part_ml[at] = make_float2(m[e], l[e]);
-            }
-          }
-          if (++head == R) {
-            head = 0;
-            ++tok;
-          }
-        }
-      }
+      left -= n;
+      if (left <= 0) break;
+      rq.next();
     }
   }
 
   __syncthreads();
-  if (*abort) {
-    // copies and products still in flight land before the CTA leaves
-    if (warp == kLoad) {
-      for (int st = 0; st < NS; ++st)
-        if (last_item >= st) {
-          const int i = last_item - (last_item - st) % NS;
-          tc::warp_drain(bar(B::FULL + st), (i / NS) & 1);
-        }
-    } else if (warp == kIssue) {
-      commit(bar(B::DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
-      __syncwarp();
-      tc::warp_drain(bar(B::DRAIN), 0);
-    }
-  } else if (warp == kLoad) {
-    // the last release of every slot lands before the CTA leaves
-    for (int st = 0; st < NS; ++st)
-      if (last_item >= st) {
-        const int i = last_item - (last_item - st) % NS;
-        tc::warp_drain(bar(B::EMPTY + st), (i / NS) & 1);
-      }
+  if (warp == kLoadK || warp == kLoadV) {
+    // After a timeout the copies still in flight land before the CTA leaves, else the last release of every slot.
+    const int which = *abort ? B::FULL : B::EMPTY, first = warp == kLoadV ? NK : 0, ns = warp == kLoadV ? NV : NK;
+    for (int st = 0; st < ns; ++st)
+      if (const int i = last_in_stage(last_item, st, ns); i >= 0) tc::warp_drain(bar(which + first + st), (i / ns) & 1);
+  } else if (warp == kIssue && *abort) {
+    // products still in flight, too
+    commit(bar(B::DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
+    __syncwarp();
+    tc::warp_drain(bar(B::DRAIN), 0);
   }
   tc::fence_before();
   __syncthreads();
   if (warp == kIssue) tmem_free(tmem, C::TMEM);
 }
 
-// Joins the parts of a row in order, a warp a row.
-template <int D, int NR>
-__global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p, int64_t rows) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int64_t unit = row / NR;
-  const Unit8 un(p, unit, NR);
-  const int r = (int)(row % NR);
-  const int64_t rho = un.row0 + r;
-  if (rho >= (int64_t)un.Lq * p.R) return;
-  const int64_t rr = (un.start + rho / p.R) * p.h + un.g * p.R + rho % p.R;
-  const int parts = p.n_splits;
-  const int64_t at = unit * parts * NR + r;  // of part 0
+// Joins the parts of a row in order: PW warps a row, each every PW-th part, then a sum over the warps.
+// (The parts are written while this kernel starts: no read-only loads of them.)
+template <int D, int NR, int PW>
+__global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p) {
+  constexpr int E = D / 32, PER = 8 / PW;  // rows a block
+  __shared__ float s_acc[8][D + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pw = warp % PW;
+  const int64_t unit = blockIdx.x / (NR / PER);
+  const int r = (int)(blockIdx.x % (NR / PER)) * PER + warp / PW;
+  const int rt = (int)(unit % p.row_tiles), g = (int)(unit / p.row_tiles % p.hkv), seq = (int)(unit / p.row_tiles / p.hkv);
+  Seq8<NR> s;
+  s.load(p, seq);
+  const bool mine = r < s.rows(p, rt);
+  const int64_t rho = (int64_t)rt * NR + r, rr = (s.start + rho / p.R) * p.h + g * p.R + rho % p.R;
+  wait_primary();
+  if (device_stopped()) return;
+  int2 who = make_int2(0, 0);
+  if (mine) who = p.info[unit];
+  who.x = max(0, min(who.x, p.ctas - 1));  // (whatever changed cu_seqlens meanwhile: within the workspace)
+  const int parts = min(who.y, p.ctas - who.x);
+  if (PW == 8 ? parts < 2 : __syncthreads_and(parts < 2)) return;  // (one part wrote the row itself)
+  // part i: the first CTA's last unit, the others' first
+  auto slot = [&](int i) { return ((int64_t)(who.x + i) * 2 + (i == 0)) * NR + r; };
   float m = kNone, acc[E] = {}, l = 0.f;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 ml = p.part_ml[at + (int64_t)i * NR];
-    if (ml.y > 0.f) m = fmaxf(m, ml.x);
-  }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w = 0.f, wl = 0.f;
-    if (i0 + lane < parts) {
-      const float2 ml = p.part_ml[at + (int64_t)(i0 + lane) * NR];
-      if (ml.y > 0.f) {
-        w = ex2(ml.x - m);
-        wl = w * ml.y;
-      }
+  if (parts > 1) {
+    for (int i = lane; i < parts; i += 32) {
+      const float2 ml = p.part_ml[slot(i)];
+      if (ml.y > 0.f) m = fmaxf(m, ml.x);
     }
-    const int e1 = min(32, parts - i0);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i0 = pw; i0 < parts; i0 += 32 * PW) {
+      float w = 0.f, wl = 0.f;
+      if (i0 + lane * PW < parts) {
+        const float2 ml = p.part_ml[slot(i0 + lane * PW)];
+        if (ml.y > 0.f) {
+          w = ex2(ml.x - m);
+          wl = w * ml.y;
+        }
+      }
+      const int e1 = min(32, (parts - i0 + PW - 1) / PW);
 #pragma unroll 4
-    for (int i = 0; i < e1; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, wl, i);
-      l += li;
-      if (wi > 0.f) {
-        const float* src = p.part_o + (at + (int64_t)(i0 + i) * NR) * D + lane * E;
+      for (int i = 0; i < e1; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        l += __shfl_sync(0xffffffffu, wl, i);
+        if (wi > 0.f) {
+          const float* src = p.part_o + slot(i0 + i * PW) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, src[e], acc[e]);
+          for (int e = 0; e < E; e += 2) {
+            const float2 y = *reinterpret_cast<const float2*>(src + e);
+            acc[e] = fmaf(wi, y.x, acc[e]);
+            acc[e + 1] = fmaf(wi, y.y, acc[e + 1]);
+          }
+        }
       }
     }
   }
+  if (PW > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_acc[warp][D] = l;
+    __syncthreads();
+    if (pw != 0) return;
+#pragma unroll
+    for (int w = 1; w < PW; ++w) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + w][lane * E + e];
+      l += s_acc[warp + w][D];
+    }
+  }
+  if (parts < 2) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -708,25 +1023,24 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p, int64
 
 // How a call is cut.
 struct Plan8 {
-  int nr, row_tiles, n_splits;
+  int nr, row_tiles, ctas;
+  bool streamed;
   int64_t units;
-  size_t ml, bytes;  // workspace: part_o at 0, part_ml at `ml`
+  size_t ml, info, bytes;  // workspace: part_o at 0, part_ml at `ml`, info at `info`
 };
-static Plan8 make_plan8(const Seqs& s, int h, int hkv, int D, int max_keys, int window, int n_sink) {
+static Plan8 make_plan8(const Seqs& s, int h, int hkv, int D) {
   Plan8 pl{};
-  const int R = h / hkv;
-  const int64_t rows = (int64_t)s.max_len * R;
-  pl.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t rows = (int64_t)s.max_len * (h / hkv);
+  pl.nr = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.row_tiles = (int)((rows + pl.nr - 1) / pl.nr);
   pl.units = (int64_t)pl.row_tiles * s.n_seqs * hkv;
-  int64_t keys = max_keys;
-  if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + pl.nr / R + 1 + up16(n_sink) + 2 * GRAN);
-  const int64_t tiles = std::max<int64_t>(1, (keys + KT - 1) / KT);
-  const int64_t want = 4 * (pl.nr == 64 ? 1 : 2) * kSms8 / pl.units;
-  pl.n_splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles, 256}));
-  const size_t part = pl.n_splits == 1 ? 0 : (size_t)pl.units * pl.n_splits * pl.nr;
-  pl.ml = (part * D * 4 + 255) & ~size_t(255);
-  pl.bytes = part ? pl.ml + part * 8 : 0;
+  pl.ctas = (pl.nr <= 16 ? 2 : 1) * kSms8;
+  pl.streamed = pl.units <= 4 * pl.ctas;
+  if (!pl.streamed) return pl;
+  const size_t part = (size_t)pl.ctas * 2 * pl.nr;
+  pl.ml = part * D * 4;
+  pl.info = pl.ml + part * 8;
+  pl.bytes = pl.info + (size_t)pl.units * 8;
   return pl;
 }
 
@@ -738,7 +1052,8 @@ static bool byte_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, con
     const uint64_t strides[2] = {(uint64_t)hkv * D, (uint64_t)c.page_stride};
     const uint32_t box[3] = {(uint32_t)D, i ? (uint32_t)GRAN : (page < KT ? page : (uint32_t)KT), 1};
     if (!tc::make_map(i ? small : big, ptr, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
       return false;
   }
   return true;
@@ -748,22 +1063,22 @@ template <int D, int NR>
 static cudaError_t run_q8(const CUtensorMap* m, const Q8Params& p, const Plan8& pl, cudaStream_t st) {
   using C = Cfg8<D, NR>;
   auto kern = attn_q8_kernel<D, NR>;
+  // (the limit belongs to the kernel, and other threads launch it too: the same for every call)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = pl.units * pl.n_splits;
+  const int64_t ctas = pl.streamed ? pl.ctas : pl.units;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   kern<<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(m[0], m[1], m[2], m[3], p);
-  if ((e = cudaGetLastError()) != cudaSuccess || pl.n_splits == 1) return e;
-  const int64_t rows = pl.units * NR;
-  q8_combine_kernel<D, NR><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, rows);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !pl.streamed) return e;
+  if (pl.units * 8 <= pl.ctas)
+    return launch_second(q8_combine_kernel<D, NR, 8>, dim3((unsigned)(pl.units * NR)), 256, 0, st, p);
+  return launch_second(q8_combine_kernel<D, NR, 1>, dim3((unsigned)(pl.units * NR / 8)), 256, 0, st, p);
 }
 
 template <int D>
-static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, int h, int hkv, int max_keys,
-                               int window, int n_sink, float scale, void* o, float* lse, void* workspace,
-                               cudaStream_t st) {
-  const Plan8 pl = make_plan8(s, h, hkv, D, max_keys, window, n_sink);
+static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, int h, int hkv, int window, int n_sink,
+                               float scale, void* o, float* lse, void* workspace, cudaStream_t st) {
+  const Plan8 pl = make_plan8(s, h, hkv, D);
   Q8Params p{};
   p.seqs = s;
   p.keys = keys;
@@ -772,27 +1087,30 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
   p.lse = lse;
   p.part_o = (float*)workspace;
   p.part_ml = (float2*)((uint8_t*)workspace + pl.ml);
+  p.info = (int2*)((uint8_t*)workspace + pl.info);
   p.h = h;
   p.hkv = hkv;
   p.R = h / hkv;
   p.window = window;
   p.n_sink = n_sink;
   p.row_tiles = pl.row_tiles;
-  p.n_splits = pl.n_splits;
+  p.streamed = pl.streamed;
+  p.ctas = pl.ctas;
+  p.min_tiles = 2;
   p.scale_log2 = scale * kLog2e;
   CUtensorMap m[4];
   if (!byte_maps(&m[0], &m[1], keys.k, keys.c, hkv, D) || !byte_maps(&m[2], &m[3], keys.v, keys.c, hkv, D))
     return cudaErrorInvalidValue;
-  return pl.nr == 16   ? run_q8<D, 16>(m, p, pl, st)
-         : pl.nr == 32 ? run_q8<D, 32>(m, p, pl, st)
-                       : run_q8<D, 64>(m, p, pl, st);
+  return pl.nr == 8    ? run_q8<D, 8>(m, p, pl, st)
+         : pl.nr == 16 ? run_q8<D, 16>(m, p, pl, st)
+                       : run_q8<D, 32>(m, p, pl, st);
 }
 
 }  // namespace span
 
 size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink) {
   if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
-  return span::make_plan8(s, h, hkv, d, max_keys, window, n_sink).bytes;
+  return span::make_plan8(s, h, hkv, d).bytes;
 }
 
 cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache, const void* k, const void* v,
@@ -807,8 +1125,8 @@ cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache,
   keys.vs = v_scales;
   keys.c = span::keys_of(&cache, nullptr, nullptr);
   keys.block_log2 = block_log2;
-  return d == 64 ? span::launch_q8_d<64>(s, q, keys, h, hkv, max_keys, window, n_sink, scale, o, lse, workspace, st)
-                 : span::launch_q8_d<128>(s, q, keys, h, hkv, max_keys, window, n_sink, scale, o, lse, workspace, st);
+  return d == 64 ? span::launch_q8_d<64>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st)
+                 : span::launch_q8_d<128>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st);
 }
 
 NSA_STATUS_ACCESSOR(span_q8)

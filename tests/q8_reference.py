@@ -3,11 +3,12 @@ error bounds of the kernels' roundings.
 
 U = 2^-24 is half a step of fp32, B = 2^-8 half a step of bf16, both relative; half a step of e4m3
 is 2^-4 relative and at least 2^-10 (codes).  The attention's bounds count, from the kernel's
-formulas: scores as fp32 sums of d products; q as two e4m3 terms (2^-22 of the row's
-largest); exponents of fp32 arguments, an argument made of a score, log2 of the value scale and
-the running maximum; a weight as f16 (2^-11) of which three e4m3 terms are taken (2^-12, and
-2^-26 of the row's largest weight times value scale; 2^-31 of it where f16 itself ends), fp32
-sums, and a bf16 output rounded once.
+formulas: scores as fp32 sums of d products; q as an e4m3 and an e5m2 term (half the least e5m2, 2^-17,
+where the row's largest is at least 2^7: 2^-24 of it); exponents of fp32 arguments, an argument
+made of a score, log2 of the value scale and the running maximum; a weight as f16 (2^-11) of which
+three e5m2 terms are taken (half a step of each is 2^-3 of what is left: 2^-9; and half the least
+e5m2, 2^-17, where the largest weight of a row is at least 2^9: 2^-26 of it; f16's own end is 2^-25
+there, 2^-34), fp32 sums, and a bf16 output rounded once.
 """
 import math
 
@@ -16,7 +17,7 @@ import torch
 from tests.span_reference import B, NEG, U
 
 E_MIN, E_MAX, TOP = -60, 60, 448.0
-P_REL, P_ABS = 2.0 ** -11 + 2.0 ** -12, 2.0 ** -26 + 2.0 ** -31
+P_REL, P_ABS = 2.0 ** -11 + 2.0 ** -9, 2.0 ** -26 + 2.0 ** -34
 
 
 def rotate(x, inv_freq, pos, interleaved):
@@ -85,7 +86,7 @@ def attend(q, kc, ks, vc, vs, see, scale):
         if not n:
             continue
         mag = ((q[:, h].abs() @ kk.abs().T) * scale).masked_fill(~see, 0.0).max(1).values
-        q_cut = (2.0 ** -22 * q[:, h].abs().max(1).values[:, None] * kk.abs().sum(1) * scale).masked_fill(~see, 0.0)
+        q_cut = (2.0 ** -24 * q[:, h].abs().max(1).values[:, None] * kk.abs().sum(1) * scale).masked_fill(~see, 0.0)
         logs = torch.log(sv).abs().max()
         es = (d + 16) * U * mag + q_cut.max(1).values + 8 * U * (mag + logs)
         rel = 2 * es + 2.0 ** -19 + n * U

@@ -172,7 +172,7 @@ def test_value_scales_far_apart(n):
 
 
 def test_queries_with_an_outlier_dimension():
-    """A dimension 1000 times the others: the rest of the row still counts to 2^-22 of it."""
+    """A dimension 1000 times the others: the rest of the row still counts to 2^-24 of it."""
     c = Cache8([300], 1, 128, 64, 64, 11)
     c.k_pages.view(torch.uint8)[..., 5] &= 0x80  # the keys have nothing there
     c.codes[0][0][..., 5] = 0.0
