@@ -625,10 +625,17 @@ NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new
 
 /* nsa_paged_attn_fwd over a cache held in 8 bits: the same arguments, masks, empty rows and
  * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
- * cache_lens has to be finite.  Scores see q as it is, down to 2^-24 of its row's largest element.
- * Weights enter the second product with a relative error below 2^-8.6 (as bf16 they would have 2^-8). */
-NSA_API size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window,
-                                                    int n_sink);
+ * cache_lens has to be finite.
+ * Calls of fewer than 320 rows (max_seqlen * h / h_kv) read the codes as they are: scores see q as it is, down to
+ * 2^-24 of its row's largest element, and weights enter the second product with a relative error
+ * below 2^-8.6 (as bf16 they would have 2^-8).  Calls of more rows, which the products bound,
+ * expand the seen keys and values to bf16 in the workspace first (exact where scales are powers of two, else
+ * rounded once), the caches of as many sequences at a time as 512 MB hold (at least of one), and
+ * are nsa_paged_attn_fwd from there on: values of these keys have to fit bf16.
+ *   max_cache_len  has to bound cache_lens there, for the workspace is sized by it (the queries of a cache longer
+ *                  than that, in pages, see no key: o = 0, lse = -inf); 0: max_pages * page_size */
+NSA_API size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, const nsa_paged_cache_q8* cache,
+                                                    int64_t max_cache_len, int window, int n_sink);
 NSA_API nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,
                                          int64_t max_cache_len, int window, int n_sink, float scale, void* o,
                                          float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);

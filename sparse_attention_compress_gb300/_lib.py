@@ -105,7 +105,7 @@ _SIGS = {
     "nsa_paged_append": ([_c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
     "nsa_paged_append_rope": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
     "nsa_paged_q8_append": ([_c_p, _c_p, _c_p, _c_p, _c_p, _c_p], _c_int),
-    "nsa_paged_q8_attn_fwd_workspace_size": ([_c_p, _c_i64, _c_int, _c_int], _c_sz),
+    "nsa_paged_q8_attn_fwd_workspace_size": ([_c_p, _c_p, _c_i64, _c_int, _c_int], _c_sz),
     "nsa_paged_q8_attn_fwd": ([_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
     "nsa_paged_attn_fwd_workspace_size": ([_c_p, _c_i64, _c_int, _c_int], _c_sz),
     "nsa_paged_attn_fwd": ([_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_f, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
@@ -992,10 +992,11 @@ def nsa_paged_q8_append(k_new, v_new, k_pages, v_pages, k_scales, v_scales, bloc
     return q_out
 
 
-def nsa_paged_q8_attn_fwd_workspace_size(shape: NsaShape, max_cache_len: int = 0, window: int = 0,
-                                         n_sink: int = 0) -> int:
+def nsa_paged_q8_attn_fwd_workspace_size(shape: NsaShape, cache: NsaPagedCacheQ8, max_cache_len: int = 0,
+                                         window: int = 0, n_sink: int = 0) -> int:
     _int32("nsa_paged_q8_attn_fwd_workspace_size", window=window, n_sink=n_sink)
-    return int(load().nsa_paged_q8_attn_fwd_workspace_size(ctypes.byref(shape), max_cache_len, window, n_sink))
+    return int(load().nsa_paged_q8_attn_fwd_workspace_size(ctypes.byref(shape), ctypes.byref(cache), max_cache_len,
+                                                           window, n_sink))
 
 
 def nsa_paged_q8_attn_fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_lens, window=0, n_sink=0,
@@ -1019,7 +1020,7 @@ def nsa_paged_q8_attn_fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     with ctx:
         if out is None:
             out = torch.empty_like(q) if share is None else _new(q.shape, _BF16, dev, share)
-        need = 0 if workspace is not None else lib.nsa_paged_q8_attn_fwd_workspace_size(sp, max_cache_len, window, n_sink)
+        need = 0 if workspace is not None else lib.nsa_paged_q8_attn_fwd_workspace_size(sp, ctypes.byref(c), max_cache_len, window, n_sink)
         ws, at, size = _scratch(fn, workspace, need, dev, dev.index)
         rc = lib.nsa_paged_q8_attn_fwd(sp, q.data_ptr(), ctypes.byref(c), max_cache_len, window, n_sink, scale,
                                        out.data_ptr(), _addr(lse), at, size, raw)

@@ -1275,10 +1275,16 @@ nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new, const 
                      "nsa_paged_q8_append");
 }
 
-size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, int64_t max_cache_len, int window, int n_sink) {
+size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, const nsa_paged_cache_q8* cache,
+                                            int64_t max_cache_len, int window, int n_sink) {
   Seqs s;
-  if (check_span_shape(shape, &s, __func__) != NSA_OK || check_span(window, n_sink, __func__) != NSA_OK) return 0;
-  return span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, span_keys(max_cache_len), window, n_sink);
+  PagedView c;
+  int block;
+  if (check_span_shape(shape, &s, __func__) != NSA_OK || check_span(window, n_sink, __func__) != NSA_OK ||
+      check_cache_q8(cache, shape->h_kv, shape->d, &c, &block, __func__) != NSA_OK)
+    return 0;
+  return span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, span_keys(max_cache_len), cache->page_size,
+                                 cache->max_pages, window, n_sink);
 }
 
 nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,
@@ -1298,7 +1304,8 @@ nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const ns
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(NSA_ERR_INVALID, "nsa_paged_q8_attn_fwd: lse misaligned");
   const int keys = span_keys(max_cache_len);
-  const size_t need = span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, keys, window, n_sink);
+  const size_t need = span_q8_workspace_bytes(s, shape->h, shape->h_kv, shape->d, keys, cache->page_size,
+                                              cache->max_pages, window, n_sink);
   if (nsa_status st = check_workspace(workspace, workspace_bytes, need, __func__)) return st;
   const size_t qb = (size_t)s.tokens * shape->h * shape->d * 2;
   NSA_REQUIRE(!overlap(o, qb, q, qb), NSA_ERR_INVALID, "nsa_paged_q8_attn_fwd: o overlaps q");

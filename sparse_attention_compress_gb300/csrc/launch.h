@@ -208,7 +208,8 @@ cudaError_t launch_paged_q8_append(const Seqs& s, const void* k_new, const void*
                                    const PagedView& cache, void* k_pages, void* v_pages, float* k_scales,
                                    float* v_scales, int block_log2, int h, int hkv, int d, cudaStream_t st);
 // Attention over a paged cache of e4m3 codes (page_stride in bytes) with scales (csrc/span_q8.cu).
-size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink);
+size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int page, int max_pages, int window,
+                               int n_sink);
 cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache, const void* k, const void* v,
                            const float* k_scales, const float* v_scales, int block_log2, int h, int hkv, int d,
                            int max_keys, int window, int n_sink, float scale, void* o, float* lse, void* workspace,

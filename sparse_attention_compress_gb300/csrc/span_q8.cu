@@ -1044,6 +1044,150 @@ static Plan8 make_plan8(const Seqs& s, int h, int hkv, int D) {
   return pl;
 }
 
+// ---------------------------------------------------------------------------- many rows
+// With many rows a sequence the products bound the call, and each key is met by many row tiles: the seen
+// part of the caches is expanded to bf16 pages of the workspace once (value = code * scale: exact
+// for scales that are powers of two, else rounded once), and span_attn.cu's kernels read those.
+struct Expand8 {
+  Keys8 keys;
+  Seqs seqs;
+  int hkv, window, n_sink, seq0;  // sequences seq0 .. of the call
+  int bound;                      // table entries that lengths within the caller's bound reach
+  int pages;                      // workspace pages of a sequence: those of the sinks, then those of the window
+  int sink_pages;
+  __nv_bfloat16 *k, *v;           // [sequences][pages][page][hkv][D]
+  int32_t* table;                 // [sequences][bound]
+  int32_t* lens;                  // [sequences]
+};
+// A block takes a page of a sequence (blockIdx.x: entry of the table) for all kv-heads.
+template <int D>
+__global__ void __launch_bounds__(256) expand_q8_kernel(const Expand8 x) {
+  const int seq = x.seq0 + blockIdx.y, pl = x.keys.c.page_log2, page = 1 << pl, e = blockIdx.x;
+  const int len = cached_len(x.keys.c, seq), Lq = seq_len(x.seqs, seq);
+  const int kv_len = len > (int64_t)x.bound << pl ? 0 : len;  // (longer than the caller said: no keys, to be seen by that)
+  // pages that some query sees: those of the sinks and from the first query's window on
+  const int first = x.window > 0 ? max(0, kv_len - Lq - x.window + 1) >> pl : 0;
+  const bool sink = e < x.sink_pages && e < first, seen = Lq > 0 && (e << pl) < kv_len && (sink || e >= first);
+  const int at = sink || first <= x.sink_pages ? e : e - first + x.sink_pages;  // its place in the workspace
+  const int pid = seen && at < x.pages ? page_of(x.keys.c, seq, e << pl) : -1;
+  if (threadIdx.x == 0) {
+    x.table[(int64_t)blockIdx.y * x.bound + e] = pid < 0 ? -1 : (int)blockIdx.y * x.pages + at;
+    if (e == 0) x.lens[blockIdx.y] = kv_len;
+  }
+  if (pid < 0) return;
+  constexpr int CH = D / 16;  // 16-byte chunks of a row
+  const int bl = x.keys.block_log2, rows = min(page, kv_len - (e << pl)) * x.hkv;
+  const int64_t to = ((int64_t)blockIdx.y * x.pages + at) * page * x.hkv * D, from = pid * x.keys.c.page_stride;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < 2 * rows * CH; i += 256) {
+    const bool is_v = i >= rows * CH;
+    const int j = is_v ? i - rows * CH : i, r = j / CH / x.hkv, g = j / CH % x.hkv;
+    const int64_t row = (int64_t)(j / CH) * D + j % CH * 16;
+    const uint4 c = *reinterpret_cast<const uint4*>((is_v ? x.keys.v : x.keys.k) + from + row);
+    const float s = __ldg((is_v ? x.keys.vs : x.keys.ks) + (((int64_t)pid * x.hkv + g) << (pl - bl)) + (r >> bl));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t h = f16x2_of_e4m3((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      o[k] = pack_bf16(f.x * s, f.y * s);
+    }
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? x.v : x.k) + to + row);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// How a call of many rows is cut: sequences by groups whose pages fit the room, one after another.
+constexpr int kManyRows = 320;                   // rows a (sequence, kv-head) from which the caches are expanded
+constexpr size_t kExpandRoom = (size_t)512 << 20;  // bytes of a group's pages, where more than a sequence's
+struct Groups8 {
+  int seqs, bound, pages, sink_pages;  // sequences of a group; table entries and workspace pages of each
+  size_t k, v, table, lens, attn, bytes;
+};
+static Groups8 make_groups8(const Seqs& s, int h, int hkv, int D, int max_keys, int page, int max_pages, int window,
+                            int n_sink) {
+  Groups8 gr{};
+  int64_t pages = std::min<int64_t>(max_pages, ((int64_t)max_keys + page - 1) / page);
+  gr.bound = (int)pages;
+  if (window > 0) {
+    gr.sink_pages = (int)std::min<int64_t>(pages, ((int64_t)n_sink + page - 1) / page);
+    pages = std::min<int64_t>(pages, gr.sink_pages + ((int64_t)window + s.max_len + page - 1) / page + 1);
+  }
+  gr.pages = (int)pages;
+  const size_t one = (size_t)pages * page * hkv * D * 2;
+  gr.seqs = (int)std::max<int64_t>(1, std::min<int64_t>(s.n_seqs, (int64_t)(kExpandRoom / (2 * one))));
+  auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
+  gr.v = up(one * gr.seqs);
+  gr.table = 2 * gr.v;
+  gr.lens = gr.table + up((size_t)gr.seqs * gr.bound * 4);
+  gr.attn = gr.lens + up((size_t)gr.seqs * 4);
+  Seqs part = s;
+  part.n_seqs = gr.seqs;
+  size_t need = span_attn_workspace_bytes(part, h, hkv, D, max_keys, window, n_sink);
+  part.n_seqs = s.n_seqs % gr.seqs;  // the last group
+  if (part.n_seqs) need = std::max(need, span_attn_workspace_bytes(part, h, hkv, D, max_keys, window, n_sink));
+  gr.bytes = gr.attn + need;
+  return gr;
+}
+static bool many_rows(const Seqs& s, int h, int hkv) { return (int64_t)s.max_len * (h / hkv) >= kManyRows; }
+
+static cudaError_t launch_expanded(const Seqs& s, const void* q, const Keys8& keys, int h, int hkv, int D, int max_keys,
+                                   int window, int n_sink, float scale, void* o, float* lse, void* workspace,
+                                   cudaStream_t st) {
+  const int page = 1 << keys.c.page_log2;
+  const Groups8 gr = make_groups8(s, h, hkv, D, max_keys, page, keys.c.max_pages, window, n_sink);
+  uint8_t* w = (uint8_t*)workspace;
+  Expand8 x{};
+  x.keys = keys;
+  x.seqs = s;
+  x.hkv = hkv;
+  x.window = window;
+  x.n_sink = n_sink;
+  x.bound = gr.bound;
+  x.pages = gr.pages;
+  x.sink_pages = gr.sink_pages;
+  x.k = (__nv_bfloat16*)w;
+  x.v = (__nv_bfloat16*)(w + gr.v);
+  x.table = (int32_t*)(w + gr.table);
+  x.lens = (int32_t*)(w + gr.lens);
+  for (int s0 = 0; s0 < s.n_seqs; s0 += gr.seqs) {
+    Seqs part = s;
+    part.n_seqs = std::min(gr.seqs, s.n_seqs - s0);
+    x.seq0 = s0;
+    const dim3 grid(gr.bound, part.n_seqs);
+    if (D == 64)
+      expand_q8_kernel<64><<<grid, 256, 0, st>>>(x);
+    else
+      expand_q8_kernel<128><<<grid, 256, 0, st>>>(x);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    PagedView c{};
+    c.table = x.table;
+    c.lens = x.lens;
+    c.n_pages = part.n_seqs * gr.pages;
+    c.page_log2 = keys.c.page_log2;
+    c.max_pages = gr.bound;
+    c.page_stride = (int64_t)page * hkv * D;
+    const char* qs = (const char*)q;
+    char* os = (char*)o;
+    float* ls = lse;
+    if (s.cu) {
+      part.cu = s.cu + s0;  // (rows are counted from the packed start)
+    } else {
+      const int64_t row = (int64_t)s0 * s.T * h;
+      qs += row * D * 2;
+      os += row * D * 2;
+      if (ls) ls += row;
+      part.tokens = (int64_t)part.n_seqs * s.T;
+    }
+    e = launch_span_attn(part, qs, &c, x.k, x.v, h, hkv, D, max_keys, window, n_sink, scale, os, ls, w + gr.attn, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 // Maps of the codes of K (or V): the tile box and the 16-row box.
 static bool byte_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, const Keys& c, int hkv, int D) {
   const uint32_t page = 1u << c.page_log2;
@@ -1108,8 +1252,11 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
 
 }  // namespace span
 
-size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int window, int n_sink) {
+size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int page, int max_pages, int window,
+                               int n_sink) {
   if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
+  if (span::many_rows(s, h, hkv))
+    return span::make_groups8(s, h, hkv, d, max_keys, page, max_pages, window, n_sink).bytes;
   return span::make_plan8(s, h, hkv, d).bytes;
 }
 
@@ -1125,6 +1272,8 @@ cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache,
   keys.vs = v_scales;
   keys.c = span::keys_of(&cache, nullptr, nullptr);
   keys.block_log2 = block_log2;
+  if (span::many_rows(s, h, hkv))
+    return span::launch_expanded(s, q, keys, h, hkv, d, max_keys, window, n_sink, scale, o, lse, workspace, st);
   return d == 64 ? span::launch_q8_d<64>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st)
                  : span::launch_q8_d<128>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st);
 }

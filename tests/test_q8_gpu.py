@@ -69,8 +69,12 @@ class Cache8:
     def args(self):
         return self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.dev_table, self.dev_lens
 
-    def reference(self, q, b, see, scale):
+    def reference(self, q, b, see, scale, many=False):
+        """`many`: a call of 320 rows or more, whose keys and values are rounded to bf16 and whose weights are bf16."""
         (kc, vc), (ks, vs) = self.codes[b], self.scales[b]
+        if many:
+            k, v = ((c * s[..., None]).to(BF).double() for c, s in ((kc, ks), (vc, vs)))
+            return ref.attend(q, k, v, see, scale)
         return ref8.attend(q, kc, ks, vc, vs, see, scale)
 
 
@@ -84,7 +88,8 @@ def _reference(c, q, cu, b, window, n_sink, scale, hide=()):
     see = ref.visible(range(c.lens[b] - (e - a), c.lens[b]), c.lens[b], window, n_sink)
     for lo, hi in hide:
         see[:, lo:hi] = False
-    return a, e, c.reference(q[a:e].double(), b, see, scale)
+    many = int((cu[1:] - cu[:-1]).max()) * q.shape[1] // c.hk >= 320
+    return a, e, c.reference(q[a:e].double(), b, see, scale, many)
 
 
 def _check(c, q, cu, o, lse, window, n_sink, scale, hide=()):
@@ -111,6 +116,9 @@ CASES = [
     ([333], [90], 128, 1, 128, 64, 32, 50, 16),                          # group 128: two row tiles a token
     ([2000, 1500], [1, 3], 16, 2, 128, 64, 64, 1000, 4),
     ([200, 650], [2, 2], 16, 1, 128, 32, 32, 0, 0),                      # 32 rows
+    ([700, 650], [39, 1], 8, 1, 128, 32, 32, 0, 0),                      # 312 rows: the most that read codes
+    ([700, 650], [40, 1], 8, 1, 128, 32, 32, 0, 0),                      # 320 rows: expanded
+    ([9, 33], [1, 1], 9, 1, 64, 32, 32, 0, 0),                           # 9 rows
     ([200, 650], [3, 1], 11, 1, 64, 64, 16, 90, 2),                      # 33 rows
 ]
 
@@ -133,11 +141,51 @@ def test_attention_is_the_same_on_every_run_and_for_every_division():
     for q_lens in ([1, 1], [3, 2], [40, 3]):
         q, cu = _queries(q_lens, 16, 128, 6)
         kw = dict(cu_seqlens=cu.cuda(), max_seqlen=max(q_lens))
-        for bound in (None, 5000, 128, 1 << 20):
+        for bound in (None, 5000, 1 << 20):
             lse = torch.empty(q.shape[0], 16, device="cuda")
             o = [nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, max_cache_len=bound, lse=lse, **kw) for _ in range(2)]
             assert torch.equal(*o)
             _check(c, q, cu, o[0], lse, 0, 0, 1.0 / math.sqrt(128))
+
+
+def test_a_bound_that_is_too_small():
+    """Codes read as they are need no bound; a call of many rows shows by -inf which caches exceeded it."""
+    c = Cache8([500, 120], 2, 64, 64, 64, 40)
+    q, cu = _queries([3, 1], 8, 64, 41)
+    lse = torch.empty(4, 8, device="cuda")
+    o = nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, max_cache_len=128, lse=lse, cu_seqlens=cu.cuda(), max_seqlen=3)
+    _check(c, q, cu, o, lse, 0, 0, 1 / 8)
+    q, cu = _queries([90, 70], 8, 64, 42)
+    lse = torch.empty(160, 8, device="cuda")
+    o = nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, max_cache_len=128, lse=lse, cu_seqlens=cu.cuda(), max_seqlen=90)
+    assert (o[:90] == 0).all() and (lse[:90] == -math.inf).all()
+    a, e, (ro, rl, eo, el) = _reference(c, q, cu, 1, 0, 0, 1 / 8)
+    ref.within(lse[a:e], rl, el, "lse")
+    ref.within(o[a:e], ro, eo, "o")
+
+
+def test_expanded_groups_of_sequences():
+    """More caches than the room for expanded pages holds at a time (dense and packed): 10 of 4096 tokens x 32 heads."""
+    hk, d, n = 32, 128, 10
+    c = Cache8([260] * n, hk, d, 128, 64, 43, spread=1)
+    table = torch.cat([c.table[:, :3], torch.full((n, 29), -1, dtype=I32)], 1)  # rows of 4096 positions
+    c.dev_table = table.cuda()
+    q, cu = _queries([320] * n, hk, d, 44)
+    keep = slice(250, 320)  # (positions from 190 on)
+    for dense in (False, True):
+        lse = torch.empty(n * 320, hk, device="cuda")
+        kw = {} if dense else dict(cu_seqlens=cu.cuda(), max_seqlen=320)
+        x = q.view(n, 320, hk, d) if dense else q
+        o = nsa.nsa_paged_q8_attn_fwd(x.cuda(), *c.args, lse=lse, **kw).view(n, 320, hk, d)
+        for b in (0, 3, n - 1):
+            see = ref.visible(range(190, 260), 260, 0, 0)
+            for h in (0, 31):
+                (kc, vc), (ks, vs) = c.codes[b], c.scales[b]
+                k, v = ((y[:, h:h + 1] * s[:, h:h + 1, None]).to(BF).double() for y, s in ((kc, ks), (vc, vs)))
+                qq = q[b * 320:(b + 1) * 320][keep, h:h + 1].double()
+                ro, rl, eo, el = ref.attend(qq, k, v, see, 1 / math.sqrt(d))
+                ref.within(o[b, keep, h:h + 1], ro, eo, f"o of {b}, {h}")
+                ref.within(lse.view(n, 320, hk)[b, keep, h:h + 1], rl, el, f"lse of {b}, {h}")
 
 
 @pytest.mark.parametrize("scale", [0.3, 4.0])
