@@ -135,9 +135,8 @@ constexpr int kTok = 4;  // tokens a block of 256 threads: 64 angles each
 __device__ __forceinline__ void rope_tokens(const Seqs& s, const Keys& c, const Rope& rp, int64_t tok0, int n_tok,
                                             const uint4* k_new, const uint4* v_new, __nv_bfloat16* k_pages,
                                             __nv_bfloat16* v_pages, float* weights, int h, int hkv, int d, bool q_only) {
-  __shared__ float2 s_cs[kTok * 64];
-  __shared__ int64_t s_row[kTok];  // row of the pool (page * page_stride / (hkv d) is no whole number: elements)
-  __shared__ int64_t s_cell[kTok];
+  __shared__ __align__(16) float2 s_cs[kTok * 64];
+  __shared__ int64_t s_row[kTok], s_cell[kTok];  // element of the pool and cell of the weights (-1: no place)
   __shared__ int s_pos[kTok], s_ok[kTok];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp < n_tok) {
@@ -167,31 +166,51 @@ __device__ __forceinline__ void rope_tokens(const Seqs& s, const Keys& c, const 
     s_cs[t * 64 + e] = turn(turn_step(__ldg(rp.inv_freq + e)), s_pos[t]);
   }
   __syncthreads();
-  const int per = d / 16, heads = q_only ? h : (rp.q ? h : 0) + 2 * hkv, nq = rp.q ? h : 0, items = heads * per;
-  for (int i = tid; i < n_tok * items; i += blockDim.x) {
-    const int t = i / items, r = i % items, head = r / per, j = r % per;
+  // A thread keeps its item j of a head and goes through the heads of the tokens, one after another (no divisions).
+  const int per_log2 = d == 128 ? 3 : 2, j = tid & ((1 << per_log2) - 1), step = blockDim.x >> per_log2;
+  const int nq = rp.q ? h : 0, heads = q_only ? nq : nq + 2 * hkv, cd = d / 8;
+  const bool turned = j < rp.rot / 16;
+  const int2 ch_k = item_chunks(rp, j), ch_v = make_int2(2 * j, 2 * j + 1);
+  for (int t = 0, head = tid >> per_log2;; head += step) {
+    while (head >= heads) {
+      head -= heads;
+      ++t;
+    }
+    if (t >= n_tok) break;
     if (!s_ok[t]) continue;
     const int64_t tok = tok0 + t;
-    const bool is_q = head < nq, is_v = head >= nq + hkv;
-    const int g = is_q ? head : is_v ? head - nq - hkv : head - nq;
-    if (!is_q && s_row[t] < 0) continue;
-    const uint4* src = is_q ? rp.q + (tok * h + g) * (d / 8) : (is_v ? v_new : k_new) + (tok * hkv + g) * (d / 8);
-    uint4* dst = is_q ? rp.q_out + (tok * h + g) * (d / 8)
-                      : reinterpret_cast<uint4*>((is_v ? v_pages : k_pages) + s_row[t] + (int64_t)g * d);
-    const int2 ch = is_v ? make_int2(2 * j, 2 * j + 1) : item_chunks(rp, j);
+    const uint4* src;
+    uint4* dst;
+    bool is_v = false;
+    if (head < nq) {
+      const int64_t row = (tok * h + head) * cd;
+      src = rp.q + row;
+      dst = rp.q_out + row;
+    } else {
+      if (s_row[t] < 0) continue;
+      int g = head - nq;
+      is_v = g >= hkv;
+      if (is_v) g -= hkv;
+      src = (is_v ? v_new : k_new) + (tok * hkv + g) * cd;
+      dst = reinterpret_cast<uint4*>((is_v ? v_pages : k_pages) + s_row[t]) + g * cd;
+      if (weights && !is_v && j == 0) weights[s_cell[t] + ((int64_t)g << c.page_log2)] = 0.f;
+    }
+    const int2 ch = is_v ? ch_v : ch_k;
     uint4 a = src[ch.x], b = src[ch.y];
-    if (!is_v && j < rp.rot / 16) {
+    if (turned && !is_v) {
       float x[16];
+      float4 cs[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cs[e] = *reinterpret_cast<const float4*>(s_cs + t * 64 + j * 8 + 2 * e);
       unpack8(a, x);
       unpack8(b, x + 8);
-      const float2* cs = s_cs + t * 64 + j * 8;
-      rotate_item(x, rp.interleaved != 0, [&](int e) { return cs[e]; });
+      rotate_item(x, rp.interleaved != 0,
+                  [&](int e) { return e & 1 ? make_float2(cs[e >> 1].z, cs[e >> 1].w) : make_float2(cs[e >> 1].x, cs[e >> 1].y); });
       a = pack8(x);
       b = pack8(x + 8);
     }
     dst[ch.x] = a;
     dst[ch.y] = b;
-    if (weights && !is_q && !is_v && j == 0) weights[s_cell[t] + ((int64_t)g << c.page_log2)] = 0.f;
   }
 }
 
@@ -203,8 +222,6 @@ __global__ void __launch_bounds__(256) append_rope_kernel(Seqs s, Keys c, Rope r
 }
 
 // ---------------------------------------------------------------------------- 8-bit cache
-constexpr int kItems = 4;  // items a thread holds in registers: 256 threads take a block of 128 x 128
-
 __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
@@ -222,27 +239,30 @@ __device__ __forceinline__ float scale_for(float top) {
   return __uint_as_float((uint32_t)(min(60, max(-60, e)) + 127) << 23);
 }
 
-// Blocks 0 .. q_blocks - 1 rotate queries, kTok tokens each.  Every other block takes one block of
-// B cache positions of a (sequence, kv-head), of K or of V: its new values to registers (K
-// rotated), their largest to the scale, the earlier codes rounded again where it grew, the
-// new ones written.
-__global__ void __launch_bounds__(256) append_q8_kernel(Seqs s, Keys c, Rope rp, int q_blocks, int n_tok, int block_log2,
+// Block b < kv_blocks takes one block of B cache positions of a (sequence, kv-head), of K or of V: its new
+// values to registers (K rotated), their largest to the scale, the earlier codes rounded again
+// where it grew, the new ones written.  The others, which take less time, rotate queries, kTok tokens each.
+// kItems: items a thread holds in registers (the blocks wait for memory, one load after another, so that the blocks
+// an SM holds are what counts: 4 x 2048 tokens 42 us with 4 items and two
+// blocks an SM, 29 with 2 and four, 26 with these blocks ahead of the queries).
+template <int kItems>
+__global__ void __launch_bounds__(256, kItems == 4 ? 2 : 4) append_q8_kernel(Seqs s, Keys c, Rope rp, int kv_blocks, int n_tok, int block_log2,
                                                         int blocks, const uint4* __restrict__ k_new,
                                                         const uint4* __restrict__ v_new, uint8_t* k_pages,
                                                         uint8_t* v_pages, float* k_scales, float* v_scales, int h,
                                                         int hkv, int d) {
-  if ((int)blockIdx.x < q_blocks) {
-    rope_tokens(s, c, rp, (int64_t)blockIdx.x * n_tok, n_tok, nullptr, nullptr, nullptr, nullptr, nullptr, h, hkv, d, true);
+  if ((int)blockIdx.x >= kv_blocks) {
+    rope_tokens(s, c, rp, (int64_t)((int)blockIdx.x - kv_blocks) * n_tok, n_tok, nullptr, nullptr, nullptr, nullptr, nullptr, h, hkv, d, true);
     return;
   }
   __shared__ uint32_t s_top[8];
   const int tid = threadIdx.x, threads = blockDim.x;
-  int64_t u = (int64_t)blockIdx.x - q_blocks;
+  int u = (int)blockIdx.x;
   const bool is_v = u & 1;
   u >>= 1;
-  const int g = (int)(u % hkv);
+  const int g = u % hkv;
   u /= hkv;
-  const int bi = (int)(u % blocks), seq = (int)(u / blocks);
+  const int bi = u % blocks, seq = u / blocks;
   const int B = 1 << block_log2, Lq = seq_len(s, seq);
   const int64_t cap = (int64_t)c.max_pages << c.page_log2, end = min((int64_t)c.lens[seq], cap);
   const int64_t first = (int64_t)c.lens[seq] - Lq;  // the first new position
@@ -372,14 +392,20 @@ cudaError_t launch_paged_q8_append(const Seqs& s, const void* k_new, const void*
   const int64_t q_blocks = rope && rope->q ? (s.tokens + n - 1) / n : 0;
   // a run of max_len positions touches at most this many blocks
   const int blocks = (s.max_len - 1 + B - 1) / B + 1;
-  const int64_t all = q_blocks + (int64_t)blocks * s.n_seqs * hkv * 2;
+  const int64_t kv_blocks = (int64_t)blocks * s.n_seqs * hkv * 2, all = q_blocks + kv_blocks;
   if (all > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  // (with queries to rotate, those blocks want all 256 threads; a few warps are enough for few tokens)
-  const int items = std::min(B, s.max_len) * (d / 16);
-  const int threads = q_blocks ? 256 : std::min(256, (items + 31) & ~31);
-  span::append_q8_kernel<<<(unsigned)all, threads, 0, st>>>(
-      s, span::keys_of(&cache, nullptr, nullptr), span::rope_of(rope), (int)q_blocks, n, block_log2, blocks,
-      (const uint4*)k_new, (const uint4*)v_new, (uint8_t*)k_pages, (uint8_t*)v_pages, k_scales, v_scales, h, hkv, d);
+  const int items = std::min(B, s.max_len) * (d / 16), threads = items <= 128 ? 128 : 256;
+  auto go = [&](auto kern) {
+    kern<<<(unsigned)all, threads, 0, st>>>(s, span::keys_of(&cache, nullptr, nullptr), span::rope_of(rope), (int)kv_blocks, n,
+                                            block_log2, blocks, (const uint4*)k_new, (const uint4*)v_new,
+                                            (uint8_t*)k_pages, (uint8_t*)v_pages, k_scales, v_scales, h, hkv, d);
+  };
+  if (items <= threads)
+    go(span::append_q8_kernel<1>);
+  else if (items <= 2 * threads)
+    go(span::append_q8_kernel<2>);
+  else
+    go(span::append_q8_kernel<4>);
   return cudaGetLastError();
 }
 

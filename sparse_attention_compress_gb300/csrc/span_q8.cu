@@ -1100,7 +1100,10 @@ __global__ void __launch_bounds__(256) expand_q8_kernel(const Expand8 x) {
 }
 
 // How a call of many rows is cut: sequences by groups whose pages fit the room, one after another.
-constexpr int kManyRows = 320;                   // rows a (sequence, kv-head) from which the caches are expanded
+// Rows a (sequence, kv-head) from which the caches are expanded.  Read as they are and expanded, us: 128 rows, d = 128,
+// 16 caches of 8192 144 and 135, 8 of 16384 118 and 137, 16 of 2048 76 and 62; 160 rows 151 and 146 (8 of 16384);
+// 96 rows, d = 64, 8 of 16384 94 and 100, 16 of 2048 62 and 46.
+constexpr int many_rows_from(int D) { return D == 64 ? 96 : 128; }
 constexpr size_t kExpandRoom = (size_t)512 << 20;  // bytes of a group's pages, where more than a sequence's
 struct Groups8 {
   int seqs, bound, pages, sink_pages;  // sequences of a group; table entries and workspace pages of each
@@ -1131,7 +1134,7 @@ static Groups8 make_groups8(const Seqs& s, int h, int hkv, int D, int max_keys, 
   gr.bytes = gr.attn + need;
   return gr;
 }
-static bool many_rows(const Seqs& s, int h, int hkv) { return (int64_t)s.max_len * (h / hkv) >= kManyRows; }
+static bool many_rows(const Seqs& s, int h, int hkv, int D) { return (int64_t)s.max_len * (h / hkv) >= many_rows_from(D); }
 
 static cudaError_t launch_expanded(const Seqs& s, const void* q, const Keys8& keys, int h, int hkv, int D, int max_keys,
                                    int window, int n_sink, float scale, void* o, float* lse, void* workspace,
@@ -1255,7 +1258,7 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
 size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int page, int max_pages, int window,
                                int n_sink) {
   if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
-  if (span::many_rows(s, h, hkv))
+  if (span::many_rows(s, h, hkv, d))
     return span::make_groups8(s, h, hkv, d, max_keys, page, max_pages, window, n_sink).bytes;
   return span::make_plan8(s, h, hkv, d).bytes;
 }
@@ -1272,7 +1275,7 @@ cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache,
   keys.vs = v_scales;
   keys.c = span::keys_of(&cache, nullptr, nullptr);
   keys.block_log2 = block_log2;
-  if (span::many_rows(s, h, hkv))
+  if (span::many_rows(s, h, hkv, d))
     return span::launch_expanded(s, q, keys, h, hkv, d, max_keys, window, n_sink, scale, o, lse, workspace, st);
   return d == 64 ? span::launch_q8_d<64>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st)
                  : span::launch_q8_d<128>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st);
