@@ -939,11 +939,13 @@ def _paged_cache_q8(fn, k_pages, v_pages, k_scales, v_scales, block_table, cache
     stride = _page_stride(fn, "k_pages", k_pages, _E4M3)
     shape = k_pages.shape
     n_pages, page, h_kv, _ = shape
-    if _page_stride(fn, "v_pages", v_pages, _E4M3) != stride or v_pages.shape != shape:
-        raise ValueError(f"{fn}: v_pages must have the shape and strides of k_pages")
-    if v_pages.device != k_pages.device:
-        raise ValueError(f"{fn}: v_pages is on {v_pages.device}, k_pages on {k_pages.device}")
     index = k_pages.get_device()
+    if not (isinstance(v_pages, torch.Tensor) and v_pages.dtype is _E4M3 and v_pages.shape == shape
+            and v_pages.stride() == k_pages.stride() and v_pages.get_device() == index):
+        if _page_stride(fn, "v_pages", v_pages, _E4M3) != stride or v_pages.shape != shape:
+            raise ValueError(f"{fn}: v_pages must have the shape and strides of k_pages")
+        if v_pages.device != k_pages.device:
+            raise ValueError(f"{fn}: v_pages is on {v_pages.device}, k_pages on {k_pages.device}")
     blocks = k_scales.shape[2] if isinstance(k_scales, torch.Tensor) and k_scales.dim() == 3 else 0
     if blocks < 1 or page % blocks:
         raise ValueError(f"{fn}: k_scales must be [n_pages, h_kv, page_size / block_size]")

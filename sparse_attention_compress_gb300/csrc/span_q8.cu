@@ -12,7 +12,7 @@
 //   Q  = 2^-a (q1 + q2)     a per row, so that max |Q 2^a| is in [128, 256); q1 in e4m3, the rest q2 in e5m2
 //   P' = p1 + p2 + p3       of P' = exp(t - m) sv 2^9 rounded to f16; all in e5m2
 // q1 leaves at most 8 units of bf16's last place, which the 3 significant bits of e5m2 hold, so Q is
-// exact down to 2^-17 of its row's largest element, and to 2^-25 of that below.  p1 + p2 + p3 is within
+// exact down to 2^-16 of its row's largest element, and to 2^-24 of that below.  p1 + p2 + p3 is within
 // 2^-9 of P' (and P' within 2^-11 of its value, half a step of f16; a bf16 P has 2^-8), down
 // to 2^-26 of the row's largest weight.  q1 and q2 share an accumulator (K is read twice); p1, p2 and p3
 // lie side by side in N with accumulator columns of their own, so that V is read once.
