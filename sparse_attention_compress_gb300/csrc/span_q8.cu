@@ -81,7 +81,7 @@ struct Q8Params {
   int h, hkv, R, window, n_sink, row_tiles;
   int ctas;         // of a streamed call
   int streamed;     // the tiles of all units in equal runs; else a CTA a unit
-  int min_tiles;    // of a run
+  int min_places;   // of a run
   float scale_log2;
 };
 
@@ -111,22 +111,36 @@ struct Seq8 {
 };
 
 // The units of a CTA's run of tiles, one after another.  Every role walks the run for itself.
+// A run is cut in places: a unit has kSwitch places that stand for the time that it takes to begin one (the
+// joining of the row sums, O's way out, the first maxima), then one for each tile.
+// 32 x 16384 .. 32768 keys, 8 rows: 0 places 85 us, 4 80.4, 8 79.5, 12 79.6, 24 80.6; 8 x 8192 keys x 8 kv-heads 46.2,
+// 40.4, 37.1, 37.4, 38.9; 32 rows over 16 x 16384 keys x 4 kv-heads 88, 86, 84, 82, 76.
 template <int NR>
 struct Walk {
+  static constexpr int kSwitch = NR == 32 ? 24 : 12;
   Seq8<NR> s;
   int seq, g, rt;
-  int a, n, all;  // tiles a .. a + n - 1 of the unit's `all`
-  int left;       // of the run, these included
-  __device__ __forceinline__ Walk(const Q8Params& p, int seq0, int64_t at, int run) : seq(seq0), g(0), rt(0), left(run) {
+  int a, n, all;  // tiles a .. a + n - 1 of the unit's `all`; n = 0: the run has no tile (left)
+  int left;       // places of the run from the unit's first on
+  int at, took;   // where in the unit's places it starts, and how many of them it takes
+  Walk() = default;
+  __device__ __forceinline__ void enter(const Q8Params& p, int place) {
+    at = place;
+    all = s.count(p, rt);
+    took = min(all + kSwitch - at, left);
+    a = max(0, at - kSwitch);
+    n = max(0, at + took - kSwitch) - a;
+  }
+  __device__ __forceinline__ Walk(const Q8Params& p, int seq0, int64_t place, int run) : seq(seq0), g(0), rt(0), left(run) {
     s.load(p, seq);
     int64_t per = 0;
-    for (int i = 0; i < p.row_tiles; ++i) per += s.count(p, i);
-    g = (int)(at / per);
-    at -= g * per;
-    for (int c; at >= (c = s.count(p, rt)); ++rt) at -= c;
-    a = (int)at;
-    all = s.count(p, rt);
-    n = min(all - a, left);
+    for (int i = 0; i < p.row_tiles; ++i)
+      if (const int c = s.count(p, i)) per += c + kSwitch;
+    g = (int)(place / per);
+    place -= g * per;
+    for (int c; place >= (c = s.count(p, rt) + kSwitch); ++rt) place -= c;
+    enter(p, (int)place);
+    if (n == 0) next(p);
   }
   // one whole unit
   __device__ __forceinline__ Walk(const Q8Params& p, int64_t unit) {
@@ -136,14 +150,14 @@ struct Walk {
     seq = (int)(unit / p.hkv);
     s.load(p, seq);
     a = 0;
-    left = n = all = s.count(p, rt);
+    n = all = s.count(p, rt);
+    left = at = took = 0;
   }
   __device__ __forceinline__ bool next(const Q8Params& p) {
-    left -= n;
-    if (left <= 0) return false;
-    a = 0;
-    all = s.count(p, ++rt);
-    if (all == 0) {
+    n = 0;
+    left -= took;
+    if (left <= kSwitch) return false;  // (no tile of the next unit)
+    if (s.count(p, ++rt) == 0) {
       rt = 0;
       if (++g == p.hkv) {
         g = 0;
@@ -152,9 +166,8 @@ struct Walk {
           s.load(p, seq);
         } while (s.count(p, 0) == 0);
       }
-      all = s.count(p, 0);
     }
-    n = min(all, left);
+    enter(p, 0);
     return true;
   }
 };
@@ -178,6 +191,7 @@ struct Turns {
 struct Part8 {
   int64_t start;
   int seq, g, rt, a, n, all, rows, off, kv_len, ctas;  // ctas: how many the unit's tiles go to
+  int more;  // whether the run goes on
   int sink_end, shift, total, full_lo, full_hi;  // tiles full_lo .. full_hi - 1: every row sees every key that has a page
 };
 template <int NR>
@@ -194,8 +208,9 @@ __device__ __forceinline__ void describe(const Q8Params& p, const Walk<NR>& u, i
   s->sink_end = tl.sink_end, s->shift = tl.shift, s->total = tl.total;
   s->full_hi = max(0, p0 + 1 - tl.shift) / KT - u.a;  // the last key is at most the first position
   s->full_lo = p.window > 0 ? max(0, (max(tl.sink_end, p1 - p.window + 1 - tl.shift) + KT - 1) / KT) - u.a : 0;
-  // the CTA that has tile e - 1 of all: floor((e ctas - 1) / total)
-  s->ctas = p.streamed ? (int)(((t + u.all) * ctas - 1) / total) - (int)blockIdx.x + 1 : 1;
+  // (of a unit that begins here, at place t) the CTA that has place e - 1 of all: floor((e ctas - 1) / total)
+  s->ctas = p.streamed ? (int)(((t + u.kSwitch + u.all) * ctas - 1) / total) - (int)blockIdx.x + 1 : 1;
+  s->more = u.left - u.took > u.kSwitch;
 }
 
 // Index of the last of items 0 .. last that went to slot st of ns (-1 if none).
@@ -483,19 +498,20 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
   const Waits wait(abort);
   // ------------------------------------------------------------------ this CTA's run of tiles
   int run = 0, ctas = 0;
-  int64_t t0 = 0, total = 0;  // the run: tiles t0 .. t0 + run - 1 of `total`
+  int64_t t0 = 0, total = 0;  // the run: places t0 .. t0 + run - 1 of `total`
   if (p.streamed) {
     const int per = (p.seqs.n_seqs + C::THREADS - 1) / C::THREADS, i0 = min(p.seqs.n_seqs, tid * per),
               i1 = min(p.seqs.n_seqs, i0 + per);
-    auto tiles_of = [&](int i) {
+    auto places_of = [&](int i) {
       Seq8<NR> s;
       s.load(p, i);
       int64_t c = 0;
-      for (int rt = 0; rt < p.row_tiles; ++rt) c += s.count(p, rt);
+      for (int rt = 0; rt < p.row_tiles; ++rt)
+        if (const int n = s.count(p, rt)) c += n + Walk<NR>::kSwitch;
       return c * p.hkv;
     };
     int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += tiles_of(i);
+    for (int i = i0; i < i1; ++i) mine += places_of(i);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -509,14 +525,14 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
-    ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / p.min_tiles));
+    ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / p.min_places));
     if (total == 0 || blockIdx.x >= ctas) return;
     t0 = total * blockIdx.x / ctas;
     run = (int)(total * (blockIdx.x + 1) / ctas - t0);
     before += incl - mine;
     if (before <= t0 && t0 < before + mine) {
       int i = i0;
-      for (int64_t c; before + (c = tiles_of(i)) <= t0; ++i) before += c;
+      for (int64_t c; before + (c = places_of(i)) <= t0; ++i) before += c;
       s_seq = i;
       s_at = t0 - before;
     }
@@ -556,7 +572,9 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
   auto width = [&](const Tiles& tl, int i) { return max(0, min(KT, (tl.width(i) + 31) & ~31)); };
 
   int last_item = -1;  // loading warps: the last turn handed to their ring
-  if (warp == kLoadK || warp == kLoadV) {
+  if (u.n == 0) {
+    // (a run that lies between two units)
+  } else if (warp == kLoadK || warp == kLoadV) {
     // ------------------------------------------------------------------ K tiles, or V tiles
     // (one code for both: instructions of warps that run rarely come from far)
     const bool is_v = warp == kLoadV;
@@ -596,10 +614,9 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
     Ring<2> rq;
     Ring<4> rs;
     bool ok = true, again = false;
-    int64_t t = t0;
     for (int k = 0; ok; ++k) {
       if (k > 1 && !(ok = wait(bar(B::QEMPTY + rq.slot), rq.phase ^ 1u))) break;
-      if (lane == 0) describe<NR>(p, u, t, total, ctas, &s_part[k & 3]);
+      if (lane == 0) describe<NR>(p, u, t0 + run - u.left - u.at, total, ctas, &s_part[k & 3]);
       if (k > 0)
         load_q8<D, NR>(p, u, q_s + rq.slot * C::Q_BYTES, s_rs[rq.slot], s_nm[k & 3][0], 0, 1, lane);
       else
@@ -628,7 +645,6 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
         rs.next();
         again |= rs.slot == 0;
       }
-      t += u.n;
       if (!u.next(p)) break;
     }
   } else if (warp == kIssue) {
@@ -688,7 +704,6 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
     const uint32_t o_t = tmem + C::O_COL + x0 + lane_base;
     load_q8<D, NR>(p, u, q_s, s_rs[0], s_nm[0][0], warp, SOFT, lane);
     named_barrier(1, (SOFT + 1) * 32);
-    int left = u.left;
     Ring<4> rsc;
     Ring<2> rq;
     bool ok = true;
@@ -920,8 +935,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
           }
         }
       }
-      left -= n;
-      if (left <= 0) break;
+      if (!u.more) break;
       rq.next();
     }
   }
@@ -1100,10 +1114,10 @@ __global__ void __launch_bounds__(256) expand_q8_kernel(const Expand8 x) {
 }
 
 // How a call of many rows is cut: sequences by groups whose pages fit the room, one after another.
-// Rows a (sequence, kv-head) from which the caches are expanded.  Read as they are and expanded, us: 128 rows, d = 128,
-// 16 caches of 8192 144 and 135, 8 of 16384 118 and 137, 16 of 2048 76 and 62; 160 rows 151 and 146 (8 of 16384);
-// 96 rows, d = 64, 8 of 16384 94 and 100, 16 of 2048 62 and 46.
-constexpr int many_rows_from(int D) { return D == 64 ? 96 : 128; }
+// Rows a (sequence, kv-head) from which the caches are expanded.  Read as they are and expanded, us: d = 128, 128 rows, 8
+// caches of 16384 keys 119 and 139, 16 of 2048 62 and 62; 160 rows, 134 and 148, 74 and 64; d = 64, 128
+// rows, 102 and 102, 59 and 46; 160 rows, 120 and 112, 69 and 49.
+constexpr int many_rows_from(int D) { return D == 64 ? 128 : 160; }
 constexpr size_t kExpandRoom = (size_t)512 << 20;  // bytes of a group's pages, where more than a sequence's
 struct Groups8 {
   int seqs, bound, pages, sink_pages;  // sequences of a group; table entries and workspace pages of each
@@ -1243,7 +1257,7 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
   p.row_tiles = pl.row_tiles;
   p.streamed = pl.streamed;
   p.ctas = pl.ctas;
-  p.min_tiles = 2;
+  p.min_places = 2;
   p.scale_log2 = scale * kLog2e;
   CUtensorMap m[4];
   if (!byte_maps(&m[0], &m[1], keys.k, keys.c, hkv, D) || !byte_maps(&m[2], &m[3], keys.v, keys.c, hkv, D))

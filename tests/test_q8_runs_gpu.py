@@ -24,7 +24,7 @@ def _random_case(seed):
     page = r.choice([16, 32, 64, 128, 256])
     block = r.choice([b for b in (16, 32, 64, 128) if b <= page])
     group, n = r.choice([1, 2, 3, 5, 8, 13, 16, 40]), r.choice([1, 2, 3, 5])
-    top = max(1, (127 if d == 128 else 95) // group) if r.random() < 0.8 else 200 // group + 1
+    top = max(1, (159 if d == 128 else 127) // group) if r.random() < 0.8 else 200 // group + 1
     q_lens = [r.randint(0, min(top, 40)) for _ in range(n)]
     q_lens[r.randrange(n)] = min(top, 40)
     lens = [max(0, r.choice([q, q + r.randint(0, 900), r.randint(0, 300), 128 * r.randint(1, 5)])) for q in q_lens]
