@@ -13,7 +13,10 @@
 // costs no precision but at the ends of its range, and a scale that grows moves the earlier codes
 // by whole binades: they are rounded again only where they reach e4m3's subnormals.
 //
-// Both are bound by HBM for chunks and by one launch for single tokens.
+// Single tokens cost one launch (3.1 us for 32 tokens into the bf16 cache, 4.1 into 8 bits).  Four sequences
+// of up to 2048 new tokens (16 query heads, 4 kv-heads of 128) take 18.3 us into the bf16 cache (81 MB read and
+// written: 4.4 TB/s; what is left is the first and the last blocks' latency) and 24.2 us into 8 bits (74 MB;
+// loads, angles, conversions and a block-wide maximum behind one another).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -240,17 +243,17 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 
 // Block b < kv_blocks takes one block of B cache positions of a (sequence, kv-head), of K or of V: its new
-// values to registers (K rotated), their largest to the scale, the earlier codes rounded again
-// where it grew, the new ones written.  The others, which take less time, rotate queries, kTok tokens each.
-// kItems: items a thread holds in registers (the blocks wait for memory, one load after another, so that the blocks
-// an SM holds are what counts: 4 x 2048 tokens 42 us with 4 items and two
-// blocks an SM, 29 with 2 and four, 26 with these blocks ahead of the queries).
+// values to registers (K rotated), their largest to the scale, the earlier codes rounded again where it
+// grew, the new ones written.  The others, which take less time, rotate queries, kTok tokens each.
+// kItems: items a thread holds in registers.  Blocks wait for memory, one load after another, so that the
+// blocks an SM holds are what counts: 4 x 2048 tokens (h 16, h_kv 4, d 128) 42 us with
+// 4 items and two blocks an SM, 29 with 2 and four, 26.5 with these blocks ahead of the queries, 25.2 with
+// the values requested before the page is known, 24.2 with five (a few spilled registers; six: 25.2).
 template <int kItems>
-__global__ void __launch_bounds__(256, kItems == 4 ? 2 : 4) append_q8_kernel(Seqs s, Keys c, Rope rp, int kv_blocks, int n_tok, int block_log2,
-                                                        int blocks, const uint4* __restrict__ k_new,
-                                                        const uint4* __restrict__ v_new, uint8_t* k_pages,
-                                                        uint8_t* v_pages, float* k_scales, float* v_scales, int h,
-                                                        int hkv, int d) {
+__global__ void __launch_bounds__(256, kItems == 4 ? 2 : 5)
+    append_q8_kernel(Seqs s, Keys c, Rope rp, int kv_blocks, int n_tok, int block_log2, int blocks,
+                     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, uint8_t* k_pages,
+                     uint8_t* v_pages, float* k_scales, float* v_scales, int h, int hkv, int d) {
   if ((int)blockIdx.x >= kv_blocks) {
     rope_tokens(s, c, rp, (int64_t)((int)blockIdx.x - kv_blocks) * n_tok, n_tok, nullptr, nullptr, nullptr, nullptr, nullptr, h, hkv, d, true);
     return;
@@ -268,42 +271,50 @@ __global__ void __launch_bounds__(256, kItems == 4 ? 2 : 4) append_q8_kernel(Seq
   const int64_t first = (int64_t)c.lens[seq] - Lq;  // the first new position
   const int64_t start = ((max(first, (int64_t)0) >> block_log2) + bi) << block_log2;
   if (start >= end) return;
+  const int r0 = (int)(max(first, start) - start), r1 = (int)(min(start + B, end) - start);  // new rows of the block
+  const int64_t tok0 = seq_start(s, seq) + start - first;  // row of the block's position 0
+  const uint4* src = is_v ? v_new : k_new;
+  const int per_log2 = d == 128 ? 3 : 2, j = tid & ((1 << per_log2) - 1);
+  const int2 ch = is_v ? make_int2(2 * j, 2 * j + 1) : item_chunks(rp, j);
+  const bool rotated = !is_v && j < rp.rot / 16;
+  // (the values are requested before the page is looked up, and the angles' steps found while they arrive)
+  uint4 in[kItems][2];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int r = r0 + ((tid + k * threads) >> per_log2);
+    in[k][0] = in[k][1] = make_uint4(0, 0, 0, 0);
+    if (r < r1) {
+      const uint4* row = src + ((tok0 + r) * hkv + g) * (d / 8);
+      in[k][0] = row[ch.x];
+      in[k][1] = row[ch.y];
+    }
+  }
   const int pid = page_of(c, seq, (int)start);
   if (pid < 0) return;
-  const int r0 = (int)(max(first, start) - start), r1 = (int)(min(start + B, end) - start);  // new rows of the block
   const int slot = (int)start & ((1 << c.page_log2) - 1);
   uint8_t* pages = (is_v ? v_pages : k_pages) + pid * c.page_stride + ((int64_t)slot * hkv + g) * d;
   float* scale = (is_v ? v_scales : k_scales) + (((int64_t)pid * hkv + g) << (c.page_log2 - block_log2)) + (slot >> block_log2);
-  const int64_t tok0 = seq_start(s, seq) + start - first;  // row of the block's position 0
-  const uint4* src = is_v ? v_new : k_new;
-  const int per = d / 16, j = tid % per;  // (threads is a multiple of 32: a thread keeps its j)
-  const int2 ch = is_v ? make_int2(2 * j, 2 * j + 1) : item_chunks(rp, j);
-  const bool rotated = !is_v && j < rp.rot / 16;
+  const bool fresh = r0 == 0;
+  const float was = fresh ? 0.f : *scale;
 
   float x[kItems][16];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int r = r0 + (tid + k * threads) / per;
-    if (r < r1) {
-      const uint4* row = src + ((tok0 + r) * hkv + g) * (d / 8);
-      unpack8(row[ch.x], x[k]);
-      unpack8(row[ch.y], x[k] + 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[k][e] = 0.f;
-    }
-  }
   if (rotated) {
     uint64_t step[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) step[e] = turn_step(__ldg(rp.inv_freq + j * 8 + e));
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int r = r0 + (tid + k * threads) / per;
-      if (r < r1) {
-        const int pos = rp.positions ? __ldg(rp.positions + tok0 + r) : (int)start + r;
-        rotate_item(x[k], rp.interleaved != 0, [&](int e) { return turn(step[e], pos); });
-      }
+      const int r = r0 + ((tid + k * threads) >> per_log2);
+      const int pos = r < r1 ? (rp.positions ? __ldg(rp.positions + tok0 + r) : (int)start + r) : 0;
+      unpack8(in[k][0], x[k]);
+      unpack8(in[k][1], x[k] + 8);
+      rotate_item(x[k], rp.interleaved != 0, [&](int e) { return turn(step[e], pos); });
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      unpack8(in[k][0], x[k]);
+      unpack8(in[k][1], x[k] + 8);
     }
   }
   // the largest finite value (bits of non-negative floats are in their order)
@@ -317,16 +328,14 @@ __global__ void __launch_bounds__(256, kItems == 4 ? 2 : 4) append_q8_kernel(Seq
     }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) s_top[tid >> 5] = top;
-  const bool fresh = r0 == 0;
-  const float was = fresh ? 0.f : *scale;
   __syncthreads();
   for (int w = 0; w < threads / 32; ++w) top = max(top, s_top[w]);
   const float need = scale_for(__uint_as_float(top));
   const float sc = was > need ? was : need;
   if (!fresh && need > was) {
     const float ratio = was / need;
-    for (int i = tid; i < r0 * per; i += threads) {
-      uint4* at = reinterpret_cast<uint4*>(pages + (int64_t)(i / per) * hkv * d) + i % per;
+    for (int i = tid; i < r0 << per_log2; i += threads) {
+      uint4* at = reinterpret_cast<uint4*>(pages + (int64_t)(i >> per_log2) * hkv * d) + j;
       const uint4 old = *at;
       const uint32_t w[4] = {old.x, old.y, old.z, old.w};
       uint32_t o[4];
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(256, kItems == 4 ? 2 : 4) append_q8_kernel(Seq
   const bool whole = (__float_as_uint(sc) & 0x7fffffu) == 0;  // a power of two: x inv is x / sc
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    const int r = r0 + (tid + k * threads) / per;
+    const int r = r0 + ((tid + k * threads) >> per_log2);
     if (r >= r1) break;
     uint32_t o[4];
 #pragma unroll
