@@ -619,13 +619,14 @@ typedef struct nsa_paged_cache_q8 {
  * new tokens stay as they are.  Deterministic.  A block is read and written as a whole, so
  * none that gets new tokens may be listed twice (a shared prefix is shared in whole blocks).
  *   k_new, v_new  [tokens, h_kv, d] bf16
- *   rope          nullable: keys as they are (rope->q then goes without rotation too: not at all) */
+ *   rope          nullable: keys are written as they are, and there are no queries */
 NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new, const void* v_new,
                                        const nsa_rope* rope, const nsa_paged_cache_q8* cache, cudaStream_t stream);
 
 /* nsa_paged_attn_fwd over a cache held in 8 bits: the same arguments, masks, empty rows and
  * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
- * cache_lens has to be finite.
+ * cache_lens has to be finite; a row of q that is not spoils its own output
+ * alone (NaN where the codes are read as they are).
  * Calls of fewer than 160 rows (max_seqlen * h / h_kv; 128 for d = 64) read the codes as they are: scores see q as it is, down to
  * 2^-24 of its row's largest element, and weights enter the second product with a relative error
  * below 2^-8.6 (as bf16 they would have 2^-8).  Calls of more rows, which the products bound,

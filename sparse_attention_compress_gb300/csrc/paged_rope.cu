@@ -169,7 +169,7 @@ __device__ __forceinline__ void rope_tokens(const Seqs& s, const Keys& c, const 
     s_cs[t * 64 + e] = turn(turn_step(__ldg(rp.inv_freq + e)), s_pos[t]);
   }
   __syncthreads();
-  // A thread keeps its item j of a head and goes through the heads of the tokens, one after another (no divisions).
+  // A thread keeps its item j of a head and goes through the heads of the tokens, one after another: no divisions.
   const int per_log2 = d == 128 ? 3 : 2, j = tid & ((1 << per_log2) - 1), step = blockDim.x >> per_log2;
   const int nq = rp.q ? h : 0, heads = q_only ? nq : nq + 2 * hkv, cd = d / 8;
   const bool turned = j < rp.rot / 16;
@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(256, kItems == 4 ? 2 : 5)
                      const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, uint8_t* k_pages,
                      uint8_t* v_pages, float* k_scales, float* v_scales, int h, int hkv, int d) {
   if ((int)blockIdx.x >= kv_blocks) {
-    rope_tokens(s, c, rp, (int64_t)((int)blockIdx.x - kv_blocks) * n_tok, n_tok, nullptr, nullptr, nullptr, nullptr, nullptr, h, hkv, d, true);
+    rope_tokens(s, c, rp, (int64_t)((int)blockIdx.x - kv_blocks) * n_tok, n_tok, nullptr, nullptr, nullptr, nullptr,
+                nullptr, h, hkv, d, true);
     return;
   }
   __shared__ uint32_t s_top[8];
@@ -293,7 +294,8 @@ __global__ void __launch_bounds__(256, kItems == 4 ? 2 : 5)
   if (pid < 0) return;
   const int slot = (int)start & ((1 << c.page_log2) - 1);
   uint8_t* pages = (is_v ? v_pages : k_pages) + pid * c.page_stride + ((int64_t)slot * hkv + g) * d;
-  float* scale = (is_v ? v_scales : k_scales) + (((int64_t)pid * hkv + g) << (c.page_log2 - block_log2)) + (slot >> block_log2);
+  float* scale = (is_v ? v_scales : k_scales) + (((int64_t)pid * hkv + g) << (c.page_log2 - block_log2)) +
+                 (slot >> block_log2);
   const bool fresh = r0 == 0;
   const float was = fresh ? 0.f : *scale;
 
@@ -405,8 +407,8 @@ cudaError_t launch_paged_q8_append(const Seqs& s, const void* k_new, const void*
   if (all > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int items = std::min(B, s.max_len) * (d / 16), threads = items <= 128 ? 128 : 256;
   auto go = [&](auto kern) {
-    kern<<<(unsigned)all, threads, 0, st>>>(s, span::keys_of(&cache, nullptr, nullptr), span::rope_of(rope), (int)kv_blocks, n,
-                                            block_log2, blocks, (const uint4*)k_new, (const uint4*)v_new,
+    kern<<<(unsigned)all, threads, 0, st>>>(s, span::keys_of(&cache, nullptr, nullptr), span::rope_of(rope),
+                                            (int)kv_blocks, n, block_log2, blocks, (const uint4*)k_new, (const uint4*)v_new,
                                             (uint8_t*)k_pages, (uint8_t*)v_pages, k_scales, v_scales, h, hkv, d);
   };
   if (items <= threads)

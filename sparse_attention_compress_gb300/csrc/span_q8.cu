@@ -26,7 +26,14 @@
 // The key tiles of all units (row tile, sequence, kv-head) are cut into equal runs, one for each CTA
 // that fits the GPU: a run may start and end inside a unit, whose parts (max, sum, unnormalised
 // o) q8_combine_kernel joins in order.  So ragged caches even out, and a CTA sets itself
-// up once.
+// up once.  The barriers of a turn cost more than its arithmetic, so a turn takes two key tiles.
+//
+// Decode, 32 caches of 16384 .. 32768 keys, 16 heads over 2 kv-heads of 128 (403 MB of codes): 79.4 us, 5.1 TB/s
+// of a copy's 6.7; the same over a bf16 cache takes 146.  Of the rest, 8 us go before the first scores (launch,
+// set-up, first copies) and 5 into the join; in between HBM runs at 6.0 TB/s.  The tensor cores are far from
+// their limit (one row of 8 in use of N = 16 costs as much as 16), but not from sight: a product with M = 128
+// takes 40 cycles or more however small its N.  With 128 rows a kv-head the softmax bounds the call: 16 caches of up
+// to 8192 keys, 8 tokens, 64 heads over 4 136 us (of which HBM 17).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -50,10 +57,11 @@ struct Keys8 {
 
 template <int D, int NR>
 struct Cfg8 {
-  static constexpr int HR = 8, SUB = 2;   // rows and keys a thread: a turn takes SUB key tiles
+  static constexpr int HR = 8, SUB = 2;   // rows and keys of a thread: a turn takes SUB key tiles
   static constexpr int GROUPS = NR / HR;  // softmax groups of four warps
   static constexpr int PER_SM = NR <= 16 ? 2 : 1;
-  static constexpr int SOFT = 4 * GROUPS, THREADS = (SOFT + 4) * 32;  // softmax warps; loads of K and of V, products, queries and scales
+  // softmax warps; then loads of K, loads of V, products, queries and scales
+  static constexpr int SOFT = 4 * GROUPS, THREADS = (SOFT + 4) * 32;
   static constexpr int TILE = KT * D;
   // Rows of one of Q's terms (columns of S^T), columns of O^T: three terms of P; the products want multiples of 16
   static constexpr int SN = NR < 16 ? 16 : NR, PN = (3 * NR + 15) / 16 * 16;
@@ -413,8 +421,8 @@ __device__ __forceinline__ uint32_t rest_of(uint32_t h, uint16_t c) {
 // Query rows r0, r0 + step, ... of a unit as two terms: row r and row SN + r of the operand; what
 // turns their scores into exponents of 2; and the running maximum of no keys.  A warp's call.
 template <int D, int NR>
-__device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, uint32_t q_s, float* s_rs, float* s_nm, int r0, int step,
-                                        int lane) {
+__device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, uint32_t q_s, float* s_rs, float* s_nm,
+                                        int r0, int step, int lane) {
   constexpr int E = D / 32, SN = Cfg8<D, NR>::SN;  // values a lane
   const int rows = u.s.rows(p, u.rt);
 #pragma unroll 4
@@ -461,7 +469,8 @@ __device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, ui
       asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, SN + r, ch) + in), "h"((uint16_t)c2) : "memory");
     }
     if (lane == 0 && r < NR) {
-      s_rs[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+      // (a row with an infinity or NaN: its terms are finite, so its scores are made NaN here)
+      s_rs[r] = p.scale_log2 * __uint_as_float(top < 0x7f800000u ? (uint32_t)(127 - ex) << 23 : 0x7fc00000u);
       s_nm[r] = -kNone;
     }
   }
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
       }
     }
   } else if (warp == kAux) {
-    // ------------------------------------------------------------------ per unit: what the softmax needs to know, queries, scales
+    // ------------------------------------------------------------------ per unit: description, queries, scales
     // The first unit's queries are the softmax warps' own; a later one's are loaded once the scales of the
     // unit before are on their way.
     Ring<2> rq;
@@ -869,9 +878,8 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
               const int col = z * NR + x0;
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(at8<C::PW>(p_s + y * C::P_TILE, krow, col >> 4) + (col & 15)),
-                           "r"(c[z][0]), "r"(c[z][1])
-                           : "memory");
+              const uint32_t to = at8<C::PW>(p_s + y * C::P_TILE, krow, col >> 4) + (col & 15);
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(to), "r"(c[z][0]), "r"(c[z][1]) : "memory");
             }
           }
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -921,10 +929,10 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
             if (e < rows) {
               if (whole) {
                 const int64_t rr = tok * p.h + g * p.R + head;
-                if (krow < D) p.o[rr * D + krow] = __float2bfloat16(sum > 0.f ? o / sum : 0.f);
-                if (p.lse && krow == 0) p.lse[rr] = sum > 0.f ? (log2f(sum) - neg) * kLn2 : kNegInf;
+                if (krow < D) p.o[rr * D + krow] = __float2bfloat16(sum != 0.f ? o / sum : 0.f);
+                if (p.lse && krow == 0) p.lse[rr] = sum != 0.f ? (log2f(sum) - neg) * kLn2 : kNegInf;
               } else {
-                if (krow < D && sum > 0.f) p.part_o[(slot * NR + x0 + e) * D + krow] = o;
+                if (krow < D && sum != 0.f) p.part_o[(slot * NR + x0 + e) * D + krow] = o;
                 if (krow == 0) p.part_ml[slot * NR + x0 + e] = make_float2(-neg, sum);
               }
             }
@@ -984,7 +992,7 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p) {
   if (parts > 1) {
     for (int i = lane; i < parts; i += 32) {
       const float2 ml = p.part_ml[slot(i)];
-      if (ml.y > 0.f) m = fmaxf(m, ml.x);
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);  // (NaN counts: it has to reach the row)
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -992,7 +1000,7 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p) {
       float w = 0.f, wl = 0.f;
       if (i0 + lane * PW < parts) {
         const float2 ml = p.part_ml[slot(i0 + lane * PW)];
-        if (ml.y > 0.f) {
+        if (ml.y != 0.f) {
           w = ex2(ml.x - m);
           wl = w * ml.y;
         }
@@ -1028,11 +1036,11 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p) {
     }
   }
   if (parts < 2) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(p.o + rr * D + lane * E + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[rr] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+  if (p.lse && lane == 0) p.lse[rr] = l != 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
 }
 
 // How a call is cut.

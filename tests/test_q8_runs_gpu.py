@@ -12,7 +12,7 @@ import sparse_attention_compress_gb300 as nsa
 from sparse_attention_compress_gb300 import _lib
 from tests import q8_reference as ref8
 from tests import span_reference as ref
-from tests.test_q8_gpu import BF, F8, I32, NAN, Cache8, _bf, _cached8, _check, _gen, _inv_freq, _queries
+from tests.test_q8_gpu import BF, F8, I32, NAN, Cache8, _bf, _cached8, _check, _gen, _inv_freq, _queries, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -250,6 +250,36 @@ def test_calls_of_other_row_counts_from_several_threads():
     assert not errors, errors
     for _, o, want, _ in work:
         assert torch.equal(o, want)
+
+
+# ----------------------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 40])  # 8 rows, more, many
+def test_queries_that_are_not_finite_spoil_their_own_rows(n, d):
+    """Where codes are read as they are, rows with NaN or an infinity give NaN, not zeros (calls of many rows have
+    the bf16 cache's answer, zeros).  Every other row is as without them."""
+    c = Cache8([700, 3000, 129], 2, d, 64, 32, 160)
+    q, cu = _queries([n] * 3, 8, d, 161)
+    bad = q.clone()
+    bad[0, 1, 5] = NAN
+    bad[n, 6, d - 1] = NAN
+    bad[3 * n - 1, 0, 0] = math.inf
+    bad[3 * n - 1, 7, :] = NAN
+    lse = torch.full((q.shape[0], 8), 7.0, device="cuda")
+    kw = dict(cu_seqlens=cu.cuda(), max_seqlen=n)
+    o = nsa.nsa_paged_q8_attn_fwd(bad.cuda(), *c.args, lse=lse, **kw)
+    assert nsa.nsa_device_status() == 0
+    rows = torch.zeros(q.shape[0], 8, dtype=torch.bool)
+    for t, h in ((0, 1), (n, 6), (3 * n - 1, 0), (3 * n - 1, 7)):
+        rows[t, h] = True
+        assert n == 40 or torch.isnan(o[t, h]).all(), (t, h)
+    keep = ~rows
+    scale = 1.0 / math.sqrt(d)
+    for b in range(3):
+        a, e, (ro, rl, eo, el) = _reference(c, q, cu, b, 0, 0, scale)
+        k = keep[a:e]
+        ref.within(lse[a:e].cpu()[k], rl[k], el[k], f"lse of sequence {b}")
+        ref.within(o[a:e].cpu()[k], ro[k], eo[k], f"o of sequence {b}")
 
 
 # ----------------------------------------------------------------------------- 32 bits
