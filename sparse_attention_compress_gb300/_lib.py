@@ -1005,7 +1005,8 @@ def nsa_paged_q8_attn_fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, 
                           scale=0.0, *, cu_seqlens=None, max_seqlen=None, max_cache_len=None, workspace=None, out=None,
                           lse=None, stream=None):
     """nsa_paged_attn_fwd over a cache held in 8 bits (as nsa_paged_q8_append writes it): k = code *
-    k_scale, v = code * v_scale, read as they are."""
+    k_scale, v = code * v_scale.  Calls of many tokens expand the keys that they see to bf16 in the workspace
+    first, which max_cache_len (a bound on cache_lens) sizes: give it where tables are much wider than caches."""
     fn = "nsa_paged_q8_attn_fwd"
     if (window | n_sink) >> 31:
         _int32(fn, window=window, n_sink=n_sink)
