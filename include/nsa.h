@@ -627,7 +627,7 @@ NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new
  * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
  * cache_lens has to be finite; a row of q that is not spoils its own output
  * alone (NaN where the codes are read as they are).
- * Calls of fewer than 160 rows (max_seqlen * h / h_kv; 128 for d = 64) read the codes as they are: scores see q as it is, down to
+ * Calls of up to 256 rows (max_seqlen * h / h_kv) read the codes as they are: scores see q as it is, down to
  * 2^-24 of its row's largest element, and weights enter the second product with a relative error
  * below 2^-8.6 (as bf16 they would have 2^-8).  Calls of more rows, which the products bound,
  * expand the seen keys and values to bf16 in the workspace first (exact where scales are powers of two, else

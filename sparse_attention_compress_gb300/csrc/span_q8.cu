@@ -32,8 +32,7 @@
 // of a copy's 6.7; the same over a bf16 cache takes 146.  Of the rest, 8 us go before the first scores (launch,
 // set-up, first copies) and 5 into the join; in between HBM runs at 6.0 TB/s.  The tensor cores are far from
 // their limit (one row of 8 in use of N = 16 costs as much as 16), but not from sight: a product with M = 128
-// takes 40 cycles or more however small its N.  With 128 rows a kv-head the softmax bounds the call: 16 caches of up
-// to 8192 keys, 8 tokens, 64 heads over 4 136 us (of which HBM 17).
+// takes 40 cycles or more however small its N.  From 33 rows on the other form is faster (attn_q8_rows_kernel).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -122,10 +121,11 @@ struct Seq8 {
 // A run is cut in places: a unit has kSwitch places that stand for the time that it takes to begin one (the
 // joining of the row sums, O's way out, the first maxima), then one for each tile.
 // 32 x 16384 .. 32768 keys, 8 rows: 0 places 85 us, 4 80.4, 8 79.5, 12 79.6, 24 80.6; 8 x 8192 keys x 8 kv-heads 46.2,
-// 40.4, 37.1, 37.4, 38.9; 32 rows over 16 x 16384 keys x 4 kv-heads 88, 86, 84, 82, 76.
+// 40.4, 37.1, 37.4, 38.9; 32 rows over 16 x 16384 keys x 4 kv-heads 88, 86, 84, 82, 76; 128 rows over 16 x up to 8192
+// keys x 4 kv-heads with 6 places 72.2, 8 72.5, 12 74.2, 24 81.6.
 template <int NR>
 struct Walk {
-  static constexpr int kSwitch = NR == 32 ? 24 : 12;
+  static constexpr int kSwitch = NR == 128 ? 8 : NR == 32 ? 24 : 12;
   Seq8<NR> s;
   int seq, g, rt;
   int a, n, all;  // tiles a .. a + n - 1 of the unit's `all`; n = 0: the run has no tile (left)
@@ -195,6 +195,57 @@ struct Turns {
   }
 };
 
+// A CTA's run: places first .. first + places - 1 of `total`, which `ctas` CTAs share.
+struct Run8 {
+  int places = 0, ctas = 0;
+  int64_t first = 0, total = 0;
+};
+// False: there is nothing for this CTA.  A streamed call's run begins in sequence *s_seq, *s_at places on (known
+// after the block's next synchronisation).
+template <int NR, int WARPS>
+__device__ __forceinline__ bool find_run(const Q8Params& p, Run8& r, int64_t* s_scan, int* s_seq, int64_t* s_at) {
+  if (!p.streamed) return Walk<NR>(p, (int64_t)blockIdx.x).n != 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.seqs.n_seqs + WARPS * 32 - 1) / (WARPS * 32), i0 = min(p.seqs.n_seqs, tid * per),
+            i1 = min(p.seqs.n_seqs, i0 + per);
+  auto places_of = [&](int i) {
+    Seq8<NR> s;
+    s.load(p, i);
+    int64_t c = 0;
+    for (int rt = 0; rt < p.row_tiles; ++rt)
+      if (const int n = s.count(p, rt)) c += n + Walk<NR>::kSwitch;
+    return c * p.hkv;
+  };
+  int64_t mine = 0;
+  for (int i = i0; i < i1; ++i) mine += places_of(i);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  r.total = total;
+  r.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / p.min_places));
+  if (total == 0 || blockIdx.x >= r.ctas) return false;
+  r.first = total * blockIdx.x / r.ctas;
+  r.places = (int)(total * (blockIdx.x + 1) / r.ctas - r.first);
+  before += incl - mine;
+  if (before <= r.first && r.first < before + mine) {
+    int i = i0;
+    for (int64_t c; before + (c = places_of(i)) <= r.first; ++i) before += c;
+    *s_seq = i;
+    *s_at = r.first - before;
+  }
+  return true;
+}
+
 // What the softmax has to know of a unit, in shared memory (its registers hold rows).
 struct Part8 {
   int64_t start;
@@ -203,8 +254,7 @@ struct Part8 {
   int sink_end, shift, total, full_lo, full_hi;  // tiles full_lo .. full_hi - 1: every row sees every key that has a page
 };
 template <int NR>
-__device__ __forceinline__ void describe(const Q8Params& p, const Walk<NR>& u, int64_t t, int64_t total, int ctas,
-                                         Part8* s) {
+__device__ __forceinline__ void describe(const Q8Params& p, const Walk<NR>& u, const Run8& r, Part8* s) {
   const Tiles tl = u.s.tiles(p, u.rt);
   const int off = u.s.kv_len - u.s.Lq, rows = u.s.rows(p, u.rt);
   const int64_t row0 = (int64_t)u.rt * NR;
@@ -217,7 +267,8 @@ __device__ __forceinline__ void describe(const Q8Params& p, const Walk<NR>& u, i
   s->full_hi = max(0, p0 + 1 - tl.shift) / KT - u.a;  // the last key is at most the first position
   s->full_lo = p.window > 0 ? max(0, (max(tl.sink_end, p1 - p.window + 1 - tl.shift) + KT - 1) / KT) - u.a : 0;
   // (of a unit that begins here, at place t) the CTA that has place e - 1 of all: floor((e ctas - 1) / total)
-  s->ctas = p.streamed ? (int)(((t + u.kSwitch + u.all) * ctas - 1) / total) - (int)blockIdx.x + 1 : 1;
+  const int64_t t = r.first + r.places - u.left - u.at;
+  s->ctas = p.streamed ? (int)(((t + u.kSwitch + u.all) * r.ctas - 1) / r.total) - (int)blockIdx.x + 1 : 1;
   s->more = u.left - u.took > u.kSwitch;
 }
 
@@ -431,8 +482,8 @@ __device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, ui
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.f;
     if (r < rows) {
-      const int64_t rho = (int64_t)u.rt * NR + r;
-      const __nv_bfloat16* src = p.q + ((u.s.start + rho / p.R) * p.h + u.g * p.R + rho % p.R) * D + lane * E;
+      const uint32_t rho = (uint32_t)u.rt * NR + r, R = p.R;  // (a call of many rows does not come here)
+      const __nv_bfloat16* src = p.q + ((u.s.start + rho / R) * p.h + u.g * p.R + rho % R) * D + lane * E;
       if constexpr (E == 4) {
         const uint2 w = *reinterpret_cast<const uint2*>(src);
         x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
@@ -506,48 +557,8 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
   if (stopped()) return;
   const Waits wait(abort);
   // ------------------------------------------------------------------ this CTA's run of tiles
-  int run = 0, ctas = 0;
-  int64_t t0 = 0, total = 0;  // the run: places t0 .. t0 + run - 1 of `total`
-  if (p.streamed) {
-    const int per = (p.seqs.n_seqs + C::THREADS - 1) / C::THREADS, i0 = min(p.seqs.n_seqs, tid * per),
-              i1 = min(p.seqs.n_seqs, i0 + per);
-    auto places_of = [&](int i) {
-      Seq8<NR> s;
-      s.load(p, i);
-      int64_t c = 0;
-      for (int rt = 0; rt < p.row_tiles; ++rt)
-        if (const int n = s.count(p, rt)) c += n + Walk<NR>::kSwitch;
-      return c * p.hkv;
-    };
-    int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += places_of(i);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
-    ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / p.min_places));
-    if (total == 0 || blockIdx.x >= ctas) return;
-    t0 = total * blockIdx.x / ctas;
-    run = (int)(total * (blockIdx.x + 1) / ctas - t0);
-    before += incl - mine;
-    if (before <= t0 && t0 < before + mine) {
-      int i = i0;
-      for (int64_t c; before + (c = places_of(i)) <= t0; ++i) before += c;
-      s_seq = i;
-      s_at = t0 - before;
-    }
-  } else {
-    if (Walk<NR>(p, (int64_t)blockIdx.x).n == 0) return;
-  }
+  Run8 r;
+  if (!find_run<NR, WARPS>(p, r, s_scan, &s_seq, &s_at)) return;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -576,7 +587,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
-  Walk<NR> u = p.streamed ? Walk<NR>(p, s_seq, s_at, run) : Walk<NR>(p, (int64_t)blockIdx.x);
+  Walk<NR> u = p.streamed ? Walk<NR>(p, s_seq, s_at, r.places) : Walk<NR>(p, (int64_t)blockIdx.x);
   // whole steps of 32 keys (the product's K): what lies past the keys is zeros
   auto width = [&](const Tiles& tl, int i) { return max(0, min(KT, (tl.width(i) + 31) & ~31)); };
 
@@ -625,7 +636,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
     bool ok = true, again = false;
     for (int k = 0; ok; ++k) {
       if (k > 1 && !(ok = wait(bar(B::QEMPTY + rq.slot), rq.phase ^ 1u))) break;
-      if (lane == 0) describe<NR>(p, u, t0 + run - u.left - u.at, total, ctas, &s_part[k & 3]);
+      if (lane == 0) describe<NR>(p, u, r, &s_part[k & 3]);
       if (k > 0)
         load_q8<D, NR>(p, u, q_s + rq.slot * C::Q_BYTES, s_rs[rq.slot], s_nm[k & 3][0], 0, 1, lane);
       else
@@ -965,6 +976,520 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
   if (warp == kIssue) tmem_free(tmem, C::TMEM);
 }
 
+// ---------------------------------------------------------------------------- many rows over long caches
+// More rows than the form above is made for: the rows are the products' M, as in span_attn.cu, and four warps
+// turn the codes into f16 tiles (exact) beside the products,
+//   S [128 rows x 128 keys] = Q K^T,   O [128 rows x d] += P V,
+// with Q 2^a in f16 (exact down to 2^-32 of the row's largest element), P' = exp(t - m) sv 2^9 in f16, in TMEM
+// over the scores it came from.  Scales stay with the scores and the weights, as above.  Four
+// threads share a row, 32 keys each, and agree on its running maximum by a vote of their warps.  S of the next
+// tile is issued before this one's P is waited for.
+// 16 caches of up to 8192 keys, 8 tokens, 64 heads over 4 kv-heads of 128: 72.5 us, of which HBM 17 (136 in tiles of
+// 32 rows by the form above, whose three terms of P cost too many conversions; 122 with those terms and the rows as M).
+// A key tile takes about 3000 cycles: the conversion of its K and V 1600 and the softmax of its rows 2100, beside
+// each other; shared memory moves 220 KB for it, 1750 cycles.
+template <int D>
+struct CfgR {
+  static constexpr int NR = 128, SOFT = 16, CONV = 4, WARPS = SOFT + CONV + 3, THREADS = WARPS * 32;
+  static constexpr int CODES = KT * D, TILE = KT * D * 2;  // bytes of a tile of codes, of a tile (or of Q) in f16
+  static constexpr int NC = D == 64 ? 6 : 3, NF = D == 64 ? 6 : 4;  // slots of codes and of tiles, K and V in turn
+  static constexpr int SMEM = TILE + NF * TILE + NC * CODES + 1024;
+  static constexpr uint32_t TMEM = 512, O_COL = 256;
+};
+template <int NC, int NF>
+struct BarsR {
+  enum : int {
+    CFULL = 0,           // [NC] codes
+    CEMPTY = NC,
+    FFULL = 2 * NC,      // [NF] tiles
+    FEMPTY = FFULL + NF,
+    SFULL = FEMPTY + NF,  // [2] S of a tile
+    PFULL = SFULL + 2,   // [2] its P
+    PVDONE = PFULL + 2,  // [2] its product
+    SCFULL = PVDONE + 2,  // [4] scales of up to four tiles
+    SCEMPTY = SCFULL + 4,
+    QFULL = SCEMPTY + 4,
+    QEMPTY = QFULL + 1,  // the unit's last S, and every softmax warp has begun the unit
+    DRAIN = QEMPTY + 1,
+    COUNT
+  };
+};
+
+constexpr uint32_t idesc_f16(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
+
+// 16 codes to 16 f16.
+__device__ __forceinline__ void f16_of_codes(uint4 c, uint4* lo, uint4* hi) {
+  lo->x = f16x2_of_e4m3((uint16_t)c.x), lo->y = f16x2_of_e4m3((uint16_t)(c.x >> 16));
+  lo->z = f16x2_of_e4m3((uint16_t)c.y), lo->w = f16x2_of_e4m3((uint16_t)(c.y >> 16));
+  hi->x = f16x2_of_e4m3((uint16_t)c.z), hi->y = f16x2_of_e4m3((uint16_t)(c.z >> 16));
+  hi->z = f16x2_of_e4m3((uint16_t)c.w), hi->w = f16x2_of_e4m3((uint16_t)(c.w >> 16));
+}
+
+// Query rows 32 cw .. 32 cw + 31 of a unit as f16, max |q 2^a| in [2^14, 2^15), and what turns their scores into
+// exponents of 2.  A warp's call; 16 bytes a lane, eight loads under way at a time.
+template <int D>
+__device__ __forceinline__ void load_q_f16(const Q8Params& p, const Walk<128>& u, uint32_t q_s, float* s_rs, int cw,
+                                           int lane) {
+  constexpr int LANES = D / 8, STEP = 32 / LANES;  // lanes of a row, rows of a load
+  const int rows = u.s.rows(p, u.rt), col = lane % LANES * 8;
+  const uint32_t group = (LANES == 16 ? 0xffffu : 0xffu) << (lane / LANES * LANES);
+#pragma unroll 1
+  for (int r0 = cw * 32 + lane / LANES; r0 < cw * 32 + 32; r0 += 8 * STEP) {
+    uint4 w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int r = r0 + e * STEP;
+      w[e] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const uint32_t rho = (uint32_t)u.rt * 128 + r, R = p.R;  // (a call of many rows does not come here)
+        w[e] = *reinterpret_cast<const uint4*>(p.q + ((u.s.start + rho / R) * p.h + u.g * p.R + rho % R) * D + col);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int r = r0 + e * STEP;
+      const uint32_t b[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+      uint32_t top = 0, h[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) top = max(top, max(b[z] << 16 & 0x7fffffffu, b[z] & 0x7fff0000u));
+      top = __reduce_max_sync(group, top);
+      const int ex = min(120, max(-120, 14 + 127 - (int)(top >> 23)));
+      const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const __half2 y = __floats2half2_rn(__uint_as_float(b[z] << 16) * up, __uint_as_float(b[z] & 0xffff0000u) * up);
+        h[z] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      st_shared(stage_at(q_s, KT * 128, r, col / 8), make_uint4(h[0], h[1], h[2], h[3]));
+      // (a row with an infinity or NaN: its scores are NaN)
+      if (col == 0)
+        s_rs[r] = p.scale_log2 * __uint_as_float(top < 0x7f800000u ? (uint32_t)(127 - ex) << 23 : 0x7fc00000u);
+      __syncwarp();
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(CfgR<D>::THREADS, 1)
+    attn_q8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k16,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v16,
+                        const Q8Params p) {
+  using C = CfgR<D>;
+  constexpr int NR = C::NR, NC = C::NC, NF = C::NF, SOFT = C::SOFT, CONV = C::CONV;
+  using B = BarsR<NC, NF>;
+  constexpr int kConv = SOFT, kLoad = SOFT + CONV, kIssue = kLoad + 1, kAux = kLoad + 2;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[B::COUNT];
+  __shared__ __align__(16) float4 s_sc[4][4][8];  // batch, tile, 16 keys: (sk, log2 sv, 1 / sv, whether there is a page)
+  __shared__ float s_rs[2][NR];                   // scale log2(e) 2^-a of a row of unit k at k % 2
+  __shared__ float s_max[4][NR], s_sum[4][NR];
+  __shared__ int64_t s_scan[C::WARPS], s_at;
+  __shared__ uint32_t s_tmem;
+  __shared__ Part8 s_part[8];  // of unit k of the run, at k % 8
+  __shared__ int s_abort, s_seq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t q_s = (smem_u32(smem_raw) + 1023) & ~1023u, tiles_s = q_s + C::TILE, codes_s = tiles_s + NF * C::TILE;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  volatile int* abort = &s_abort;
+
+  launch_dependents();
+  if (stopped()) return;
+  const Waits wait(abort);
+  Run8 r;
+  if (!find_run<NR, C::WARPS>(p, r, s_scan, &s_seq, &s_at)) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < NC; ++i) {
+      tc::mbar_init(bar(B::CFULL + i), 1);
+      tc::mbar_init(bar(B::CEMPTY + i), CONV);
+    }
+    for (int i = 0; i < NF; ++i) {
+      tc::mbar_init(bar(B::FFULL + i), CONV);
+      tc::mbar_init(bar(B::FEMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(B::SFULL + i), 1);
+      tc::mbar_init(bar(B::PFULL + i), SOFT);
+      tc::mbar_init(bar(B::PVDONE + i), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(bar(B::SCFULL + i), 1);
+      tc::mbar_init(bar(B::SCEMPTY + i), SOFT);
+    }
+    tc::mbar_init(bar(B::QFULL), CONV);
+    tc::mbar_init(bar(B::QEMPTY), SOFT + 1);
+    tc::mbar_init(bar(B::DRAIN), 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kIssue) {
+    tmem_alloc(smem_u32(&s_tmem), C::TMEM);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+  Walk<NR> u = p.streamed ? Walk<NR>(p, s_seq, s_at, r.places) : Walk<NR>(p, (int64_t)blockIdx.x);
+  // whole steps of 32 keys: what lies past the keys is zeros
+  auto width = [&](const Tiles& tl, int i) { return max(0, min(KT, (tl.width(i) + 31) & ~31)); };
+
+  int last_item = -1;  // loading warp: the last tile handed to the ring of codes; issuing warp: the last one used
+  if (u.n == 0) {
+    // (a run that lies between two units)
+  } else if (warp == kLoad) {
+    // ------------------------------------------------------------------ codes of K and V tiles, in turn
+    Turns<NR, 1> t(p, u);
+    Ring<NC> rc;
+    bool ok = true;
+    for (; ok && t.more; t.next(p)) {
+      const int i = t.u.a + t.j;
+      const int pid = page_at(p.keys.c, t.u.seq, i * KT + (lane & 7) * GRAN, t.tl.sink_end, t.tl.shift, t.u.s.kv_len);
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y) {
+        if (last_item + 1 >= NC && !(ok = wait(bar(B::CEMPTY + rc.slot), rc.phase ^ 1u))) break;
+        load_tile8<D>(codes_s + rc.slot * C::CODES, y ? &tm_v : &tm_k, y ? &tm_v16 : &tm_k16, y ? p.keys.v : p.keys.k,
+                      p.keys.c, p.hkv, t.u.g, pid, i * KT, t.tl.sink_end, t.tl.shift, width(t.tl, i), t.u.s.kv_len,
+                      bar(B::CFULL + rc.slot), lane);
+        ++last_item;
+        rc.next();
+      }
+    }
+  } else if (warp >= kConv && warp < kConv + CONV) {
+    // ------------------------------------------------------------------ codes to f16; queries
+    const int cw = warp - kConv, ct = tid - kConv * 32;
+    Turns<NR, 1> t(p, u);
+    Ring<NC> rc;
+    Ring<NF> rf;
+    bool ok = true;
+    int item = 0;
+    for (int k = 0; ok && t.more;) {
+      if (t.j == 0) {
+        if (k > 0 && !(ok = wait(bar(B::QEMPTY), (k - 1) & 1))) break;
+        load_q_f16<D>(p, t.u, q_s, s_rs[k & 1], cw, lane);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::QFULL));
+        ++k;
+      }
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y, ++item) {
+        if (!(ok = wait(bar(B::CFULL + rc.slot), rc.phase) &&
+                   (item < NF || wait(bar(B::FEMPTY + rf.slot), rf.phase ^ 1u))))
+          break;
+        const uint32_t from = codes_s + rc.slot * C::CODES, to = tiles_s + rf.slot * C::TILE;
+        // Eight lanes take four 16-byte chunks of two rows whose numbers differ in bits 0 and 2 (d = 128; of two rows
+        // that follow one another for d = 64): other banks for each, of the codes and of the f16.
+        constexpr int N = KT * (D / 16) / (CONV * 32);  // chunks of a thread
+        const int j = ct >> 3, sub = ct >> 2 & 1;
+#pragma unroll 1
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          uint4 c[4];
+          auto row_of = [&](int e) {
+            return D == 128 ? (ct >> 5) * 8 + (e >> 1) * 32 + ((j & 3) * 2 ^ (sub ? 5 : 0)) : e * 32 + j * 2 + sub;
+          };
+          auto chunk_of = [&](int e) { return (ct & 3) + (D == 128 ? (e & 1) * 4 : 0); };
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] = ld_shared(at8<D>(from, row_of(e0 + e), chunk_of(e)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 lo, hi;
+            f16_of_codes(c[e], &lo, &hi);
+            const int row = row_of(e0 + e), ch = 2 * chunk_of(e);
+            st_shared(stage_at(to, KT * 128, row, ch), lo);
+            st_shared(stage_at(to, KT * 128, row, ch + 1), hi);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(bar(B::FFULL + rf.slot));
+          tc::mbar_arrive(bar(B::CEMPTY + rc.slot));
+        }
+        rc.next();
+        rf.next();
+      }
+      if (ok) t.next(p);
+    }
+  } else if (warp == kAux) {
+    // ------------------------------------------------------------------ per unit: description, scales
+    Ring<4> rs;
+    bool ok = true, again = false;
+    for (int k = 0; ok; ++k) {
+      const Tiles tl = u.s.tiles(p, u.rt);
+      for (int i = 0; i < u.n; i += 4) {
+        if (again && !(ok = wait(bar(B::SCEMPTY + rs.slot), rs.phase ^ 1u))) break;
+        // (four batches are under way at most, so unit k - 8's description is no longer in use)
+        if (i == 0 && lane == 0) describe<NR>(p, u, r, &s_part[k & 7]);
+        const int tile = u.a + i + (lane >> 3), place = tile * KT + (lane & 7) * GRAN;
+        const int key = place < tl.sink_end ? place : place + tl.shift;
+        float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tile < u.a + u.n && place < tl.total && key < u.s.kv_len) {
+          const int pid = page_of(p.keys.c, u.seq, key);
+          if (pid >= 0) {
+            const int pl = p.keys.c.page_log2, bl = p.keys.block_log2;
+            const int64_t at = (((int64_t)pid * p.hkv + u.g) << (pl - bl)) + ((key & ((1 << pl) - 1)) >> bl);
+            const float sv = __ldg(p.keys.vs + at);
+            sc = make_float4(__ldg(p.keys.ks + at), log2f(sv), 1.f / sv, 1.f);
+          }
+        }
+        s_sc[rs.slot][lane >> 3][lane & 7] = sc;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::SCFULL + rs.slot));
+        rs.next();
+        again |= rs.slot == 0;
+      }
+      if (!u.next(p)) break;
+    }
+  } else if (warp == kIssue) {
+    // ------------------------------------------------------------------ products: S of tile it, then O of tile it - 1
+    const uint32_t lead = elect(), q_d = desc_k(q_s), k_d = desc_k(tiles_s), v_d = desc_mn(tiles_s);
+    constexpr uint32_t kSlot = C::TILE >> 4, kGroup = KT * 128 >> 4;
+    Turns<NR, 1> ts(p, u), to = ts;
+    Ring<NF> rk, rv;
+    rv.next();
+    bool ok = true;
+    int k = 0;
+    for (uint32_t it = 0; ok && to.more; ++it) {
+      if (ts.more) {
+        const int w = width(ts.tl, ts.u.a + ts.j);
+        if (ts.j == 0 && !(ok = wait(bar(B::QFULL), k++ & 1))) break;
+        if (!(ok = wait(bar(B::FFULL + rk.slot), rk.phase))) break;
+        tc::fence_after();
+        // (over the P of two tiles ago, whose product was issued before: products execute in issue order)
+        const uint32_t s_t = tmem + (it & 1) * 128, kk = k_d + rk.slot * kSlot;
+        const uint32_t id_s = idesc_f16(0) | (uint32_t)(w >> 3) << 17;
+        if (w > 0) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_ss(s_t, q_d + (s >> 2) * kGroup + (s & 3) * 2, kk + (s >> 2) * kGroup + (s & 3) * 2, id_s, s > 0, lead);
+        }
+        commit(bar(B::SFULL + (it & 1)), lead);
+        commit(bar(B::FEMPTY + rk.slot), lead);
+        rk.next();
+        rk.next();
+        ts.next(p);
+        if (ts.more && ts.j == 0) commit(bar(B::QEMPTY), lead);
+      }
+      if (it > 0) {
+        const uint32_t b = (it - 1) & 1;
+        if (!(ok = wait(bar(B::FFULL + rv.slot), rv.phase) && wait(bar(B::PFULL + b), ((it - 1) >> 1) & 1))) break;
+        tc::fence_after();
+        const int w = width(to.tl, to.u.a + to.j);
+        const uint32_t vv = v_d + rv.slot * kSlot, p_t = tmem + b * 128;
+        constexpr uint32_t id = idesc_f16(D) | kBMn;
+        if (w == KT) {
+#pragma unroll
+          for (int s = 0; s < KT / 16; ++s)
+            mma_ts(tmem + C::O_COL, p_t + s * 8, vv + s * (2048 >> 4), id, s > 0 || to.j > 0, lead);
+        } else {
+#pragma unroll
+          for (int s = 0; s < KT / 16; ++s)
+            if (s * 16 < w) mma_ts(tmem + C::O_COL, p_t + s * 8, vv + s * (2048 >> 4), id, s > 0 || to.j > 0, lead);
+        }
+        commit(bar(B::PVDONE + b), lead);
+        commit(bar(B::FEMPTY + rv.slot), lead);
+        last_item += 2;
+        rv.next();
+        rv.next();
+        to.next(p);
+      }
+    }
+  } else if (warp < SOFT) {
+    // ------------------------------------------------------------------ softmax: quarter x of a row's keys
+    constexpr int OC = D / 4;  // columns of O that a thread rescales and writes
+    const int x = warp >> 2, row = tid & 127, vote = 1 + (warp & 3);  // (vote: the barrier of a row's warps)
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16, o_t = tmem + C::O_COL + x * OC + lane_base;
+    Ring<4> rsc;
+    bool ok = true;
+    uint32_t it = 0;  // tiles of the run
+    for (int k = 0;; ++k) {
+      ok = ok && wait(bar(B::SCFULL + rsc.slot), rsc.phase) && wait(bar(B::QFULL), k & 1);
+      if (bar_or(vote, 128, !ok)) break;
+      __syncwarp();
+      const float rs = s_rs[k & 1][row];
+      const volatile Part8& u = s_part[k & 7];
+      const int n = u.n, rows = u.rows;
+      const bool valid = row < rows, work = (warp & 3) * 32 < rows;
+      const int pos = valid ? u.off + (int)(((uint32_t)u.rt * NR + row) / (uint32_t)p.R) : -1;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B::QEMPTY));
+      // nm: minus the running maximum less kRoom; lim: what moves it (at first, any key)
+      float nm = 0.f, l = 0.f, lim = kNegInf;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++it) {
+        const uint32_t b = it & 1, s_t = tmem + b * 128 + lane_base;
+        if (i > 0 && (i & 3) == 0) ok = ok && wait(bar(B::SCFULL + rsc.slot), rsc.phase);
+        ok = ok && wait(bar(B::SFULL + b), (it >> 1) & 1);
+        tc::fence_after();
+        const float4* sc = &s_sc[rsc.slot][i & 3][x * 2];
+        float v[32];
+        bool need = false;
+        float top = kNegInf;
+        if (ok && work) {
+          tc::tmem_ld32_nowait(s_t + x * 32, v);
+          tmem_wait_ld(v);
+          uint32_t pages = 0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float4 c = sc[g];
+            pages |= (uint32_t)(c.w != 0.f) << g;
+            const uint64_t f = pair(rs * c.x, rs * c.x), a = pair(c.y + nm, c.y + nm);
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+              const float2 y = unpair(fma2(pair(v[e], v[e + 1]), f, a));
+              v[e] = y.x;
+              v[e + 1] = y.y;
+            }
+          }
+          if (i < u.full_lo || i >= u.full_hi || pages != 3u) {
+            // seen columns: [j_lo, j_hi) and the sinks [0, j_sink) before j_hi
+            const int at = u.a + i, key0 = at * KT + u.shift, w = min(KT, up16(u.total - at * KT));
+            const int j_hi = min(pos + 1 - key0, w), j_lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;
+            const int j_sink = p.n_sink - at * KT - (u.sink_end > 0 ? 0 : u.shift);
+            uint32_t see = bits(j_lo - x * 32, j_hi - x * 32) | bits(0, min(j_sink, j_hi) - x * 32);
+            see &= (pages & 1u ? 0xffffu : 0u) | (pages & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (see >> e) & 1u ? v[e] : kNegInf;
+          }
+          float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], v[e], v[e + 1]);
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          need = valid && top > lim;
+        }
+        tc::fence_before();
+        // (also: all four warps have read S, over which P goes)
+        const bool move = bar_or(vote, 128, need || !ok);
+        tc::fence_after();
+        if (move) {
+          if (ok) s_max[x][row] = top;
+          if (it > 0) ok = ok && wait(bar(B::PVDONE + ((it - 1) & 1)), ((it - 1) >> 1) & 1);  // O is complete
+          if (bar_or(vote, 128, !ok || *abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          if (work) {
+            const float joint = fmaxf(fmaxf(s_max[0][row], s_max[1][row]), fmaxf(s_max[2][row], s_max[3][row]));
+            const bool mine = valid && joint > lim;
+            const float up = mine ? kRoom - joint : 0.f, al = lim == kNegInf ? 1.f : ex2(up);
+            nm += up;
+            l *= al;
+            if (mine) lim = kMoves;
+            const uint64_t up2 = pair(up, up);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = unpair(add2(pair(v[e], v[e + 1]), up2));
+              v[e] = y.x;
+              v[e + 1] = y.y;
+            }
+            if (i > 0) {
+              __syncwarp();
+#pragma unroll 1
+              for (int c = 0; c < OC; c += 8) {
+                float ov[8];
+                tmem_ld_nowait<8>(o_t + c, ov);
+                tmem_landed<8>(ov);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ov[e] *= al;
+                tmem_st_nowait<8>(o_t + c, ov);
+              }
+              tmem_wait_st();
+            }
+          }
+        }
+        if (!ok) continue;  // (to the next vote)
+        if (work) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+              const float e0 = ex2(v[e]), e1 = ex2(v[e + 1]);
+              sum = add2(sum, pair(e0, e1));
+              const __half2 h = __floats2half2_rn(e0, e1);
+              pk[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            const float2 y = unpair(sum);
+            l = fmaf(y.x + y.y, sc[g].z, l);
+          }
+          tmem_st16_nowait(s_t + x * 16, pk);
+          tmem_wait_st();
+        }
+        tc::fence_before();
+        __syncwarp();
+        const bool release = i + 1 == n || (i & 3) == 3;
+        if (lane == 0) {
+          tc::mbar_arrive(bar(B::PFULL + b));
+          if (release) tc::mbar_arrive(bar(B::SCEMPTY + rsc.slot));
+        }
+        if (release) rsc.next();
+      }
+      // ---------------------------------------------------------------- the unit's rows, or its part of them
+      ok = ok && wait(bar(B::PVDONE + ((it - 1) & 1)), ((it - 1) >> 1) & 1);
+      tc::fence_after();
+      s_sum[x][row] = l;
+      if (bar_or(vote, 128, !ok)) break;  // (also after a timeout: all four warps come here)
+      if (work) {
+        const float sum = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
+        const bool whole = n == u.all;
+        const int g = u.g;
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (u.a == 0);
+        const uint32_t rho = (uint32_t)u.rt * NR + row, R = p.R;
+        const int64_t rr = (u.start + rho / R) * p.h + g * p.R + rho % R;
+        if (p.streamed && u.a == 0 && tid == 0)
+          p.info[((int64_t)u.seq * p.hkv + g) * p.row_tiles + u.rt] = make_int2(blockIdx.x, u.ctas);
+        if (x == 0 && valid) {
+          if (whole && p.lse) p.lse[rr] = sum != 0.f ? (log2f(sum) - nm) * kLn2 : kNegInf;
+          if (!whole) p.part_ml[slot * NR + row] = make_float2(sum != 0.f ? -nm : kNone, sum);
+        }
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < OC; c += 8) {
+          float ov[8];
+          tmem_ld_nowait<8>(o_t + c, ov);
+          tmem_landed<8>(ov);
+          if (valid && whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ov[e] = sum != 0.f ? ov[e] * inv : 0.f;  // (a row without keys may hold no product)
+            *reinterpret_cast<uint4*>(p.o + rr * D + x * OC + c) =
+                make_uint4(pack_bf16(ov[0], ov[1]), pack_bf16(ov[2], ov[3]), pack_bf16(ov[4], ov[5]), pack_bf16(ov[6], ov[7]));
+          } else if (valid && sum != 0.f) {
+            float* to = p.part_o + (slot * NR + row) * D + x * OC + c;
+            *reinterpret_cast<float4*>(to) = make_float4(ov[0], ov[1], ov[2], ov[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(ov[4], ov[5], ov[6], ov[7]);
+          }
+          __syncwarp();
+        }
+        tc::fence_before();  // (the next unit's first product writes O after these loads)
+      }
+      if (!u.more) break;
+    }
+  }
+
+  __syncthreads();
+  if (warp == kLoad && *abort) {
+    // after a timeout the copies still in flight land before the CTA leaves
+    for (int st = 0; st < NC; ++st)
+      if (const int i = last_in_stage(last_item, st, NC); i >= 0) tc::warp_drain(bar(B::CFULL + st), (i / NC) & 1);
+  } else if (warp == kIssue) {
+    // and the products, and the last release of every slot
+    if (u.n > 0) {
+      commit(bar(B::DRAIN), elect());  // (the lane that issued: a commit covers its own products alone)
+      __syncwarp();
+      tc::warp_drain(bar(B::DRAIN), 0);
+    }
+    if (!*abort)
+      for (int st = 0; st < NF; ++st)
+        if (const int i = last_in_stage(last_item, st, NF); i >= 0) tc::warp_drain(bar(B::FEMPTY + st), (i / NF) & 1);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kIssue) tmem_free(tmem, C::TMEM);
+}
+
 // Joins the parts of a row in order: PW warps a row, each every PW-th part, then a sum over the warps.
 // (The parts are written while this kernel starts: no read-only loads of them.)
 template <int D, int NR, int PW>
@@ -1044,6 +1569,9 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8Params p) {
 }
 
 // How a call is cut.
+// Rows of a (sequence, kv-head) up to which the cache is the products' M.  16 caches of 6550 keys x 4 kv-heads,
+// d = 128, us, as M and as N: 32 rows 46 and 61, 48 67 and 60, 64 66 and 61, 128 122 and 63.
+constexpr int kFewRows8 = 32;
 struct Plan8 {
   int nr, row_tiles, ctas;
   bool streamed;
@@ -1053,7 +1581,7 @@ struct Plan8 {
 static Plan8 make_plan8(const Seqs& s, int h, int hkv, int D) {
   Plan8 pl{};
   const int64_t rows = (int64_t)s.max_len * (h / hkv);
-  pl.nr = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  pl.nr = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kFewRows8 ? 32 : 128;
   pl.row_tiles = (int)((rows + pl.nr - 1) / pl.nr);
   pl.units = (int64_t)pl.row_tiles * s.n_seqs * hkv;
   pl.ctas = (pl.nr <= 16 ? 2 : 1) * kSms8;
@@ -1122,10 +1650,10 @@ __global__ void __launch_bounds__(256) expand_q8_kernel(const Expand8 x) {
 }
 
 // How a call of many rows is cut: sequences by groups whose pages fit the room, one after another.
-// Rows a (sequence, kv-head) from which the caches are expanded.  Read as they are and expanded, us: d = 128, 128 rows, 8
-// caches of 16384 keys 119 and 139, 16 of 2048 62 and 62; 160 rows, 134 and 148, 74 and 64; d = 64, 128
-// rows, 102 and 102, 59 and 46; 160 rows, 120 and 112, 69 and 49.
-constexpr int many_rows_from(int D) { return D == 64 ? 128 : 160; }
+// Rows a (sequence, kv-head) from which the caches are expanded: more than two row tiles.  Codes and expanded, us, d =
+// 128: 8 caches of 16384 keys, 160 rows 47 and 67, 256 48 and 71, 512 67 and 73; 16 of 2048
+// keys, 256 rows 34 and 43, 512 both 43; d = 64, 8 of 16384, 256 rows 42 and 52, 512 60 and 53.
+constexpr int kManyRows = 257;
 constexpr size_t kExpandRoom = (size_t)512 << 20;  // bytes of a group's pages, where more than a sequence's
 struct Groups8 {
   int seqs, bound, pages, sink_pages;  // sequences of a group; table entries and workspace pages of each
@@ -1156,7 +1684,7 @@ static Groups8 make_groups8(const Seqs& s, int h, int hkv, int D, int max_keys, 
   gr.bytes = gr.attn + need;
   return gr;
 }
-static bool many_rows(const Seqs& s, int h, int hkv, int D) { return (int64_t)s.max_len * (h / hkv) >= many_rows_from(D); }
+static bool many_rows(const Seqs& s, int h, int hkv) { return (int64_t)s.max_len * (h / hkv) >= kManyRows; }
 
 static cudaError_t launch_expanded(const Seqs& s, const void* q, const Keys8& keys, int h, int hkv, int D, int max_keys,
                                    int window, int n_sink, float scale, void* o, float* lse, void* workspace,
@@ -1228,10 +1756,8 @@ static bool byte_maps(CUtensorMap* big, CUtensorMap* small, const void* ptr, con
   return true;
 }
 
-template <int D, int NR>
-static cudaError_t run_q8(const CUtensorMap* m, const Q8Params& p, const Plan8& pl, cudaStream_t st) {
-  using C = Cfg8<D, NR>;
-  auto kern = attn_q8_kernel<D, NR>;
+template <int D, int NR, typename C, typename Kern>
+static cudaError_t run_q8(Kern kern, const CUtensorMap* m, const Q8Params& p, const Plan8& pl, cudaStream_t st) {
   // (the limit belongs to the kernel, and other threads launch it too: the same for every call)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -1270,9 +1796,10 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
   CUtensorMap m[4];
   if (!byte_maps(&m[0], &m[1], keys.k, keys.c, hkv, D) || !byte_maps(&m[2], &m[3], keys.v, keys.c, hkv, D))
     return cudaErrorInvalidValue;
-  return pl.nr == 8    ? run_q8<D, 8>(m, p, pl, st)
-         : pl.nr == 16 ? run_q8<D, 16>(m, p, pl, st)
-                       : run_q8<D, 32>(m, p, pl, st);
+  return pl.nr == 8    ? run_q8<D, 8, Cfg8<D, 8>>(attn_q8_kernel<D, 8>, m, p, pl, st)
+         : pl.nr == 16 ? run_q8<D, 16, Cfg8<D, 16>>(attn_q8_kernel<D, 16>, m, p, pl, st)
+         : pl.nr == 32 ? run_q8<D, 32, Cfg8<D, 32>>(attn_q8_kernel<D, 32>, m, p, pl, st)
+                       : run_q8<D, 128, CfgR<D>>(attn_q8_rows_kernel<D>, m, p, pl, st);
 }
 
 }  // namespace span
@@ -1280,7 +1807,7 @@ static cudaError_t launch_q8_d(const Seqs& s, const void* q, const Keys8& keys, 
 size_t span_q8_workspace_bytes(const Seqs& s, int h, int hkv, int d, int max_keys, int page, int max_pages, int window,
                                int n_sink) {
   if (s.tokens == 0 || s.n_seqs == 0 || s.max_len == 0) return 0;
-  if (span::many_rows(s, h, hkv, d))
+  if (span::many_rows(s, h, hkv))
     return span::make_groups8(s, h, hkv, d, max_keys, page, max_pages, window, n_sink).bytes;
   return span::make_plan8(s, h, hkv, d).bytes;
 }
@@ -1297,7 +1824,7 @@ cudaError_t launch_span_q8(const Seqs& s, const void* q, const PagedView& cache,
   keys.vs = v_scales;
   keys.c = span::keys_of(&cache, nullptr, nullptr);
   keys.block_log2 = block_log2;
-  if (span::many_rows(s, h, hkv, d))
+  if (span::many_rows(s, h, hkv))
     return span::launch_expanded(s, q, keys, h, hkv, d, max_keys, window, n_sink, scale, o, lse, workspace, st);
   return d == 64 ? span::launch_q8_d<64>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st)
                  : span::launch_q8_d<128>(s, q, keys, h, hkv, window, n_sink, scale, o, lse, workspace, st);

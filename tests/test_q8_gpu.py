@@ -70,7 +70,7 @@ class Cache8:
         return self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.dev_table, self.dev_lens
 
     def reference(self, q, b, see, scale, many=False):
-        """`many`: a call of 160 rows or more (128 for d = 64), whose keys and values are rounded to bf16 and whose weights are bf16."""
+        """`many`: a call of more than 256 rows, whose keys and values are rounded to bf16 and whose weights are bf16."""
         (kc, vc), (ks, vs) = self.codes[b], self.scales[b]
         if many:
             k, v = ((c * s[..., None]).to(BF).double() for c, s in ((kc, ks), (vc, vs)))
@@ -88,7 +88,7 @@ def _reference(c, q, cu, b, window, n_sink, scale, hide=()):
     see = ref.visible(range(c.lens[b] - (e - a), c.lens[b]), c.lens[b], window, n_sink)
     for lo, hi in hide:
         see[:, lo:hi] = False
-    many = int((cu[1:] - cu[:-1]).max()) * q.shape[1] // c.hk >= (160 if c.d == 128 else 128)
+    many = int((cu[1:] - cu[:-1]).max()) * q.shape[1] // c.hk > 256
     return a, e, c.reference(q[a:e].double(), b, see, scale, many)
 
 
@@ -116,10 +116,14 @@ CASES = [
     ([333], [90], 128, 1, 128, 64, 32, 50, 16),                          # group 128: two row tiles a token
     ([2000, 1500], [1, 3], 16, 2, 128, 64, 64, 1000, 4),
     ([200, 650], [2, 2], 16, 1, 128, 32, 32, 0, 0),                      # 32 rows
-    ([700, 650], [19, 1], 8, 1, 128, 32, 32, 0, 0),                      # 152 rows: codes
-    ([700, 650], [20, 1], 8, 1, 128, 32, 32, 0, 0),                      # 160 rows: expanded
-    ([700, 650], [127, 1], 1, 1, 64, 16, 16, 0, 0),                      # 127 rows: codes
-    ([700, 650], [128, 1], 1, 1, 64, 16, 16, 0, 0),                      # 128 rows: expanded
+    ([700, 650], [19, 1], 8, 1, 128, 32, 32, 0, 0),                      # 152 rows: two row tiles
+    ([700, 650], [20, 1], 8, 1, 128, 32, 32, 0, 0),                      # 160 rows
+    ([700, 650], [127, 1], 1, 1, 64, 16, 16, 0, 0),                      # 127 rows
+    ([700, 650], [128, 1], 1, 1, 64, 16, 16, 0, 0),                      # 128 rows: a whole row tile
+    ([700, 650], [32, 1], 8, 1, 128, 32, 32, 0, 0),                      # 256 rows: codes
+    ([700, 650], [257, 1], 1, 1, 128, 32, 32, 0, 0),                     # 257 rows: expanded
+    ([700, 650], [64, 3], 4, 1, 64, 16, 16, 200, 7),                     # 256 rows: codes
+    ([700, 650], [86, 1], 3, 1, 64, 16, 16, 0, 0),                       # 258 rows: expanded
     ([9, 33], [1, 1], 9, 1, 64, 32, 32, 0, 0),                           # 9 rows
     ([200, 650], [3, 1], 11, 1, 64, 64, 16, 90, 2),                      # 33 rows
 ]

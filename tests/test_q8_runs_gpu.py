@@ -45,7 +45,7 @@ def test_attention_at_random_sizes(seed):
     _check(c, q, cu, o, lse, window, n_sink, 1.0 / math.sqrt(d))
 
 
-@pytest.mark.parametrize("n,hk,H,q_len", [(1300, 1, 4, 1), (700, 2, 2, 1), (350, 2, 22, 5), (200, 7, 14, 20)])
+@pytest.mark.parametrize("n,hk,H,q_len", [(1300, 1, 4, 1), (700, 2, 2, 1), (350, 2, 22, 5), (200, 7, 14, 20), (350, 2, 14, 7), (200, 2, 32, 12)])
 def test_more_units_than_runs_take(n, hk, H, q_len):
     """Calls of so many units that each takes a CTA (and no join), ragged, some without queries or keys."""
     g = torch.Generator().manual_seed(7)
