@@ -45,6 +45,29 @@ def test_attention_at_random_sizes(seed):
     _check(c, q, cu, o, lse, window, n_sink, 1.0 / math.sqrt(d))
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_of_33_to_256_rows(seed):
+    r = random.Random(1000 + seed)
+    d, hk, page = r.choice([64, 128]), r.choice([1, 2, 3]), r.choice([16, 32, 64, 128, 256])
+    block = r.choice([b for b in (16, 32, 64, 128) if b <= page])
+    group, n = r.choice([1, 3, 5, 8, 16, 40, 128]), r.choice([1, 2, 5, 9])
+    top = max(1, r.randint(33, 256) // group)
+    q_lens = [r.randint(0, top) for _ in range(n)]
+    q_lens[r.randrange(n)] = top
+    lens = [r.choice([q, q + r.randint(0, 900), r.randint(0, 300), 128 * r.randint(1, 9), q + r.randint(2000, 5000)])
+            for q in q_lens]
+    window = r.choice([0, 0, 1, r.randint(1, 50), r.randint(50, 600)])
+    n_sink = r.choice([0, r.randint(1, 200)]) if window else 0
+    c = Cache8(lens, hk, d, page, block, seed, odd_scales=seed % 2 == 1, spread=r.choice([0, 3, 20]))
+    q, cu = _queries(q_lens, group * hk, d, seed, r.choice([0.3, 1.0, 6.0]))
+    lse = torch.full((q.shape[0], group * hk), NAN, device="cuda")
+    kw = dict(window=window, n_sink=n_sink, cu_seqlens=cu.cuda(), max_seqlen=top)
+    o = nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, lse=lse, **kw)
+    assert nsa.nsa_device_status() == 0
+    _check(c, q, cu, o, lse, window, n_sink, 1.0 / math.sqrt(d))
+    assert torch.equal(o, nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, **kw))
+
+
 @pytest.mark.parametrize("n,hk,H,q_len", [(1300, 1, 4, 1), (700, 2, 2, 1), (350, 2, 22, 5), (200, 7, 14, 20), (350, 2, 14, 7), (200, 2, 32, 12)])
 def test_more_units_than_runs_take(n, hk, H, q_len):
     """Calls of so many units that each takes a CTA (and no join), ragged, some without queries or keys."""
