@@ -9,12 +9,14 @@
 //   O^T [d x rows]        += V tile^T [d x 128 keys] P^T
 // (kind::f8f6f4; V is read MN-major, so nothing is transposed or converted).  Both partners
 // have to be 8-bit floats as well, whose few significant bits would be too few, so they are sums of terms:
-//   Q  = 2^-a (q1 + q2)     a per row, so that max |Q 2^a| is in [128, 256); q1 in e4m3, the rest q2 in e5m2
+//   Q  = 2^-a (q1 + q2 + q3)  a per row, so that max |Q 2^a| is in [128, 256); q1 in e4m3, the rest in e5m2
 //   P' = p1 + p2 + p3       of P' = exp(t - m) sv 2^9 rounded to f16; all in e5m2
-// q1 leaves at most 8 units of bf16's last place, which the 3 significant bits of e5m2 hold, so Q is
+// q1 leaves at most 8 units of bf16's last place, which the 3 significant bits of e5m2 hold, where it is
+// normal: from 2^-6 on.  Below, it leaves up to 2^-10, of which q2 leaves up to 2^-14 (without q3, 2^-21 of
+// the row's largest element would go), and q3 half a step of e5m2's subnormals, 2^-17: so Q is
 // exact down to 2^-16 of its row's largest element, and to 2^-24 of that below.  p1 + p2 + p3 is within
 // 2^-9 of P' (and P' within 2^-11 of its value, half a step of f16; a bf16 P has 2^-8), down
-// to 2^-26 of the row's largest weight.  q1 and q2 share an accumulator (K is read twice); p1, p2 and p3
+// to 2^-26 of the row's largest weight.  q1, q2 and q3 share an accumulator (K is read three times); p1, p2 and p3
 // lie side by side in N with accumulator columns of their own, so that V is read once.
 // A key's value scale sv is part of its weight, and the running maximum is that of t + log2 sv:
 // what is held in few bits is what the sum is made of.  The row sum takes exp(t - m) alone.
@@ -28,8 +30,8 @@
 // o) q8_combine_kernel joins in order.  So ragged caches even out, and a CTA sets itself
 // up once.  The barriers of a turn cost more than its arithmetic, so a turn takes two key tiles.
 //
-// Decode, 32 caches of 16384 .. 32768 keys, 16 heads over 2 kv-heads of 128 (403 MB of codes): 79.4 us, 5.1 TB/s
-// of a copy's 6.7; the same over a bf16 cache takes 146.  Of the rest, 8 us go before the first scores (launch,
+// Decode, 32 caches of 16384 .. 32768 keys, 16 heads over 2 kv-heads of 128 (403 MB of codes): 81.1 us, 5.0 TB/s
+// of a copy's 6.7 (80.1 with Q in two terms); the same over a bf16 cache takes 146.  Of the rest, 8 us go before the first scores (launch,
 // set-up, first copies) and 5 into the join; in between HBM runs at 6.0 TB/s.  The tensor cores are far from
 // their limit (one row of 8 in use of N = 16 costs as much as 16), but not from sight: a product with M = 128
 // takes 40 cycles or more however small its N.  From 33 rows on the other form is faster (attn_q8_rows_kernel).
@@ -62,10 +64,11 @@ struct Cfg8 {
   // softmax warps; then loads of K, loads of V, products, queries and scales
   static constexpr int SOFT = 4 * GROUPS, THREADS = (SOFT + 4) * 32;
   static constexpr int TILE = KT * D;
-  // Rows of one of Q's terms (columns of S^T), columns of O^T: three terms of P; the products want multiples of 16
+  // Columns of S^T, columns of O^T: three terms of P; the products want multiples of 16.  Q's terms lie NR rows apart: with
+  // 8 rows a product reads the next term's, too, into columns that no one reads
   static constexpr int SN = NR < 16 ? 16 : NR, PN = (3 * NR + 15) / 16 * 16;
   static constexpr int PW = NR == 8 ? 32 : NR == 16 ? 64 : 128;  // bytes of a key's line of P (PN, and room for the swizzle)
-  static constexpr int Q_BYTES = 2 * SN * D, P_TILE = KT * PW;  // of one of two Q buffers, of a key tile's P
+  static constexpr int Q_BYTES = (2 * NR + SN) * D, P_TILE = KT * PW;  // of one of two Q buffers, of a key tile's P
   // Slots of a turn's K tiles and of its V tiles
   static constexpr int TURN = SUB * TILE, ROOM = ((PER_SM == 2 ? 108 : 219) * 1024 - SUB * P_TILE - 2 * Q_BYTES) / TURN;
   static constexpr int NS = ROOM > 8 ? 8 : ROOM, NK = NS / 2, NV = NS - NK;
@@ -368,15 +371,15 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t b, uint32_
       "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(AHI), "n"(BHI)
       : "memory");
 }
-// S^T[128 x SN] = K[128 x D] (Q1 + Q2)[SN x D]^T, all K-major, Q2 behind Q1.
-template <int D, int SN>
+// S^T[128 x SN] = K[128 x D] (Q1 + Q2 + Q3)[SN x D]^T, all K-major, Q's terms NR rows apart.
+template <int D, int NR, int SN>
 __device__ __forceinline__ void mma_s8(uint32_t d_tmem, uint32_t k, uint32_t q, uint32_t lead) {
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s)
-    mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + s * 2, idesc8(128, SN, false, false), s > 0, lead);
+  for (int z = 0; z < 3; ++z)
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s)
-    mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + (SN * D >> 4) + s * 2, idesc8(128, SN, true, false), 1, lead);
+    for (int s = 0; s < D / 32; ++s)
+      mma8<kDescHi8<D>, kDescHi8<D>>(d_tmem, k + s * 2, q + z * (NR * D >> 4) + s * 2, idesc8(128, SN, z > 0, false),
+                                     z > 0 || s > 0, lead);
 }
 // O^T[128 x PN] (+)= V[128 x D]^T P[128 x PN], both MN-major (D = 64: the lanes from 64 on repeat the
 // first ones, V's second column group lying 0 bytes behind the first).
@@ -462,22 +465,24 @@ __device__ __forceinline__ uint16_t e5m2x2_of(uint32_t h2) {
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(h2));
   return r;
 }
-// h less its two e5m2 (the high bytes of f16): exact, since they are h rounded to fewer bits.
+// Two e5m2 are the high bytes of two f16.
+__device__ __forceinline__ uint32_t f16x2_of_e5m2(uint16_t c) { return __byte_perm(c, 0, 0x1404); }
+// h less its two e5m2: exact, since they are h rounded to fewer bits.
 __device__ __forceinline__ uint32_t rest_of(uint32_t h, uint16_t c) {
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(h), "r"(__byte_perm(c, 0, 0x1404)));
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(h), "r"(f16x2_of_e5m2(c)));
   return r;
 }
 
-// Query rows r0, r0 + step, ... of a unit as two terms: row r and row SN + r of the operand; what
+// Query rows r0, r0 + step, ... of a unit as three terms: rows r, NR + r and 2 NR + r of the operand; what
 // turns their scores into exponents of 2; and the running maximum of no keys.  A warp's call.
 template <int D, int NR>
 __device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, uint32_t q_s, float* s_rs, float* s_nm,
                                         int r0, int step, int lane) {
-  constexpr int E = D / 32, SN = Cfg8<D, NR>::SN;  // values a lane
+  constexpr int E = D / 32;  // values a lane
   const int rows = u.s.rows(p, u.rt);
 #pragma unroll 4
-  for (int r = r0; r < SN; r += step) {
+  for (int r = r0; r < NR; r += step) {
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.f;
@@ -499,28 +504,33 @@ __device__ __forceinline__ void load_q8(const Q8Params& p, const Walk<NR>& u, ui
     top = __reduce_max_sync(0xffffffffu, top);
     const int ex = min(120, max(-120, 7 + 127 - (int)(top >> 23)));  // max |x| 2^ex in [128, 256)
     const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-    uint32_t c1 = 0, c2 = 0;
+    uint32_t c[3] = {};
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float y0 = x[e] * up, y1 = x[e + 1] * up;
-      uint16_t h1, h2;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(h1) : "f"(y1), "f"(y0));
-      const uint32_t b = f16x2_of_e4m3(h1);
+      uint16_t h[3];
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(h[0]) : "f"(y1), "f"(y0));
+      const uint32_t b = f16x2_of_e4m3(h[0]);
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
-      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(h2) : "f"(y1 - f.y), "f"(y0 - f.x));
-      c1 |= (uint32_t)h1 << (8 * e);
-      c2 |= (uint32_t)h2 << (8 * e);
+      const float d0 = y0 - f.x, d1 = y1 - f.y;  // (what is left is exact)
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(h[1]) : "f"(d1), "f"(d0));
+      const uint32_t b2 = f16x2_of_e5m2(h[1]);
+      const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&b2));
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(h[2]) : "f"(d1 - f2.y), "f"(d0 - f2.x));
+#pragma unroll
+      for (int z = 0; z < 3; ++z) c[z] |= (uint32_t)h[z] << (8 * e);
     }
     const int ch = lane * E / 16, in = lane * E % 16;
-    if constexpr (E == 4) {
-      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "r"(c1) : "memory");
-      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at8<D>(q_s, SN + r, ch) + in), "r"(c2) : "memory");
-    } else {
-      asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, r, ch) + in), "h"((uint16_t)c1) : "memory");
-      asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at8<D>(q_s, SN + r, ch) + in), "h"((uint16_t)c2) : "memory");
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+      const uint32_t to = at8<D>(q_s, z * NR + r, ch) + in;
+      if constexpr (E == 4)
+        asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(to), "r"(c[z]) : "memory");
+      else
+        asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(to), "h"((uint16_t)c[z]) : "memory");
     }
-    if (lane == 0 && r < NR) {
-      // (a row with an infinity or NaN: its terms are finite, so its scores are made NaN here)
+    if (lane == 0) {
+      // (a row with an infinity or NaN: an infinity's terms are finite, so its scores are made NaN here)
       s_rs[r] = p.scale_log2 * __uint_as_float(top < 0x7f800000u ? (uint32_t)(127 - ex) << 23 : 0x7fc00000u);
       s_nm[r] = -kNone;
     }
@@ -709,7 +719,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
         const uint32_t s_t = tmem + b * SUB * C::SN;
         // (without a second tile, at the end of a unit, old keys give scores that no one reads)
 #pragma unroll
-        for (int y = 0; y < SUB; ++y) mma_s8<D, C::SN>(s_t + y * C::SN, kk + y * (C::TILE >> 4), q, lead);
+        for (int y = 0; y < SUB; ++y) mma_s8<D, NR, C::SN>(s_t + y * C::SN, kk + y * (C::TILE >> 4), q, lead);
         commit(bar(B::SFULL + b), lead);
         commit(bar(B::EMPTY + rk.slot), lead);
         rk.next();
