@@ -569,7 +569,8 @@ NSA_API nsa_status nsa_paged_evict(int n_seqs, int h_kv, int d, const nsa_paged_
  *   positions  nullable device int32 [tokens]: the position of every token (NULL: its position
  *              in the cache; a cache that was cut no longer tells it)
  *   q, q_out   [tokens, h, d] bf16, or both NULL: the queries of the same tokens, rotated to q_out
- *              (which may be q itself), those of tokens that find no place in the cache included
+ *              (which may be q itself and otherwise overlaps no input), those of tokens that find no place in the
+ *              cache included
  * rot_dim is a multiple of 16 in [16, d]. */
 typedef struct nsa_rope {
   const float* inv_freq;

@@ -912,7 +912,7 @@ def nsa_paged_append_rope(k_new, v_new, k_pages, v_pages, block_table, cache_len
     """nsa_paged_append of keys that are rotated by their position on the way: pair i of the first
     2 * len(inv_freq) dimensions by position * inv_freq[i].  positions (int32 [tokens]) where the
     place in the cache is not the position.  With q (the same tokens' queries) returns them
-    rotated too, in q_out (which may be q)."""
+    rotated too, in q_out (which may be q, and otherwise overlaps no input)."""
     fn = "nsa_paged_append_rope"
     dev = k_pages.device
     ctx, raw, share = _on(dev, stream)

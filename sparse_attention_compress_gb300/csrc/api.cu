@@ -1190,8 +1190,11 @@ nsa_status nsa_paged_attn_fwd(const nsa_shape* shape, const void* q, const nsa_p
 }
 
 // ---- rotation and the cache held in 8 bits
-// Validate a rotation and the queries that it takes along (`need`: there has to be one).
-static nsa_status check_rope(const nsa_rope* r, const Seqs& s, int h, int d, bool need, RopeArgs* out, const char* fn) {
+// Validate a rotation and the queries that it takes along (`need`: there has to be one).  Other blocks read
+// the call's inputs while rotated queries are written.
+static nsa_status check_rope(const nsa_rope* r, const Seqs& s, const nsa_shape* shape, const void* k_new,
+                             const void* v_new, bool need, RopeArgs* out, const char* fn) {
+  const int h = shape->h, d = shape->d;
   *out = RopeArgs{};
   if (!r) {
     NSA_REQUIRE(!need, NSA_ERR_INVALID, "%s: null rope", fn);
@@ -1208,6 +1211,11 @@ static nsa_status check_rope(const nsa_rope* r, const Seqs& s, int h, int d, boo
     const size_t qb = (size_t)s.tokens * h * d * 2;
     NSA_REQUIRE(r->q == r->q_out || !overlap(r->q, qb, r->q_out, qb), NSA_ERR_INVALID,
                 "%s: q_out overlaps q and is not q itself", fn);
+    const size_t kb = (size_t)s.tokens * shape->h_kv * d * 2;
+    NSA_REQUIRE(!overlap(r->q_out, qb, k_new, kb) && !overlap(r->q_out, qb, v_new, kb) &&
+                    !overlap(r->q_out, qb, r->inv_freq, (size_t)r->rot_dim / 2 * 4) &&
+                    !(r->positions && overlap(r->q_out, qb, r->positions, (size_t)s.tokens * 4)),
+                NSA_ERR_INVALID, "%s: q_out overlaps k_new, v_new, inv_freq or positions", fn);
   }
   out->inv_freq = r->inv_freq;
   out->positions = r->positions;
@@ -1226,7 +1234,7 @@ nsa_status nsa_paged_append_rope(const nsa_shape* shape, const void* k_new, cons
   RopeArgs r;
   if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
   if (nsa_status st = check_cache(cache, shape->h_kv, shape->d, true, &c, __func__)) return st;
-  if (nsa_status st = check_rope(rope, s, shape->h, shape->d, true, &r, __func__)) return st;
+  if (nsa_status st = check_rope(rope, s, shape, k_new, v_new, true, &r, __func__)) return st;
   if (s.tokens == 0) return NSA_OK;
   NSA_PTR(k_new);
   NSA_PTR(v_new);
@@ -1265,7 +1273,7 @@ nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new, const 
   int block;
   if (nsa_status st = check_span_shape(shape, &s, __func__)) return st;
   if (nsa_status st = check_cache_q8(cache, shape->h_kv, shape->d, &c, &block, __func__)) return st;
-  if (nsa_status st = check_rope(rope, s, shape->h, shape->d, false, &r, __func__)) return st;
+  if (nsa_status st = check_rope(rope, s, shape, k_new, v_new, false, &r, __func__)) return st;
   if (s.tokens == 0) return NSA_OK;
   NSA_PTR(k_new);
   NSA_PTR(v_new);
