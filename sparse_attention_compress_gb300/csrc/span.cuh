@@ -258,7 +258,6 @@ struct Waits {
 // Position in a ring of n slots: the slot and the parity of its phase.
 template <int N>
 struct Ring {
-  static constexpr int kSlots = N;
   int slot = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void next() {

@@ -58,7 +58,7 @@ struct Keys8 {
 
 template <int D, int NR>
 struct Cfg8 {
-  static constexpr int HR = 8, SUB = 2;   // rows and keys of a thread: a turn takes SUB key tiles
+  static constexpr int HR = 8, SUB = 2;   // rows (as many as tmem_ld8_nowait's columns) and keys of a thread: a turn takes SUB key tiles
   static constexpr int GROUPS = NR / HR;  // softmax groups of four warps
   static constexpr int PER_SM = NR <= 16 ? 2 : 1;
   // softmax warps; then loads of K, loads of V, products, queries and scales
@@ -400,24 +400,12 @@ __device__ __forceinline__ void mma_o8_cut(uint32_t d_tmem, uint32_t v, uint32_t
                                       s > 0 || !first, lead);
 }
 
-// N TMEM columns of a lane (8, 16 or 32), without the wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld_nowait(uint32_t a, float* v) {
+// Eight TMEM columns of a lane, without the wait.
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t a, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(a));
-  } else if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(a));
-  } else {
-    static_assert(N == 32, "");
-    tc::tmem_ld32_nowait(a, v);
-  }
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
 }
 // Waits for every load of the thread and makes v's registers depend on it.
 template <int N>
@@ -426,14 +414,11 @@ __device__ __forceinline__ void tmem_landed(float* v) {
 #pragma unroll
   for (int e = 0; e < N; ++e) asm volatile("" : "+f"(v[e]));
 }
-template <int N>
-__device__ __forceinline__ void tmem_st_nowait(uint32_t a, const float* v) {
+__device__ __forceinline__ void tmem_st8_nowait(uint32_t a, const float* v) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-#pragma unroll
-  for (int e = 0; e < N; e += 8)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a + e), "r"(r[e]),
-                 "r"(r[e + 1]), "r"(r[e + 2]), "r"(r[e + 3]), "r"(r[e + 4]), "r"(r[e + 5]), "r"(r[e + 6]), "r"(r[e + 7])
-                 : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ bool device_stopped() { return tc::device_status_set(); }
@@ -783,7 +768,7 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
         float v[SUB][HR];
         auto scores = [&](bool raw) {
 #pragma unroll
-          for (int y = 0; y < SUB; ++y) tmem_ld_nowait<HR>(s_t + y * C::SN, v[y]);
+          for (int y = 0; y < SUB; ++y) tmem_ld8_nowait(s_t + y * C::SN, v[y]);
           tmem_landed<SUB * HR>(&v[0][0]);
           const float* rs = s_rs[rq.slot] + x0;
 #pragma unroll
@@ -857,11 +842,11 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
               float ov[HR];
-              tmem_ld_nowait<HR>(o_t + z * NR, ov);
+              tmem_ld8_nowait(o_t + z * NR, ov);
               tmem_landed<HR>(ov);
 #pragma unroll
               for (int e = 0; e < HR; ++e) ov[e] *= al[e];
-              tmem_st_nowait<HR>(o_t + z * NR, ov);
+              tmem_st8_nowait(o_t + z * NR, ov);
             }
             tmem_wait_st();
           }
@@ -936,31 +921,27 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
         int64_t tok = (int64_t)u.rt * NR + x0;  // token and head of the row
         int head = (int)(tok % p.R);
         tok = u.start + tok / p.R;
+        float w[24];
 #pragma unroll
-        for (int e0 = 0; e0 < HR; e0 += 8) {
-          float w[24];
+        for (int y = 0; y < 3; ++y) tmem_ld8_nowait(o_t + y * NR, w + 8 * y);
+        tmem_landed<24>(w);
 #pragma unroll
-          for (int y = 0; y < 3; ++y) tmem_ld_nowait<8>(o_t + y * NR + e0, w + 8 * y);
-          tmem_landed<24>(w);
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int e = e0 + y;
-            const float o = w[y] + (w[8 + y] + w[16 + y]);
-            const float sum = (s_sum[x][0][e] + s_sum[x][1][e]) + (s_sum[x][2][e] + s_sum[x][3][e]), neg = nm[e];
-            if (e < rows) {
-              if (whole) {
-                const int64_t rr = tok * p.h + g * p.R + head;
-                if (krow < D) p.o[rr * D + krow] = __float2bfloat16(sum != 0.f ? o / sum : 0.f);
-                if (p.lse && krow == 0) p.lse[rr] = sum != 0.f ? (log2f(sum) - neg) * kLn2 : kNegInf;
-              } else {
-                if (krow < D && sum != 0.f) p.part_o[(slot * NR + x0 + e) * D + krow] = o;
-                if (krow == 0) p.part_ml[slot * NR + x0 + e] = make_float2(-neg, sum);
-              }
+        for (int e = 0; e < HR; ++e) {
+          const float o = w[e] + (w[8 + e] + w[16 + e]);
+          const float sum = (s_sum[x][0][e] + s_sum[x][1][e]) + (s_sum[x][2][e] + s_sum[x][3][e]), neg = nm[e];
+          if (e < rows) {
+            if (whole) {
+              const int64_t rr = tok * p.h + g * p.R + head;
+              if (krow < D) p.o[rr * D + krow] = __float2bfloat16(sum != 0.f ? o / sum : 0.f);
+              if (p.lse && krow == 0) p.lse[rr] = sum != 0.f ? (log2f(sum) - neg) * kLn2 : kNegInf;
+            } else {
+              if (krow < D && sum != 0.f) p.part_o[(slot * NR + x0 + e) * D + krow] = o;
+              if (krow == 0) p.part_ml[slot * NR + x0 + e] = make_float2(-neg, sum);
             }
-            if (++head == p.R) {
-              head = 0;
-              ++tok;
-            }
+          }
+          if (++head == p.R) {
+            head = 0;
+            ++tok;
           }
         }
       }
@@ -1398,11 +1379,11 @@ __global__ void __launch_bounds__(CfgR<D>::THREADS, 1)
 #pragma unroll 1
               for (int c = 0; c < OC; c += 8) {
                 float ov[8];
-                tmem_ld_nowait<8>(o_t + c, ov);
+                tmem_ld8_nowait(o_t + c, ov);
                 tmem_landed<8>(ov);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ov[e] *= al;
-                tmem_st_nowait<8>(o_t + c, ov);
+                tmem_st8_nowait(o_t + c, ov);
               }
               tmem_wait_st();
             }
@@ -1459,7 +1440,7 @@ __global__ void __launch_bounds__(CfgR<D>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < OC; c += 8) {
           float ov[8];
-          tmem_ld_nowait<8>(o_t + c, ov);
+          tmem_ld8_nowait(o_t + c, ov);
           tmem_landed<8>(ov);
           if (valid && whole) {
 #pragma unroll
@@ -1611,7 +1592,7 @@ static Plan8 make_plan8(const Seqs& s, int h, int hkv, int D) {
 struct Expand8 {
   Keys8 keys;
   Seqs seqs;
-  int hkv, window, n_sink, seq0;  // sequences seq0 .. of the call
+  int hkv, window, seq0;          // sequences seq0 .. of the call
   int bound;                      // table entries that lengths within the caller's bound reach
   int pages;                      // workspace pages of a sequence: those of the sinks, then those of the window
   int sink_pages;
@@ -1667,7 +1648,7 @@ constexpr int kManyRows = 257;
 constexpr size_t kExpandRoom = (size_t)512 << 20;  // bytes of a group's pages, where more than a sequence's
 struct Groups8 {
   int seqs, bound, pages, sink_pages;  // sequences of a group; table entries and workspace pages of each
-  size_t k, v, table, lens, attn, bytes;
+  size_t v, table, lens, attn, bytes;  // workspace: K's pages at 0, the others there
 };
 static Groups8 make_groups8(const Seqs& s, int h, int hkv, int D, int max_keys, int page, int max_pages, int window,
                             int n_sink) {
@@ -1707,7 +1688,6 @@ static cudaError_t launch_expanded(const Seqs& s, const void* q, const Keys8& ke
   x.seqs = s;
   x.hkv = hkv;
   x.window = window;
-  x.n_sink = n_sink;
   x.bound = gr.bound;
   x.pages = gr.pages;
   x.sink_pages = gr.sink_pages;
