@@ -588,7 +588,8 @@ NSA_API nsa_status nsa_paged_append_rope(const nsa_shape* shape, const void* k_n
 /* ---------------------------------------------------------------------------------------
  * Paged cache held in 8 bits: pages, table and lengths as in nsa_paged_cache, with e4m3 codes in
  * place of bf16 values and an fp32 scale for each block of block_size tokens and kv-head, for K
- * and for V: value = code * scale.
+ * and for V: value = code * scale.  nsa_paged_q8_append and nsa_paged_q8_attn_fwd take it;
+ * nsa_paged_attn_weights and nsa_paged_evict take bf16 pages alone.
  *   k_pages, v_pages    [n_pages][page_stride bytes] e4m3; a page is page_size rows [h_kv, d].
  *                       page_stride >= page_size * h_kv * d, a multiple of 16
  *   k_scales, v_scales  [n_pages, h_kv, page_size / block_size] fp32.  nsa_paged_q8_append writes
@@ -626,16 +627,20 @@ NSA_API nsa_status nsa_paged_q8_append(const nsa_shape* shape, const void* k_new
 
 /* nsa_paged_attn_fwd over a cache held in 8 bits: the same arguments, masks, empty rows and
  * statistics, with k = code * k_scale and v = code * v_scale.  Every code at a position below
- * cache_lens has to be finite; a row of q that is not spoils its own output
- * alone (NaN where the codes are read as they are).
+ * cache_lens has to be finite; a row of q that is not spoils its own output alone: o and lse are
+ * NaN in calls of up to 256 rows, 0 and -inf (nsa_paged_attn_fwd's answer) in calls of more.
  * Calls of up to 256 rows (max_seqlen * h / h_kv) read the codes as they are: scores see q as it is, down to
- * 2^-24 of its row's largest element, and weights enter the second product with a relative error
- * below 2^-8.6 (as bf16 they would have 2^-8).  Calls of more rows, which the products bound,
+ * 2^-24 of its row's largest element.  A weight times its value scale enters the second product with an error of
+ * 2^-8.6 of it (up to 32 rows) or 2^-11 (33 to 256; as bf16 it would have 2^-8), and of 2^-26 or 2^-34 of the
+ * row's largest such product; lse and the sum that divides o miss keys for which it is below 2^-120 of
+ * that largest one.  Calls of more rows, which the products bound,
  * expand the seen keys and values to bf16 in the workspace first (exact where scales are powers of two, else
  * rounded once), the caches of as many sequences at a time as 512 MB hold (at least of one), and
- * are nsa_paged_attn_fwd from there on: values of these keys have to fit bf16.
- *   max_cache_len  has to bound cache_lens there, for the workspace is sized by it (the queries of a cache longer
- *                  than that, in pages, see no key: o = 0, lse = -inf); 0: max_pages * page_size */
+ * are nsa_paged_attn_fwd from there on: values of these keys have to fit bf16, and weights are bf16.
+ *   max_cache_len  calls of up to 256 rows do not use it.  In calls of more rows, unlike in
+ *                  nsa_paged_attn_fwd, it decides the result: the workspace is sized by it, so it has to bound
+ *                  cache_lens, and the queries of a cache longer than that, in pages, see no key (o = 0,
+ *                  lse = -inf, and no error).  0, which is always right: max_pages * page_size */
 NSA_API size_t nsa_paged_q8_attn_fwd_workspace_size(const nsa_shape* shape, const nsa_paged_cache_q8* cache,
                                                     int64_t max_cache_len, int window, int n_sink);
 NSA_API nsa_status nsa_paged_q8_attn_fwd(const nsa_shape* shape, const void* q, const nsa_paged_cache_q8* cache,

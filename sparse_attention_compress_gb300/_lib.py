@@ -1005,8 +1005,10 @@ def nsa_paged_q8_attn_fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, 
                           scale=0.0, *, cu_seqlens=None, max_seqlen=None, max_cache_len=None, workspace=None, out=None,
                           lse=None, stream=None):
     """nsa_paged_attn_fwd over a cache held in 8 bits (as nsa_paged_q8_append writes it): k = code *
-    k_scale, v = code * v_scale.  Calls of many tokens expand the keys that they see to bf16 in the workspace
-    first, which max_cache_len (a bound on cache_lens) sizes: give it where tables are much wider than caches."""
+    k_scale, v = code * v_scale.  Calls of more than 256 rows (tokens x heads of a group) expand the keys that they see
+    to bf16 in the workspace first, which max_cache_len sizes: give it where tables are much wider than caches.
+    There it has to bound cache_lens: the queries of a longer cache see no key (out = 0, lse = -inf, no error).
+    None is always right."""
     fn = "nsa_paged_q8_attn_fwd"
     if (window | n_sink) >> 31:
         _int32(fn, window=window, n_sink=n_sink)

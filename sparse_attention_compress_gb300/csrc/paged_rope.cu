@@ -15,8 +15,9 @@
 //
 // Single tokens cost one launch (3.1 us for 32 tokens into the bf16 cache, 4.1 into 8 bits).  Four sequences
 // of up to 2048 new tokens (16 query heads, 4 kv-heads of 128) take 18.3 us into the bf16 cache (81 MB read and
-// written: 4.4 TB/s; what is left is the first and the last blocks' latency) and 24.2 us into 8 bits (74 MB;
-// loads, angles, conversions and a block-wide maximum behind one another).
+// written: 4.4 TB/s; its 1639 blocks are one and a half rounds, and two synchronisations come before a block's first
+// load of values) and 24.2 us into 8 bits (74 MB; loads, angles, conversions and a block-wide maximum behind one
+// another, three and a half rounds).
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -30,9 +30,9 @@
 // o) q8_combine_kernel joins in order.  So ragged caches even out, and a CTA sets itself
 // up once.  The barriers of a turn cost more than its arithmetic, so a turn takes two key tiles.
 //
-// Decode, 32 caches of 16384 .. 32768 keys, 16 heads over 2 kv-heads of 128 (403 MB of codes): 81.1 us, 5.0 TB/s
-// of a copy's 6.7 (80.1 with Q in two terms); the same over a bf16 cache takes 146.  Of the rest, 8 us go before the first scores (launch,
-// set-up, first copies) and 5 into the join; in between HBM runs at 6.0 TB/s.  The tensor cores are far from
+// Decode, 32 caches of 16384 .. 32768 keys, 16 heads over 2 kv-heads of 128 (403 MB of codes): 81 us, 5.0 TB/s
+// of a copy's 6.7 (80 with Q in two terms); the same values in a bf16 cache take 143.  Of the rest, 8 us go before
+// the first scores (launch, set-up, first copies) and 5 into the join; in between HBM runs at 6.0 TB/s.  The tensor cores are far from
 // their limit (one row of 8 in use of N = 16 costs as much as 16), but not from sight: a product with M = 128
 // takes 40 cycles or more however small its N.  From 33 rows on the other form is faster (attn_q8_rows_kernel).
 #include <algorithm>
@@ -124,8 +124,9 @@ struct Seq8 {
 // A run is cut in places: a unit has kSwitch places that stand for the time that it takes to begin one (the
 // joining of the row sums, O's way out, the first maxima), then one for each tile.
 // 32 x 16384 .. 32768 keys, 8 rows: 0 places 85 us, 4 80.4, 8 79.5, 12 79.6, 24 80.6; 8 x 8192 keys x 8 kv-heads 46.2,
-// 40.4, 37.1, 37.4, 38.9; 32 rows over 16 x 16384 keys x 4 kv-heads 88, 86, 84, 82, 76; 128 rows over 16 x up to 8192
-// keys x 4 kv-heads with 6 places 72.2, 8 72.5, 12 74.2, 24 81.6.
+// 40.4, 37.1, 37.4, 38.9; 32 rows over 16 x 16384 keys x 4 kv-heads 88, 86, 84, 82, 76 (24 is the most that was tried);
+// 128 rows over 16 x up to 8192 keys x 4 kv-heads with 6 places 72.2, 8 72.5, 12 74.2, 24 81.6.  16 rows take the 8-row
+// form's number.
 template <int NR>
 struct Walk {
   static constexpr int kSwitch = NR == 128 ? 8 : NR == 32 ? 24 : 12;
@@ -978,7 +979,9 @@ __global__ void __launch_bounds__(Cfg8<D, NR>::THREADS, Cfg8<D, NR>::PER_SM)
 // 16 caches of up to 8192 keys, 8 tokens, 64 heads over 4 kv-heads of 128: 72.5 us, of which HBM 17 (136 in tiles of
 // 32 rows by the form above, whose three terms of P cost too many conversions; 122 with those terms and the rows as M).
 // A key tile takes about 3000 cycles: the conversion of its K and V 1600 and the softmax of its rows 2100, beside
-// each other; shared memory moves 220 KB for it, 1750 cycles.
+// each other; shared memory moves 220 KB for it, 1750 cycles.  A CTA's 22 tiles are so 33 of the 72.5 us; the join takes 10,
+// and the rest goes into starts and changes of unit, at which Q's one buffer and the converting warps' load of
+// it let everything behind them run empty.
 template <int D>
 struct CfgR {
   static constexpr int NR = 128, SOFT = 16, CONV = 4, WARPS = SOFT + CONV + 3, THREADS = WARPS * 32;
