@@ -46,3 +46,24 @@ def test_elements_far_below_a_rows_largest(n, d):
             o = nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, scale=scale, cu_seqlens=cu.cuda(), max_seqlen=n, lse=lse)
             assert nsa.nsa_device_status() == 0
             _check(c, q, cu, o, lse, 0, 0, scale)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 20])  # 8, 16, 32 and 160 rows
+@pytest.mark.parametrize("first", [60, -60])
+def test_value_scales_at_both_ends_of_their_range(n, first):
+    """Value scales of 2^60 in one half of a cache and 2^-60 in the other, scores near one another: every key counts in
+    the row's sum, also where the parts of a row have one kind of scale alone."""
+    c = Cache8([6000], 1, 128, 64, 64, 210)
+    half = 6000 // 128 * 64
+    at = torch.arange(6000)
+    scales = torch.where(at < half, 2.0 ** first, 2.0 ** -first).double()
+    c.scales[0][1] = scales[:, None]
+    vs = c.v_scales.cpu()
+    vs[c.table[0].long()[at // 64], 0, 0] = scales.float()
+    c.v_scales = vs.cuda()
+    q = (torch.randn(n, 8, 128, generator=_gen(211)) * 0.01).to(BF)
+    cu = torch.tensor([0, n], dtype=torch.int32)
+    lse = torch.empty(n, 8, device="cuda")
+    o = nsa.nsa_paged_q8_attn_fwd(q.cuda(), *c.args, cu_seqlens=cu.cuda(), max_seqlen=n, lse=lse)
+    assert nsa.nsa_device_status() == 0
+    _check(c, q, cu, o, lse, 0, 0, 1 / math.sqrt(128))
